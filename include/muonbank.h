@@ -64,8 +64,8 @@ extern "C" {
 enum {
   MB_OK = 0,
   MB_ERR_NULL = -1,          /* a required pointer is NULL */
-  MB_ERR_SHAPE = -2,         /* batch/rows/cols <= 0, or a size past the limits of mb_shape */
-  MB_ERR_ALIGN = -3,         /* a pointer is not 16-byte aligned */
+  MB_ERR_SHAPE = -2,         /* batch/rows/cols <= 0, or a size past the limits of mb_shape (or of a block operator) */
+  MB_ERR_ALIGN = -3,         /* a pointer is not 16-byte aligned (block operators: not aligned to its element) */
   MB_ERR_NS_STEPS = -4,      /* ns_steps outside 0..16 */
   MB_ERR_WORKSPACE = -5,     /* workspace NULL or smaller than required */
   MB_ERR_CUDA = -6,          /* a CUDA runtime call or kernel launch failed */
@@ -243,6 +243,118 @@ int mb_sync_status(void* cuda_stream);
  * up, latches MB_ERR_TIMEOUT and returns.  For testing failure detection. */
 int mb_selftest_timeout(unsigned limit_us, void* cuda_stream);
 
+/* ---- block operators ----
+ *
+ * The memory-bound operators of a transformer block that stand between its matrix
+ * products (the matrices the banks hold), each with its gradient: layer norm,
+ * rotary positions with one or several axes, and the routing of tokens over a
+ * bank of experts with its balance loss.  The pages name none of them; they are
+ * here so that a block whose matrices this library steps can be trained with it.
+ *
+ * They share the conventions above (caller's buffers, asynchronous on the stream,
+ * statuses, identical bits from run to run) with these differences:
+ *   - element types are given per call (MB_F32, MB_BF16, MB_F16); arithmetic,
+ *     statistics and sums are fp32, with one rounding at each store;
+ *   - pointers need only their element's alignment, rows and heads may be strided
+ *     (strides in elements; the innermost elements are contiguous).  16-byte
+ *     aligned rows of a multiple of 8 elements take 16-byte accesses;
+ *   - a size of zero (rows, batch, tokens) is legal: nothing is read, sums over
+ *     nothing are written as zero, and pointers to nothing may be NULL;
+ *   - a result may be written over the input that it replaces element by element
+ *     (y over x, dx over x or dy, dst over src, dlogits over logits) with the same
+ *     strides; no other overlap.
+ */
+enum {
+  MB_F32 = 0,
+  MB_BF16 = 1,
+  MB_F16 = 2,
+  MB_I32 = 3,   /* positions only */
+  MB_I64 = 4    /* positions only */
+};
+
+/* Layer norm of each row of x [rows, cols]:
+ *   m = mean(x);  r = 1 / sqrt(mean((x - m)^2) + eps);  y = (x - m) r w + b
+ * w, b: [cols] of type w_type (`type` or MB_F32), each may be NULL (ones, zeros).
+ * mean, rstd: fp32 [rows] results for the backward pass, each may be NULL.
+ * x_stride: elements from row to row (0: one row for all); y_stride >= cols.
+ * MB_ERR_SHAPE: rows < 0, cols outside 1..2^30, a stride that is negative or too
+ * small.  MB_ERR_ARG: a type, or eps not finite or negative. */
+int mb_layer_norm(const void* x, int64_t x_stride, int type, const void* w, const void* b,
+                  int w_type, void* y, int64_t y_stride, float* mean, float* rstd,
+                  int64_t rows, int64_t cols, float eps, void* cuda_stream);
+
+/* Its gradient, with h = (x - m) r and g = dy w:
+ *   dx = r (g - mean(g) - h mean(g h));  dw = sum over rows of dy h;  db = of dy
+ * mean and rstd are those of the forward pass.  dw, db: [cols] of w_type, each may
+ * be NULL (not wanted).  The workspace is only needed for dw or db. */
+int mb_layer_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* out_bytes);
+int mb_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                           int type, const void* w, int w_type, const float* mean,
+                           const float* rstd, void* dx, int64_t dx_stride, void* dw, void* db,
+                           int64_t rows, int64_t cols, void* workspace, size_t workspace_bytes,
+                           void* cuda_stream);
+
+/* Heads of q or k: element (b, t, h, i) is at b src_batch + t src_token + h src_head + i. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t heads;             /* 0: absent */
+  int64_t src_batch, src_token, src_head, dst_batch, dst_token, dst_head;
+} mb_head_tensor;
+
+#define MB_ROTARY_MAX_AXES 4
+typedef struct {
+  mb_head_tensor q, k;
+  int32_t type, interleaved; /* pairs are (2i, 2i+1) if interleaved, else (i, i + pairs) */
+  int64_t batch, tokens;
+  int32_t dim, pairs;        /* elements of a head; the first 2 * pairs turn, the rest is copied */
+  const void* positions;     /* position of (axis a, b, t) at a pos_axis + b pos_batch + t pos_token */
+  int64_t pos_axis, pos_batch, pos_token;
+  int32_t position_type, axes;             /* MB_I32, MB_I64 or MB_F32; 1..MB_ROTARY_MAX_AXES */
+  int32_t sections[MB_ROTARY_MAX_AXES];    /* pairs of each axis, in order; they add up to `pairs` */
+  const float* inv_freq;     /* fp32 [pairs]: radians per position of each pair */
+} mb_rotary_desc;
+
+/* Turns pair i of every head of q and k at each token by positions[its axis] * inv_freq[i]
+ * (the product rounded to fp32):  u' = u cos - v sin,  v' = v cos + u sin.
+ * mb_rotary_backward turns back by the same angles: the gradient with respect to the
+ * source (src: dq or dk), and the inverse.  Limits (else MB_ERR_SHAPE): pairs 1..4096,
+ * 2 pairs <= dim <= 65536, heads of q and k together 1..65536, batch * tokens < 2^31;
+ * strides are not negative, and not 0 in a destination where there is more than one.
+ * The descriptor is read during the call only. */
+int mb_rotary(const mb_rotary_desc* desc, void* cuda_stream);
+int mb_rotary_backward(const mb_rotary_desc* desc, void* cuda_stream);
+
+/* Routing of tokens over experts by their logits [tokens, experts].
+ *   - A token counts unless `valid` (bytes [tokens], may be NULL) is 0 there or all its
+ *     logits are -inf; N tokens count.  p = softmax of its logits (0 for the others).
+ *   - It chooses the top_k largest logits, the lowest index first among equals and NaN
+ *     above all.  An expert at -inf is never chosen: such a place, and all places of a
+ *     token that does not count, get index -1 and gate 0.
+ *   - gate is p at the chosen experts, or, with normalize, p over the sum of the chosen p.
+ *   - counts[e] is the number of places given to e, and
+ *       loss = experts / (top_k N^2) * sum_e counts[e] * sum_t p[t, e]
+ *     (1 when perfectly balanced; 0 when no token counts).
+ *   - NaN or +inf among a token's logits makes its p, its gates and the loss NaN.
+ * Results: index int32 and gate fp32 [tokens, top_k]; counts int32 [experts]; loss fp32
+ * [1]; used int32 [1] = N.  Limits (else MB_ERR_SHAPE): experts 1..1024, top_k
+ * 1..min(experts, 32), tokens * top_k < 2^31. */
+int mb_router_workspace_bytes(int64_t tokens, int64_t experts, size_t* out_bytes);
+int mb_router(const void* logits, int64_t stride, int type, const uint8_t* valid, int64_t tokens,
+              int64_t experts, int top_k, int normalize, int32_t* index, float* gate,
+              int32_t* counts, float* loss, int32_t* used, void* workspace,
+              size_t workspace_bytes, void* cuda_stream);
+
+/* Gradient of the logits from that of the loss (fp32 [1], may be NULL: zero) and of the
+ * gates (fp32 [tokens, top_k], may be NULL: zero; not read at index -1), given the forward
+ * pass's index, gate, counts and used.  Counts are constants of the loss.  The rows of tokens
+ * that do not count are zero. */
+int mb_router_backward(const float* dloss, const float* dgate, const void* logits, int64_t stride,
+                       int type, const uint8_t* valid, int64_t tokens, int64_t experts, int top_k,
+                       int normalize, const int32_t* index, const float* gate,
+                       const int32_t* counts, const int32_t* used, void* dlogits,
+                       int64_t dlogits_stride, void* cuda_stream);
+
 /* ---- measurement hooks ---- */
 
 /* Number of kernels this host thread has launched through the library so far. */
@@ -257,7 +369,12 @@ enum {
   MB_MARK_NS_GEMM = 4,    /* after the tensor-core Newton-Schulz launch (all steps) */
   MB_MARK_NS0 = 5,        /* after the ns_steps = 0 scaling, or the copy-out of a stage call */
   MB_MARK_ROWSTATS = 6,   /* after the NorMuon row statistics */
-  MB_MARK_UPDATE = 7      /* after S5 */
+  MB_MARK_UPDATE = 7,     /* after S5 */
+  MB_MARK_LAYER_NORM = 8, /* after the launches of a block operator */
+  MB_MARK_LAYER_NORM_BACKWARD = 9,
+  MB_MARK_ROTARY = 10,    /* (either direction) */
+  MB_MARK_ROUTER = 11,
+  MB_MARK_ROUTER_BACKWARD = 12
 };
 
 /* Starts recording a CUDA event on the launching stream at every stage

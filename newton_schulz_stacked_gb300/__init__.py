@@ -16,6 +16,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import _binding as _b
+from .blocks import (RouterOutput, mb_layer_norm, mb_layer_norm_backward, mb_rotary, mb_rotary_backward,  # noqa: F401
+                     mb_router, mb_router_backward)
 from ._binding import MuonBankError, MB_MAX_BANKS, MB_STEP_FUSE_ROWSTATS, MB_STEP_FUSE_UPDATE  # noqa: F401
 
 __all__ = [
@@ -24,6 +26,8 @@ __all__ = [
     "mb_newton_schulz_coeffs", "mb_update", "mb_normuon_update", "mb_newton_schulz_noalloc", "mb_workspace_views",
     "mb_sync_status", "mb_selftest_timeout", "mb_status_string", "MuonBankError",
     "BankState", "load_library", "mb_launch_count", "StageTimer",
+    "mb_layer_norm", "mb_layer_norm_backward", "mb_rotary", "mb_rotary_backward", "mb_router", "mb_router_backward",
+    "RouterOutput",
 ]
 
 _TWO_BYTE = (torch.bfloat16, torch.int16, torch.uint16, torch.float16)

@@ -1,0 +1,94 @@
+"""The block operators under torch's autograd: each forward call joined with its backward call."""
+from __future__ import annotations
+
+from typing import NamedTuple, Sequence
+
+import torch
+
+from . import blocks as _k
+
+
+class Routing(NamedTuple):
+    """index int32 and gate fp32 [tokens, top_k], counts int32 [experts], loss fp32 scalar."""
+    index: torch.Tensor
+    gate: torch.Tensor
+    counts: torch.Tensor
+    loss: torch.Tensor
+
+
+def _readable(g: torch.Tensor) -> torch.Tensor:
+    """Autograd may hand over an expanded gradient (of a sum, say): its elements are laid out first."""
+    return g if g.shape[-1] == 1 or g.stride(-1) == 1 else g.contiguous()
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = _k.mb_layer_norm(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.has_bias = bias is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        if not dy.is_contiguous():
+            dy = dy.contiguous()
+        dx, dweight, dbias = _k.mb_layer_norm_backward(dy, x, mean, rstd, weight, bias=ctx.has_bias)
+        return dx, dweight, dbias, None
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5) -> torch.Tensor:
+    """Layer norm over the last dimension, differentiable in x, weight and bias."""
+    if weight is None and bias is not None:
+        raise ValueError("a bias needs a weight")
+    return _LayerNorm.apply(x, weight, bias, eps)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, sections, interleaved):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.sections, ctx.interleaved = sections, interleaved
+        ctx.set_materialize_grads(False)
+        return _k.mb_rotary(q, k, positions, inv_freq, sections, interleaved)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        positions, inv_freq = ctx.saved_tensors
+        args = (positions, inv_freq, ctx.sections, ctx.interleaved)
+        if dq is not None:
+            dq, dk = _k.mb_rotary_backward(_readable(dq), None if dk is None else _readable(dk), *args)
+        elif dk is not None:
+            dk, _ = _k.mb_rotary_backward(_readable(dk), None, *args)
+        return dq, dk, None, None, None, None
+
+
+def rotary(q, k, positions, inv_freq, sections: Sequence[int], interleaved: bool = False):
+    """mb_rotary, differentiable in q and k (k may be None): (q_out, k_out)."""
+    return _Rotary.apply(q, k, positions, inv_freq, tuple(sections), interleaved)
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, valid, normalize):
+        out = _k.mb_router(logits, top_k, valid, normalize)
+        ctx.save_for_backward(logits, valid, out.index, out.gate, out.counts, out.used)
+        ctx.normalize = normalize
+        ctx.mark_non_differentiable(out.index, out.counts)
+        ctx.set_materialize_grads(False)
+        return out.index, out.gate, out.counts, out.loss.reshape(())
+
+    @staticmethod
+    def backward(ctx, _index, dgate, _counts, dloss):
+        if dgate is None and dloss is None:
+            return None, None, None, None
+        logits, valid, index, gate, counts, used = ctx.saved_tensors
+        return _k.mb_router_backward(None if dloss is None else dloss.reshape(1),
+                                     None if dgate is None else dgate.contiguous(), logits, index, gate, counts, used,
+                                     valid, ctx.normalize), None, None, None
+
+
+def route(logits, top_k: int, valid=None, normalize: bool = False) -> Routing:
+    """mb_router, differentiable in the logits through the gates and the balance loss."""
+    return Routing(*_Route.apply(logits, top_k, valid, normalize))

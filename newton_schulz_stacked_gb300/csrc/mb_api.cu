@@ -6,6 +6,7 @@
 #include <string>
 #include <vector>
 
+#include "mb_block.h"
 #include "mb_device.cuh"
 #include "mb_internal.h"
 #include "muonbank.h"
@@ -76,6 +77,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 struct DeviceState {
   bool ready = false;
   int* status = nullptr;
+  int sms = 0;
 };
 
 std::mutex g_mu;
@@ -122,6 +124,7 @@ int device_state(DeviceState** out) {
     MB_TRY_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
     MB_TRY_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
     if (major != 10 || minor != 3) return MB_ERR_UNSUPPORTED;
+    MB_TRY_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
     void* p = nullptr;
     MB_TRY_CUDA(cudaGetSymbolAddress(&p, g_status));
     d.status = static_cast<int*>(p);
@@ -732,20 +735,36 @@ int ns_stage(const void* u_bf16, void* v_bf16, mb_shape shape, int ns_steps, con
 }
 
 }  // namespace
+
+// What the block operators' entries (mb_block_api.cu) share with the step's.
+int api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+
+int api_device_sms(int* sms) {
+  DeviceState* ds = nullptr;
+  MB_TRY(device_state(&ds));
+  *sms = ds->sms;
+  return MB_OK;
+}
+
+void api_launched(int label, int launches, cudaStream_t stream) {
+  g_launch_count += launches;
+  mark(label, stream);
+}
+
 }  // namespace mb
 
 using namespace mb;
 
 extern "C" {
 
-int mb_version(void) { return (1 << 16) | 0; }
+int mb_version(void) { return (1 << 16) | 1; }
 
 const char* mb_status_string(int status) {
   switch (status) {
     case MB_OK: return "ok";
     case MB_ERR_NULL: return "a required pointer is NULL";
-    case MB_ERR_SHAPE: return "invalid bank shape";
-    case MB_ERR_ALIGN: return "pointer not 16-byte aligned (workspace: 256-byte)";
+    case MB_ERR_SHAPE: return "invalid shape or stride";
+    case MB_ERR_ALIGN: return "pointer not aligned (a bank's: 16 bytes; a workspace: 256; a block operator's: its element)";
     case MB_ERR_NS_STEPS: return "ns_steps outside 0..16";
     case MB_ERR_WORKSPACE: return "workspace missing or too small";
     case MB_ERR_CUDA: return "CUDA error";

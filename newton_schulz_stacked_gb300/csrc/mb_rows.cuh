@@ -1,0 +1,163 @@
+// What the block operators (layer norm, rotary, router) share: the element types, a thread's
+// eight elements of a row, and sums over the threads of a row.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+namespace mb {
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+
+// Two neighbouring 16-bit values of one 32-bit word (the low half is the first).
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight consecutive elements at a 16-byte boundary, as loaded (one 16-byte access for the
+// 16-bit types, two for fp32).
+template <typename T>
+struct Eight {
+  static constexpr int WORDS = sizeof(T) / 2;   // 16-byte words
+  uint4 w[WORDS];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2(u[i], T());
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(w);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = pack2(v[2 * i], v[2 * i + 1], T());
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+  }
+};
+
+// Piece v of thread t's share of a row that `tpr` threads hold together.
+// VEC: the eight elements from column (v tpr + t) 8 on; rows start at 16-byte boundaries and
+// hold a multiple of eight elements.  Otherwise eight single elements, tpr columns apart, so
+// that neighbouring threads still read neighbouring elements whatever the row's alignment.
+template <typename T, bool VEC>
+struct Piece;
+
+template <typename T>
+struct Piece<T, true> {
+  Eight<T> e;
+  static __device__ __forceinline__ int col(int v, int j, int t, int tpr) { return (v * tpr + t) * 8 + j; }
+  static __device__ __forceinline__ bool in(int v, int, int t, int tpr, int cols) { return (v * tpr + t) * 8 < cols; }
+  __device__ __forceinline__ void load(const T* row, int cols, int v, int t, int tpr, bool on = true) {
+    if (on && in(v, 0, t, tpr, cols)) e.load(row + col(v, 0, t, tpr));
+    else e.zero();
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const { e.get(f); }
+  static __device__ __forceinline__ void store(T* row, int cols, int v, int t, int tpr, const float (&f)[8]) {
+    if (in(v, 0, t, tpr, cols)) {
+      Eight<T> o;
+      o.set(f);
+      o.store(row + col(v, 0, t, tpr));
+    }
+  }
+};
+
+template <typename T>
+struct Piece<T, false> {
+  float f_[8];
+  static __device__ __forceinline__ int col(int v, int j, int t, int tpr) { return (v * 8 + j) * tpr + t; }
+  static __device__ __forceinline__ bool in(int v, int j, int t, int tpr, int cols) {
+    return col(v, j, t, tpr) < cols;
+  }
+  __device__ __forceinline__ void load(const T* row, int cols, int v, int t, int tpr, bool on = true) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f_[j] = on && in(v, j, t, tpr, cols) ? to_float(row[col(v, j, t, tpr)]) : 0.f;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = f_[j];
+  }
+  static __device__ __forceinline__ void store(T* row, int cols, int v, int t, int tpr, const float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (in(v, j, t, tpr, cols)) row[col(v, j, t, tpr)] = from_float<T>(f[j]);
+  }
+};
+
+// A parameter vector (weight or bias) in fp32 or in the activations' type T; null reads as `otherwise`.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_param(const void* p, bool f32, float otherwise, int cols, int v, int t, int tpr,
+                                           float (&f)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = otherwise;
+  } else if (f32) {
+    Piece<float, VEC> w;
+    w.load(static_cast<const float*>(p), cols, v, t, tpr);
+    w.get(f);
+  } else {
+    Piece<T, VEC> w;
+    w.load(static_cast<const T*>(p), cols, v, t, tpr);
+    w.get(f);
+  }
+}
+
+// Sum over the aligned group of `width` lanes (a power of two); every lane gets it.
+__device__ __forceinline__ float group_sum(float x, int width) {
+  for (int o = width >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+
+// Programmatic launch: a kernel launched beside the one before it in the stream waits here
+// until that kernel's writes are visible.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace mb
