@@ -1,9 +1,10 @@
-"""Builds libmuonbank.so in-tree with nvcc for sm_103a.
+"""Builds libmuonbank.so in-tree with nvcc for sm_103a, and the block operators' Python binding.
 
 Each .cu file compiles in parallel to an object under ``_build/``; the objects
 link into ``newton_schulz_stacked_gb300/libmuonbank.so`` with the CUDA runtime
 linked statically (the driver API is reached through the runtime's
-entry-point query, so no libcuda link is needed).
+entry-point query, so no libcuda link is needed).  ``csrc/mb_torch.cpp`` compiles with
+the host compiler against the installed torch into ``_blocks.so``, which links to the library.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import shutil
 import signal
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -123,5 +125,69 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=()) ->
     return LIB_PATH
 
 
+# ---------------------------------------------------------------- the block operators' binding
+
+BINDING_SRC = os.path.join(CSRC, "mb_torch.cpp")
+BINDING_PATH = os.path.join(HERE, "_blocks.so")
+
+
+def _binding_commands():
+    """The compile and the link command of _blocks.so."""
+    import torch
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found")
+    top = os.path.dirname(torch.__file__)
+    inc, libs = os.path.join(top, "include"), os.path.join(top, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    obj = os.path.join(BUILD_DIR, "mb_torch.o")
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", inc, "-I",
+                os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-I", cuda,
+                "-c", BINDING_SRC, "-o", obj]
+    link = [cxx, "-shared", "-o", BINDING_PATH + ".tmp", obj, "-L", HERE, "-lmuonbank", "-L", libs, "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    stamp = hashlib.sha256("\0".join([*compile_, *link, torch.__version__, sys.version]).encode()).hexdigest()
+    return compile_, link, stamp
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        raise RuntimeError(f"{what} failed")
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING_PATH):
+        return False
+    if os.path.getmtime(BINDING_PATH) < max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "muonbank.h"))):
+        return False
+    try:
+        with open(BINDING_PATH + ".flags") as f:
+            return f.read().strip() == _binding_commands()[2]
+    except OSError:
+        return False
+
+
+def build_all(force: bool = False) -> str:
+    """The library and the binding, compiled side by side; returns the binding's path."""
+    if not force and binding_up_to_date():
+        build_library()
+        return BINDING_PATH
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    compile_, link, stamp = _binding_commands()
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_run, compile_, "compile of the binding")
+        build_library(force=force)
+        obj.result()
+    _run(link, "link of the binding")
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    with open(BINDING_PATH + ".flags", "w") as f:
+        f.write(stamp + "\n")
+    return BINDING_PATH
+
+
 if __name__ == "__main__":
-    print(build_library(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    if "-v" in sys.argv:
+        build_library(force="--force" in sys.argv, verbose=True)
+    print(build_all(force="--force" in sys.argv and "-v" not in sys.argv))

@@ -21,8 +21,8 @@ ROUND[torch.float32] = (0.0, 2.0 ** -149)
 
 @pytest.fixture(scope="module")
 def nss():
-    from newton_schulz_stacked_gb300.build import build_library
-    build_library()
+    from newton_schulz_stacked_gb300.build import build_all
+    build_all()
     import newton_schulz_stacked_gb300 as m
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
     m.load_library()
