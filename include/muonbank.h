@@ -346,7 +346,7 @@ int mb_router(const void* logits, int64_t stride, int type, const uint8_t* valid
               size_t workspace_bytes, void* cuda_stream);
 
 /* Gradient of the logits from that of the loss (fp32 [1], may be NULL: zero) and of the
- * gates (fp32 [tokens, top_k], may be NULL: zero; not read at index -1), given the forward
+ * gates (fp32 [tokens, top_k], may be NULL: zero; ignored at index -1), given the forward
  * pass's index, gate, counts and used.  Counts are constants of the loss.  The rows of tokens
  * that do not count are zero. */
 int mb_router_backward(const float* dloss, const float* dgate, const void* logits, int64_t stride,

@@ -17,11 +17,24 @@
 namespace mb {
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 16;             // per CTA, two CTAs per SM
 constexpr int THREADS = WARPS * 32;
 constexpr unsigned FULL = 0xFFFFFFFFu;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float MINUS_INF = -__builtin_huge_valf();
 
-// Unsigned keys in the order of the logits: -inf (an expert that is not available) is 0, NaN is
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Exact keys in the order of the logits: -inf (an expert that is not available) is 0, NaN is
 // above everything, both zeros are one.
 __device__ __forceinline__ uint32_t key_of(float l) {
   const uint32_t u = __float_as_uint(l + 0.f);
@@ -31,7 +44,7 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
-  if (key == 0u) return __uint_as_float(0xFF800000u);
+  if (key == 0u) return MINUS_INF;
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
@@ -63,6 +76,11 @@ __device__ __forceinline__ float group_add(float x) {
 }
 template <int G>
 __device__ __forceinline__ float group_fmax(float x) {
+  if constexpr (G == 32) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+  }
 #pragma unroll
   for (int o = G >> 1; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, o));
   return x;
@@ -72,31 +90,42 @@ __device__ __forceinline__ float group_fmax(float x) {
 template <int G>
 __device__ __forceinline__ int expert_of(int c, int g, int j) { return (c * G + g) * 8 + j; }
 
-// The lane's logits of one token; experts past the last read as -inf.
+// The lane's logits of one token as loaded (one load ahead of their use); experts past the
+// last, and tokens that are not read, are -inf.
 template <typename T, bool VEC, int G, int NC>
-__device__ __forceinline__ void load_logits(const T* row, bool on, int experts, int g, float (&l)[8 * NC]) {
+struct Logits {
+  Eight<T> v[VEC ? NC : 1];
+  float f[VEC ? 1 : 8 * NC];
+  bool on;
+  __device__ __forceinline__ void load(const T* row, bool read, int experts, int g) {
+    on = read;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int e0 = expert_of<G>(c, g, 0);
-    if constexpr (VEC) {
-      if (on && e0 < experts) {
-        Eight<T> v;
-        float f[8];
-        v.load(row + e0);
-        v.get(f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) l[8 * c + j] = f[j];
+    for (int c = 0; c < NC; ++c) {
+      const int e0 = expert_of<G>(c, g, 0);
+      if constexpr (VEC) {
+        if (on && e0 < experts) v[c].load(row + e0);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) l[8 * c + j] = __uint_as_float(0xFF800000u);
+        for (int j = 0; j < 8; ++j) f[8 * c + j] = on && e0 + j < experts ? to_float(row[e0 + j]) : MINUS_INF;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        l[8 * c + j] = on && e0 + j < experts ? to_float(row[e0 + j]) : __uint_as_float(0xFF800000u);
     }
   }
-}
+  __device__ __forceinline__ void get(int experts, int g, float (&l)[8 * NC]) const {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if constexpr (VEC) {
+        float x[8];
+        v[c].get(x);
+        const bool in = on && expert_of<G>(c, g, 0) < experts;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) l[8 * c + j] = in ? x[j] : MINUS_INF;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) l[8 * c + j] = f[8 * c + j];
+      }
+    }
+  }
+};
 
 // The counts and the loss from the CTAs' sums: E experts in `n` rows of sums; called by the
 // `threads` threads of one CTA for the experts [e_begin, e_end); returns (to every thread) the
@@ -148,14 +177,87 @@ __device__ __forceinline__ float loss_of(float share, int used, int experts, int
 
 // ---------------------------------------------------------------- forward
 
+// A lane keeps the r-th chosen experts with r % G equal to its place in the group.
+template <int G>
+struct Slots {
+  static constexpr int N = G >= 32 ? 1 : 32 / G > 8 ? 8 : 32 / G;   // k <= 8 G and k <= 32
+};
+
+// The k largest of a token's logits for any values: k rounds over exact keys, the winner's lane
+// looking for its next among what comes after the one just taken.  Writes the lane's chosen
+// experts, and the softmax's terms and sum in the plain form exp(l - max).
+template <int G, int V>
+__device__ __forceinline__ void select_exact(const float (&l)[V], int g, int k, int (&idx)[Slots<G>::N], float (&e)[V],
+                                          float& sum, float& m, bool& some) {
+  constexpr int SLOTS = Slots<G>::N;
+  uint32_t key[V], k1 = 0;
+  int i1 = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    key[j] = key_of(l[j]);
+    if (key[j] > k1) {
+      k1 = key[j];
+      i1 = j;
+    }
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) idx[s] = -1;
+  for (int r = 0; r < k; ++r) {
+    const uint32_t best = group_max<G>(k1);
+    if (r == 0) top = best;
+    const uint32_t mine = k1 == best && best != 0 ? expert_of<G>(i1 / 8, g, i1 & 7) : 0x7FFFFFFFu;
+    const uint32_t who = group_min<G>(mine);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+      if (r == s * G + g && best != 0) idx[s] = static_cast<int>(who);
+    if (best != 0 && mine == who) {
+      const uint32_t lk = k1;
+      const int li = i1;
+      k1 = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool after = key[j] < lk || (key[j] == lk && j > li);
+        if (after && key[j] > k1) {
+          k1 = key[j];
+          i1 = j;
+        }
+      }
+    }
+  }
+  some = top != 0;
+  m = value_of(top);
+  sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    e[j] = key[j] == 0 ? 0.f : expf(l[j] - m);
+    sum += e[j];
+  }
+  sum = group_add<G>(sum);
+  // NaN or +inf among the logits makes the sum NaN, and with it every probability of the token
+  if (top >= 0xFF800000u) sum = __uint_as_float(0x7FC00000u);
+}
+
+// Selection without conditions per element.  With c = max * log2(e) rounded up, x = l log2(e) - c
+// is at most 0, monotone in l, and the exponent the softmax needs anyway.  The bits of such an x
+// grow as l falls, so a key of x's upper bits and the expert's number in the low ones sorts by
+// falling logit, then by number, with one minimum per comparison.  A lane keeps its best three
+// keys; k rounds of a minimum over the group take the best and pop it from its lane.  The exact
+// selection takes over for the warp where this one cannot tell: a lane gave all three; among the
+// chosen and those that agree with the last of them, some agree in the upper bits but not in
+// their logits; fewer than k logits are above -inf in x; or the sum is not that of a softmax
+// (NaN, infinities, overflow).  On random fp32 logits of 256 experts with k = 8 that is one
+// token in twenty.
 template <typename T, bool VEC, int G, int NC>
-__global__ void __launch_bounds__(THREADS) router_kernel(const RouterParams p) {
+__global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const RouterParams p) {
   extern __shared__ float dyn[];                       // [WARPS][experts] sums of p, then [experts] counts
   __shared__ float sf[THREADS];
   __shared__ int si[THREADS];
   constexpr int V = 8 * NC;
   constexpr int TOK = 32 / G;                          // tokens per warp
-  constexpr int SLOTS = G >= 32 ? 1 : 32 / G > 8 ? 8 : 32 / G;   // chosen experts a lane keeps (k <= 8 G and k <= 32)
+  constexpr int SLOTS = Slots<G>::N;
+  constexpr uint32_t IDX = 8 * G * NC - 1;             // the expert's bits of a key
+  constexpr uint32_t NONE = 0xFFFFFFFFu, CLOSED = 0xFF800000u;   // a key from here on: x = -inf, or no key
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane % G;
   int* scount = reinterpret_cast<int*>(dyn + WARPS * p.experts);
@@ -166,93 +268,116 @@ __global__ void __launch_bounds__(THREADS) router_kernel(const RouterParams p) {
   for (int j = 0; j < V; ++j) psum[j] = 0.f;
   int used_here = 0;
   const long long stride = static_cast<long long>(gridDim.x) * WARPS * TOK;
-  for (long long base = (static_cast<long long>(blockIdx.x) * WARPS + warp) * TOK; base < p.tokens; base += stride) {
+  const T* logits = static_cast<const T*>(p.logits);
+  Logits<T, VEC, G, NC> next;
+  auto fetch = [&](long long base) {
     const long long token = base + lane / G;
     const bool on = token < p.tokens && (!p.valid || p.valid[token] != 0);
+    next.load(logits + token * p.stride, on, p.experts, g);
+  };
+  long long base = (static_cast<long long>(blockIdx.x) * WARPS + warp) * TOK;
+  if (base < p.tokens) fetch(base);
+  for (; base < p.tokens; base += stride) {
+    const long long token = base + lane / G;
     float l[V];
-    load_logits<T, VEC, G, NC>(static_cast<const T*>(p.logits) + token * p.stride, on, p.experts, g, l);
-    uint32_t key[V];
+    next.get(p.experts, g, l);
+    const bool on = next.on;
+    if (base + stride < p.tokens) fetch(base + stride);
+    float m = l[0];
 #pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = key_of(l[j]);
-    // the lane's best two, the lower index first among equals; `last` is the last one taken from it
-    uint32_t k1 = 0, k2 = 0;
-    int i1 = 0, i2 = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const bool b1 = key[j] > k1, b2 = key[j] > k2;
-      k2 = b1 ? k1 : b2 ? key[j] : k2;
-      i2 = b1 ? i1 : b2 ? j : i2;
-      k1 = b1 ? key[j] : k1;
-      i1 = b1 ? j : i1;
-    }
-    bool second = true;                                // k2, i2 hold the lane's next
-    uint32_t sel_key[SLOTS];
-    int sel_idx[SLOTS];
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      sel_key[s] = 0;
-      sel_idx[s] = -1;
-    }
-    uint32_t top = 0;
-    for (int r = 0; r < p.k; ++r) {
-      const uint32_t best = group_max<G>(k1);
-      if (r == 0) top = best;
-      const uint32_t mine = k1 == best && best != 0 ? expert_of<G>(i1 / 8, g, i1 & 7) : 0x7FFFFFFFu;
-      const uint32_t who = group_min<G>(mine);
-#pragma unroll
-      for (int s = 0; s < SLOTS; ++s) {
-        if (r == s * G + g) {
-          sel_key[s] = best;
-          sel_idx[s] = best != 0 ? static_cast<int>(who) : -1;
-        }
-      }
-      const bool won = best != 0 && mine == who;
-      if (won) {
-        if (second) {
-          k1 = k2;
-          i1 = i2;
-          second = false;
-        } else {                                       // the best of what comes after the one just taken
-          const uint32_t lk = k1;
-          const int li = i1;
-          k1 = 0;
-          i1 = 0;
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const bool after = key[j] < lk || (key[j] == lk && j > li);
-            if (after && key[j] > k1) {
-              k1 = key[j];
-              i1 = j;
-            }
-          }
-        }
-      }
-    }
-    const bool used = on && top != 0;
-    const float m = value_of(top);
-    float sum = 0.f;
+    for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
+    m = group_fmax<G>(m);
+    const float down = 0.f - __fmul_ru(m, LOG2E);      // +0 for a maximum of either zero
+    float e[V], sum = 0.f;
+    uint32_t k1 = NONE, k2 = NONE, k3 = NONE;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      l[j] = key[j] == 0 ? 0.f : expf(l[j] - m);
-      sum += l[j];
+      const float x = fmaf(l[j], LOG2E, down);
+      e[j] = exp2_approx(x);
+      sum += e[j];
+      const uint32_t key = (__float_as_uint(x) & ~IDX) | static_cast<uint32_t>(expert_of<G>(j / 8, g, j & 7));
+      const uint32_t a = min(k1, key), b = max(k1, key), b2 = min(k2, b), d = max(k2, b);
+      k1 = a;
+      k2 = b2;
+      k3 = min(k3, d);
     }
     sum = group_add<G>(sum);
-    // NaN or +inf among the logits makes the sum NaN, and with it every probability of the token
-    if (top == 0xFFFFFFFFu || top == 0xFF800000u) sum = __uint_as_float(0x7FC00000u);
-    const float inv = used ? 1.f / sum : 0.f;
-    if (used) {
+    uint32_t sel[SLOTS], last = 0;
+    int idx[SLOTS];
 #pragma unroll
-      for (int j = 0; j < V; ++j) psum[j] = fmaf(l[j], inv, psum[j]);
-      if (g == 0) ++used_here;
-    }
-    float w[SLOTS], chosen = 0.f;
+    for (int s = 0; s < SLOTS; ++s) sel[s] = NONE;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      w[s] = sel_idx[s] >= 0 ? expf(value_of(sel_key[s]) - m) : 0.f;
-      chosen += w[s];
+      for (int q = 0; q < G && s * G + q < p.k; ++q) {
+        last = group_min<G>(k1);
+        if (q == g) sel[s] = last;
+        if (k1 == last) {
+          k1 = k2;
+          k2 = k3;
+          k3 = NONE;
+        }
+      }
+    }
+    const bool given = k1 == NONE;                     // the lane has no key left of its three
+    const uint32_t after = group_min<G>(k1);           // the first that is not chosen
+    // the chosen logits, and whether an order between neighbours was decided by the numbers alone
+    float w[SLOTS];
+    bool unsure = on && (given || last >= CLOSED || !(sum >= 0.5f));
+    const T* row = logits + token * p.stride;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      idx[s] = sel[s] < CLOSED && on ? static_cast<int>(sel[s] & IDX) : -1;
+      w[s] = idx[s] >= 0 ? to_float(row[idx[s]]) : 0.f;
+    }
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      if (s * G + 1 >= p.k) break;
+      const int r = s * G + g;
+      // the next in the order: the neighbour lane's, or at the group's end the first lane's next slot
+      const int from = (lane & ~(G - 1)) | ((g + 1) & (G - 1));
+      const uint32_t same_slot = __shfl_sync(FULL, sel[s], from);
+      const float same_value = __shfl_sync(FULL, w[s], from);
+      uint32_t nk = same_slot;
+      float nv = same_value;
+      if (s + 1 < SLOTS) {
+        const uint32_t up = __shfl_sync(FULL, sel[s + 1 < SLOTS ? s + 1 : s], from);
+        const float uv = __shfl_sync(FULL, w[s + 1 < SLOTS ? s + 1 : s], from);
+        if (g == G - 1) {
+          nk = up;
+          nv = uv;
+        }
+      }
+      if (r + 1 < p.k) unsure |= idx[s] >= 0 && (sel[s] & ~IDX) == (nk & ~IDX) && !(w[s] == nv);
+    }
+    // the same between the last chosen and all that agree with it
+    const bool tie = on && !unsure && last < CLOSED && (last & ~IDX) == (after & ~IDX);
+    if (__any_sync(FULL, tie)) {
+      const float worst = tie ? to_float(row[last & IDX]) : 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        unsure |= tie && (__float_as_uint(fmaf(l[j], LOG2E, down)) & ~IDX) == (last & ~IDX) && !(l[j] == worst);
+    }
+    bool some = on && m > MINUS_INF;
+    if (__any_sync(FULL, unsure)) {
+      select_exact<G, V>(l, g, p.k, idx, e, sum, m, some);
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) w[s] = idx[s] >= 0 ? expf(to_float(row[idx[s]]) - m) : 0.f;
+    } else {
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) w[s] = idx[s] >= 0 ? exp2_approx(fmaf(w[s], LOG2E, down)) : 0.f;
+    }
+    const bool used = on && some;
+    const float inv = used ? reciprocal(sum) : 0.f;
+    if (used) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) psum[j] = fmaf(e[j], inv, psum[j]);
+      if (g == 0) ++used_here;
     }
     float scale = inv;
     if (p.normalize) {
+      float chosen = 0.f;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) chosen += w[s];
       chosen = group_add<G>(chosen);
       scale = used ? (sum != sum ? sum : 1.f / chosen) : 0.f;
     }
@@ -261,9 +386,9 @@ __global__ void __launch_bounds__(THREADS) router_kernel(const RouterParams p) {
       for (int s = 0; s < SLOTS; ++s) {
         const int r = s * G + g;
         if (r < p.k) {
-          p.index[token * p.k + r] = sel_idx[s];
-          p.gate[token * p.k + r] = sel_idx[s] >= 0 ? w[s] * scale : 0.f;
-          if (sel_idx[s] >= 0) atomicAdd(&scount[sel_idx[s]], 1);
+          p.index[token * p.k + r] = idx[s];
+          p.gate[token * p.k + r] = idx[s] >= 0 ? w[s] * scale : 0.f;
+          if (idx[s] >= 0) atomicAdd(&scount[idx[s]], 1);
         }
       }
     }
@@ -312,24 +437,31 @@ __global__ void __launch_bounds__(512) router_finish_kernel(const RouterParams p
   const float mine = finish_experts(p, p.parts, e0, e1, sf, si);
   if (threadIdx.x == 0) share = mine;
   cluster_sync_all();
-  if (rank == 0 && threadIdx.x == 0) {
-    float all = 0.f;
-    for (int i = 0; i < FINISH_CTAS; ++i) all += __uint_as_float(ld_cluster_u32(map_to_rank(&share, i)));
+  if (rank == 0 && threadIdx.x < 32) {
+    const float of = threadIdx.x < FINISH_CTAS ? __uint_as_float(ld_cluster_u32(map_to_rank(&share, threadIdx.x))) : 0.f;
+    const float all = group_add<32>(of);
     int used = 0;
-    for (int i = 0; i < p.parts; ++i) used += p.part_used[i];
-    p.loss[0] = loss_of(all, used, p.experts, p.k);
-    p.used[0] = used;
+    for (int i = threadIdx.x; i < p.parts; i += 32) used += p.part_used[i];
+    used = __reduce_add_sync(FULL, used);
+    if (threadIdx.x == 0) {
+      p.loss[0] = loss_of(all, used, p.experts, p.k);
+      p.used[0] = used;
+    }
   }
   cluster_sync_all();                                  // the shares are read before their CTAs end
 }
 
 // ---------------------------------------------------------------- backward
 
+// With a_e = c_e (+ dgate at the chosen experts, unnormalised gates), dl = p (a - sum p a); with
+// normalised gates gate (dgate - sum gate dgate) is added at the chosen ones instead.  What
+// belongs to the chosen experts goes to their lanes through shared memory.
 template <typename T, bool VEC, int G, int NC>
-__global__ void __launch_bounds__(THREADS) router_bwd_kernel(const RouterBwdParams p) {
-  extern __shared__ float dyn[];                       // [WARPS][TOK][G * 8 * NC] what the gates add, zero between tokens
+__global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_bwd_kernel(const RouterBwdParams p) {
+  extern __shared__ __align__(16) float dyn[];         // [WARPS][TOK][8 G NC], zero between tokens
   constexpr int V = 8 * NC;
   constexpr int TOK = 32 / G;
+  constexpr int SLOTS = Slots<G>::N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane % G;
   float* add = dyn + (warp * TOK + lane / G) * (G * V);
@@ -349,81 +481,131 @@ __global__ void __launch_bounds__(THREADS) router_bwd_kernel(const RouterBwdPara
   }
   __syncwarp();
   const long long stride = static_cast<long long>(gridDim.x) * WARPS * TOK;
-  for (long long base = (static_cast<long long>(blockIdx.x) * WARPS + warp) * TOK; base < p.tokens; base += stride) {
+  const T* logits = static_cast<const T*>(p.logits);
+  Logits<T, VEC, G, NC> next;
+  int next_e[SLOTS];                                   // the lane's chosen experts of the next token
+  float next_d[SLOTS], next_w[SLOTS];                  // ... their dgate and gate
+  auto fetch = [&](long long base) {
     const long long token = base + lane / G;
     const bool on = token < p.tokens && (!p.valid || p.valid[token] != 0);
+    next.load(logits + token * p.stride, on, p.experts, g);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      if (s * G >= p.k) break;
+      const int r = s * G + g;
+      const bool has = on && r < p.k && p.dgate;
+      next_e[s] = has ? p.index[token * p.k + r] : -1;
+      next_d[s] = has ? p.dgate[token * p.k + r] : 0.f;
+      next_w[s] = has && p.normalize ? p.gate[token * p.k + r] : 0.f;
+    }
+  };
+  long long base = (static_cast<long long>(blockIdx.x) * WARPS + warp) * TOK;
+  if (base < p.tokens) fetch(base);
+  for (; base < p.tokens; base += stride) {
+    const long long token = base + lane / G;
     float l[V];
-    load_logits<T, VEC, G, NC>(static_cast<const T*>(p.logits) + token * p.stride, on, p.experts, g, l);
-    // the gates' share: t_r = gate_r dgate_r (- gate_r sum gate dgate if normalised), put where
-    // the expert's lane finds it
-    float dot = 0.f;
-    if (p.dgate && on) {
-      for (int r = g; r < p.k; r += G) {
-        if (p.index[token * p.k + r] >= 0) dot = fmaf(p.gate[token * p.k + r], p.dgate[token * p.k + r], dot);
+    next.get(p.experts, g, l);
+    const bool on = next.on;
+    int mine[SLOTS];
+    float part[SLOTS];
+    if (p.dgate) {
+      float dot = 0.f;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        if (s * G >= p.k) break;
+        mine[s] = next_e[s] < p.experts ? next_e[s] : -1;
+        part[s] = next_d[s];
+        if (p.normalize && mine[s] >= 0) dot = fmaf(next_w[s], next_d[s], dot);
+      }
+      if (p.normalize) {
+        dot = group_add<G>(dot);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+          if (s * G >= p.k) break;
+          part[s] = next_w[s] * (part[s] - dot);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        if (s * G >= p.k) break;
+        if (mine[s] >= 0) add[mine[s]] = part[s];
       }
     }
-    dot = group_add<G>(dot);
-    if (p.dgate && on) {
-      for (int r = g; r < p.k; r += G) {
-        const int e = p.index[token * p.k + r];
-        if (e >= 0 && e < p.experts)
-          add[e] = p.gate[token * p.k + r] * (p.dgate[token * p.k + r] - (p.normalize ? dot : 0.f));
-      }
-    }
+    if (base + stride < p.tokens) fetch(base + stride);
     float m = l[0];
 #pragma unroll
     for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
     m = group_fmax<G>(m);
-    float sum = 0.f;
-    bool any = false;                                  // some logit is not -inf (NaN counts)
+    const float shift = m * LOG2E;
+    float e[V], sum = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const bool off = l[j] == __uint_as_float(0xFF800000u);
-      any |= !off;
-      l[j] = off ? 0.f : expf(l[j] - m);
-      sum += l[j];
+      e[j] = exp2_approx(fmaf(l[j], LOG2E, -shift));
+      sum += e[j];
     }
     sum = group_add<G>(sum);
-    float pc = 0.f;
+    if (__any_sync(FULL, on && !(sum >= 0.5f))) {      // NaN, infinities, overflow, or no available expert
+      bool any = false;
+      float again = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) pc = fmaf(l[j], c[j], pc);
-    pc = group_add<G>(pc);
-    const bool some = group_max<G>(any ? 1u : 0u) != 0u;
-    const float inv = some ? 1.f / sum : 0.f;
-    const float back = pc * inv + (p.normalize ? 0.f : dot);
+      for (int j = 0; j < V; ++j) {
+        any |= !(l[j] == MINUS_INF);
+        e[j] = l[j] == MINUS_INF ? 0.f : expf(l[j] - m);
+        again += e[j];
+      }
+      again = group_add<G>(again);
+      sum = group_max<G>(any ? 1u : 0u) != 0u ? again : __uint_as_float(0x7F800000u);   // 1 / sum = 0: every p is 0
+    }
+    const float inv = on ? reciprocal(sum) : 0.f;
     __syncwarp();
+    float out[V], pa = 0.f;
+#pragma unroll
+    for (int q = 0; q < NC; ++q) {
+      const float4* from = reinterpret_cast<const float4*>(add + expert_of<G>(q, g, 0));
+      const float4 x = from[0], y = from[1];
+      const float t[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = 8 * q + j;
+        e[i] = on ? e[i] * inv : 0.f;
+        out[i] = t[j];
+        pa = fmaf(e[i], p.normalize ? c[i] : c[i] + t[j], pa);
+      }
+    }
+    pa = group_add<G>(pa);
     if (token < p.tokens) {
-      T* out = static_cast<T*>(p.dlogits) + token * p.dstride;
+      T* to = static_cast<T*>(p.dlogits) + token * p.dstride;
 #pragma unroll
       for (int q = 0; q < NC; ++q) {
         const int e0 = expert_of<G>(q, g, 0);
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float pr = l[8 * q + j] * inv;
-          f[j] = fmaf(pr, c[8 * q + j] - back, add[e0 + j]);
+          const int i = 8 * q + j;
+          f[j] = p.normalize ? fmaf(e[i], c[i] - pa, out[i]) : e[i] * (c[i] + out[i] - pa);
         }
         if constexpr (VEC) {
           if (e0 < p.experts) {
             Eight<T> o;
             o.set(f);
-            o.store(out + e0);
+            o.store(to + e0);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (e0 + j < p.experts) out[e0 + j] = from_float<T>(f[j]);
+            if (e0 + j < p.experts) to[e0 + j] = from_float<T>(f[j]);
         }
       }
     }
-    __syncwarp();
-    if (p.dgate && on) {
-      for (int r = g; r < p.k; r += G) {
-        const int e = p.index[token * p.k + r];
-        if (e >= 0 && e < p.experts) add[e] = 0.f;
+    if (p.dgate) {
+      __syncwarp();
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        if (s * G >= p.k) break;
+        if (mine[s] >= 0) add[mine[s]] = 0.f;
       }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -480,9 +662,13 @@ cudaError_t fwd(const RouterParams& p, cudaStream_t s, int* launches) {
   const int g = lanes_for(p.experts), nc = pieces_for(p.experts, g);
   const auto kernel = vec ? fwd_kernel<T, true>(g, nc) : fwd_kernel<T, false>(g, nc);
   const size_t smem = static_cast<size_t>(WARPS + 1) * p.experts * 4;
+  cudaError_t e;
+  if (smem > 40 * 1024 &&
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
+          cudaSuccess)
+    return e;
   kernel<<<p.parts, THREADS, smem, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches = 1;
   if (p.parts == 1) return cudaSuccess;
   *launches = 2;
@@ -497,7 +683,12 @@ cudaError_t bwd(const RouterBwdParams& p, int sms, cudaStream_t s) {
   const auto kernel = vec ? bwd_kernel<T, true>(g, nc) : bwd_kernel<T, false>(g, nc);
   const size_t smem = static_cast<size_t>(THREADS) * 8 * nc * 4;
   const int per = WARPS * (32 / g);
-  const int want = static_cast<int>((static_cast<long long>(p.tokens) + per - 1) / per), most = 4 * sms;
+  const int want = static_cast<int>((static_cast<long long>(p.tokens) + per - 1) / per), most = 2 * sms;
+  if (smem > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
   kernel<<<want < most ? want : most, THREADS, smem, s>>>(p);
   return cudaGetLastError();
 }
