@@ -98,8 +98,7 @@ struct RouterParams {
   int* counts;             // [experts]
   float* loss;             // [1]
   int* used;               // [1]
-  float* part_prob;        // [parts][experts]
-  int* part_count;         // [parts][experts]
+  int2* parts_sums;        // [parts][experts] {sum of p (fp32 bits), count}
   int* part_used;          // [parts]
   int parts;
 };

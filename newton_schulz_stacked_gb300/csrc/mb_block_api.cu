@@ -64,15 +64,14 @@ int router_call_checks(int64_t tokens, int64_t experts, int top_k, int type) {
 }
 
 struct RouterWorkspace {
-  size_t prob, count, used, end;
+  size_t sums, used, end;
 };
 
 RouterWorkspace router_workspace(int64_t tokens, int64_t experts) {
   const size_t parts = router_parts(static_cast<int>(tokens), static_cast<int>(experts), 1 << 20);
   RouterWorkspace w{};
-  w.prob = 0;
-  w.count = w.prob + parts * experts * 4;
-  w.used = w.count + parts * experts * 4;
+  w.sums = 0;
+  w.used = w.sums + parts * experts * sizeof(int2);
   w.end = w.used + parts * 4;
   return w;
 }
@@ -265,8 +264,7 @@ int mb_router(const void* logits, int64_t stride, int type, const uint8_t* valid
   p.loss = loss;
   p.used = used;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part_prob = reinterpret_cast<float*>(ws + w.prob);
-  p.part_count = reinterpret_cast<int*>(ws + w.count);
+  p.parts_sums = reinterpret_cast<int2*>(ws + w.sums);
   p.part_used = reinterpret_cast<int*>(ws + w.used);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = launch_router(p, type, sms, st, &launches);

@@ -86,6 +86,10 @@ __device__ __forceinline__ float group_fmax(float x) {
   return x;
 }
 
+__device__ __forceinline__ void count_one(int* counter) {
+  asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(smem_u32(counter)) : "memory");
+}
+
 // Expert of element j of piece c of lane g in its group.
 template <int G>
 __device__ __forceinline__ int expert_of(int c, int g, int j) { return (c * G + g) * 8 + j; }
@@ -104,34 +108,66 @@ struct Logits {
       const int e0 = expert_of<G>(c, g, 0);
       if constexpr (VEC) {
         if (on && e0 < experts) v[c].load(row + e0);
+        else v[c].fill(minus_inf_bits(T()));
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[8 * c + j] = on && e0 + j < experts ? to_float(row[e0 + j]) : MINUS_INF;
       }
     }
   }
-  __device__ __forceinline__ void get(int experts, int g, float (&l)[8 * NC]) const {
+  __device__ __forceinline__ void get(float (&l)[8 * NC]) const {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if constexpr (VEC) {
-        float x[8];
-        v[c].get(x);
-        const bool in = on && expert_of<G>(c, g, 0) < experts;
+      float x[8];
+      if constexpr (VEC) v[c].get(x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) l[8 * c + j] = in ? x[j] : MINUS_INF;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) l[8 * c + j] = f[8 * c + j];
-      }
+      for (int j = 0; j < 8; ++j) l[8 * c + j] = VEC ? x[j] : f[8 * c + j];
     }
   }
 };
 
-// The counts and the loss from the CTAs' sums: E experts in `n` rows of sums; called by the
-// `threads` threads of one CTA for the experts [e_begin, e_end); returns (to every thread) the
-// share of  sum_e counts_e sum_t p_te  of these experts.  smem: threads floats and ints.
-__device__ __forceinline__ float finish_experts(const RouterParams& p, int n, int e_begin, int e_end, float* sf,
-                                                int* si) {
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
+  const uint32_t lo = min(a, b);
+  b = max(a, b);
+  a = lo;
+}
+
+// A lane's least D of V keys, in order, by networks of minima and maxima: all eight of eight (19
+// comparisons), or the least four by fours.
+template <int D, int V>
+__device__ __forceinline__ void least(const uint32_t (&key)[V], uint32_t (&out)[D]) {
+  if constexpr (D == 8) {
+    static_assert(V == 8, "all of a lane's keys");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[j] = key[j];
+    order2(out[0], out[2]), order2(out[1], out[3]), order2(out[4], out[6]), order2(out[5], out[7]);
+    order2(out[0], out[4]), order2(out[1], out[5]), order2(out[2], out[6]), order2(out[3], out[7]);
+    order2(out[0], out[1]), order2(out[2], out[3]), order2(out[4], out[5]), order2(out[6], out[7]);
+    order2(out[2], out[4]), order2(out[3], out[5]);
+    order2(out[1], out[4]), order2(out[3], out[6]);
+    order2(out[1], out[2]), order2(out[3], out[4]), order2(out[5], out[6]);
+  } else {
+    static_assert(D == 4, "");
+#pragma unroll
+    for (int q = 0; q < V; q += 4) {
+      uint32_t f[4] = {key[q], key[q + 1], key[q + 2], key[q + 3]};
+      order2(f[0], f[1]), order2(f[2], f[3]), order2(f[0], f[2]), order2(f[1], f[3]), order2(f[1], f[2]);
+      if (q == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[j] = f[j];
+      } else {                                         // the least four of both: a bitonic sequence, sorted
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[j] = min(out[j], f[3 - j]);
+        order2(out[0], out[2]), order2(out[1], out[3]), order2(out[0], out[1]), order2(out[2], out[3]);
+      }
+    }
+  }
+}
+
+// The counts and the loss from the CTAs' sums ({sum of p, count} of every expert, n rows of them);
+// called by the threads of one CTA for the experts [e_begin, e_end); returns (to every thread) the
+// share of  sum_e counts_e sum_t p_te  of these experts.  sums: 33 entries per warp.
+__device__ __forceinline__ float finish_experts(const RouterParams& p, int n, int e_begin, int e_end, int2* sums) {
   // 32 experts by (threads / 32) slices of the rows at a time, added in a fixed order
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, slices = blockDim.x >> 5;
   float share = 0.f;
@@ -140,33 +176,31 @@ __device__ __forceinline__ float finish_experts(const RouterParams& p, int n, in
     float a = 0.f;
     int c = 0;
     if (e < e_end) {
-#pragma unroll 4
+#pragma unroll 10
       for (int i = slice; i < n; i += slices) {
-        a += p.part_prob[static_cast<size_t>(i) * p.experts + e];
-        c += p.part_count[static_cast<size_t>(i) * p.experts + e];
+        const int2 v = p.parts_sums[static_cast<size_t>(i) * p.experts + e];
+        a += __int_as_float(v.x);
+        c += v.y;
       }
     }
-    sf[threadIdx.x] = a;
-    si[threadIdx.x] = c;
+    sums[slice * 33 + lane] = make_int2(__float_as_int(a), c);
     __syncthreads();
-    if (slice == 0) {
-      for (int i = 1; i < slices; ++i) {
-        a += sf[i * 32 + lane];
-        c += si[i * 32 + lane];
-      }
-      if (e < e_end) {
-        p.counts[e] = c;
+    for (int i = slice; i < 32; i += slices) {         // expert e0 + i: the slices' sums over a warp's lanes
+      const int2 v = lane < slices ? sums[lane * 33 + i] : make_int2(0, 0);
+      a = group_add<32>(__int_as_float(v.x));
+      c = __reduce_add_sync(FULL, v.y);
+      if (e0 + i < e_end) {
+        if (lane == 0) p.counts[e0 + i] = c;
         share += a * static_cast<float>(c);
       }
     }
     __syncthreads();
   }
-  if (slice == 0) {
-    share = group_add<32>(share);
-    if (lane == 0) sf[0] = share;
-  }
+  if (lane == 0) sums[slice].x = __float_as_int(share);
   __syncthreads();
-  return sf[0];
+  share = group_add<32>(lane < slices ? __int_as_float(sums[lane].x) : 0.f);
+  __syncthreads();
+  return share;
 }
 
 __device__ __forceinline__ float loss_of(float share, int used, int experts, int k) {
@@ -184,33 +218,34 @@ struct Slots {
 };
 
 // The k largest of a token's logits for any values: k rounds over exact keys, the winner's lane
-// looking for its next among what comes after the one just taken.  Writes the lane's chosen
-// experts, and the softmax's terms and sum in the plain form exp(l - max).
-template <int G, int V>
-__device__ __forceinline__ void select_exact(const float (&l)[V], int g, int k, int (&idx)[Slots<G>::N], float (&e)[V],
-                                          float& sum, float& m, bool& some) {
-  constexpr int SLOTS = Slots<G>::N;
+// looking for its next among what comes after the one just taken.  Puts the chosen experts into
+// `order` (-1: none) and returns the softmax's maximum and sum in the plain form exp(l - max).
+// A call of its own, with nothing passed in registers but the row: it is rare, and inlined it
+// cost the common way 58 of 340 instructions per token.
+struct ExactSoftmax {
+  float m, sum;
+  bool some;
+};
+template <typename T, int G, int V>
+__device__ __noinline__ ExactSoftmax select_exact(const T* row, bool on, int experts, int k, int g, uint32_t* order) {
   uint32_t key[V], k1 = 0;
   int i1 = 0;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    key[j] = key_of(l[j]);
+    const int e = expert_of<G>(j / 8, g, j & 7);
+    key[j] = on && e < experts ? key_of(to_float(row[e])) : 0;
     if (key[j] > k1) {
       k1 = key[j];
       i1 = j;
     }
   }
   uint32_t top = 0;
-#pragma unroll
-  for (int s = 0; s < SLOTS; ++s) idx[s] = -1;
   for (int r = 0; r < k; ++r) {
     const uint32_t best = group_max<G>(k1);
     if (r == 0) top = best;
     const uint32_t mine = k1 == best && best != 0 ? expert_of<G>(i1 / 8, g, i1 & 7) : 0x7FFFFFFFu;
     const uint32_t who = group_min<G>(mine);
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s)
-      if (r == s * G + g && best != 0) idx[s] = static_cast<int>(who);
+    order[r] = best != 0 ? who : 0xFFFFFFFFu;
     if (best != 0 && mine == who) {
       const uint32_t lk = k1;
       const int li = i1;
@@ -225,143 +260,145 @@ __device__ __forceinline__ void select_exact(const float (&l)[V], int g, int k, 
       }
     }
   }
-  some = top != 0;
-  m = value_of(top);
-  sum = 0.f;
+  ExactSoftmax x{value_of(top), 0.f, top != 0};
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    e[j] = key[j] == 0 ? 0.f : expf(l[j] - m);
-    sum += e[j];
-  }
-  sum = group_add<G>(sum);
+  for (int j = 0; j < V; ++j) x.sum += key[j] == 0 ? 0.f : expf(value_of(key[j]) - x.m);
+  x.sum = group_add<G>(x.sum);
   // NaN or +inf among the logits makes the sum NaN, and with it every probability of the token
-  if (top >= 0xFF800000u) sum = __uint_as_float(0x7FC00000u);
+  if (top >= 0xFF800000u) x.sum = __uint_as_float(0x7FC00000u);
+  return x;
 }
 
 // Selection without conditions per element.  With c = max * log2(e) rounded up, x = l log2(e) - c
 // is at most 0, monotone in l, and the exponent the softmax needs anyway.  The bits of such an x
 // grow as l falls, so a key of x's upper bits and the expert's number in the low ones sorts by
-// falling logit, then by number, with one minimum per comparison.  A lane keeps its best three
-// keys; k rounds of a minimum over the group take the best and pop it from its lane.  The exact
-// selection takes over for the warp where this one cannot tell: a lane gave all three; among the
-// chosen and those that agree with the last of them, some agree in the upper bits but not in
+// falling logit, then by number, with one minimum per comparison.  A lane keeps its best few keys
+// (D); rounds of a minimum over the group take the best and pop it from its lane.  The exact
+// selection takes over for the warp where this one cannot tell: a lane gave all it kept; among
+// the chosen and those that agree with the last of them, some agree in the upper bits but not in
 // their logits; fewer than k logits are above -inf in x; or the sum is not that of a softmax
-// (NaN, infinities, overflow).  On random fp32 logits of 256 experts with k = 8 that is one
-// token in twenty.
+// (NaN, infinities, overflow).  It costs ten times the instructions, so a lane
+// keeps four keys of 16 or 32 lanes (on normal logits with k = 8, one token in 300 of 128 experts
+// and one in 1000 of 256 needs a fifth; keeping three, one in 25 of 256 took 22 of 69 us), and
+// all eight where fewer lanes share the experts.
 template <typename T, bool VEC, int G, int NC>
 __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const RouterParams p) {
-  extern __shared__ float dyn[];                       // [WARPS][experts] sums of p, then [experts] counts
-  __shared__ float sf[THREADS];
-  __shared__ int si[THREADS];
+  // [WARPS][experts] sums of p, [experts] counts, [WARPS][TOK][k + 1] chosen keys
+  extern __shared__ float dyn[];
+  __shared__ int2 sums[WARPS * 33];
+  __shared__ int warp_used[WARPS];
   constexpr int V = 8 * NC;
   constexpr int TOK = 32 / G;                          // tokens per warp
   constexpr int SLOTS = Slots<G>::N;
-  constexpr uint32_t IDX = 8 * G * NC - 1;             // the expert's bits of a key
-  constexpr uint32_t NONE = 0xFFFFFFFFu, CLOSED = 0xFF800000u;   // a key from here on: x = -inf, or no key
+  constexpr uint32_t IDX = NC == 1 ? 255 : 256 * NC - 1;   // the expert's bits of a key
+  constexpr uint32_t CLOSED = 0xFF800000u;             // a key from here on: x = -inf
+  constexpr uint32_t NONE = 0xFFFFFFFFu;               // no key
+  constexpr int D = G >= 16 ? 4 : 8;                   // keys a lane keeps
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane % G;
   int* scount = reinterpret_cast<int*>(dyn + WARPS * p.experts);
+  uint32_t* order = reinterpret_cast<uint32_t*>(scount + p.experts) + (warp * TOK + lane / G) * (p.k + 1);
   for (int e = threadIdx.x; e < p.experts; e += THREADS) scount[e] = 0;
   __syncthreads();
   float psum[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) psum[j] = 0.f;
+  // the bytes that the lane's eight experts have in keys of one piece
+  const uint32_t low_bytes = static_cast<uint32_t>(8 * g) * 0x01010101u + 0x03020100u;
+  const uint32_t high_bytes = low_bytes + 0x04040404u;
   int used_here = 0;
-  const long long stride = static_cast<long long>(gridDim.x) * WARPS * TOK;
-  const T* logits = static_cast<const T*>(p.logits);
+  const int stride = static_cast<int>(gridDim.x) * WARPS * TOK;   // tokens < 2^31, checked before the launch
   Logits<T, VEC, G, NC> next;
-  auto fetch = [&](long long base) {
-    const long long token = base + lane / G;
-    const bool on = token < p.tokens && (!p.valid || p.valid[token] != 0);
-    next.load(logits + token * p.stride, on, p.experts, g);
-  };
-  long long base = (static_cast<long long>(blockIdx.x) * WARPS + warp) * TOK;
-  if (base < p.tokens) fetch(base);
-  for (; base < p.tokens; base += stride) {
-    const long long token = base + lane / G;
+  long long token = static_cast<long long>(blockIdx.x * WARPS + warp) * TOK + lane / G;
+  const T* row = static_cast<const T*>(p.logits) + token * p.stride;   // of `token`, then of the next one to load
+  const long long row_step = stride * p.stride;
+  auto fetch = [&](long long t) { next.load(row, t < p.tokens && (!p.valid || p.valid[t] != 0), p.experts, g); };
+  long long at = token * p.k + g;                      // of the lane's first chosen expert in index and gate
+  const long long at_step = static_cast<long long>(stride) * p.k;
+  const long long first = token - lane / G;            // of the warp's tokens: the loop runs by it
+  if (first < p.tokens) fetch(token);
+  for (long long base = first; base < p.tokens; base += stride, token += stride) {
     float l[V];
-    next.get(p.experts, g, l);
+    next.get(l);
     const bool on = next.on;
-    if (base + stride < p.tokens) fetch(base + stride);
+    const T* here = row;
+    row += row_step;
+    if (base + stride < p.tokens) fetch(token + stride);
     float m = l[0];
 #pragma unroll
     for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
     m = group_fmax<G>(m);
     const float down = 0.f - __fmul_ru(m, LOG2E);      // +0 for a maximum of either zero
     float e[V], sum = 0.f;
-    uint32_t k1 = NONE, k2 = NONE, k3 = NONE;
+    uint32_t key[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float x = fmaf(l[j], LOG2E, down);
       e[j] = exp2_approx(x);
       sum += e[j];
-      const uint32_t key = (__float_as_uint(x) & ~IDX) | static_cast<uint32_t>(expert_of<G>(j / 8, g, j & 7));
-      const uint32_t a = min(k1, key), b = max(k1, key), b2 = min(k2, b), d = max(k2, b);
-      k1 = a;
-      k2 = b2;
-      k3 = min(k3, d);
+      if constexpr (NC == 1)      // the expert's byte in place of the lowest one
+        key[j] = __byte_perm(__float_as_uint(x), j < 4 ? low_bytes : high_bytes, 0x3210 + 4 + (j & 3));
+      else
+        key[j] = (__float_as_uint(x) & ~IDX) | static_cast<uint32_t>(expert_of<G>(j / 8, g, j & 7));
     }
     sum = group_add<G>(sum);
-    uint32_t sel[SLOTS], last = 0;
+    uint32_t own[D];
+    least<D, V>(key, own);
+    const uint32_t deepest = own[D - 1];
+    // the k best of the group and the first after them, in order; a lane that has given the last
+    // of its kept keys gives it again, and is found by that
+#pragma unroll 3
+    for (int r = 0; r <= p.k; ++r) {
+      const uint32_t best = group_min<G>(own[0]);
+      const bool won = own[0] == best;
+      order[r] = best;                                 // the same value from every lane of the group
+#pragma unroll
+      for (int d = 0; d + 1 < D; ++d) own[d] = won ? own[d + 1] : own[d];
+      if constexpr (D == V) own[D - 1] = won ? NONE : own[D - 1];
+    }
+    __syncwarp();
+    const uint32_t last = order[p.k - 1], after = order[p.k];
+    bool unsure = on && ((D < V && deepest <= last) || last >= CLOSED || !(sum >= 0.5f));
     int idx[SLOTS];
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) sel[s] = NONE;
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      for (int q = 0; q < G && s * G + q < p.k; ++q) {
-        last = group_min<G>(k1);
-        if (q == g) sel[s] = last;
-        if (k1 == last) {
-          k1 = k2;
-          k2 = k3;
-          k3 = NONE;
-        }
-      }
-    }
-    const bool given = k1 == NONE;                     // the lane has no key left of its three
-    const uint32_t after = group_min<G>(k1);           // the first that is not chosen
-    // the chosen logits, and whether an order between neighbours was decided by the numbers alone
-    float w[SLOTS];
-    bool unsure = on && (given || last >= CLOSED || !(sum >= 0.5f));
-    const T* row = logits + token * p.stride;
+    float w[SLOTS];                                    // the chosen logits, then the softmax's terms
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      idx[s] = sel[s] < CLOSED && on ? static_cast<int>(sel[s] & IDX) : -1;
-      w[s] = idx[s] >= 0 ? to_float(row[idx[s]]) : 0.f;
-    }
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
-      if (s * G + 1 >= p.k) break;
       const int r = s * G + g;
-      // the next in the order: the neighbour lane's, or at the group's end the first lane's next slot
-      const int from = (lane & ~(G - 1)) | ((g + 1) & (G - 1));
-      const uint32_t same_slot = __shfl_sync(FULL, sel[s], from);
-      const float same_value = __shfl_sync(FULL, w[s], from);
-      uint32_t nk = same_slot;
-      float nv = same_value;
-      if (s + 1 < SLOTS) {
-        const uint32_t up = __shfl_sync(FULL, sel[s + 1 < SLOTS ? s + 1 : s], from);
-        const float uv = __shfl_sync(FULL, w[s + 1 < SLOTS ? s + 1 : s], from);
-        if (g == G - 1) {
-          nk = up;
-          nv = uv;
+      idx[s] = -1;
+      w[s] = 0.f;
+      if (s * G < p.k && r < p.k && on) {
+        const uint32_t mine = order[r], then = order[r + 1];
+        if (mine < CLOSED) {
+          idx[s] = static_cast<int>(mine & IDX);
+          w[s] = to_float(here[idx[s]]);
+          // neighbours whose order the numbers alone decided have to be equal
+          if (r + 1 < p.k && (mine & ~IDX) == (then & ~IDX)) unsure |= !(w[s] == to_float(here[then & IDX]));
         }
       }
-      if (r + 1 < p.k) unsure |= idx[s] >= 0 && (sel[s] & ~IDX) == (nk & ~IDX) && !(w[s] == nv);
     }
-    // the same between the last chosen and all that agree with it
-    const bool tie = on && !unsure && last < CLOSED && (last & ~IDX) == (after & ~IDX);
+    // and so do the last chosen and all that agree with it
+    const bool tie = on && !unsure && (last & ~IDX) == (after & ~IDX);
     if (__any_sync(FULL, tie)) {
-      const float worst = tie ? to_float(row[last & IDX]) : 0.f;
+      const float worst = tie ? to_float(here[last & IDX]) : 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j)
         unsure |= tie && (__float_as_uint(fmaf(l[j], LOG2E, down)) & ~IDX) == (last & ~IDX) && !(l[j] == worst);
     }
     bool some = on && m > MINUS_INF;
     if (__any_sync(FULL, unsure)) {
-      select_exact<G, V>(l, g, p.k, idx, e, sum, m, some);
+      __syncwarp();
+      const ExactSoftmax x = select_exact<T, G, V>(here, on, p.experts, p.k, g, order);
+      __syncwarp();
+      sum = x.sum;
+      some = x.some;
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s) w[s] = idx[s] >= 0 ? expf(to_float(row[idx[s]]) - m) : 0.f;
+      for (int j = 0; j < V; ++j) e[j] = l[j] == MINUS_INF ? 0.f : expf(l[j] - x.m);
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        const int r = s * G + g;
+        idx[s] = r < p.k ? static_cast<int>(order[r]) : -1;
+        w[s] = idx[s] >= 0 ? expf(to_float(here[idx[s]]) - x.m) : 0.f;
+      }
     } else {
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) w[s] = idx[s] >= 0 ? exp2_approx(fmaf(w[s], LOG2E, down)) : 0.f;
@@ -373,23 +410,24 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       for (int j = 0; j < V; ++j) psum[j] = fmaf(e[j], inv, psum[j]);
       if (g == 0) ++used_here;
     }
-    float scale = inv;
+    float scale = inv;                                 // of the terms of the chosen: 0 or NaN with them
     if (p.normalize) {
       float chosen = 0.f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) chosen += w[s];
       chosen = group_add<G>(chosen);
-      scale = used ? (sum != sum ? sum : 1.f / chosen) : 0.f;
+      scale = used ? (sum != sum ? sum : reciprocal(chosen)) : 0.f;
     }
-    if (token < p.tokens) {
+    int* to_index = p.index + at;
+    float* to_gate = p.gate + at;
+    at += at_step;
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s) {
-        const int r = s * G + g;
-        if (r < p.k) {
-          p.index[token * p.k + r] = idx[s];
-          p.gate[token * p.k + r] = idx[s] >= 0 ? w[s] * scale : 0.f;
-          if (idx[s] >= 0) atomicAdd(&scount[idx[s]], 1);
-        }
+    for (int s = 0; s < SLOTS; ++s) {
+      if (s * G >= p.k) break;
+      if (s * G + g < p.k && token < p.tokens) {
+        to_index[s * G] = idx[s];
+        to_gate[s * G] = w[s] * scale;                 // w is 0 at a place without an expert
+        if (idx[s] >= 0) count_one(&scount[idx[s]]);
       }
     }
   }
@@ -401,21 +439,20 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
     if (lane < G && e < p.experts) dyn[warp * p.experts + e] = psum[j];
   }
   used_here = __reduce_add_sync(FULL, used_here);
-  if (lane == 0) si[warp] = used_here;
+  if (lane == 0) warp_used[warp] = used_here;
   let_next_kernel_start();
   __syncthreads();
   for (int e = threadIdx.x; e < p.experts; e += THREADS) {
     float a = 0.f;
     for (int w = 0; w < WARPS; ++w) a += dyn[w * p.experts + e];
-    p.part_prob[static_cast<size_t>(blockIdx.x) * p.experts + e] = a;
-    p.part_count[static_cast<size_t>(blockIdx.x) * p.experts + e] = scount[e];
+    p.parts_sums[static_cast<size_t>(blockIdx.x) * p.experts + e] = make_int2(__float_as_int(a), scount[e]);
   }
   int total = 0;
-  for (int w = 0; w < WARPS; ++w) total += si[w];
+  for (int w = 0; w < WARPS; ++w) total += warp_used[w];
   if (threadIdx.x == 0) p.part_used[blockIdx.x] = total;
   if (gridDim.x == 1) {                                // the only CTA finishes by itself
     __syncthreads();
-    const float share = finish_experts(p, 1, 0, p.experts, sf, si);
+    const float share = finish_experts(p, 1, 0, p.experts, sums);
     if (threadIdx.x == 0) {
       p.loss[0] = loss_of(share, total, p.experts, p.k);
       p.used[0] = total;
@@ -426,15 +463,14 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
 // A cluster of CTAs shares the experts; the first one adds the shares of the loss.
 constexpr int FINISH_CTAS = 8;
 
-__global__ void __launch_bounds__(512) router_finish_kernel(const RouterParams p) {
-  __shared__ float sf[512];
-  __shared__ int si[512];
+__global__ void __launch_bounds__(1024) router_finish_kernel(const RouterParams p) {
+  __shared__ int2 sums[32 * 33];
   __shared__ float share;
   wait_for_previous_kernel();
   const uint32_t rank = cluster_ctarank();
   const int per = (p.experts + FINISH_CTAS - 1) / FINISH_CTAS;
   const int e0 = static_cast<int>(rank) * per, e1 = e0 + per < p.experts ? e0 + per : p.experts;
-  const float mine = finish_experts(p, p.parts, e0, e1, sf, si);
+  const float mine = finish_experts(p, p.parts, e0, e1, sums);
   if (threadIdx.x == 0) share = mine;
   cluster_sync_all();
   if (rank == 0 && threadIdx.x < 32) {
@@ -504,7 +540,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_bwd_kernel(co
   for (; base < p.tokens; base += stride) {
     const long long token = base + lane / G;
     float l[V];
-    next.get(p.experts, g, l);
+    next.get(l);
     const bool on = next.on;
     int mine[SLOTS];
     float part[SLOTS];
@@ -661,7 +697,7 @@ cudaError_t fwd(const RouterParams& p, cudaStream_t s, int* launches) {
   const bool vec = p.experts % 8 == 0 && vec_rows(p.logits, p.stride, sizeof(T), p.tokens);
   const int g = lanes_for(p.experts), nc = pieces_for(p.experts, g);
   const auto kernel = vec ? fwd_kernel<T, true>(g, nc) : fwd_kernel<T, false>(g, nc);
-  const size_t smem = static_cast<size_t>(WARPS + 1) * p.experts * 4;
+  const size_t smem = (static_cast<size_t>(WARPS + 1) * p.experts + WARPS * (32 / g) * (p.k + 1)) * 4;
   cudaError_t e;
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
@@ -672,7 +708,7 @@ cudaError_t fwd(const RouterParams& p, cudaStream_t s, int* launches) {
   *launches = 1;
   if (p.parts == 1) return cudaSuccess;
   *launches = 2;
-  return launch_after(router_finish_kernel, dim3(FINISH_CTAS), dim3(512), 0, s, p, FINISH_CTAS);
+  return launch_after(router_finish_kernel, dim3(FINISH_CTAS), dim3(1024), 0, s, p, FINISH_CTAS);
 }
 
 template <typename T>

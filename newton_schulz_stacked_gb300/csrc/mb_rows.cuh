@@ -12,6 +12,11 @@ namespace mb {
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+// -inf as Eight::fill takes it.
+__device__ __forceinline__ uint32_t minus_inf_bits(float) { return 0xFF800000u; }
+__device__ __forceinline__ uint32_t minus_inf_bits(__nv_bfloat16) { return 0xFF80FF80u; }
+__device__ __forceinline__ uint32_t minus_inf_bits(__half) { return 0xFC00FC00u; }
+
 template <typename T>
 __device__ __forceinline__ T from_float(float x);
 template <>
@@ -47,9 +52,11 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-  __device__ __forceinline__ void zero() {
+  __device__ __forceinline__ void zero() { fill(0); }
+  // Every element as the 32-bit pattern `u` holds it (a pair of 16-bit elements, or one of fp32).
+  __device__ __forceinline__ void fill(uint32_t u) {
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < WORDS; ++i) w[i] = make_uint4(u, u, u, u);
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
