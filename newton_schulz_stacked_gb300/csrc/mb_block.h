@@ -16,9 +16,8 @@ void api_launched(int label, int launches, cudaStream_t stream);   // counts lau
 
 // ---------------------------------------------------------------- layer norm
 
-constexpr int LN_FWD_MAX_COLS = 32768;   // widest row one CTA keeps in registers, forward
-constexpr int LN_BWD_MAX_COLS = 8192;    // and backward; wider rows are read again from memory
-constexpr int LN_MAX_PARTS = 304;        // partial sums of the weight's gradient, rows of [2][cols]
+constexpr int LN_MAX_COLS = 8192;     // widest row that stays in registers; wider ones are read again from memory
+constexpr int LN_MAX_PARTS = 456;     // partial sums of the weight's gradient, rows of [2][cols]
 
 struct LnFwdParams {
   const void* x;

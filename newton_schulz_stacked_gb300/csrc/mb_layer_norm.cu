@@ -6,6 +6,8 @@
 //
 // Both directions are bound by HBM (two and three passes of the elements' size): a row is read
 // once and stays in its threads' registers through the statistics and the result.
+#include <algorithm>
+
 #include "mb_block.h"
 #include "mb_rows.cuh"
 #include "muonbank.h"
@@ -13,50 +15,102 @@
 namespace mb {
 namespace {
 
-// Sum over the threads of a row: `tpr` lanes of a warp, or the whole CTA (MULTI) through
-// shared memory.  Every thread gets the sum, formed in the same order in each of them.
-template <bool MULTI, int R>
-__device__ __forceinline__ void row_sum(float (&s)[R], int tpr, float* smem) {
-  const int width = MULTI ? 32 : tpr;
-  for (int o = width >> 1; o > 0; o >>= 1)
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Sums over the threads of a row, N of them at once; every thread gets them, formed in the same
+// order in each.  `part` has one entry per warp of the CTA; a group of more than one warp waits
+// at its own barrier, and takes the two halves of `part` in turn (a half is written again only
+// after the barrier behind the other half's use).
+template <int N, int WARPS>
+struct RowSums {
+  float (*part)[WARPS][N];
+  int tpr, warp, first_warp, barrier, parity;
+  __device__ __forceinline__ RowSums(float (*smem)[WARPS][N], int tpr_, int group)
+      : part(smem), tpr(tpr_), warp(threadIdx.x >> 5), first_warp(group * (tpr_ >> 5)), barrier(1 + group), parity(0) {}
+  __device__ __forceinline__ void operator()(float (&s)[N]) {
+    const int width = tpr < 32 ? tpr : 32;
+    for (int o = width >> 1; o > 0; o >>= 1)
 #pragma unroll
-    for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], o);
-  if constexpr (MULTI) {
-    static_assert(R == 1, "a CTA holds one row at a time");
-    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    __syncthreads();                       // the previous sum has been read
-    if ((threadIdx.x & 31) == 0) smem[warp] = s[0];
-    __syncthreads();
-    float t = 0.f;
-    for (int i = 0; i < nw; ++i) t += smem[i];
-    s[0] = t;
+      for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+    if (tpr > 32) {
+      if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int k = 0; k < N; ++k) part[parity][warp][k] = s[k];
+      group_barrier(barrier, tpr);
+#pragma unroll
+      for (int k = 0; k < N; ++k) s[k] = 0.f;
+      for (int u = 0; u < tpr >> 5; ++u)
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] += part[parity][first_warp + u][k];
+      parity ^= 1;
+    }
   }
+};
+
+// The same over a whole CTA, for the kernels that give it one row at a time.
+__device__ __forceinline__ float cta_sum(float s, float* smem) {
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  __syncthreads();                         // the previous sum has been read
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0.f;
+  for (int i = 0; i < static_cast<int>(blockDim.x) >> 5; ++i) s += smem[i];
+  return s;
 }
 
 // ---------------------------------------------------------------- forward
 
-// R rows at a time per group of tpr threads (MULTI: one row per CTA), NV pieces of eight
-// elements per thread and row.  The variance sums squares of differences from the mean, over
-// the registers: no cancellation however far the mean is from zero.
-template <typename T, bool VEC, int NV, int R, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? 1024 : 256) ln_fwd_kernel(const LnFwdParams p) {
-  __shared__ float smem[32];
+// CTAs per SM of the kernel below: 80 registers with 16-bit vectors, else 128.
+template <typename T, bool VEC>
+constexpr int fwd_ctas() { return VEC && sizeof(T) == 2 ? 3 : 2; }
+
+// Rows of up to 1024 elements: tpr lanes of a warp hold a row in NV pieces of eight elements each
+// and take R rows at a time, the next R already being loaded; no barrier in the loop.  Weight and
+// bias wait in shared memory, in fp32 and in the order in which the lanes read them.  The variance
+// sums squares of differences from the mean, over the registers: no cancellation however far the
+// mean is from zero.
+template <typename T, bool VEC, int NV, int R>
+__global__ void __launch_bounds__(256, fwd_ctas<T, VEC>()) ln_fwd_kernel(const LnFwdParams p) {
+  extern __shared__ __align__(16) float wb[];          // [2][NV][8 or (halves of) 4][tpr]
   using P = Piece<T, VEC>;
   const int tpr = p.tpr, cols = p.cols;
-  const int t = MULTI ? threadIdx.x : threadIdx.x % tpr;
-  const int groups = MULTI ? 1 : blockDim.x / tpr, g = MULTI ? 0 : threadIdx.x / tpr;
+  const int t = threadIdx.x % tpr, g = threadIdx.x / tpr, groups = blockDim.x / tpr;
   const float inv_n = 1.f / static_cast<float>(cols);
-  const long long step = static_cast<long long>(groups) * R;
-  for (long long base = blockIdx.x * step; base < p.rows; base += gridDim.x * step) {
-    P x[R][NV];
-    float s[R];
+  const long long step = static_cast<long long>(groups) * R, stride = step * gridDim.x;
+  P x[R][NV], next[R][NV];
+  auto fetch = [&](long long base) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long row = base + r * groups + g;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        x[r][v].load(static_cast<const T*>(p.x) + row * p.x_stride, cols, v, t, tpr, row < p.rows);
+        next[r][v].load(static_cast<const T*>(p.x) + row * p.x_stride, cols, v, t, tpr, row < p.rows);
     }
+  };
+  long long base = blockIdx.x * step;
+  fetch(base);
+  if (g == 0) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float f[8];
+        load_param<T, VEC>(k ? p.b : p.w, p.w_f32, k ? 0.f : 1.f, cols, v, t, tpr, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wb[((k * NV + v) * 8 + (j & 4)) * tpr + t * 4 + (j & 3)] = f[j];
+      }
+    }
+  }
+  __syncthreads();
+  for (; base < p.rows; base += stride) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) x[r][v] = next[r][v];
+    if (base + stride < p.rows) fetch(base + stride);
+    float s[R], m[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s[r] = 0.f;
@@ -68,12 +122,13 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) ln_fwd_kernel(const LnFwdP
         for (int j = 0; j < 8; ++j) s[r] += f[j];      // elements past the row are zero
       }
     }
-    row_sum<MULTI, R>(s, tpr, smem);
-    float m[R], q[R];
+    for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], o);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r] = s[r] * inv_n;
-      q[r] = 0.f;
+      s[r] = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float f[8];
@@ -81,26 +136,32 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) ln_fwd_kernel(const LnFwdP
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float d = P::in(v, j, t, tpr, cols) ? f[j] - m[r] : 0.f;
-          q[r] = fmaf(d, d, q[r]);
+          s[r] = fmaf(d, d, s[r]);
         }
       }
     }
-    row_sum<MULTI, R>(q, tpr, smem);
-    float rs[R];
+    for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], o);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      rs[r] = rsqrtf(fmaf(q[r], inv_n, p.eps));
+      s[r] = rsqrtf(fmaf(s[r], inv_n, p.eps));
       const long long row = base + r * groups + g;
       if (t == 0 && row < p.rows) {
         if (p.mean) p.mean[row] = m[r];
-        if (p.rstd) p.rstd[row] = rs[r];
+        if (p.rstd) p.rstd[row] = s[r];
       }
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float w[8], b[8];
-      load_param<T, VEC>(p.w, p.w_f32, 1.f, cols, v, t, tpr, w);
-      load_param<T, VEC>(p.b, p.w_f32, 0.f, cols, v, t, tpr, b);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 w4 = *reinterpret_cast<const float4*>(wb + ((v * 8 + 4 * h) * tpr + t * 4));
+        const float4 b4 = *reinterpret_cast<const float4*>(wb + (((NV + v) * 8 + 4 * h) * tpr + t * 4));
+        w[4 * h] = w4.x, w[4 * h + 1] = w4.y, w[4 * h + 2] = w4.z, w[4 * h + 3] = w4.w;
+        b[4 * h] = b4.x, b[4 * h + 1] = b4.y, b[4 * h + 2] = b4.z, b[4 * h + 3] = b4.w;
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const long long row = base + r * groups + g;
@@ -108,9 +169,77 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) ln_fwd_kernel(const LnFwdP
           float f[8];
           x[r][v].get(f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - m[r]) * rs[r], w[j], b[j]);
+          for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - m[r]) * s[r], w[j], b[j]);
           P::store(static_cast<T*>(p.y) + row * p.y_stride, cols, v, t, tpr, f);
         }
+      }
+    }
+  }
+}
+
+// Rows of up to 8192 elements: a thread owns eight columns and keeps their weight and bias; a
+// group of tpr threads (whole warps) covers a row and takes R rows at a time, the next R already
+// being loaded.
+template <typename T, bool VEC, int R, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_fwd_group_kernel(const LnFwdParams p) {
+  __shared__ float part[2][MAXT / 32][R];
+  using P = Piece<T, VEC>;
+  const int tpr = p.tpr, cols = p.cols, groups = blockDim.x / tpr;
+  const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr;
+  const float inv_n = 1.f / static_cast<float>(cols);
+  const long long step = static_cast<long long>(groups) * R, stride = step * gridDim.x;
+  P x[R], next[R];
+  auto fetch = [&](long long row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      next[r].load(static_cast<const T*>(p.x) + (row0 + r) * p.x_stride, cols, 0, t, tpr, row0 + r < p.rows);
+  };
+  long long row0 = blockIdx.x * step + g * R;
+  fetch(row0);
+  float w[8], b[8];
+  load_param<T, VEC>(p.w, p.w_f32, 1.f, cols, 0, t, tpr, w);
+  load_param<T, VEC>(p.b, p.w_f32, 0.f, cols, 0, t, tpr, b);
+  RowSums<R, MAXT / 32> sums(part, tpr, g);
+  for (; row0 < p.rows; row0 += stride) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = next[r];
+    if (row0 + stride < p.rows) fetch(row0 + stride);
+    float s[R], m[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float f[8];
+      x[r].get(f);
+      s[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[r] += f[j];
+    }
+    sums(s);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float f[8];
+      x[r].get(f);
+      m[r] = s[r] * inv_n;
+      s[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = P::in(0, j, t, tpr, cols) ? f[j] - m[r] : 0.f;
+        s[r] = fmaf(d, d, s[r]);
+      }
+    }
+    sums(s);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row0 + r < p.rows) {
+        s[r] = rsqrtf(fmaf(s[r], inv_n, p.eps));
+        if (t == 0) {
+          if (p.mean) p.mean[row0 + r] = m[r];
+          if (p.rstd) p.rstd[row0 + r] = s[r];
+        }
+        float f[8];
+        x[r].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - m[r]) * s[r], w[j], b[j]);
+        P::store(static_cast<T*>(p.y) + (row0 + r) * p.y_stride, cols, 0, t, tpr, f);
       }
     }
   }
@@ -127,16 +256,15 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdParams p) 
   const float inv_n = 1.f / static_cast<float>(cols);
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* xr = static_cast<const T*>(p.x) + row * p.x_stride;
-    float s[1] = {0.f}, q[1] = {0.f}, f[8];
+    float s = 0.f, q = 0.f, f[8];
     for (int v = 0; v < nv; ++v) {
       P x;
       x.load(xr, cols, v, t, tpr);
       x.get(f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += f[j];
+      for (int j = 0; j < 8; ++j) s += f[j];
     }
-    row_sum<true, 1>(s, tpr, smem);
-    const float m = s[0] * inv_n;
+    const float m = cta_sum(s, smem) * inv_n;
     for (int v = 0; v < nv; ++v) {
       P x;
       x.load(xr, cols, v, t, tpr);
@@ -144,11 +272,10 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdParams p) 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = P::in(v, j, t, tpr, cols) ? f[j] - m : 0.f;
-        q[0] = fmaf(d, d, q[0]);
+        q = fmaf(d, d, q);
       }
     }
-    row_sum<true, 1>(q, tpr, smem);
-    const float rs = rsqrtf(fmaf(q[0], inv_n, p.eps));
+    const float rs = rsqrtf(fmaf(cta_sum(q, smem), inv_n, p.eps));
     if (t == 0) {
       if (p.mean) p.mean[row] = m;
       if (p.rstd) p.rstd[row] = rs;
@@ -169,10 +296,6 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdParams p) 
 
 // ---------------------------------------------------------------- backward
 
-__device__ __forceinline__ void group_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 __device__ __forceinline__ void put_param_grad(void* out, bool f32, int c, float v, __nv_bfloat16) {
   if (f32) static_cast<float*>(out)[c] = v;
   else static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(v);
@@ -185,41 +308,52 @@ __device__ __forceinline__ void put_param_grad(void* out, bool, int c, float v, 
   static_cast<float*>(out)[c] = v;
 }
 
-// A thread owns eight columns: a group of tpr threads covers a row, takes R rows at a time and
-// adds dy h and dy of its columns over all its rows in registers, so the weight's gradient needs
-// no second pass over dy and x.  The CTA's groups add theirs in shared memory at the end, the
-// CTAs through `parts` (fixed orders throughout: results repeat bit for bit).
+// A thread owns eight columns: a group of tpr threads covers a row, takes R rows at a time (the
+// next R already being loaded) and adds dy h and dy of its columns over all its rows in registers,
+// so the weight's gradient needs no second pass over dy and x.  The CTA's groups add theirs in
+// shared memory at the end, the CTAs through `parts` (fixed orders throughout: results repeat bit
+// for bit).
 template <typename T, bool VEC, int R, int MAXT>
-__global__ void __launch_bounds__(MAXT) ln_bwd_kernel(const LnBwdParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p) {
   extern __shared__ float dyn[];                       // [threads][16] at the end
   __shared__ float part[2][MAXT / 32][2 * R];
   using P = Piece<T, VEC>;
   const int tpr = p.tpr, cols = p.cols, groups = p.groups;
   const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = tpr >> 5, first_warp = g * warps;  // of this group, if it has whole warps
   const float inv_n = 1.f / static_cast<float>(cols);
+  // every group of the CTA goes round the same number of times (a warp may hold several groups)
+  const long long step = static_cast<long long>(groups) * R, stride = step * gridDim.x;
+  P x[R], dy[R], next_x[R], next_dy[R];
+  float m[R], rs[R], next_m[R], next_rs[R];
+  auto fetch = [&](long long row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + g * R + r;
+      const bool on = row < p.rows;
+      next_x[r].load(static_cast<const T*>(p.x) + row * p.x_stride, cols, 0, t, tpr, on);
+      next_dy[r].load(static_cast<const T*>(p.dy) + row * p.dy_stride, cols, 0, t, tpr, on);
+      next_m[r] = on ? p.mean[row] : 0.f;
+      next_rs[r] = on ? p.rstd[row] : 0.f;
+    }
+  };
+  long long base = blockIdx.x * step;
+  fetch(base);
   float w[8], dw[8], db[8];
   load_param<T, VEC>(p.w, p.w_f32, 1.f, cols, 0, t, tpr, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.f;
-  const long long nblocks = (p.rows + R - 1) / R;
-  const long long stride = static_cast<long long>(gridDim.x) * groups;
-  // every group of the CTA goes round the same number of times (a warp may hold several groups)
-  const long long rounds = (nblocks - static_cast<long long>(blockIdx.x) * groups + stride - 1) / stride;
-  int parity = 0;
-  for (long long i = 0; i < rounds; ++i, parity ^= 1) {
-    const long long row0 = (static_cast<long long>(blockIdx.x) * groups + g + i * stride) * R;
-    P x[R], dy[R];
-    float m[R], rs[R], s[2 * R];
+  RowSums<2 * R, MAXT / 32> sums(part, tpr, g);
+  for (; base < p.rows; base += stride) {
+    const long long row0 = base + g * R;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool on = row0 + r < p.rows;
-      x[r].load(static_cast<const T*>(p.x) + (row0 + r) * p.x_stride, cols, 0, t, tpr, on);
-      dy[r].load(static_cast<const T*>(p.dy) + (row0 + r) * p.dy_stride, cols, 0, t, tpr, on);
-      m[r] = on ? p.mean[row0 + r] : 0.f;
-      rs[r] = on ? p.rstd[row0 + r] : 0.f;
+      x[r] = next_x[r];
+      dy[r] = next_dy[r];
+      m[r] = next_m[r];
+      rs[r] = next_rs[r];
     }
+    if (base + stride < p.rows) fetch(base + stride);
+    float s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float xf[8], df[8];
@@ -227,7 +361,7 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_kernel(const LnBwdParams p) {
       dy[r].get(df);
       s[2 * r] = s[2 * r + 1] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {                    // dy is zero past the row, and h is finite for a finite row
+      for (int j = 0; j < 8; ++j) {                    // dy is zero past the row, and h finite for a finite row
         const float h = P::in(0, j, t, tpr, cols) ? (xf[j] - m[r]) * rs[r] : 0.f;
         const float gr = df[j] * w[j];
         s[2 * r] += gr;
@@ -236,21 +370,7 @@ __global__ void __launch_bounds__(MAXT) ln_bwd_kernel(const LnBwdParams p) {
         db[j] += df[j];
       }
     }
-    const int width = tpr < 32 ? tpr : 32;
-    for (int o = width >> 1; o > 0; o >>= 1)
-#pragma unroll
-      for (int k = 0; k < 2 * R; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
-    if (warps > 1) {
-      if (lane == 0)
-#pragma unroll
-        for (int k = 0; k < 2 * R; ++k) part[parity][warp][k] = s[k];
-      group_barrier(1 + g, tpr);        // the other parity's sums are read before anyone passes the next one
-#pragma unroll
-      for (int k = 0; k < 2 * R; ++k) s[k] = 0.f;
-      for (int u = 0; u < warps; ++u)
-#pragma unroll
-        for (int k = 0; k < 2 * R; ++k) s[k] += part[parity][first_warp + u][k];
-    }
+    sums(s);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (row0 + r < p.rows) {
@@ -297,24 +417,26 @@ struct LnPartsParams {
   void *dw, *db;
 };
 
-// dw and db from the partial sums: 32 columns by 8 slices of the parts per CTA.
+// dw and db from the partial sums: 32 columns by 32 slices of the parts per CTA.
 template <typename T>
-__global__ void __launch_bounds__(256) ln_parts_kernel(const LnPartsParams p) {
-  __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) ln_parts_kernel(const LnPartsParams p) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
   wait_for_previous_kernel();
   float a = 0.f;
   if (c < 2ll * p.cols) {
-#pragma unroll 4
-    for (int i = slice; i < p.n; i += 8) a += p.parts[static_cast<size_t>(i) * 2 * p.cols + c];
+#pragma unroll 10
+    for (int i = slice; i < p.n; i += 32) a += p.parts[static_cast<size_t>(i) * 2 * p.cols + c];
   }
   s[slice][lane] = a;
   __syncthreads();
-  if (slice == 0 && c < 2ll * p.cols) {
-    for (int i = 1; i < 8; ++i) a += s[i][lane];
-    void* out = c < p.cols ? p.dw : p.db;
-    if (out) put_param_grad(out, p.w_f32, static_cast<int>(c < p.cols ? c : c - p.cols), a, T());
+  // column 32 blockIdx + slice: its slices' sums over the lanes
+  const long long mine = static_cast<long long>(blockIdx.x) * 32 + slice;
+  a = group_sum(s[lane][slice], 32);
+  if (lane == 0 && mine < 2ll * p.cols) {
+    void* out = mine < p.cols ? p.dw : p.db;
+    if (out) put_param_grad(out, p.w_f32, static_cast<int>(mine < p.cols ? mine : mine - p.cols), a, T());
   }
 }
 
@@ -330,7 +452,7 @@ __global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(const LnBwdParams p) 
     const T* xr = static_cast<const T*>(p.x) + row * p.x_stride;
     const T* dr = static_cast<const T*>(p.dy) + row * p.dy_stride;
     const float m = p.mean[row], rs = p.rstd[row];
-    float s1[1] = {0.f}, s2[1] = {0.f}, xf[8], df[8], w[8];
+    float s1 = 0.f, s2 = 0.f, xf[8], df[8], w[8];
     for (int v = 0; v < nv; ++v) {
       P x, dy;
       x.load(xr, cols, v, t, tpr);
@@ -341,13 +463,11 @@ __global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(const LnBwdParams p) 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float h = P::in(v, j, t, tpr, cols) ? (xf[j] - m) * rs : 0.f;
-        s1[0] = fmaf(df[j], w[j], s1[0]);
-        s2[0] = fmaf(df[j] * w[j], h, s2[0]);
+        s1 = fmaf(df[j], w[j], s1);
+        s2 = fmaf(df[j] * w[j], h, s2);
       }
     }
-    row_sum<true, 1>(s1, tpr, smem);
-    row_sum<true, 1>(s2, tpr, smem);
-    const float c1 = s1[0] * inv_n, c2 = s2[0] * inv_n;
+    const float c1 = cta_sum(s1, smem) * inv_n, c2 = cta_sum(s2, smem) * inv_n;
     for (int v = 0; v < nv; ++v) {
       P x, dy;
       x.load(xr, cols, v, t, tpr);
@@ -394,36 +514,54 @@ int pow2_at_least(int x) {
   return p;
 }
 
+// How groups of threads share rows of up to 8192 elements: 576 threads per SM at 112 registers in
+// two or three CTAs up to rows of 2304 elements, then one CTA of 128 or 64 registers.
+struct GroupShape {
+  int tpr, groups;      // threads per row, rows side by side in a CTA
+  int most;             // the kernel's MAXT
+  int rows;             // rows at a time of a group
+  int ctas;             // per SM
+};
+GroupShape group_shape(int cols, bool vec) {
+  const int pieces = (cols + 7) / 8;
+  GroupShape g{};
+  g.tpr = pieces <= 32 ? pow2_at_least(pieces) : (pieces + 31) / 32 * 32;
+  g.most = g.tpr <= 288 ? 288 : g.tpr <= 512 ? 512 : 1024;
+  g.groups = g.tpr < 32 ? 256 / g.tpr : g.most / g.tpr;
+  g.rows = vec && g.most <= 512 ? 2 : 1;
+  g.ctas = g.most == 288 ? std::min(3, 576 / (g.groups * g.tpr)) : 1;
+  return g;
+}
+int cta_count(long long rows, long long per_cta, int most) {
+  const long long want = (rows + per_cta - 1) / per_cta;
+  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+}
+
 template <typename T, bool VEC>
 cudaError_t fwd(LnFwdParams p, int sms, cudaStream_t s) {
   const int pieces = (p.cols + 7) / 8;
-  if (p.cols > LN_FWD_MAX_COLS) {
-    const int grid = static_cast<int>(p.rows < 2 * sms ? p.rows : 2 * sms);
-    ln_fwd_wide_kernel<T, VEC><<<grid, 1024, 0, s>>>(p);
-    return cudaGetLastError();
+  if (p.cols > LN_MAX_COLS) {
+    ln_fwd_wide_kernel<T, VEC><<<cta_count(p.rows, 1, 2 * sms), 1024, 0, s>>>(p);
+  } else if (pieces > 128) {
+    const GroupShape g = group_shape(p.cols, VEC);
+    p.tpr = g.tpr;
+    const int grid = cta_count(p.rows, g.groups * g.rows, g.ctas * sms), threads = g.groups * g.tpr;
+    constexpr int R = VEC ? 2 : 1;
+    if (g.most == 288) ln_fwd_group_kernel<T, VEC, R, 288><<<grid, threads, 0, s>>>(p);
+    else if (g.most == 512) ln_fwd_group_kernel<T, VEC, R, 512><<<grid, threads, 0, s>>>(p);
+    else ln_fwd_group_kernel<T, VEC, 1, 1024><<<grid, threads, 0, s>>>(p);
+  } else {
+    const int nv = (pieces + 31) / 32;
+    constexpr int R1 = VEC ? 4 : 2, R2 = VEC ? 2 : 1;  // rows at a time of one and two pieces
+    const int r = nv == 1 ? R1 : nv == 2 ? R2 : 1;
+    p.tpr = pieces >= 32 ? 32 : pow2_at_least(pieces);
+    const int grid = cta_count(p.rows, static_cast<long long>(256 / p.tpr) * r, fwd_ctas<T, VEC>() * sms);
+    const size_t smem = static_cast<size_t>(2 * nv * 8) * p.tpr * sizeof(float);
+    if (nv == 1) ln_fwd_kernel<T, VEC, 1, R1><<<grid, 256, smem, s>>>(p);
+    else if (nv == 2) ln_fwd_kernel<T, VEC, 2, R2><<<grid, 256, smem, s>>>(p);
+    else if (nv == 3) ln_fwd_kernel<T, VEC, 3, 1><<<grid, 256, smem, s>>>(p);
+    else ln_fwd_kernel<T, VEC, 4, 1><<<grid, 256, smem, s>>>(p);
   }
-  if (pieces > 128) {                       // one CTA per row
-    int nv = 1;
-    while (nv < 4 && pieces > 256 * nv) nv *= 2;
-    const int threads = (pieces + 32 * nv - 1) / (32 * nv) * 32;
-    p.tpr = threads;
-    const long long cap = 1ll << 30;
-    const int grid = static_cast<int>(p.rows < cap ? p.rows : cap);
-    if (nv == 1) ln_fwd_kernel<T, VEC, 1, 1, true><<<grid, threads, 0, s>>>(p);
-    else if (nv == 2) ln_fwd_kernel<T, VEC, 2, 1, true><<<grid, threads, 0, s>>>(p);
-    else ln_fwd_kernel<T, VEC, 4, 1, true><<<grid, threads, 0, s>>>(p);
-    return cudaGetLastError();
-  }
-  const int nv = (pieces + 31) / 32;
-  p.tpr = pieces >= 32 ? 32 : pow2_at_least(pieces);
-  const int r = nv == 1 ? 4 : nv == 2 ? 2 : 1;
-  const long long per_cta = static_cast<long long>(256 / p.tpr) * r;
-  const long long want = (p.rows + per_cta - 1) / per_cta, cap = 1ll << 30;
-  const int grid = static_cast<int>(want < cap ? want : cap);
-  if (nv == 1) ln_fwd_kernel<T, VEC, 1, 4, false><<<grid, 256, 0, s>>>(p);
-  else if (nv == 2) ln_fwd_kernel<T, VEC, 2, 2, false><<<grid, 256, 0, s>>>(p);
-  else if (nv == 3) ln_fwd_kernel<T, VEC, 3, 1, false><<<grid, 256, 0, s>>>(p);
-  else ln_fwd_kernel<T, VEC, 4, 1, false><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -437,14 +575,14 @@ cudaError_t fwd_any(const LnFwdParams& p, int sms, cudaStream_t s) {
 template <typename T>
 cudaError_t add_parts(const LnBwdParams& p, int n, cudaStream_t s) {
   LnPartsParams q{p.parts, n, p.cols, p.w_f32, p.dw, p.db};
-  return launch_after(ln_parts_kernel<T>, dim3((2u * p.cols + 31) / 32), dim3(256), 0, s, q);
+  return launch_after(ln_parts_kernel<T>, dim3((2u * p.cols + 31) / 32), dim3(1024), 0, s, q);
 }
 
 template <typename T, bool VEC>
 cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
   const bool params = p.dw || p.db;
   cudaError_t e;
-  if (p.cols > LN_BWD_MAX_COLS) {
+  if (p.cols > LN_MAX_COLS) {
     if (params) {
       const int slabs = static_cast<int>(p.rows < 1 ? 1 : p.rows < 64 ? p.rows : 64);
       ln_bwd_wide_params_kernel<T><<<dim3((p.cols + 255) / 256, slabs), 256, 0, s>>>(p);
@@ -453,24 +591,20 @@ cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
       *launches += 2;
     }
     if (p.rows == 0) return cudaSuccess;
-    const int grid = static_cast<int>(p.rows < 2 * sms ? p.rows : 2 * sms);
-    ln_bwd_wide_kernel<T, VEC><<<grid, 1024, 0, s>>>(p);
+    ln_bwd_wide_kernel<T, VEC><<<cta_count(p.rows, 1, 2 * sms), 1024, 0, s>>>(p);
     *launches += 1;
     return cudaGetLastError();
   }
-  const int pieces = (p.cols + 7) / 8;
-  p.tpr = pieces <= 32 ? pow2_at_least(pieces) : (pieces + 31) / 32 * 32;
-  const int r = p.tpr <= 512 ? 4 : 1, most = p.tpr <= 512 ? 512 : 1024;
-  p.groups = most / p.tpr;
-  // whole warps only: groups of fewer than 32 threads fill them
-  const int threads = p.groups * p.tpr;
-  const long long blocks = (p.rows + r - 1) / r, want = (blocks + p.groups - 1) / p.groups;
-  int grid = static_cast<int>(want < sms ? want : sms);
-  if (grid > LN_MAX_PARTS) grid = LN_MAX_PARTS;
-  if (grid < 1) grid = 1;                   // no rows: the sums are zero, and written
+  const GroupShape g = group_shape(p.cols, VEC);
+  p.tpr = g.tpr;
+  p.groups = g.groups;
+  const int threads = g.groups * g.tpr;
+  const int grid = cta_count(p.rows, g.groups * g.rows, std::min(LN_MAX_PARTS, g.ctas * sms));
   if (grid == 1 || !params) p.parts = nullptr;
   const size_t smem = params ? static_cast<size_t>(threads) * 16 * sizeof(float) : 0;
-  auto kernel = r == 4 ? ln_bwd_kernel<T, VEC, 4, 512> : ln_bwd_kernel<T, VEC, 1, 1024>;
+  constexpr int R = VEC ? 2 : 1;
+  auto kernel = g.most == 288   ? ln_bwd_kernel<T, VEC, R, 288>
+                : g.most == 512 ? ln_bwd_kernel<T, VEC, R, 512> : ln_bwd_kernel<T, VEC, 1, 1024>;
   if (smem > 48 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
           cudaSuccess)
