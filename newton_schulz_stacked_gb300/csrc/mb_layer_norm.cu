@@ -30,22 +30,23 @@ struct RowSums {
   __device__ __forceinline__ RowSums(float (*smem)[WARPS][N], int tpr_, int group)
       : part(smem), tpr(tpr_), warp(threadIdx.x >> 5), first_warp(group * (tpr_ >> 5)), barrier(1 + group), parity(0) {}
   __device__ __forceinline__ void operator()(float (&s)[N]) {
-    const int width = tpr < 32 ? tpr : 32;
-    for (int o = width >> 1; o > 0; o >>= 1)
+    if (tpr <= 32) {
+      for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
-      for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
-    if (tpr > 32) {
-      if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int k = 0; k < N; ++k) part[parity][warp][k] = s[k];
-      group_barrier(barrier, tpr);
-#pragma unroll
-      for (int k = 0; k < N; ++k) s[k] = 0.f;
-      for (int u = 0; u < tpr >> 5; ++u)
-#pragma unroll
-        for (int k = 0; k < N; ++k) s[k] += part[parity][first_warp + u][k];
-      parity ^= 1;
+        for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
+      return;
     }
+    const int lane = threadIdx.x & 31;
+    int which;
+    const float sum = warp_sums<N>(s, lane, &which);
+    if ((lane & (32 / N - 1)) == 0) part[parity][warp][which] = sum;
+    group_barrier(barrier, tpr);
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = 0.f;
+    for (int u = 0; u < tpr >> 5; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) s[k] += part[parity][first_warp + u][k];
+    parity ^= 1;
   }
 };
 
@@ -61,6 +62,34 @@ __device__ __forceinline__ float cta_sum(float s, float* smem) {
 }
 
 // ---------------------------------------------------------------- forward
+
+// a += the squares of the piece's differences from m, within the row.
+template <typename P>
+__device__ __forceinline__ void add_squares(const P& x, float m, int cols, int v, int t, int tpr, float2& a) {
+  float2 f[4];
+  get_pairs(x, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 d = __fadd2_rn(f[j], both(-m));
+    if (!P::in(v, 2 * j, t, tpr, cols)) d.x = 0.f;
+    if (!P::in(v, 2 * j + 1, t, tpr, cols)) d.y = 0.f;
+    a = __ffma2_rn(d, d, a);
+  }
+}
+// f <- (f - m) r w + b
+__device__ __forceinline__ void normalise(float2 (&f)[4], float m, float r, const float2 (&w)[4], const float2 (&b)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[j], both(-m)), both(r)), w[j], b[j]);
+}
+// A weight or bias as pairs.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_param_pairs(const void* p, bool f32, float otherwise, int cols, int t, int tpr,
+                                                 float2 (&f)[4]) {
+  float v[8];
+  load_param<T, VEC>(p, f32, otherwise, cols, 0, t, tpr, v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
+}
 
 // CTAs per SM of the kernel below: 80 registers with 16-bit vectors, else 128.
 template <typename T, bool VEC>
@@ -113,14 +142,15 @@ __global__ void __launch_bounds__(256, fwd_ctas<T, VEC>()) ln_fwd_kernel(const L
     float s[R], m[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[r] = 0.f;
+      float2 a = both(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        float f[8];
-        x[r][v].get(f);
+        float2 f[4];
+        get_pairs(x[r][v], f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[r] += f[j];      // elements past the row are zero
+        for (int j = 0; j < 4; ++j) a = __fadd2_rn(a, f[j]);      // elements past the row are zero
       }
+      s[r] = a.x + a.y;
     }
     for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -128,17 +158,10 @@ __global__ void __launch_bounds__(256, fwd_ctas<T, VEC>()) ln_fwd_kernel(const L
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r] = s[r] * inv_n;
-      s[r] = 0.f;
+      float2 a = both(0.f);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float f[8];
-        x[r][v].get(f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = P::in(v, j, t, tpr, cols) ? f[j] - m[r] : 0.f;
-          s[r] = fmaf(d, d, s[r]);
-        }
-      }
+      for (int v = 0; v < NV; ++v) add_squares<P>(x[r][v], m[r], cols, v, t, tpr, a);
+      s[r] = a.x + a.y;
     }
     for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -154,23 +177,22 @@ __global__ void __launch_bounds__(256, fwd_ctas<T, VEC>()) ln_fwd_kernel(const L
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float w[8], b[8];
+      float2 w[4], b[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float4 w4 = *reinterpret_cast<const float4*>(wb + ((v * 8 + 4 * h) * tpr + t * 4));
         const float4 b4 = *reinterpret_cast<const float4*>(wb + (((NV + v) * 8 + 4 * h) * tpr + t * 4));
-        w[4 * h] = w4.x, w[4 * h + 1] = w4.y, w[4 * h + 2] = w4.z, w[4 * h + 3] = w4.w;
-        b[4 * h] = b4.x, b[4 * h + 1] = b4.y, b[4 * h + 2] = b4.z, b[4 * h + 3] = b4.w;
+        w[2 * h] = make_float2(w4.x, w4.y), w[2 * h + 1] = make_float2(w4.z, w4.w);
+        b[2 * h] = make_float2(b4.x, b4.y), b[2 * h + 1] = make_float2(b4.z, b4.w);
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const long long row = base + r * groups + g;
         if (row < p.rows) {
-          float f[8];
-          x[r][v].get(f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - m[r]) * s[r], w[j], b[j]);
-          P::store(static_cast<T*>(p.y) + row * p.y_stride, cols, v, t, tpr, f);
+          float2 f[4];
+          get_pairs(x[r][v], f);
+          normalise(f, m[r], s[r], w, b);
+          store_pairs<P>(static_cast<T*>(p.y) + row * p.y_stride, cols, v, t, tpr, f);
         }
       }
     }
@@ -196,9 +218,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_fwd_group_kernel
   };
   long long row0 = blockIdx.x * step + g * R;
   fetch(row0);
-  float w[8], b[8];
-  load_param<T, VEC>(p.w, p.w_f32, 1.f, cols, 0, t, tpr, w);
-  load_param<T, VEC>(p.b, p.w_f32, 0.f, cols, 0, t, tpr, b);
+  float2 w[4], b[4];
+  load_param_pairs<T, VEC>(p.w, p.w_f32, 1.f, cols, t, tpr, w);
+  load_param_pairs<T, VEC>(p.b, p.w_f32, 0.f, cols, t, tpr, b);
   RowSums<R, MAXT / 32> sums(part, tpr, g);
   for (; row0 < p.rows; row0 += stride) {
 #pragma unroll
@@ -207,24 +229,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_fwd_group_kernel
     float s[R], m[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float f[8];
-      x[r].get(f);
-      s[r] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[r] += f[j];
+      float2 f[4], a;
+      get_pairs(x[r], f);
+      a = __fadd2_rn(__fadd2_rn(f[0], f[1]), __fadd2_rn(f[2], f[3]));
+      s[r] = a.x + a.y;
     }
     sums(s);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float f[8];
-      x[r].get(f);
       m[r] = s[r] * inv_n;
-      s[r] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = P::in(0, j, t, tpr, cols) ? f[j] - m[r] : 0.f;
-        s[r] = fmaf(d, d, s[r]);
-      }
+      float2 a = both(0.f);
+      add_squares<P>(x[r], m[r], cols, 0, t, tpr, a);
+      s[r] = a.x + a.y;
     }
     sums(s);
 #pragma unroll
@@ -235,11 +251,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_fwd_group_kernel
           if (p.mean) p.mean[row0 + r] = m[r];
           if (p.rstd) p.rstd[row0 + r] = s[r];
         }
-        float f[8];
-        x[r].get(f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - m[r]) * s[r], w[j], b[j]);
-        P::store(static_cast<T*>(p.y) + (row0 + r) * p.y_stride, cols, 0, t, tpr, f);
+        float2 f[4];
+        get_pairs(x[r], f);
+        normalise(f, m[r], s[r], w, b);
+        store_pairs<P>(static_cast<T*>(p.y) + (row0 + r) * p.y_stride, cols, 0, t, tpr, f);
       }
     }
   }
@@ -323,8 +338,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const
   const float inv_n = 1.f / static_cast<float>(cols);
   // every group of the CTA goes round the same number of times (a warp may hold several groups)
   const long long step = static_cast<long long>(groups) * R, stride = step * gridDim.x;
-  P x[R], dy[R], next_x[R], next_dy[R];
-  float m[R], rs[R], next_m[R], next_rs[R];
+  P next_x[R], next_dy[R];
+  float next_m[R], next_rs[R];
   auto fetch = [&](long long row0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -338,52 +353,44 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const
   };
   long long base = blockIdx.x * step;
   fetch(base);
-  float w[8], dw[8], db[8];
-  load_param<T, VEC>(p.w, p.w_f32, 1.f, cols, 0, t, tpr, w);
+  float2 w[4], dw[4], db[4];
+  load_param_pairs<T, VEC>(p.w, p.w_f32, 1.f, cols, t, tpr, w);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.f;
+  for (int j = 0; j < 4; ++j) dw[j] = db[j] = both(0.f);
   RowSums<2 * R, MAXT / 32> sums(part, tpr, g);
   for (; base < p.rows; base += stride) {
     const long long row0 = base + g * R;
+    float2 h[R][4], gr[R][4];                          // (x - m) r and dy w of the rows
+    float rs[R], s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[r] = next_x[r];
-      dy[r] = next_dy[r];
-      m[r] = next_m[r];
+      float2 df[4], s1 = both(0.f), s2 = both(0.f);
       rs[r] = next_rs[r];
+      get_pairs(next_x[r], h[r]);
+      get_pairs(next_dy[r], df);
+      const float m = next_m[r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                    // past the row dy is 0, and h of no consequence
+        h[r][j] = __fmul2_rn(__fadd2_rn(h[r][j], both(-m)), both(rs[r]));
+        gr[r][j] = __fmul2_rn(df[j], w[j]);
+        s1 = __fadd2_rn(s1, gr[r][j]);
+        s2 = __ffma2_rn(gr[r][j], h[r][j], s2);
+        dw[j] = __ffma2_rn(df[j], h[r][j], dw[j]);
+        db[j] = __fadd2_rn(db[j], df[j]);
+      }
+      s[2 * r] = s1.x + s1.y;
+      s[2 * r + 1] = s2.x + s2.y;
     }
     if (base + stride < p.rows) fetch(base + stride);
-    float s[2 * R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float xf[8], df[8];
-      x[r].get(xf);
-      dy[r].get(df);
-      s[2 * r] = s[2 * r + 1] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {                    // dy is zero past the row, and h finite for a finite row
-        const float h = P::in(0, j, t, tpr, cols) ? (xf[j] - m[r]) * rs[r] : 0.f;
-        const float gr = df[j] * w[j];
-        s[2 * r] += gr;
-        s[2 * r + 1] = fmaf(gr, h, s[2 * r + 1]);
-        dw[j] = fmaf(df[j], h, dw[j]);
-        db[j] += df[j];
-      }
-    }
     sums(s);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (row0 + r < p.rows) {
-        float xf[8], df[8];
-        x[r].get(xf);
-        dy[r].get(df);
         const float c1 = s[2 * r] * inv_n, c2 = s[2 * r + 1] * inv_n;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float h = (xf[j] - m[r]) * rs[r];
-          xf[j] = rs[r] * (fmaf(df[j], w[j], -c1) - h * c2);
-        }
-        P::store(static_cast<T*>(p.dx) + (row0 + r) * p.dx_stride, cols, 0, t, tpr, xf);
+        for (int j = 0; j < 4; ++j)
+          h[r][j] = __fmul2_rn(__fadd2_rn(gr[r][j], __ffma2_rn(h[r][j], both(-c2), both(-c1))), both(rs[r]));
+        store_pairs<P>(static_cast<T*>(p.dx) + (row0 + r) * p.dx_stride, cols, 0, t, tpr, h[r]);
       }
     }
   }
@@ -392,8 +399,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const
   // the CTA's sum over its groups: [16 values][threads], so that threads touch neighbouring words
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    dyn[j * blockDim.x + threadIdx.x] = dw[j];
-    dyn[(8 + j) * blockDim.x + threadIdx.x] = db[j];
+    dyn[j * blockDim.x + threadIdx.x] = j & 1 ? dw[j / 2].y : dw[j / 2].x;
+    dyn[(8 + j) * blockDim.x + threadIdx.x] = j & 1 ? db[j / 2].y : db[j / 2].x;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 16 * tpr; e += blockDim.x) {

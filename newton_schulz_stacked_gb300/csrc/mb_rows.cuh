@@ -136,6 +136,21 @@ struct Piece<T, false> {
   }
 };
 
+// A piece as four pairs, for the packed fp32 instructions (two operations per issue).
+template <typename P>
+__device__ __forceinline__ void get_pairs(const P& p, float2 (&f)[4]) {
+  float v[8];
+  p.get(v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
+}
+template <typename P, typename T>
+__device__ __forceinline__ void store_pairs(T* row, int cols, int v, int t, int tpr, const float2 (&f)[4]) {
+  const float o[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+  P::store(row, cols, v, t, tpr, o);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // A parameter vector (weight or bias) in fp32 or in the activations' type T; null reads as `otherwise`.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_param(const void* p, bool f32, float otherwise, int cols, int v, int t, int tpr,
@@ -158,6 +173,28 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, float otherw
 __device__ __forceinline__ float group_sum(float x, int width) {
   for (int o = width >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
   return x;
+}
+
+// Sums of N values (1, 2, 4 or 8) over a warp, one of them per lane: the halves of the lanes that
+// split at 16, 8, ... keep half of the values each, so N values cost N - 1 exchanges and then
+// five less log2(N), not 5 N.  Returns the sum of value *which.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&s)[N], int lane, int* which) {
+  int k = 0, o = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1, o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? s[n + i] : s[i], give = up ? s[i] : s[n + i];
+      s[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+    }
+    k += up ? n : 0;
+  }
+#pragma unroll
+  for (; o > 0; o >>= 1) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
+  *which = k;
+  return s[0];
 }
 
 // Programmatic launch: a kernel launched beside the one before it in the stream waits here
