@@ -91,6 +91,27 @@ __device__ __forceinline__ void load_param_pairs(const void* p, bool f32, float 
   for (int j = 0; j < 4; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
 }
 
+// A weight or bias in shared memory, in fp32: [piece][half][thread][4], so that 16-byte reads of
+// neighbouring threads meet no bank twice.
+template <typename T, bool VEC, int NV>
+__device__ __forceinline__ void stage_param(const void* p, bool f32, float otherwise, int cols, int t, int tpr, float* to) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    float f[8];
+    load_param<T, VEC>(p, f32, otherwise, cols, v, t, tpr, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) to[(v * 8 + (j & 4)) * tpr + t * 4 + (j & 3)] = f[j];
+  }
+}
+__device__ __forceinline__ void staged_param(const float* from, int v, int t, int tpr, float2 (&f)[4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 x = *reinterpret_cast<const float4*>(from + ((v * 8 + 4 * h) * tpr + t * 4));
+    f[2 * h] = make_float2(x.x, x.y);
+    f[2 * h + 1] = make_float2(x.z, x.w);
+  }
+}
+
 // CTAs per SM of the kernel below: 80 registers with 16-bit vectors, else 128.
 template <typename T, bool VEC>
 constexpr int fwd_ctas() { return VEC && sizeof(T) == 2 ? 3 : 2; }
@@ -121,16 +142,8 @@ __global__ void __launch_bounds__(256, fwd_ctas<T, VEC>()) ln_fwd_kernel(const L
   long long base = blockIdx.x * step;
   fetch(base);
   if (g == 0) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float f[8];
-        load_param<T, VEC>(k ? p.b : p.w, p.w_f32, k ? 0.f : 1.f, cols, v, t, tpr, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) wb[((k * NV + v) * 8 + (j & 4)) * tpr + t * 4 + (j & 3)] = f[j];
-      }
-    }
+    stage_param<T, VEC, NV>(p.w, p.w_f32, 1.f, cols, t, tpr, wb);
+    stage_param<T, VEC, NV>(p.b, p.w_f32, 0.f, cols, t, tpr, wb + NV * 8 * tpr);
   }
   __syncthreads();
   for (; base < p.rows; base += stride) {
@@ -178,13 +191,8 @@ __global__ void __launch_bounds__(256, fwd_ctas<T, VEC>()) ln_fwd_kernel(const L
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float2 w[4], b[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 w4 = *reinterpret_cast<const float4*>(wb + ((v * 8 + 4 * h) * tpr + t * 4));
-        const float4 b4 = *reinterpret_cast<const float4*>(wb + (((NV + v) * 8 + 4 * h) * tpr + t * 4));
-        w[2 * h] = make_float2(w4.x, w4.y), w[2 * h + 1] = make_float2(w4.z, w4.w);
-        b[2 * h] = make_float2(b4.x, b4.y), b[2 * h + 1] = make_float2(b4.z, b4.w);
-      }
+      staged_param(wb, v, t, tpr, w);
+      staged_param(wb, NV + v, t, tpr, b);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const long long row = base + r * groups + g;
@@ -418,6 +426,104 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const
   }
 }
 
+// Threads of a CTA (one per SM) of the kernel below, by what the registers of NV pieces allow.
+template <int NV>
+constexpr int BWD_THREADS = NV == 2 ? 512 : NV == 3 ? 384 : 256;
+
+// Rows of 257 to 1024 elements: a warp holds a row in NV pieces per lane and sums over it by
+// exchanges alone; the next row is already being loaded.  Sums of the gradient as above.
+template <typename T, bool VEC, int NV>
+__global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const LnBwdParams p) {
+  extern __shared__ __align__(16) float dyn[];         // the weight [NV][8][32]; at the end [warps][NV][16][32] sums
+  using P = Piece<T, VEC>;
+  constexpr int WARPS = BWD_THREADS<NV> / 32;
+  const int cols = p.cols, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float inv_n = 1.f / static_cast<float>(cols);
+  const long long stride = static_cast<long long>(gridDim.x) * WARPS;
+  long long row = static_cast<long long>(blockIdx.x) * WARPS + warp;
+  P next_x[NV], next_dy[NV];
+  float next_m = 0.f, next_rs = 0.f;
+  const T *x = static_cast<const T*>(p.x) + row * p.x_stride, *dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
+  T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
+  auto fetch = [&](long long r) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      next_x[v].load(x, cols, v, lane, 32);
+      next_dy[v].load(dy, cols, v, lane, 32);
+    }
+    next_m = p.mean[r];
+    next_rs = p.rstd[r];
+    x += stride * p.x_stride;
+    dy += stride * p.dy_stride;
+  };
+  if (row < p.rows) fetch(row);
+  if (warp == 0) stage_param<T, VEC, NV>(p.w, p.w_f32, 1.f, cols, lane, 32, dyn);
+  __syncthreads();
+  float2 dw[NV][4], db[NV][4];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[v][j] = db[v][j] = both(0.f);
+  for (; row < p.rows; row += stride) {
+    float2 h[NV][4], gr[NV][4], s1 = both(0.f), s2 = both(0.f);
+    const float2 m = both(-next_m), rs = both(next_rs);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float2 w[4];
+      staged_param(dyn, v, lane, 32, w);
+      get_pairs(next_x[v], h[v]);
+      get_pairs(next_dy[v], gr[v]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                    // past the row dy is 0, and h of no consequence
+        const float2 d = gr[v][j];
+        h[v][j] = __fmul2_rn(__fadd2_rn(h[v][j], m), rs);
+        gr[v][j] = __fmul2_rn(d, w[j]);
+        s1 = __fadd2_rn(s1, gr[v][j]);
+        s2 = __ffma2_rn(gr[v][j], h[v][j], s2);
+        dw[v][j] = __ffma2_rn(d, h[v][j], dw[v][j]);
+        db[v][j] = __fadd2_rn(db[v][j], d);
+      }
+    }
+    if (row + stride < p.rows) fetch(row + stride);
+    const float c1 = group_sum(s1.x + s1.y, 32) * inv_n, c2 = group_sum(s2.x + s2.y, 32) * inv_n;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[v][j] = __fmul2_rn(__fadd2_rn(gr[v][j], __ffma2_rn(h[v][j], both(-c2), both(-c1))), rs);
+      store_pairs<P>(dx, cols, v, lane, 32, h[v]);
+    }
+    dx += stride * p.dx_stride;
+  }
+  let_next_kernel_start();
+  if (!p.dw && !p.db) return;
+  __syncthreads();                                     // the weight has been read
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float* to = dyn + ((warp * NV + v) * 16 + j) * 32 + lane;
+      to[0] = j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x;
+      to[8 * 32] = j & 1 ? db[v][j / 2].y : db[v][j / 2].x;
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < NV * 16 * 32; e += blockDim.x) {
+    const int tt = e & 31, k = (e >> 5) & 15, v = e >> 9, j = k & 7;
+    if (!P::in(v, j, tt, 32, cols)) continue;
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) sum += dyn[u * NV * 512 + e];
+    const int c = P::col(v, j, tt, 32);
+    if (p.parts) {
+      p.parts[(static_cast<size_t>(blockIdx.x) * 2 + (k >> 3)) * cols + c] = sum;
+    } else {
+      void* out = k < 8 ? p.dw : p.db;
+      if (out) put_param_grad(out, p.w_f32, c, sum, T());
+    }
+  }
+}
+
 struct LnPartsParams {
   const float* parts;
   int n, cols, w_f32;
@@ -602,17 +708,29 @@ cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
     *launches += 1;
     return cudaGetLastError();
   }
-  const GroupShape g = group_shape(p.cols, VEC);
-  p.tpr = g.tpr;
-  p.groups = g.groups;
-  const int threads = g.groups * g.tpr;
-  const int grid = cta_count(p.rows, g.groups * g.rows, std::min(LN_MAX_PARTS, g.ctas * sms));
+  int grid, threads;
+  size_t smem;
+  void (*kernel)(LnBwdParams);
+  const int pieces = (p.cols + 7) / 8;
+  if (pieces > 32 && pieces <= 128) {
+    const int nv = (pieces + 31) / 32;
+    threads = nv == 2 ? BWD_THREADS<2> : nv == 3 ? BWD_THREADS<3> : BWD_THREADS<4>;
+    grid = cta_count(p.rows, threads / 32, std::min(LN_MAX_PARTS, sms));
+    smem = static_cast<size_t>(nv) * (params ? 16 * threads : 8 * 32) * sizeof(float);
+    kernel = nv == 2 ? ln_bwd_warp_kernel<T, VEC, 2> : nv == 3 ? ln_bwd_warp_kernel<T, VEC, 3> : ln_bwd_warp_kernel<T, VEC, 4>;
+  } else {
+    const GroupShape g = group_shape(p.cols, VEC);
+    p.tpr = g.tpr;
+    p.groups = g.groups;
+    threads = g.groups * g.tpr;
+    grid = cta_count(p.rows, g.groups * g.rows, std::min(LN_MAX_PARTS, g.ctas * sms));
+    smem = params ? static_cast<size_t>(threads) * 16 * sizeof(float) : 0;
+    constexpr int R = VEC ? 2 : 1;
+    kernel = g.most == 288   ? ln_bwd_kernel<T, VEC, R, 288>
+             : g.most == 512 ? ln_bwd_kernel<T, VEC, R, 512> : ln_bwd_kernel<T, VEC, 1, 1024>;
+  }
   if (grid == 1 || !params) p.parts = nullptr;
-  const size_t smem = params ? static_cast<size_t>(threads) * 16 * sizeof(float) : 0;
-  constexpr int R = VEC ? 2 : 1;
-  auto kernel = g.most == 288   ? ln_bwd_kernel<T, VEC, R, 288>
-                : g.most == 512 ? ln_bwd_kernel<T, VEC, R, 512> : ln_bwd_kernel<T, VEC, 1, 1024>;
-  if (smem > 48 * 1024 &&
+  if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
           cudaSuccess)
     return e;
