@@ -16,7 +16,6 @@ void api_launched(int label, int launches, cudaStream_t stream);   // counts lau
 
 // ---------------------------------------------------------------- layer norm
 
-constexpr int LN_MAX_COLS = 8192;     // widest row that stays in registers; wider ones are read again from memory
 constexpr int LN_MAX_PARTS = 456;     // partial sums of the weight's gradient, rows of [2][cols]
 
 struct LnFwdParams {

@@ -1,0 +1,470 @@
+// Layer norm over the rows of [rows, cols], backward, with the reduction of the weight's and bias's
+// gradients over the rows.  All arithmetic is fp32.
+//
+//   h = (x - m) r;  g = dy w;  dx = r (g - mean_j g - h mean_j(g h))
+//   dw = sum_rows dy h;  db = sum_rows dy
+//
+// HBM bounds it (x and dy are read, dx is written once): both sums over a row and the sums over
+// the rows come from the same pass.
+#include "mb_layer_norm.cuh"
+
+namespace mb {
+namespace {
+
+__device__ __forceinline__ void put_param_grad(void* out, bool f32, int c, float v, __nv_bfloat16) {
+  if (f32) static_cast<float*>(out)[c] = v;
+  else static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void put_param_grad(void* out, bool f32, int c, float v, __half) {
+  if (f32) static_cast<float*>(out)[c] = v;
+  else static_cast<__half*>(out)[c] = __float2half_rn(v);
+}
+__device__ __forceinline__ void put_param_grad(void* out, bool, int c, float v, float) {
+  static_cast<float*>(out)[c] = v;
+}
+
+// A thread owns eight columns: a group of tpr threads covers a row, takes R rows at a time (the
+// next R already being loaded) and adds dy h and dy of its columns over all its rows in registers,
+// so the weight's gradient needs no second pass over dy and x.  The CTA's groups add theirs in
+// shared memory at the end, the CTAs through `parts` (fixed orders throughout: results repeat bit
+// for bit).  SHIFT: a group's rows are a multiple of 16 bytes apart, so that it keeps its columns.
+template <typename T, Access A, int R, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p) {
+  extern __shared__ float dyn[];                       // [16][threads] at the end
+  __shared__ float part[2][MAXT / 32][2 * R];
+  __shared__ int shifts[256];
+  using P = Piece<T, A>;
+  const int tpr = p.tpr, cols = p.cols, groups = p.groups;
+  const int g = threadIdx.x / tpr;
+  Place at{cols, tpr, static_cast<int>(threadIdx.x) - g * tpr, 0};
+  const float inv_n = 1.f / static_cast<float>(cols);
+  // every group of the CTA goes round the same number of times (a warp may hold several groups)
+  const long long step = static_cast<long long>(groups) * R, stride = step * gridDim.x;
+  P next_x[R], next_dy[R];
+  float next_m[R], next_rs[R];
+  long long base = blockIdx.x * step;
+  if (A == Access::SHIFT) {
+    at.shift = shift_of(static_cast<const T*>(p.x) + (base + g) * p.x_stride);
+    if (at.t == 0) shifts[g] = at.shift;
+  }
+  auto fetch = [&](long long row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + g * R + r;
+      const bool on = row < p.rows, edge = row == 0 || row == p.rows - 1;
+      next_x[r].load(static_cast<const T*>(p.x) + row * p.x_stride, at, 0, on, edge);
+      next_dy[r].load(static_cast<const T*>(p.dy) + row * p.dy_stride, at, 0, on, edge);
+      next_m[r] = on ? p.mean[row] : 0.f;
+      next_rs[r] = on ? p.rstd[row] : 0.f;
+    }
+  };
+  fetch(base);
+  float2 w[4], dw[4], db[4];
+  param_pairs<T, A>(p.w, p.w_f32, 1.f, at, 0, w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dw[j] = db[j] = both(0.f);
+  RowSums<2 * R, MAXT / 32> sums(part, tpr, g);
+  for (; base < p.rows; base += stride) {
+    const long long row0 = base + g * R;
+    float2 h[R][4], gr[R][4];                          // (x - m) r and dy w of the rows
+    float rs[R], s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 df[4], s1 = both(0.f), s2 = both(0.f);
+      rs[r] = next_rs[r];
+      get_pairs(next_x[r], at, 0, h[r]);
+      get_pairs(next_dy[r], at, 0, df);
+      const float m = next_m[r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                    // past the row dy is 0, and h of no consequence
+        h[r][j] = __fmul2_rn(__fadd2_rn(h[r][j], both(-m)), both(rs[r]));
+        gr[r][j] = __fmul2_rn(df[j], w[j]);
+        s1 = __fadd2_rn(s1, gr[r][j]);
+        s2 = __ffma2_rn(gr[r][j], h[r][j], s2);
+        dw[j] = __ffma2_rn(df[j], h[r][j], dw[j]);
+        db[j] = __fadd2_rn(db[j], df[j]);
+      }
+      s[2 * r] = s1.x + s1.y;
+      s[2 * r + 1] = s2.x + s2.y;
+    }
+    if (base + stride < p.rows) fetch(base + stride);
+    sums(s);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row0 + r < p.rows) {
+        const float c1 = s[2 * r] * inv_n, c2 = s[2 * r + 1] * inv_n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[r][j] = __fmul2_rn(__fadd2_rn(gr[r][j], __ffma2_rn(h[r][j], both(-c2), both(-c1))), both(rs[r]));
+        store_pairs<P>(static_cast<T*>(p.dx) + (row0 + r) * p.dx_stride, at, 0, h[r]);
+      }
+    }
+  }
+  let_next_kernel_start();
+  if (!p.dw && !p.db) return;
+  // the CTA's sum over its groups: [16 values][threads], so that threads touch neighbouring words
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    dyn[j * blockDim.x + threadIdx.x] = j & 1 ? dw[j / 2].y : dw[j / 2].x;
+    dyn[(8 + j) * blockDim.x + threadIdx.x] = j & 1 ? db[j / 2].y : db[j / 2].x;
+  }
+  __syncthreads();
+  const int count = A == Access::SHIFT ? 2 * cols : 16 * tpr;
+  for (int e = threadIdx.x; e < count; e += blockDim.x) {
+    float sum = 0.f;
+    int c, k;                                          // the column, and whether of dw or db
+    if constexpr (A == Access::SHIFT) {
+      k = e >= cols;
+      c = e - k * cols;
+      for (int u = 0; u < groups; ++u) {
+        const int i = c + shifts[u];
+        sum += dyn[(k * 8 + (i & 7)) * blockDim.x + u * tpr + (i >> 3)];
+      }
+    } else {
+      const int i = e / tpr, tt = e - i * tpr;
+      const Place there{cols, tpr, tt, 0};
+      if (!P::in(there, 0, i & 7)) continue;
+      for (int u = 0; u < groups; ++u) sum += dyn[i * blockDim.x + u * tpr + tt];
+      c = P::col(there, 0, i & 7);
+      k = i >> 3;
+    }
+    if (p.parts) {
+      p.parts[(static_cast<size_t>(blockIdx.x) * 2 + k) * cols + c] = sum;
+    } else {
+      void* out = k ? p.db : p.dw;
+      if (out) put_param_grad(out, p.w_f32, c, sum, T());
+    }
+  }
+}
+
+// Threads of a CTA (one per SM) of the kernel below, by what the registers of NV pieces allow.
+template <int NV>
+constexpr int BWD_THREADS = NV == 2 ? 512 : NV == 3 ? 384 : 256;
+
+// Rows of 257 to 1024 elements: a warp holds a row in NV pieces per lane and sums over it by
+// exchanges alone; the next row is already being loaded.  Sums of the gradient as above.
+template <typename T, Access A, int NV>
+__global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const LnBwdParams p) {
+  extern __shared__ __align__(16) float dyn[];         // the weight; at the end [warps][NV][16][32] sums
+  using P = Piece<T, A>;
+  constexpr int WARPS = BWD_THREADS<NV> / 32;
+  __shared__ int shifts[WARPS];
+  const int cols = p.cols, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float inv_n = 1.f / static_cast<float>(cols);
+  const long long stride = static_cast<long long>(gridDim.x) * WARPS;
+  long long row = static_cast<long long>(blockIdx.x) * WARPS + warp;
+  P next_x[NV], next_dy[NV];
+  float next_m = 0.f, next_rs = 0.f;
+  const T *x = static_cast<const T*>(p.x) + row * p.x_stride, *dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
+  T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
+  Place at{cols, 32, lane, 0};
+  if (A == Access::SHIFT) {
+    at.shift = shift_of(x);
+    if (lane == 0) shifts[warp] = at.shift;
+  }
+  auto fetch = [&](long long r) {
+    const bool edge = r == 0 || r == p.rows - 1;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      next_x[v].load(x, at, v, true, edge);
+      next_dy[v].load(dy, at, v, true, edge);
+    }
+    next_m = p.mean[r];
+    next_rs = p.rstd[r];
+    x += stride * p.x_stride;
+    dy += stride * p.dy_stride;
+  };
+  if (row < p.rows) fetch(row);
+  Staged<A, NV>::template put<T>(dyn, p.w, p.w_f32, 1.f, cols, 32);
+  __syncthreads();
+  float2 dw[NV][4], db[NV][4];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[v][j] = db[v][j] = both(0.f);
+  for (; row < p.rows; row += stride) {
+    float2 h[NV][4], gr[NV][4], s1 = both(0.f), s2 = both(0.f);
+    const float2 m = both(-next_m), rs = both(next_rs);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float2 w[4];
+      Staged<A, NV>::get(dyn, at, v, w);
+      get_pairs(next_x[v], at, v, h[v]);
+      get_pairs(next_dy[v], at, v, gr[v]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                    // past the row dy is 0, and h of no consequence
+        const float2 d = gr[v][j];
+        h[v][j] = __fmul2_rn(__fadd2_rn(h[v][j], m), rs);
+        gr[v][j] = __fmul2_rn(d, w[j]);
+        s1 = __fadd2_rn(s1, gr[v][j]);
+        s2 = __ffma2_rn(gr[v][j], h[v][j], s2);
+        dw[v][j] = __ffma2_rn(d, h[v][j], dw[v][j]);
+        db[v][j] = __fadd2_rn(db[v][j], d);
+      }
+    }
+    if (row + stride < p.rows) fetch(row + stride);
+    const float c1 = group_sum(s1.x + s1.y, 32) * inv_n, c2 = group_sum(s2.x + s2.y, 32) * inv_n;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[v][j] = __fmul2_rn(__fadd2_rn(gr[v][j], __ffma2_rn(h[v][j], both(-c2), both(-c1))), rs);
+      store_pairs<P>(dx, at, v, h[v]);
+    }
+    dx += stride * p.dx_stride;
+  }
+  let_next_kernel_start();
+  if (!p.dw && !p.db) return;
+  __syncthreads();                                     // the weight has been read
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float* to = dyn + ((warp * NV + v) * 16 + j) * 32 + lane;
+      to[0] = j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x;
+      to[8 * 32] = j & 1 ? db[v][j / 2].y : db[v][j / 2].x;
+    }
+  }
+  __syncthreads();
+  const int count = A == Access::SHIFT ? 2 * cols : NV * 16 * 32;
+  for (int e = threadIdx.x; e < count; e += blockDim.x) {
+    float sum = 0.f;
+    int c, k;                                          // the column, and whether of dw or db
+    if constexpr (A == Access::SHIFT) {
+      k = e >= cols;
+      c = e - k * cols;
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) {
+        const int i = c + shifts[u];
+        sum += dyn[((u * NV + (i >> 8)) * 16 + k * 8 + (i & 7)) * 32 + ((i >> 3) & 31)];
+      }
+    } else {
+      const int j = (e >> 5) & 7, v = e >> 9;
+      const Place there{cols, 32, e & 31, 0};
+      if (!P::in(there, v, j)) continue;
+#pragma unroll
+      for (int u = 0; u < WARPS; ++u) sum += dyn[u * NV * 512 + e];
+      c = P::col(there, v, j);
+      k = (e >> 8) & 1;
+    }
+    if (p.parts) {
+      p.parts[(static_cast<size_t>(blockIdx.x) * 2 + k) * cols + c] = sum;
+    } else {
+      void* out = k ? p.db : p.dw;
+      if (out) put_param_grad(out, p.w_f32, c, sum, T());
+    }
+  }
+}
+
+struct LnPartsParams {
+  const float* parts;
+  int n, cols, w_f32;
+  void *dw, *db;
+};
+
+// dw and db from the partial sums: 32 columns by 32 slices of the parts per CTA.
+template <typename T>
+__global__ void __launch_bounds__(1024) ln_parts_kernel(const LnPartsParams p) {
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
+  wait_for_previous_kernel();
+  float a = 0.f;
+  if (c < 2ll * p.cols) {
+#pragma unroll 10
+    for (int i = slice; i < p.n; i += 32) a += p.parts[static_cast<size_t>(i) * 2 * p.cols + c];
+  }
+  s[slice][lane] = a;
+  __syncthreads();
+  // column 32 blockIdx + slice: its slices' sums over the lanes
+  const long long mine = static_cast<long long>(blockIdx.x) * 32 + slice;
+  a = group_sum(s[lane][slice], 32);
+  if (lane == 0 && mine < 2ll * p.cols) {
+    void* out = mine < p.cols ? p.dw : p.db;
+    if (out) put_param_grad(out, p.w_f32, static_cast<int>(mine < p.cols ? mine : mine - p.cols), a, T());
+  }
+}
+
+// Wide rows: dx with one CTA per row, which reads the row twice ...
+template <typename T, Access A>
+__global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(const LnBwdParams p) {
+  __shared__ float smem[32];
+  using P = Piece<T, A>;
+  const Place at{p.cols, static_cast<int>(blockDim.x), static_cast<int>(threadIdx.x), 0};
+  const int nv = (p.cols + 8 * at.tpr - 1) / (8 * at.tpr);
+  const float inv_n = 1.f / static_cast<float>(p.cols);
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* xr = static_cast<const T*>(p.x) + row * p.x_stride;
+    const T* dr = static_cast<const T*>(p.dy) + row * p.dy_stride;
+    const float2 m = both(-p.mean[row]), rs = both(p.rstd[row]);
+    float2 s1 = both(0.f), s2 = both(0.f), h[4], g[4], w[4];
+    P x, dy;
+    auto piece = [&](int v) {                          // h and g of piece v
+      x.load(xr, at, v, true, false);
+      dy.load(dr, at, v, true, false);
+      param_pairs<T, A>(p.w, p.w_f32, 1.f, at, v, w);
+      get_pairs(x, at, v, h);
+      get_pairs(dy, at, v, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[j] = __fmul2_rn(__fadd2_rn(h[j], m), rs);
+        g[j] = __fmul2_rn(g[j], w[j]);
+      }
+    };
+    for (int v = 0; v < nv; ++v) {
+      piece(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s1 = __fadd2_rn(s1, g[j]);
+        s2 = __ffma2_rn(g[j], h[j], s2);
+      }
+    }
+    const float c1 = cta_sum(s1.x + s1.y, smem) * inv_n, c2 = cta_sum(s2.x + s2.y, smem) * inv_n;
+    for (int v = 0; v < nv; ++v) {
+      piece(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = __fmul2_rn(__fadd2_rn(g[j], __ffma2_rn(h[j], both(-c2), both(-c1))), rs);
+      store_pairs<P>(static_cast<T*>(p.dx) + row * p.dx_stride, at, v, h);
+    }
+  }
+}
+
+// ... and, before it (dx may lie over x or dy), the weight's gradient with one thread per
+// column and slab of rows.
+template <typename T>
+__global__ void __launch_bounds__(256) ln_bwd_wide_params_kernel(const LnBwdParams p) {
+  const long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= p.cols) return;
+  float dw = 0.f, db = 0.f;
+#pragma unroll 4
+  for (long long row = blockIdx.y; row < p.rows; row += gridDim.y) {
+    const float d = to_float(static_cast<const T*>(p.dy)[row * p.dy_stride + c]);
+    const float h = (to_float(static_cast<const T*>(p.x)[row * p.x_stride + c]) - p.mean[row]) * p.rstd[row];
+    dw = fmaf(d, h, dw);
+    db += d;
+  }
+  float* out = p.parts + static_cast<size_t>(blockIdx.y) * 2 * p.cols;
+  out[c] = dw;
+  out[p.cols + c] = db;
+}
+
+// ---------------------------------------------------------------- launches
+
+constexpr int BWD_MAX_COLS = 8192;   // wider rows are read again from memory
+
+// How groups of threads share rows of up to 8192 elements: 576 threads per SM at 96 registers in
+// two or three CTAs up to rows of 2304 elements, then one CTA of 128 or 64 registers.
+struct GroupShape {
+  int tpr, groups;      // threads per row, rows side by side in a CTA
+  int most;             // the kernel's MAXT
+  int rows;             // rows at a time of a group
+  int ctas;             // per SM
+};
+GroupShape group_shape(int pieces, bool vec) {
+  GroupShape g{};
+  g.tpr = pieces <= 32 ? pow2_at_least(pieces) : (pieces + 31) / 32 * 32;
+  g.most = g.tpr <= 288 ? 288 : g.tpr <= 512 ? 512 : 1024;
+  g.groups = g.tpr < 32 ? 256 / g.tpr : g.most / g.tpr;
+  g.rows = vec && g.most <= 512 ? 2 : 1;
+  g.ctas = g.most == 288 ? std::min(3, 576 / (g.groups * g.tpr)) : 1;
+  return g;
+}
+template <typename T>
+cudaError_t add_parts(const LnBwdParams& p, int n, cudaStream_t s) {
+  LnPartsParams q{p.parts, n, p.cols, p.w_f32, p.dw, p.db};
+  return launch_after(ln_parts_kernel<T>, dim3((2u * p.cols + 31) / 32), dim3(1024), 0, s, q);
+}
+
+template <typename T, Access A>
+cudaError_t bwd_wide(const LnBwdParams& p, int sms, cudaStream_t s, int* launches) {
+  cudaError_t e;
+  if (p.dw || p.db) {
+    const int slabs = static_cast<int>(p.rows < 1 ? 1 : p.rows < 64 ? p.rows : 64);
+    ln_bwd_wide_params_kernel<T><<<dim3((p.cols + 255) / 256, slabs), 256, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = add_parts<T>(p, slabs, s)) != cudaSuccess) return e;
+    *launches += 2;
+  }
+  if (p.rows == 0) return cudaSuccess;
+  ln_bwd_wide_kernel<T, A><<<cta_count(p.rows, 1, 2 * sms), 1024, 0, s>>>(p);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+template <typename T, Access A>
+cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
+  const bool params = p.dw || p.db;
+  cudaError_t e;
+  int grid, threads, rows_per_cta;
+  size_t smem;
+  void (*kernel)(LnBwdParams);
+  const int pieces = (p.cols + (A == Access::SHIFT ? 14 : 7)) / 8;
+  if (pieces > 32 && pieces <= 128) {
+    const int nv = (pieces + 31) / 32;
+    threads = nv == 2 ? BWD_THREADS<2> : nv == 3 ? BWD_THREADS<3> : BWD_THREADS<4>;
+    rows_per_cta = threads / 32;
+    grid = cta_count(p.rows, rows_per_cta, std::min(LN_MAX_PARTS, sms));
+    const int staged = nv == 2 ? Staged<A, 2>::floats(32) : nv == 3 ? Staged<A, 3>::floats(32) : Staged<A, 4>::floats(32);
+    smem = static_cast<size_t>(params ? std::max(staged, 16 * nv * threads) : staged) * sizeof(float);
+    kernel = nv == 2 ? ln_bwd_warp_kernel<T, A, 2> : nv == 3 ? ln_bwd_warp_kernel<T, A, 3> : ln_bwd_warp_kernel<T, A, 4>;
+  } else {
+    const GroupShape g = group_shape(pieces, A == Access::VEC);
+    p.tpr = g.tpr;
+    p.groups = g.groups;
+    threads = g.groups * g.tpr;
+    rows_per_cta = g.groups * g.rows;
+    grid = cta_count(p.rows, rows_per_cta, std::min(LN_MAX_PARTS, g.ctas * sms));
+    smem = params ? static_cast<size_t>(threads) * 16 * sizeof(float) : 0;
+    constexpr int R = A == Access::VEC ? 2 : 1;
+    kernel = g.most == 288   ? ln_bwd_kernel<T, A, R, 288>
+             : g.most == 512 ? ln_bwd_kernel<T, A, R, 512> : ln_bwd_kernel<T, A, 1, 1024>;
+  }
+  // SHIFT: a group's rows lie `grid * rows_per_cta` apart, which has to be a multiple of 16 bytes
+  // whatever the row; eight rows always are one
+  if (A == Access::SHIFT)
+    while (grid > 1 && grid * rows_per_cta % 8 != 0) --grid;
+  if (A == Access::SHIFT && grid * rows_per_cta % 8 != 0 && p.rows > rows_per_cta)
+    return bwd<T, Access::SCALAR>(p, sms, s, launches);
+  if (grid == 1 || !params) p.parts = nullptr;
+  if (smem > 40 * 1024 &&
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
+          cudaSuccess)
+    return e;
+  kernel<<<grid, threads, smem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  *launches += 1;
+  if (!p.parts) return cudaSuccess;
+  *launches += 1;
+  return add_parts<T>(p, grid, s);
+}
+
+template <typename T>
+cudaError_t bwd_any(const LnBwdParams& p, int sms, cudaStream_t s, int* launches) {
+  constexpr int SIZE = sizeof(T);
+  const bool vec = p.cols % 8 == 0 && aligned_rows(p.x, p.x_stride, SIZE, p.rows) &&
+                   aligned_rows(p.dy, p.dy_stride, SIZE, p.rows) && aligned_rows(p.dx, p.dx_stride, SIZE, p.rows) &&
+                   aligned(p.w);
+  if (p.cols > BWD_MAX_COLS)
+    return vec ? bwd_wide<T, Access::VEC>(p, sms, s, launches) : bwd_wide<T, Access::SCALAR>(p, sms, s, launches);
+  if (vec) return bwd<T, Access::VEC>(p, sms, s, launches);
+  // fp32 rows go by single elements, which are 128 bytes to a warp already: 5003 x 1001 takes 19.1 us
+  // so and 23.2 in shifted pieces, 67041 x 1001 138 and 149; 16-bit rows of 134083 x 1001 410 and 182
+  if constexpr (SIZE == 2) {
+    if (p.cols + 14 <= BWD_MAX_COLS && shiftable(p.x_stride, p.cols, p.rows) && shiftable(p.dy_stride, p.cols, p.rows) &&
+        same_shift(p.x, p.x_stride, p.dy, p.dy_stride, SIZE, p.rows) &&
+        same_shift(p.x, p.x_stride, p.dx, p.dx_stride, SIZE, p.rows))
+      return bwd<T, Access::SHIFT>(p, sms, s, launches);
+  }
+  return bwd<T, Access::SCALAR>(p, sms, s, launches);
+}
+
+}  // namespace
+
+cudaError_t launch_layer_norm_backward(LnBwdParams p, int type, int sms, cudaStream_t s, int* launches) {
+  *launches = 0;
+  if (type == MB_F32) return bwd_any<float>(p, sms, s, launches);
+  if (type == MB_BF16) return bwd_any<__nv_bfloat16>(p, sms, s, launches);
+  return bwd_any<__half>(p, sms, s, launches);
+}
+
+}  // namespace mb

@@ -88,85 +88,163 @@ struct Eight {
   }
 };
 
-// Piece v of thread t's share of a row that `tpr` threads hold together.
-// VEC: the eight elements from column (v tpr + t) 8 on; rows start at 16-byte boundaries and
-// hold a multiple of eight elements.  Otherwise eight single elements, tpr columns apart, so
-// that neighbouring threads still read neighbouring elements whatever the row's alignment.
-template <typename T, bool VEC>
+// How the threads of a row take its elements, in pieces of eight:
+//   VEC     neighbouring elements in 16-byte accesses: rows start at 16-byte boundaries and hold a
+//           multiple of eight elements;
+//   SHIFT   the same accesses for rows that start anywhere: pieces start at the row's 16-byte
+//           boundaries, `shift` elements before it, and the first and last hold less;
+//   SCALAR  single elements, one per thread in turn.
+enum class Access { SCALAR, VEC, SHIFT };
+
+// A thread's place in a row of `cols` elements that `tpr` threads hold together.
+struct Place {
+  int cols, tpr, t, shift;
+};
+
+// Elements from the last 16-byte boundary to p.
+template <typename T>
+__device__ __forceinline__ int shift_of(const T* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / static_cast<int>(sizeof(T));
+}
+
+// Piece v of a thread's share of a row: its eight elements as loaded, at the columns col(v, j).
+// What lies outside the row reads as zero.
+template <typename T, Access A>
 struct Piece;
 
 template <typename T>
-struct Piece<T, true> {
+struct Piece<T, Access::VEC> {
   Eight<T> e;
-  static __device__ __forceinline__ int col(int v, int j, int t, int tpr) { return (v * tpr + t) * 8 + j; }
-  static __device__ __forceinline__ bool in(int v, int, int t, int tpr, int cols) { return (v * tpr + t) * 8 < cols; }
-  __device__ __forceinline__ void load(const T* row, int cols, int v, int t, int tpr, bool on = true) {
-    if (on && in(v, 0, t, tpr, cols)) e.load(row + col(v, 0, t, tpr));
+  static __device__ __forceinline__ int col(const Place& p, int v, int j) { return (v * p.tpr + p.t) * 8 + j; }
+  static __device__ __forceinline__ bool in(const Place& p, int v, int) { return col(p, v, 0) < p.cols; }
+  __device__ __forceinline__ void load(const T* row, const Place& p, int v, bool on, bool) {
+    if (on && in(p, v, 0)) e.load(row + col(p, v, 0));
     else e.zero();
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const { e.get(f); }
-  static __device__ __forceinline__ void store(T* row, int cols, int v, int t, int tpr, const float (&f)[8]) {
-    if (in(v, 0, t, tpr, cols)) {
+  __device__ __forceinline__ void get(const Place&, int, float (&f)[8]) const { e.get(f); }
+  static __device__ __forceinline__ void store(T* row, const Place& p, int v, const float (&f)[8]) {
+    if (in(p, v, 0)) {
       Eight<T> o;
       o.set(f);
-      o.store(row + col(v, 0, t, tpr));
+      o.store(row + col(p, v, 0));
     }
   }
 };
 
 template <typename T>
-struct Piece<T, false> {
-  float f_[8];
-  static __device__ __forceinline__ int col(int v, int j, int t, int tpr) { return (v * 8 + j) * tpr + t; }
-  static __device__ __forceinline__ bool in(int v, int j, int t, int tpr, int cols) {
-    return col(v, j, t, tpr) < cols;
+struct Piece<T, Access::SHIFT> {
+  Eight<T> e;
+  static __device__ __forceinline__ int col(const Place& p, int v, int j) {
+    return (v * p.tpr + p.t) * 8 - p.shift + j;
   }
-  __device__ __forceinline__ void load(const T* row, int cols, int v, int t, int tpr, bool on = true) {
+  static __device__ __forceinline__ bool in(const Place& p, int v, int j) {
+    const int c = col(p, v, j);
+    return c >= 0 && c < p.cols;
+  }
+  // The first and last piece take in neighbours of the row, which get() drops (another thread may
+  // be writing over those meanwhile); `edge`: the first or last row, beyond which nothing may be
+  // read, so its own elements are picked one by one.
+  __device__ __forceinline__ void load(const T* row, const Place& p, int v, bool on, bool edge) {
+    const int c = col(p, v, 0);
+    const bool some = on && c + 8 > 0 && c < p.cols, whole = c >= 0 && c + 8 <= p.cols;
+    if (some && (whole || !edge)) {
+      e.load(row + c);
+    } else if (some) {
+      float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f_[j] = on && in(v, j, t, tpr, cols) ? to_float(row[col(v, j, t, tpr)]) : 0.f;
+      for (int j = 0; j < 8; ++j) f[j] = in(p, v, j) ? to_float(row[c + j]) : 0.f;
+      e.set(f);
+    } else {
+      e.zero();
+    }
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(const Place& p, int v, float (&f)[8]) const {
+    e.get(f);
+    const int c = col(p, v, 0);
+    if (c < 0 || c + 8 > p.cols) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!in(p, v, j)) f[j] = 0.f;
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, const Place& p, int v, const float (&f)[8]) {
+    const int c = col(p, v, 0);
+    if (c >= 0 && c + 8 <= p.cols) {
+      Eight<T> o;
+      o.set(f);
+      o.store(row + c);
+    } else if (c + 8 > 0 && c < p.cols) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in(p, v, j)) row[c + j] = from_float<T>(f[j]);
+    }
+  }
+};
+
+template <typename T>
+struct Piece<T, Access::SCALAR> {
+  float f_[8];
+  static __device__ __forceinline__ int col(const Place& p, int v, int j) { return (v * 8 + j) * p.tpr + p.t; }
+  static __device__ __forceinline__ bool in(const Place& p, int v, int j) { return col(p, v, j) < p.cols; }
+  __device__ __forceinline__ void load(const T* row, const Place& p, int v, bool on, bool) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f_[j] = on && in(p, v, j) ? to_float(row[col(p, v, j)]) : 0.f;
+  }
+  __device__ __forceinline__ void get(const Place&, int, float (&f)[8]) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = f_[j];
   }
-  static __device__ __forceinline__ void store(T* row, int cols, int v, int t, int tpr, const float (&f)[8]) {
+  static __device__ __forceinline__ void store(T* row, const Place& p, int v, const float (&f)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (in(v, j, t, tpr, cols)) row[col(v, j, t, tpr)] = from_float<T>(f[j]);
+      if (in(p, v, j)) row[col(p, v, j)] = from_float<T>(f[j]);
   }
 };
 
 // A piece as four pairs, for the packed fp32 instructions (two operations per issue).
 template <typename P>
-__device__ __forceinline__ void get_pairs(const P& p, float2 (&f)[4]) {
-  float v[8];
-  p.get(v);
+__device__ __forceinline__ void get_pairs(const P& x, const Place& p, int v, float2 (&f)[4]) {
+  float e[8];
+  x.get(p, v, e);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
+  for (int j = 0; j < 4; ++j) f[j] = make_float2(e[2 * j], e[2 * j + 1]);
 }
 template <typename P, typename T>
-__device__ __forceinline__ void store_pairs(T* row, int cols, int v, int t, int tpr, const float2 (&f)[4]) {
+__device__ __forceinline__ void store_pairs(T* row, const Place& p, int v, const float2 (&f)[4]) {
   const float o[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
-  P::store(row, cols, v, t, tpr, o);
+  P::store(row, p, v, o);
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// A parameter vector (weight or bias) in fp32 or in the activations' type T; null reads as `otherwise`.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_param(const void* p, bool f32, float otherwise, int cols, int v, int t, int tpr,
-                                           float (&f)[8]) {
-  if (!p) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = otherwise;
-  } else if (f32) {
-    Piece<float, VEC> w;
-    w.load(static_cast<const float*>(p), cols, v, t, tpr);
-    w.get(f);
+// Element c of a parameter vector (weight or bias) in fp32 or in the activations' type T; null
+// reads as `otherwise`.
+template <typename T>
+__device__ __forceinline__ float param(const void* p, bool f32, float otherwise, int c) {
+  if (!p) return otherwise;
+  return f32 ? static_cast<const float*>(p)[c] : to_float(static_cast<const T*>(p)[c]);
+}
+// ... and a thread's piece of it.
+template <typename T, Access A>
+__device__ __forceinline__ void param_pairs(const void* p, bool f32, float otherwise, const Place& at, int v,
+                                            float2 (&f)[4]) {
+  float e[8];
+  if (A == Access::VEC && p) {
+    if (f32) {
+      Piece<float, Access::VEC> w;
+      w.load(static_cast<const float*>(p), at, v, true, false);
+      w.get(at, v, e);
+    } else {
+      Piece<T, Access::VEC> w;
+      w.load(static_cast<const T*>(p), at, v, true, false);
+      w.get(at, v, e);
+    }
   } else {
-    Piece<T, VEC> w;
-    w.load(static_cast<const T*>(p), cols, v, t, tpr);
-    w.get(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      e[j] = Piece<T, A>::in(at, v, j) ? param<T>(p, f32, otherwise, Piece<T, A>::col(at, v, j)) : 0.f;
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = make_float2(e[2 * j], e[2 * j + 1]);
 }
 
 // Sum over the aligned group of `width` lanes (a power of two); every lane gets it.
