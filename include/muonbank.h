@@ -338,7 +338,7 @@ int mb_rotary_backward(const mb_rotary_desc* desc, void* cuda_stream);
  *   - NaN or +inf among a token's logits makes its p, its gates and the loss NaN.
  * Results: index int32 and gate fp32 [tokens, top_k]; counts int32 [experts]; loss fp32
  * [1]; used int32 [1] = N.  Limits (else MB_ERR_SHAPE): experts 1..1024, top_k
- * 1..min(experts, 32), tokens * top_k < 2^31. */
+ * 1..min(experts, 32), tokens * top_k < 2^31.  Few tokens need no workspace (0 bytes). */
 int mb_router_workspace_bytes(int64_t tokens, int64_t experts, size_t* out_bytes);
 int mb_router(const void* logits, int64_t stride, int type, const uint8_t* valid, int64_t tokens,
               int64_t experts, int top_k, int normalize, int32_t* index, float* gate,

@@ -165,7 +165,7 @@ __device__ __forceinline__ void least(const uint32_t (&key)[V], uint32_t (&out)[
 }
 
 // The counts and the loss from the CTAs' sums ({sum of p, count} of every expert, n rows of them);
-// called by the threads of one CTA for the experts [e_begin, e_end); returns (to every thread) the
+// called by the threads of a CTA for the experts [e_begin, e_end); returns (to every thread) the
 // share of  sum_e counts_e sum_t p_te  of these experts.  sums: 33 entries per warp.
 __device__ __forceinline__ float finish_experts(const RouterParams& p, int n, int e_begin, int e_end, int2* sums) {
   // 32 experts by (threads / 32) slices of the rows at a time, added in a fixed order
@@ -285,7 +285,7 @@ template <typename T, bool VEC, int G, int NC>
 __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const RouterParams p) {
   // [WARPS][experts] sums of p, [experts] counts, [WARPS][TOK][k + 1] chosen keys
   extern __shared__ float dyn[];
-  __shared__ int2 sums[WARPS * 33];
+  __shared__ float warp_share[WARPS];
   __shared__ int warp_used[WARPS];
   constexpr int V = 8 * NC;
   constexpr int TOK = 32 / G;                          // tokens per warp
@@ -442,21 +442,32 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
   if (lane == 0) warp_used[warp] = used_here;
   let_next_kernel_start();
   __syncthreads();
+  int total = 0;
+  for (int w = 0; w < WARPS; ++w) total += warp_used[w];
+  float share = 0.f;
   for (int e = threadIdx.x; e < p.experts; e += THREADS) {
     float a = 0.f;
     for (int w = 0; w < WARPS; ++w) a += dyn[w * p.experts + e];
-    p.parts_sums[static_cast<size_t>(blockIdx.x) * p.experts + e] = make_int2(__float_as_int(a), scount[e]);
-  }
-  int total = 0;
-  for (int w = 0; w < WARPS; ++w) total += warp_used[w];
-  if (threadIdx.x == 0) p.part_used[blockIdx.x] = total;
-  if (gridDim.x == 1) {                                // the only CTA finishes by itself
-    __syncthreads();
-    const float share = finish_experts(p, 1, 0, p.experts, sums);
-    if (threadIdx.x == 0) {
-      p.loss[0] = loss_of(share, total, p.experts, p.k);
-      p.used[0] = total;
+    const int c = scount[e];
+    if (gridDim.x > 1) {
+      p.parts_sums[static_cast<size_t>(blockIdx.x) * p.experts + e] = make_int2(__float_as_int(a), c);
+    } else {
+      p.counts[e] = c;
+      share += a * static_cast<float>(c);
     }
+  }
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) p.part_used[blockIdx.x] = total;
+    return;
+  }
+  // the only CTA finishes by itself
+  share = group_add<32>(share);
+  if (lane == 0) warp_share[warp] = share;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < WARPS; ++w) share += warp_share[w];
+    p.loss[0] = loss_of(share, total, p.experts, p.k);
+    p.used[0] = total;
   }
 }
 
@@ -468,6 +479,11 @@ __global__ void __launch_bounds__(1024) router_finish_kernel(const RouterParams 
   __shared__ float share;
   wait_for_previous_kernel();
   const uint32_t rank = cluster_ctarank();
+  int used = 0;                                        // of the first warp, asked for before the sums
+  if (rank == 0 && threadIdx.x < 32) {
+#pragma unroll 10
+    for (int i = threadIdx.x; i < p.parts; i += 32) used += p.part_used[i];
+  }
   const int per = (p.experts + FINISH_CTAS - 1) / FINISH_CTAS;
   const int e0 = static_cast<int>(rank) * per, e1 = e0 + per < p.experts ? e0 + per : p.experts;
   const float mine = finish_experts(p, p.parts, e0, e1, sums);
@@ -476,8 +492,6 @@ __global__ void __launch_bounds__(1024) router_finish_kernel(const RouterParams 
   if (rank == 0 && threadIdx.x < 32) {
     const float of = threadIdx.x < FINISH_CTAS ? __uint_as_float(ld_cluster_u32(map_to_rank(&share, threadIdx.x))) : 0.f;
     const float all = group_add<32>(of);
-    int used = 0;
-    for (int i = threadIdx.x; i < p.parts; i += 32) used += p.part_used[i];
     used = __reduce_add_sync(FULL, used);
     if (threadIdx.x == 0) {
       p.loss[0] = loss_of(all, used, p.experts, p.k);
@@ -501,21 +515,6 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_bwd_kernel(co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane % G;
   float* add = dyn + (warp * TOK + lane / G) * (G * V);
-#pragma unroll
-  for (int j = 0; j < V; ++j) add[expert_of<G>(j / 8, g, j & 7)] = 0.f;
-  float c[V];
-  {
-    const int n = *p.used;
-    const float nf = static_cast<float>(n > 0 ? n : 1);
-    const float d = p.dloss && n > 0
-                        ? *p.dloss * (static_cast<float>(p.experts) / (static_cast<float>(p.k) * nf)) / nf : 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = expert_of<G>(j / 8, g, j & 7);
-      c[j] = e < p.experts ? d * static_cast<float>(p.counts[e]) : 0.f;
-    }
-  }
-  __syncwarp();
   const long long stride = static_cast<long long>(gridDim.x) * WARPS * TOK;
   const T* logits = static_cast<const T*>(p.logits);
   Logits<T, VEC, G, NC> next;
@@ -536,7 +535,25 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_bwd_kernel(co
     }
   };
   long long base = (static_cast<long long>(blockIdx.x) * WARPS + warp) * TOK;
-  if (base < p.tokens) fetch(base);
+  if (base < p.tokens) fetch(base);                    // before the counts, so that their latencies overlap
+#pragma unroll
+  for (int j = 0; j < V; ++j) add[expert_of<G>(j / 8, g, j & 7)] = 0.f;
+  float c[V];
+  {
+    const int n = *p.used;
+    const float dloss = p.dloss ? *p.dloss : 0.f;
+    int count[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = expert_of<G>(j / 8, g, j & 7);
+      count[j] = e < p.experts ? p.counts[e] : 0;
+    }
+    const float nf = static_cast<float>(n > 0 ? n : 1);
+    const float d = n > 0 ? dloss * (static_cast<float>(p.experts) / (static_cast<float>(p.k) * nf)) / nf : 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] = d * static_cast<float>(count[j]);
+  }
+  __syncwarp();
   for (; base < p.tokens; base += stride) {
     const long long token = base + lane / G;
     float l[V];

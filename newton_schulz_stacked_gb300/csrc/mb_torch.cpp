@@ -143,7 +143,8 @@ struct Workspace {
   Workspace(PyObject* given, size_t need, c10::Device device) {
     const Tensor* t = tensor_or_none(given, "workspace");
     if (!t) {
-      own = make({static_cast<int64_t>(need > 0 ? need : 1)}, ScalarType::Byte, device);
+      if (need == 0) return;
+      own = make({static_cast<int64_t>(need)}, ScalarType::Byte, device);
       t = &own;
     } else if (t->device() != device || !t->is_contiguous()) {
       throw Refused{"workspace must be a contiguous tensor on " + device.str()};

@@ -119,7 +119,9 @@ def _router(lib, logits=GOOD, stride=16, kind=0, valid=None, tokens=8, experts=1
 
 def test_router_statuses(lib, b):
     out = ctypes.c_size_t()
-    assert lib.mb_router_workspace_bytes(8, 16, ctypes.byref(out)) == b.MB_OK and out.value > 0
+    assert lib.mb_router_workspace_bytes(8, 16, ctypes.byref(out)) == b.MB_OK and out.value == 0    # one CTA's work
+    many = dict(tokens=100000)
+    assert lib.mb_router_workspace_bytes(100000, 16, ctypes.byref(out)) == b.MB_OK and out.value > 0
     assert lib.mb_router_workspace_bytes(8, 1025, ctypes.byref(out)) == b.MB_ERR_SHAPE
     assert lib.mb_router_workspace_bytes(8, 16, None) == b.MB_ERR_NULL
     for name in ("logits", "index", "gate", "counts", "loss", "used"):
@@ -129,10 +131,10 @@ def test_router_statuses(lib, b):
                    dict(tokens=1 << 31), dict(tokens=1 << 30, k=2), dict(stride=-1)):
         assert _router(lib, **change) == b.MB_ERR_SHAPE, change
     assert _router(lib, kind=4) == b.MB_ERR_ARG
-    assert _router(lib, ws=None) == b.MB_ERR_WORKSPACE
-    assert lib.mb_router_workspace_bytes(8, 16, ctypes.byref(out)) == b.MB_OK
-    assert _router(lib, nbytes=out.value - 1) == b.MB_ERR_WORKSPACE
-    assert _router(lib, ws=GOOD + 4) == b.MB_ERR_ALIGN
+    assert _router(lib, ws=None, **many) == b.MB_ERR_WORKSPACE
+    assert lib.mb_router_workspace_bytes(100000, 16, ctypes.byref(out)) == b.MB_OK
+    assert _router(lib, nbytes=out.value - 1, **many) == b.MB_ERR_WORKSPACE
+    assert _router(lib, ws=GOOD + 4, **many) == b.MB_ERR_ALIGN
 
 
 def test_router_backward_statuses(lib, b):
