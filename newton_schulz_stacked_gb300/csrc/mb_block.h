@@ -120,8 +120,8 @@ int router_parts(int tokens, int experts, int sms);
 cudaError_t launch_router(RouterParams p, int type, int sms, cudaStream_t s, int* launches);
 cudaError_t launch_router_backward(RouterBwdParams p, int type, int sms, cudaStream_t s, int* launches);
 
-// A launch that may start while the kernel before it in the stream drains (its kernel calls
-// wait_for_previous_kernel before it reads what that one writes).
+// A launch that may start while the kernel before it in the stream drains: its kernel begins with
+// begin_after_previous, before it reads or writes anything.
 template <typename P>
 cudaError_t launch_after(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const P& p,
                          int cluster = 0) {

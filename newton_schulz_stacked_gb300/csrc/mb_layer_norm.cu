@@ -46,6 +46,7 @@ constexpr int FWD_CTAS = A != Access::SCALAR && sizeof(T) == 2 && NV <= 4 ? 3 : 
 // far the mean is from zero.
 template <typename T, Access A, int NV, int R>
 __global__ void __launch_bounds__(256, FWD_CTAS<T, A, NV>) ln_fwd_kernel(const LnFwdParams p) {
+  begin_after_previous();
   extern __shared__ __align__(16) float wb[];          // the weight, then the bias
   using P = Piece<T, A>;
   constexpr bool AHEAD = A != Access::SCALAR && NV <= 4;
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(256, FWD_CTAS<T, A, NV>) ln_fwd_kernel(const L
 // in NV pieces each; several CTAs per SM keep loads in flight while others wait at their sums.
 template <typename T, Access A, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT) ln_fwd_cta_kernel(const LnFwdParams p) {
+  begin_after_previous();
   __shared__ float smem[32];
   using P = Piece<T, A>;
   const Place at{p.cols, static_cast<int>(blockDim.x), static_cast<int>(threadIdx.x), 0};
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(MAXT) ln_fwd_cta_kernel(const LnFwdParams p) {
 // time out of L2 for all but the widest).
 template <typename T, Access A>
 __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdParams p) {
+  begin_after_previous();
   __shared__ float smem[32];
   using P = Piece<T, A>;
   const Place at{p.cols, static_cast<int>(blockDim.x), static_cast<int>(threadIdx.x), 0};
@@ -219,15 +222,15 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdParams p) 
 constexpr int SHIFT_MAX_COLS = 4096;
 
 template <typename T, Access A, int NV, int R>
-void fwd_warp(LnFwdParams p, int sms, cudaStream_t s) {
+cudaError_t fwd_warp(LnFwdParams p, int sms, cudaStream_t s) {
   const int grid = cta_count(p.rows, static_cast<long long>(256 / p.tpr) * R, FWD_CTAS<T, A, NV> * sms);
   const size_t smem = 2 * static_cast<size_t>(Staged<A, NV>::floats(p.tpr)) * sizeof(float);
-  ln_fwd_kernel<T, A, NV, R><<<grid, 256, smem, s>>>(p);
+  return launch_after(ln_fwd_kernel<T, A, NV, R>, dim3(grid), dim3(256), smem, s, p);
 }
 
 // Rows of more than 1024 elements.
 template <typename T, Access A>
-void fwd_long(const LnFwdParams& p, int pieces, int sms, cudaStream_t s) {
+cudaError_t fwd_long(const LnFwdParams& p, int pieces, int sms, cudaStream_t s) {
   constexpr bool SCALAR = A == Access::SCALAR;
   if constexpr (!SCALAR) {
     if (pieces <= 256) return fwd_warp<T, A, 8, 1>(p, sms, s);
@@ -237,11 +240,11 @@ void fwd_long(const LnFwdParams& p, int pieces, int sms, cudaStream_t s) {
     constexpr int NV = SCALAR ? 2 : 8, MAXT = SCALAR ? 1024 : 512;
     if (pieces <= NV * MAXT) {
       const int threads = (pieces + 32 * NV - 1) / (32 * NV) * 32;
-      ln_fwd_cta_kernel<T, A, NV, MAXT><<<cta_count(p.rows, 1, 1 << 20), threads, 0, s>>>(p);
-    } else {
-      ln_fwd_wide_kernel<T, A><<<cta_count(p.rows, 1, 2 * sms), 1024, 0, s>>>(p);
+      return launch_after(ln_fwd_cta_kernel<T, A, NV, MAXT>, dim3(cta_count(p.rows, 1, 1 << 20)), dim3(threads), 0, s, p);
     }
+    return launch_after(ln_fwd_wide_kernel<T, A>, dim3(cta_count(p.rows, 1, 2 * sms)), dim3(1024), 0, s, p);
   }
+  return cudaErrorInvalidValue;
 }
 
 template <typename T, Access A>
@@ -249,12 +252,11 @@ cudaError_t fwd(LnFwdParams p, int sms, cudaStream_t s) {
   constexpr bool SCALAR = A == Access::SCALAR;
   const int pieces = (p.cols + (A == Access::SHIFT ? 14 : 7)) / 8;
   p.tpr = pieces >= 32 ? 32 : pow2_at_least(pieces);
-  if (pieces <= 32) fwd_warp<T, A, 1, SCALAR ? 2 : 4>(p, sms, s);
-  else if (pieces <= 64) fwd_warp<T, A, 2, SCALAR ? 1 : 2>(p, sms, s);
-  else if (pieces <= 96) fwd_warp<T, A, 3, 1>(p, sms, s);
-  else if (pieces <= 128) fwd_warp<T, A, 4, 1>(p, sms, s);
-  else fwd_long<T, A>(p, pieces, sms, s);
-  return cudaGetLastError();
+  if (pieces <= 32) return fwd_warp<T, A, 1, SCALAR ? 2 : 4>(p, sms, s);
+  if (pieces <= 64) return fwd_warp<T, A, 2, SCALAR ? 1 : 2>(p, sms, s);
+  if (pieces <= 96) return fwd_warp<T, A, 3, 1>(p, sms, s);
+  if (pieces <= 128) return fwd_warp<T, A, 4, 1>(p, sms, s);
+  return fwd_long<T, A>(p, pieces, sms, s);
 }
 
 template <typename T>

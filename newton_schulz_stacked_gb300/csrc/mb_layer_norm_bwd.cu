@@ -30,6 +30,7 @@ __device__ __forceinline__ void put_param_grad(void* out, bool, int c, float v, 
 // for bit).  SHIFT: a group's rows are a multiple of 16 bytes apart, so that it keeps its columns.
 template <typename T, Access A, int R, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p) {
+  begin_after_previous();
   extern __shared__ float dyn[];                       // [16][threads] at the end
   __shared__ float part[2][MAXT / 32][2 * R];
   __shared__ int shifts[256];
@@ -100,7 +101,6 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const
       }
     }
   }
-  let_next_kernel_start();
   if (!p.dw && !p.db) return;
   // the CTA's sum over its groups: [16 values][threads], so that threads touch neighbouring words
 #pragma unroll
@@ -145,6 +145,7 @@ constexpr int BWD_THREADS = NV == 2 ? 512 : NV == 3 ? 384 : 256;
 // exchanges alone; the next row is already being loaded.  Sums of the gradient as above.
 template <typename T, Access A, int NV>
 __global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const LnBwdParams p) {
+  begin_after_previous();
   extern __shared__ __align__(16) float dyn[];         // the weight; at the end [warps][NV][16][32] sums
   using P = Piece<T, A>;
   constexpr int WARPS = BWD_THREADS<NV> / 32;
@@ -213,7 +214,6 @@ __global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const L
     }
     dx += stride * p.dx_stride;
   }
-  let_next_kernel_start();
   if (!p.dw && !p.db) return;
   __syncthreads();                                     // the weight has been read
 #pragma unroll
@@ -265,10 +265,10 @@ struct LnPartsParams {
 // dw and db from the partial sums: 32 columns by 32 slices of the parts per CTA.
 template <typename T>
 __global__ void __launch_bounds__(1024) ln_parts_kernel(const LnPartsParams p) {
+  begin_after_previous();
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
-  wait_for_previous_kernel();
   float a = 0.f;
   if (c < 2ll * p.cols) {
 #pragma unroll 10
@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(1024) ln_parts_kernel(const LnPartsParams p) {
 // Wide rows: dx with one CTA per row, which reads the row twice ...
 template <typename T, Access A>
 __global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(const LnBwdParams p) {
+  begin_after_previous();
   __shared__ float smem[32];
   using P = Piece<T, A>;
   const Place at{p.cols, static_cast<int>(blockDim.x), static_cast<int>(threadIdx.x), 0};
@@ -333,6 +334,7 @@ __global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(const LnBwdParams p) 
 // column and slab of rows.
 template <typename T>
 __global__ void __launch_bounds__(256) ln_bwd_wide_params_kernel(const LnBwdParams p) {
+  begin_after_previous();
   const long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= p.cols) return;
   float dw = 0.f, db = 0.f;
@@ -380,15 +382,14 @@ cudaError_t bwd_wide(const LnBwdParams& p, int sms, cudaStream_t s, int* launche
   cudaError_t e;
   if (p.dw || p.db) {
     const int slabs = static_cast<int>(p.rows < 1 ? 1 : p.rows < 64 ? p.rows : 64);
-    ln_bwd_wide_params_kernel<T><<<dim3((p.cols + 255) / 256, slabs), 256, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(ln_bwd_wide_params_kernel<T>, dim3((p.cols + 255) / 256, slabs), dim3(256), 0, s, p)) != cudaSuccess)
+      return e;
     if ((e = add_parts<T>(p, slabs, s)) != cudaSuccess) return e;
     *launches += 2;
   }
   if (p.rows == 0) return cudaSuccess;
-  ln_bwd_wide_kernel<T, A><<<cta_count(p.rows, 1, 2 * sms), 1024, 0, s>>>(p);
   *launches += 1;
-  return cudaGetLastError();
+  return launch_after(ln_bwd_wide_kernel<T, A>, dim3(cta_count(p.rows, 1, 2 * sms)), dim3(1024), 0, s, p);
 }
 
 template <typename T, Access A>
@@ -430,8 +431,7 @@ cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
           cudaSuccess)
     return e;
-  kernel<<<grid, threads, smem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_after(kernel, dim3(grid), dim3(threads), smem, s, p)) != cudaSuccess) return e;
   *launches += 1;
   if (!p.parts) return cudaSuccess;
   *launches += 1;

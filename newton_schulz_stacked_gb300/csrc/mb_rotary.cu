@@ -87,6 +87,7 @@ constexpr int ITEMS_AHEAD = N * sizeof(T) < 16 ? 4 : sizeof(T) == 2 ? 1 : 2;
 // copied rest.  A thread loads AHEAD items before it works on them.
 template <typename T, int N, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rotary_kernel(const RotaryParams p) {
+  begin_after_previous();
   extern __shared__ float2 cs[];                     // [tile][pairs] cosine, sine; then the tile's TokenBases
   TokenBase* base = reinterpret_cast<TokenBase*>(cs + static_cast<size_t>(p.tile) * p.pairs);
   constexpr int AHEAD = ITEMS_AHEAD<T, N>;
@@ -230,8 +231,7 @@ cudaError_t rotary(RotaryParams p, int sms, cudaStream_t s) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, THREADS, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(grid), dim3(THREADS), smem, s, p);
 }
 
 template <typename T>

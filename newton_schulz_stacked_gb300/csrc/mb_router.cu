@@ -283,6 +283,7 @@ __device__ __noinline__ ExactSoftmax select_exact(const T* row, bool on, int exp
 // all eight where fewer lanes share the experts.
 template <typename T, bool VEC, int G, int NC>
 __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const RouterParams p) {
+  begin_after_previous();
   // [WARPS][experts] sums of p, [experts] counts, [WARPS][TOK][k + 1] chosen keys
   extern __shared__ float dyn[];
   __shared__ float warp_share[WARPS];
@@ -440,7 +441,6 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
   }
   used_here = __reduce_add_sync(FULL, used_here);
   if (lane == 0) warp_used[warp] = used_here;
-  let_next_kernel_start();
   __syncthreads();
   int total = 0;
   for (int w = 0; w < WARPS; ++w) total += warp_used[w];
@@ -475,9 +475,9 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
 constexpr int FINISH_CTAS = 8;
 
 __global__ void __launch_bounds__(1024) router_finish_kernel(const RouterParams p) {
+  begin_after_previous();
   __shared__ int2 sums[32 * 33];
   __shared__ float share;
-  wait_for_previous_kernel();
   const uint32_t rank = cluster_ctarank();
   int used = 0;                                        // of the first warp, asked for before the sums
   if (rank == 0 && threadIdx.x < 32) {
@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(1024) router_finish_kernel(const RouterParams 
 // belongs to the chosen experts goes to their lanes through shared memory.
 template <typename T, bool VEC, int G, int NC>
 __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_bwd_kernel(const RouterBwdParams p) {
+  begin_after_previous();
   extern __shared__ __align__(16) float dyn[];         // [WARPS][TOK][8 G NC], zero between tokens
   constexpr int V = 8 * NC;
   constexpr int TOK = 32 / G;
@@ -720,8 +721,7 @@ cudaError_t fwd(const RouterParams& p, cudaStream_t s, int* launches) {
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
           cudaSuccess)
     return e;
-  kernel<<<p.parts, THREADS, smem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_after(kernel, dim3(p.parts), dim3(THREADS), smem, s, p)) != cudaSuccess) return e;
   *launches = 1;
   if (p.parts == 1) return cudaSuccess;
   *launches = 2;
@@ -742,8 +742,7 @@ cudaError_t bwd(const RouterBwdParams& p, int sms, cudaStream_t s) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  kernel<<<want < most ? want : most, THREADS, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(want < most ? want : most), dim3(THREADS), smem, s, p);
 }
 
 }  // namespace
