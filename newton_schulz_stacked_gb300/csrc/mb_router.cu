@@ -9,6 +9,8 @@
 // G lanes hold one token's logits, eight (times NC) neighbouring experts each, so a warp works
 // on 32 / G tokens, each logit is read once, and a lane meets the same experts in every token:
 // the sums over tokens of p stay in its registers.
+#include <algorithm>
+
 #include "mb_block.h"
 #include "mb_device.cuh"
 #include "mb_rows.cuh"
@@ -90,6 +92,14 @@ __device__ __forceinline__ void count_one(int* counter) {
   asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(smem_u32(counter)) : "memory");
 }
 
+// Whether any lane of this lane's group says so.
+template <int G>
+__device__ __forceinline__ bool any_of_group(bool x, int lane) {
+  if constexpr (G == 32) return __any_sync(FULL, x) != 0;
+  const uint32_t votes = __ballot_sync(FULL, x) >> (lane & ~(G - 1));
+  return (votes & ((1u << (G & 31)) - 1u)) != 0;
+}
+
 // Expert of element j of piece c of lane g in its group.
 template <int G>
 __device__ __forceinline__ int expert_of(int c, int g, int j) { return (c * G + g) * 8 + j; }
@@ -132,34 +142,41 @@ __device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
   a = lo;
 }
 
-// A lane's least D of V keys, in order, by networks of minima and maxima: all eight of eight (19
-// comparisons), or the least four by fours.
+// All eight in order (19 comparisons).
+__device__ __forceinline__ void sort8(uint32_t (&k)[8]) {
+  order2(k[0], k[2]), order2(k[1], k[3]), order2(k[4], k[6]), order2(k[5], k[7]);
+  order2(k[0], k[4]), order2(k[1], k[5]), order2(k[2], k[6]), order2(k[3], k[7]);
+  order2(k[0], k[1]), order2(k[2], k[3]), order2(k[4], k[5]), order2(k[6], k[7]);
+  order2(k[2], k[4]), order2(k[3], k[5]);
+  order2(k[1], k[4]), order2(k[3], k[6]);
+  order2(k[1], k[2]), order2(k[3], k[4]), order2(k[5], k[6]);
+}
+__device__ __forceinline__ void sort4(uint32_t (&k)[4]) {
+  order2(k[0], k[1]), order2(k[2], k[3]), order2(k[0], k[2]), order2(k[1], k[3]), order2(k[1], k[2]);
+}
+
+// A lane's least D (4 or 8) of V keys, in order, by networks of minima and maxima: D at a time, the
+// least D of both sorted runs being a bitonic sequence.
 template <int D, int V>
 __device__ __forceinline__ void least(const uint32_t (&key)[V], uint32_t (&out)[D]) {
-  if constexpr (D == 8) {
-    static_assert(V == 8, "all of a lane's keys");
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = key[j];
-    order2(out[0], out[2]), order2(out[1], out[3]), order2(out[4], out[6]), order2(out[5], out[7]);
-    order2(out[0], out[4]), order2(out[1], out[5]), order2(out[2], out[6]), order2(out[3], out[7]);
-    order2(out[0], out[1]), order2(out[2], out[3]), order2(out[4], out[5]), order2(out[6], out[7]);
-    order2(out[2], out[4]), order2(out[3], out[5]);
-    order2(out[1], out[4]), order2(out[3], out[6]);
-    order2(out[1], out[2]), order2(out[3], out[4]), order2(out[5], out[6]);
-  } else {
-    static_assert(D == 4, "");
+  for (int q = 0; q < V; q += D) {
+    uint32_t f[D];
 #pragma unroll
-    for (int q = 0; q < V; q += 4) {
-      uint32_t f[4] = {key[q], key[q + 1], key[q + 2], key[q + 3]};
-      order2(f[0], f[1]), order2(f[2], f[3]), order2(f[0], f[2]), order2(f[1], f[3]), order2(f[1], f[2]);
-      if (q == 0) {
+    for (int j = 0; j < D; ++j) f[j] = key[q + j];
+    if constexpr (D == 8) sort8(f);
+    else sort4(f);
+    if (q == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) out[j] = f[j];
-      } else {                                         // the least four of both: a bitonic sequence, sorted
+      for (int j = 0; j < D; ++j) out[j] = f[j];
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) out[j] = min(out[j], f[3 - j]);
-        order2(out[0], out[2]), order2(out[1], out[3]), order2(out[0], out[1]), order2(out[2], out[3]);
-      }
+      for (int j = 0; j < D; ++j) out[j] = min(out[j], f[D - 1 - j]);
+#pragma unroll
+      for (int d = D / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int j = 0; j < D; ++j)
+          if ((j & d) == 0) order2(out[j], out[j + d]);
     }
   }
 }
@@ -212,40 +229,37 @@ __device__ __forceinline__ float loss_of(float share, int used, int experts, int
 // ---------------------------------------------------------------- forward
 
 // A lane keeps the r-th chosen experts with r % G equal to its place in the group.
-template <int G>
+template <int G, int V = 8>
 struct Slots {
-  static constexpr int N = G >= 32 ? 1 : 32 / G > 8 ? 8 : 32 / G;   // k <= 8 G and k <= 32
+  static constexpr int N = 32 / G < V ? 32 / G : V;    // k <= V G and k <= 32
 };
 
-// The k largest of a token's logits for any values: k rounds over exact keys, the winner's lane
-// looking for its next among what comes after the one just taken.  Puts the chosen experts into
-// `order` (-1: none) and returns the softmax's maximum and sum in the plain form exp(l - max).
-// A call of its own, with nothing passed in registers but the row: it is rare, and inlined it
-// cost the common way 58 of 340 instructions per token.
-struct ExactSoftmax {
-  float m, sum;
-  bool some;
-};
-template <typename T, int G, int V>
-__device__ __noinline__ ExactSoftmax select_exact(const T* row, bool on, int experts, int k, int g, uint32_t* order) {
-  uint32_t key[V], k1 = 0;
+// A token's softmax and its k largest logits for any values: k rounds over exact keys, the winner's
+// lane looking for its next among what comes after the one just taken.  The terms are exp(l - max);
+// NaN or +inf among the logits makes the sum NaN, and with it every probability of the token.
+template <int G, int V, int SLOTS>
+__device__ __forceinline__ void select_exact(const float (&l)[V], int g, int k, int (&idx)[SLOTS], float (&e)[V],
+                                             float& sum, float& m, bool& some) {
+  uint32_t key[V], k1 = 0, top = 0;
   int i1 = 0;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = expert_of<G>(j / 8, g, j & 7);
-    key[j] = on && e < experts ? key_of(to_float(row[e])) : 0;
+    key[j] = key_of(l[j]);
     if (key[j] > k1) {
       k1 = key[j];
       i1 = j;
     }
   }
-  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) idx[s] = -1;
   for (int r = 0; r < k; ++r) {
     const uint32_t best = group_max<G>(k1);
     if (r == 0) top = best;
     const uint32_t mine = k1 == best && best != 0 ? expert_of<G>(i1 / 8, g, i1 & 7) : 0x7FFFFFFFu;
     const uint32_t who = group_min<G>(mine);
-    order[r] = best != 0 ? who : 0xFFFFFFFFu;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+      if (r == s * G + g && best != 0) idx[s] = static_cast<int>(who);
     if (best != 0 && mine == who) {
       const uint32_t lk = k1;
       const int li = i1;
@@ -260,27 +274,36 @@ __device__ __noinline__ ExactSoftmax select_exact(const T* row, bool on, int exp
       }
     }
   }
-  ExactSoftmax x{value_of(top), 0.f, top != 0};
+  some = top != 0;
+  m = value_of(top);
+  sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) x.sum += key[j] == 0 ? 0.f : expf(value_of(key[j]) - x.m);
-  x.sum = group_add<G>(x.sum);
-  // NaN or +inf among the logits makes the sum NaN, and with it every probability of the token
-  if (top >= 0xFF800000u) x.sum = __uint_as_float(0x7FC00000u);
-  return x;
+  for (int j = 0; j < V; ++j) {
+    e[j] = key[j] == 0 ? 0.f : expf(l[j] - m);
+    sum += e[j];
+  }
+  sum = group_add<G>(sum);
+  if (top >= 0xFF800000u) sum = __uint_as_float(0x7FC00000u);
 }
 
 // Selection without conditions per element.  With c = max * log2(e) rounded up, x = l log2(e) - c
 // is at most 0, monotone in l, and the exponent the softmax needs anyway.  The bits of such an x
 // grow as l falls, so a key of x's upper bits and the expert's number in the low ones sorts by
 // falling logit, then by number, with one minimum per comparison.  A lane keeps its best few keys
-// (D); rounds of a minimum over the group take the best and pop it from its lane.  The exact
-// selection takes over for the warp where this one cannot tell: a lane gave all it kept; among
-// the chosen and those that agree with the last of them, some agree in the upper bits but not in
-// their logits; fewer than k logits are above -inf in x; or the sum is not that of a softmax
-// (NaN, infinities, overflow).  It costs ten times the instructions, so a lane
-// keeps four keys of 16 or 32 lanes (on normal logits with k = 8, one token in 300 of 128 experts
-// and one in 1000 of 256 needs a fifth; keeping three, one in 25 of 256 took 22 of 69 us), and
-// all eight where fewer lanes share the experts.
+// (D); rounds of a minimum over the group take the best and pop it from its lane.
+//
+// Some tokens this cannot decide: a lane gave all it kept; logits that agree in the upper bits came
+// out in the wrong order, or the lesser was chosen; fewer than k logits are above -inf in x; or the
+// sum is not that of a softmax (NaN, infinities, overflow).  They are
+// left out, marked in `index`, and a second loop selects for them exactly (in the first loop that
+// path cost a fifth of its instructions even where it was not taken).  On normal fp32 logits with
+// k = 8 that is one token in 2000.  A lane keeps eight keys of up to 16 lanes, four of 32: keeping four
+// of 16, one token in 80 of 256 experts was left over, and 131072 tokens took 88 us.
+//
+// A lane holds 16 experts (32 beyond 512) and not eight, although that leaves registers for half the
+// warps: 262144 tokens of 128 experts take 80 us and not 100, bf16 of 64 36 and not 47.
+constexpr int UNDECIDED = -2;
+
 template <typename T, bool VEC, int G, int NC>
 __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const RouterParams p) {
   begin_after_previous();
@@ -290,11 +313,12 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
   __shared__ int warp_used[WARPS];
   constexpr int V = 8 * NC;
   constexpr int TOK = 32 / G;                          // tokens per warp
-  constexpr int SLOTS = Slots<G>::N;
-  constexpr uint32_t IDX = NC == 1 ? 255 : 256 * NC - 1;   // the expert's bits of a key
+  constexpr int SLOTS = Slots<G, V>::N;
+  constexpr bool BYTE = V * G <= 256;                  // the expert's number is a byte
+  constexpr uint32_t IDX = BYTE ? 255 : V * G - 1;     // its bits of a key
   constexpr uint32_t CLOSED = 0xFF800000u;             // a key from here on: x = -inf
   constexpr uint32_t NONE = 0xFFFFFFFFu;               // no key
-  constexpr int D = G >= 16 ? 4 : 8;                   // keys a lane keeps
+  constexpr int D = G < 32 ? 8 : 4;                    // keys a lane keeps
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane % G;
   int* scount = reinterpret_cast<int*>(dyn + WARPS * p.experts);
@@ -304,10 +328,11 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
   float psum[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) psum[j] = 0.f;
-  // the bytes that the lane's eight experts have in keys of one piece
-  const uint32_t low_bytes = static_cast<uint32_t>(8 * g) * 0x01010101u + 0x03020100u;
-  const uint32_t high_bytes = low_bytes + 0x04040404u;
+  uint32_t bytes[V / 4];                               // the numbers of the lane's experts, four to a word
+#pragma unroll
+  for (int q = 0; q < V / 4; ++q) bytes[q] = static_cast<uint32_t>(expert_of<G>(q / 2, g, 4 * (q & 1))) * 0x01010101u + 0x03020100u;
   int used_here = 0;
+  bool left_over = false;
   const int stride = static_cast<int>(gridDim.x) * WARPS * TOK;   // tokens < 2^31, checked before the launch
   Logits<T, VEC, G, NC> next;
   long long token = static_cast<long long>(blockIdx.x * WARPS + warp) * TOK + lane / G;
@@ -337,8 +362,8 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       const float x = fmaf(l[j], LOG2E, down);
       e[j] = exp2_approx(x);
       sum += e[j];
-      if constexpr (NC == 1)      // the expert's byte in place of the lowest one
-        key[j] = __byte_perm(__float_as_uint(x), j < 4 ? low_bytes : high_bytes, 0x3210 + 4 + (j & 3));
+      if constexpr (BYTE)         // in place of the lowest byte
+        key[j] = __byte_perm(__float_as_uint(x), bytes[j / 4], 0x3210 + 4 + (j & 3));
       else
         key[j] = (__float_as_uint(x) & ~IDX) | static_cast<uint32_t>(expert_of<G>(j / 8, g, j & 7));
     }
@@ -372,52 +397,39 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
         if (mine < CLOSED) {
           idx[s] = static_cast<int>(mine & IDX);
           w[s] = to_float(here[idx[s]]);
-          // neighbours whose order the numbers alone decided have to be equal
-          if (r + 1 < p.k && (mine & ~IDX) == (then & ~IDX)) unsure |= !(w[s] == to_float(here[then & IDX]));
+          // neighbours whose order the numbers alone decided: the second may not be the larger
+          if (r + 1 < p.k && (mine & ~IDX) == (then & ~IDX)) unsure |= !(w[s] >= to_float(here[then & IDX]));
         }
       }
     }
-    // and so do the last chosen and all that agree with it
-    const bool tie = on && !unsure && (last & ~IDX) == (after & ~IDX);
+    // nor may one left out be larger than the last chosen
+    const bool tie = on && (last & ~IDX) == (after & ~IDX);
     if (__any_sync(FULL, tie)) {
-      const float worst = tie ? to_float(here[last & IDX]) : 0.f;
+      const float worst = tie && last < CLOSED ? to_float(here[last & IDX]) : 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        unsure |= tie && (__float_as_uint(fmaf(l[j], LOG2E, down)) & ~IDX) == (last & ~IDX) && !(l[j] == worst);
-    }
-    bool some = on && m > MINUS_INF;
-    if (__any_sync(FULL, unsure)) {
-      __syncwarp();
-      const ExactSoftmax x = select_exact<T, G, V>(here, on, p.experts, p.k, g, order);
-      __syncwarp();
-      sum = x.sum;
-      some = x.some;
-#pragma unroll
-      for (int j = 0; j < V; ++j) e[j] = l[j] == MINUS_INF ? 0.f : expf(l[j] - x.m);
-#pragma unroll
-      for (int s = 0; s < SLOTS; ++s) {
-        const int r = s * G + g;
-        idx[s] = r < p.k ? static_cast<int>(order[r]) : -1;
-        w[s] = idx[s] >= 0 ? expf(to_float(here[idx[s]]) - x.m) : 0.f;
+      for (int j = 0; j < V; ++j) {
+        const uint32_t x = __float_as_uint(fmaf(l[j], LOG2E, down)) & ~IDX;
+        unsure |= tie && x == (last & ~IDX) && (x | expert_of<G>(j / 8, g, j & 7)) > last && !(l[j] <= worst);
       }
-    } else {
-#pragma unroll
-      for (int s = 0; s < SLOTS; ++s) w[s] = idx[s] >= 0 ? exp2_approx(fmaf(w[s], LOG2E, down)) : 0.f;
     }
-    const bool used = on && some;
+    unsure = any_of_group<G>(unsure, lane);
+    left_over |= unsure;
+    const bool used = on && !unsure;
     const float inv = used ? reciprocal(sum) : 0.f;
     if (used) {
 #pragma unroll
       for (int j = 0; j < V; ++j) psum[j] = fmaf(e[j], inv, psum[j]);
       if (g == 0) ++used_here;
     }
-    float scale = inv;                                 // of the terms of the chosen: 0 or NaN with them
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) w[s] = idx[s] >= 0 ? exp2_approx(fmaf(w[s], LOG2E, down)) : 0.f;
+    float scale = inv;
     if (p.normalize) {
       float chosen = 0.f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) chosen += w[s];
-      chosen = group_add<G>(chosen);
-      scale = used ? (sum != sum ? sum : reciprocal(chosen)) : 0.f;
+      chosen = group_add<G>(chosen);                   // by every lane, whether its token counts or not
+      scale = used ? reciprocal(chosen) : 0.f;
     }
     int* to_index = p.index + at;
     float* to_gate = p.gate + at;
@@ -426,9 +438,54 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
     for (int s = 0; s < SLOTS; ++s) {
       if (s * G >= p.k) break;
       if (s * G + g < p.k && token < p.tokens) {
-        to_index[s * G] = idx[s];
+        to_index[s * G] = unsure ? UNDECIDED : idx[s];
         to_gate[s * G] = w[s] * scale;                 // w is 0 at a place without an expert
-        if (idx[s] >= 0) count_one(&scount[idx[s]]);
+        if (used && idx[s] >= 0) count_one(&scount[idx[s]]);
+      }
+    }
+  }
+  __syncwarp();
+  // the tokens left over, exactly: a lane looks up one of the warp's next 32, then their groups work
+  for (long long from = first; __any_sync(FULL, left_over) && from < p.tokens; from += G * static_cast<long long>(stride)) {
+    const long long look = from + lane / TOK * static_cast<long long>(stride) + lane % TOK;
+    uint32_t todo = __ballot_sync(FULL, look < p.tokens && p.index[look * p.k] == UNDECIDED);
+    while (todo != 0) {
+      const int round = (__ffs(static_cast<int>(todo)) - 1) / TOK;
+      const bool mine = (todo >> (round * TOK + lane / G) & 1u) != 0;
+      todo &= ~((TOK == 32 ? FULL : (1u << (TOK & 31)) - 1u) << (round * TOK));
+      const long long t = from + round * static_cast<long long>(stride) + lane / G;
+      const T* row = static_cast<const T*>(p.logits) + t * p.stride;
+      float l[V], e[V], sum, m;
+      int idx[SLOTS];
+      bool some;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int x = expert_of<G>(j / 8, g, j & 7);
+        l[j] = mine && x < p.experts ? to_float(row[x]) : MINUS_INF;
+      }
+      select_exact<G, V, SLOTS>(l, g, p.k, idx, e, sum, m, some);
+      const float inv = some ? 1.f / sum : 0.f;
+      float w[SLOTS], chosen = 0.f;
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        w[s] = mine && idx[s] >= 0 ? expf(to_float(row[idx[s]]) - m) : 0.f;
+        chosen += w[s];
+      }
+      chosen = group_add<G>(chosen);
+      const float scale = p.normalize && some && sum == sum ? 1.f / chosen : inv;
+      if (mine && some) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) psum[j] = fmaf(e[j], inv, psum[j]);
+        if (g == 0) ++used_here;
+      }
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        const int r = s * G + g;
+        if (mine && r < p.k) {
+          p.index[t * p.k + r] = idx[s];
+          p.gate[t * p.k + r] = idx[s] >= 0 ? w[s] * scale : 0.f;
+          if (idx[s] >= 0) count_one(&scount[idx[s]]);
+        }
       }
     }
   }
@@ -671,20 +728,31 @@ int lanes_for(int experts) {
   return g;
 }
 
+// Lanes of a token and pieces of eight experts per lane in the forward pass.
+struct FwdShape {
+  int g, nc, ctas;     // and CTAs per SM
+};
+FwdShape fwd_shape(int experts) {
+  if (experts <= 8) return {1, 1, 2};
+  int g = 1;
+  while (g < 32 && g * 16 < experts) g *= 2;
+  return {g, experts > 512 ? 4 : 2, 1};
+}
+
 template <typename P>
 using Kernel = void (*)(P);
 
 template <typename T, bool VEC>
 Kernel<RouterParams> fwd_kernel(int g, int nc) {
   if (nc == 4) return router_kernel<T, VEC, 32, 4>;
-  if (nc == 2) return router_kernel<T, VEC, 32, 2>;
+  if (nc == 1) return router_kernel<T, VEC, 1, 1>;
   switch (g) {
-    case 1: return router_kernel<T, VEC, 1, 1>;
-    case 2: return router_kernel<T, VEC, 2, 1>;
-    case 4: return router_kernel<T, VEC, 4, 1>;
-    case 8: return router_kernel<T, VEC, 8, 1>;
-    case 16: return router_kernel<T, VEC, 16, 1>;
-    default: return router_kernel<T, VEC, 32, 1>;
+    case 1: return router_kernel<T, VEC, 1, 2>;
+    case 2: return router_kernel<T, VEC, 2, 2>;
+    case 4: return router_kernel<T, VEC, 4, 2>;
+    case 8: return router_kernel<T, VEC, 8, 2>;
+    case 16: return router_kernel<T, VEC, 16, 2>;
+    default: return router_kernel<T, VEC, 32, 2>;
   }
 }
 template <typename T, bool VEC>
@@ -713,9 +781,9 @@ int pieces_for(int experts, int g) {
 template <typename T>
 cudaError_t fwd(const RouterParams& p, cudaStream_t s, int* launches) {
   const bool vec = p.experts % 8 == 0 && vec_rows(p.logits, p.stride, sizeof(T), p.tokens);
-  const int g = lanes_for(p.experts), nc = pieces_for(p.experts, g);
-  const auto kernel = vec ? fwd_kernel<T, true>(g, nc) : fwd_kernel<T, false>(g, nc);
-  const size_t smem = (static_cast<size_t>(WARPS + 1) * p.experts + WARPS * (32 / g) * (p.k + 1)) * 4;
+  const FwdShape f = fwd_shape(p.experts);
+  const auto kernel = vec ? fwd_kernel<T, true>(f.g, f.nc) : fwd_kernel<T, false>(f.g, f.nc);
+  const size_t smem = (static_cast<size_t>(WARPS + 1) * p.experts + WARPS * (32 / f.g) * (p.k + 1)) * 4;
   cudaError_t e;
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
@@ -747,14 +815,13 @@ cudaError_t bwd(const RouterBwdParams& p, int sms, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs of the forward pass: up to two per SM, at least two tokens per group of lanes in each
-// where there are enough of them (one CTA also finishes the sums without a second launch).
+// CTAs of the forward pass: as many as the SMs hold, with at least two tokens per group of lanes in
+// each where there are enough of them (one CTA also finishes the sums without a second launch).
 int router_parts(int tokens, int experts, int sms) {
-  const int per = WARPS * (32 / lanes_for(experts)) * 2;
-  int want = static_cast<int>((static_cast<long long>(tokens) + per - 1) / per);
-  if (want > 2 * sms) want = 2 * sms;
-  if (want > ROUTER_MAX_PARTS) want = ROUTER_MAX_PARTS;
-  return want < 1 ? 1 : want;
+  const FwdShape f = fwd_shape(experts);
+  const long long per = WARPS * (32 / f.g) * 2, want = (tokens + per - 1) / per;
+  const long long most = std::min<long long>(static_cast<long long>(f.ctas) * sms, ROUTER_MAX_PARTS);
+  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
 }
 
 cudaError_t launch_router(RouterParams p, int type, int sms, cudaStream_t s, int* launches) {
