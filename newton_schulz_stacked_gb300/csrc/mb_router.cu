@@ -234,71 +234,85 @@ struct Slots {
   static constexpr int N = 32 / G < V ? 32 / G : V;    // k <= V G and k <= 32
 };
 
-// A token's softmax and its k largest logits for any values: k rounds over exact keys, the winner's
-// lane looking for its next among what comes after the one just taken.  The terms are exp(l - max);
-// NaN or +inf among the logits makes the sum NaN, and with it every probability of the token.
-template <int G, int V, int SLOTS>
-__device__ __forceinline__ void select_exact(const float (&l)[V], int g, int k, int (&idx)[SLOTS], float (&e)[V],
-                                             float& sum, float& m, bool& some) {
-  uint32_t key[V], k1 = 0, top = 0;
-  int i1 = 0;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    key[j] = key_of(l[j]);
-    if (key[j] > k1) {
-      k1 = key[j];
-      i1 = j;
-    }
-  }
-#pragma unroll
-  for (int s = 0; s < SLOTS; ++s) idx[s] = -1;
+// A token's softmax and its k largest logits for any values, in little code, because it is rare and
+// its instructions have to be fetched first: every round looks for the best that comes after the one
+// before it, over exact keys.  Puts the chosen experts into `order` (-1: none).  The terms of the
+// softmax are exp(l - m); NaN or +inf among the logits makes the sum NaN, and with it every
+// probability of the token.
+struct ExactSoftmax {
+  float m, sum;
+  bool some;
+};
+template <typename T, int G, int V>
+__device__ __forceinline__ ExactSoftmax select_exact(const T* row, bool mine, int experts, int g, int k, uint32_t* order) {
+  ExactSoftmax x{0.f, 0.f, false};
+  uint32_t before = 0xFFFFFFFFu, top = 0;
+  uint32_t before_e = 0xFFFFFFFFu;                     // the first round takes any
+#pragma unroll 1
   for (int r = 0; r < k; ++r) {
-    const uint32_t best = group_max<G>(k1);
-    if (r == 0) top = best;
-    const uint32_t mine = k1 == best && best != 0 ? expert_of<G>(i1 / 8, g, i1 & 7) : 0x7FFFFFFFu;
-    const uint32_t who = group_min<G>(mine);
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s)
-      if (r == s * G + g && best != 0) idx[s] = static_cast<int>(who);
-    if (best != 0 && mine == who) {
-      const uint32_t lk = k1;
-      const int li = i1;
-      k1 = 0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const bool after = key[j] < lk || (key[j] == lk && j > li);
-        if (after && key[j] > k1) {
-          k1 = key[j];
-          i1 = j;
-        }
+    uint32_t best = 0, who = 0x7FFFFFFFu;
+#pragma unroll 4
+    for (int j = 0; j < V; ++j) {
+      const uint32_t e = expert_of<G>(j / 8, g, j & 7);
+      const uint32_t key = mine && e < static_cast<uint32_t>(experts) ? key_of(to_float(row[e])) : 0;
+      const bool after = r == 0 || key < before || (key == before && e > before_e);
+      if (after && key > best) {
+        best = key;
+        who = e;
+      }
+    }
+    before = group_max<G>(best);
+    before_e = group_min<G>(best == before && before != 0 ? who : 0x7FFFFFFFu);
+    if (r == 0) top = before;
+    order[r] = before != 0 ? before_e : 0xFFFFFFFFu;   // the same value from every lane of the group
+  }
+  x.some = top != 0;
+  x.m = value_of(top);
+#pragma unroll 4
+  for (int j = 0; j < V; ++j) {
+    const int e = expert_of<G>(j / 8, g, j & 7);
+    const float l = mine && e < experts ? to_float(row[e]) : MINUS_INF;
+    x.sum += l == MINUS_INF ? 0.f : expf(l - x.m);
+  }
+  x.sum = group_add<G>(x.sum);
+  if (top >= 0xFF800000u) x.sum = __uint_as_float(0x7FC00000u);
+  return x;
+}
+
+// Puts keys 0..k, whose upper bits are in order, in the order of their logits (the lower number first
+// among equals, as they come).
+template <uint32_t IDX, typename T>
+__device__ __forceinline__ void put_right(uint32_t* order, int k, const T* row) {
+  bool moved = true;
+#pragma unroll 1
+  for (int pass = 0; pass < k && moved; ++pass) {
+    moved = false;
+#pragma unroll 1
+    for (int r = 0; r < k; ++r) {
+      const uint32_t a = order[r], b = order[r + 1];
+      if (((a ^ b) & ~IDX) == 0 && to_float(row[a & IDX]) < to_float(row[b & IDX])) {
+        order[r] = b;
+        order[r + 1] = a;
+        moved = true;
       }
     }
   }
-  some = top != 0;
-  m = value_of(top);
-  sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    e[j] = key[j] == 0 ? 0.f : expf(l[j] - m);
-    sum += e[j];
-  }
-  sum = group_add<G>(sum);
-  if (top >= 0xFF800000u) sum = __uint_as_float(0x7FC00000u);
 }
 
 // Selection without conditions per element.  With c = max * log2(e) rounded up, x = l log2(e) - c
 // is at most 0, monotone in l, and the exponent the softmax needs anyway.  The bits of such an x
 // grow as l falls, so a key of x's upper bits and the expert's number in the low ones sorts by
 // falling logit, then by number, with one minimum per comparison.  A lane keeps its best few keys
-// (D); rounds of a minimum over the group take the best and pop it from its lane.
+// (D: eight of up to 8 lanes, four of 32); rounds of a minimum over the group take the best and pop
+// it from its lane.  Where a lane gave all it kept, the rounds are done again over all keys (with
+// k = 8 that is one token in 1000 of 256 experts, and every one of equal logits).
 //
-// Some tokens this cannot decide: a lane gave all it kept; logits that agree in the upper bits came
-// out in the wrong order, or the lesser was chosen; fewer than k logits are above -inf in x; or the
-// sum is not that of a softmax (NaN, infinities, overflow).  They are
-// left out, marked in `index`, and a second loop selects for them exactly (in the first loop that
-// path cost a fifth of its instructions even where it was not taken).  On normal fp32 logits with
-// k = 8 that is one token in 2000.  A lane keeps eight keys of up to 16 lanes, four of 32: keeping four
-// of 16, one token in 80 of 256 experts was left over, and 131072 tokens took 88 us.
+// Neighbours in the order whose keys agree in the upper bits are compared themselves and put right by
+// their group's first lane.  Some tokens this cannot decide: more than the first left out agrees
+// with the last chosen, and is larger; fewer than k are above -inf in x though not in the logits; or
+// the sum is not that of a softmax (NaN, infinities, overflow).  They are left out, marked in
+// `index`, and a second loop selects for them exactly (in the first loop that path cost a fifth of
+// its instructions even where it was not taken).
 //
 // A lane holds 16 experts (32 beyond 512) and not eight, although that leaves registers for half the
 // warps: 262144 tokens of 128 experts take 80 us and not 100, bf16 of 64 36 and not 47.
@@ -346,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
   for (long long base = first; base < p.tokens; base += stride, token += stride) {
     float l[V];
     next.get(l);
-    const bool on = next.on;
+    bool on = next.on;
     const T* here = row;
     row += row_step;
     if (base + stride < p.tokens) fetch(token + stride);
@@ -354,6 +368,13 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
 #pragma unroll
     for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
     m = group_fmax<G>(m);
+    if (__any_sync(FULL, on && m == MINUS_INF)) {      // no expert is open, or NaN hides behind -inf
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < V; ++j) nan |= l[j] != l[j];
+      nan = any_of_group<G>(nan, lane);
+      on &= m > MINUS_INF || nan;
+    }
     const float down = 0.f - __fmul_ru(m, LOG2E);      // +0 for a maximum of either zero
     float e[V], sum = 0.f;
     uint32_t key[V];
@@ -372,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
     least<D, V>(key, own);
     const uint32_t deepest = own[D - 1];
     // the k best of the group and the first after them, in order; a lane that has given the last
-    // of its kept keys gives it again, and is found by that
+    // of its kept keys gives it again
 #pragma unroll 3
     for (int r = 0; r <= p.k; ++r) {
       const uint32_t best = group_min<G>(own[0]);
@@ -383,10 +404,32 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       if constexpr (D == V) own[D - 1] = won ? NONE : own[D - 1];
     }
     __syncwarp();
-    const uint32_t last = order[p.k - 1], after = order[p.k];
-    bool unsure = on && ((D < V && deepest <= last) || last >= CLOSED || !(sum >= 0.5f));
+    if (D < V && p.k >= D && __any_sync(FULL, on && deepest <= order[p.k - 1])) {
+      // a lane gave all it kept: the rounds again, over all keys
+      uint32_t taken = 0;
+      bool none = true;
+      __syncwarp();
+#pragma unroll 1
+      for (int r = 0; r <= p.k; ++r) {
+        uint32_t mine = NONE;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const uint32_t x = (__float_as_uint(fmaf(l[j], LOG2E, down)) & ~IDX) |
+                             static_cast<uint32_t>(expert_of<G>(j / 8, g, j & 7));
+          if (none || x > taken) mine = min(mine, x);
+        }
+        const uint32_t best = group_min<G>(mine);
+        order[r] = best;
+        if (mine == best) {
+          taken = best;
+          none = false;
+        }
+      }
+      __syncwarp();
+    }
     int idx[SLOTS];
     float w[SLOTS];                                    // the chosen logits, then the softmax's terms
+    bool wrong = false;                                // a key's successor has the larger logit
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       const int r = s * G + g;
@@ -397,19 +440,41 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
         if (mine < CLOSED) {
           idx[s] = static_cast<int>(mine & IDX);
           w[s] = to_float(here[idx[s]]);
-          // neighbours whose order the numbers alone decided: the second may not be the larger
-          if (r + 1 < p.k && (mine & ~IDX) == (then & ~IDX)) unsure |= !(w[s] >= to_float(here[then & IDX]));
+          if ((mine & ~IDX) == (then & ~IDX)) wrong |= !(w[s] >= to_float(here[then & IDX]));
         }
       }
     }
-    // nor may one left out be larger than the last chosen
-    const bool tie = on && (last & ~IDX) == (after & ~IDX);
-    if (__any_sync(FULL, tie)) {
-      const float worst = tie && last < CLOSED ? to_float(here[last & IDX]) : 0.f;
+    if (__any_sync(FULL, wrong)) {
+      if (g == 0 && on) put_right<IDX>(order, p.k, here);
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint32_t x = __float_as_uint(fmaf(l[j], LOG2E, down)) & ~IDX;
-        unsure |= tie && x == (last & ~IDX) && (x | expert_of<G>(j / 8, g, j & 7)) > last && !(l[j] <= worst);
+      for (int s = 0; s < SLOTS; ++s) {
+        if (idx[s] >= 0) {
+          idx[s] = static_cast<int>(order[s * G + g] & IDX);
+          w[s] = to_float(here[idx[s]]);
+        }
+      }
+    }
+    const uint32_t last = order[p.k - 1], after = order[p.k];
+    bool unsure = on && !(sum >= 0.5f);
+    if (__any_sync(FULL, on && last >= CLOSED)) {      // fewer than k above -inf: in the logits, or only in x?
+#pragma unroll
+      for (int j = 0; j < V; ++j) unsure |= on && l[j] > MINUS_INF && fmaf(l[j], LOG2E, down) == MINUS_INF;
+    }
+    const bool tie = on && last < CLOSED && (last & ~IDX) == (after & ~IDX);
+    if (__any_sync(FULL, tie)) {                       // no other that agrees with the last may be larger
+      const float worst = tie ? to_float(here[last & IDX]) : 0.f;
+      uint32_t larger = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (tie && ((__float_as_uint(fmaf(l[j], LOG2E, down)) ^ last) & ~IDX) == 0 && !(l[j] <= worst)) larger |= 1u << j;
+      while (larger != 0) {
+        const int j = __ffs(static_cast<int>(larger)) - 1, e = expert_of<G>(j / 8, g, j & 7);
+        larger &= larger - 1;
+        bool chosen = false;
+#pragma unroll 1
+        for (int r = 0; r < p.k; ++r) chosen |= (order[r] & IDX) == static_cast<uint32_t>(e);
+        unsure |= !chosen;
       }
     }
     unsure = any_of_group<G>(unsure, lane);
@@ -443,6 +508,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
         if (used && idx[s] >= 0) count_one(&scount[idx[s]]);
       }
     }
+    __syncwarp();                                      // the order has been read
   }
   __syncwarp();
   // the tokens left over, exactly: a lane looks up one of the warp's next 32, then their groups work
@@ -455,27 +521,27 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       todo &= ~((TOK == 32 ? FULL : (1u << (TOK & 31)) - 1u) << (round * TOK));
       const long long t = from + round * static_cast<long long>(stride) + lane / G;
       const T* row = static_cast<const T*>(p.logits) + t * p.stride;
-      float l[V], e[V], sum, m;
+      const ExactSoftmax x = select_exact<T, G, V>(row, mine, p.experts, g, p.k, order);
+      __syncwarp();
+      const float inv = x.some ? 1.f / x.sum : 0.f;
       int idx[SLOTS];
-      bool some;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int x = expert_of<G>(j / 8, g, j & 7);
-        l[j] = mine && x < p.experts ? to_float(row[x]) : MINUS_INF;
-      }
-      select_exact<G, V, SLOTS>(l, g, p.k, idx, e, sum, m, some);
-      const float inv = some ? 1.f / sum : 0.f;
       float w[SLOTS], chosen = 0.f;
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
-        w[s] = mine && idx[s] >= 0 ? expf(to_float(row[idx[s]]) - m) : 0.f;
+        const int r = s * G + g;
+        idx[s] = mine && r < p.k ? static_cast<int>(order[r]) : -1;
+        w[s] = idx[s] >= 0 ? expf(to_float(row[idx[s]]) - x.m) : 0.f;
         chosen += w[s];
       }
       chosen = group_add<G>(chosen);
-      const float scale = p.normalize && some && sum == sum ? 1.f / chosen : inv;
-      if (mine && some) {
+      const float scale = p.normalize && x.some && x.sum == x.sum ? 1.f / chosen : inv;
+      if (mine && x.some) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) psum[j] = fmaf(e[j], inv, psum[j]);
+        for (int j = 0; j < V; ++j) {
+          const int e = expert_of<G>(j / 8, g, j & 7);
+          const float l = e < p.experts ? to_float(row[e]) : MINUS_INF;
+          psum[j] += l == MINUS_INF && x.sum == x.sum ? 0.f : exp2_approx((l - x.m) * LOG2E) * inv;
+        }
         if (g == 0) ++used_here;
       }
 #pragma unroll
@@ -487,6 +553,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
           if (idx[s] >= 0) count_one(&scount[idx[s]]);
         }
       }
+      __syncwarp();
     }
   }
   // the CTA's sums, in a fixed order: the warp's token groups, then its warps
@@ -734,9 +801,10 @@ struct FwdShape {
 };
 FwdShape fwd_shape(int experts) {
   if (experts <= 8) return {1, 1, 2};
+  if (experts > 128) return {32, experts > 512 ? 4 : experts > 256 ? 2 : 1, experts > 256 ? 1 : 2};
   int g = 1;
-  while (g < 32 && g * 16 < experts) g *= 2;
-  return {g, experts > 512 ? 4 : 2, 1};
+  while (g * 16 < experts) g *= 2;
+  return {g, 2, 1};
 }
 
 template <typename P>
@@ -745,13 +813,12 @@ using Kernel = void (*)(P);
 template <typename T, bool VEC>
 Kernel<RouterParams> fwd_kernel(int g, int nc) {
   if (nc == 4) return router_kernel<T, VEC, 32, 4>;
-  if (nc == 1) return router_kernel<T, VEC, 1, 1>;
+  if (nc == 1) return g == 1 ? router_kernel<T, VEC, 1, 1> : router_kernel<T, VEC, 32, 1>;
   switch (g) {
     case 1: return router_kernel<T, VEC, 1, 2>;
     case 2: return router_kernel<T, VEC, 2, 2>;
     case 4: return router_kernel<T, VEC, 4, 2>;
     case 8: return router_kernel<T, VEC, 8, 2>;
-    case 16: return router_kernel<T, VEC, 16, 2>;
     default: return router_kernel<T, VEC, 32, 2>;
   }
 }
