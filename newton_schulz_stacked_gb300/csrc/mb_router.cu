@@ -722,7 +722,9 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_bwd_kernel(co
       sum += e[j];
     }
     sum = group_add<G>(sum);
-    if (__any_sync(FULL, on && !(sum >= 0.5f))) {      // NaN, infinities, overflow, or no available expert
+    // a softmax's sum is between 1 and the number of experts: else NaN, infinities, overflow (of the
+    // exponents, to either side), or no open expert
+    if (__any_sync(FULL, on && !(sum >= 0.5f && sum <= 2.f * ROUTER_MAX_EXPERTS))) {
       bool any = false;
       float again = 0.f;
 #pragma unroll

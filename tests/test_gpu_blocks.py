@@ -206,6 +206,28 @@ def test_layer_norm_strided_rows_and_guard_bands(nss, dtype, cols, pad, before):
     dx.check("dx")
 
 
+# every distance of a row from a 16-byte boundary, the same and different ones in a call's tensors, and
+# enough rows that every group of threads takes several
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(9001, 17), (3001, 130), (4003, 251), (5001, 263), (4001, 517), (3501, 775), (2501, 1009),
+                                       (1203, 1031), (903, 2051), (703, 3999), (403, 5003)])
+def test_layer_norm_unaligned_rows(nss, dtype, rows, cols):
+    dtype = TYPES[dtype]
+    x, w, b, dy = norm_inputs(rows + cols, rows, cols, dtype, torch.float32)
+    _, mean, rstd = check_norm_forward(nss, x, w, b)
+    check_norm_backward(nss, dy, x, mean, rstd, w)
+    for before, pads in ((3, (0, 0, 0, 0)), (5, (7, 7, 7, 7)), (2, (8, 0, 16, 8)), (1, (1, 0, 3, 2))):
+        src, grad, y, dx = (Guarded((rows, cols), dtype, before, pad) for pad in pads)
+        src.t.copy_(x)
+        grad.t.copy_(dy)
+        # a neighbour of the row that is not finite must not be taken in
+        src.buf[~src.mark], grad.buf[~grad.mark] = float("nan"), float("inf")
+        check_norm_forward(nss, src.t, w, b, y=y.t)
+        y.check("y")
+        check_norm_backward(nss, grad.t, src.t, mean, rstd, w, dx=dx.t)
+        dx.check("dx")
+
+
 @pytest.mark.parametrize("cols", [40, 768, 1001, 4096, 8200, 33001])
 def test_layer_norm_in_place_and_broadcast(nss, cols):
     x, w, b, dy = norm_inputs(11, 45, cols, torch.bfloat16, torch.float32)
@@ -495,6 +517,41 @@ def test_router_ties_and_extremes(nss, experts, k):
         within(out.gate, gate, 2.1 * (2 * 16 + 49) * U * gate + 2.0 ** -125, "gate")
     descending = torch.arange(experts, 0, -1, device="cuda").float().expand(50, experts) * 0.1
     check_router(nss, descending, k)                       # rows 0 elements apart
+
+
+@pytest.mark.parametrize("experts,k", [(8, 3), (16, 16), (24, 8), (60, 4), (64, 8), (128, 8), (256, 8), (256, 4), (500, 6), (1000, 8)])
+def test_router_near_ties(nss, experts, k):
+    """Logits that differ in their last bits only, alone and among others, in every order."""
+    g = gen(77 + experts)
+    t = 700
+    near = 2.0 + torch.randint(0, 9, (t, experts), generator=g, device="cuda") * 2.0 ** -22
+    few = torch.rand((t, experts), generator=g, device="cuda") < 8.0 / experts
+    for scale in (1.0, 1e-3, 300.0):
+        check_router(nss, near * scale, k)
+        check_router(nss, torch.where(few, near, randn(g, t, experts).clamp(max=1.9)) * scale, k, normalize=True)
+        check_router(nss, torch.where(few, near, torch.tensor(float("-inf"), device="cuda")) * scale, k)
+    check_router(nss, torch.zeros(t, experts, device="cuda"), k)
+    check_router(nss, torch.full((t, experts), -7.25, device="cuda").half(), k, normalize=True)
+    # logits near zero under a larger one: distinct bf16 values that one exponent stands for
+    tiny = (randn(g, t, experts) * 1e-30).bfloat16()
+    tiny[:, 3] = 5.0
+    check_router(nss, tiny, k)
+
+
+@pytest.mark.parametrize("experts,k", [(8, 2), (64, 8), (256, 8), (1000, 3)])
+def test_router_huge_logits(nss, experts, k):
+    """Finite logits whose exponents overflow fp32: the largest win, and the rest has probability 0."""
+    g = gen(5)
+    for signs in (1.0, -1.0):
+        l = signs * (2.5e38 + 5e37 * torch.rand((90, experts), generator=g, device="cuda"))
+        l[::3] = randn(g, 30, experts)                     # ordinary tokens beside them
+        l[1::3, ::2] = -3.4e38
+        out = nss.mb_router(l, k)
+        p, index, gate, counts, loss, n = router_ref(l, k, None, False)
+        assert torch.equal(out.index.long(), index) and torch.equal(out.counts.long(), counts) and out.used.item() == 90
+        within(out.gate, gate, 2.1 * (2 * 16 + 49) * U * gate + 2.0 ** -120, "gate")
+        d = nss.mb_router_backward(torch.ones(1, device="cuda"), torch.ones(90, k, device="cuda"), l, *out[:3], out.used)
+        assert torch.isfinite(d).all()
 
 
 def test_router_without_tokens(nss):
