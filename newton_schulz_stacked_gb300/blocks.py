@@ -3,7 +3,8 @@
 Each function has the name of the C entry point it calls (include/muonbank.h gives the
 formulas), takes CUDA tensors and enqueues the work on the current CUDA stream, or on
 `stream`.  Results are new tensors unless the caller passes them; a given result may be the
-input that it replaces.  Every operator has its gradient as a call of its own;
+input that it replaces.  New tensors of one call may share an allocation (mean and rstd; index and
+gate; counts, loss and used).  Every operator has its gradient as a call of its own;
 `newton_schulz_stacked_gb300.autograd` joins the pairs for torch's autograd.
 
 Tensors may be strided in all but their last dimension; a tensor that is not laid out so, or

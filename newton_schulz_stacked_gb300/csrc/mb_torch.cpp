@@ -136,6 +136,33 @@ Tensor result(PyObject* o, const char* what, c10::IntArrayRef shape, ScalarType 
   return *t;
 }
 
+// New results of one call that live equally long in one allocation, 256 bytes apart: an allocation costs 0.7 us of a
+// call, a tensor on a ready one 0.2.
+struct Together {
+  c10::Device device;
+  size_t bytes = 0;
+  c10::Storage storage;
+  explicit Together(c10::Device d) : device(d) {}
+  // reserves room for a result that the caller did not pass; its place
+  size_t room(PyObject* given, int64_t elements) {
+    const size_t at = bytes;
+    if (given == Py_None) bytes += (static_cast<size_t>(elements) * 4 + 255) / 256 * 256;
+    return at;
+  }
+  void allocate() {
+    if (bytes > 0) storage = make({static_cast<int64_t>(bytes)}, ScalarType::Byte, device).storage();
+  }
+  // the given tensor, or the one at `at` (of a 4-byte type)
+  Tensor take(PyObject* given, const char* what, c10::IntArrayRef shape, ScalarType dtype, size_t at) {
+    if (given != Py_None || bytes == 0) return result(given, what, shape, dtype, device);
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                        c10::scalarTypeToTypeMeta(dtype));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset(static_cast<int64_t>(at / 4));
+    return t;
+  }
+};
+
 struct Workspace {
   Tensor own;
   void* ptr = nullptr;
@@ -251,8 +278,11 @@ PyObject* layer_norm(PyObject* const* a, Py_ssize_t n) {
   const auto lead = x.sizes().slice(0, x.dim() - 1);
   const float eps = number(a[3]);
   const Tensor y = result(a[4], "y", x.sizes(), x.scalar_type(), device);
-  const Tensor mean = result(a[5], "mean", lead, ScalarType::Float, device);
-  const Tensor rstd = result(a[6], "rstd", lead, ScalarType::Float, device);
+  Together stats(device);
+  const size_t mean_at = stats.room(a[5], s.rows), rstd_at = stats.room(a[6], s.rows);
+  stats.allocate();
+  const Tensor mean = stats.take(a[5], "mean", lead, ScalarType::Float, mean_at);
+  const Tensor rstd = stats.take(a[6], "rstd", lead, ScalarType::Float, rstd_at);
   checked("mb_layer_norm",
           mb_layer_norm(x.data_ptr(), row_stride(x, "x"), s.type, wp, bp, s.w_type, y.data_ptr(), row_stride(y, "y"),
                         static_cast<float*>(dense(&mean, "mean", lead, ScalarType::Float, device)),
@@ -419,11 +449,17 @@ PyObject* router(PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   checked("mb_router_workspace_bytes", mb_router_workspace_bytes(tokens, experts, &need));
   const Workspace ws(a[9], need, device);
-  const Tensor index = result(a[4], "index", {tokens, k}, ScalarType::Int, device);
-  const Tensor gate = result(a[5], "gate", {tokens, k}, ScalarType::Float, device);
-  const Tensor counts = result(a[6], "counts", {experts}, ScalarType::Int, device);
-  const Tensor loss = result(a[7], "loss", {1}, ScalarType::Float, device);
-  const Tensor used = result(a[8], "used", {1}, ScalarType::Int, device);
+  // what belongs to tokens apart from the rest: a loss that is kept must not keep the tokens' results
+  Together each(device), all(device);
+  const size_t index_at = each.room(a[4], tokens * k), gate_at = each.room(a[5], tokens * k);
+  const size_t counts_at = all.room(a[6], experts), loss_at = all.room(a[7], 1), used_at = all.room(a[8], 1);
+  each.allocate();
+  all.allocate();
+  const Tensor index = each.take(a[4], "index", {tokens, k}, ScalarType::Int, index_at);
+  const Tensor gate = each.take(a[5], "gate", {tokens, k}, ScalarType::Float, gate_at);
+  const Tensor counts = all.take(a[6], "counts", {experts}, ScalarType::Int, counts_at);
+  const Tensor loss = all.take(a[7], "loss", {1}, ScalarType::Float, loss_at);
+  const Tensor used = all.take(a[8], "used", {1}, ScalarType::Int, used_at);
   checked("mb_router",
           mb_router(l.data_ptr(), row_stride(l, "logits"), type, valid, tokens, experts, static_cast<int>(k), normalize,
                     static_cast<int32_t*>(dense(&index, "index", {tokens, k}, ScalarType::Int, device)),
