@@ -39,7 +39,7 @@ __device__ __forceinline__ void normalise(float2 (&f)[4], float m, float r, cons
 template <typename T, Access A, int NV>
 constexpr int FWD_CTAS = A != Access::SCALAR && sizeof(T) == 2 && NV <= 4 ? 3 : sizeof(T) == 4 && NV > 8 ? 1 : 2;
 
-// Rows of up to 4096 elements: tpr lanes of a warp hold a row in NV pieces each and take R rows at a
+// Rows of up to 4096 elements (512 by single elements): tpr lanes of a warp hold a row in NV pieces each and take R rows at a
 // time; no barrier in the loop.  Up to four pieces the next rows are already being loaded (AHEAD);
 // with more, a warp's own row is enough in flight.  Weight and bias wait in shared memory.  The
 // variance sums squares of differences from the mean, over the registers: no cancellation however
@@ -219,8 +219,6 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdParams p) 
 
 // ---------------------------------------------------------------- launches
 
-constexpr int SHIFT_MAX_COLS = 4096;
-
 template <typename T, Access A, int NV, int R>
 cudaError_t fwd_warp(LnFwdParams p, int sms, cudaStream_t s) {
   const int grid = cta_count(p.rows, static_cast<long long>(256 / p.tpr) * R, FWD_CTAS<T, A, NV> * sms);
@@ -228,15 +226,24 @@ cudaError_t fwd_warp(LnFwdParams p, int sms, cudaStream_t s) {
   return launch_after(ln_fwd_kernel<T, A, NV, R>, dim3(grid), dim3(256), smem, s, p);
 }
 
-// Rows of more than 1024 elements.
 template <typename T, Access A>
-cudaError_t fwd_long(const LnFwdParams& p, int pieces, int sms, cudaStream_t s) {
-  constexpr bool SCALAR = A == Access::SCALAR;
+cudaError_t fwd(LnFwdParams p, int sms, cudaStream_t s) {
+  constexpr bool SCALAR = A == Access::SCALAR, SHIFT = A == Access::SHIFT;
+  const int pieces = (p.cols + (SHIFT ? 14 : 7)) / 8;
+  p.tpr = pieces >= 32 ? 32 : pow2_at_least(pieces);
+  if constexpr (!SHIFT) {
+    if (pieces <= 32) return fwd_warp<T, A, 1, SCALAR ? 2 : 4>(p, sms, s);
+    if (pieces <= 64) return fwd_warp<T, A, 2, SCALAR ? 1 : 2>(p, sms, s);
+  }
   if constexpr (!SCALAR) {
+    if (pieces <= 96) return fwd_warp<T, A, 3, 1>(p, sms, s);
+    if (pieces <= 128) return fwd_warp<T, A, 4, 1>(p, sms, s);
     if (pieces <= 256) return fwd_warp<T, A, 8, 1>(p, sms, s);
+  }
+  if constexpr (A == Access::VEC) {
     if (pieces <= 512) return fwd_warp<T, A, 16, 1>(p, sms, s);
   }
-  if constexpr (A != Access::SHIFT) {                  // SHIFT ends at 4096 elements
+  if constexpr (!SHIFT) {
     constexpr int NV = SCALAR ? 2 : 8, MAXT = SCALAR ? 1024 : 512;
     if (pieces <= NV * MAXT) {
       const int threads = (pieces + 32 * NV - 1) / (32 * NV) * 32;
@@ -244,19 +251,7 @@ cudaError_t fwd_long(const LnFwdParams& p, int pieces, int sms, cudaStream_t s) 
     }
     return launch_after(ln_fwd_wide_kernel<T, A>, dim3(cta_count(p.rows, 1, 2 * sms)), dim3(1024), 0, s, p);
   }
-  return cudaErrorInvalidValue;
-}
-
-template <typename T, Access A>
-cudaError_t fwd(LnFwdParams p, int sms, cudaStream_t s) {
-  constexpr bool SCALAR = A == Access::SCALAR;
-  const int pieces = (p.cols + (A == Access::SHIFT ? 14 : 7)) / 8;
-  p.tpr = pieces >= 32 ? 32 : pow2_at_least(pieces);
-  if (pieces <= 32) return fwd_warp<T, A, 1, SCALAR ? 2 : 4>(p, sms, s);
-  if (pieces <= 64) return fwd_warp<T, A, 2, SCALAR ? 1 : 2>(p, sms, s);
-  if (pieces <= 96) return fwd_warp<T, A, 3, 1>(p, sms, s);
-  if (pieces <= 128) return fwd_warp<T, A, 4, 1>(p, sms, s);
-  return fwd_long<T, A>(p, pieces, sms, s);
+  return cudaErrorInvalidValue;                        // SHIFT is for 513 to 2034 elements
 }
 
 template <typename T>
@@ -265,7 +260,9 @@ cudaError_t fwd_any(const LnFwdParams& p, int sms, cudaStream_t s) {
   if (p.cols % 8 == 0 && aligned_rows(p.x, p.x_stride, SIZE, p.rows) && aligned_rows(p.y, p.y_stride, SIZE, p.rows) &&
       aligned(p.w) && aligned(p.b))
     return fwd<T, Access::VEC>(p, sms, s);
-  if (p.cols + 14 <= SHIFT_MAX_COLS && shiftable(p.x_stride, p.cols, p.rows) &&
+  // 2^26 elements in rows of 1001 take 102 us so and 146 by single elements (bf16; fp32 114 and 149), in
+  // rows of 2003 93 and 143 (110 and 147); in rows of 303 224 and 168 (195 and 178), of 3001 184 and 152
+  if (p.cols > 512 && p.cols + 14 <= 2048 && shiftable(p.x_stride, p.cols, p.rows) &&
       same_shift(p.x, p.x_stride, p.y, p.y_stride, SIZE, p.rows))
     return fwd<T, Access::SHIFT>(p, sms, s);
   return fwd<T, Access::SCALAR>(p, sms, s);

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const L
   extern __shared__ __align__(16) float dyn[];         // the weight; at the end [warps][NV][16][32] sums
   using P = Piece<T, A>;
   constexpr int WARPS = BWD_THREADS<NV> / 32;
-  __shared__ int shifts[WARPS];
+  static_assert(A != Access::SHIFT, "single elements are as fast here");
   const int cols = p.cols, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float inv_n = 1.f / static_cast<float>(cols);
   const long long stride = static_cast<long long>(gridDim.x) * WARPS;
@@ -158,17 +158,12 @@ __global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const L
   float next_m = 0.f, next_rs = 0.f;
   const T *x = static_cast<const T*>(p.x) + row * p.x_stride, *dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
   T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
-  Place at{cols, 32, lane, 0};
-  if (A == Access::SHIFT) {
-    at.shift = shift_of(x);
-    if (lane == 0) shifts[warp] = at.shift;
-  }
+  const Place at{cols, 32, lane, 0};
   auto fetch = [&](long long r) {
-    const bool edge = r == 0 || r == p.rows - 1;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      next_x[v].load(x, at, v, true, edge);
-      next_dy[v].load(dy, at, v, true, edge);
+      next_x[v].load(x, at, v, true, false);
+      next_dy[v].load(dy, at, v, true, false);
     }
     next_m = p.mean[r];
     next_rs = p.rstd[r];
@@ -226,27 +221,14 @@ __global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const L
     }
   }
   __syncthreads();
-  const int count = A == Access::SHIFT ? 2 * cols : NV * 16 * 32;
-  for (int e = threadIdx.x; e < count; e += blockDim.x) {
+  for (int e = threadIdx.x; e < NV * 16 * 32; e += blockDim.x) {
+    const int j = (e >> 5) & 7, v = e >> 9, k = (e >> 8) & 1;      // k: of dw or db
+    const Place there{cols, 32, e & 31, 0};
+    if (!P::in(there, v, j)) continue;
     float sum = 0.f;
-    int c, k;                                          // the column, and whether of dw or db
-    if constexpr (A == Access::SHIFT) {
-      k = e >= cols;
-      c = e - k * cols;
 #pragma unroll
-      for (int u = 0; u < WARPS; ++u) {
-        const int i = c + shifts[u];
-        sum += dyn[((u * NV + (i >> 8)) * 16 + k * 8 + (i & 7)) * 32 + ((i >> 3) & 31)];
-      }
-    } else {
-      const int j = (e >> 5) & 7, v = e >> 9;
-      const Place there{cols, 32, e & 31, 0};
-      if (!P::in(there, v, j)) continue;
-#pragma unroll
-      for (int u = 0; u < WARPS; ++u) sum += dyn[u * NV * 512 + e];
-      c = P::col(there, v, j);
-      k = (e >> 8) & 1;
-    }
+    for (int u = 0; u < WARPS; ++u) sum += dyn[u * NV * 512 + e];
+    const int c = P::col(there, v, j);
     if (p.parts) {
       p.parts[(static_cast<size_t>(blockIdx.x) * 2 + k) * cols + c] = sum;
     } else {
@@ -392,50 +374,67 @@ cudaError_t bwd_wide(const LnBwdParams& p, int sms, cudaStream_t s, int* launche
   return launch_after(ln_bwd_wide_kernel<T, A>, dim3(cta_count(p.rows, 1, 2 * sms)), dim3(1024), 0, s, p);
 }
 
-template <typename T, Access A>
-cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
-  const bool params = p.dw || p.db;
-  cudaError_t e;
+// A kernel and its launch.
+struct BwdLaunch {
+  void (*kernel)(LnBwdParams);
   int grid, threads, rows_per_cta;
   size_t smem;
-  void (*kernel)(LnBwdParams);
-  const int pieces = (p.cols + (A == Access::SHIFT ? 14 : 7)) / 8;
-  if (pieces > 32 && pieces <= 128) {
-    const int nv = (pieces + 31) / 32;
-    threads = nv == 2 ? BWD_THREADS<2> : nv == 3 ? BWD_THREADS<3> : BWD_THREADS<4>;
-    rows_per_cta = threads / 32;
-    grid = cta_count(p.rows, rows_per_cta, std::min(LN_MAX_PARTS, sms));
-    const int staged = nv == 2 ? Staged<A, 2>::floats(32) : nv == 3 ? Staged<A, 3>::floats(32) : Staged<A, 4>::floats(32);
-    smem = static_cast<size_t>(params ? std::max(staged, 16 * nv * threads) : staged) * sizeof(float);
-    kernel = nv == 2 ? ln_bwd_warp_kernel<T, A, 2> : nv == 3 ? ln_bwd_warp_kernel<T, A, 3> : ln_bwd_warp_kernel<T, A, 4>;
-  } else {
-    const GroupShape g = group_shape(pieces, A == Access::VEC);
-    p.tpr = g.tpr;
-    p.groups = g.groups;
-    threads = g.groups * g.tpr;
-    rows_per_cta = g.groups * g.rows;
-    grid = cta_count(p.rows, rows_per_cta, std::min(LN_MAX_PARTS, g.ctas * sms));
-    smem = params ? static_cast<size_t>(threads) * 16 * sizeof(float) : 0;
-    constexpr int R = A == Access::VEC ? 2 : 1;
-    kernel = g.most == 288   ? ln_bwd_kernel<T, A, R, 288>
+};
+
+template <typename T, Access A>
+BwdLaunch bwd_warp_launch(const LnBwdParams& p, int pieces, int sms) {
+  const bool params = p.dw || p.db;
+  const int nv = (pieces + 31) / 32;
+  BwdLaunch l{};
+  l.threads = nv == 2 ? BWD_THREADS<2> : nv == 3 ? BWD_THREADS<3> : BWD_THREADS<4>;
+  l.rows_per_cta = l.threads / 32;
+  l.grid = cta_count(p.rows, l.rows_per_cta, std::min(LN_MAX_PARTS, sms));
+  const int staged = nv == 2 ? Staged<A, 2>::floats(32) : nv == 3 ? Staged<A, 3>::floats(32) : Staged<A, 4>::floats(32);
+  l.smem = static_cast<size_t>(params ? std::max(staged, 16 * nv * l.threads) : staged) * sizeof(float);
+  l.kernel = nv == 2 ? ln_bwd_warp_kernel<T, A, 2> : nv == 3 ? ln_bwd_warp_kernel<T, A, 3> : ln_bwd_warp_kernel<T, A, 4>;
+  return l;
+}
+
+template <typename T, Access A>
+BwdLaunch bwd_group_launch(LnBwdParams& p, int pieces, int sms) {
+  const GroupShape g = group_shape(pieces, A == Access::VEC);
+  p.tpr = g.tpr;
+  p.groups = g.groups;
+  constexpr int R = A == Access::VEC ? 2 : 1;
+  BwdLaunch l{};
+  l.threads = g.groups * g.tpr;
+  l.rows_per_cta = g.groups * g.rows;
+  l.grid = cta_count(p.rows, l.rows_per_cta, std::min(LN_MAX_PARTS, g.ctas * sms));
+  l.smem = p.dw || p.db ? static_cast<size_t>(l.threads) * 16 * sizeof(float) : 0;
+  l.kernel = g.most == 288   ? ln_bwd_kernel<T, A, R, 288>
              : g.most == 512 ? ln_bwd_kernel<T, A, R, 512> : ln_bwd_kernel<T, A, 1, 1024>;
+  return l;
+}
+
+template <typename T, Access A>
+cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
+  const int pieces = (p.cols + (A == Access::SHIFT ? 14 : 7)) / 8;
+  BwdLaunch l;
+  if constexpr (A == Access::SHIFT) {
+    l = bwd_group_launch<T, A>(p, pieces, sms);
+    // a group's rows lie grid * rows_per_cta apart, which has to be a multiple of 16 bytes whatever
+    // the row; eight rows always are one
+    while (l.grid > 1 && l.grid * l.rows_per_cta % 8 != 0) --l.grid;
+    if (l.grid * l.rows_per_cta % 8 != 0 && p.rows > l.rows_per_cta) return bwd<T, Access::SCALAR>(p, sms, s, launches);
+  } else {
+    l = pieces > 32 && pieces <= 128 ? bwd_warp_launch<T, A>(p, pieces, sms) : bwd_group_launch<T, A>(p, pieces, sms);
   }
-  // SHIFT: a group's rows lie `grid * rows_per_cta` apart, which has to be a multiple of 16 bytes
-  // whatever the row; eight rows always are one
-  if (A == Access::SHIFT)
-    while (grid > 1 && grid * rows_per_cta % 8 != 0) --grid;
-  if (A == Access::SHIFT && grid * rows_per_cta % 8 != 0 && p.rows > rows_per_cta)
-    return bwd<T, Access::SCALAR>(p, sms, s, launches);
-  if (grid == 1 || !params) p.parts = nullptr;
-  if (smem > 40 * 1024 &&
-      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
+  if (l.grid == 1 || !(p.dw || p.db)) p.parts = nullptr;
+  cudaError_t e;
+  if (l.smem > 40 * 1024 &&
+      (e = cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l.smem))) !=
           cudaSuccess)
     return e;
-  if ((e = launch_after(kernel, dim3(grid), dim3(threads), smem, s, p)) != cudaSuccess) return e;
+  if ((e = launch_after(l.kernel, dim3(l.grid), dim3(l.threads), l.smem, s, p)) != cudaSuccess) return e;
   *launches += 1;
   if (!p.parts) return cudaSuccess;
   *launches += 1;
-  return add_parts<T>(p, grid, s);
+  return add_parts<T>(p, l.grid, s);
 }
 
 template <typename T>
@@ -447,14 +446,13 @@ cudaError_t bwd_any(const LnBwdParams& p, int sms, cudaStream_t s, int* launches
   if (p.cols > BWD_MAX_COLS)
     return vec ? bwd_wide<T, Access::VEC>(p, sms, s, launches) : bwd_wide<T, Access::SCALAR>(p, sms, s, launches);
   if (vec) return bwd<T, Access::VEC>(p, sms, s, launches);
-  // fp32 rows go by single elements, which are 128 bytes to a warp already: 5003 x 1001 takes 19.1 us
-  // so and 23.2 in shifted pieces, 67041 x 1001 138 and 149; 16-bit rows of 134083 x 1001 410 and 182
-  if constexpr (SIZE == 2) {
-    if (p.cols + 14 <= BWD_MAX_COLS && shiftable(p.x_stride, p.cols, p.rows) && shiftable(p.dy_stride, p.cols, p.rows) &&
-        same_shift(p.x, p.x_stride, p.dy, p.dy_stride, SIZE, p.rows) &&
-        same_shift(p.x, p.x_stride, p.dx, p.dx_stride, SIZE, p.rows))
-      return bwd<T, Access::SHIFT>(p, sms, s, launches);
-  }
+  // not where a warp holds a row and reads 64 or 128 bytes at a time by single elements too: 2^26 bf16
+  // elements in rows of 777 take 115 us so and 90 by single ones; in rows of 201 148 and 318, of 2003
+  // 124 and 313 (fp32: 161 and 204, 154 and 212)
+  if ((p.cols + 14 <= 256 || p.cols > 1024) && p.cols + 14 <= BWD_MAX_COLS && shiftable(p.x_stride, p.cols, p.rows) &&
+      shiftable(p.dy_stride, p.cols, p.rows) && same_shift(p.x, p.x_stride, p.dy, p.dy_stride, SIZE, p.rows) &&
+      same_shift(p.x, p.x_stride, p.dx, p.dx_stride, SIZE, p.rows))
+    return bwd<T, Access::SHIFT>(p, sms, s, launches);
   return bwd<T, Access::SCALAR>(p, sms, s, launches);
 }
 

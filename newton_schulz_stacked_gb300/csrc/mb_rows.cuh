@@ -183,16 +183,16 @@ struct Piece<T, Access::SHIFT> {
 
 template <typename T>
 struct Piece<T, Access::SCALAR> {
-  float f_[8];
+  T e_[8];             // converted when they are used: a conversion here would wait for the load
   static __device__ __forceinline__ int col(const Place& p, int v, int j) { return (v * 8 + j) * p.tpr + p.t; }
   static __device__ __forceinline__ bool in(const Place& p, int v, int j) { return col(p, v, j) < p.cols; }
   __device__ __forceinline__ void load(const T* row, const Place& p, int v, bool on, bool) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f_[j] = on && in(p, v, j) ? to_float(row[col(p, v, j)]) : 0.f;
+    for (int j = 0; j < 8; ++j) e_[j] = on && in(p, v, j) ? row[col(p, v, j)] : from_float<T>(0.f);
   }
   __device__ __forceinline__ void get(const Place&, int, float (&f)[8]) const {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = f_[j];
+    for (int j = 0; j < 8; ++j) f[j] = to_float(e_[j]);
   }
   static __device__ __forceinline__ void store(T* row, const Place& p, int v, const float (&f)[8]) {
 #pragma unroll
