@@ -238,6 +238,178 @@ __global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const L
   }
 }
 
+// Aligned rows of 1025 to 8192 elements: a group of up to 512 threads holds a row, 16 elements per
+// thread in 16-byte chunks.  Every thread copies its own chunks of the next rows into its own places
+// of a ring in shared memory (so nothing but its own wait orders them), and a row is finished while
+// the next one's sums are under way: one barrier per row, behind a row's worth of other work.
+template <typename T>
+struct Ring {
+  static constexpr int E = 16 / sizeof(T);             // elements of a chunk
+  static constexpr int NC = 16 / E;                    // chunks per thread
+  static constexpr int STAGES = 12 / NC;               // rows: 192 KB with 512 threads
+  static constexpr int MAX_THREADS = 512;
+  static size_t bytes(int threads) { return static_cast<size_t>(STAGES) * 2 * NC * threads * 16; }
+};
+
+__device__ __forceinline__ void chunk_pairs(const uint4& c, float2 (&f)[2], float) {
+  f[0] = make_float2(__uint_as_float(c.x), __uint_as_float(c.y));
+  f[1] = make_float2(__uint_as_float(c.z), __uint_as_float(c.w));
+}
+template <typename T>
+__device__ __forceinline__ void chunk_pairs(const uint4& c, float2 (&f)[4], T) {
+  f[0] = unpack2(c.x, T());
+  f[1] = unpack2(c.y, T());
+  f[2] = unpack2(c.z, T());
+  f[3] = unpack2(c.w, T());
+}
+__device__ __forceinline__ uint4 chunk_of(const float2 (&f)[2], float) {
+  return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+}
+template <typename T>
+__device__ __forceinline__ uint4 chunk_of(const float2 (&f)[4], T) {
+  return make_uint4(pack2(f[0].x, f[0].y, T()), pack2(f[1].x, f[1].y, T()), pack2(f[2].x, f[2].y, T()),
+                    pack2(f[3].x, f[3].y, T()));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(Ring<T>::MAX_THREADS, 1) ln_bwd_ring_kernel(const LnBwdParams p) {
+  begin_after_previous();
+  constexpr int E = Ring<T>::E, NC = Ring<T>::NC, NP = E / 2, STAGES = Ring<T>::STAGES;
+  constexpr int WARPS = Ring<T>::MAX_THREADS / 32;
+  extern __shared__ __align__(16) float dyn[];         // the ring [STAGES][x, dy][NC][threads]; at the end [32][threads] sums
+  __shared__ float2 part[2][WARPS];
+  const int tpr = p.tpr, cols = p.cols, groups = p.groups, threads = blockDim.x;
+  const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float inv_n = 1.f / static_cast<float>(cols);
+  uint4* const mine = reinterpret_cast<uint4*>(dyn) + threadIdx.x;
+  auto place = [&](int stage, int k, int c) { return mine + ((stage * 2 + k) * NC + c) * threads; };
+  auto col = [&](int c) { return (c * tpr + t) * E; };
+
+  // the rows go round the CTAs first
+  const long long stride = static_cast<long long>(gridDim.x) * groups;
+  long long row = blockIdx.x + static_cast<long long>(gridDim.x) * g, ahead = row;
+  const T *x = static_cast<const T*>(p.x) + row * p.x_stride, *dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
+  auto fetch = [&](int stage) {
+    if (ahead < p.rows) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (col(c) < cols) {
+          copy_16(place(stage, 0, c), x + col(c));
+          copy_16(place(stage, 1, c), dy + col(c));
+        }
+      }
+    }
+    copies_end_group();
+    ahead += stride;
+    x += stride * p.x_stride;
+    dy += stride * p.dy_stride;
+  };
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (col(c) >= cols) {
+      for (int k = 0; k < STAGES * 2; ++k) place(k >> 1, k & 1, c)[0] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s);
+  float next_m = 0.f, next_rs = 0.f;
+  if (row < p.rows) next_m = p.mean[row], next_rs = p.rstd[row];
+  float2 w[NC][NP], dw[NC][NP], db[NC][NP];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const bool in = col(c) < cols;
+      w[c][j].x = in ? param<T>(p.w, p.w_f32, 1.f, col(c) + 2 * j) : 0.f;
+      w[c][j].y = in ? param<T>(p.w, p.w_f32, 1.f, col(c) + 2 * j + 1) : 0.f;
+      dw[c][j] = db[c][j] = both(0.f);
+    }
+  }
+
+  float m = 0.f, rs = 0.f;                             // of the row to be finished
+  int stage = 0, before = STAGES - 1, parity = 0;      // places of the present row and of the one before
+  T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
+  auto finish = [&](int from, int half) {
+    float2 sum = both(0.f);
+    for (int u = 0; u < tpr >> 5; ++u) sum = __fadd2_rn(sum, part[half][g * (tpr >> 5) + u]);
+    const float2 c1 = both(-sum.x * inv_n), c2 = both(-sum.y * inv_n), r = both(rs);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float2 h[NP], d[NP];
+      chunk_pairs(*place(from, 0, c), h, T());
+      chunk_pairs(*place(from, 1, c), d, T());
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        h[j] = __fmul2_rn(__fadd2_rn(h[j], both(-m)), r);
+        h[j] = __fmul2_rn(__ffma2_rn(d[j], w[c][j], __ffma2_rn(h[j], c2, c1)), r);
+      }
+      if (col(c) < cols) *reinterpret_cast<uint4*>(dx + col(c)) = chunk_of(h, T());
+    }
+    dx += stride * p.dx_stride;
+  };
+  bool first = true;
+  for (; row < p.rows; row += stride) {
+    copies_wait<STAGES - 2>();
+    const float m_now = next_m, rs_now = next_rs;
+    if (row + stride < p.rows) next_m = p.mean[row + stride], next_rs = p.rstd[row + stride];
+    float2 s1 = both(0.f), s2 = both(0.f);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float2 h[NP], d[NP];
+      chunk_pairs(*place(stage, 0, c), h, T());
+      chunk_pairs(*place(stage, 1, c), d, T());
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {                   // past the row dy is 0, and h of no consequence
+        h[j] = __fmul2_rn(__fadd2_rn(h[j], both(-m_now)), both(rs_now));
+        const float2 gr = __fmul2_rn(d[j], w[c][j]);
+        s1 = __fadd2_rn(s1, gr);
+        s2 = __ffma2_rn(gr, h[j], s2);
+        dw[c][j] = __ffma2_rn(d[j], h[j], dw[c][j]);
+        db[c][j] = __fadd2_rn(db[c][j], d[j]);
+      }
+    }
+    float s[2] = {s1.x + s1.y, s2.x + s2.y};
+    int which;
+    const float sum = warp_sums<2>(s, lane, &which);
+    if ((lane & 15) == 0) (which ? part[parity][warp].y : part[parity][warp].x) = sum;
+    if (!first) finish(before, parity ^ 1);
+    first = false;
+    fetch(before);                                     // its row has been finished
+    m = m_now;
+    rs = rs_now;
+    before = stage;
+    stage = stage + 1 < STAGES ? stage + 1 : 0;
+    parity ^= 1;
+    group_barrier(1 + g, tpr);
+  }
+  if (!first) finish(before, parity ^ 1);
+  if (!p.dw && !p.db) return;
+  copies_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      dyn[(c * E + j) * threads + threadIdx.x] = j & 1 ? dw[c][j / 2].y : dw[c][j / 2].x;
+      dyn[(16 + c * E + j) * threads + threadIdx.x] = j & 1 ? db[c][j / 2].y : db[c][j / 2].x;
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 32 * tpr; e += threads) {
+    const int i = e / tpr, tt = e - i * tpr, k = i >> 4;           // k: of dw or db
+    const int c = ((i & 15) / E * tpr + tt) * E + (i & 15) % E;
+    if (c >= cols) continue;
+    float sum = 0.f;
+    for (int u = 0; u < groups; ++u) sum += dyn[i * threads + u * tpr + tt];
+    if (p.parts) {
+      p.parts[(static_cast<size_t>(blockIdx.x) * 2 + k) * cols + c] = sum;
+    } else {
+      void* out = k ? p.db : p.dw;
+      if (out) put_param_grad(out, p.w_f32, c, sum, T());
+    }
+  }
+}
+
 struct LnPartsParams {
   const float* parts;
   int n, cols, w_f32;
@@ -395,6 +567,19 @@ BwdLaunch bwd_warp_launch(const LnBwdParams& p, int pieces, int sms) {
   return l;
 }
 
+template <typename T>
+BwdLaunch bwd_ring_launch(LnBwdParams& p, int sms) {
+  p.tpr = (p.cols + 16 * 32 - 1) / (16 * 32) * 32;
+  p.groups = Ring<T>::MAX_THREADS / p.tpr;
+  BwdLaunch l{};
+  l.threads = p.groups * p.tpr;
+  l.rows_per_cta = p.groups;
+  l.grid = cta_count(p.rows, 1, std::min(LN_MAX_PARTS, sms));
+  l.smem = Ring<T>::bytes(l.threads);
+  l.kernel = ln_bwd_ring_kernel<T>;
+  return l;
+}
+
 template <typename T, Access A>
 BwdLaunch bwd_group_launch(LnBwdParams& p, int pieces, int sms) {
   const GroupShape g = group_shape(pieces, A == Access::VEC);
@@ -422,7 +607,9 @@ cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
     while (l.grid > 1 && l.grid * l.rows_per_cta % 8 != 0) --l.grid;
     if (l.grid * l.rows_per_cta % 8 != 0 && p.rows > l.rows_per_cta) return bwd<T, Access::SCALAR>(p, sms, s, launches);
   } else {
-    l = pieces > 32 && pieces <= 128 ? bwd_warp_launch<T, A>(p, pieces, sms) : bwd_group_launch<T, A>(p, pieces, sms);
+    if (pieces > 32 && pieces <= 128) l = bwd_warp_launch<T, A>(p, pieces, sms);
+    else if (A == Access::VEC && pieces > 128) l = bwd_ring_launch<T>(p, sms);
+    else l = bwd_group_launch<T, A>(p, pieces, sms);
   }
   if (l.grid == 1 || !(p.dw || p.db)) p.parts = nullptr;
   cudaError_t e;

@@ -275,6 +275,19 @@ __device__ __forceinline__ float warp_sums(float (&s)[N], int lane, int* which) 
   return s[0];
 }
 
+// Asynchronous copies of 16 bytes to shared memory by single threads, in groups that complete in order;
+// copies_wait<N> waits for all but the thread's last N groups.
+__device__ __forceinline__ void copy_16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The begin of a kernel launched with launch_after: its CTAs may be on their SMs before the kernel
 // ahead of it in the stream has ended, and wait here until that one's writes are visible; then the
 // next such kernel may do the same.  A launch costs 1 to 2 us less of the stream's time so.

@@ -251,6 +251,26 @@ def test_layer_norm_in_place_and_broadcast(nss, cols):
         same_bits(c, d, "broadcast dy")
 
 
+# rows enough for several turns of the backward pass's ring of rows, and too few for one; every number of groups per CTA
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(0, 2048), (1, 1032), (153, 8192), (3100, 8184), (2300, 4608), (7001, 2568), (9001, 1928),
+                                       (12001, 1040)])
+def test_layer_norm_long_rows(nss, dtype, rows, cols):
+    dtype = TYPES[dtype]
+    for wtype in {dtype, torch.float32}:
+        x, w, b, dy = norm_inputs(rows + cols, rows, cols, dtype, wtype)
+        _, mean, rstd = check_norm_forward(nss, x, w, b)
+        src, grad, dx = (Guarded((rows, cols), dtype, 8, pad) for pad in (0, 16, 8))
+        src.t.copy_(x)
+        grad.t.copy_(dy)
+        src.buf[~src.mark], grad.buf[~grad.mark] = float("nan"), float("inf")
+        got = check_norm_backward(nss, grad.t, src.t, mean, rstd, w, dx=dx.t)
+        dx.check("dx")
+        again = nss.mb_layer_norm_backward(dy, x, mean, rstd, w, dx=x)
+        for a, c, what in zip(again, got, ("dx", "dw", "db")):
+            same_bits(a, c, f"{what} over x, from another layout")
+
+
 def test_layer_norm_of_nothing(nss):
     w, b = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
     x = torch.empty((0, 64), device="cuda", dtype=torch.bfloat16)
