@@ -246,9 +246,10 @@ template <typename T>
 struct Ring {
   static constexpr int E = 16 / sizeof(T);             // elements of a chunk
   static constexpr int NC = 16 / E;                    // chunks per thread
-  static constexpr int STAGES = 12 / NC;               // rows: 192 KB with 512 threads
+  static constexpr int R = 4 / NC;                     // rows at a time
+  static constexpr int STAGES = 3;                     // times R rows: 192 KB with 512 threads
   static constexpr int MAX_THREADS = 512;
-  static size_t bytes(int threads) { return static_cast<size_t>(STAGES) * 2 * NC * threads * 16; }
+  static size_t bytes(int threads) { return static_cast<size_t>(STAGES) * R * 2 * NC * threads * 16; }
 };
 
 __device__ __forceinline__ void chunk_pairs(const uint4& c, float2 (&f)[2], float) {
@@ -274,28 +275,31 @@ __device__ __forceinline__ uint4 chunk_of(const float2 (&f)[4], T) {
 template <typename T>
 __global__ void __launch_bounds__(Ring<T>::MAX_THREADS, 1) ln_bwd_ring_kernel(const LnBwdParams p) {
   begin_after_previous();
-  constexpr int E = Ring<T>::E, NC = Ring<T>::NC, NP = E / 2, STAGES = Ring<T>::STAGES;
+  constexpr int E = Ring<T>::E, NC = Ring<T>::NC, NP = E / 2, STAGES = Ring<T>::STAGES, R = Ring<T>::R;
   constexpr int WARPS = Ring<T>::MAX_THREADS / 32;
-  extern __shared__ __align__(16) float dyn[];         // the ring [STAGES][x, dy][NC][threads]; at the end [32][threads] sums
-  __shared__ float2 part[2][WARPS];
+  extern __shared__ __align__(16) float dyn[];         // the ring [STAGES][R][x, dy][NC][threads]; at the end [32][threads] sums
+  __shared__ float2 part[2][WARPS][R];
   const int tpr = p.tpr, cols = p.cols, groups = p.groups, threads = blockDim.x;
   const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv_n = 1.f / static_cast<float>(cols);
   uint4* const mine = reinterpret_cast<uint4*>(dyn) + threadIdx.x;
-  auto place = [&](int stage, int k, int c) { return mine + ((stage * 2 + k) * NC + c) * threads; };
+  auto place = [&](int stage, int r, int k, int c) { return mine + (((stage * R + r) * 2 + k) * NC + c) * threads; };
   auto col = [&](int c) { return (c * tpr + t) * E; };
 
-  // the rows go round the CTAs first
-  const long long stride = static_cast<long long>(gridDim.x) * groups;
-  long long row = blockIdx.x + static_cast<long long>(gridDim.x) * g, ahead = row;
+  // R rows at a time; they go round the CTAs first
+  const long long stride = static_cast<long long>(gridDim.x) * groups * R;
+  long long row = (blockIdx.x + static_cast<long long>(gridDim.x) * g) * R, ahead = row;
   const T *x = static_cast<const T*>(p.x) + row * p.x_stride, *dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
   auto fetch = [&](int stage) {
-    if (ahead < p.rows) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (col(c) < cols) {
-          copy_16(place(stage, 0, c), x + col(c));
-          copy_16(place(stage, 1, c), dy + col(c));
+    for (int r = 0; r < R; ++r) {
+      if (ahead + r < p.rows) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          if (col(c) < cols) {
+            copy_16(place(stage, r, 0, c), x + r * p.x_stride + col(c));
+            copy_16(place(stage, r, 1, c), dy + r * p.dy_stride + col(c));
+          }
         }
       }
     }
@@ -307,13 +311,21 @@ __global__ void __launch_bounds__(Ring<T>::MAX_THREADS, 1) ln_bwd_ring_kernel(co
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     if (col(c) >= cols) {
-      for (int k = 0; k < STAGES * 2; ++k) place(k >> 1, k & 1, c)[0] = make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < STAGES * R * 2; ++k) *place(0, 0, k, c) = make_uint4(0, 0, 0, 0);
     }
   }
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) fetch(s);
-  float next_m = 0.f, next_rs = 0.f;
-  if (row < p.rows) next_m = p.mean[row], next_rs = p.rstd[row];
+  float next_m[R], next_rs[R];
+  auto fetch_stats = [&](long long row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool on = row0 + r < p.rows;
+      next_m[r] = on ? p.mean[row0 + r] : 0.f;
+      next_rs[r] = on ? p.rstd[row0 + r] : 0.f;
+    }
+  };
+  fetch_stats(row);
   float2 w[NC][NP], dw[NC][NP], db[NC][NP];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -326,63 +338,81 @@ __global__ void __launch_bounds__(Ring<T>::MAX_THREADS, 1) ln_bwd_ring_kernel(co
     }
   }
 
-  float m = 0.f, rs = 0.f;                             // of the row to be finished
-  int stage = 0, before = STAGES - 1, parity = 0;      // places of the present row and of the one before
+  float m[R], rs[R];                                   // of the rows to be finished
+  int stage = 0, before = STAGES - 1, parity = 0;      // places of the present rows and of the ones before
   T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
-  auto finish = [&](int from, int half) {
-    float2 sum = both(0.f);
-    for (int u = 0; u < tpr >> 5; ++u) sum = __fadd2_rn(sum, part[half][g * (tpr >> 5) + u]);
-    const float2 c1 = both(-sum.x * inv_n), c2 = both(-sum.y * inv_n), r = both(rs);
+  auto finish = [&](int from, int half, long long row0) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float2 h[NP], d[NP];
-      chunk_pairs(*place(from, 0, c), h, T());
-      chunk_pairs(*place(from, 1, c), d, T());
+    for (int r = 0; r < R; ++r) {
+      if (R > 1 && row0 + r >= p.rows) break;
+      float2 sum = both(0.f);
+      for (int u = 0; u < tpr >> 5; ++u) sum = __fadd2_rn(sum, part[half][g * (tpr >> 5) + u][r]);
+      const float2 c1 = both(-sum.x * inv_n), c2 = both(-sum.y * inv_n), scale = both(rs[r]);
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        h[j] = __fmul2_rn(__fadd2_rn(h[j], both(-m)), r);
-        h[j] = __fmul2_rn(__ffma2_rn(d[j], w[c][j], __ffma2_rn(h[j], c2, c1)), r);
+      for (int c = 0; c < NC; ++c) {
+        float2 h[NP], d[NP];
+        chunk_pairs(*place(from, r, 0, c), h, T());
+        chunk_pairs(*place(from, r, 1, c), d, T());
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          h[j] = __fmul2_rn(__fadd2_rn(h[j], both(-m[r])), scale);
+          h[j] = __fmul2_rn(__ffma2_rn(d[j], w[c][j], __ffma2_rn(h[j], c2, c1)), scale);
+        }
+        if (col(c) < cols) *reinterpret_cast<uint4*>(dx + r * p.dx_stride + col(c)) = chunk_of(h, T());
       }
-      if (col(c) < cols) *reinterpret_cast<uint4*>(dx + col(c)) = chunk_of(h, T());
     }
     dx += stride * p.dx_stride;
   };
   bool first = true;
   for (; row < p.rows; row += stride) {
     copies_wait<STAGES - 2>();
-    const float m_now = next_m, rs_now = next_rs;
-    if (row + stride < p.rows) next_m = p.mean[row + stride], next_rs = p.rstd[row + stride];
-    float2 s1 = both(0.f), s2 = both(0.f);
+    float m_now[R], rs_now[R], s[2 * R];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float2 h[NP], d[NP];
-      chunk_pairs(*place(stage, 0, c), h, T());
-      chunk_pairs(*place(stage, 1, c), d, T());
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {                   // past the row dy is 0, and h of no consequence
-        h[j] = __fmul2_rn(__fadd2_rn(h[j], both(-m_now)), both(rs_now));
-        const float2 gr = __fmul2_rn(d[j], w[c][j]);
-        s1 = __fadd2_rn(s1, gr);
-        s2 = __ffma2_rn(gr, h[j], s2);
-        dw[c][j] = __ffma2_rn(d[j], h[j], dw[c][j]);
-        db[c][j] = __fadd2_rn(db[c][j], d[j]);
-      }
+    for (int r = 0; r < R; ++r) {
+      m_now[r] = next_m[r];
+      rs_now[r] = next_rs[r];
     }
-    float s[2] = {s1.x + s1.y, s2.x + s2.y};
+    fetch_stats(row + stride);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 s1 = both(0.f), s2 = both(0.f);
+      if (R == 1 || row + r < p.rows) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float2 h[NP], d[NP];
+          chunk_pairs(*place(stage, r, 0, c), h, T());
+          chunk_pairs(*place(stage, r, 1, c), d, T());
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {               // past the row dy is 0, and h of no consequence
+            h[j] = __fmul2_rn(__fadd2_rn(h[j], both(-m_now[r])), both(rs_now[r]));
+            const float2 gr = __fmul2_rn(d[j], w[c][j]);
+            s1 = __fadd2_rn(s1, gr);
+            s2 = __ffma2_rn(gr, h[j], s2);
+            dw[c][j] = __ffma2_rn(d[j], h[j], dw[c][j]);
+            db[c][j] = __fadd2_rn(db[c][j], d[j]);
+          }
+        }
+      }
+      s[2 * r] = s1.x + s1.y;
+      s[2 * r + 1] = s2.x + s2.y;
+    }
     int which;
-    const float sum = warp_sums<2>(s, lane, &which);
-    if ((lane & 15) == 0) (which ? part[parity][warp].y : part[parity][warp].x) = sum;
-    if (!first) finish(before, parity ^ 1);
+    const float sum = warp_sums<2 * R>(s, lane, &which);
+    if ((lane & (16 / R - 1)) == 0) reinterpret_cast<float*>(part[parity][warp])[which] = sum;
+    if (!first) finish(before, parity ^ 1, row - stride);
     first = false;
-    fetch(before);                                     // its row has been finished
-    m = m_now;
-    rs = rs_now;
+    fetch(before);                                     // its rows have been finished
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = m_now[r];
+      rs[r] = rs_now[r];
+    }
     before = stage;
     stage = stage + 1 < STAGES ? stage + 1 : 0;
     parity ^= 1;
     group_barrier(1 + g, tpr);
   }
-  if (!first) finish(before, parity ^ 1);
+  if (!first) finish(before, parity ^ 1, row - stride);
   if (!p.dw && !p.db) return;
   copies_wait<0>();
   __syncthreads();
@@ -574,7 +604,7 @@ BwdLaunch bwd_ring_launch(LnBwdParams& p, int sms) {
   BwdLaunch l{};
   l.threads = p.groups * p.tpr;
   l.rows_per_cta = p.groups;
-  l.grid = cta_count(p.rows, 1, std::min(LN_MAX_PARTS, sms));
+  l.grid = cta_count(p.rows, Ring<T>::R, std::min(LN_MAX_PARTS, sms));
   l.smem = Ring<T>::bytes(l.threads);
   l.kernel = ln_bwd_ring_kernel<T>;
   return l;
