@@ -29,7 +29,7 @@ __device__ __forceinline__ void put_param_grad(void* out, bool, int c, float v, 
 // shared memory at the end, the CTAs through `parts` (fixed orders throughout: results repeat bit
 // for bit).  SHIFT: a group's rows are a multiple of 16 bytes apart, so that it keeps its columns.
 template <typename T, Access A, int R, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT <= 288 ? 2 : 1) ln_bwd_kernel(const LnBwdParams p) {
   begin_after_previous();
   extern __shared__ float dyn[];                       // [16][threads] at the end
   __shared__ float part[2][MAXT / 32][2 * R];
@@ -137,18 +137,27 @@ __global__ void __launch_bounds__(MAXT, MAXT == 288 ? 2 : 1) ln_bwd_kernel(const
   }
 }
 
-// Threads of a CTA (one per SM) of the kernel below, by what the registers of NV pieces allow.
-template <int NV>
-constexpr int BWD_THREADS = NV == 2 ? 512 : NV == 3 ? 384 : 256;
+// Threads of a CTA (one per SM) of the kernel below, by what the registers of NV pieces allow: more of
+// them spill (2^26 fp32 elements in rows of 768: 126 us, with 384 threads 143; of 512 122 and, with 512
+// threads, 137; 2^27 bf16 elements in unaligned rows of 511 162 and 205, of 761 170 and 263).
+template <typename T, Access A, int NV>
+constexpr int BWD_THREADS = NV == 2 ? (sizeof(T) == 2 && A == Access::VEC ? 512 : 384)
+                          : NV == 3 && sizeof(T) == 2 && A == Access::VEC ? 384 : 256;
+
+// Most pieces of a row in this kernel: 16-bit aligned rows of more than 768 elements are faster through
+// the ring below (2^27 bf16 elements in rows of 1024 131 us and not 143), fp32 ones not (2^26 in rows of
+// 1024 131 and 122).
+template <typename T, Access A>
+constexpr int WARP_PIECES = A == Access::VEC && sizeof(T) == 2 ? 96 : 128;
 
 // Rows of 257 to 1024 elements: a warp holds a row in NV pieces per lane and sums over it by
 // exchanges alone; the next row is already being loaded.  Sums of the gradient as above.
 template <typename T, Access A, int NV>
-__global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const LnBwdParams p) {
+__global__ void __launch_bounds__(BWD_THREADS<T, A, NV>, 1) ln_bwd_warp_kernel(const LnBwdParams p) {
   begin_after_previous();
   extern __shared__ __align__(16) float dyn[];         // the weight; at the end [warps][NV][16][32] sums
   using P = Piece<T, A>;
-  constexpr int WARPS = BWD_THREADS<NV> / 32;
+  constexpr int WARPS = BWD_THREADS<T, A, NV> / 32;
   static_assert(A != Access::SHIFT, "single elements are as fast here");
   const int cols = p.cols, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float inv_n = 1.f / static_cast<float>(cols);
@@ -238,17 +247,19 @@ __global__ void __launch_bounds__(BWD_THREADS<NV>, 1) ln_bwd_warp_kernel(const L
   }
 }
 
-// Aligned rows of 1025 to 8192 elements: a group of up to 512 threads holds a row, 16 elements per
+// Longer aligned rows, up to 8192 elements: a group of up to 512 threads holds a row, 16 elements per
 // thread in 16-byte chunks.  Every thread copies its own chunks of the next rows into its own places
 // of a ring in shared memory (so nothing but its own wait orders them), and a row is finished while
-// the next one's sums are under way: one barrier per row, behind a row's worth of other work.
-template <typename T>
+// the next one's sums are under way: one barrier per row, behind a row's worth of other work.  2^27
+// bf16 elements in rows of 2048 take 128 us (6.3 TB/s; with the next row in registers 174), of 8192 148
+// (230); fp32 255 and 281 (343 and 414).
+template <typename T, int EL>                          // EL: elements of a row per thread
 struct Ring {
   static constexpr int E = 16 / sizeof(T);             // elements of a chunk
-  static constexpr int NC = 16 / E;                    // chunks per thread
-  static constexpr int R = 4 / NC;                     // rows at a time
-  static constexpr int STAGES = 3;                     // times R rows: 192 KB with 512 threads
-  static constexpr int MAX_THREADS = 512;
+  static constexpr int NC = EL / E;                    // chunks per thread
+  static constexpr int R = NC == 2 ? 2 : 1;            // rows at a time
+  static constexpr int STAGES = 3;       // times R rows: 192 to 210 KB
+  static constexpr int MAX_THREADS = EL == 16 ? 512 : 448;
   static size_t bytes(int threads) { return static_cast<size_t>(STAGES) * R * 2 * NC * threads * 16; }
 };
 
@@ -272,12 +283,13 @@ __device__ __forceinline__ uint4 chunk_of(const float2 (&f)[4], T) {
                     pack2(f[3].x, f[3].y, T()));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(Ring<T>::MAX_THREADS, 1) ln_bwd_ring_kernel(const LnBwdParams p) {
+template <typename T, int EL>
+__global__ void __launch_bounds__(Ring<T, EL>::MAX_THREADS, 1) ln_bwd_ring_kernel(const LnBwdParams p) {
   begin_after_previous();
-  constexpr int E = Ring<T>::E, NC = Ring<T>::NC, NP = E / 2, STAGES = Ring<T>::STAGES, R = Ring<T>::R;
-  constexpr int WARPS = Ring<T>::MAX_THREADS / 32;
-  extern __shared__ __align__(16) float dyn[];         // the ring [STAGES][R][x, dy][NC][threads]; at the end [32][threads] sums
+  using Shape = Ring<T, EL>;
+  constexpr int E = Shape::E, NC = Shape::NC, NP = E / 2, STAGES = Shape::STAGES, R = Shape::R;
+  constexpr int WARPS = Shape::MAX_THREADS / 32;
+  extern __shared__ __align__(16) float dyn[];         // the ring [STAGES][R][x, dy][NC][threads]; at the end [2 EL][threads] sums
   __shared__ float2 part[2][WARPS][R];
   const int tpr = p.tpr, cols = p.cols, groups = p.groups, threads = blockDim.x;
   const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -421,13 +433,13 @@ __global__ void __launch_bounds__(Ring<T>::MAX_THREADS, 1) ln_bwd_ring_kernel(co
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       dyn[(c * E + j) * threads + threadIdx.x] = j & 1 ? dw[c][j / 2].y : dw[c][j / 2].x;
-      dyn[(16 + c * E + j) * threads + threadIdx.x] = j & 1 ? db[c][j / 2].y : db[c][j / 2].x;
+      dyn[(EL + c * E + j) * threads + threadIdx.x] = j & 1 ? db[c][j / 2].y : db[c][j / 2].x;
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 32 * tpr; e += threads) {
-    const int i = e / tpr, tt = e - i * tpr, k = i >> 4;           // k: of dw or db
-    const int c = ((i & 15) / E * tpr + tt) * E + (i & 15) % E;
+  for (int e = threadIdx.x; e < 2 * EL * tpr; e += threads) {
+    const int i = e / tpr, tt = e - i * tpr, k = i >= EL, n = i - k * EL;   // k: of dw or db
+    const int c = (n / E * tpr + tt) * E + n % E;
     if (c >= cols) continue;
     float sum = 0.f;
     for (int u = 0; u < groups; ++u) sum += dyn[i * threads + u * tpr + tt];
@@ -538,22 +550,21 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_params_kernel(const LnBwdPara
 
 constexpr int BWD_MAX_COLS = 8192;   // wider rows are read again from memory
 
-// How groups of threads share rows of up to 8192 elements: 576 threads per SM at 96 registers in
-// two or three CTAs up to rows of 2304 elements, then one CTA of 128 or 64 registers.
+// How groups of threads share rows: up to 256 elements, and unaligned ones of more than 1024.  256
+// threads in two CTAs of 128 registers; longer rows 576 threads per SM at 96 registers in two or
+// three CTAs up to 2304 elements, then one CTA of 128 or 64 registers.
 struct GroupShape {
   int tpr, groups;      // threads per row, rows side by side in a CTA
   int most;             // the kernel's MAXT
-  int rows;             // rows at a time of a group
   int ctas;             // per SM
 };
-GroupShape group_shape(int pieces, bool vec) {
-  GroupShape g{};
-  g.tpr = pieces <= 32 ? pow2_at_least(pieces) : (pieces + 31) / 32 * 32;
-  g.most = g.tpr <= 288 ? 288 : g.tpr <= 512 ? 512 : 1024;
-  g.groups = g.tpr < 32 ? 256 / g.tpr : g.most / g.tpr;
-  g.rows = vec && g.most <= 512 ? 2 : 1;
-  g.ctas = g.most == 288 ? std::min(3, 576 / (g.groups * g.tpr)) : 1;
-  return g;
+GroupShape group_shape(int pieces) {
+  if (pieces <= 32) {
+    const int tpr = pow2_at_least(pieces);
+    return {tpr, 256 / tpr, 256, 2};
+  }
+  const int tpr = (pieces + 31) / 32 * 32, most = tpr <= 288 ? 288 : tpr <= 512 ? 512 : 1024;
+  return {tpr, most / tpr, most, most == 288 ? std::min(3, 576 / (most / tpr * tpr)) : 1};
 }
 template <typename T>
 cudaError_t add_parts(const LnBwdParams& p, int n, cudaStream_t s) {
@@ -588,41 +599,65 @@ BwdLaunch bwd_warp_launch(const LnBwdParams& p, int pieces, int sms) {
   const bool params = p.dw || p.db;
   const int nv = (pieces + 31) / 32;
   BwdLaunch l{};
-  l.threads = nv == 2 ? BWD_THREADS<2> : nv == 3 ? BWD_THREADS<3> : BWD_THREADS<4>;
+  l.threads = nv == 2 ? BWD_THREADS<T, A, 2> : nv == 3 ? BWD_THREADS<T, A, 3> : BWD_THREADS<T, A, 4>;
   l.rows_per_cta = l.threads / 32;
   l.grid = cta_count(p.rows, l.rows_per_cta, std::min(LN_MAX_PARTS, sms));
   const int staged = nv == 2 ? Staged<A, 2>::floats(32) : nv == 3 ? Staged<A, 3>::floats(32) : Staged<A, 4>::floats(32);
   l.smem = static_cast<size_t>(params ? std::max(staged, 16 * nv * l.threads) : staged) * sizeof(float);
-  l.kernel = nv == 2 ? ln_bwd_warp_kernel<T, A, 2> : nv == 3 ? ln_bwd_warp_kernel<T, A, 3> : ln_bwd_warp_kernel<T, A, 4>;
+  l.kernel = nv == 2 ? ln_bwd_warp_kernel<T, A, 2> : ln_bwd_warp_kernel<T, A, 3>;
+  if constexpr (WARP_PIECES<T, A> > 96) {
+    if (nv == 4) l.kernel = ln_bwd_warp_kernel<T, A, 4>;
+  }
   return l;
 }
 
-template <typename T>
+template <typename T, int EL>
 BwdLaunch bwd_ring_launch(LnBwdParams& p, int sms) {
-  p.tpr = (p.cols + 16 * 32 - 1) / (16 * 32) * 32;
-  p.groups = Ring<T>::MAX_THREADS / p.tpr;
+  using Shape = Ring<T, EL>;
+  p.tpr = (p.cols + EL * 32 - 1) / (EL * 32) * 32;
+  p.groups = Shape::MAX_THREADS / p.tpr;
   BwdLaunch l{};
   l.threads = p.groups * p.tpr;
-  l.rows_per_cta = p.groups;
-  l.grid = cta_count(p.rows, Ring<T>::R, std::min(LN_MAX_PARTS, sms));
-  l.smem = Ring<T>::bytes(l.threads);
-  l.kernel = ln_bwd_ring_kernel<T>;
+  l.rows_per_cta = p.groups * Shape::R;
+  l.grid = cta_count(p.rows, Shape::R, std::min(LN_MAX_PARTS, sms));
+  l.smem = Shape::bytes(l.threads);
+  l.kernel = ln_bwd_ring_kernel<T, EL>;
+  return l;
+}
+template <typename T>
+BwdLaunch bwd_ring_launch(LnBwdParams& p, int sms) {
+  // with 24 elements per thread where that makes two groups of one, whose rows then overlap (2^27 bf16
+  // elements in rows of 4608: 161 us and not 192); where 16 make two or more they are faster (of 3000:
+  // 164 and 169, of 1536 127 and 148); fp32 rows have enough in flight
+  const BwdLaunch l = bwd_ring_launch<T, 16>(p, sms);
+  if constexpr (sizeof(T) == 2) {
+    LnBwdParams q = p;
+    const BwdLaunch more = bwd_ring_launch<T, 24>(q, sms);
+    if (p.groups == 1 && q.groups > 1) {
+      p = q;
+      return more;
+    }
+  }
   return l;
 }
 
 template <typename T, Access A>
 BwdLaunch bwd_group_launch(LnBwdParams& p, int pieces, int sms) {
-  const GroupShape g = group_shape(pieces, A == Access::VEC);
+  const GroupShape g = group_shape(pieces);
   p.tpr = g.tpr;
   p.groups = g.groups;
   constexpr int R = A == Access::VEC ? 2 : 1;
   BwdLaunch l{};
   l.threads = g.groups * g.tpr;
-  l.rows_per_cta = g.groups * g.rows;
+  l.rows_per_cta = g.groups * R;
   l.grid = cta_count(p.rows, l.rows_per_cta, std::min(LN_MAX_PARTS, g.ctas * sms));
   l.smem = p.dw || p.db ? static_cast<size_t>(l.threads) * 16 * sizeof(float) : 0;
-  l.kernel = g.most == 288   ? ln_bwd_kernel<T, A, R, 288>
-             : g.most == 512 ? ln_bwd_kernel<T, A, R, 512> : ln_bwd_kernel<T, A, 1, 1024>;
+  l.kernel = ln_bwd_kernel<T, A, R, 256>;
+  if constexpr (A != Access::VEC) {
+    if (g.most == 288) l.kernel = ln_bwd_kernel<T, A, 1, 288>;
+    if (g.most == 512) l.kernel = ln_bwd_kernel<T, A, 1, 512>;
+    if (g.most == 1024) l.kernel = ln_bwd_kernel<T, A, 1, 1024>;
+  }
   return l;
 }
 
@@ -637,8 +672,8 @@ cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
     while (l.grid > 1 && l.grid * l.rows_per_cta % 8 != 0) --l.grid;
     if (l.grid * l.rows_per_cta % 8 != 0 && p.rows > l.rows_per_cta) return bwd<T, Access::SCALAR>(p, sms, s, launches);
   } else {
-    if (pieces > 32 && pieces <= 128) l = bwd_warp_launch<T, A>(p, pieces, sms);
-    else if (A == Access::VEC && pieces > 128) l = bwd_ring_launch<T>(p, sms);
+    if (pieces > 32 && pieces <= WARP_PIECES<T, A>) l = bwd_warp_launch<T, A>(p, pieces, sms);
+    else if (A == Access::VEC && pieces > 32) l = bwd_ring_launch<T>(p, sms);
     else l = bwd_group_launch<T, A>(p, pieces, sms);
   }
   if (l.grid == 1 || !(p.dw || p.db)) p.parts = nullptr;
