@@ -142,6 +142,160 @@ __global__ void __launch_bounds__(256, FWD_CTAS<T, A, NV>) ln_fwd_kernel(const L
   }
 }
 
+// Aligned rows through a ring in shared memory: a group of up to 512 threads holds a row, 16 elements
+// per thread in 16-byte chunks, R rows at a time.  Every thread copies its own chunks of the next rows
+// into its own places (so nothing but its own wait orders them).  While the sum of one set of rows is
+// formed, the squares of the set before are, with the mean known, and the set before that is finished:
+// one barrier per set, behind other work.  (Eight elements per thread, of 1024 threads, were slower:
+// 2^27 bf16 elements in rows of 8192 136 us and not 107.)
+template <typename T>
+struct FwdRing {
+  static constexpr int E = 16 / sizeof(T);             // elements of a chunk
+  static constexpr int NC = 16 / E;                    // chunks per thread
+  static constexpr int R = 4 / NC;                     // rows at a time
+  static constexpr int STAGES = 5;                     // times R rows: 160 KB with 512 threads
+  static constexpr int MAX_THREADS = 512;
+  static size_t bytes(int threads) { return static_cast<size_t>(STAGES) * R * NC * threads * 16; }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(FwdRing<T>::MAX_THREADS, 1) ln_fwd_ring_kernel(const LnFwdParams p) {
+  begin_after_previous();
+  using Shape = FwdRing<T>;
+  constexpr int E = Shape::E, NC = Shape::NC, NP = E / 2, STAGES = Shape::STAGES, R = Shape::R;
+  extern __shared__ __align__(16) uint4 ring[];        // [STAGES][R][NC][threads]
+  __shared__ float part[2][Shape::MAX_THREADS / 32][2 * R];        // sums of R rows, sums of squares of R
+  const int tpr = p.tpr, cols = p.cols, threads = blockDim.x, groups = threads / tpr;
+  const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float inv_n = 1.f / static_cast<float>(cols);
+  uint4* const mine = ring + threadIdx.x;
+  auto place = [&](int stage, int r, int c) { return mine + ((stage * R + r) * NC + c) * threads; };
+  auto col = [&](int c) { return (c * tpr + t) * E; };
+
+  // sets of R rows, which go round the CTAs first
+  const long long stride = static_cast<long long>(gridDim.x) * groups * R;
+  const long long row0 = (blockIdx.x + static_cast<long long>(gridDim.x) * g) * R;
+  const int sets = row0 < p.rows ? static_cast<int>((p.rows - row0 + stride - 1) / stride) : 0;
+  long long ahead = row0;
+  const T* x = static_cast<const T*>(p.x) + row0 * p.x_stride;
+  auto fetch = [&](int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (ahead + r < p.rows) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (col(c) < cols) copy_16(place(stage, r, c), x + r * p.x_stride + col(c));
+      }
+    }
+    copies_end_group();
+    ahead += stride;
+    x += stride * p.x_stride;
+  };
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (col(c) >= cols) {
+      for (int k = 0; k < STAGES * R; ++k) *place(0, k, c) = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < STAGES - 2; ++s) fetch(s);
+  float2 w[NC][NP], b[NC][NP];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const bool in = col(c) < cols;
+      w[c][j].x = in ? param<T>(p.w, p.w_f32, 1.f, col(c) + 2 * j) : 0.f;
+      w[c][j].y = in ? param<T>(p.w, p.w_f32, 1.f, col(c) + 2 * j + 1) : 0.f;
+      b[c][j].x = in ? param<T>(p.b, p.w_f32, 0.f, col(c) + 2 * j) : 0.f;
+      b[c][j].y = in ? param<T>(p.b, p.w_f32, 0.f, col(c) + 2 * j + 1) : 0.f;
+    }
+  }
+
+  float m1[R], m2[R];                                  // means of the sets one and two before
+#pragma unroll
+  for (int r = 0; r < R; ++r) m1[r] = m2[r] = 0.f;
+  int at0 = 0, at1 = STAGES - 1, at2 = STAGES - 2;     // places of the present set and of those before
+  long long row = row0 - 2 * stride;                   // of the set to be finished
+  T* y = static_cast<T*>(p.y) + row * p.y_stride;
+  for (int k = 0; k < sets + 2; ++k) {
+    const int parity = k & 1;
+    float sums[2 * R], s[2 * R];
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) sums[i] = s[i] = 0.f;
+    if (k > 0) {
+      const bool on = lane < tpr >> 5;
+#pragma unroll
+      for (int i = 0; i < 2 * R; ++i) s[i] = on ? part[parity ^ 1][g * (tpr >> 5) + lane][i] : 0.f;
+      int which;
+      const float sum = warp_sums<2 * R>(s, lane, &which);
+#pragma unroll
+      for (int i = 0; i < 2 * R; ++i) sums[i] = __shfl_sync(0xFFFFFFFFu, sum, i * (16 / R));
+    }
+    copies_wait<STAGES - 3>();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m2[r] = m1[r];
+      m1[r] = sums[r] * inv_n;
+      float2 a = both(0.f), q = both(0.f);
+      if (k < sets && row + 2 * stride + r < p.rows) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {                 // past the row there are zeros
+          float2 f[NP];
+          chunk_pairs(*place(at0, r, c), f, T());
+#pragma unroll
+          for (int j = 0; j < NP; ++j) a = __fadd2_rn(a, f[j]);
+        }
+      }
+      if (k > 0 && k <= sets && row + stride + r < p.rows) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          if (col(c) < cols) {
+            float2 f[NP];
+            chunk_pairs(*place(at1, r, c), f, T());
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              f[j] = __fadd2_rn(f[j], both(-m1[r]));
+              q = __ffma2_rn(f[j], f[j], q);
+            }
+          }
+        }
+      }
+      s[r] = a.x + a.y;
+      s[R + r] = q.x + q.y;
+    }
+    int which;
+    const float sum = warp_sums<2 * R>(s, lane, &which);
+    if ((lane & (16 / R - 1)) == 0) part[parity][warp][which] = sum;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (k > 1 && row + r < p.rows) {
+        const float rs = rsqrtf(fmaf(sums[R + r], inv_n, p.eps));
+        if (t == 0) {
+          if (p.mean) p.mean[row + r] = m2[r];
+          if (p.rstd) p.rstd[row + r] = rs;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float2 f[NP];
+          chunk_pairs(*place(at2, r, c), f, T());
+#pragma unroll
+          for (int j = 0; j < NP; ++j)
+            f[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[j], both(-m2[r])), both(rs)), w[c][j], b[c][j]);
+          if (col(c) < cols) *reinterpret_cast<uint4*>(y + r * p.y_stride + col(c)) = chunk_of(f, T());
+        }
+      }
+    }
+    row += stride;
+    y += stride * p.y_stride;
+    fetch(at2);                                        // its set has been finished
+    at2 = at1;
+    at1 = at0;
+    at0 = at0 + 1 < STAGES ? at0 + 1 : 0;
+    group_barrier(1 + g, tpr);
+  }
+}
+
 // Rows of up to 32768 elements (16384 by single elements): one CTA per row, which its threads hold
 // in NV pieces each; several CTAs per SM keep loads in flight while others wait at their sums.
 template <typename T, Access A, int NV, int MAXT>
@@ -227,11 +381,30 @@ cudaError_t fwd_warp(LnFwdParams p, int sms, cudaStream_t s) {
   return launch_after(ln_fwd_kernel<T, A, NV, R>, dim3(grid), dim3(256), smem, s, p);
 }
 
+template <typename T>
+cudaError_t fwd_ring(LnFwdParams p, int sms, cudaStream_t s) {
+  using Shape = FwdRing<T>;
+  p.tpr = (p.cols + 16 * 32 - 1) / (16 * 32) * 32;
+  const int threads = Shape::MAX_THREADS / p.tpr * p.tpr;
+  const size_t smem = Shape::bytes(threads);
+  const cudaError_t e =
+      cudaFuncSetAttribute(ln_fwd_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_after(ln_fwd_ring_kernel<T>, dim3(cta_count(p.rows, Shape::R, sms)), dim3(threads), smem, s, p);
+}
+
 template <typename T, Access A>
 cudaError_t fwd(LnFwdParams p, int sms, cudaStream_t s) {
   constexpr bool SCALAR = A == Access::SCALAR, SHIFT = A == Access::SHIFT;
   const int pieces = (p.cols + (SHIFT ? 14 : 7)) / 8;
   p.tpr = pieces >= 32 ? 32 : pow2_at_least(pieces);
+  if constexpr (A == Access::VEC) {
+    // 9728 bf16 rows of 8192 elements take 60 us so and 84 by a CTA per row (fp32 104 and 119), of 4096 33
+    // and, by a warp per row, 36 (fp32 rows up to 4096 are as fast so); but 608 rows of 8192 8.6 and 6.0,
+    // and 1216 of 4096 8.6 and 6.8: a ring pays from about 2^16 elements per SM
+    if (pieces > (sizeof(T) == 2 ? 256 : 512) && pieces <= 1024 && p.rows * p.cols >= 65536ll * sms)
+      return fwd_ring<T>(p, sms, s);
+  }
   if constexpr (!SHIFT) {
     if (pieces <= 32) return fwd_warp<T, A, 1, SCALAR ? 2 : 4>(p, sms, s);
     if (pieces <= 64) return fwd_warp<T, A, 2, SCALAR ? 1 : 2>(p, sms, s);

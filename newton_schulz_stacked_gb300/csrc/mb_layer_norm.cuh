@@ -104,6 +104,27 @@ struct Staged {
   }
 };
 
+// A chunk of 16 bytes as pairs, and back.
+__device__ __forceinline__ void chunk_pairs(const uint4& c, float2 (&f)[2], float) {
+  f[0] = make_float2(__uint_as_float(c.x), __uint_as_float(c.y));
+  f[1] = make_float2(__uint_as_float(c.z), __uint_as_float(c.w));
+}
+template <typename T>
+__device__ __forceinline__ void chunk_pairs(const uint4& c, float2 (&f)[4], T) {
+  f[0] = unpack2(c.x, T());
+  f[1] = unpack2(c.y, T());
+  f[2] = unpack2(c.z, T());
+  f[3] = unpack2(c.w, T());
+}
+__device__ __forceinline__ uint4 chunk_of(const float2 (&f)[2], float) {
+  return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+}
+template <typename T>
+__device__ __forceinline__ uint4 chunk_of(const float2 (&f)[4], T) {
+  return make_uint4(pack2(f[0].x, f[0].y, T()), pack2(f[1].x, f[1].y, T()), pack2(f[2].x, f[2].y, T()),
+                    pack2(f[3].x, f[3].y, T()));
+}
+
 // ---------------------------------------------------------------- host side
 
 inline bool aligned_rows(const void* p, long long stride, int size, long long rows) {

@@ -251,10 +251,10 @@ def test_layer_norm_in_place_and_broadcast(nss, cols):
         same_bits(c, d, "broadcast dy")
 
 
-# rows enough for several turns of the backward pass's ring of rows, and too few for one; every number of groups per CTA
+# rows enough for several turns of the ring of rows of either pass, and too few for one; every number of groups per CTA
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,cols", [(0, 2048), (1, 1032), (153, 8192), (3100, 8184), (2300, 4608), (7001, 2568), (9001, 1928),
-                                       (12001, 1040)])
+                                       (12001, 1040), (5003, 4096), (1700, 8192)])
 def test_layer_norm_long_rows(nss, dtype, rows, cols):
     dtype = TYPES[dtype]
     for wtype in {dtype, torch.float32}:
@@ -264,8 +264,13 @@ def test_layer_norm_long_rows(nss, dtype, rows, cols):
         src.t.copy_(x)
         grad.t.copy_(dy)
         src.buf[~src.mark], grad.buf[~grad.mark] = float("nan"), float("inf")
+        check_norm_forward(nss, src.t, w, b, y=dx.t)
+        dx.check("y")
         got = check_norm_backward(nss, grad.t, src.t, mean, rstd, w, dx=dx.t)
         dx.check("dx")
+        y, inplace = nss.mb_layer_norm(x, w, b)[0], x.clone()
+        nss.mb_layer_norm(inplace, w, b, y=inplace)
+        same_bits(inplace, y, "y over x")
         again = nss.mb_layer_norm_backward(dy, x, mean, rstd, w, dx=x)
         for a, c, what in zip(again, got, ("dx", "dw", "db")):
             same_bits(a, c, f"{what} over x, from another layout")
