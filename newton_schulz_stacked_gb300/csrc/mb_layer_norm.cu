@@ -224,13 +224,7 @@ __global__ void __launch_bounds__(FwdRing<T>::MAX_THREADS, 1) ln_fwd_ring_kernel
 #pragma unroll
     for (int i = 0; i < 2 * R; ++i) sums[i] = s[i] = 0.f;
     if (k > 0) {
-      const bool on = lane < tpr >> 5;
-#pragma unroll
-      for (int i = 0; i < 2 * R; ++i) s[i] = on ? part[parity ^ 1][g * (tpr >> 5) + lane][i] : 0.f;
-      int which;
-      const float sum = warp_sums<2 * R>(s, lane, &which);
-#pragma unroll
-      for (int i = 0; i < 2 * R; ++i) sums[i] = __shfl_sync(0xFFFFFFFFu, sum, i * (16 / R));
+      sums_of_warps<2 * R>(part[parity ^ 1] + g * (tpr >> 5), tpr >> 5, lane, sums);
     }
     copies_wait<STAGES - 3>();
 #pragma unroll

@@ -251,26 +251,27 @@ __global__ void __launch_bounds__(BWD_THREADS<T, A, NV>, 1) ln_bwd_warp_kernel(c
 // thread in 16-byte chunks.  Every thread copies its own chunks of the next rows into its own places
 // of a ring in shared memory (so nothing but its own wait orders them), and a row is finished while
 // the next one's sums are under way: one barrier per row, behind a row's worth of other work.  2^27
-// bf16 elements in rows of 2048 take 128 us (6.3 TB/s; with the next row in registers 174), of 8192 148
-// (230); fp32 255 and 281 (343 and 414).
-template <typename T, int EL>                          // EL: elements of a row per thread
+// bf16 elements in rows of 1536 to 4096 take 125 to 151 us, of 8192 135 (6.0 TB/s; with the next row in
+// registers 167 to 179, and 230); fp32 245 to 277 (of 8192 414).  Rows of 4097 to 5376 leave a third to
+// half of the threads out and take 163 to 174: 24 elements per thread, so that two fit, spill (185).
+template <typename T>
 struct Ring {
   static constexpr int E = 16 / sizeof(T);             // elements of a chunk
-  static constexpr int NC = EL / E;                    // chunks per thread
-  static constexpr int R = NC == 2 ? 2 : 1;            // rows at a time
-  static constexpr int STAGES = 3;       // times R rows: 192 to 210 KB
-  static constexpr int MAX_THREADS = EL == 16 ? 512 : 448;
+  static constexpr int NC = 16 / E;                    // chunks per thread
+  static constexpr int R = 4 / NC;                     // rows at a time
+  static constexpr int STAGES = 3;                     // times R rows: 192 KB with 512 threads
+  static constexpr int MAX_THREADS = 512;
   static size_t bytes(int threads) { return static_cast<size_t>(STAGES) * R * 2 * NC * threads * 16; }
 };
 
-template <typename T, int EL>
-__global__ void __launch_bounds__(Ring<T, EL>::MAX_THREADS, 1) ln_bwd_ring_kernel(const LnBwdParams p) {
+template <typename T>
+__global__ void __launch_bounds__(Ring<T>::MAX_THREADS, 1) ln_bwd_ring_kernel(const LnBwdParams p) {
   begin_after_previous();
-  using Shape = Ring<T, EL>;
+  using Shape = Ring<T>;
   constexpr int E = Shape::E, NC = Shape::NC, NP = E / 2, STAGES = Shape::STAGES, R = Shape::R;
   constexpr int WARPS = Shape::MAX_THREADS / 32;
-  extern __shared__ __align__(16) float dyn[];         // the ring [STAGES][R][x, dy][NC][threads]; at the end [2 EL][threads] sums
-  __shared__ float2 part[2][WARPS][R];
+  extern __shared__ __align__(16) float dyn[];         // the ring [STAGES][R][x, dy][NC][threads]; at the end [32][threads] sums
+  __shared__ float part[2][WARPS][2 * R];              // of every row: sum g, sum g h
   const int tpr = p.tpr, cols = p.cols, groups = p.groups, threads = blockDim.x;
   const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv_n = 1.f / static_cast<float>(cols);
@@ -334,12 +335,12 @@ __global__ void __launch_bounds__(Ring<T, EL>::MAX_THREADS, 1) ln_bwd_ring_kerne
   int stage = 0, before = STAGES - 1, parity = 0;      // places of the present rows and of the ones before
   T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
   auto finish = [&](int from, int half, long long row0) {
+    float sums[2 * R];
+    sums_of_warps<2 * R>(part[half] + g * (tpr >> 5), tpr >> 5, lane, sums);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (R > 1 && row0 + r >= p.rows) break;
-      float2 sum = both(0.f);
-      for (int u = 0; u < tpr >> 5; ++u) sum = __fadd2_rn(sum, part[half][g * (tpr >> 5) + u][r]);
-      const float2 c1 = both(-sum.x * inv_n), c2 = both(-sum.y * inv_n), scale = both(rs[r]);
+      const float2 c1 = both(-sums[2 * r] * inv_n), c2 = both(-sums[2 * r + 1] * inv_n), scale = both(rs[r]);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float2 h[NP], d[NP];
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(Ring<T, EL>::MAX_THREADS, 1) ln_bwd_ring_kerne
     }
     int which;
     const float sum = warp_sums<2 * R>(s, lane, &which);
-    if ((lane & (16 / R - 1)) == 0) reinterpret_cast<float*>(part[parity][warp])[which] = sum;
+    if ((lane & (16 / R - 1)) == 0) part[parity][warp][which] = sum;
     if (!first) finish(before, parity ^ 1, row - stride);
     first = false;
     fetch(before);                                     // its rows have been finished
@@ -413,12 +414,12 @@ __global__ void __launch_bounds__(Ring<T, EL>::MAX_THREADS, 1) ln_bwd_ring_kerne
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       dyn[(c * E + j) * threads + threadIdx.x] = j & 1 ? dw[c][j / 2].y : dw[c][j / 2].x;
-      dyn[(EL + c * E + j) * threads + threadIdx.x] = j & 1 ? db[c][j / 2].y : db[c][j / 2].x;
+      dyn[(16 + c * E + j) * threads + threadIdx.x] = j & 1 ? db[c][j / 2].y : db[c][j / 2].x;
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * EL * tpr; e += threads) {
-    const int i = e / tpr, tt = e - i * tpr, k = i >= EL, n = i - k * EL;   // k: of dw or db
+  for (int e = threadIdx.x; e < 32 * tpr; e += threads) {
+    const int i = e / tpr, tt = e - i * tpr, k = i >> 4, n = i & 15;   // k: of dw or db
     const int c = (n / E * tpr + tt) * E + n % E;
     if (c >= cols) continue;
     float sum = 0.f;
@@ -591,36 +592,19 @@ BwdLaunch bwd_warp_launch(const LnBwdParams& p, int pieces, int sms) {
   return l;
 }
 
-template <typename T, int EL>
+template <typename T>
 BwdLaunch bwd_ring_launch(LnBwdParams& p, int sms) {
-  using Shape = Ring<T, EL>;
-  p.tpr = (p.cols + EL * 32 - 1) / (EL * 32) * 32;
+  using Shape = Ring<T>;
+  p.tpr = (p.cols + 16 * 32 - 1) / (16 * 32) * 32;
   p.groups = Shape::MAX_THREADS / p.tpr;
   BwdLaunch l{};
   l.threads = p.groups * p.tpr;
   l.rows_per_cta = p.groups * Shape::R;
   l.grid = cta_count(p.rows, Shape::R, std::min(LN_MAX_PARTS, sms));
   l.smem = Shape::bytes(l.threads);
-  l.kernel = ln_bwd_ring_kernel<T, EL>;
+  l.kernel = ln_bwd_ring_kernel<T>;
   return l;
 }
-template <typename T>
-BwdLaunch bwd_ring_launch(LnBwdParams& p, int sms) {
-  // with 24 elements per thread where that makes two groups of one, whose rows then overlap (2^27 bf16
-  // elements in rows of 4608: 161 us and not 192); where 16 make two or more they are faster (of 3000:
-  // 164 and 169, of 1536 127 and 148); fp32 rows have enough in flight
-  const BwdLaunch l = bwd_ring_launch<T, 16>(p, sms);
-  if constexpr (sizeof(T) == 2) {
-    LnBwdParams q = p;
-    const BwdLaunch more = bwd_ring_launch<T, 24>(q, sms);
-    if (p.groups == 1 && q.groups > 1) {
-      p = q;
-      return more;
-    }
-  }
-  return l;
-}
-
 template <typename T, Access A>
 BwdLaunch bwd_group_launch(LnBwdParams& p, int pieces, int sms) {
   const GroupShape g = group_shape(pieces);
