@@ -394,6 +394,10 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
         key[j] = (__float_as_uint(x) & ~IDX) | static_cast<uint32_t>(expert_of<G>(j / 8, g, j & 7));
     }
     sum = group_add<G>(sum);
+    // A sum below this is not a softmax's, and NaN in x makes it NaN. Of the other tokens the keys say
+    // nothing: where the maximum is -inf beside NaN, those of the places past the last expert are no
+    // longer CLOSED, so no logit is read by such a key. The second loop selects for them.
+    const bool sure = on && sum >= 0.5f;
     uint32_t own[D];
     least<D, V>(key, own);
     const uint32_t deepest = own[D - 1];
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       if constexpr (D == V) own[D - 1] = won ? NONE : own[D - 1];
     }
     __syncwarp();
-    if (D < V && p.k >= D && __any_sync(FULL, on && deepest <= order[p.k - 1])) {
+    if (D < V && p.k >= D && __any_sync(FULL, sure && deepest <= order[p.k - 1])) {
       // a lane gave all it kept: the rounds again, over all keys
       uint32_t taken = 0;
       bool none = true;
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       const int r = s * G + g;
       idx[s] = -1;
       w[s] = 0.f;
-      if (s * G < p.k && r < p.k && on) {
+      if (s * G < p.k && r < p.k && sure) {
         const uint32_t mine = order[r], then = order[r + 1];
         if (mine < CLOSED) {
           idx[s] = static_cast<int>(mine & IDX);
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       }
     }
     if (__any_sync(FULL, wrong)) {
-      if (g == 0 && on) put_right<IDX>(order, p.k, here);
+      if (g == 0 && sure) put_right<IDX>(order, p.k, here);
       __syncwarp();
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
@@ -461,12 +465,12 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       }
     }
     const uint32_t last = order[p.k - 1], after = order[p.k];
-    bool unsure = on && !(sum >= 0.5f);
+    bool unsure = on && !sure;
     if (__any_sync(FULL, on && last >= CLOSED)) {      // fewer than k above -inf: in the logits, or only in x?
 #pragma unroll
       for (int j = 0; j < V; ++j) unsure |= on && l[j] > MINUS_INF && fmaf(l[j], LOG2E, down) == MINUS_INF;
     }
-    const bool tie = on && last < CLOSED && (last & ~IDX) == (after & ~IDX);
+    const bool tie = sure && last < CLOSED && (last & ~IDX) == (after & ~IDX);
     if (__any_sync(FULL, tie)) {                       // no other that agrees with the last may be larger
       const float worst = tie ? to_float(here[last & IDX]) : 0.f;
       uint32_t larger = 0;
