@@ -120,6 +120,15 @@ int router_parts(int tokens, int experts, int sms);
 cudaError_t launch_router(RouterParams p, int type, int sms, cudaStream_t s, int* launches);
 cudaError_t launch_router_backward(RouterBwdParams p, int type, int sms, cudaStream_t s, int* launches);
 
+// Lets a launch with `smem` bytes of dynamic shared memory be made.  `most`: the most that any launch of this
+// kernel asks for, so that every call sets the same limit: a smaller one, set by another host thread between
+// this and the launch, would refuse the launch.  What a launch occupies goes by its own size.
+template <typename P>
+cudaError_t allow_shared(void (*kernel)(P), size_t smem, size_t most) {
+  if (smem <= 40 * 1024) return cudaSuccess;         // with a kernel's own arrays within the 48 KB of every launch
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+}
+
 // A launch that may start while the kernel before it in the stream drains: its kernel begins with
 // begin_after_previous, before it reads or writes anything.
 template <typename P>

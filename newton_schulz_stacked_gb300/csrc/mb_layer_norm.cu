@@ -381,8 +381,7 @@ cudaError_t fwd_ring(LnFwdParams p, int sms, cudaStream_t s) {
   p.tpr = (p.cols + 16 * 32 - 1) / (16 * 32) * 32;
   const int threads = Shape::MAX_THREADS / p.tpr * p.tpr;
   const size_t smem = Shape::bytes(threads);
-  const cudaError_t e =
-      cudaFuncSetAttribute(ln_fwd_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = allow_shared(ln_fwd_ring_kernel<T>, smem, Shape::bytes(Shape::MAX_THREADS));
   if (e != cudaSuccess) return e;
   return launch_after(ln_fwd_ring_kernel<T>, dim3(cta_count(p.rows, Shape::R, sms)), dim3(threads), smem, s, p);
 }

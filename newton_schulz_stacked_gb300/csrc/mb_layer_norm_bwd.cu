@@ -572,7 +572,7 @@ cudaError_t bwd_wide(const LnBwdParams& p, int sms, cudaStream_t s, int* launche
 struct BwdLaunch {
   void (*kernel)(LnBwdParams);
   int grid, threads, rows_per_cta;
-  size_t smem;
+  size_t smem, most_smem;      // of this launch; of any launch of the kernel
 };
 
 template <typename T, Access A>
@@ -584,7 +584,8 @@ BwdLaunch bwd_warp_launch(const LnBwdParams& p, int pieces, int sms) {
   l.rows_per_cta = l.threads / 32;
   l.grid = cta_count(p.rows, l.rows_per_cta, std::min(LN_MAX_PARTS, sms));
   const int staged = nv == 2 ? Staged<A, 2>::floats(32) : nv == 3 ? Staged<A, 3>::floats(32) : Staged<A, 4>::floats(32);
-  l.smem = static_cast<size_t>(params ? std::max(staged, 16 * nv * l.threads) : staged) * sizeof(float);
+  l.most_smem = static_cast<size_t>(std::max(staged, 16 * nv * l.threads)) * sizeof(float);
+  l.smem = params ? l.most_smem : static_cast<size_t>(staged) * sizeof(float);
   l.kernel = nv == 2 ? ln_bwd_warp_kernel<T, A, 2> : ln_bwd_warp_kernel<T, A, 3>;
   if constexpr (WARP_PIECES<T, A> > 96) {
     if (nv == 4) l.kernel = ln_bwd_warp_kernel<T, A, 4>;
@@ -602,6 +603,7 @@ BwdLaunch bwd_ring_launch(LnBwdParams& p, int sms) {
   l.rows_per_cta = p.groups * Shape::R;
   l.grid = cta_count(p.rows, Shape::R, std::min(LN_MAX_PARTS, sms));
   l.smem = Shape::bytes(l.threads);
+  l.most_smem = Shape::bytes(Shape::MAX_THREADS);
   l.kernel = ln_bwd_ring_kernel<T>;
   return l;
 }
@@ -616,6 +618,7 @@ BwdLaunch bwd_group_launch(LnBwdParams& p, int pieces, int sms) {
   l.rows_per_cta = g.groups * R;
   l.grid = cta_count(p.rows, l.rows_per_cta, std::min(LN_MAX_PARTS, g.ctas * sms));
   l.smem = p.dw || p.db ? static_cast<size_t>(l.threads) * 16 * sizeof(float) : 0;
+  l.most_smem = static_cast<size_t>(g.most) * 16 * sizeof(float);
   l.kernel = ln_bwd_kernel<T, A, R, 256>;
   if constexpr (A != Access::VEC) {
     if (g.most == 288) l.kernel = ln_bwd_kernel<T, A, 1, 288>;
@@ -642,10 +645,7 @@ cudaError_t bwd(LnBwdParams p, int sms, cudaStream_t s, int* launches) {
   }
   if (l.grid == 1 || !(p.dw || p.db)) p.parts = nullptr;
   cudaError_t e;
-  if (l.smem > 40 * 1024 &&
-      (e = cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l.smem))) !=
-          cudaSuccess)
-    return e;
+  if ((e = allow_shared(l.kernel, l.smem, l.most_smem)) != cudaSuccess) return e;
   if ((e = launch_after(l.kernel, dim3(l.grid), dim3(l.threads), l.smem, s, p)) != cudaSuccess) return e;
   *launches += 1;
   if (!p.parts) return cudaSuccess;

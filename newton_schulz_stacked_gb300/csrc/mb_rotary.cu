@@ -227,11 +227,10 @@ cudaError_t rotary(RotaryParams p, int sms, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(tile) * p.pairs * sizeof(float2) + static_cast<size_t>(tile) * sizeof(TokenBase);
   const unsigned grid = static_cast<unsigned>((p.all_tokens + tile - 1) / tile);
   auto kernel = p.interleaved ? rotary_kernel<T, N, true> : rotary_kernel<T, N, false>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  // a tile has at most ROTARY_MAX_PAIRS pairs and four times THREADS tokens
+  const cudaError_t e =
+      allow_shared(kernel, smem, ROTARY_MAX_PAIRS * sizeof(float2) + 4 * THREADS * sizeof(TokenBase));
+  if (e != cudaSuccess) return e;
   return launch_after(kernel, dim3(grid), dim3(THREADS), smem, s, p);
 }
 

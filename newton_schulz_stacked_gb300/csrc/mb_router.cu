@@ -864,12 +864,13 @@ cudaError_t fwd(const RouterParams& p, cudaStream_t s, int* launches) {
   const bool vec = p.experts % 8 == 0 && vec_rows(p.logits, p.stride, sizeof(T), p.tokens);
   const FwdShape f = fwd_shape(p.experts);
   const auto kernel = vec ? fwd_kernel<T, true>(f.g, f.nc) : fwd_kernel<T, false>(f.g, f.nc);
-  const size_t smem = (static_cast<size_t>(WARPS + 1) * p.experts + WARPS * (32 / f.g) * (p.k + 1)) * 4;
+  const auto bytes = [&](int experts, int k) {
+    return (static_cast<size_t>(WARPS + 1) * experts + WARPS * (32 / f.g) * (k + 1)) * 4;
+  };
+  const size_t smem = bytes(p.experts, p.k);
+  const int places = 8 * f.g * f.nc;                   // the most experts of this kernel
   cudaError_t e;
-  if (smem > 40 * 1024 &&
-      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
-          cudaSuccess)
-    return e;
+  if ((e = allow_shared(kernel, smem, bytes(places, std::min(places, ROUTER_MAX_K)))) != cudaSuccess) return e;
   if ((e = launch_after(kernel, dim3(p.parts), dim3(THREADS), smem, s, p)) != cudaSuccess) return e;
   *launches = 1;
   if (p.parts == 1) return cudaSuccess;
@@ -886,11 +887,8 @@ cudaError_t bwd(const RouterBwdParams& p, int sms, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(THREADS) * 8 * nc * 4;
   const int per = WARPS * (32 / g);
   const int want = static_cast<int>((static_cast<long long>(p.tokens) + per - 1) / per), most = 2 * sms;
-  if (smem > 40 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_shared(kernel, smem, smem);          // by the kernel alone
+  if (e != cudaSuccess) return e;
   return launch_after(kernel, dim3(want < most ? want : most), dim3(THREADS), smem, s, p);
 }
 
