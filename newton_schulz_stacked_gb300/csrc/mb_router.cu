@@ -379,6 +379,9 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       for (int j = 0; j < V; ++j) nan |= l[j] != l[j];
       nan = any_of_group<G>(nan, lane);
       on &= m > MINUS_INF || nan;
+      // x = -inf, and with it a closed key, for the places past the last expert too: -inf - (-inf) would be
+      // NaN, their keys would come before closed ones, and the comparisons below would read past the row
+      if (m == MINUS_INF && nan) m = 0.f;
     }
     const float down = 0.f - __fmul_ru(m, LOG2E);      // +0 for a maximum of either zero
     float e[V], sum = 0.f;
@@ -394,10 +397,6 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
         key[j] = (__float_as_uint(x) & ~IDX) | static_cast<uint32_t>(expert_of<G>(j / 8, g, j & 7));
     }
     sum = group_add<G>(sum);
-    // A sum below this is not a softmax's, and NaN in x makes it NaN. Of the other tokens the keys say
-    // nothing: where the maximum is -inf beside NaN, those of the places past the last expert are no
-    // longer CLOSED, so no logit is read by such a key. The second loop selects for them.
-    const bool sure = on && sum >= 0.5f;
     uint32_t own[D];
     least<D, V>(key, own);
     const uint32_t deepest = own[D - 1];
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       if constexpr (D == V) own[D - 1] = won ? NONE : own[D - 1];
     }
     __syncwarp();
-    if (D < V && p.k >= D && __any_sync(FULL, sure && deepest <= order[p.k - 1])) {
+    if (D < V && p.k >= D && __any_sync(FULL, on && deepest <= order[p.k - 1])) {
       // a lane gave all it kept: the rounds again, over all keys
       uint32_t taken = 0;
       bool none = true;
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       const int r = s * G + g;
       idx[s] = -1;
       w[s] = 0.f;
-      if (s * G < p.k && r < p.k && sure) {
+      if (s * G < p.k && r < p.k && on) {
         const uint32_t mine = order[r], then = order[r + 1];
         if (mine < CLOSED) {
           idx[s] = static_cast<int>(mine & IDX);
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       }
     }
     if (__any_sync(FULL, wrong)) {
-      if (g == 0 && sure) put_right<IDX>(order, p.k, here);
+      if (g == 0 && on) put_right<IDX>(order, p.k, here);
       __syncwarp();
 #pragma unroll
       for (int s = 0; s < SLOTS; ++s) {
@@ -465,12 +464,12 @@ __global__ void __launch_bounds__(THREADS, NC == 1 ? 2 : 1) router_kernel(const 
       }
     }
     const uint32_t last = order[p.k - 1], after = order[p.k];
-    bool unsure = on && !sure;
+    bool unsure = on && !(sum >= 0.5f);
     if (__any_sync(FULL, on && last >= CLOSED)) {      // fewer than k above -inf: in the logits, or only in x?
 #pragma unroll
       for (int j = 0; j < V; ++j) unsure |= on && l[j] > MINUS_INF && fmaf(l[j], LOG2E, down) == MINUS_INF;
     }
-    const bool tie = sure && last < CLOSED && (last & ~IDX) == (after & ~IDX);
+    const bool tie = on && last < CLOSED && (last & ~IDX) == (after & ~IDX);
     if (__any_sync(FULL, tie)) {                       // no other that agrees with the last may be larger
       const float worst = tie ? to_float(here[last & IDX]) : 0.f;
       uint32_t larger = 0;
