@@ -1,4 +1,9 @@
-"""The block operators under torch's autograd: each forward call joined with its backward call."""
+"""The block operators under torch's autograd: each forward call joined with its backward call.
+
+rotary is linear in q and k and can be differentiated any number of times.  layer_norm and route
+have first derivatives only: differentiating their gradients (of create_graph=True) raises
+RuntimeError.
+"""
 from __future__ import annotations
 
 from typing import NamedTuple, Sequence
@@ -21,6 +26,25 @@ def _readable(g: torch.Tensor) -> torch.Tensor:
     return g if g.shape[-1] == 1 or g.stride(-1) == 1 else g.contiguous()
 
 
+class _FirstOnly(torch.autograd.Function):
+    """A gradient that has none itself.  Its inputs tie it into the graph, so that the gradient is not
+    taken for a constant: a second derivative that needs it raises."""
+
+    @staticmethod
+    def forward(ctx, name, call, *inputs):
+        ctx.name = name
+        return call(*inputs)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} has no second derivative")
+
+
+def _first_only(name, call, *inputs):
+    """call(*inputs); under create_graph=True, as a step of the graph."""
+    return _FirstOnly.apply(name, call, *inputs) if torch.is_grad_enabled() else call(*inputs)
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
@@ -34,7 +58,8 @@ class _LayerNorm(torch.autograd.Function):
         x, weight, mean, rstd = ctx.saved_tensors
         if not dy.is_contiguous():
             dy = dy.contiguous()
-        dx, dweight, dbias = _k.mb_layer_norm_backward(dy, x, mean, rstd, weight, bias=ctx.has_bias)
+        dx, dweight, dbias = _first_only(
+            "layer_norm", lambda *t: _k.mb_layer_norm_backward(*t, bias=ctx.has_bias), dy, x, mean, rstd, weight)
         return dx, dweight, dbias, None
 
 
@@ -47,26 +72,29 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5) -> torch.Tensor:
 
 class _Rotary(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, sections, interleaved):
+    def forward(ctx, q, k, positions, inv_freq, sections, interleaved, back):
         ctx.save_for_backward(positions, inv_freq)
-        ctx.sections, ctx.interleaved = sections, interleaved
+        ctx.args = sections, interleaved
+        ctx.back = back
         ctx.set_materialize_grads(False)
-        return _k.mb_rotary(q, k, positions, inv_freq, sections, interleaved)
+        return (_k.mb_rotary_backward if back else _k.mb_rotary)(q, k, positions, inv_freq, sections, interleaved)
 
     @staticmethod
     def backward(ctx, dq, dk):
-        positions, inv_freq = ctx.saved_tensors
-        args = (positions, inv_freq, ctx.sections, ctx.interleaved)
+        def turn_back(a, b):
+            b = None if b is None else _readable(b)
+            return _Rotary.apply(_readable(a), b, *ctx.saved_tensors, *ctx.args, not ctx.back)
+
         if dq is not None:
-            dq, dk = _k.mb_rotary_backward(_readable(dq), None if dk is None else _readable(dk), *args)
+            dq, dk = turn_back(dq, dk)
         elif dk is not None:
-            dk, _ = _k.mb_rotary_backward(_readable(dk), None, *args)
-        return dq, dk, None, None, None, None
+            dk, _ = turn_back(dk, None)
+        return dq, dk, None, None, None, None, None
 
 
 def rotary(q, k, positions, inv_freq, sections: Sequence[int], interleaved: bool = False):
     """mb_rotary, differentiable in q and k (k may be None): (q_out, k_out)."""
-    return _Rotary.apply(q, k, positions, inv_freq, tuple(sections), interleaved)
+    return _Rotary.apply(q, k, positions, inv_freq, tuple(sections), interleaved, False)
 
 
 class _Route(torch.autograd.Function):
@@ -84,9 +112,10 @@ class _Route(torch.autograd.Function):
         if dgate is None and dloss is None:
             return None, None, None, None
         logits, valid, index, gate, counts, used = ctx.saved_tensors
-        return _k.mb_router_backward(None if dloss is None else dloss.reshape(1),
-                                     None if dgate is None else dgate.contiguous(), logits, index, gate, counts, used,
-                                     valid, ctx.normalize), None, None, None
+        dlogits = _first_only(
+            "route", lambda *t: _k.mb_router_backward(*t, normalize=ctx.normalize), None if dloss is None else dloss.reshape(1),
+            None if dgate is None else dgate.contiguous(), logits, index, gate, counts, used, valid)
+        return dlogits, None, None, None
 
 
 def route(logits, top_k: int, valid=None, normalize: bool = False) -> Routing:
