@@ -3,9 +3,10 @@
 Each function has the name of the C entry point it calls (include/muonbank.h gives the
 formulas), takes CUDA tensors and enqueues the work on the current CUDA stream, or on
 `stream`.  Results are new tensors unless the caller passes them; a given result may be the
-input that it replaces.  New tensors of one call may share an allocation (mean and rstd; index and
-gate; counts, loss and used).  Every operator has its gradient as a call of its own;
-`newton_schulz_stacked_gb300.autograd` joins the pairs for torch's autograd.
+input that it replaces, and counts as modified in place.  New tensors of one call may share an
+allocation (mean and rstd; index and gate; counts, loss and used).  Every operator has its gradient
+as a call of its own; autograd does not record these calls, but
+`newton_schulz_stacked_gb300.autograd` joins the pairs for it.
 
 Tensors may be strided in all but their last dimension; a tensor that is not laid out so, or
 has another shape, type or device than the call's others, is refused with ValueError, and what

@@ -221,8 +221,13 @@ PyObject* wrap(const Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
 }
-// The given tensor's own object, or a new one.
-PyObject* give(PyObject* given, const Tensor& t) { return given == Py_None ? wrap(t) : Py_NewRef(given); }
+// The given tensor's own object, or a new one; called once the kernels are launched.  A given tensor counts as
+// modified in place, so that a backward pass that has saved it notices (one of inference mode has no version).
+PyObject* give(PyObject* given, const Tensor& t) {
+  if (given == Py_None) return wrap(t);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return Py_NewRef(given);
+}
 
 template <typename... O>
 PyObject* tuple(O... o) {
