@@ -217,6 +217,16 @@ void checked(const char* name, int status) {
   throw Raised{};
 }
 
+// A call of the library, its arguments ready, while other threads may run: a launch waits where the stream's
+// queue is full.
+template <typename CALL>
+int unlocked(CALL&& call) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int status = call();
+  PyEval_RestoreThread(state);
+  return status;
+}
+
 PyObject* wrap(const Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
@@ -288,11 +298,15 @@ PyObject* layer_norm(PyObject* const* a, Py_ssize_t n) {
   stats.allocate();
   const Tensor mean = stats.take(a[5], "mean", lead, ScalarType::Float, mean_at);
   const Tensor rstd = stats.take(a[6], "rstd", lead, ScalarType::Float, rstd_at);
-  checked("mb_layer_norm",
-          mb_layer_norm(x.data_ptr(), row_stride(x, "x"), s.type, wp, bp, s.w_type, y.data_ptr(), row_stride(y, "y"),
-                        static_cast<float*>(dense(&mean, "mean", lead, ScalarType::Float, device)),
-                        static_cast<float*>(dense(&rstd, "rstd", lead, ScalarType::Float, device)), s.rows, s.cols,
-                        eps, where.stream));
+  const void* xp = x.data_ptr();
+  void* yp = y.data_ptr();
+  auto* mp = static_cast<float*>(dense(&mean, "mean", lead, ScalarType::Float, device));
+  auto* rp = static_cast<float*>(dense(&rstd, "rstd", lead, ScalarType::Float, device));
+  const int64_t x_stride = row_stride(x, "x"), y_stride = row_stride(y, "y");
+  checked("mb_layer_norm", unlocked([&] {
+            return mb_layer_norm(xp, x_stride, s.type, wp, bp, s.w_type, yp, y_stride, mp, rp, s.rows, s.cols, eps,
+                                 where.stream);
+          }));
   return tuple(give(a[4], y), give(a[5], mean), give(a[6], rstd));
 }
 
@@ -326,10 +340,14 @@ PyObject* layer_norm_backward(PyObject* const* a, Py_ssize_t n) {
   } else if (a[7] != Py_None || a[8] != Py_None) {
     throw Refused{"dweight and dbias need a weight"};
   }
-  checked("mb_layer_norm_backward",
-          mb_layer_norm_backward(dy.data_ptr(), row_stride(dy, "dy"), x.data_ptr(), row_stride(x, "x"), s.type, wp,
-                                 s.w_type, mean, rstd, dx.data_ptr(), row_stride(dx, "dx"), dwp, dbp, s.rows, s.cols,
-                                 ws ? ws->ptr : nullptr, ws ? ws->bytes : 0, where.stream));
+  const void *dyp = dy.data_ptr(), *xp = x.data_ptr();
+  void* dxp = dx.data_ptr();
+  const int64_t dy_stride = row_stride(dy, "dy"), x_stride = row_stride(x, "x"), dx_stride = row_stride(dx, "dx");
+  checked("mb_layer_norm_backward", unlocked([&] {
+            return mb_layer_norm_backward(dyp, dy_stride, xp, x_stride, s.type, wp, s.w_type, mean, rstd, dxp, dx_stride,
+                                          dwp, dbp, s.rows, s.cols, ws ? ws->ptr : nullptr, ws ? ws->bytes : 0,
+                                          where.stream);
+          }));
   return tuple(give(a[6], dx), give(a[7], dw), give(a[8], db));
 }
 
@@ -425,7 +443,7 @@ PyObject* rotary(PyObject* const* a, Py_ssize_t n, const char* name) {
   }
   r.pos_axis = pos.stride(0);
   r.positions = pos.data_ptr();
-  checked(name, CALL(&r, where.stream));
+  checked(name, unlocked([&] { return CALL(&r, where.stream); }));
   return tuple(give(a[6], qo), give(a[7], ko));
 }
 
@@ -465,14 +483,17 @@ PyObject* router(PyObject* const* a, Py_ssize_t n) {
   const Tensor counts = all.take(a[6], "counts", {experts}, ScalarType::Int, counts_at);
   const Tensor loss = all.take(a[7], "loss", {1}, ScalarType::Float, loss_at);
   const Tensor used = all.take(a[8], "used", {1}, ScalarType::Int, used_at);
-  checked("mb_router",
-          mb_router(l.data_ptr(), row_stride(l, "logits"), type, valid, tokens, experts, static_cast<int>(k), normalize,
-                    static_cast<int32_t*>(dense(&index, "index", {tokens, k}, ScalarType::Int, device)),
-                    static_cast<float*>(dense(&gate, "gate", {tokens, k}, ScalarType::Float, device)),
-                    static_cast<int32_t*>(dense(&counts, "counts", {experts}, ScalarType::Int, device)),
-                    static_cast<float*>(dense(&loss, "loss", {1}, ScalarType::Float, device)),
-                    static_cast<int32_t*>(dense(&used, "used", {1}, ScalarType::Int, device)), ws.ptr, ws.bytes,
-                    where.stream));
+  auto* ip = static_cast<int32_t*>(dense(&index, "index", {tokens, k}, ScalarType::Int, device));
+  auto* gp = static_cast<float*>(dense(&gate, "gate", {tokens, k}, ScalarType::Float, device));
+  auto* cp = static_cast<int32_t*>(dense(&counts, "counts", {experts}, ScalarType::Int, device));
+  auto* lossp = static_cast<float*>(dense(&loss, "loss", {1}, ScalarType::Float, device));
+  auto* usedp = static_cast<int32_t*>(dense(&used, "used", {1}, ScalarType::Int, device));
+  const void* lp = l.data_ptr();
+  const int64_t stride = row_stride(l, "logits");
+  checked("mb_router", unlocked([&] {
+            return mb_router(lp, stride, type, valid, tokens, experts, static_cast<int>(k), normalize, ip, gp, cp, lossp,
+                             usedp, ws.ptr, ws.bytes, where.stream);
+          }));
   return tuple(give(a[4], index), give(a[5], gate), give(a[6], counts), give(a[7], loss), give(a[8], used));
 }
 
@@ -489,17 +510,21 @@ PyObject* router_backward(PyObject* const* a, Py_ssize_t n) {
   if (k < 1 || k > experts) checked("mb_router_backward", MB_ERR_SHAPE);
   const Tensor dl = result(a[9], "dlogits", l.sizes(), l.scalar_type(), device);
   const auto f32 = ScalarType::Float, i32 = ScalarType::Int;
-  checked("mb_router_backward",
-          mb_router_backward(
-              static_cast<const float*>(dense(tensor_or_none(a[0], "dloss"), "dloss", {1}, f32, device)),
-              static_cast<const float*>(dense(tensor_or_none(a[1], "dgate"), "dgate", {tokens, k}, f32, device)),
-              l.data_ptr(), row_stride(l, "logits"), type, valid_of(a[7], tokens, device), tokens, experts,
-              static_cast<int>(k), truth(a[8]),
-              static_cast<const int32_t*>(dense(&index, "index", {tokens, k}, i32, device)),
-              static_cast<const float*>(dense(&tensor(a[4], "gate"), "gate", {tokens, k}, f32, device)),
-              static_cast<const int32_t*>(dense(&tensor(a[5], "counts"), "counts", {experts}, i32, device)),
-              static_cast<const int32_t*>(dense(&tensor(a[6], "used"), "used", {1}, i32, device)), dl.data_ptr(),
-              row_stride(dl, "dlogits"), where.stream));
+  const auto* dlossp = static_cast<const float*>(dense(tensor_or_none(a[0], "dloss"), "dloss", {1}, f32, device));
+  const auto* dgatep = static_cast<const float*>(dense(tensor_or_none(a[1], "dgate"), "dgate", {tokens, k}, f32, device));
+  const uint8_t* valid = valid_of(a[7], tokens, device);
+  const int normalize = truth(a[8]);
+  const auto* ip = static_cast<const int32_t*>(dense(&index, "index", {tokens, k}, i32, device));
+  const auto* gp = static_cast<const float*>(dense(&tensor(a[4], "gate"), "gate", {tokens, k}, f32, device));
+  const auto* cp = static_cast<const int32_t*>(dense(&tensor(a[5], "counts"), "counts", {experts}, i32, device));
+  const auto* usedp = static_cast<const int32_t*>(dense(&tensor(a[6], "used"), "used", {1}, i32, device));
+  const void* lp = l.data_ptr();
+  void* dlp = dl.data_ptr();
+  const int64_t stride = row_stride(l, "logits"), dl_stride = row_stride(dl, "dlogits");
+  checked("mb_router_backward", unlocked([&] {
+            return mb_router_backward(dlossp, dgatep, lp, stride, type, valid, tokens, experts, static_cast<int>(k),
+                                      normalize, ip, gp, cp, usedp, dlp, dl_stride, where.stream);
+          }));
   return give(a[9], dl);
 }
 

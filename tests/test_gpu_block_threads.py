@@ -1,11 +1,12 @@
 """Block operators called by several host threads."""
 import ctypes
 import threading
+import time
 
 import pytest
 import torch
 
-from test_gpu_blocks import nss      # noqa: F401  (a fixture)
+from test_gpu_blocks import gen, norm_inputs, nss, randn, same_bits      # noqa: F401  (nss is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +84,65 @@ def test_c_calls_of_one_kernel_at_two_sizes(nss):
     _together(norm_calls(8192), norm_calls(4608), norm_calls(2568))
     _together(router_calls(1024, 8), router_calls(640, 8))
     _together(norm_calls(8177), norm_calls(6001))
+
+
+def test_python_calls_side_by_side(nss):
+    """Each thread on its own stream gets the bits that it gets alone."""
+    x, w, b, dy = norm_inputs(1, 60, 4608, torch.bfloat16, torch.float32)
+    x2, w2, b2, dy2 = norm_inputs(2, 60, 8192, torch.bfloat16, torch.float32)
+    logits = randn(gen(3), 400, 256)
+    _, mean, rstd = nss.mb_layer_norm(x, w, b)
+    _, mean2, rstd2 = nss.mb_layer_norm(x2, w2, b2)
+    calls = [lambda **s: nss.mb_layer_norm_backward(dy, x, mean, rstd, w, **s),
+             lambda **s: nss.mb_layer_norm_backward(dy2, x2, mean2, rstd2, w2, **s),
+             lambda **s: nss.mb_router(logits, 8, **s)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+
+    def worker(call, ref):
+        stream = torch.cuda.Stream()
+
+        def run():
+            for _ in range(200):
+                got = call(stream=stream)
+                stream.synchronize()
+                for a, c in zip(got, ref):
+                    same_bits(a, c, "beside other threads")
+        return run
+
+    _together(*(worker(c, r) for c, r in zip(calls, want)))
+
+
+def test_other_threads_run_while_a_call_waits(nss):
+    """A stream takes a limited number of launches; the call that finds it full waits, and only its own thread with it."""
+    x, w, b, _ = norm_inputs(4, 4, 64, torch.float32, torch.float32)
+    y, mean, rstd = nss.mb_layer_norm(x, w, b)
+    torch.cuda.synchronize()
+    stop, longest = threading.Event(), [0.0]
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            longest[0] = max(longest[0], now - last)
+            last = now
+
+    ticker = threading.Thread(target=tick)
+    ticker.start()
+    time.sleep(0.05)
+    longest[0], waited = 0.0, 0.0
+    try:
+        torch.cuda._sleep(2_000_000_000)                     # about a second of the GPU's clock, ahead of the calls
+        for _ in range(20000):
+            t = time.perf_counter()
+            nss.mb_layer_norm(x, w, b, y=y, mean=mean, rstd=rstd)
+            waited = max(waited, time.perf_counter() - t)
+            if waited > 0.2:
+                break
+    finally:
+        stop.set()
+        ticker.join()
+        torch.cuda.synchronize()
+    assert waited > 0.2, "no call had to wait"
+    assert longest[0] < 0.5 * waited, f"another thread stood still for {longest[0]:.3f} s of {waited:.3f}"
