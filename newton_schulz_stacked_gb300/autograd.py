@@ -22,7 +22,9 @@ class Routing(NamedTuple):
 
 
 def _readable(g: torch.Tensor) -> torch.Tensor:
-    """Autograd may hand over an expanded gradient (of a sum, say): its elements are laid out first."""
+    """Autograd may hand over an expanded gradient (of a sum, say) or a negated view (through a conjugate): its
+    elements are laid out first."""
+    g = g.resolve_neg()
     return g if g.shape[-1] == 1 or g.stride(-1) == 1 else g.contiguous()
 
 
@@ -56,8 +58,7 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        if not dy.is_contiguous():
-            dy = dy.contiguous()
+        dy = dy.resolve_neg().contiguous()
         dx, dweight, dbias = _first_only(
             "layer_norm", lambda *t: _k.mb_layer_norm_backward(*t, bias=ctx.has_bias), dy, x, mean, rstd, weight)
         return dx, dweight, dbias, None
@@ -113,8 +114,8 @@ class _Route(torch.autograd.Function):
             return None, None, None, None
         logits, valid, index, gate, counts, used = ctx.saved_tensors
         dlogits = _first_only(
-            "route", lambda *t: _k.mb_router_backward(*t, normalize=ctx.normalize), None if dloss is None else dloss.reshape(1),
-            None if dgate is None else dgate.contiguous(), logits, index, gate, counts, used, valid)
+            "route", lambda *t: _k.mb_router_backward(*t, normalize=ctx.normalize), None if dloss is None else dloss.resolve_neg().reshape(1),
+            None if dgate is None else dgate.resolve_neg().contiguous(), logits, index, gate, counts, used, valid)
         return dlogits, None, None, None
 
 

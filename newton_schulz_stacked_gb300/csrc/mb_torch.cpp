@@ -47,7 +47,10 @@ std::string str(const Tensor& t) {
 const Tensor* tensor_or_none(PyObject* o, const char* what) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) throw Refused{std::string(what) + " must be a tensor"};
-  return &THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  // such a view's memory holds other values than the tensor
+  if (t.is_neg()) throw Refused{std::string(what) + " is a negated view: call resolve_neg() first"};
+  return &t;
 }
 const Tensor& tensor(PyObject* o, const char* what) {
   const Tensor* t = tensor_or_none(o, what);

@@ -74,3 +74,24 @@ def test_rotary_second_derivative(nss, with_k):
     for a, c in zip(got, want):
         # three rotations of 8 U each, products of up to three rounded factors
         assert ((a.double() - c).abs() <= 100 * 2.0 ** -24 * (c.abs() + c.abs().amax())).all()
+
+
+def test_negated_gradients(nss):
+    """A gradient that comes through a conjugate's imaginary part may be a negated view."""
+    from newton_schulz_stacked_gb300 import autograd as A
+
+    def minus(t):
+        return torch.complex(torch.zeros_like(t), t).conj().imag
+
+    def grads(f, *leaves):
+        return torch.autograd.grad(f(*leaves), leaves)
+
+    q, k, pos, freq = rotary_inputs(5, 1, 3, 2, 1, 8, (4,), torch.float32)
+    logits = randn(gen(6), 9, 4).requires_grad_()
+    x, w, b, _ = norm_inputs(7, 1, 1, torch.float32, torch.float32)
+    leaves = [v.requires_grad_() for v in (x, w, b)]
+    for f, at in ((lambda l: A.route(l, 2).loss, [logits]), (lambda l: A.route(l[:1], 1).gate, [logits]),
+                  (lambda *v: A.layer_norm(*v), leaves),
+                  (lambda a: A.rotary(a, None, pos, freq, (4,))[0], [q.requires_grad_()])):
+        for a, c in zip(grads(lambda *v: minus(f(*v)).sum(), *at), grads(lambda *v: -f(*v).sum(), *at)):
+            assert torch.equal(a, c)

@@ -70,3 +70,18 @@ def test_results_made_in_inference_mode(nss):
         same_bits(nss.mb_layer_norm(x, w, b, y=y)[0], want, "in inference mode")
     y.untyped_storage()                                      # an inference tensor has no version to move
     same_bits(nss.mb_layer_norm(x, w, b, y=y)[0], want, "afterwards")
+
+
+def test_negated_views_are_refused(nss):
+    """The imaginary part of a conjugate is a view whose memory holds the negated values: reading it as it lies would
+    turn the wrong way."""
+    q, _, pos, freq = rotary_inputs(7, 1, 6, 2, 1, 16, (8,), torch.float32)
+    lazy = torch.complex(pos.float(), pos.float()).conj().imag
+    assert lazy.is_neg() and torch.equal(lazy, -pos.float())
+    for call in (nss.mb_rotary, nss.mb_rotary_backward):
+        with pytest.raises(ValueError, match="resolve_neg"):
+            call(q, None, lazy, freq, (8,))
+        same_bits(call(q, None, lazy.resolve_neg(), freq, (8,))[0], call(q, None, -pos.float(), freq, (8,))[0], "resolved")
+    x = torch.complex(q, q).conj().imag[..., :1]              # one element per row: any stride would do
+    with pytest.raises(ValueError, match="resolve_neg"):
+        nss.mb_layer_norm(x)
