@@ -16,7 +16,11 @@ void api_launched(int label, int launches, cudaStream_t stream);   // counts lau
 
 // ---------------------------------------------------------------- layer norm
 
-constexpr int LN_MAX_PARTS = 456;     // partial sums of the weight's gradient, rows of [2][cols]
+// Partial sums of the weight's gradient, rows of [2][cols]: one per CTA, or, of rows of more than LN_BWD_MAX_COLS
+// elements, one per slab of rows.
+constexpr int LN_MAX_PARTS = 456;
+constexpr int LN_BWD_MAX_COLS = 8192;    // wider rows are read again from memory
+constexpr int LN_WIDE_SLABS = 64;
 
 struct LnFwdParams {
   const void* x;

@@ -48,7 +48,8 @@ int norm_checks(int64_t rows, int64_t cols, int type, int w_type) {
 }
 
 size_t norm_workspace(int64_t rows, int64_t cols) {
-  const int64_t parts = rows < 1 ? 1 : rows < LN_MAX_PARTS ? rows : LN_MAX_PARTS;
+  const int64_t most = cols > LN_BWD_MAX_COLS ? LN_WIDE_SLABS : LN_MAX_PARTS;
+  const int64_t parts = rows < 1 ? 1 : rows < most ? rows : most;
   return static_cast<size_t>(parts) * 2 * static_cast<size_t>(cols) * sizeof(float);
 }
 

@@ -529,8 +529,6 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_params_kernel(const LnBwdPara
 
 // ---------------------------------------------------------------- launches
 
-constexpr int BWD_MAX_COLS = 8192;   // wider rows are read again from memory
-
 // How groups of threads share rows: up to 256 elements, and unaligned ones of more than 1024.  256
 // threads in two CTAs of 128 registers; longer rows 576 threads per SM at 96 registers in two or
 // three CTAs up to 2304 elements, then one CTA of 128 or 64 registers.
@@ -557,7 +555,7 @@ template <typename T, Access A>
 cudaError_t bwd_wide(const LnBwdParams& p, int sms, cudaStream_t s, int* launches) {
   cudaError_t e;
   if (p.dw || p.db) {
-    const int slabs = static_cast<int>(p.rows < 1 ? 1 : p.rows < 64 ? p.rows : 64);
+    const int slabs = static_cast<int>(p.rows < 1 ? 1 : p.rows < LN_WIDE_SLABS ? p.rows : LN_WIDE_SLABS);
     if ((e = launch_after(ln_bwd_wide_params_kernel<T>, dim3((p.cols + 255) / 256, slabs), dim3(256), 0, s, p)) != cudaSuccess)
       return e;
     if ((e = add_parts<T>(p, slabs, s)) != cudaSuccess) return e;
@@ -659,13 +657,13 @@ cudaError_t bwd_any(const LnBwdParams& p, int sms, cudaStream_t s, int* launches
   const bool vec = p.cols % 8 == 0 && aligned_rows(p.x, p.x_stride, SIZE, p.rows) &&
                    aligned_rows(p.dy, p.dy_stride, SIZE, p.rows) && aligned_rows(p.dx, p.dx_stride, SIZE, p.rows) &&
                    aligned(p.w);
-  if (p.cols > BWD_MAX_COLS)
+  if (p.cols > LN_BWD_MAX_COLS)
     return vec ? bwd_wide<T, Access::VEC>(p, sms, s, launches) : bwd_wide<T, Access::SCALAR>(p, sms, s, launches);
   if (vec) return bwd<T, Access::VEC>(p, sms, s, launches);
   // not where a warp holds a row and reads 64 or 128 bytes at a time by single elements too: 2^26 bf16
   // elements in rows of 777 take 115 us so and 90 by single ones; in rows of 201 148 and 318, of 2003
   // 124 and 313 (fp32: 161 and 204, 154 and 212)
-  if ((p.cols + 14 <= 256 || p.cols > 1024) && p.cols + 14 <= BWD_MAX_COLS && shiftable(p.x_stride, p.cols, p.rows) &&
+  if ((p.cols + 14 <= 256 || p.cols > 1024) && p.cols + 14 <= LN_BWD_MAX_COLS && shiftable(p.x_stride, p.cols, p.rows) &&
       shiftable(p.dy_stride, p.cols, p.rows) && same_shift(p.x, p.x_stride, p.dy, p.dy_stride, SIZE, p.rows) &&
       same_shift(p.x, p.x_stride, p.dx, p.dx_stride, SIZE, p.rows))
     return bwd<T, Access::SHIFT>(p, sms, s, launches);
