@@ -52,15 +52,16 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps):
         y, mean, rstd = _k.mb_layer_norm(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
-        ctx.has_bias = bias is not None
         return y
 
     @staticmethod
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dy = dy.resolve_neg().contiguous()
+        _, weight_grad, bias_grad, _ = ctx.needs_input_grad   # not of frozen parameters
         dx, dweight, dbias = _first_only(
-            "layer_norm", lambda *t: _k.mb_layer_norm_backward(*t, bias=ctx.has_bias), dy, x, mean, rstd, weight)
+            "layer_norm", lambda *t: _k.mb_layer_norm_backward(*t, bias=bias_grad, weight_grad=weight_grad), dy, x, mean,
+            rstd, weight)
         return dx, dweight, dbias, None
 
 

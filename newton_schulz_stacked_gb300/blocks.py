@@ -58,14 +58,16 @@ def mb_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=Non
 
 
 def mb_layer_norm_backward(dy, x, mean, rstd, weight=None, bias: bool = True, dx=None, dweight=None, dbias=None,
-                           workspace=None, stream=None):
+                           workspace=None, stream=None, weight_grad: bool = True):
     """Gradients of mb_layer_norm: (dx, dweight, dbias).
 
-    mean and rstd are the forward call's.  With a weight, dweight and (unless bias is False)
-    dbias come in the weight's type; without one they are None.
+    mean and rstd are the forward call's.  With a weight, dweight (unless weight_grad is False) and
+    dbias (unless bias is False) come in the weight's type; without one they are None, but a dbias
+    that is passed, in x's type or float32, is written.  Without either the sums over the rows are
+    left out, and with them a launch.
     """
     return (_native or load_binding()).mb_layer_norm_backward(dy, x, mean, rstd, weight, bias, dx, dweight, dbias,
-                                                              workspace, stream)
+                                                              workspace, stream, weight_grad)
 
 
 def mb_rotary(q, k, positions, inv_freq, sections: Sequence[int], interleaved: bool = False, q_out=None, k_out=None,

@@ -267,7 +267,8 @@ struct NormShape {
   int type, w_type;
 };
 
-NormShape norm_shape(const Tensor& x, const Tensor* w) {
+// w: a weight, bias or gradient of one, whose type the others share.
+NormShape norm_shape(const Tensor& x, const Tensor* w, const char* what) {
   if (x.dim() < 1) throw Refused{"x must have at least one dimension"};
   NormShape s{};
   s.cols = x.sizes().back();
@@ -277,8 +278,8 @@ NormShape norm_shape(const Tensor& x, const Tensor* w) {
   s.w_type = MB_F32;
   if (w) {
     if (w->scalar_type() != x.scalar_type() && w->scalar_type() != ScalarType::Float)
-      throw Refused{std::string("weight has dtype ") + c10::toString(w->scalar_type()) + ", expected x's or float32"};
-    s.w_type = type_of(*w, "weight");
+      throw Refused{std::string(what) + " has dtype " + c10::toString(w->scalar_type()) + ", expected x's or float32"};
+    s.w_type = type_of(*w, what);
   }
   return s;
 }
@@ -290,7 +291,7 @@ PyObject* layer_norm(PyObject* const* a, Py_ssize_t n) {
   Where where(x, a[7], a, n);
   const Tensor *w = tensor_or_none(a[1], "weight"), *b = tensor_or_none(a[2], "bias");
   const Tensor* param = w ? w : b;
-  const NormShape s = norm_shape(x, param);
+  const NormShape s = norm_shape(x, param, w ? "weight" : "bias");
   const auto wt = param ? param->scalar_type() : ScalarType::Float;
   const void *wp = dense(w, "weight", {s.cols}, wt, device), *bp = dense(b, "bias", {s.cols}, wt, device);
   const auto lead = x.sizes().slice(0, x.dim() - 1);
@@ -313,35 +314,38 @@ PyObject* layer_norm(PyObject* const* a, Py_ssize_t n) {
   return tuple(give(a[4], y), give(a[5], mean), give(a[6], rstd));
 }
 
-// dy, x, mean, rstd, weight, bias (whether there is one), dx, dweight, dbias, workspace, stream
+// dy, x, mean, rstd, weight, bias (whether its gradient is wanted), dx, dweight, dbias, workspace, stream, weight_grad
+// (whether the weight's is)
 PyObject* layer_norm_backward(PyObject* const* a, Py_ssize_t n) {
   const Tensor &x = cuda_tensor(a[1], "x"), &dy = tensor(a[0], "dy");
   const auto device = x.device();
   Where where(x, a[10], a, n);
-  const Tensor* w = tensor_or_none(a[4], "weight");
-  const NormShape s = norm_shape(x, w);
+  const Tensor *w = tensor_or_none(a[4], "weight"), *given_db = tensor_or_none(a[8], "dbias");
+  if (!w && a[7] != Py_None) throw Refused{"dweight needs a weight"};
+  const Tensor* param = w ? w : given_db;
+  const NormShape s = norm_shape(x, param, w ? "weight" : "dbias");
   like(dy, "dy", x.sizes(), x.scalar_type(), device);
   const auto lead = x.sizes().slice(0, x.dim() - 1);
   const auto* mean = static_cast<float*>(dense(&tensor(a[2], "mean"), "mean", lead, ScalarType::Float, device));
   const auto* rstd = static_cast<float*>(dense(&tensor(a[3], "rstd"), "rstd", lead, ScalarType::Float, device));
   const Tensor dx = result(a[6], "dx", x.sizes(), x.scalar_type(), device);
+  const auto wt = param ? param->scalar_type() : ScalarType::Float;
+  const void* wp = dense(w, "weight", {s.cols}, wt, device);
   Tensor dw, db;
-  void *wp = nullptr, *dwp = nullptr, *dbp = nullptr;
-  std::optional<Workspace> ws;
-  if (w) {
-    const auto wt = w->scalar_type();
-    wp = dense(w, "weight", {s.cols}, wt, device);
+  void *dwp = nullptr, *dbp = nullptr;
+  if (a[7] != Py_None || (w && truth(a[11]))) {
     dw = result(a[7], "dweight", {s.cols}, wt, device);
     dwp = dense(&dw, "dweight", {s.cols}, wt, device);
-    if (a[8] != Py_None || truth(a[5])) {
-      db = result(a[8], "dbias", {s.cols}, wt, device);
-      dbp = dense(&db, "dbias", {s.cols}, wt, device);
-    }
+  }
+  if (given_db || (w && truth(a[5]))) {
+    db = result(a[8], "dbias", {s.cols}, wt, device);
+    dbp = dense(&db, "dbias", {s.cols}, wt, device);
+  }
+  std::optional<Workspace> ws;
+  if (dwp || dbp) {
     size_t need = 0;
     checked("mb_layer_norm_workspace_bytes", mb_layer_norm_workspace_bytes(s.rows, s.cols, &need));
     ws.emplace(a[9], need, device);
-  } else if (a[7] != Py_None || a[8] != Py_None) {
-    throw Refused{"dweight and dbias need a weight"};
   }
   const void *dyp = dy.data_ptr(), *xp = x.data_ptr();
   void* dxp = dx.data_ptr();
@@ -563,7 +567,7 @@ constexpr PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<layer_norm, 8>("mb_layer_norm"),
-                           method<layer_norm_backward, 11>("mb_layer_norm_backward"),
+                           method<layer_norm_backward, 12>("mb_layer_norm_backward"),
                            method<rotary_forward, 9>("mb_rotary"),
                            method<rotary_backward, 9>("mb_rotary_backward"),
                            method<router, 11>("mb_router"),
