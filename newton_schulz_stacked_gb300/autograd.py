@@ -95,7 +95,11 @@ class _Rotary(torch.autograd.Function):
 
 
 def rotary(q, k, positions, inv_freq, sections: Sequence[int], interleaved: bool = False):
-    """mb_rotary, differentiable in q and k (k may be None): (q_out, k_out)."""
+    """mb_rotary, differentiable in q and k (k may be None): (q_out, k_out).  positions and inv_freq have no
+    gradient: one that requires it is refused."""
+    for name, t in (("positions", positions), ("inv_freq", inv_freq)):
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, which rotary does not have: pass {name}.detach()")
     return _Rotary.apply(q, k, positions, inv_freq, tuple(sections), interleaved, False)
 
 
