@@ -316,7 +316,7 @@ typedef struct {
 } mb_rotary_desc;
 
 /* Turns pair i of every head of q and k at each token by positions[its axis] * inv_freq[i]
- * (the product rounded to fp32):  u' = u cos - v sin,  v' = v cos + u sin.
+ * (position and product rounded to fp32):  u' = u cos - v sin,  v' = v cos + u sin.
  * mb_rotary_backward turns back by the same angles: the gradient with respect to the
  * source (src: dq or dk), and the inverse.  Limits (else MB_ERR_SHAPE): pairs 1..4096,
  * 2 pairs <= dim <= 65536, heads of q and k together 1..65536, batch * tokens < 2^31;
@@ -336,6 +336,8 @@ int mb_rotary_backward(const mb_rotary_desc* desc, void* cuda_stream);
  *       loss = experts / (top_k N^2) * sum_e counts[e] * sum_t p[t, e]
  *     (1 when perfectly balanced; 0 when no token counts).
  *   - NaN or +inf among a token's logits makes its p, its gates and the loss NaN.
+ *   - The softmax's exponentials and reciprocals are the hardware's approximations, each within
+ *     about 2^-22 of its value, and an exp(logit - largest) below 2^-126 counts as 0.
  * Results: index int32 and gate fp32 [tokens, top_k]; counts int32 [experts]; loss fp32
  * [1]; used int32 [1] = N.  Limits (else MB_ERR_SHAPE): experts 1..1024, top_k
  * 1..min(experts, 32), tokens * top_k < 2^31.  Few tokens need no workspace (0 bytes). */

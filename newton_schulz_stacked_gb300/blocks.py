@@ -8,7 +8,7 @@ allocation (mean and rstd; index and gate; counts, loss and used).  Every operat
 as a call of its own; autograd does not record these calls, but
 `newton_schulz_stacked_gb300.autograd` joins the pairs for it.
 
-Tensors may be strided in all but their last dimension; a tensor that is not laid out so, or
+Tensors may be strided in all but their last dimension (a norm's rows evenly spaced); a tensor that is not laid out so, or
 has another shape, type or device than the call's others, is refused with ValueError, and what
 the library refuses raises MuonBankError.  With `stream` (a torch stream or its handle), new
 tensors belong to that stream and the given ones are marked as used on it; the caller orders

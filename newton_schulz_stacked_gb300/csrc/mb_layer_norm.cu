@@ -428,7 +428,7 @@ cudaError_t fwd_any(const LnFwdParams& p, int sms, cudaStream_t s) {
       aligned(p.w) && aligned(p.b))
     return fwd<T, Access::VEC>(p, sms, s);
   // 2^26 elements in rows of 1001 take 102 us so and 146 by single elements (bf16; fp32 114 and 149), in
-  // rows of 2003 93 and 143 (110 and 147); in rows of 303 224 and 168 (195 and 178), of 3001 184 and 152
+  // rows of 2003 92 and 142 (109 and 146), of 777 126 and 177 (134 and 181); in rows of 303 224 and 168 (195 and 178), of 3001 184 and 152
   if (p.cols > 512 && p.cols + 14 <= 2048 && shiftable(p.x_stride, p.cols, p.rows) &&
       same_shift(p.x, p.x_stride, p.y, p.y_stride, SIZE, p.rows))
     return fwd<T, Access::SHIFT>(p, sms, s);

@@ -661,8 +661,8 @@ cudaError_t bwd_any(const LnBwdParams& p, int sms, cudaStream_t s, int* launches
     return vec ? bwd_wide<T, Access::VEC>(p, sms, s, launches) : bwd_wide<T, Access::SCALAR>(p, sms, s, launches);
   if (vec) return bwd<T, Access::VEC>(p, sms, s, launches);
   // not where a warp holds a row and reads 64 or 128 bytes at a time by single elements too: 2^26 bf16
-  // elements in rows of 777 take 115 us so and 90 by single ones; in rows of 201 148 and 318, of 2003
-  // 124 and 313 (fp32: 161 and 204, 154 and 212)
+  // elements in rows of 777 take 151 us so and 90 by single ones, of 303 188 and 115; in rows of 201 145 and
+  // 165, of 2003 123 and 313 (fp32: 169 and 127, 201 and 145; 165 and 190, 154 and 211)
   if ((p.cols + 14 <= 256 || p.cols > 1024) && p.cols + 14 <= LN_BWD_MAX_COLS && shiftable(p.x_stride, p.cols, p.rows) &&
       shiftable(p.dy_stride, p.cols, p.rows) && same_shift(p.x, p.x_stride, p.dy, p.dy_stride, SIZE, p.rows) &&
       same_shift(p.x, p.x_stride, p.dx, p.dx_stride, SIZE, p.rows))

@@ -25,6 +25,10 @@ constexpr unsigned FULL = 0xFFFFFFFFu;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float MINUS_INF = -__builtin_huge_valf();
 
+// The softmax takes these approximations in place of expf and a division: one instruction per element in a
+// kernel that instructions bound.  The results of a call are within 1.7e-7 of their size (with expf and a
+// division 5e-8 to 6e-8); exponentials below 2^-126 are 0, which against a sum of at least 1 changes none but
+// their own.
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
