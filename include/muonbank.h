@@ -269,7 +269,8 @@ enum {
   MB_BF16 = 1,
   MB_F16 = 2,
   MB_I32 = 3,   /* positions only */
-  MB_I64 = 4    /* positions only */
+  MB_I64 = 4,   /* positions only */
+  MB_E4M3 = 5   /* 8-bit moments only */
 };
 
 /* Layer norm of each row of x [rows, cols]:
@@ -357,6 +358,63 @@ int mb_router_backward(const float* dloss, const float* dgate, const void* logit
                        const int32_t* counts, const int32_t* used, void* dlogits,
                        int64_t dlogits_stride, void* cuda_stream);
 
+/* ---- AdamW over the tensors that are in no bank ----
+ *
+ * Embeddings, heads, norms, biases: what Muon does not take.  One launch steps a list of tensors of any sizes
+ * and types.  Per element, every operation rounded to fp32 on its own, in this order:
+ *   g = grad * grad_scale (if given)
+ *   m <- m b1 + g (1 - b1);   v <- v b2 + (g g) (1 - b2);   r = sqrt(v)
+ *   w <- w decay - (m / (r root + eps)) rate
+ * decay = 1 - (lr lr_mul) (wd wd_mul), rate = lr lr_mul / (1 - b1^step), root = 1 / sqrt(1 - b2^step): formed in
+ * double, rounded to fp32.  w is param widened to fp32, or, with a mantissa, the fp32 number whose high half is
+ * param (bf16) and whose low half is mantissa; a 16-bit param without one is rounded to the nearest.
+ *
+ * 8-bit moments (state_type MB_E4M3): exp_avg and exp_avg_sq hold e4m3 codes of m and of r; each block of 256
+ * consecutive elements (the last may be shorter) has an fp32 scale in avg_scale and sq_scale, and stands for
+ * m = code * avg_scale, v = (code * sq_scale)^2.  After a step a block's scale is the largest finite magnitude
+ * of its values / 448 (multiplied by 1/448 rounded to fp32), the codes are the values * (448 * (1 / magnitude)),
+ * and a magnitude below 2^-100 counts as 0.  The codes are rounded to the nearest (ties to even), or, with
+ * `stochastic`, at random: 16 random bits times 2^-16 of the code's step are added before the rest is dropped.  A
+ * positive r never becomes code 0; a value that is not finite becomes NaN.  All codes and scales zero is the
+ * state before the first step.  The random bits of element i of tensor number p of the call are those of
+ *   h(i + h(h(h(seed) + step) + p)), the low half for m, the high half for r, with
+ *   h(x):  x *= 0x9E3779B1;  x ^= x >> 16;  x *= 0x6A09E667;  x ^= x >> 15;  x *= 0xBB67AE85;  x ^= x >> 16
+ * modulo 2^32.
+ */
+typedef struct {
+  void* param;               /* [n], updated in place */
+  const void* grad;          /* [n] */
+  void* exp_avg;             /* [n] fp32 or e4m3, in place */
+  void* exp_avg_sq;          /* [n] likewise */
+  uint16_t* mantissa;        /* [n] low halves of a bf16 param, in place; or NULL */
+  float* avg_scale;          /* [ceil(n / 256)] with MB_E4M3, in place; else not read */
+  float* sq_scale;
+  int64_t n;                 /* 0 to 2^40 */
+  int32_t param_type, grad_type;   /* MB_F32, MB_BF16, MB_F16 */
+  int32_t state_type;        /* MB_F32 or MB_E4M3 */
+  float lr_mul, wd_mul;      /* this tensor's factors of lr and wd */
+} mb_adamw_tensor;
+
+#define MB_ADAMW_MAX_TENSORS 65536
+
+/* One step.  Pointers need their elements' alignment (16-byte aligned tensors move in 16-byte accesses); no tensor
+ * may overlap another of the call, but for gradients, which are only read.  step counts from 1.  grad_scale: fp32 [1]
+ * in device memory (a clipping factor, say), or NULL.  The array is read during the call only.  One launch per 320
+ * tensors and kind of moments.  MB_ERR_ARG: a type, a mantissa beside another param type than MB_BF16, lr, wd or
+ * eps not finite (or 1e30 and more), eps negative, beta1 or beta2 outside [0, 1), step outside 1..2^53. */
+int adamw_multi_step(const mb_adamw_tensor* tensors, int n_tensors, double lr, double wd, double beta1,
+                     double beta2, double eps, int64_t step, const float* grad_scale, int stochastic,
+                     uint32_t seed, void* cuda_stream);
+
+/* The same with {lr, wd, beta1, beta2, eps, step}, fp64 [6] in device memory, read when the step runs, so that a
+ * captured graph replays with new values; what cannot be a value latches MB_ERR_ARG for mb_sync_status and leaves
+ * the results undefined.  The same bits as the call by value, but for the last place of pow() in double.  The
+ * workspace (16-byte aligned) belongs to one call at a time. */
+int adamw_multi_step_dev_workspace_bytes(int n_tensors, size_t* out_bytes);
+int adamw_multi_step_dev(const mb_adamw_tensor* tensors, int n_tensors, const double* scalars_dev,
+                         const float* grad_scale, int stochastic, uint32_t seed, void* workspace,
+                         size_t workspace_bytes, void* cuda_stream);
+
 /* ---- measurement hooks ---- */
 
 /* Number of kernels this host thread has launched through the library so far. */
@@ -376,7 +434,8 @@ enum {
   MB_MARK_LAYER_NORM_BACKWARD = 9,
   MB_MARK_ROTARY = 10,    /* (either direction) */
   MB_MARK_ROUTER = 11,
-  MB_MARK_ROUTER_BACKWARD = 12
+  MB_MARK_ROUTER_BACKWARD = 12,
+  MB_MARK_ADAMW = 13      /* after an AdamW step's launches */
 };
 
 /* Starts recording a CUDA event on the launching stream at every stage

@@ -33,8 +33,9 @@ MB_NOALLOC_SCRATCH_BYTES = 32 << 20
 MB_MAX_BANKS = 8
 MB_STEP_FUSE_UPDATE = 1
 MB_STEP_FUSE_ROWSTATS = 2
-MB_F32, MB_BF16, MB_F16, MB_I32, MB_I64 = range(5)
+MB_F32, MB_BF16, MB_F16, MB_I32, MB_I64, MB_E4M3 = range(6)
 MB_ROTARY_MAX_AXES = 4
+MB_ADAMW_MAX_TENSORS = 65536
 
 
 class MbShape(ctypes.Structure):
@@ -59,7 +60,14 @@ class MbRotaryDesc(ctypes.Structure):
                 ("sections", ctypes.c_int32 * MB_ROTARY_MAX_AXES), ("inv_freq", c_void_p)]
 
 
+class MbAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "mantissa", "avg_scale", "sq_scale")] + [
+        ("n", c_int64), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32), ("state_type", ctypes.c_int32),
+        ("lr_mul", c_float), ("wd_mul", c_float)]
+
+
 _P = c_void_p
+_D = ctypes.c_double
 _SIGNATURES = {
     "mb_workspace_bytes": (c_int, [MbShape, c_int, ctypes.POINTER(c_size_t)]),
     "muon_bank_step": (c_int, [_P, _P, _P, _P, MbShape, c_float, c_float, c_float, c_int, _P, c_size_t, _P]),
@@ -91,6 +99,11 @@ _SIGNATURES = {
                           _P]),
     "mb_router_backward": (c_int, [_P, _P, _P, c_int64, c_int, _P, c_int64, c_int64, c_int, c_int, _P, _P, _P, _P, _P,
                                    c_int64, _P]),
+    "adamw_multi_step": (c_int, [ctypes.POINTER(MbAdamwTensor), c_int, _D, _D, _D, _D, _D, c_int64, _P, c_int,
+                                 ctypes.c_uint32, _P]),
+    "adamw_multi_step_dev_workspace_bytes": (c_int, [c_int, ctypes.POINTER(c_size_t)]),
+    "adamw_multi_step_dev": (c_int, [ctypes.POINTER(MbAdamwTensor), c_int, _P, _P, c_int, ctypes.c_uint32, _P, c_size_t,
+                                     _P]),
     "mb_sync_status": (c_int, [_P]),
     "mb_selftest_timeout": (c_int, [c_uint, _P]),
     "mb_status_string": (ctypes.c_char_p, [c_int]),
@@ -103,7 +116,7 @@ _SIGNATURES = {
 
 MARK_NAMES = {0: "begin", 1: "momentum", 2: "scale", 3: "small_ns", 4: "ns_gemm", 5: "ns0", 6: "rowstats",
               7: "update", 8: "layer_norm", 9: "layer_norm_backward", 10: "rotary", 11: "router",
-              12: "router_backward"}
+              12: "router_backward", 13: "adamw"}
 
 _lib = None
 

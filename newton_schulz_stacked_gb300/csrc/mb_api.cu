@@ -746,6 +746,13 @@ int api_device_sms(int* sms) {
   return MB_OK;
 }
 
+int api_device_status(int** status) {
+  DeviceState* ds = nullptr;
+  MB_TRY(device_state(&ds));
+  *status = ds->status;
+  return MB_OK;
+}
+
 void api_launched(int label, int launches, cudaStream_t stream) {
   g_launch_count += launches;
   mark(label, stream);

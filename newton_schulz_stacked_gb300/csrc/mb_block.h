@@ -12,6 +12,7 @@ namespace mb {
 
 int api_cuda_fail(cudaError_t e);    // keeps the message, returns MB_ERR_CUDA
 int api_device_sms(int* sms);        // checks the current device; its SM count
+int api_device_status(int** status); // checks the current device; its latched status word
 void api_launched(int label, int launches, cudaStream_t stream);   // counts launches and marks their end
 
 // ---------------------------------------------------------------- layer norm

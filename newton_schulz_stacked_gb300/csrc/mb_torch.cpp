@@ -14,8 +14,11 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <optional>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "muonbank.h"
 
@@ -535,6 +538,186 @@ PyObject* router_backward(PyObject* const* a, Py_ssize_t n) {
   return give(a[9], dl);
 }
 
+// ---------------------------------------------------------------- AdamW
+
+// The tensors of a call as descriptors, and the memory that it writes.
+struct AdamwList {
+  std::vector<mb_adamw_tensor> descs;
+  std::vector<Tensor> written;
+  std::vector<std::pair<uintptr_t, uintptr_t>> ranges;
+  Tensor first;
+  c10::Device device = c10::Device(c10::kCPU);
+
+  void* place(const Tensor& t, const std::string& what, int64_t n, ScalarType dtype, ScalarType also, bool write) {
+    if (t.scalar_type() != dtype && t.scalar_type() != also)
+      throw Refused{what + " has dtype " + c10::toString(t.scalar_type()) + ", expected " + c10::toString(dtype)};
+    if (t.numel() != n)
+      throw Refused{what + " has " + std::to_string(t.numel()) + " elements, expected " + std::to_string(n)};
+    if (t.device() != device) throw Refused{what + " is on " + t.device().str() + ", expected " + device.str()};
+    if (!t.is_contiguous()) throw Refused{what + " must be contiguous"};
+    void* p = t.data_ptr();
+    if (write && n > 0) {
+      written.push_back(t);
+      ranges.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + t.nbytes());
+    }
+    return p;
+  }
+
+  void add(PyObject* item, Py_ssize_t at, const char* names[7]) {
+    PyObject* seq = PySequence_Fast(item, "each tensor of the call is an AdamState");
+    if (!seq) throw Raised{};
+    try {
+      if (PySequence_Fast_GET_SIZE(seq) != 9) throw Refused{"each tensor of the call is an AdamState"};
+      PyObject** f = PySequence_Fast_ITEMS(seq);
+      auto name = [&](int i) { return std::string(names[i]) + " of tensor " + std::to_string(at); };
+      auto given = [&](int i) -> const Tensor* { return tensor_or_none(f[i], names[i]); };
+      mb_adamw_tensor d{};
+      const Tensor &param = cuda_tensor(f[0], names[0]), &grad = tensor(f[1], names[1]);
+      const Tensor &avg = tensor(f[2], names[2]), &sq = tensor(f[3], names[3]);
+      if (at == 0) {
+        first = param;
+        device = param.device();
+      }
+      d.n = param.numel();
+      d.param_type = type_of(param, names[0]);
+      d.grad_type = type_of(grad, names[1]);
+      const auto none = ScalarType::Undefined;
+      d.param = place(param, name(0), d.n, param.scalar_type(), none, true);
+      if (grad.sizes() != param.sizes())
+        throw Refused{name(1) + " is " + str(grad) + ", its parameter " + str(param)};
+      d.grad = place(grad, name(1), d.n, grad.scalar_type(), none, false);
+      const bool eight = avg.scalar_type() == ScalarType::Float8_e4m3fn;
+      const auto state = eight ? ScalarType::Float8_e4m3fn : ScalarType::Float;
+      d.state_type = eight ? MB_E4M3 : MB_F32;
+      d.exp_avg = place(avg, name(2), d.n, state, none, true);
+      d.exp_avg_sq = place(sq, name(3), d.n, state, none, true);
+      if (const Tensor* low = given(4)) {
+        if (param.scalar_type() != ScalarType::BFloat16) throw Refused{name(4) + " needs a bfloat16 parameter"};
+        d.mantissa = static_cast<uint16_t*>(place(*low, name(4), d.n, ScalarType::Short, ScalarType::UInt16, true));
+      }
+      for (int i = 5; i < 7; ++i) {
+        const Tensor* scale = given(i);
+        if (eight != (scale != nullptr))
+          throw Refused{name(i) + (eight ? " is missing: 8-bit moments need it" : " is for 8-bit moments only")};
+        if (eight)
+          (i == 5 ? d.avg_scale : d.sq_scale) =
+              static_cast<float*>(place(*scale, name(i), (d.n + 255) / 256, ScalarType::Float, none, true));
+      }
+      d.lr_mul = number(f[7]);
+      d.wd_mul = number(f[8]);
+      descs.push_back(d);
+    } catch (...) {
+      Py_DECREF(seq);
+      throw;
+    }
+    Py_DECREF(seq);
+  }
+
+  explicit AdamwList(PyObject* list) {
+    static const char* names[7] = {"param", "grad", "exp_avg", "exp_avg_sq", "mantissa", "avg_scale", "sq_scale"};
+    PyObject* seq = PySequence_Fast(list, "tensors must be a sequence of AdamState");
+    if (!seq) throw Raised{};
+    try {
+      const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+      if (n == 0) throw Refused{"no tensors"};
+      if (n > MB_ADAMW_MAX_TENSORS) checked("adamw_multi_step", MB_ERR_TOO_MANY);
+      descs.reserve(n);
+      for (Py_ssize_t i = 0; i < n; ++i) add(PySequence_Fast_GET_ITEM(seq, i), i, names);
+    } catch (...) {
+      Py_DECREF(seq);
+      throw;
+    }
+    Py_DECREF(seq);
+    // a tensor that is given twice would be stepped by two CTAs at once
+    std::sort(ranges.begin(), ranges.end());
+    for (size_t i = 1; i < ranges.size(); ++i)
+      if (ranges[i].first < ranges[i - 1].second) throw Refused{"tensors of the call that it writes overlap"};
+  }
+
+  void stepped() const {
+    for (const Tensor& t : written)
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+};
+
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+// Marks the list's tensors as used on the stream that the call was given.
+void record(const AdamwList& list, PyObject* tensors, const Where& where, PyObject* given) {
+  if (given == Py_None) return;
+  const auto s = c10::cuda::getStreamFromExternal(where.stream, list.device.index());
+  PyObject* seq = PySequence_Fast(tensors, "");
+  if (!seq) throw Raised{};
+  for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(seq); ++i) {
+    PyObject* item = PySequence_Fast(PySequence_Fast_GET_ITEM(seq, i), "");
+    if (!item) {
+      Py_DECREF(seq);
+      throw Raised{};
+    }
+    for (Py_ssize_t j = 0; j < PySequence_Fast_GET_SIZE(item); ++j) {
+      PyObject* t = PySequence_Fast_GET_ITEM(item, j);
+      if (THPVariable_Check(t) && THPVariable_Unpack(t).is_cuda()) THPVariable_Unpack(t).record_stream(s.unwrap());
+    }
+    Py_DECREF(item);
+  }
+  Py_DECREF(seq);
+}
+
+// The seed of stochastic rounding (None: to the nearest).
+uint32_t seed_of(PyObject* o, int* stochastic) {
+  *stochastic = o != Py_None;
+  if (!*stochastic) return 0;
+  const long long v = integer(o, "seed");
+  if (v < 0 || v >= (1ll << 32)) throw Refused{"seed is out of range: 0 to 2^32 - 1"};
+  return static_cast<uint32_t>(v);
+}
+
+// tensors, lr, wd, beta1, beta2, eps, step, grad_scale, seed, stream
+PyObject* adamw(PyObject* const* a, Py_ssize_t n) {
+  const AdamwList list(a[0]);
+  Where where(list.first, a[9], a, n);
+  record(list, a[0], where, a[9]);
+  const double lr = real(a[1]), wd = real(a[2]), beta1 = real(a[3]), beta2 = real(a[4]), eps = real(a[5]);
+  const long long step = integer(a[6], "step");
+  const auto* scale =
+      static_cast<const float*>(dense(tensor_or_none(a[7], "grad_scale"), "grad_scale", {1}, ScalarType::Float, list.device));
+  int stochastic = 0;
+  const uint32_t seed = seed_of(a[8], &stochastic);
+  checked("adamw_multi_step", unlocked([&] {
+            return adamw_multi_step(list.descs.data(), static_cast<int>(list.descs.size()), lr, wd, beta1, beta2, eps, step,
+                                    scale, stochastic, seed, where.stream);
+          }));
+  list.stepped();
+  Py_RETURN_NONE;
+}
+
+// tensors, scalars, grad_scale, seed, workspace, stream
+PyObject* adamw_dev(PyObject* const* a, Py_ssize_t n) {
+  const AdamwList list(a[0]);
+  Where where(list.first, a[5], a, n);
+  record(list, a[0], where, a[5]);
+  const auto* scalars =
+      static_cast<const double*>(dense(&tensor(a[1], "scalars"), "scalars", {6}, ScalarType::Double, list.device));
+  const auto* scale =
+      static_cast<const float*>(dense(tensor_or_none(a[2], "grad_scale"), "grad_scale", {1}, ScalarType::Float, list.device));
+  int stochastic = 0;
+  const uint32_t seed = seed_of(a[3], &stochastic);
+  const int count = static_cast<int>(list.descs.size());
+  size_t need = 0;
+  checked("adamw_multi_step_dev_workspace_bytes", adamw_multi_step_dev_workspace_bytes(count, &need));
+  const Workspace ws(a[4], need, list.device);
+  checked("adamw_multi_step_dev", unlocked([&] {
+            return adamw_multi_step_dev(list.descs.data(), count, scalars, scale, stochastic, seed, ws.ptr, ws.bytes,
+                                        where.stream);
+          }));
+  list.stepped();
+  return a[4] == Py_None ? wrap(ws.own) : Py_NewRef(a[4]);
+}
+
 // ---------------------------------------------------------------- the module
 
 PyObject* rotary_forward(PyObject* const* a, Py_ssize_t n) { return rotary<mb_rotary>(a, n, "mb_rotary"); }
@@ -572,6 +755,8 @@ PyMethodDef g_methods[] = {method<layer_norm, 8>("mb_layer_norm"),
                            method<rotary_backward, 9>("mb_rotary_backward"),
                            method<router, 11>("mb_router"),
                            method<router_backward, 11>("mb_router_backward"),
+                           method<adamw, 10>("adamw_multi_step"),
+                           method<adamw_dev, 6>("adamw_multi_step_dev"),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_blocks", "Native calls of the block operators.", -1, g_methods,
