@@ -50,7 +50,7 @@ struct AdamTensor {
 struct AdamScalars {
   float b1, c1, b2, c2, root, eps;
   uint32_t key;
-  uint32_t pad;
+  float minus_zero;
 };
 
 template <int CAP>
@@ -75,6 +75,28 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// Two fp32 operations in one instruction, each rounded on its own.  A product is a fused one with -0 as its summand, which
+// changes no value and comes from memory: packed products, explicit roundings or a constant -0 or not, were contracted
+// with the sums that follow them.
+__device__ __forceinline__ uint64_t bits_of(float2 v) {
+  return static_cast<uint64_t>(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 pair_of(uint64_t u) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(u)), __uint_as_float(static_cast<uint32_t>(u >> 32)));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b, float minus_zero) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(make_float2(minus_zero, minus_zero))));
+  return pair_of(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+  return pair_of(d);
+}
+
 // ---------------------------------------------------------------- a lane's eight elements, of a type known at run time
 
 struct Raw {
@@ -93,26 +115,13 @@ __device__ __forceinline__ Raw load_eight(const void* p, long long at, int type)
   return r;
 }
 
-__device__ __forceinline__ void widen(const Raw& r, int type, float (&v)[8]) {
+__device__ __forceinline__ void widen(const Raw& r, int type, float2 (&v)[4]) {
   const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-  if (type == MB_F32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
-  } else if (type == MB_BF16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2(u[i], __nv_bfloat16());
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2(u[i], __half());
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    v[i] = type == MB_F32    ? make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))
+           : type == MB_BF16 ? unpack2(u[i], __nv_bfloat16())
+                             : unpack2(u[i], __half());
 }
 
 __device__ __forceinline__ float load_one(const void* p, long long at, int type) {
@@ -127,21 +136,17 @@ __device__ __forceinline__ void store_one(void* p, long long at, int type, float
   else static_cast<__half*>(p)[at] = from_float<__half>(v);
 }
 
-__device__ __forceinline__ void store_eight(void* p, long long at, int type, const float (&v)[8]) {
+__device__ __forceinline__ void store_eight(void* p, long long at, int type, const float2 (&v)[4]) {
   if (type == MB_F32) {
-    uint4* q = reinterpret_cast<uint4*>(static_cast<float*>(p) + at);
-    q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-    q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     return;
   }
   uint32_t u[4];
-  if (type == MB_BF16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = pack2(v[2 * i], v[2 * i + 1], __nv_bfloat16());
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = pack2(v[2 * i], v[2 * i + 1], __half());
-  }
+  for (int i = 0; i < 4; ++i)
+    u[i] = type == MB_BF16 ? pack2(v[i].x, v[i].y, __nv_bfloat16()) : pack2(v[i].x, v[i].y, __half());
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
@@ -152,19 +157,29 @@ __device__ __forceinline__ float2 widen_codes(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-__device__ __forceinline__ uint32_t codes_of(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
+__device__ __forceinline__ uint32_t codes_of(float2 v) { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3); }
 
-// The largest magnitude of the warp's finite values.  The bits of non-negative floats are ordered as their values are.
-__device__ __forceinline__ float block_size(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The largest magnitude of the warp's finite values.  The bits of non-negative floats are ordered as their values are, and
+// those of infinities and NaN are above: only a warp that has one of them looks at each.
+__device__ __forceinline__ float block_size(const float2 (&v)[4], bool& all_finite) {
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-    top = max(top, a < 0x7F800000u ? a : 0u);
+  for (int j = 0; j < 4; ++j) top = max(top, max(magnitude(v[j].x), magnitude(v[j].y)));
+  top = __reduce_max_sync(0xffffffffu, top);
+  all_finite = top < 0x7F800000u;
+  if (!all_finite) {
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t a = magnitude(j & 1 ? v[j / 2].y : v[j / 2].x);
+      top = max(top, a < 0x7F800000u ? a : 0u);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
   }
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  return __uint_as_float(top);
 }
 
 // The e4m3 number that q becomes with 16 random bits: a step of the number's exponent (20 dropped mantissa bits) times
@@ -179,196 +194,241 @@ __device__ __forceinline__ float round_at_random(float q, uint32_t bits16) {
   return isnan(q) ? q : copysignf(a, q);
 }
 
-// A block's values over its scale, as e4m3 numbers still in fp32; a value that is not finite becomes NaN, alone.  Returns
-// the scale.
+// A block's values over its scale, as e4m3 numbers still in fp32 (rounded where `random`, else by codes_of); a value that is
+// not finite becomes NaN, alone.  Returns the scale.
 template <bool ROOT>
-__device__ __forceinline__ float scale_block(const float (&v)[8], float (&q)[8], bool random, const uint32_t (&bits)[8]) {
-  const float size = block_size(v);
+__device__ __forceinline__ float scale_block(const float2 (&v)[4], float2 (&q)[4], bool random, const uint32_t (&bits)[8]) {
+  bool all_finite;
+  const float size = block_size(v, all_finite);
   const bool some = size >= LEAST_SCALED;
   const float inv = some ? __fmul_rn(__frcp_rn(size), TOP) : 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float x = __fmul_rn(v[j], inv);
-    x = fabsf(x) < 480.f ? x : __uint_as_float(0x7FC00000u);
-    if (random) x = round_at_random(x, ROOT ? bits[j] >> 16 : bits[j] & 0xFFFFu);
-    if (ROOT && some && v[j] > 0.f) x = x < 0x1p-9f ? 0x1p-9f : x;
-    q[j] = x;
+  for (int j = 0; j < 4; ++j) q[j] = make_float2(__fmul_rn(v[j].x, inv), __fmul_rn(v[j].y, inv));
+  if (!all_finite) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[j].x = fabsf(q[j].x) < 480.f ? q[j].x : __uint_as_float(0x7FC00000u);
+      q[j].y = fabsf(q[j].y) < 480.f ? q[j].y : __uint_as_float(0x7FC00000u);
+    }
+  }
+  if (random) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[j].x = round_at_random(q[j].x, ROOT ? bits[2 * j] >> 16 : bits[2 * j] & 0xFFFFu);
+      q[j].y = round_at_random(q[j].y, ROOT ? bits[2 * j + 1] >> 16 : bits[2 * j + 1] & 0xFFFFu);
+    }
+  }
+  if (ROOT && some) {
+    // (roots are never negative) the least code for what is positive below it: rare, so the lane's least is looked at first
+    float least = TOP;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) least = fminf(least, fminf(q[j].x, q[j].y));
+    if (least < 0x1p-9f) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        q[j].x = v[j].x > 0.f && q[j].x < 0x1p-9f ? 0x1p-9f : q[j].x;
+        q[j].y = v[j].y > 0.f && q[j].y < 0x1p-9f ? 0x1p-9f : q[j].y;
+      }
+    }
   }
   return some ? __fmul_rn(size, 1.f / TOP) : 0.f;
 }
 
 // ---------------------------------------------------------------- the step
 
-__device__ __forceinline__ float step_one(float g, float& m, float& v, float& r, float w, const AdamScalars& s, float decay,
-                                          float rate) {
-  m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(g, s.c1));
-  v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(g, g), s.c2));
-  r = __fsqrt_rn(v);
-  const float d = __fadd_rn(__fmul_rn(r, s.root), s.eps);
-  return __fsub_rn(__fmul_rn(w, decay), __fmul_rn(__fdiv_rn(m, d), rate));
+// A lane's eight elements: as pairs, the operations two at a time.
+struct Lane {
+  float2 g[4], w[4], m[4], v[4], r[4];
+};
+
+// The step of eight elements.  EIGHT: v comes as its root r.
+template <bool EIGHT>
+__device__ __forceinline__ void step_eight(Lane& e, const AdamScalars& s, float decay, float rate, const float* grad_scale) {
+  const float z = s.minus_zero;
+  if (grad_scale) {
+    const float2 gs = both(*grad_scale);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e.g[j] = mul2(e.g[j], gs, z);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (EIGHT) e.v[j] = mul2(e.r[j], e.r[j], z);
+    e.m[j] = add2(mul2(e.m[j], both(s.b1), z), mul2(e.g[j], both(s.c1), z));
+    e.v[j] = add2(mul2(e.v[j], both(s.b2), z), mul2(mul2(e.g[j], e.g[j], z), both(s.c2), z));
+    e.r[j] = make_float2(__fsqrt_rn(e.v[j].x), __fsqrt_rn(e.v[j].y));
+    const float2 d = add2(mul2(e.r[j], both(s.root), z), both(s.eps));
+    const float2 q = make_float2(__fdiv_rn(e.m[j].x, d.x), __fdiv_rn(e.m[j].y, d.y));
+    e.w[j] = add2(mul2(e.w[j], both(decay), z), mul2(q, both(-rate), z));
+  }
 }
 
-// One block of 256 elements from `at` on, by one warp.  VEC: eight neighbouring elements to a lane in 16-byte accesses
-// (8-byte ones of codes); else every 32nd element, what lies past the end as zeros.
-template <bool EIGHT, bool VEC>
-__device__ __forceinline__ void step_block(const AdamTensor& T, const AdamScalars& s, float decay, float rate,
-                                           const float* grad_scale, bool random, long long at, int lane) {
-  const int pt = T.param_type, gt = T.grad_type;
-  float g[8], w[8], m[8], v[8], r[8];
-  long long where[8];
-  bool in[8];
+// The moments of a whole block as codes still in fp32 (m, v), their scales stored.  where: the lane's elements.
+__device__ __forceinline__ void pack_moments(Lane& e, const AdamTensor& T, uint32_t key, bool random, long long at, int lane,
+                                             uint32_t first, uint32_t apart) {
+  uint32_t bits[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    where[j] = VEC ? at + 8 * lane + j : at + 32 * j + lane;
-    in[j] = VEC || where[j] < T.n;
+  for (int j = 0; j < 8; ++j) bits[j] = 0;
+  if (random) {
+    const uint32_t k = mix(key + static_cast<uint32_t>(T.position)) + first;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bits[j] = mix(k + apart * j);
   }
-  if constexpr (VEC) {
+  float2 q[4];
+  const float ms = scale_block<false>(e.m, q, random, bits);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e.m[j] = q[j];
+  const float vs = scale_block<true>(e.r, q, random, bits);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e.v[j] = q[j];
+  if (lane == 0) {
+    T.avg_scale[at / BLOCK] = ms;
+    T.sq_scale[at / BLOCK] = vs;
+  }
+}
+
+// What a lane loads of a whole aligned block: eight neighbouring elements in 16-byte accesses (8-byte ones of codes), held
+// as they come, so that the next block's can be on their way under this block's arithmetic.
+template <bool EIGHT>
+struct Loaded {
+  Raw g, p;
+  uint4 low;
+  Raw m, v;
+  uint2 mc, vc;
+  float ms, vs;
+  __device__ __forceinline__ void load(const AdamTensor& T, long long at, int lane) {
     const long long first = at + 8 * lane;
-    const Raw gr = load_eight(T.grad, first, gt), pr = load_eight(T.param, first, pt);
-    uint4 low = make_uint4(0, 0, 0, 0);
+    g = load_eight(T.grad, first, T.grad_type);
+    p = load_eight(T.param, first, T.param_type);
     if (T.mantissa) low = *reinterpret_cast<const uint4*>(T.mantissa + first);
     if constexpr (EIGHT) {
-      const uint2 mc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.avg) + first);
-      const uint2 vc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.sq) + first);
-      const float ms = T.avg_scale[at / BLOCK], vs = T.sq_scale[at / BLOCK];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 a = widen_codes((j < 2 ? mc.x : mc.y) >> (16 * (j & 1)) & 0xFFFFu);
-        const float2 b = widen_codes((j < 2 ? vc.x : vc.y) >> (16 * (j & 1)) & 0xFFFFu);
-        m[2 * j] = __fmul_rn(a.x, ms);
-        m[2 * j + 1] = __fmul_rn(a.y, ms);
-        r[2 * j] = __fmul_rn(b.x, vs);
-        r[2 * j + 1] = __fmul_rn(b.y, vs);
-      }
+      mc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.avg) + first);
+      vc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.sq) + first);
+      ms = T.avg_scale[at / BLOCK];
+      vs = T.sq_scale[at / BLOCK];
     } else {
-      const Raw mr = load_eight(T.avg, first, MB_F32), vr = load_eight(T.sq, first, MB_F32);
-      widen(mr, MB_F32, m);
-      widen(vr, MB_F32, v);
+      m = load_eight(T.avg, first, MB_F32);
+      v = load_eight(T.sq, first, MB_F32);
     }
-    widen(gr, gt, g);
-    widen(pr, pt, w);
+  }
+  __device__ __forceinline__ void get(const AdamTensor& T, Lane& e, float z) const {
+    widen(g, T.grad_type, e.g);
+    widen(p, T.param_type, e.w);
     if (T.mantissa) {
       const uint32_t l[4] = {low.x, low.y, low.z, low.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        w[2 * j] = __uint_as_float(__float_as_uint(w[2 * j]) | (l[j] & 0xFFFFu));
-        w[2 * j + 1] = __uint_as_float(__float_as_uint(w[2 * j + 1]) | (l[j] >> 16));
+        e.w[j].x = __uint_as_float(__float_as_uint(e.w[j].x) | (l[j] & 0xFFFFu));
+        e.w[j].y = __uint_as_float(__float_as_uint(e.w[j].y) | (l[j] >> 16));
       }
     }
-  } else {
-    float ms = 0.f, vs = 0.f;
     if constexpr (EIGHT) {
-      ms = T.avg_scale[at / BLOCK];
-      vs = T.sq_scale[at / BLOCK];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      g[j] = w[j] = m[j] = v[j] = r[j] = 0.f;
-      if (!in[j]) continue;
-      g[j] = load_one(T.grad, where[j], gt);
-      // a bf16 weight with a low half is taken by its bits
-      w[j] = T.mantissa ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(T.param)[where[j]]) << 16 |
-                                          T.mantissa[where[j]])
-                        : load_one(T.param, where[j], pt);
-      if constexpr (EIGHT) {
-        m[j] = __fmul_rn(widen_codes(static_cast<const uint8_t*>(T.avg)[where[j]]).x, ms);
-        r[j] = __fmul_rn(widen_codes(static_cast<const uint8_t*>(T.sq)[where[j]]).x, vs);
-      } else {
-        m[j] = static_cast<const float*>(T.avg)[where[j]];
-        v[j] = static_cast<const float*>(T.sq)[where[j]];
-      }
-    }
-  }
-  if constexpr (EIGHT) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(r[j], r[j]);
-  }
-  if (grad_scale) {
-    const float gs = *grad_scale;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], gs);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = step_one(g[j], m[j], v[j], r[j], w[j], s, decay, rate);
-  float ms = 0.f, vs = 0.f;
-  if constexpr (EIGHT) {
-    // past the end there is nothing whose size would count
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = in[j] ? m[j] : 0.f;
-      r[j] = in[j] ? r[j] : 0.f;
-    }
-    uint32_t bits[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bits[j] = 0;
-    if (random) {
-      const uint32_t key = mix(s.key + static_cast<uint32_t>(T.position));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) bits[j] = mix(static_cast<uint32_t>(where[j]) + key);
-    }
-    float q[8];
-    ms = scale_block<false>(m, q, random, bits);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m[j] = q[j];
-    vs = scale_block<true>(r, q, random, bits);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = q[j];
-    if (lane == 0) {
-      T.avg_scale[at / BLOCK] = ms;
-      T.sq_scale[at / BLOCK] = vs;
-    }
-  }
-  if constexpr (VEC) {
-    const long long first = at + 8 * lane;
-    if (T.mantissa) {
-      uint32_t hi[4], lo[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t a = __float_as_uint(w[2 * j]), b = __float_as_uint(w[2 * j + 1]);
-        hi[j] = __byte_perm(a, b, 0x7632);
-        lo[j] = __byte_perm(a, b, 0x5410);
+        e.m[j] = mul2(widen_codes((j < 2 ? mc.x : mc.y) >> (16 * (j & 1)) & 0xFFFFu), both(ms), z);
+        e.r[j] = mul2(widen_codes((j < 2 ? vc.x : vc.y) >> (16 * (j & 1)) & 0xFFFFu), both(vs), z);
       }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(T.param) + first) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(T.mantissa + first) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     } else {
-      store_eight(T.param, first, pt, w);
+      widen(m, MB_F32, e.m);
+      widen(v, MB_F32, e.v);
+    }
+  }
+};
+
+template <bool EIGHT>
+__device__ __forceinline__ void store_block(const Lane& e, const AdamTensor& T, long long at, int lane) {
+  const long long first = at + 8 * lane;
+  if (T.mantissa) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = __float_as_uint(e.w[j].x), b = __float_as_uint(e.w[j].y);
+      hi[j] = __byte_perm(a, b, 0x7632);
+      lo[j] = __byte_perm(a, b, 0x5410);
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(T.param) + first) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(T.mantissa + first) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  } else {
+    store_eight(T.param, first, T.param_type, e.w);
+  }
+  if constexpr (EIGHT) {
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.avg) + first) =
+        make_uint2(codes_of(e.m[0]) | codes_of(e.m[1]) << 16, codes_of(e.m[2]) | codes_of(e.m[3]) << 16);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.sq) + first) =
+        make_uint2(codes_of(e.v[0]) | codes_of(e.v[1]) << 16, codes_of(e.v[2]) | codes_of(e.v[3]) << 16);
+  } else {
+    store_eight(T.avg, first, MB_F32, e.m);
+    store_eight(T.sq, first, MB_F32, e.v);
+  }
+}
+
+// A block of a tensor that is not aligned, or a tensor's last: a lane has every 32nd element, zeros past the end.
+template <bool EIGHT>
+__device__ __forceinline__ void step_single(const AdamTensor& T, const AdamScalars& s, float decay, float rate,
+                                            const float* grad_scale, bool random, long long at, int lane) {
+  const long long first = at + lane;
+  Lane e;
+  float* const eg = &e.g[0].x;
+  float* const ew = &e.w[0].x;
+  float* const em = &e.m[0].x;
+  float* const ev = &e.v[0].x;
+  float* const er = &e.r[0].x;
+  float ms = 0.f, vs = 0.f;
+  if constexpr (EIGHT) {
+    ms = T.avg_scale[at / BLOCK];
+    vs = T.sq_scale[at / BLOCK];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const long long i = first + 32 * j;
+    eg[j] = ew[j] = em[j] = ev[j] = er[j] = 0.f;
+    if (i >= T.n) continue;
+    eg[j] = load_one(T.grad, i, T.grad_type);
+    // a bf16 weight with a low half is taken by its bits
+    ew[j] = T.mantissa
+                ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(T.param)[i]) << 16 | T.mantissa[i])
+                : load_one(T.param, i, T.param_type);
+    if constexpr (EIGHT) {
+      em[j] = __fmul_rn(widen_codes(static_cast<const uint8_t*>(T.avg)[i]).x, ms);
+      er[j] = __fmul_rn(widen_codes(static_cast<const uint8_t*>(T.sq)[i]).x, vs);
+    } else {
+      em[j] = static_cast<const float*>(T.avg)[i];
+      ev[j] = static_cast<const float*>(T.sq)[i];
+    }
+  }
+  step_eight<EIGHT>(e, s, decay, rate, grad_scale);
+  if constexpr (EIGHT) {
+    // past the end there is nothing whose size would count (NaN, where grad_scale is one)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (first + 32 * j >= T.n) em[j] = er[j] = 0.f;
+    pack_moments(e, T, s.key, random, at, lane, static_cast<uint32_t>(first), 32u);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const long long i = first + 32 * j;
+    if (i >= T.n) continue;
+    if (T.mantissa) {
+      static_cast<uint16_t*>(T.param)[i] = static_cast<uint16_t>(__float_as_uint(ew[j]) >> 16);
+      T.mantissa[i] = static_cast<uint16_t>(__float_as_uint(ew[j]));
+    } else {
+      store_one(T.param, i, T.param_type, ew[j]);
     }
     if constexpr (EIGHT) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.avg) + first) =
-          make_uint2(codes_of(m[0], m[1]) | codes_of(m[2], m[3]) << 16, codes_of(m[4], m[5]) | codes_of(m[6], m[7]) << 16);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.sq) + first) =
-          make_uint2(codes_of(v[0], v[1]) | codes_of(v[2], v[3]) << 16, codes_of(v[4], v[5]) | codes_of(v[6], v[7]) << 16);
+      static_cast<uint8_t*>(T.avg)[i] = static_cast<uint8_t>(codes_of(make_float2(em[j], 0.f)));
+      static_cast<uint8_t*>(T.sq)[i] = static_cast<uint8_t>(codes_of(make_float2(ev[j], 0.f)));
     } else {
-      store_eight(T.avg, first, MB_F32, m);
-      store_eight(T.sq, first, MB_F32, v);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!in[j]) continue;
-      if (T.mantissa) {
-        static_cast<uint16_t*>(T.param)[where[j]] = static_cast<uint16_t>(__float_as_uint(w[j]) >> 16);
-        T.mantissa[where[j]] = static_cast<uint16_t>(__float_as_uint(w[j]));
-      } else {
-        store_one(T.param, where[j], pt, w[j]);
-      }
-      if constexpr (EIGHT) {
-        static_cast<uint8_t*>(T.avg)[where[j]] = static_cast<uint8_t>(codes_of(m[j], 0.f));
-        static_cast<uint8_t*>(T.sq)[where[j]] = static_cast<uint8_t>(codes_of(v[j], 0.f));
-      } else {
-        static_cast<float*>(T.avg)[where[j]] = m[j];
-        static_cast<float*>(T.sq)[where[j]] = v[j];
-      }
+      static_cast<float*>(T.avg)[i] = em[j];
+      static_cast<float*>(T.sq)[i] = ev[j];
     }
   }
 }
 
-// Blocks of 256 elements that a warp takes in turn.
-constexpr int TURNS = 2;
+// Blocks of 256 elements that a warp takes in turn, the next one's loads under this one's arithmetic.
+constexpr int TURNS = 4;
 constexpr int CHUNK = WARPS * TURNS * BLOCK;
 
 template <int CAP, bool EIGHT>
-__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ AdamParams<CAP> p) {
+__global__ void __launch_bounds__(THREADS, 3) adamw_kernel(const __grid_constant__ AdamParams<CAP> p) {
   begin_after_previous();
   int i = 0, end = p.count;
   while (end - i > 1) {
@@ -385,14 +445,21 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
     rate = each[1];
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long begin = static_cast<long long>(blockIdx.x - T.first) * CHUNK + warp * BLOCK;
-#pragma unroll
-  for (int u = 0; u < TURNS; ++u) {
-    const long long at = begin + u * (WARPS * BLOCK);
-    if (at >= T.n) return;
-    if (T.aligned && at + BLOCK <= T.n) step_block<EIGHT, true>(T, s, decay, rate, p.grad_scale, p.random, at, lane);
-    else step_block<EIGHT, false>(T, s, decay, rate, p.grad_scale, p.random, at, lane);
+  long long at = static_cast<long long>(blockIdx.x - T.first) * CHUNK + warp * BLOCK;
+  const long long stop = min(static_cast<long long>(blockIdx.x - T.first + 1) * CHUNK, T.n);
+  if (T.aligned) {
+    Loaded<EIGHT> next;
+    if (at + BLOCK <= stop) next.load(T, at, lane);
+    for (; at + BLOCK <= stop; at += WARPS * BLOCK) {
+      Lane e;
+      next.get(T, e, s.minus_zero);
+      if (at + (WARPS + 1) * BLOCK <= stop) next.load(T, at + WARPS * BLOCK, lane);
+      step_eight<EIGHT>(e, s, decay, rate, p.grad_scale);
+      if constexpr (EIGHT) pack_moments(e, T, s.key, p.random, at, lane, static_cast<uint32_t>(at) + 8 * lane, 1u);
+      store_block<EIGHT>(e, T, at, lane);
+    }
   }
+  for (; at < stop; at += WARPS * BLOCK) step_single<EIGHT>(T, s, decay, rate, p.grad_scale, p.random, at, lane);
 }
 
 // ---------------------------------------------------------------- scalars
@@ -420,6 +487,7 @@ __host__ __device__ inline Derived derive(double beta1, double beta2, double eps
   d.s.c2 = static_cast<float>(1.0 - beta2);
   d.s.root = static_cast<float>(1.0 / sqrt(1.0 - pow(beta2, step)));
   d.s.eps = static_cast<float>(eps);
+  d.s.minus_zero = -0.f;
   d.s.key = mix(mix(seed) + static_cast<uint32_t>(static_cast<unsigned long long>(step)));
   d.rate_per_lr = 1.0 - pow(beta1, step);
   return d;

@@ -540,103 +540,133 @@ PyObject* router_backward(PyObject* const* a, Py_ssize_t n) {
 
 // ---------------------------------------------------------------- AdamW
 
-// The tensors of a call as descriptors, and the memory that it writes.
+// The tensors of a call as descriptors, and the ones that it writes.
 struct AdamwList {
+  static constexpr const char* NAMES[7] = {"param", "grad", "exp_avg", "exp_avg_sq", "mantissa", "avg_scale", "sq_scale"};
   std::vector<mb_adamw_tensor> descs;
-  std::vector<Tensor> written;
-  std::vector<std::pair<uintptr_t, uintptr_t>> ranges;
+  std::vector<const Tensor*> written;      // held by the call's list, which `seq` and `items` hold
+  std::vector<PyObject*> held;
   Tensor first;
   c10::Device device = c10::Device(c10::kCPU);
 
-  void* place(const Tensor& t, const std::string& what, int64_t n, ScalarType dtype, ScalarType also, bool write) {
+  static std::string name(int field, Py_ssize_t at) { return std::string(NAMES[field]) + " of tensor " + std::to_string(at); }
+
+  void* place(const Tensor& t, int field, Py_ssize_t at, int64_t n, ScalarType dtype, ScalarType also) {
     if (t.scalar_type() != dtype && t.scalar_type() != also)
-      throw Refused{what + " has dtype " + c10::toString(t.scalar_type()) + ", expected " + c10::toString(dtype)};
+      throw Refused{name(field, at) + " has dtype " + c10::toString(t.scalar_type()) + ", expected " + c10::toString(dtype)};
     if (t.numel() != n)
-      throw Refused{what + " has " + std::to_string(t.numel()) + " elements, expected " + std::to_string(n)};
-    if (t.device() != device) throw Refused{what + " is on " + t.device().str() + ", expected " + device.str()};
-    if (!t.is_contiguous()) throw Refused{what + " must be contiguous"};
-    void* p = t.data_ptr();
-    if (write && n > 0) {
-      written.push_back(t);
-      ranges.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + t.nbytes());
-    }
-    return p;
+      throw Refused{name(field, at) + " has " + std::to_string(t.numel()) + " elements, expected " + std::to_string(n)};
+    if (t.device() != device) throw Refused{name(field, at) + " is on " + t.device().str() + ", expected " + device.str()};
+    if (!t.is_contiguous()) throw Refused{name(field, at) + " must be contiguous"};
+    if (field != 1) written.push_back(&t);
+    return t.data_ptr();
   }
 
-  void add(PyObject* item, Py_ssize_t at, const char* names[7]) {
-    PyObject* seq = PySequence_Fast(item, "each tensor of the call is an AdamState");
-    if (!seq) throw Raised{};
-    try {
-      if (PySequence_Fast_GET_SIZE(seq) != 9) throw Refused{"each tensor of the call is an AdamState"};
-      PyObject** f = PySequence_Fast_ITEMS(seq);
-      auto name = [&](int i) { return std::string(names[i]) + " of tensor " + std::to_string(at); };
-      auto given = [&](int i) -> const Tensor* { return tensor_or_none(f[i], names[i]); };
-      mb_adamw_tensor d{};
-      const Tensor &param = cuda_tensor(f[0], names[0]), &grad = tensor(f[1], names[1]);
-      const Tensor &avg = tensor(f[2], names[2]), &sq = tensor(f[3], names[3]);
-      if (at == 0) {
-        first = param;
-        device = param.device();
-      }
-      d.n = param.numel();
-      d.param_type = type_of(param, names[0]);
-      d.grad_type = type_of(grad, names[1]);
-      const auto none = ScalarType::Undefined;
-      d.param = place(param, name(0), d.n, param.scalar_type(), none, true);
-      if (grad.sizes() != param.sizes())
-        throw Refused{name(1) + " is " + str(grad) + ", its parameter " + str(param)};
-      d.grad = place(grad, name(1), d.n, grad.scalar_type(), none, false);
-      const bool eight = avg.scalar_type() == ScalarType::Float8_e4m3fn;
-      const auto state = eight ? ScalarType::Float8_e4m3fn : ScalarType::Float;
-      d.state_type = eight ? MB_E4M3 : MB_F32;
-      d.exp_avg = place(avg, name(2), d.n, state, none, true);
-      d.exp_avg_sq = place(sq, name(3), d.n, state, none, true);
-      if (const Tensor* low = given(4)) {
-        if (param.scalar_type() != ScalarType::BFloat16) throw Refused{name(4) + " needs a bfloat16 parameter"};
-        d.mantissa = static_cast<uint16_t*>(place(*low, name(4), d.n, ScalarType::Short, ScalarType::UInt16, true));
-      }
-      for (int i = 5; i < 7; ++i) {
-        const Tensor* scale = given(i);
-        if (eight != (scale != nullptr))
-          throw Refused{name(i) + (eight ? " is missing: 8-bit moments need it" : " is for 8-bit moments only")};
-        if (eight)
-          (i == 5 ? d.avg_scale : d.sq_scale) =
-              static_cast<float*>(place(*scale, name(i), (d.n + 255) / 256, ScalarType::Float, none, true));
-      }
-      d.lr_mul = number(f[7]);
-      d.wd_mul = number(f[8]);
-      descs.push_back(d);
-    } catch (...) {
-      Py_DECREF(seq);
-      throw;
+  void add(PyObject* const* f, Py_ssize_t at) {
+    mb_adamw_tensor d{};
+    const Tensor &param = cuda_tensor(f[0], NAMES[0]), &grad = tensor(f[1], NAMES[1]);
+    const Tensor &avg = tensor(f[2], NAMES[2]), &sq = tensor(f[3], NAMES[3]);
+    const Tensor *low = tensor_or_none(f[4], NAMES[4]);
+    const Tensor* scale[2] = {tensor_or_none(f[5], NAMES[5]), tensor_or_none(f[6], NAMES[6])};
+    if (at == 0) {
+      first = param;
+      device = param.device();
     }
-    Py_DECREF(seq);
+    d.n = param.numel();
+    d.param_type = type_of(param, NAMES[0]);
+    d.grad_type = type_of(grad, NAMES[1]);
+    const auto none = ScalarType::Undefined;
+    const size_t begin = written.size();
+    d.param = place(param, 0, at, d.n, param.scalar_type(), none);
+    if (grad.sizes() != param.sizes()) throw Refused{name(1, at) + " is " + str(grad) + ", its parameter " + str(param)};
+    d.grad = place(grad, 1, at, d.n, grad.scalar_type(), none);
+    const bool eight = avg.scalar_type() == ScalarType::Float8_e4m3fn;
+    const auto state = eight ? ScalarType::Float8_e4m3fn : ScalarType::Float;
+    d.state_type = eight ? MB_E4M3 : MB_F32;
+    d.exp_avg = place(avg, 2, at, d.n, state, none);
+    d.exp_avg_sq = place(sq, 3, at, d.n, state, none);
+    if (low) {
+      if (param.scalar_type() != ScalarType::BFloat16) throw Refused{name(4, at) + " needs a bfloat16 parameter"};
+      d.mantissa = static_cast<uint16_t*>(place(*low, 4, at, d.n, ScalarType::Short, ScalarType::UInt16));
+    }
+    for (int i = 0; i < 2; ++i) {
+      if (eight != (scale[i] != nullptr))
+        throw Refused{name(5 + i, at) + (eight ? " is missing: 8-bit moments need it" : " is for 8-bit moments only")};
+      if (eight)
+        (i == 0 ? d.avg_scale : d.sq_scale) =
+            static_cast<float*>(place(*scale[i], 5 + i, at, (d.n + 255) / 256, ScalarType::Float, none));
+    }
+    // the element's own tensors one against another, the gradient among them
+    const auto apart = [](const Tensor& a, const Tensor& b) {
+      const auto p = reinterpret_cast<uintptr_t>(a.data_ptr()), q = reinterpret_cast<uintptr_t>(b.data_ptr());
+      return p + a.nbytes() <= q || q + b.nbytes() <= p;
+    };
+    for (size_t i = begin; i < written.size(); ++i) {
+      if (!apart(*written[i], grad)) throw Refused{"the gradient of tensor " + std::to_string(at) + " overlaps what the call writes"};
+      for (size_t j = begin; j < i; ++j)
+        if (!apart(*written[i], *written[j])) throw Refused{"tensors that the call writes overlap in tensor " + std::to_string(at)};
+    }
+    d.lr_mul = number(f[7]);
+    d.wd_mul = number(f[8]);
+    descs.push_back(d);
+  }
+
+  // A tensor that is given twice would be stepped by two CTAs at once.
+  void check_params() const {
+    const auto size = [](const mb_adamw_tensor& d) { return static_cast<size_t>(d.n) * (d.param_type == MB_F32 ? 4 : 2); };
+    std::vector<std::pair<uintptr_t, uintptr_t>> at;
+    at.reserve(descs.size());
+    for (const auto& d : descs)
+      if (d.n > 0) at.emplace_back(reinterpret_cast<uintptr_t>(d.param), reinterpret_cast<uintptr_t>(d.param) + size(d));
+    if (!std::is_sorted(at.begin(), at.end())) std::sort(at.begin(), at.end());
+    for (size_t i = 1; i < at.size(); ++i)
+      if (at[i].first < at[i - 1].second) throw Refused{"parameters of the call overlap"};
   }
 
   explicit AdamwList(PyObject* list) {
-    static const char* names[7] = {"param", "grad", "exp_avg", "exp_avg_sq", "mantissa", "avg_scale", "sq_scale"};
-    PyObject* seq = PySequence_Fast(list, "tensors must be a sequence of AdamState");
-    if (!seq) throw Raised{};
     try {
+      PyObject* seq = PySequence_Fast(list, "tensors must be a sequence of AdamState");
+      if (!seq) throw Raised{};
+      held.push_back(seq);
       const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
       if (n == 0) throw Refused{"no tensors"};
       if (n > MB_ADAMW_MAX_TENSORS) checked("adamw_multi_step", MB_ERR_TOO_MANY);
       descs.reserve(n);
-      for (Py_ssize_t i = 0; i < n; ++i) add(PySequence_Fast_GET_ITEM(seq, i), i, names);
+      written.reserve(5 * n);
+      held.reserve(n + 1);
+      for (Py_ssize_t i = 0; i < n; ++i) {
+        PyObject* item = PySequence_Fast_GET_ITEM(seq, i);
+        if (!PyTuple_Check(item) || PyTuple_GET_SIZE(item) != 9) throw Refused{"each tensor of the call is an AdamState"};
+        held.push_back(Py_NewRef(item));       // other threads may change the list while the call launches
+        PyObject* f[9];
+        for (int k = 0; k < 9; ++k) f[k] = PyTuple_GET_ITEM(item, k);
+        add(f, i);
+      }
+      check_params();
     } catch (...) {
-      Py_DECREF(seq);
+      release();
       throw;
     }
-    Py_DECREF(seq);
-    // a tensor that is given twice would be stepped by two CTAs at once
-    std::sort(ranges.begin(), ranges.end());
-    for (size_t i = 1; i < ranges.size(); ++i)
-      if (ranges[i].first < ranges[i - 1].second) throw Refused{"tensors of the call that it writes overlap"};
+  }
+  AdamwList(const AdamwList&) = delete;
+  ~AdamwList() { release(); }
+  void release() {
+    for (PyObject* o : held) Py_DECREF(o);
+    held.clear();
   }
 
+  // Marks the tensors as used on the stream that the call was given.
+  void record(cudaStream_t stream) const {
+    const auto s = c10::cuda::getStreamFromExternal(stream, device.index()).unwrap();
+    for (size_t i = 1; i < held.size(); ++i)
+      for (int k = 0; k < 7; ++k) {
+        PyObject* t = PyTuple_GET_ITEM(held[i], k);
+        if (t != Py_None) THPVariable_Unpack(t).record_stream(s);
+      }
+  }
   void stepped() const {
-    for (const Tensor& t : written)
-      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    for (const Tensor* t : written)
+      if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
   }
 };
 
@@ -644,27 +674,6 @@ double real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Raised{};
   return v;
-}
-
-// Marks the list's tensors as used on the stream that the call was given.
-void record(const AdamwList& list, PyObject* tensors, const Where& where, PyObject* given) {
-  if (given == Py_None) return;
-  const auto s = c10::cuda::getStreamFromExternal(where.stream, list.device.index());
-  PyObject* seq = PySequence_Fast(tensors, "");
-  if (!seq) throw Raised{};
-  for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(seq); ++i) {
-    PyObject* item = PySequence_Fast(PySequence_Fast_GET_ITEM(seq, i), "");
-    if (!item) {
-      Py_DECREF(seq);
-      throw Raised{};
-    }
-    for (Py_ssize_t j = 0; j < PySequence_Fast_GET_SIZE(item); ++j) {
-      PyObject* t = PySequence_Fast_GET_ITEM(item, j);
-      if (THPVariable_Check(t) && THPVariable_Unpack(t).is_cuda()) THPVariable_Unpack(t).record_stream(s.unwrap());
-    }
-    Py_DECREF(item);
-  }
-  Py_DECREF(seq);
 }
 
 // The seed of stochastic rounding (None: to the nearest).
@@ -680,7 +689,7 @@ uint32_t seed_of(PyObject* o, int* stochastic) {
 PyObject* adamw(PyObject* const* a, Py_ssize_t n) {
   const AdamwList list(a[0]);
   Where where(list.first, a[9], a, n);
-  record(list, a[0], where, a[9]);
+  if (a[9] != Py_None) list.record(where.stream);
   const double lr = real(a[1]), wd = real(a[2]), beta1 = real(a[3]), beta2 = real(a[4]), eps = real(a[5]);
   const long long step = integer(a[6], "step");
   const auto* scale =
@@ -699,7 +708,7 @@ PyObject* adamw(PyObject* const* a, Py_ssize_t n) {
 PyObject* adamw_dev(PyObject* const* a, Py_ssize_t n) {
   const AdamwList list(a[0]);
   Where where(list.first, a[5], a, n);
-  record(list, a[0], where, a[5]);
+  if (a[5] != Py_None) list.record(where.stream);
   const auto* scalars =
       static_cast<const double*>(dense(&tensor(a[1], "scalars"), "scalars", {6}, ScalarType::Double, list.device));
   const auto* scale =
