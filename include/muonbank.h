@@ -358,6 +358,67 @@ int mb_router_backward(const float* dloss, const float* dgate, const void* logit
                        const int32_t* counts, const int32_t* used, void* dlogits,
                        int64_t dlogits_stride, void* cuda_stream);
 
+/* ---- products with bias, activation and residual, over groups of rows ----
+ *
+ * The products of a block with a bank's matrices, with what stands around them, and their gradient.  The rows of x
+ * are one group with one matrix, or, with `ends`, consecutive groups with a matrix each (a bank of experts, tokens
+ * sorted by expert): group g has the rows from ends[g - 1] (0 for the first) up to ends[g].
+ *   z = x W_g^T + b_g;   y = act(z) + residual
+ *   act: z; max(z, 0); max(z, 0)^2; z s(z); z s(2 sqrt(2/pi) (z + 0.044715 z^3)), s(t) = 1 / (1 + exp(-t))
+ * and, given dy,
+ *   dz = dy act'(z) (0 at 0 for max(z, 0));   db_g = sum of dz;   dx = dz W_g;   dW_g = dz^T x   (sums over the group's rows)
+ * (the residual's gradient is dy itself).  Rows from the last end on belong to no group: their y, z and dx are zero,
+ * and nothing of them is in dW and db.  A group without rows has zero dW and db.
+ *
+ * Operands are bf16 or fp16, sums fp32, each result rounded once; dz is rounded to the operands' type before the
+ * products (the tensor cores take no wider operand), but not for db.  Activations take the hardware's exponential
+ * and reciprocal, each within about 2^-22.  The conventions are the block operators'; operands whose rows do not
+ * start at 16-byte boundaries are copied to the workspace first. */
+enum { MB_ACT_NONE = 0, MB_ACT_RELU = 1, MB_ACT_RELU2 = 2, MB_ACT_SILU = 3, MB_ACT_GELU = 4 };
+
+typedef struct {
+  const void* x;             /* [rows, in], row stride x_stride (elements) */
+  const void* weight;        /* [groups, out, in] */
+  const void* bias;          /* [groups, out], or NULL */
+  const void* residual;      /* [rows, out], or NULL */
+  const int32_t* ends;       /* [groups] in device memory, or NULL with groups = 1 */
+  void* y;                   /* [rows, out] */
+  void* z;                   /* [rows, out] for the backward pass, or NULL */
+  int64_t x_stride, residual_stride, y_stride, z_stride;
+  int64_t rows;              /* 0 to 2^30 */
+  int32_t in, out;           /* 1 to 2^20 */
+  int32_t groups;            /* 1 to 1024 */
+  int32_t type;              /* MB_BF16 or MB_F16: all but the bias */
+  int32_t bias_type;         /* `type` or MB_F32 */
+  int32_t activation;        /* MB_ACT_* */
+} mb_linear_desc;
+
+typedef struct {
+  const void* dy;            /* [rows, out] */
+  const void* x;             /* [rows, in]; read for dweight */
+  const void* weight;        /* [groups, out, in]; read for dx */
+  const void* z;             /* [rows, out] of the forward pass; not read with MB_ACT_NONE */
+  const int32_t* ends;
+  void* dx;                  /* [rows, in], or NULL: not wanted */
+  void* dweight;             /* [groups, out, in], or NULL */
+  void* dbias;               /* [groups, out] of bias_type, or NULL */
+  int64_t dy_stride, x_stride, z_stride, dx_stride;
+  int64_t rows;
+  int32_t in, out, groups, type, bias_type, activation;
+} mb_linear_backward_desc;
+
+/* The descriptors are read during the call only.  y may be written over the residual with the same stride; no other
+ * overlap.  Ends that are negative, fall, or pass `rows` are held to what can be (no access leaves the tensors) and
+ * latch MB_ERR_ARG for mb_sync_status.  The workspace (256-byte aligned; its size depends on the descriptor's pointers
+ * and strides) is needed for operands that have to be copied, dz, the bias's sums and contractions that are cut over
+ * several CTAs; many forward calls need none.  MB_ERR_SHAPE: sizes past the limits above, in * out * groups past 2^40,
+ * strides that are negative, or too small in a result. */
+int mb_linear_workspace_bytes(const mb_linear_desc* desc, size_t* out_bytes);
+int mb_linear(const mb_linear_desc* desc, void* workspace, size_t workspace_bytes, void* cuda_stream);
+int mb_linear_backward_workspace_bytes(const mb_linear_backward_desc* desc, size_t* out_bytes);
+int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, size_t workspace_bytes,
+                       void* cuda_stream);
+
 /* ---- AdamW over the tensors that are in no bank ----
  *
  * Embeddings, heads, norms, biases: what Muon does not take.  One launch steps a list of tensors of any sizes
@@ -435,7 +496,9 @@ enum {
   MB_MARK_ROTARY = 10,    /* (either direction) */
   MB_MARK_ROUTER = 11,
   MB_MARK_ROUTER_BACKWARD = 12,
-  MB_MARK_ADAMW = 13      /* after an AdamW step's launches */
+  MB_MARK_ADAMW = 13,     /* after an AdamW step's launches */
+  MB_MARK_LINEAR = 14,    /* after a product's */
+  MB_MARK_LINEAR_BACKWARD = 15
 };
 
 /* Starts recording a CUDA event on the launching stream at every stage

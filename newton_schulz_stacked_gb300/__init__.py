@@ -16,8 +16,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import _binding as _b
-from .blocks import (RouterOutput, mb_layer_norm, mb_layer_norm_backward, mb_rotary, mb_rotary_backward,  # noqa: F401
-                     mb_router, mb_router_backward)
+from .blocks import (RouterOutput, mb_layer_norm, mb_layer_norm_backward, mb_linear, mb_linear_backward,  # noqa: F401
+                     mb_rotary, mb_rotary_backward, mb_router, mb_router_backward)
 from .adamw import AdamState, adamw_multi_step, adamw_multi_step_dev, adamw_state                           # noqa: F401
 from ._binding import MuonBankError, MB_MAX_BANKS, MB_STEP_FUSE_ROWSTATS, MB_STEP_FUSE_UPDATE  # noqa: F401
 
@@ -28,7 +28,7 @@ __all__ = [
     "mb_sync_status", "mb_selftest_timeout", "mb_status_string", "MuonBankError",
     "BankState", "load_library", "mb_launch_count", "StageTimer",
     "mb_layer_norm", "mb_layer_norm_backward", "mb_rotary", "mb_rotary_backward", "mb_router", "mb_router_backward",
-    "RouterOutput", "AdamState", "adamw_state", "adamw_multi_step", "adamw_multi_step_dev",
+    "RouterOutput", "mb_linear", "mb_linear_backward", "AdamState", "adamw_state", "adamw_multi_step", "adamw_multi_step_dev",
 ]
 
 _TWO_BYTE = (torch.bfloat16, torch.int16, torch.uint16, torch.float16)

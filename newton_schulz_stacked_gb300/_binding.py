@@ -36,6 +36,7 @@ MB_STEP_FUSE_ROWSTATS = 2
 MB_F32, MB_BF16, MB_F16, MB_I32, MB_I64, MB_E4M3 = range(6)
 MB_ROTARY_MAX_AXES = 4
 MB_ADAMW_MAX_TENSORS = 65536
+MB_ACT_NONE, MB_ACT_RELU, MB_ACT_RELU2, MB_ACT_SILU, MB_ACT_GELU = range(5)
 
 
 class MbShape(ctypes.Structure):
@@ -58,6 +59,18 @@ class MbRotaryDesc(ctypes.Structure):
                 ("positions", c_void_p), ("pos_axis", c_int64), ("pos_batch", c_int64), ("pos_token", c_int64),
                 ("position_type", ctypes.c_int32), ("axes", ctypes.c_int32),
                 ("sections", ctypes.c_int32 * MB_ROTARY_MAX_AXES), ("inv_freq", c_void_p)]
+
+
+class MbLinearDesc(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("x", "weight", "bias", "residual", "ends", "y", "z")] + [
+        (n, c_int64) for n in ("x_stride", "residual_stride", "y_stride", "z_stride", "rows")] + [
+        (n, ctypes.c_int32) for n in ("inputs", "out", "groups", "type", "bias_type", "activation")]
+
+
+class MbLinearBackwardDesc(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("dy", "x", "weight", "z", "ends", "dx", "dweight", "dbias")] + [
+        (n, c_int64) for n in ("dy_stride", "x_stride", "z_stride", "dx_stride", "rows")] + [
+        (n, ctypes.c_int32) for n in ("inputs", "out", "groups", "type", "bias_type", "activation")]
 
 
 class MbAdamwTensor(ctypes.Structure):
@@ -99,6 +112,10 @@ _SIGNATURES = {
                           _P]),
     "mb_router_backward": (c_int, [_P, _P, _P, c_int64, c_int, _P, c_int64, c_int64, c_int, c_int, _P, _P, _P, _P, _P,
                                    c_int64, _P]),
+    "mb_linear_workspace_bytes": (c_int, [ctypes.POINTER(MbLinearDesc), ctypes.POINTER(c_size_t)]),
+    "mb_linear": (c_int, [ctypes.POINTER(MbLinearDesc), _P, c_size_t, _P]),
+    "mb_linear_backward_workspace_bytes": (c_int, [ctypes.POINTER(MbLinearBackwardDesc), ctypes.POINTER(c_size_t)]),
+    "mb_linear_backward": (c_int, [ctypes.POINTER(MbLinearBackwardDesc), _P, c_size_t, _P]),
     "adamw_multi_step": (c_int, [ctypes.POINTER(MbAdamwTensor), c_int, _D, _D, _D, _D, _D, c_int64, _P, c_int,
                                  ctypes.c_uint32, _P]),
     "adamw_multi_step_dev_workspace_bytes": (c_int, [c_int, ctypes.POINTER(c_size_t)]),
@@ -116,7 +133,7 @@ _SIGNATURES = {
 
 MARK_NAMES = {0: "begin", 1: "momentum", 2: "scale", 3: "small_ns", 4: "ns_gemm", 5: "ns0", 6: "rowstats",
               7: "update", 8: "layer_norm", 9: "layer_norm_backward", 10: "rotary", 11: "router",
-              12: "router_backward", 13: "adamw"}
+              12: "router_backward", 13: "adamw", 14: "linear", 15: "linear_backward"}
 
 _lib = None
 

@@ -1,6 +1,6 @@
 """The block operators under torch's autograd: each forward call joined with its backward call.
 
-rotary is linear in q and k and can be differentiated any number of times.  layer_norm and route
+rotary is linear in q and k and can be differentiated any number of times.  layer_norm, linear and route
 have first derivatives only: differentiating their gradients (of create_graph=True) raises
 RuntimeError.
 """
@@ -127,3 +127,42 @@ class _Route(torch.autograd.Function):
 def route(logits, top_k: int, valid=None, normalize: bool = False) -> Routing:
     """mb_router, differentiable in the logits through the gates and the balance loss."""
     return Routing(*_Route.apply(logits, top_k, valid, normalize))
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation, ends):
+        keep = activation != "none" and any(ctx.needs_input_grad[:3])
+        y, z = _k.mb_linear(x, weight, bias, residual, activation, ends, keep=keep)
+        ctx.save_for_backward(x, weight, z, ends)
+        ctx.activation = activation
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, z, ends = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        grads = (None, None, None)
+        if any(want[:3]):
+            def call(dy, x, weight, z, ends):
+                dbias = None
+                if want[2]:
+                    dbias = torch.empty(weight.shape[:-1], dtype=ctx.bias_dtype, device=weight.device)
+                return _k.mb_linear_backward(dy, x, weight, z, ctx.activation, ends, input_grad=want[0], weight_grad=want[1],
+                                             dbias=dbias)
+            grads = _first_only("linear", call, dy.resolve_neg().contiguous(), x, weight, z, ends)
+        return (*grads, _of_groups(dy, ends) if want[3] else None, None, None)
+
+
+def _of_groups(dy, ends):
+    """dy, zero in the rows that belong to no group: their residual is not in y."""
+    if ends is None:
+        return dy
+    rows = torch.arange(dy.shape[:-1].numel(), device=dy.device).view(dy.shape[:-1])
+    return torch.where((rows < ends[-1])[..., None], dy, 0)
+
+
+def linear(x, weight, bias=None, residual=None, activation: str = "none", ends=None) -> torch.Tensor:
+    """mb_linear, differentiable in x, weight, bias and residual; over groups of rows where ends are given."""
+    return _Linear.apply(x, weight, bias, residual, activation, ends)

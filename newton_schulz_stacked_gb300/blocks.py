@@ -1,4 +1,4 @@
-"""The operators of a block between its matrix products: layer norm, rotary positions, expert routing.
+"""The operators of a block: products with bias, activation and residual, layer norm, rotary positions, expert routing.
 
 Each function has the name of the C entry point it calls (include/muonbank.h gives the
 formulas), takes CUDA tensors and enqueues the work on the current CUDA stream, or on
@@ -109,3 +109,28 @@ def mb_router_backward(dloss, dgate, logits, index, gate, counts, used, valid=No
     [tokens, top_k]); either may be None.  index, gate, counts and used are the forward call's."""
     return (_native or load_binding()).mb_router_backward(dloss, dgate, logits, index, gate, counts, used, valid, normalize,
                                                           dlogits, stream)
+
+
+def mb_linear(x, weight, bias=None, residual=None, activation: str = "none", ends=None, keep: bool = False, y=None, z=None,
+              workspace=None, stream=None):
+    """act(x W^T + bias) + residual: (y, z), z = x W^T + bias if keep (for the backward pass), else None.
+
+    x is [..., in] in bfloat16 or float16, weight [out, in], bias [out] in x's type or float32, residual
+    [..., out].  With `ends`, int32 [groups], weight is a bank [groups, out, in] (and bias [groups, out]): the rows of x
+    are consecutive groups, group g ending before row ends[g], such as tokens sorted by expert with
+    ends = counts.cumsum(0, dtype=torch.int32); rows from the last end on get zeros.  The ends stay on the device.
+    activation: "none", "relu", "relu2" (its square), "silu" or "gelu" (the tanh form).
+    """
+    return (_native or load_binding()).mb_linear(x, weight, bias, residual, activation, ends, keep, y, z, workspace, stream)
+
+
+def mb_linear_backward(dy, x, weight, z=None, activation: str = "none", ends=None, input_grad: bool = True,
+                       weight_grad: bool = True, bias: bool = False, dx=None, dweight=None, dbias=None, workspace=None,
+                       stream=None):
+    """Gradients of mb_linear: (dx, dweight, dbias), None for those that are not wanted (input_grad, weight_grad, bias).
+
+    z is the forward call's (not needed without an activation).  dweight is laid out as the weight, the gradient of a bank as
+    muon_multi_step takes it; dbias comes in x's type unless a float32 one is passed.  The residual's gradient is dy.
+    """
+    return (_native or load_binding()).mb_linear_backward(dy, x, weight, z, activation, ends, input_grad, weight_grad, bias,
+                                                          dx, dweight, dbias, workspace, stream)

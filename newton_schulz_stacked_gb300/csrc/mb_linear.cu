@@ -1,0 +1,487 @@
+// The products of mb_linear on the sm_103a tensor cores: y = act(x W^T + b) + residual over groups of rows, and the two
+// products of its gradient, dx = dz W and dW = dz^T x, in one launch.
+//
+// Pairs of CTAs compute tiles of 256 rows x 256 (or 128) columns with M = 256 tcgen05 MMAs (cta_group::2): CTA r of a
+// pair holds rows 128 r .. of the A operand and half of the B operand's, staged by TMA with 128-byte swizzle in 64-deep
+// blocks, and receives its 128 rows x all columns of the fp32 sums in TMEM (two accumulators, so that one tile's epilogue
+// runs under the next one's MMAs).  An operand whose contraction runs along memory is staged K-major, one box a block;
+// the others (W in dx, both in dW) as boxes of 64 x 64 in MN-major layout.
+//
+// A pair takes the units pair, pair + pairs, ...; every role finds them itself from the groups' first rows and tiles, which
+// each CTA works out in shared memory from the ends in device memory, so that the host need not know them.  Tiles never
+// cross groups; a tile's operand rows past its group belong to the next group and are computed but not stored.  In dW
+// the contraction runs over the group's rows and its last block may reach into the next group's: there the loads complete on
+// a barrier of their own CTA, a warp clears the rows past the group's end in both operands (zero times the next group's
+// infinity would not be zero), and the MMAs wait for both CTAs' warps.  Rows past the tensor, and columns past its
+// width, are read as zeros by TMA.
+//
+// Roles (11 warps, both CTAs):
+//   warp 0 lane 0   TMA producer, a ring of STAGES blocks; the bytes of both CTAs complete on the even CTA's barrier
+//   warp 1          TMEM; lane 0 of the even CTA issues the MMAs and releases stages in both CTAs
+//   warps 2..9      epilogue of the CTA's 128 rows, two warps per 32 TMEM lanes, 32 x 32 chunks through shared memory to
+//                   row-wise stores; before its first tile each takes a share of what else the call leaves to do: zeros in
+//                   rows of no group, dbias from the slabs' sums
+//   warp 10         clears the blocks that reach past a group
+//
+// A long contraction over few tiles is cut into parts whose fp32 sums go to the workspace, and linear_join_kernel adds them
+// in order.
+#include <atomic>
+#include <type_traits>
+
+#include "mb_block.h"
+#include "mb_linear.cuh"
+
+namespace mb {
+namespace {
+
+constexpr int BM = 128;
+constexpr int STAGES = 5;
+constexpr int TILE_BYTES = BM * LINEAR_DEEP * 2;     // 16 KB: a CTA's rows of one operand's block
+constexpr int BOX_BYTES = 64 * LINEAR_DEEP * 2;      // 8 KB: one 64 x 64 box
+constexpr int EPI_WARPS = 8;
+constexpr int FIX_WARP = 2 + EPI_WARPS;
+constexpr int THREADS = 32 * (FIX_WARP + 1);
+constexpr int BIAS_BYTES = 4 * 32 * 4;               // per epilogue warp
+constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * (CHUNK_BYTES + BIAS_BYTES) + GROUPS_BYTES + 1024 /* alignment */ +
+                     512 /* barriers */;
+static_assert(SMEM <= 232448, "shared memory per CTA");
+constexpr uint32_t ACC_COLS = 256, TMEM_COLS = 512;
+
+// Instruction descriptor, kind::f16, fp32 sums, M = 256 (a pair).
+template <typename T>
+__device__ __forceinline__ uint32_t instruction(int n, int a_mn, int b_mn) {
+  const uint32_t kind = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
+  return (1u << 4) | kind | static_cast<uint32_t>(a_mn) << 15 | static_cast<uint32_t>(b_mn) << 16 |
+         static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(256 >> 4) << 24;
+}
+
+__device__ __forceinline__ void tmem_ld_32x32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Whether block kb of a unit reaches into the next group's rows.
+__device__ __forceinline__ bool reaches_past(const LinearParams& P, const LinearJob& J, const Unit& u, int kb) {
+  return J.over_rows && u.k_end < P.rows && u.k_begin + (kb + 1) * LINEAR_DEEP > u.k_end;
+}
+
+// A share of the work beside the tiles, by the epilogue's warps: warp `me` of `all`.
+template <typename T>
+__device__ void side_work(const LinearParams& P, const Groups& G, long long me, long long all, int lane) {
+  if (P.ends && P.jobs > 0 && !P.job[P.jobs - 1].over_rows) {
+    // zeros in the rows of no group
+    const LinearJob& J = P.job[P.jobs - 1];
+    for (long long row = G.row[G.n] + me; row < P.rows; row += all) {
+      for (int which = 0; which < 2; ++which) {
+        uint16_t* out = static_cast<uint16_t*>(which ? P.z : J.out);
+        if (!out) continue;
+        out += row * (which ? P.z_ld : J.ld);
+        if ((which ? P.z_access : J.access) == 16)
+          for (int c = lane; c < J.N / 8; c += 32) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+        else
+          for (int c = lane; c < J.N; c += 32) out[c] = 0;
+      }
+    }
+  }
+  if (P.db) {
+    // dbias of 32 columns of one group: its sums over the slabs that hold its rows, in order
+    const int across = (P.db_cols + 31) / 32;
+    for (long long i = me; i < static_cast<long long>(G.n) * across; i += all) {
+      const int g = static_cast<int>(i / across), col = static_cast<int>(i % across) * 32 + lane;
+      if (col >= P.db_cols) continue;
+      float sum = 0.f;
+      const int begin = G.row[g], end = G.row[g + 1];
+      if (end > begin) {
+        const int last = (end - 1) / P.slab;
+#pragma unroll 8
+        for (int s = begin / P.slab; s <= last; ++s) sum += P.db_parts[static_cast<long long>(s + g) * P.db_cols + col];
+      }
+      const long long at = static_cast<long long>(g) * P.db_cols + col;
+      if (P.db_f32) static_cast<float*>(P.db)[at] = sum;
+      else static_cast<T*>(P.db)[at] = from_float<T>(sum);
+    }
+  }
+}
+
+template <bool FORWARD, typename T>
+__global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constant__ LinearParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * TILE_BYTES;
+  uint8_t* sChunk = sB + STAGES * TILE_BYTES;
+  uint8_t* sBias = sChunk + EPI_WARPS * CHUNK_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sBias + EPI_WARPS * BIAS_BYTES);   // [STAGES] (even) both CTAs' operands landed
+  uint64_t* empty = full + STAGES;           // [STAGES] the pair's MMAs are done with the stage
+  uint64_t* past = empty + STAGES;           // [STAGES] this CTA's part of a block that reaches past its group landed
+  uint64_t* cleared = past + STAGES;         // [STAGES] (even) both CTAs have cleared it
+  uint64_t* tfull = cleared + STAGES;        // [2] accumulator ready for the epilogue
+  uint64_t* tempty = tfull + 2;              // [2] (even) both CTAs' epilogues drained the accumulator
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Groups G;
+  G.row = reinterpret_cast<int*>(tmem_slot + 4);
+  G.tile = G.row + LINEAR_MAX_GROUPS + 1;
+  G.n = P.groups;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool even = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&past[s], 1);
+      mbar_init(&cleared[s], 2);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * EPI_WARPS);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  begin_after_previous();
+  if (warp == FIX_WARP && fill_groups(G, P.ends, P.rows, lane) && blockIdx.x == 0 && P.status_from && lane == 0)
+    latch_status(P.status, DEV_BAD_SCALAR);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();      // both CTAs' barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&]() {
+    latch_status(P.status, DEV_TIMEOUT);
+    *abort_flag = 1;
+  };
+  // The pair's MMAs write the odd CTA's accumulators at the even CTA's TMEM address.
+  if (threadIdx.x == 0 && ld_cluster_u32(map_to_rank(tmem_slot, rank ^ 1u)) != tmem) {
+    latch_status(P.status, DEV_PAIR_TMEM);
+    *abort_flag = 1;
+  }
+
+  const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const long long first_units = P.jobs > 0 ? job_units(P.job[0], G) : 0;
+  const long long units = first_units + (P.jobs > 1 ? job_units(P.job[1], G) : 0);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer (both CTAs)
+      for (int j = 0; j < P.jobs; ++j) {
+        tma_prefetch_map(&P.job[j].a);
+        tma_prefetch_map(&P.job[j].b);
+      }
+      const uint32_t full_even = map_to_rank(&full[0], 0), past_own = map_to_rank(&past[0], rank);
+      int st = 0;
+      uint32_t ph = 0, it = 0;
+      bool ok = true;
+      for (long long at = pair; at < units && ok && !*abort_flag; at += pairs) {
+        Unit u;
+        decode_unit(P, G, first_units, at, u);
+        const LinearJob& J = P.job[u.job];
+        const int m0 = u.m0 + static_cast<int>(rank) * BM, n0 = u.n0 + static_cast<int>(rank) * (u.wide >> 1);
+        const int b_boxes = u.wide >> 7;
+        const uint32_t b_bytes = J.b_mn ? b_boxes * BOX_BYTES : (J.wide >> 1) * LINEAR_DEEP * 2;
+        const int batch = J.over_rows ? 0 : u.group;
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+          if (it >= STAGES && !mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          uint32_t bar = full_even + 8u * static_cast<uint32_t>(st);
+          if (!reaches_past(P, J, u, kb)) {
+            if (even) mbar_expect_tx(&full[st], 2u * (TILE_BYTES + b_bytes));   // both CTAs' boxes
+          } else {
+            if (even) mbar_arrive(&full[st]);
+            bar = past_own + 8u * static_cast<uint32_t>(st);
+            mbar_expect_tx(&past[st], TILE_BYTES + b_bytes);
+          }
+          uint8_t* a = sA + st * TILE_BYTES;
+          uint8_t* b = sB + st * TILE_BYTES;
+          const int k0 = u.k_begin + kb * LINEAR_DEEP;
+          if (!J.a_mn) {
+            tma_load_3d_pair(a, &J.a, bar, k0, m0, 0);
+          } else {
+            tma_load_3d_pair(a, &J.a, bar, m0, k0, 0);
+            tma_load_3d_pair(a + BOX_BYTES, &J.a, bar, m0 + 64, k0, 0);
+          }
+          if (!J.b_mn) {
+            tma_load_3d_pair(b, &J.b, bar, k0, n0, batch);
+          } else {
+            for (int c = 0; c < b_boxes; ++c) tma_load_3d_pair(b + c * BOX_BYTES, &J.b, bar, n0 + 64 * c, k0, batch);
+          }
+          if (++st == STAGES) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // this CTA stays until the multicast releases of every stage it filled have arrived
+      for (uint32_t i = it > STAGES ? it - STAGES : 0u; i < it; ++i) {
+        if (!mbar_wait_cluster_or_abort(&empty[i % STAGES], (i / STAGES) & 1, abort_flag)) {
+          fail();
+          break;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (even && lane == 0) {
+      // ---------------- MMA issuer of the pair
+      uint32_t it = 0, k = 0, past_phase = 0;
+      bool ok = true;
+      for (long long at = pair; at < units && ok && !*abort_flag; at += pairs, ++k) {
+        Unit u;
+        decode_unit(P, G, first_units, at, u);
+        const LinearJob& J = P.job[u.job];
+        const uint32_t buf = k & 1;
+        if (k >= 2 && !mbar_wait_cluster_or_abort(&tempty[buf], ((k >> 1) - 1) & 1, abort_flag)) {
+          fail();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t dacc = tmem + buf * ACC_COLS;
+        const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
+        const uint32_t a_step = J.a_mn ? 2048u : 32u, b_step = J.b_mn ? 2048u : 32u;
+        const uint32_t a_lbo = J.a_mn ? BOX_BYTES : 16u, b_lbo = J.b_mn ? BOX_BYTES : 16u;
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+          const int st = it % STAGES;
+          if (!mbar_wait_or_abort(&full[st], (it / STAGES) & 1, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          if (reaches_past(P, J, u, kb)) {
+            if (!mbar_wait_cluster_or_abort(&cleared[st], (past_phase >> st) & 1u, abort_flag)) {
+              fail();
+              ok = false;
+              break;
+            }
+            past_phase ^= 1u << st;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + st * TILE_BYTES), b0 = smem_u32(sB + st * TILE_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < LINEAR_DEEP / 16; ++kk) {
+            umma_bf16_pair(dacc, smem_desc_sw128(a0 + kk * a_step, a_lbo, 1024),
+                           smem_desc_sw128(b0 + kk * b_step, b_lbo, 1024), idesc, (kb > u.kb0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit_pair_both(&empty[st]);   // the stage may be refilled in both CTAs
+        }
+        umma_commit_pair_both(&tfull[buf]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == FIX_WARP) {
+    // ---------------- blocks that reach past a group: their rows from the group's end on become zero
+    uint32_t it = 0, past_phase = 0;
+    const uint32_t cleared_even = map_to_rank(&cleared[0], 0);
+    for (long long at = pair; at < units && !*abort_flag; at += pairs) {
+      Unit u;
+      decode_unit(P, G, first_units, at, u);
+      const LinearJob& J = P.job[u.job];
+      const int blocks = u.kb1 - u.kb0;
+      if (blocks > 0 && reaches_past(P, J, u, u.kb1 - 1)) {      // only a group's last block does
+        const int st = (it + blocks - 1) % STAGES;
+        if (!mbar_wait_or_abort(&past[st], (past_phase >> st) & 1u, abort_flag)) {
+          fail();
+          break;
+        }
+        past_phase ^= 1u << st;
+        // a box's rows of 128 bytes are its rows of the contraction (the swizzle stays within a row)
+        const int keep = u.k_end - u.k_begin - (u.kb1 - 1) * LINEAR_DEEP;
+        for (int box = 0; box < 2 + (u.wide >> 7); ++box) {
+          uint8_t* base = box < 2 ? sA + st * TILE_BYTES + box * BOX_BYTES : sB + st * TILE_BYTES + (box - 2) * BOX_BYTES;
+          for (int i = keep * 8 + lane; i < LINEAR_DEEP * 8; i += 32) reinterpret_cast<uint4*>(base)[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cleared_even + 8u * static_cast<uint32_t>(st));
+      }
+      it += blocks;
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue
+    const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
+    WarpPlace w;
+    w.lane = lane;
+    w.buf = sChunk + ew * CHUNK_BYTES;
+    w.bias = reinterpret_cast<float*>(sBias + ew * BIAS_BYTES);
+    const uint32_t tempty_even = map_to_rank(&tempty[0], 0);
+    side_work<T>(P, G, static_cast<long long>(blockIdx.x) * EPI_WARPS + ew, static_cast<long long>(gridDim.x) * EPI_WARPS, lane);
+    uint32_t k = 0;
+    for (long long at = pair; at < units; at += pairs, ++k) {
+      Unit u;
+      decode_unit(P, G, first_units, at, u);
+      const LinearJob& J = P.job[u.job];
+      const uint32_t buf = k & 1;
+      w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
+      w.rows = min(32, u.m_end - w.row0);
+      if constexpr (FORWARD) fetch_bias<T>(P, J, u, w, half);
+      if (!mbar_wait_or_abort(&tfull[buf], (k >> 1) & 1, abort_flag)) {
+        fail();
+        break;
+      }
+      if (__any_sync(0xffffffffu, *abort_flag)) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem + buf * ACC_COLS + (static_cast<uint32_t>(quad * 32) << 16);
+      const int chunks = u.wide / 32;
+      for (int c = half; c < chunks; c += 2) {
+        float v[32];
+        __syncwarp();
+        tmem_ld_32x32(tacc + 32 * c, v);
+        if (u.kb0 == u.kb1) {                  // nothing to add up: the accumulator holds another tile
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (J.splits > 1) {
+          float4* part = part_of(J, u, u.split, rank, ew, c >> 1);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) part[32 * i + lane] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+          finish_chunk<FORWARD, T>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(tempty_even + 8u * buf);    // the even CTA's MMA issuer may reuse the accumulator
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();      // no multicast or remote arrival targets a CTA that has left
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+// The parts of a job's contraction added in order, then the epilogue: one CTA per half of a pair's tile, its warps as the
+// epilogue's.
+template <bool FORWARD, typename T>
+__global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __grid_constant__ LinearParams P, int job) {
+  __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
+  __shared__ alignas(16) uint8_t chunk[EPI_WARPS * CHUNK_BYTES];
+  __shared__ alignas(16) float bias[EPI_WARPS * 128];
+  begin_after_previous();
+  const LinearJob& J = P.job[job];
+  Groups G{groups, groups + LINEAR_MAX_GROUPS + 1, P.groups};
+  const int ew = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (ew == 0) fill_groups(G, P.ends, P.rows, lane);
+  __syncthreads();
+  const long long tile = blockIdx.x >> 1;
+  const uint32_t rank = blockIdx.x & 1;
+  if (tile >= job_units(J, G) / J.splits) return;
+  Unit u;
+  u.job = job;
+  u.split = 0;
+  decode_tile(J, G, tile, u);
+  const int quad = (ew + 2) & 3, half = ew >> 2;         // as warps 2..9 of the kernel above
+  WarpPlace w;
+  w.lane = lane;
+  w.buf = chunk + ew * CHUNK_BYTES;
+  w.bias = bias + ew * 128;
+  w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
+  w.rows = min(32, u.m_end - w.row0);
+  if (w.rows <= 0) return;
+  if constexpr (FORWARD) fetch_bias<T>(P, J, u, w, half);
+  for (int c = half; c < u.wide / 32; c += 2) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    for (int s = 0; s < J.splits; ++s) {
+      const float4* part = part_of(J, u, s, rank, ew, c >> 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 q = part[32 * i + lane];
+        v[4 * i] += q.x;
+        v[4 * i + 1] += q.y;
+        v[4 * i + 2] += q.z;
+        v[4 * i + 3] += q.w;
+      }
+    }
+    finish_chunk<FORWARD, T>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
+  }
+}
+
+// Per-device set-up (the shared-memory limit, the number of pairs that can be resident) is done by the first call on each
+// device; concurrent first calls do the same idempotent work.
+template <bool FORWARD, typename T>
+cudaError_t launch_form(const LinearParams& p, int pairs_wanted, cudaStream_t s) {
+  static std::atomic<int> resident[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int most = resident[dev].load(std::memory_order_acquire);
+  if (most == 0) {
+    e = cudaFuncSetAttribute(linear_kernel<FORWARD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&most, linear_kernel<FORWARD, T>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (most <= 0) return cudaErrorInvalidConfiguration;
+    resident[dev].store(most, std::memory_order_release);
+  }
+  const int pairs = pairs_wanted < most ? pairs_wanted : most;
+  return launch_after(linear_kernel<FORWARD, T>, dim3(2 * pairs), dim3(THREADS), SMEM, s, p, 2);
+}
+
+template <bool FORWARD, typename T>
+cudaError_t launch_join_form(const LinearParams& p, int job, long long tiles, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles));
+  cfg.blockDim = dim3(32 * EPI_WARPS);
+  cfg.stream = s;
+  cudaLaunchAttribute a[1]{};
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_join_kernel<FORWARD, T>, p, job);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearParams& p, int type, bool forward, int pairs_wanted, cudaStream_t s) {
+  if (type == MB_BF16)
+    return forward ? launch_form<true, __nv_bfloat16>(p, pairs_wanted, s) : launch_form<false, __nv_bfloat16>(p, pairs_wanted, s);
+  return forward ? launch_form<true, __half>(p, pairs_wanted, s) : launch_form<false, __half>(p, pairs_wanted, s);
+}
+
+cudaError_t launch_linear_join(const LinearParams& p, int job, int type, bool forward, long long tiles, cudaStream_t s) {
+  if (type == MB_BF16)
+    return forward ? launch_join_form<true, __nv_bfloat16>(p, job, tiles, s) : launch_join_form<false, __nv_bfloat16>(p, job, tiles, s);
+  return forward ? launch_join_form<true, __half>(p, job, tiles, s) : launch_join_form<false, __half>(p, job, tiles, s);
+}
+
+}  // namespace mb

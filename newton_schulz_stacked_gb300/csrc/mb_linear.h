@@ -1,0 +1,86 @@
+// Parameter blocks of the products with bias, activation and residual (mb_linear) between their C entries
+// (mb_linear_api.cu) and the kernels (mb_linear.cu, mb_linear_rows.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace mb {
+
+constexpr int LINEAR_MAX_GROUPS = 1024;
+constexpr int LINEAR_TILE = 256;         // rows of a pair's tile
+constexpr int LINEAR_DEEP = 64;          // of the contraction in one stage
+
+// One product D = A B^T over tiles of 256 rows x `wide` columns, by pairs of CTAs.
+//   rows of a group (forward, dx):  D's rows are the group's, B is the group's matrix;
+//   over a group's rows (dweight):  the contraction runs over them, D is the group's matrix.
+struct LinearJob {
+  CUtensorMap a, b;
+  int a_mn, b_mn;          // the operand's rows run along memory (boxes of 64 x 64), not the contraction
+  int over_rows;
+  int M;                   // over_rows: D's rows
+  int N, K;                // D's columns; the contraction (not over_rows)
+  int wide;                // 128 or 256
+  int m_tiles, n_tiles;    // m_tiles: over_rows only
+  int splits;              // parts of the contraction
+  int access;              // bytes that D's rows allow to be stored at a time: 16, 4 or 2
+  void* out;
+  long long ld, group_stride;
+  float* parts;            // splits > 1: fp32 sums of every (split, tile), laid out by the epilogue's warps
+  long long part_tiles;    // tiles that it holds for each split
+};
+
+struct LinearParams {
+  LinearJob job[2];
+  int jobs;
+  int rows, groups;
+  const int* ends;         // [groups] or null: one group of all rows
+  int status_from;         // whether this launch reports bad ends
+  // forward
+  const void* bias;        // [groups, out] or null
+  int bias_f32, act;
+  const void* residual;
+  long long residual_ld;
+  int residual_access;
+  void* z;
+  long long z_ld;
+  int z_access;
+  // dbias, from the sums over slabs of rows that the launch before made: [slabs + groups][db_cols]
+  const float* db_parts;
+  void* db;
+  int db_f32, db_cols, slab;
+  int* status;
+};
+
+// dz = dy act'(z) and the sums of dz over slabs of rows.
+struct LinearSlopeParams {
+  const void* dy;
+  long long dy_ld;
+  const void* z;           // or null: dz = dy, not written
+  long long z_ld;
+  void* dz;                // [rows, dz_ld], 16-byte aligned rows
+  long long dz_ld;
+  int act, rows, cols, groups;
+  const int* ends;
+  float* parts;            // or null
+  int slab;                // rows of a slab
+  int aligned;
+};
+
+// Rows of 2-byte elements into rows that start at 16-byte boundaries.
+struct LinearPackParams {
+  const uint16_t* src;
+  long long src_ld;
+  uint16_t* dst;
+  long long dst_ld;
+  long long rows;
+  int cols;
+};
+
+cudaError_t launch_linear(const LinearParams& p, int type, bool forward, int pairs_wanted, cudaStream_t s);
+cudaError_t launch_linear_join(const LinearParams& p, int job, int type, bool forward, long long tiles, cudaStream_t s);
+cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream_t s);
+cudaError_t launch_linear_pack(const LinearPackParams& p, int sms, cudaStream_t s);
+
+}  // namespace mb

@@ -1,0 +1,450 @@
+// C entries of the products with bias, activation and residual: checks, the plan of a call (what is copied, how the
+// products are cut), tensor maps and the launches.
+#include <cmath>
+
+#include "mb_block.h"
+#include "mb_device.cuh"
+#include "mb_linear.h"
+#include "muonbank.h"
+
+namespace mb {
+namespace {
+
+#define MB_TRY(expr)            \
+  do {                          \
+    int r_ = (expr);            \
+    if (r_ != MB_OK) return r_; \
+  } while (0)
+
+constexpr int64_t MAX_ROWS = 1ll << 30, MAX_WIDTH = 1ll << 20;
+constexpr int64_t MAX_PAIRS = 76;        // what the cuts are planned for: the pairs of a GB300's 152 SMs
+constexpr int MAX_SPLITS = 16;
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t parts_of(int64_t n, int64_t by) { return (n + by - 1) / by; }
+bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// ---------------------------------------------------------------- checks
+
+int check_two(const void* p, bool need) {
+  if (!p) return need ? MB_ERR_NULL : MB_OK;
+  return aligned(p, 2) ? MB_OK : MB_ERR_ALIGN;
+}
+
+int check_shape(int64_t rows, int64_t in, int64_t out, int64_t groups, const int32_t* ends) {
+  if (rows < 0 || rows > MAX_ROWS || in < 1 || in > MAX_WIDTH || out < 1 || out > MAX_WIDTH) return MB_ERR_SHAPE;
+  if (groups < 1 || groups > LINEAR_MAX_GROUPS || (!ends && groups != 1)) return MB_ERR_SHAPE;
+  if (groups * in * out > (1ll << 40)) return MB_ERR_SHAPE;
+  // tiles are numbered with 32 bits
+  const int64_t widest = in > out ? in : out;
+  if ((parts_of(rows, LINEAR_TILE) + groups) * parts_of(widest, 128) >= (1ll << 30)) return MB_ERR_SHAPE;
+  if (groups * parts_of(out, LINEAR_TILE) * parts_of(in, 128) >= (1ll << 30)) return MB_ERR_SHAPE;
+  return aligned(ends, 4) ? MB_OK : MB_ERR_ALIGN;
+}
+
+int check_types(int type, int bias_type, int act) {
+  if (type != MB_BF16 && type != MB_F16) return MB_ERR_ARG;
+  if (bias_type != type && bias_type != MB_F32) return MB_ERR_ARG;
+  return act >= MB_ACT_NONE && act <= MB_ACT_GELU ? MB_OK : MB_ERR_ARG;
+}
+
+bool bad_stride(int64_t stride, int64_t rows, int64_t cols, bool write) {
+  return stride < 0 || stride > (1ll << 36) || (write && rows > 1 && stride < cols);
+}
+
+// ---------------------------------------------------------------- operands
+
+// A matrix of 2-byte elements as TMA reads it: the caller's, or a copy of it in the workspace.
+struct Operand {
+  const void* base;
+  int64_t ld;
+  bool copy;
+  size_t at;               // the copy's place in the workspace
+  int64_t rows, cols;
+  const void* src;
+  int64_t src_ld;
+};
+
+Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+  Operand o{p, ld, false, 0, rows, cols, p, ld};
+  if (rows <= 1) o.ld = up(cols, 8);             // a stride that is never taken
+  o.copy = !aligned(p, 16) || o.ld % 8 != 0 || o.ld < cols;
+  if (o.copy) o.ld = up(cols, 8);
+  return o;
+}
+
+int access_of(const void* p, int64_t ld, int64_t cols, int64_t rows) {
+  const int64_t step = rows > 1 ? ld : 0;
+  if (aligned(p, 16) && step % 8 == 0 && cols % 8 == 0) return 16;
+  return aligned(p, 4) && step % 2 == 0 && cols % 2 == 0 ? 4 : 2;
+}
+
+// ---------------------------------------------------------------- plans
+
+struct Workspace {
+  size_t end = 0;
+  size_t take(int64_t bytes) {
+    const size_t at = end;
+    end += static_cast<size_t>(up(bytes, 1024));
+    return at;
+  }
+};
+
+// How a product's tiles are cut: their width, and the parts of the contraction.
+struct Cut {
+  int wide, splits;
+  int64_t tiles, blocks;   // tiles (the most that there can be), blocks of the contraction (on average)
+  size_t at;               // of the parts' sums
+};
+
+Cut cut_tiles(int64_t m_tiles, int64_t n, int64_t blocks) {
+  Cut c{};
+  // A tile of 128 columns takes about 0.6 of the time of one of 256: narrow tiles where they fill the pairs better.
+  const int64_t wide = m_tiles * parts_of(n, 256), narrow = m_tiles * parts_of(n, 128);
+  c.wide = n <= 128 || 10 * parts_of(wide, MAX_PAIRS) > 6 * parts_of(narrow, MAX_PAIRS) ? 128 : 256;
+  c.tiles = c.wide == 256 ? wide : narrow;
+  c.blocks = blocks;
+  c.splits = 1;
+  return c;
+}
+
+// The time of the busiest pair, in blocks, when its units are dealt out in turn: `first` before `second`.  An epilogue that
+// nothing hides, and the sums of a part on their way to memory and back, count as some blocks.
+double busiest(const Cut& first, int splits, const Cut* second) {
+  const double a = static_cast<double>(first.blocks) / splits + 4 + (splits > 1 ? 10 : 0);
+  const double b = second ? static_cast<double>(second->blocks) + 4 : 0;
+  const int64_t n = first.tiles * splits, all = n + (second ? second->tiles : 0);
+  double most = 0;
+  for (int64_t p = 0; p < MAX_PAIRS; ++p) {
+    const int64_t mine_a = n > p ? parts_of(n - p, MAX_PAIRS) : 0;
+    const int64_t mine = all > p ? parts_of(all - p, MAX_PAIRS) : 0;
+    const double t = mine_a * a + (mine - mine_a) * b;
+    if (t > most) most = t;
+  }
+  return most + (splits > 1 ? 12 : 0);           // the join's launch
+}
+
+void cut_contraction(Cut& c, const Cut* second) {
+  double best = busiest(c, 1, second);
+  for (int s = 2; s <= MAX_SPLITS && c.blocks / s >= 8; ++s) {
+    const double t = busiest(c, s, second);
+    if (t < 0.97 * best) {
+      best = t;
+      c.splits = s;
+    }
+  }
+}
+
+void reserve_parts(Cut& c, Workspace& ws) {
+  if (c.splits > 1) c.at = ws.take(c.splits * c.tiles * c.wide * LINEAR_TILE * 4);
+}
+
+struct ForwardPlan {
+  Operand x, w;
+  Cut y;
+  size_t end;
+};
+
+ForwardPlan plan_forward(const mb_linear_desc& d) {
+  ForwardPlan p{};
+  Workspace ws;
+  p.x = operand(d.x, d.x_stride, d.rows, d.in);
+  p.w = operand(d.weight, d.in, static_cast<int64_t>(d.groups) * d.out, d.in);
+  if (p.x.copy) p.x.at = ws.take(p.x.rows * p.x.ld * 2);
+  if (p.w.copy) p.w.at = ws.take(p.w.rows * p.w.ld * 2);
+  p.y = cut_tiles(parts_of(d.rows, LINEAR_TILE) + (d.ends ? d.groups : 0), d.out, parts_of(d.in, LINEAR_DEEP));
+  cut_contraction(p.y, nullptr);
+  reserve_parts(p.y, ws);
+  p.end = ws.end;
+  return p;
+}
+
+struct BackwardPlan {
+  bool slope;              // dz is formed (else it is dy)
+  Operand dz, x, w;
+  Cut dx, dw;
+  int slab;
+  int64_t slabs;
+  size_t db_parts, end;
+};
+
+BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
+  BackwardPlan p{};
+  Workspace ws;
+  const bool products = d.dx || d.dweight;
+  p.slope = d.activation != MB_ACT_NONE;
+  if (p.slope) {
+    p.dz = Operand{nullptr, up(d.out, 8), false, 0, d.rows, d.out, nullptr, 0};
+    p.dz.at = ws.take(d.rows * p.dz.ld * 2);
+  } else if (products) {
+    p.dz = operand(d.dy, d.dy_stride, d.rows, d.out);
+    if (p.dz.copy) p.dz.at = ws.take(p.dz.rows * p.dz.ld * 2);
+  }
+  if (d.dweight) {
+    p.x = operand(d.x, d.x_stride, d.rows, d.in);
+    if (p.x.copy) p.x.at = ws.take(p.x.rows * p.x.ld * 2);
+    p.dw = cut_tiles(d.groups * parts_of(d.out, LINEAR_TILE), d.in, parts_of(parts_of(d.rows, d.groups), LINEAR_DEEP));
+  }
+  if (d.dx) {
+    p.w = operand(d.weight, d.in, static_cast<int64_t>(d.groups) * d.out, d.in);
+    if (p.w.copy) p.w.at = ws.take(p.w.rows * p.w.ld * 2);
+    p.dx = cut_tiles(parts_of(d.rows, LINEAR_TILE) + (d.ends ? d.groups : 0), d.in, parts_of(d.out, LINEAR_DEEP));
+  }
+  if (d.dweight) cut_contraction(p.dw, d.dx ? &p.dx : nullptr);
+  else if (d.dx) cut_contraction(p.dx, nullptr);
+  if (d.dweight) reserve_parts(p.dw, ws);
+  if (d.dx) reserve_parts(p.dx, ws);
+  // slabs of rows: about four CTAs for an SM, 32 to 1024 rows
+  const int64_t columns = parts_of(d.out, 256);
+  int64_t slab = up(parts_of(d.rows * columns, 608), 32);
+  slab = slab < 32 ? 32 : slab > 1024 ? 1024 : slab;
+  if (parts_of(d.rows, slab) > 65535) slab = up(parts_of(d.rows, 65535), 32);
+  p.slab = static_cast<int>(slab);
+  p.slabs = parts_of(d.rows, slab);
+  if (d.dbias) p.db_parts = ws.take((p.slabs + d.groups) * d.out * 4);
+  p.end = ws.end;
+  return p;
+}
+
+// ---------------------------------------------------------------- calls
+
+struct Call {
+  cudaStream_t stream;
+  int type, sms, launches;
+  int* status;
+  uint8_t* ws;
+
+  // The operand's copy in the workspace, where it needs one.
+  int lay_out(Operand& o) {
+    if (!o.copy) return MB_OK;
+    o.base = ws + o.at;
+    const LinearPackParams p{static_cast<const uint16_t*>(o.src), o.src_ld, reinterpret_cast<uint16_t*>(ws + o.at), o.ld,
+                             o.rows, static_cast<int>(o.cols)};
+    const cudaError_t e = launch_linear_pack(p, sms, stream);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    ++launches;
+    return MB_OK;
+  }
+  int map(CUtensorMap* m, const Operand& o, int64_t rows, int64_t batch, int box_rows) const {
+    return api_encode_rows(m, o.base, type == MB_BF16, o.cols, rows, batch, o.ld, box_rows);
+  }
+};
+
+void set_cut(LinearJob& j, const Cut& c, uint8_t* ws) {
+  j.wide = c.wide;
+  j.n_tiles = static_cast<int>(parts_of(j.N, c.wide));
+  j.splits = c.splits;
+  j.parts = c.splits > 1 ? reinterpret_cast<float*>(ws + c.at) : nullptr;
+  j.part_tiles = c.tiles;
+}
+
+int run_products(const LinearParams& p, const Cut* const cuts[2], bool forward, Call& call) {
+  int64_t units = 0;
+  for (int j = 0; j < p.jobs; ++j) units += cuts[j]->tiles * cuts[j]->splits;
+  // (a launch without tiles still has rows to clear and sums to finish)
+  const int pairs = static_cast<int>(p.jobs == 0 ? MAX_PAIRS : units < 1 ? 1 : units < 4096 ? units : 4096);
+  cudaError_t e = launch_linear(p, call.type, forward, pairs, call.stream);
+  if (e != cudaSuccess) return api_cuda_fail(e);
+  ++call.launches;
+  for (int j = 0; j < p.jobs; ++j) {
+    if (cuts[j]->splits == 1) continue;
+    e = launch_linear_join(p, j, call.type, forward, cuts[j]->tiles, call.stream);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    ++call.launches;
+  }
+  return MB_OK;
+}
+
+int begin_call(Call& call, int type, void* workspace, size_t bytes, size_t need, void* cuda_stream) {
+  if (need > 0) {
+    if (!workspace || bytes < need) return MB_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MB_ERR_ALIGN;
+  }
+  call = Call{static_cast<cudaStream_t>(cuda_stream), type, 0, 0, nullptr, static_cast<uint8_t*>(workspace)};
+  MB_TRY(api_device_sms(&call.sms));
+  return api_device_status(&call.status);
+}
+
+int check_forward(const mb_linear_desc& d) {
+  MB_TRY(check_shape(d.rows, d.in, d.out, d.groups, d.ends));
+  MB_TRY(check_types(d.type, d.bias_type, d.activation));
+  if (bad_stride(d.x_stride, d.rows, d.in, false) || bad_stride(d.y_stride, d.rows, d.out, true) ||
+      (d.residual && bad_stride(d.residual_stride, d.rows, d.out, false)) ||
+      (d.z && bad_stride(d.z_stride, d.rows, d.out, true)))
+    return MB_ERR_SHAPE;
+  const bool some = d.rows > 0;
+  MB_TRY(check_two(d.x, some));
+  MB_TRY(check_two(d.y, some));
+  MB_TRY(check_two(d.weight, some));
+  MB_TRY(check_two(d.residual, false));
+  MB_TRY(check_two(d.z, false));
+  if (d.bias && !aligned(d.bias, d.bias_type == MB_F32 ? 4 : 2)) return MB_ERR_ALIGN;
+  return MB_OK;
+}
+
+int check_backward(const mb_linear_backward_desc& d) {
+  MB_TRY(check_shape(d.rows, d.in, d.out, d.groups, d.ends));
+  MB_TRY(check_types(d.type, d.bias_type, d.activation));
+  const bool slope = d.activation != MB_ACT_NONE, some = d.rows > 0;
+  if (bad_stride(d.dy_stride, d.rows, d.out, false) || (d.dweight && bad_stride(d.x_stride, d.rows, d.in, false)) ||
+      (slope && bad_stride(d.z_stride, d.rows, d.out, false)) || (d.dx && bad_stride(d.dx_stride, d.rows, d.in, true)))
+    return MB_ERR_SHAPE;
+  MB_TRY(check_two(d.dy, some));
+  MB_TRY(check_two(d.x, some && d.dweight));
+  MB_TRY(check_two(d.weight, some && d.dx));
+  MB_TRY(check_two(d.z, some && slope));
+  MB_TRY(check_two(d.dx, false));
+  MB_TRY(check_two(d.dweight, false));
+  if (d.dbias && !aligned(d.dbias, d.bias_type == MB_F32 ? 4 : 2)) return MB_ERR_ALIGN;
+  return MB_OK;
+}
+
+}  // namespace
+}  // namespace mb
+
+using namespace mb;
+
+extern "C" {
+
+int mb_linear_workspace_bytes(const mb_linear_desc* desc, size_t* out_bytes) {
+  if (!desc || !out_bytes) return MB_ERR_NULL;
+  MB_TRY(check_forward(*desc));
+  *out_bytes = desc->rows == 0 ? 0 : plan_forward(*desc).end;
+  return MB_OK;
+}
+
+int mb_linear(const mb_linear_desc* desc, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  if (!desc) return MB_ERR_NULL;
+  const mb_linear_desc& d = *desc;
+  MB_TRY(check_forward(d));
+  if (d.rows == 0) return MB_OK;
+  ForwardPlan plan = plan_forward(d);
+  Call call{};
+  MB_TRY(begin_call(call, d.type, workspace, workspace_bytes, plan.end, cuda_stream));
+  MB_TRY(call.lay_out(plan.x));
+  MB_TRY(call.lay_out(plan.w));
+  LinearParams p{};
+  p.jobs = 1;
+  p.rows = static_cast<int>(d.rows);
+  p.groups = d.groups;
+  p.ends = d.ends;
+  p.status = call.status;
+  p.status_from = 1;
+  p.bias = d.bias;
+  p.bias_f32 = d.bias_type == MB_F32;
+  p.act = d.activation;
+  p.residual = d.residual;
+  p.residual_ld = d.residual_stride;
+  p.residual_access = access_of(d.residual, d.residual_stride, d.out, d.rows);
+  p.z = d.z;
+  p.z_ld = d.z_stride;
+  p.z_access = access_of(d.z, d.z_stride, d.out, d.rows);
+  LinearJob& j = p.job[0];
+  j.N = d.out;
+  j.K = d.in;
+  j.out = d.y;
+  j.ld = d.y_stride;
+  j.access = access_of(d.y, d.y_stride, d.out, d.rows);
+  set_cut(j, plan.y, call.ws);
+  MB_TRY(call.map(&j.a, plan.x, d.rows, 1, 128));
+  MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, j.wide / 2));
+  const Cut* const cuts[2] = {&plan.y, nullptr};
+  MB_TRY(run_products(p, cuts, true, call));
+  api_launched(MB_MARK_LINEAR, call.launches, call.stream);
+  return MB_OK;
+}
+
+int mb_linear_backward_workspace_bytes(const mb_linear_backward_desc* desc, size_t* out_bytes) {
+  if (!desc || !out_bytes) return MB_ERR_NULL;
+  MB_TRY(check_backward(*desc));
+  *out_bytes = desc->rows == 0 ? 0 : plan_backward(*desc).end;
+  return MB_OK;
+}
+
+int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  if (!desc) return MB_ERR_NULL;
+  const mb_linear_backward_desc& d = *desc;
+  MB_TRY(check_backward(d));
+  if (!d.dx && !d.dweight && !d.dbias) return MB_OK;
+  Call call{};
+  if (d.rows == 0) {                             // sums over nothing
+    MB_TRY(begin_call(call, d.type, workspace, workspace_bytes, 0, cuda_stream));
+    const size_t n = static_cast<size_t>(d.groups) * d.out;
+    cudaError_t e = cudaSuccess;
+    if (d.dweight) e = cudaMemsetAsync(d.dweight, 0, n * d.in * 2, call.stream);
+    if (e == cudaSuccess && d.dbias) e = cudaMemsetAsync(d.dbias, 0, n * (d.bias_type == MB_F32 ? 4 : 2), call.stream);
+    return e == cudaSuccess ? MB_OK : api_cuda_fail(e);
+  }
+  BackwardPlan plan = plan_backward(d);
+  MB_TRY(begin_call(call, d.type, workspace, workspace_bytes, plan.end, cuda_stream));
+  if (plan.slope) plan.dz.base = call.ws + plan.dz.at;
+  else if (d.dx || d.dweight) MB_TRY(call.lay_out(plan.dz));
+  if (d.dweight) MB_TRY(call.lay_out(plan.x));
+  if (d.dx) MB_TRY(call.lay_out(plan.w));
+  if (plan.slope || d.dbias) {
+    LinearSlopeParams s{};
+    s.dy = d.dy;
+    s.dy_ld = d.dy_stride;
+    s.z = plan.slope ? d.z : nullptr;
+    s.z_ld = d.z_stride;
+    s.dz = plan.slope ? call.ws + plan.dz.at : nullptr;
+    s.dz_ld = plan.dz.ld;
+    s.act = d.activation;
+    s.rows = static_cast<int>(d.rows);
+    s.cols = d.out;
+    s.groups = d.groups;
+    s.ends = d.ends;
+    s.parts = d.dbias ? reinterpret_cast<float*>(call.ws + plan.db_parts) : nullptr;
+    s.slab = plan.slab;
+    s.aligned = access_of(d.dy, d.dy_stride, d.out, d.rows) == 16 &&
+                (!plan.slope || access_of(d.z, d.z_stride, d.out, d.rows) == 16);
+    const cudaError_t e = launch_linear_slope(s, d.type, call.stream);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    ++call.launches;
+  }
+  LinearParams p{};
+  p.rows = static_cast<int>(d.rows);
+  p.groups = d.groups;
+  p.ends = d.ends;
+  p.status = call.status;
+  p.status_from = 1;
+  p.db = d.dbias;
+  p.db_parts = reinterpret_cast<const float*>(call.ws + plan.db_parts);
+  p.db_f32 = d.bias_type == MB_F32;
+  p.db_cols = d.out;
+  p.slab = plan.slab;
+  const Cut* cuts[2] = {nullptr, nullptr};
+  if (d.dweight) {                               // the longer units first
+    LinearJob& j = p.job[p.jobs];
+    cuts[p.jobs++] = &plan.dw;
+    j.over_rows = j.a_mn = j.b_mn = 1;
+    j.M = d.out;
+    j.m_tiles = static_cast<int>(parts_of(d.out, LINEAR_TILE));
+    j.N = d.in;
+    j.out = d.dweight;
+    j.ld = d.in;
+    j.group_stride = static_cast<int64_t>(d.out) * d.in;
+    j.access = access_of(d.dweight, d.in, d.in, 2);
+    set_cut(j, plan.dw, call.ws);
+    MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 64));
+    MB_TRY(call.map(&j.b, plan.x, d.rows, 1, 64));
+  }
+  if (d.dx) {
+    LinearJob& j = p.job[p.jobs];
+    cuts[p.jobs++] = &plan.dx;
+    j.b_mn = 1;
+    j.N = d.in;
+    j.K = d.out;
+    j.out = d.dx;
+    j.ld = d.dx_stride;
+    j.access = access_of(d.dx, d.dx_stride, d.in, d.rows);
+    set_cut(j, plan.dx, call.ws);
+    MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 128));
+    MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, 64));
+  }
+  MB_TRY(run_products(p, cuts, false, call));
+  api_launched(MB_MARK_LINEAR_BACKWARD, call.launches, call.stream);
+  return MB_OK;
+}
+
+}  // extern "C"

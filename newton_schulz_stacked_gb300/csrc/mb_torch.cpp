@@ -538,6 +538,164 @@ PyObject* router_backward(PyObject* const* a, Py_ssize_t n) {
   return give(a[9], dl);
 }
 
+// ---------------------------------------------------------------- linear
+
+int activation_of(PyObject* o) {
+  const char* names[] = {"none", "relu", "relu2", "silu", "gelu"};
+  if (PyUnicode_Check(o))
+    for (int i = 0; i < 5; ++i)
+      if (PyUnicode_CompareWithASCIIString(o, names[i]) == 0) return i;
+  throw Refused{"activation must be 'none', 'relu', 'relu2', 'silu' or 'gelu'"};
+}
+
+struct LinearShape {
+  int64_t rows, in, out, groups;
+  int type;
+  const int32_t* ends;
+  c10::DimVector lead;        // of x, without its last dimension
+  c10::DimVector param;       // of a bias
+};
+
+LinearShape linear_shape(const Tensor& x, const Tensor& w, PyObject* ends) {
+  LinearShape s{};
+  if (x.dim() < 1) throw Refused{"x must have at least one dimension"};
+  if (w.dim() != 2 && w.dim() != 3) throw Refused{"weight must be [out, in], or [groups, out, in] with ends"};
+  if (x.scalar_type() != ScalarType::BFloat16 && x.scalar_type() != ScalarType::Half)
+    throw Refused{std::string("x has dtype ") + c10::toString(x.scalar_type()) + ", expected bfloat16 or float16"};
+  s.type = type_of(x, "x");
+  const auto wn = w.sizes();
+  s.in = wn[w.dim() - 1];
+  s.out = wn[w.dim() - 2];
+  s.groups = w.dim() == 3 ? wn[0] : 1;
+  if (s.in == 0 || s.out == 0 || s.groups == 0) throw Refused{"weight has no elements"};
+  if (s.in > 1 << 20 || s.out > 1 << 20 || s.groups > 1024) checked("mb_linear", MB_ERR_SHAPE);
+  if (x.sizes().back() != s.in)
+    throw Refused{"x is " + str(x) + ", its last dimension must be the weight's " + std::to_string(s.in)};
+  dense(&w, "weight", wn, x.scalar_type(), x.device());
+  s.rows = x.numel() / s.in;
+  if (s.rows > 1ll << 30) checked("mb_linear", MB_ERR_SHAPE);
+  s.lead.assign(x.sizes().begin(), x.sizes().end() - 1);
+  const Tensor* e = tensor_or_none(ends, "ends");
+  if ((e != nullptr) != (w.dim() == 3))
+    throw Refused{e ? "ends needs a weight of [groups, out, in]" : "a weight of [groups, out, in] needs ends"};
+  if (e) s.ends = static_cast<const int32_t*>(dense(e, "ends", {s.groups}, ScalarType::Int, x.device()));
+  s.param.assign(wn.begin(), wn.end() - 1);
+  return s;
+}
+
+c10::DimVector with(const c10::DimVector& lead, int64_t last) {
+  c10::DimVector d(lead);
+  d.push_back(last);
+  return d;
+}
+
+// x, weight, bias, residual, activation, ends, keep, y, z, workspace, stream
+PyObject* linear(PyObject* const* a, Py_ssize_t n) {
+  const Tensor &x = cuda_tensor(a[0], "x"), &w = tensor(a[1], "weight");
+  const auto device = x.device();
+  const auto dtype = x.scalar_type();
+  Where where(x, a[10], a, n);
+  const LinearShape s = linear_shape(x, w, a[5]);
+  const auto shape = with(s.lead, s.out);
+  mb_linear_desc d{};
+  d.activation = activation_of(a[4]);
+  const Tensor* bias = tensor_or_none(a[2], "bias");
+  d.bias_type = MB_F32;
+  if (bias) {
+    if (bias->scalar_type() != dtype && bias->scalar_type() != ScalarType::Float)
+      throw Refused{std::string("bias has dtype ") + c10::toString(bias->scalar_type()) + ", expected x's or float32"};
+    d.bias_type = type_of(*bias, "bias");
+    d.bias = dense(bias, "bias", s.param, bias->scalar_type(), device);
+  }
+  const Tensor* residual = tensor_or_none(a[3], "residual");
+  if (residual) {
+    like(*residual, "residual", shape, dtype, device);
+    d.residual = residual->data_ptr();
+    d.residual_stride = row_stride(*residual, "residual");
+  }
+  const Tensor y = result(a[7], "y", shape, dtype, device);
+  Tensor z;
+  if (a[8] != Py_None || truth(a[6])) {
+    z = result(a[8], "z", shape, dtype, device);
+    d.z = z.data_ptr();
+    d.z_stride = row_stride(z, "z");
+  }
+  d.x = x.data_ptr();
+  d.x_stride = row_stride(x, "x");
+  d.weight = w.data_ptr();
+  d.ends = s.ends;
+  d.y = y.data_ptr();
+  d.y_stride = row_stride(y, "y");
+  d.rows = s.rows;
+  d.in = static_cast<int32_t>(s.in);
+  d.out = static_cast<int32_t>(s.out);
+  d.groups = static_cast<int32_t>(s.groups);
+  d.type = s.type;
+  size_t need = 0;
+  checked("mb_linear_workspace_bytes", mb_linear_workspace_bytes(&d, &need));
+  const Workspace ws(a[9], need, device);
+  checked("mb_linear", unlocked([&] { return mb_linear(&d, ws.ptr, ws.bytes, where.stream); }));
+  return tuple(give(a[7], y), give(a[8], z));
+}
+
+// dy, x, weight, z, activation, ends, input_grad, weight_grad, bias (whether its gradient is wanted), dx, dweight, dbias,
+// workspace, stream
+PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
+  const Tensor &x = cuda_tensor(a[1], "x"), &w = tensor(a[2], "weight"), &dy = tensor(a[0], "dy");
+  const auto device = x.device();
+  const auto dtype = x.scalar_type();
+  Where where(x, a[13], a, n);
+  const LinearShape s = linear_shape(x, w, a[5]);
+  const auto shape = with(s.lead, s.out);
+  mb_linear_backward_desc d{};
+  d.activation = activation_of(a[4]);
+  like(dy, "dy", shape, dtype, device);
+  d.dy = dy.data_ptr();
+  d.dy_stride = row_stride(dy, "dy");
+  if (d.activation != MB_ACT_NONE) {
+    const Tensor* z = tensor_or_none(a[3], "z");
+    if (!z) throw Refused{"the gradient of an activation needs z (keep=True in the forward call)"};
+    like(*z, "z", shape, dtype, device);
+    d.z = z->data_ptr();
+    d.z_stride = row_stride(*z, "z");
+  }
+  Tensor dx, dw, db;
+  if (a[9] != Py_None || truth(a[6])) {
+    dx = result(a[9], "dx", x.sizes(), dtype, device);
+    d.dx = dx.data_ptr();
+    d.dx_stride = row_stride(dx, "dx");
+  }
+  if (a[10] != Py_None || truth(a[7])) {
+    dw = result(a[10], "dweight", w.sizes(), dtype, device);
+    d.dweight = dense(&dw, "dweight", w.sizes(), dtype, device);
+  }
+  d.bias_type = s.type;
+  if (a[11] != Py_None || truth(a[8])) {
+    const Tensor* given = tensor_or_none(a[11], "dbias");
+    auto type = dtype;
+    if (given && given->scalar_type() == ScalarType::Float) {
+      type = ScalarType::Float;
+      d.bias_type = MB_F32;
+    }
+    db = result(a[11], "dbias", s.param, type, device);
+    d.dbias = dense(&db, "dbias", s.param, type, device);
+  }
+  d.x = x.data_ptr();
+  d.x_stride = row_stride(x, "x");
+  d.weight = w.data_ptr();
+  d.ends = s.ends;
+  d.rows = s.rows;
+  d.in = static_cast<int32_t>(s.in);
+  d.out = static_cast<int32_t>(s.out);
+  d.groups = static_cast<int32_t>(s.groups);
+  d.type = s.type;
+  size_t need = 0;
+  checked("mb_linear_backward_workspace_bytes", mb_linear_backward_workspace_bytes(&d, &need));
+  const Workspace ws(a[12], need, device);
+  checked("mb_linear_backward", unlocked([&] { return mb_linear_backward(&d, ws.ptr, ws.bytes, where.stream); }));
+  return tuple(give(a[9], dx), give(a[10], dw), give(a[11], db));
+}
+
 // ---------------------------------------------------------------- AdamW
 
 // The tensors of a call as descriptors, and the ones that it writes.
@@ -764,6 +922,8 @@ PyMethodDef g_methods[] = {method<layer_norm, 8>("mb_layer_norm"),
                            method<rotary_backward, 9>("mb_rotary_backward"),
                            method<router, 11>("mb_router"),
                            method<router_backward, 11>("mb_router_backward"),
+                           method<linear, 11>("mb_linear"),
+                           method<linear_backward, 14>("mb_linear_backward"),
                            method<adamw, 10>("adamw_multi_step"),
                            method<adamw_dev, 6>("adamw_multi_step_dev"),
                            {nullptr, nullptr, 0, nullptr}};
