@@ -15,8 +15,9 @@
 // infinity would not be zero), and the MMAs wait for both CTAs' warps.  Rows past the tensor, and columns past its
 // width, are read as zeros by TMA.
 //
-// Roles (11 warps, both CTAs):
-//   warp 0 lane 0   TMA producer, a ring of STAGES blocks; the bytes of both CTAs complete on the even CTA's barrier
+// Roles (12 warps, both CTAs):
+//   warps 0 and 11  lane 0: TMA producers of the A and the B operand, a ring of STAGES blocks; the bytes of both CTAs complete
+//                   on the even CTA's barrier
 //   warp 1          TMEM; lane 0 of the even CTA issues the MMAs and releases stages in both CTAs
 //   warps 2..9      epilogue of the CTA's 128 rows, two warps per 32 TMEM lanes, 32 x 32 chunks through shared memory to
 //                   row-wise stores; before its first tile each takes a share of what else the call leaves to do: zeros in
@@ -26,6 +27,7 @@
 // A long contraction over few tiles is cut into parts whose fp32 sums go to the workspace, and linear_join_kernel adds them
 // in order.
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "mb_block.h"
@@ -39,8 +41,8 @@ constexpr int STAGES = 5;
 constexpr int TILE_BYTES = BM * LINEAR_DEEP * 2;     // 16 KB: a CTA's rows of one operand's block
 constexpr int BOX_BYTES = 64 * LINEAR_DEEP * 2;      // 8 KB: one 64 x 64 box
 constexpr int EPI_WARPS = 8;
-constexpr int FIX_WARP = 2 + EPI_WARPS;
-constexpr int THREADS = 32 * (FIX_WARP + 1);
+constexpr int A_WARP = 0, FIX_WARP = 2 + EPI_WARPS, B_WARP = FIX_WARP + 1;
+constexpr int THREADS = 32 * (B_WARP + 1);
 constexpr int BIAS_BYTES = 4 * 32 * 4;               // per epilogue warp
 constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * (CHUNK_BYTES + BIAS_BYTES) + GROUPS_BYTES + 1024 /* alignment */ +
                      512 /* barriers */;
@@ -72,9 +74,36 @@ __device__ __forceinline__ void tmem_ld_32x32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Whether block kb of a unit reaches into the next group's rows.
-__device__ __forceinline__ bool reaches_past(const LinearParams& P, const LinearJob& J, const Unit& u, int kb) {
-  return J.over_rows && u.k_end < P.rows && u.k_begin + (kb + 1) * LINEAR_DEEP > u.k_end;
+// The first block of a unit that reaches into the next group's rows (the last block, or none: INT_MAX).
+__device__ __forceinline__ int past_from(const LinearParams& P, const LinearJob& J, const Unit& u) {
+  const int whole = (u.k_end - u.k_begin) / LINEAR_DEEP;
+  return J.over_rows && u.k_end < P.rows && whole * LINEAR_DEEP < u.k_end - u.k_begin ? whole : INT_MAX;
+}
+
+// How a CTA loads one operand of a unit, block after block: held in registers, since a loop that reads the parameters again
+// for each block (as the compiler does behind a barrier's memory clobber) costs the producer more than the MMAs take.
+struct Feed {
+  const CUtensorMap* map;
+  int x, y, x_step, y_step, batch, boxes;
+  uint32_t bytes;          // of both operands
+  int past_from;
+};
+__device__ __forceinline__ Feed feed_of(const LinearParams& P, const Unit& u, bool for_a, uint32_t rank) {
+  const LinearJob& J = P.job[u.job];
+  Feed f;
+  f.map = for_a ? &J.a : &J.b;
+  const int mn = for_a ? u.m0 + static_cast<int>(rank) * BM : u.n0 + static_cast<int>(rank) * (u.wide >> 1);
+  const int k = u.k_begin + u.kb0 * LINEAR_DEEP;
+  const bool turned = for_a ? J.a_mn : J.b_mn;
+  f.x = turned ? mn : k;
+  f.y = turned ? k : mn;
+  f.x_step = turned ? 0 : LINEAR_DEEP;
+  f.y_step = turned ? LINEAR_DEEP : 0;
+  f.batch = for_a || J.over_rows ? 0 : u.group;
+  f.boxes = !turned ? 1 : for_a ? 2 : u.wide >> 7;
+  f.bytes = TILE_BYTES + (J.b_mn ? (u.wide >> 7) * BOX_BYTES : (J.wide >> 1) * LINEAR_DEEP * 2);
+  f.past_from = past_from(P, J, u);
+  return f;
 }
 
 // A share of the work beside the tiles, by the epilogue's warps: warp `me` of `all`.
@@ -181,53 +210,41 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   const long long first_units = P.jobs > 0 ? job_units(P.job[0], G) : 0;
   const long long units = first_units + (P.jobs > 1 ? job_units(P.job[1], G) : 0);
 
-  if (warp == 0) {
+  if (warp == A_WARP || warp == B_WARP) {
     if (lane == 0) {
-      // ---------------- TMA producer (both CTAs)
-      for (int j = 0; j < P.jobs; ++j) {
-        tma_prefetch_map(&P.job[j].a);
-        tma_prefetch_map(&P.job[j].b);
-      }
+      // ---------------- TMA producer of one operand (both CTAs); the A operand's also announces the bytes of both
+      const bool for_a = warp == A_WARP;
+      for (int j = 0; j < P.jobs; ++j) tma_prefetch_map(for_a ? &P.job[j].a : &P.job[j].b);
       const uint32_t full_even = map_to_rank(&full[0], 0), past_own = map_to_rank(&past[0], rank);
+      uint8_t* const ring = for_a ? sA : sB;
       int st = 0;
       uint32_t ph = 0, it = 0;
       bool ok = true;
       for (long long at = pair; at < units && ok && !*abort_flag; at += pairs) {
         Unit u;
         decode_unit(P, G, first_units, at, u);
-        const LinearJob& J = P.job[u.job];
-        const int m0 = u.m0 + static_cast<int>(rank) * BM, n0 = u.n0 + static_cast<int>(rank) * (u.wide >> 1);
-        const int b_boxes = u.wide >> 7;
-        const uint32_t b_bytes = J.b_mn ? b_boxes * BOX_BYTES : (J.wide >> 1) * LINEAR_DEEP * 2;
-        const int batch = J.over_rows ? 0 : u.group;
+        const Feed f = feed_of(P, u, for_a, rank);
+        int x = f.x, y = f.y;
         for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
           if (it >= STAGES && !mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          uint32_t bar = full_even + 8u * static_cast<uint32_t>(st);
-          if (!reaches_past(P, J, u, kb)) {
-            if (even) mbar_expect_tx(&full[st], 2u * (TILE_BYTES + b_bytes));   // both CTAs' boxes
-          } else {
-            if (even) mbar_arrive(&full[st]);
-            bar = past_own + 8u * static_cast<uint32_t>(st);
-            mbar_expect_tx(&past[st], TILE_BYTES + b_bytes);
+          const uint32_t bar = (kb < f.past_from ? full_even : past_own) + 8u * static_cast<uint32_t>(st);
+          if (for_a) {
+            if (kb < f.past_from) {
+              if (even) mbar_expect_tx(&full[st], 2u * f.bytes);
+            } else {
+              if (even) mbar_arrive(&full[st]);
+              mbar_expect_tx(&past[st], f.bytes);
+            }
           }
-          uint8_t* a = sA + st * TILE_BYTES;
-          uint8_t* b = sB + st * TILE_BYTES;
-          const int k0 = u.k_begin + kb * LINEAR_DEEP;
-          if (!J.a_mn) {
-            tma_load_3d_pair(a, &J.a, bar, k0, m0, 0);
-          } else {
-            tma_load_3d_pair(a, &J.a, bar, m0, k0, 0);
-            tma_load_3d_pair(a + BOX_BYTES, &J.a, bar, m0 + 64, k0, 0);
-          }
-          if (!J.b_mn) {
-            tma_load_3d_pair(b, &J.b, bar, k0, n0, batch);
-          } else {
-            for (int c = 0; c < b_boxes; ++c) tma_load_3d_pair(b + c * BOX_BYTES, &J.b, bar, n0 + 64 * c, k0, batch);
-          }
+          uint8_t* to = ring + st * TILE_BYTES;
+          tma_load_3d_pair(to, f.map, bar, x, y, f.batch);
+          if (f.boxes > 1) tma_load_3d_pair(to + BOX_BYTES, f.map, bar, x + 64, y, f.batch);
+          x += f.x_step;
+          y += f.y_step;
           if (++st == STAGES) {
             st = 0;
             ph ^= 1u;
@@ -261,14 +278,15 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
         const uint32_t a_step = J.a_mn ? 2048u : 32u, b_step = J.b_mn ? 2048u : 32u;
         const uint32_t a_lbo = J.a_mn ? BOX_BYTES : 16u, b_lbo = J.b_mn ? BOX_BYTES : 16u;
-        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+        const int past_at = past_from(P, J, u), kb0 = u.kb0, kb1 = u.kb1;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int st = it % STAGES;
           if (!mbar_wait_or_abort(&full[st], (it / STAGES) & 1, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          if (reaches_past(P, J, u, kb)) {
+          if (kb >= past_at) {
             if (!mbar_wait_cluster_or_abort(&cleared[st], (past_phase >> st) & 1u, abort_flag)) {
               fail();
               ok = false;
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
 #pragma unroll
           for (int kk = 0; kk < LINEAR_DEEP / 16; ++kk) {
             umma_bf16_pair(dacc, smem_desc_sw128(a0 + kk * a_step, a_lbo, 1024),
-                           smem_desc_sw128(b0 + kk * b_step, b_lbo, 1024), idesc, (kb > u.kb0 || kk > 0) ? 1u : 0u);
+                           smem_desc_sw128(b0 + kk * b_step, b_lbo, 1024), idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
           }
           umma_commit_pair_both(&empty[st]);   // the stage may be refilled in both CTAs
         }
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       decode_unit(P, G, first_units, at, u);
       const LinearJob& J = P.job[u.job];
       const int blocks = u.kb1 - u.kb0;
-      if (blocks > 0 && reaches_past(P, J, u, u.kb1 - 1)) {      // only a group's last block does
+      if (blocks > 0 && u.kb1 - 1 >= past_from(P, J, u)) {      // only a group's last block does
         const int st = (it + blocks - 1) % STAGES;
         if (!mbar_wait_or_abort(&past[st], (past_phase >> st) & 1u, abort_flag)) {
           fail();
