@@ -16,13 +16,15 @@
 // width, are read as zeros by TMA.
 //
 // Roles (12 warps, both CTAs):
-//   warps 0 and 11  lane 0: TMA producers of the A and the B operand, a ring of STAGES blocks; the bytes of both CTAs complete
+//   warps 0 and 11  TMA producers of the A and the B operand, a ring of STAGES blocks; the bytes of both CTAs complete
 //                   on the even CTA's barrier
-//   warp 1          TMEM; lane 0 of the even CTA issues the MMAs and releases stages in both CTAs
+//   warp 1          TMEM; in the even CTA it issues the MMAs and releases stages in both CTAs
 //   warps 2..9      epilogue of the CTA's 128 rows, two warps per 32 TMEM lanes, 32 x 32 chunks through shared memory to
 //                   row-wise stores; before its first tile each takes a share of what else the call leaves to do: zeros in
 //                   rows of no group, dbias from the slabs' sums
 //   warp 10         clears the blocks that reach past a group
+// Producers and issuer run as whole warps, the same in all lanes, and elect a lane for each TMA copy, MMA or commit: those take
+// their operands from uniform registers, and values that one lane alone has worked out are moved there one by one.
 //
 // A long contraction over few tiles is cut into parts whose fp32 sums go to the workspace, and linear_join_kernel adds them
 // in order.
@@ -44,7 +46,7 @@ constexpr int EPI_WARPS = 8;
 constexpr int A_WARP = 0, FIX_WARP = 2 + EPI_WARPS, B_WARP = FIX_WARP + 1;
 constexpr int THREADS = 32 * (B_WARP + 1);
 constexpr int BIAS_BYTES = 4 * 32 * 4;               // per epilogue warp
-constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * (CHUNK_BYTES + BIAS_BYTES) + GROUPS_BYTES + 1024 /* alignment */ +
+constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * (2 * CHUNK_BYTES + BIAS_BYTES) + GROUPS_BYTES + 1024 /* alignment */ +
                      512 /* barriers */;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t ACC_COLS = 256, TMEM_COLS = 512;
@@ -57,8 +59,8 @@ __device__ __forceinline__ uint32_t instruction(int n, int a_mn, int b_mn) {
          static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(256 >> 4) << 24;
 }
 
-__device__ __forceinline__ void tmem_ld_32x32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
+// 32 lanes x 32 columns of sums: the load, and the wait that its registers are ready after.
+__device__ __forceinline__ void tmem_ld_32x32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -69,9 +71,41 @@ __device__ __forceinline__ void tmem_ld_32x32(uint32_t taddr, float (&v)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_ready(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ int same(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// A unit as the producers and the MMA issuer take it: the same in all lanes, and known to be (shuffled from one).
+__device__ __forceinline__ void decode_same(const LinearParams& P, const Groups& G, int first_units, int at, Unit& u) {
+  decode_unit(P, G, first_units, at, u);
+  u.job = same(u.job);
+  u.group = same(u.group);
+  u.m0 = same(u.m0);
+  u.n0 = same(u.n0);
+  u.wide = same(u.wide);
+  u.k_begin = same(u.k_begin);
+  u.k_end = same(u.k_end);
+  u.kb0 = same(u.kb0);
+  u.kb1 = same(u.kb1);
 }
 
 // The first block of a unit that reaches into the next group's rows (the last block, or none: INT_MAX).
@@ -151,7 +185,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * TILE_BYTES;
   uint8_t* sChunk = sB + STAGES * TILE_BYTES;
-  uint8_t* sBias = sChunk + EPI_WARPS * CHUNK_BYTES;
+  uint8_t* sBias = sChunk + EPI_WARPS * 2 * CHUNK_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(sBias + EPI_WARPS * BIAS_BYTES);   // [STAGES] (even) both CTAs' operands landed
   uint64_t* empty = full + STAGES;           // [STAGES] the pair's MMAs are done with the stage
   uint64_t* past = empty + STAGES;           // [STAGES] this CTA's part of a block that reaches past its group landed
@@ -165,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   G.tile = G.row + LINEAR_MAX_GROUPS + 1;
   G.n = P.groups;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = same(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool even = rank == 0;
 
@@ -206,112 +240,117 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     *abort_flag = 1;
   }
 
-  const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const long long first_units = P.jobs > 0 ? job_units(P.job[0], G) : 0;
-  const long long units = first_units + (P.jobs > 1 ? job_units(P.job[1], G) : 0);
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int first_units = P.jobs > 0 ? job_units(P.job[0], G) : 0;
+  const int units = first_units + (P.jobs > 1 ? job_units(P.job[1], G) : 0);
 
   if (warp == A_WARP || warp == B_WARP) {
-    if (lane == 0) {
-      // ---------------- TMA producer of one operand (both CTAs); the A operand's also announces the bytes of both
-      const bool for_a = warp == A_WARP;
-      for (int j = 0; j < P.jobs; ++j) tma_prefetch_map(for_a ? &P.job[j].a : &P.job[j].b);
-      const uint32_t full_even = map_to_rank(&full[0], 0), past_own = map_to_rank(&past[0], rank);
-      uint8_t* const ring = for_a ? sA : sB;
-      int st = 0;
-      uint32_t ph = 0, it = 0;
-      bool ok = true;
-      for (long long at = pair; at < units && ok && !*abort_flag; at += pairs) {
-        Unit u;
-        decode_unit(P, G, first_units, at, u);
-        const Feed f = feed_of(P, u, for_a, rank);
-        int x = f.x, y = f.y;
-        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-          if (it >= STAGES && !mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag)) {
-            fail();
-            ok = false;
-            break;
-          }
-          const uint32_t bar = (kb < f.past_from ? full_even : past_own) + 8u * static_cast<uint32_t>(st);
+    // ---------------- TMA producer of one operand (both CTAs); the A operand's also announces the bytes of both
+    const bool for_a = warp == A_WARP;
+    const uint32_t full_even = map_to_rank(&full[0], 0), past_own = map_to_rank(&past[0], rank);
+    uint8_t* const ring = for_a ? sA : sB;
+    uint32_t st = 0, ph = 0, it = 0;
+    bool ok = true;
+    for (int at = pair; at < units && ok && !__any_sync(0xffffffffu, *abort_flag); at += pairs) {
+      Unit u;
+      decode_same(P, G, first_units, at, u);
+      const Feed f = feed_of(P, u, for_a, rank);
+      int x = f.x, y = f.y;
+      for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+        if (it >= STAGES) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag));
+          if (!ok) break;
+        }
+        const bool past_end = kb >= f.past_from;
+        const uint32_t bar = (past_end ? past_own : full_even) + 8u * st;
+        uint8_t* to = ring + st * TILE_BYTES;
+        if (elect_lane()) {
           if (for_a) {
-            if (kb < f.past_from) {
+            if (!past_end) {
               if (even) mbar_expect_tx(&full[st], 2u * f.bytes);
             } else {
               if (even) mbar_arrive(&full[st]);
               mbar_expect_tx(&past[st], f.bytes);
             }
           }
-          uint8_t* to = ring + st * TILE_BYTES;
           tma_load_3d_pair(to, f.map, bar, x, y, f.batch);
           if (f.boxes > 1) tma_load_3d_pair(to + BOX_BYTES, f.map, bar, x + 64, y, f.batch);
-          x += f.x_step;
-          y += f.y_step;
+        }
+        __syncwarp();
+        x += f.x_step;
+        y += f.y_step;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok) fail();
+    // this CTA stays until the multicast releases of every stage it filled have arrived
+    for (uint32_t i = it > STAGES ? it - STAGES : 0u; i < it; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[i % STAGES], (i / STAGES) & 1, abort_flag))) {
+        fail();
+        break;
+      }
+    }
+  } else if (warp == 1) {
+    if (even) {
+      // ---------------- MMA issuer of the pair.  The next unit is decoded under this one's first MMAs.
+      const uint64_t desc = smem_desc_sw128(0, 0, 1024);             // but for the address and the step between boxes
+      const uint32_t a_ring = smem_u32(sA) >> 4, b_ring = smem_u32(sB) >> 4;
+      uint32_t k = 0, past_phase = 0, st = 0, ph = 0;
+      bool ok = true;
+      Unit u;
+      if (pair < units) decode_same(P, G, first_units, pair, u);
+      for (int at = pair; at < units && ok && !__any_sync(0xffffffffu, *abort_flag); at += pairs, ++k) {
+        const LinearJob& J = P.job[u.job];
+        const uint32_t buf = k & 1;
+        const uint32_t dacc = tmem + buf * ACC_COLS;
+        const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
+        const uint32_t a_step = (J.a_mn ? 2048u : 32u) >> 4, b_step = (J.b_mn ? 2048u : 32u) >> 4;
+        const uint64_t a_desc = desc | static_cast<uint64_t>((J.a_mn ? BOX_BYTES : 16) >> 4) << 16;
+        const uint64_t b_desc = desc | static_cast<uint64_t>((J.b_mn ? BOX_BYTES : 16) >> 4) << 16;
+        const int past_at = past_from(P, J, u), kb0 = u.kb0, kb1 = u.kb1;
+        if (k >= 2) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&tempty[buf], ((k >> 1) - 1) & 1, abort_flag));
+          if (!ok) break;
+        }
+        tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&full[st], ph, abort_flag));
+          if (!ok) break;
+          if (kb >= past_at) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&cleared[st], (past_phase >> st) & 1u, abort_flag));
+            if (!ok) break;
+            past_phase ^= 1u << st;
+          }
+          tc_fence_after();
+          const uint64_t a0 = a_desc + (a_ring + st * (TILE_BYTES >> 4)), b0 = b_desc + (b_ring + st * (TILE_BYTES >> 4));
+          if (elect_lane()) {
+#pragma unroll
+            for (int kk = 0; kk < LINEAR_DEEP / 16; ++kk)
+              umma_bf16_pair(dacc, a0 + kk * a_step, b0 + kk * b_step, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+            umma_commit_pair_both(&empty[st]);   // the stage may be refilled in both CTAs
+          }
+          __syncwarp();
           if (++st == STAGES) {
             st = 0;
             ph ^= 1u;
           }
+          if (kb == kb0 && at + pairs < units) decode_same(P, G, first_units, at + pairs, u);
         }
+        if (kb0 == kb1 && at + pairs < units) decode_same(P, G, first_units, at + pairs, u);
+        if (elect_lane()) umma_commit_pair_both(&tfull[buf]);
+        __syncwarp();
       }
-      // this CTA stays until the multicast releases of every stage it filled have arrived
-      for (uint32_t i = it > STAGES ? it - STAGES : 0u; i < it; ++i) {
-        if (!mbar_wait_cluster_or_abort(&empty[i % STAGES], (i / STAGES) & 1, abort_flag)) {
-          fail();
-          break;
-        }
-      }
-    }
-  } else if (warp == 1) {
-    if (even && lane == 0) {
-      // ---------------- MMA issuer of the pair
-      uint32_t it = 0, k = 0, past_phase = 0;
-      bool ok = true;
-      for (long long at = pair; at < units && ok && !*abort_flag; at += pairs, ++k) {
-        Unit u;
-        decode_unit(P, G, first_units, at, u);
-        const LinearJob& J = P.job[u.job];
-        const uint32_t buf = k & 1;
-        if (k >= 2 && !mbar_wait_cluster_or_abort(&tempty[buf], ((k >> 1) - 1) & 1, abort_flag)) {
-          fail();
-          break;
-        }
-        tc_fence_after();
-        const uint32_t dacc = tmem + buf * ACC_COLS;
-        const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
-        const uint32_t a_step = J.a_mn ? 2048u : 32u, b_step = J.b_mn ? 2048u : 32u;
-        const uint32_t a_lbo = J.a_mn ? BOX_BYTES : 16u, b_lbo = J.b_mn ? BOX_BYTES : 16u;
-        const int past_at = past_from(P, J, u), kb0 = u.kb0, kb1 = u.kb1;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int st = it % STAGES;
-          if (!mbar_wait_or_abort(&full[st], (it / STAGES) & 1, abort_flag)) {
-            fail();
-            ok = false;
-            break;
-          }
-          if (kb >= past_at) {
-            if (!mbar_wait_cluster_or_abort(&cleared[st], (past_phase >> st) & 1u, abort_flag)) {
-              fail();
-              ok = false;
-              break;
-            }
-            past_phase ^= 1u << st;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + st * TILE_BYTES), b0 = smem_u32(sB + st * TILE_BYTES);
-#pragma unroll
-          for (int kk = 0; kk < LINEAR_DEEP / 16; ++kk) {
-            umma_bf16_pair(dacc, smem_desc_sw128(a0 + kk * a_step, a_lbo, 1024),
-                           smem_desc_sw128(b0 + kk * b_step, b_lbo, 1024), idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-          }
-          umma_commit_pair_both(&empty[st]);   // the stage may be refilled in both CTAs
-        }
-        umma_commit_pair_both(&tfull[buf]);
-      }
+      if (!ok) fail();
     }
     __syncwarp();
   } else if (warp == FIX_WARP) {
     // ---------------- blocks that reach past a group: their rows from the group's end on become zero
     uint32_t it = 0, past_phase = 0;
     const uint32_t cleared_even = map_to_rank(&cleared[0], 0);
-    for (long long at = pair; at < units && !*abort_flag; at += pairs) {
+    for (int at = pair; at < units && !*abort_flag; at += pairs) {
       Unit u;
       decode_unit(P, G, first_units, at, u);
       const LinearJob& J = P.job[u.job];
@@ -341,12 +380,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
     WarpPlace w;
     w.lane = lane;
-    w.buf = sChunk + ew * CHUNK_BYTES;
+    w.buf = sChunk + ew * 2 * CHUNK_BYTES;
+    w.buf_z = w.buf + CHUNK_BYTES;
     w.bias = reinterpret_cast<float*>(sBias + ew * BIAS_BYTES);
     const uint32_t tempty_even = map_to_rank(&tempty[0], 0);
     side_work<T>(P, G, static_cast<long long>(blockIdx.x) * EPI_WARPS + ew, static_cast<long long>(gridDim.x) * EPI_WARPS, lane);
     uint32_t k = 0;
-    for (long long at = pair; at < units; at += pairs, ++k) {
+    for (int at = pair; at < units; at += pairs, ++k) {
       Unit u;
       decode_unit(P, G, first_units, at, u);
       const LinearJob& J = P.job[u.job];
@@ -362,26 +402,29 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       tc_fence_after();
       const uint32_t tacc = tmem + buf * ACC_COLS + (static_cast<uint32_t>(quad * 32) << 16);
       const int chunks = u.wide / 32;
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld_32x32(tacc + 32 * half, r);
       for (int c = half; c < chunks; c += 2) {
         float v[32];
-        __syncwarp();
-        tmem_ld_32x32(tacc + 32 * c, v);
-        if (u.kb0 == u.kb1) {                  // nothing to add up: the accumulator holds another tile
+        tmem_ld_ready(r);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
+        for (int i = 0; i < 32; ++i) v[i] = u.kb0 < u.kb1 ? __uint_as_float(r[i]) : 0.f;   // (else it holds another tile)
+        __syncwarp();
+        if (c + 2 < chunks) tmem_ld_32x32(tacc + 32 * (c + 2), r);     // under this chunk's work
         if (J.splits > 1) {
           float4* part = part_of(J, u, u.split, rank, ew, c >> 1);
 #pragma unroll
           for (int i = 0; i < 8; ++i) part[32 * i + lane] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else {
-          finish_chunk<FORWARD, T>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
+          finish_chunk<FORWARD, T, true>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(tempty_even + 8u * buf);    // the even CTA's MMA issuer may reuse the accumulator
     }
+    if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
   tc_fence_before();
@@ -393,12 +436,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   }
 }
 
-// The parts of a job's contraction added in order, then the epilogue: one CTA per half of a pair's tile, its warps as the
-// epilogue's.
+// The parts of a job's contraction added in order, then the epilogue: a CTA for one chunk of every epilogue warp of half a
+// pair's tile, so that a few tiles' parts are read by many CTAs.
 template <bool FORWARD, typename T>
 __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __grid_constant__ LinearParams P, int job) {
   __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
-  __shared__ alignas(16) uint8_t chunk[EPI_WARPS * CHUNK_BYTES];
+  __shared__ alignas(16) uint8_t chunk[EPI_WARPS * 2 * CHUNK_BYTES];
   __shared__ alignas(16) float bias[EPI_WARPS * 128];
   begin_after_previous();
   const LinearJob& J = P.job[job];
@@ -406,7 +449,7 @@ __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __gri
   const int ew = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (ew == 0) fill_groups(G, P.ends, P.rows, lane);
   __syncthreads();
-  const long long tile = blockIdx.x >> 1;
+  const int tile = blockIdx.x >> 1;
   const uint32_t rank = blockIdx.x & 1;
   if (tile >= job_units(J, G) / J.splits) return;
   Unit u;
@@ -416,29 +459,31 @@ __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __gri
   const int quad = (ew + 2) & 3, half = ew >> 2;         // as warps 2..9 of the kernel above
   WarpPlace w;
   w.lane = lane;
-  w.buf = chunk + ew * CHUNK_BYTES;
+  w.buf = chunk + ew * 2 * CHUNK_BYTES;
+  w.buf_z = w.buf + CHUNK_BYTES;
   w.bias = bias + ew * 128;
   w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
   w.rows = min(32, u.m_end - w.row0);
   if (w.rows <= 0) return;
   if constexpr (FORWARD) fetch_bias<T>(P, J, u, w, half);
-  for (int c = half; c < u.wide / 32; c += 2) {
-    float v[32];
+  const int c = half + 2 * blockIdx.y;
+  if (c >= u.wide / 32) return;
+  float v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    for (int s = 0; s < J.splits; ++s) {
-      const float4* part = part_of(J, u, s, rank, ew, c >> 1);
+  for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 2
+  for (int s = 0; s < J.splits; ++s) {
+    const float4* part = part_of(J, u, s, rank, ew, c >> 1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 q = part[32 * i + lane];
-        v[4 * i] += q.x;
-        v[4 * i + 1] += q.y;
-        v[4 * i + 2] += q.z;
-        v[4 * i + 3] += q.w;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float4 q = part[32 * i + lane];
+      v[4 * i] += q.x;
+      v[4 * i + 1] += q.y;
+      v[4 * i + 2] += q.z;
+      v[4 * i + 3] += q.w;
     }
-    finish_chunk<FORWARD, T>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
   }
+  finish_chunk<FORWARD, T, false>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
 }
 
 // Per-device set-up (the shared-memory limit, the number of pairs that can be resident) is done by the first call on each
@@ -477,7 +522,7 @@ cudaError_t launch_form(const LinearParams& p, int pairs_wanted, cudaStream_t s)
 template <bool FORWARD, typename T>
 cudaError_t launch_join_form(const LinearParams& p, int job, long long tiles, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), p.job[job].wide / 64);
   cfg.blockDim = dim3(32 * EPI_WARPS);
   cfg.stream = s;
   cudaLaunchAttribute a[1]{};

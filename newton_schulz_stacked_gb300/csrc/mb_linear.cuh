@@ -63,7 +63,7 @@ __device__ __forceinline__ bool fill_groups(const Groups& G, const int* ends, in
 // One pair's unit of work: a tile of a job, or a part of its contraction.
 struct Unit {
   int job, group;
-  long long tile;          // of the job
+  int tile;                // of the job
   int split;
   int m0, m_end;           // D's rows: the tile's first, and where the group's (or matrix's) end
   int n0, wide;            // D's columns
@@ -71,14 +71,15 @@ struct Unit {
   int kb0, kb1;            // blocks of 64 of the contraction
 };
 
-__device__ __forceinline__ long long job_units(const LinearJob& J, const Groups& G) {
-  return static_cast<long long>(J.over_rows ? G.n * J.m_tiles : G.tile[G.n]) * J.n_tiles * J.splits;
+// (the host refuses what 31 bits cannot number: a division of 64 bits takes a role longer than a block's MMAs)
+__device__ __forceinline__ int job_units(const LinearJob& J, const Groups& G) {
+  return (J.over_rows ? G.n * J.m_tiles : G.tile[G.n]) * J.n_tiles * J.splits;
 }
 
-__device__ __forceinline__ void decode_tile(const LinearJob& J, const Groups& G, long long tile, Unit& u) {
+__device__ __forceinline__ void decode_tile(const LinearJob& J, const Groups& G, int tile, Unit& u) {
   u.tile = tile;
-  const int n = static_cast<int>(tile % J.n_tiles);
-  int m = static_cast<int>(tile / J.n_tiles);
+  int m = tile / J.n_tiles;
+  const int n = tile - m * J.n_tiles;
   int blocks;
   if (J.over_rows) {
     u.group = m / J.m_tiles;
@@ -105,17 +106,26 @@ __device__ __forceinline__ void decode_tile(const LinearJob& J, const Groups& G,
   u.n0 = n * J.wide;
   // the last columns' tile is as narrow as its operand's layout allows
   const int left = J.N - u.n0, step = J.b_mn ? 128 : 64;
-  u.wide = min(J.wide, (left + step - 1) / step * step);
-  u.kb0 = static_cast<int>(static_cast<long long>(blocks) * u.split / J.splits);
-  u.kb1 = static_cast<int>(static_cast<long long>(blocks) * (u.split + 1) / J.splits);
+  u.wide = min(J.wide, (left + step - 1) & -step);
+  u.kb0 = 0;
+  u.kb1 = blocks;
+  if (J.splits > 1) {                            // (blocks < 2^24, splits < 2^5)
+    u.kb0 = blocks * u.split / J.splits;
+    u.kb1 = blocks * (u.split + 1) / J.splits;
+  }
 }
 
-__device__ __forceinline__ void decode_unit(const LinearParams& P, const Groups& G, long long first_units, long long at, Unit& u) {
+__device__ __forceinline__ void decode_unit(const LinearParams& P, const Groups& G, int first_units, int at, Unit& u) {
   u.job = at >= first_units ? 1 : 0;
   if (u.job) at -= first_units;
   const LinearJob& J = P.job[u.job];
-  u.split = static_cast<int>(at % J.splits);
-  decode_tile(J, G, at / J.splits, u);
+  u.split = 0;
+  if (J.splits > 1) {
+    const int tile = at / J.splits;
+    u.split = at - tile * J.splits;
+    at = tile;
+  }
+  decode_tile(J, G, at, u);
 }
 
 // ---------------------------------------------------------------- activations
@@ -251,24 +261,32 @@ __device__ __forceinline__ void add_row(const uint8_t* buf, float (&v)[32], int 
   }
 }
 
-// What an epilogue's warp holds: its rows of the tile, its chunk buffer, and the forward pass's bias of its columns.
+// What an epilogue's warp holds: its rows of the tile, its chunk buffers, and the forward pass's bias of its columns.
 struct WarpPlace {
   int row0;                // D's row of lane 0
   int rows;                // of the 32, how many belong to the group
   int lane;
-  uint8_t* buf;            // CHUNK_BYTES
+  uint8_t *buf, *buf_z;    // CHUNK_BYTES each
   float* bias;             // of the chunks that it takes, 32 each
 };
 
 // One chunk's sums to the results: columns col0 .. col0 + 31, `bias` those columns' (forward).
 //   z = v + bias;  y = act(z) + residual;  each rounded once.
-template <bool FORWARD, typename T>
+// Whole chunks leave by TMA where the results' layout allows it (BULK), the others by row-wise stores.
+template <bool FORWARD, typename T, bool BULK>
 __device__ __forceinline__ void finish_chunk(const LinearParams& P, const LinearJob& J, const Unit& u, const WarpPlace& w,
                                              float (&v)[32], int col0, const float* bias) {
   const int cols = J.N - col0;
   if (w.rows <= 0 || cols <= 0) return;            // (the same for all lanes)
-  uint16_t* out = static_cast<uint16_t*>(J.out) + u.group * J.group_stride + w.row0 * J.ld + col0;
+  const bool z = FORWARD && P.z != nullptr, residual = FORWARD && P.residual != nullptr;
+  if constexpr (BULK) {
+    if (w.lane == 0) bulk_wait_read_all();         // the chunk before has left the buffers
+    __syncwarp();
+  }
   if constexpr (FORWARD) {
+    if (residual)
+      load_chunk(P.residual_access, w.buf, static_cast<const uint16_t*>(P.residual) + w.row0 * P.residual_ld + col0,
+                 P.residual_ld, w.rows, cols, w.lane);
     if (P.bias) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -279,27 +297,32 @@ __device__ __forceinline__ void finish_chunk(const LinearParams& P, const Linear
         v[4 * i + 3] += b.w;
       }
     }
-    if (P.z) {
-      put_row<T>(w.buf, v, w.lane);
-      __syncwarp();
-      store_chunk(P.z_access, w.buf, static_cast<uint16_t*>(P.z) + w.row0 * P.z_ld + col0, P.z_ld, w.rows, cols, w.lane);
-      __syncwarp();
-    }
+    if (z) put_row<T>(w.buf_z, v, w.lane);
     with_activation(P.act, [&](auto act) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = activate<decltype(act)::value>(v[i]);
     });
-    if (P.residual) {
-      load_chunk(P.residual_access, w.buf, static_cast<const uint16_t*>(P.residual) + w.row0 * P.residual_ld + col0,
-                 P.residual_ld, w.rows, cols, w.lane);
+    if (residual) {
       __syncwarp();
-      add_row<T>(w.buf, v, w.lane);
-      __syncwarp();
+      add_row<T>(w.buf, v, w.lane);                // (a lane reads and writes its own row)
     }
   }
   put_row<T>(w.buf, v, w.lane);
+  if (BULK && J.bulk && w.rows >= 32) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (w.lane == 0) {
+      tma_store_3d(&J.d, w.buf, col0, w.row0, u.group * J.over_rows);
+      if (z) tma_store_3d(&P.z_map, w.buf_z, col0, w.row0, 0);
+      bulk_commit();
+    }
+    return;
+  }
   __syncwarp();
+  uint16_t* out = static_cast<uint16_t*>(J.out) + u.group * J.group_stride + w.row0 * J.ld + col0;
   store_chunk(J.access, w.buf, out, J.ld, w.rows, cols, w.lane);
+  if (z)
+    store_chunk(P.z_access, w.buf_z, static_cast<uint16_t*>(P.z) + w.row0 * P.z_ld + col0, P.z_ld, w.rows, cols, w.lane);
   __syncwarp();
 }
 

@@ -17,6 +17,8 @@ constexpr int LINEAR_DEEP = 64;          // of the contraction in one stage
 //   over a group's rows (dweight):  the contraction runs over them, D is the group's matrix.
 struct LinearJob {
   CUtensorMap a, b;
+  CUtensorMap d;           // the result in boxes of 32 x 32 (64-byte swizzle), where `bulk`
+  int bulk;                // whole chunks are stored by TMA (of the forward pass: z too)
   int a_mn, b_mn;          // the operand's rows run along memory (boxes of 64 x 64), not the contraction
   int over_rows;
   int M;                   // over_rows: D's rows
@@ -46,6 +48,7 @@ struct LinearParams {
   void* z;
   long long z_ld;
   int z_access;
+  CUtensorMap z_map;       // where job[0].bulk
   // dbias, from the sums over slabs of rows that the launch before made: [slabs + groups][db_cols]
   const float* db_parts;
   void* db;

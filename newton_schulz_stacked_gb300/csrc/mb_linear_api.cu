@@ -226,9 +226,17 @@ struct Call {
     return MB_OK;
   }
   int map(CUtensorMap* m, const Operand& o, int64_t rows, int64_t batch, int box_rows) const {
-    return api_encode_rows(m, o.base, type == MB_BF16, o.cols, rows, batch, o.ld, box_rows);
+    return api_encode_rows(m, o.base, type == MB_BF16, o.cols, rows, batch, o.ld, box_rows, 64);
+  }
+  int result_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t batch, int64_t ld) const {
+    return api_encode_rows(m, p, type == MB_BF16, cols, rows, batch, rows > 1 ? ld : up(cols, 8), 32, 32);
   }
 };
+
+// Whole chunks of a result leave by TMA: rows at 16-byte boundaries.
+bool bulk_stores(const void* p, int64_t ld, int64_t cols, int64_t rows) {
+  return aligned(p, 16) && (rows <= 1 || (ld % 8 == 0 && ld >= cols));
+}
 
 void set_cut(LinearJob& j, const Cut& c, uint8_t* ws) {
   j.wide = c.wide;
@@ -348,6 +356,12 @@ int mb_linear(const mb_linear_desc* desc, void* workspace, size_t workspace_byte
   set_cut(j, plan.y, call.ws);
   MB_TRY(call.map(&j.a, plan.x, d.rows, 1, 128));
   MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, j.wide / 2));
+  j.bulk = j.splits == 1 && bulk_stores(d.y, d.y_stride, d.out, d.rows) &&
+           (!d.z || bulk_stores(d.z, d.z_stride, d.out, d.rows));
+  if (j.bulk) {
+    MB_TRY(call.result_map(&j.d, d.y, d.rows, d.out, 1, d.y_stride));
+    if (d.z) MB_TRY(call.result_map(&p.z_map, d.z, d.rows, d.out, 1, d.z_stride));
+  }
   const Cut* const cuts[2] = {&plan.y, nullptr};
   MB_TRY(run_products(p, cuts, true, call));
   api_launched(MB_MARK_LINEAR, call.launches, call.stream);
@@ -428,6 +442,8 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     set_cut(j, plan.dw, call.ws);
     MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 64));
     MB_TRY(call.map(&j.b, plan.x, d.rows, 1, 64));
+    j.bulk = j.splits == 1 && bulk_stores(d.dweight, d.in, d.in, 2);
+    if (j.bulk) MB_TRY(call.result_map(&j.d, d.dweight, d.out, d.in, d.groups, d.in));
   }
   if (d.dx) {
     LinearJob& j = p.job[p.jobs];
@@ -441,6 +457,8 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     set_cut(j, plan.dx, call.ws);
     MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 128));
     MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, 64));
+    j.bulk = j.splits == 1 && bulk_stores(d.dx, d.dx_stride, d.in, d.rows);
+    if (j.bulk) MB_TRY(call.result_map(&j.d, d.dx, d.rows, d.in, 1, d.dx_stride));
   }
   MB_TRY(run_products(p, cuts, false, call));
   api_launched(MB_MARK_LINEAR_BACKWARD, call.launches, call.stream);
