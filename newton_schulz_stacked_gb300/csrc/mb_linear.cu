@@ -7,7 +7,7 @@
 // runs under the next one's MMAs).  An operand whose contraction runs along memory is staged K-major, one box a block;
 // the others (W in dx, both in dW) as boxes of 64 x 64 in MN-major layout.
 //
-// A pair takes the units pair, pair + pairs, ...; every role finds them itself from the groups' first rows and tiles, which
+// The units are dealt to the pairs in turn (Deal); the roles find them themselves from the groups' first rows and tiles, which
 // each CTA works out in shared memory from the ends in device memory, so that the host need not know them.  Tiles never
 // cross groups; a tile's operand rows past its group belong to the next group and are computed but not stored.  In dW
 // the contraction runs over the group's rows and its last block may reach into the next group's: there the loads complete on
@@ -108,6 +108,20 @@ __device__ __forceinline__ void decode_same(const LinearParams& P, const Groups&
   u.kb1 = same(u.kb1);
 }
 
+// What the MMA issuer has to know of a block, written by the A operand's producer of the even CTA: it need not decode units
+// itself, which took it longer (750 cycles) than a block's MMAs.
+struct BlockNote {
+  uint32_t idesc, flags;
+};
+enum : uint32_t {
+  NOTE_FIRST = 1,          // of its unit: the accumulator starts anew
+  NOTE_LAST = 2,
+  NOTE_NOTHING = 4,        // a unit without blocks: no MMAs
+  NOTE_PAST = 8,           // reaches past its group: wait until it is cleared
+  NOTE_A_MN = 16,
+  NOTE_B_MN = 32
+};
+
 // The first block of a unit that reaches into the next group's rows (the last block, or none: INT_MAX).
 __device__ __forceinline__ int past_from(const LinearParams& P, const LinearJob& J, const Unit& u) {
   const int whole = (u.k_end - u.k_begin) / LINEAR_DEEP;
@@ -192,7 +206,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   uint64_t* cleared = past + STAGES;         // [STAGES] (even) both CTAs have cleared it
   uint64_t* tfull = cleared + STAGES;        // [2] accumulator ready for the epilogue
   uint64_t* tempty = tfull + 2;              // [2] (even) both CTAs' epilogues drained the accumulator
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  BlockNote* notes = reinterpret_cast<BlockNote*>(tempty + 2);      // [STAGES]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(notes + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Groups G;
   G.row = reinterpret_cast<int*>(tmem_slot + 4);
@@ -240,9 +255,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     *abort_flag = 1;
   }
 
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int first_units = P.jobs > 0 ? job_units(P.job[0], G) : 0;
-  const int units = first_units + (P.jobs > 1 ? job_units(P.job[1], G) : 0);
+  const Deal deal(blockIdx.x >> 1, gridDim.x >> 1, first_units,
+                  first_units + (P.jobs > 1 ? job_units(P.job[1], G) : 0), P.extra);
+  const int mine = deal.count();
 
   if (warp == A_WARP || warp == B_WARP) {
     // ---------------- TMA producer of one operand (both CTAs); the A operand's also announces the bytes of both
@@ -251,30 +267,37 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     uint8_t* const ring = for_a ? sA : sB;
     uint32_t st = 0, ph = 0, it = 0;
     bool ok = true;
-    for (int at = pair; at < units && ok && !__any_sync(0xffffffffu, *abort_flag); at += pairs) {
+    for (int i = 0; i < mine && ok && !__any_sync(0xffffffffu, *abort_flag); ++i) {
       Unit u;
-      decode_same(P, G, first_units, at, u);
+      decode_same(P, G, first_units, deal(i), u);
       const Feed f = feed_of(P, u, for_a, rank);
+      const LinearJob& J = P.job[u.job];
+      const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
+      const uint32_t flags = (J.a_mn ? NOTE_A_MN : 0u) | (J.b_mn ? NOTE_B_MN : 0u) | (u.kb0 < u.kb1 ? 0u : NOTE_NOTHING);
+      const int kb0 = u.kb0, kb1 = max(u.kb1, kb0 + 1);        // a unit without blocks takes a stage for its note
       int x = f.x, y = f.y;
-      for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
         if (it >= STAGES) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag));
           if (!ok) break;
         }
-        const bool past_end = kb >= f.past_from;
+        const bool nothing = (flags & NOTE_NOTHING) != 0, past_end = !nothing && kb >= f.past_from;
         const uint32_t bar = (past_end ? past_own : full_even) + 8u * st;
         uint8_t* to = ring + st * TILE_BYTES;
         if (elect_lane()) {
           if (for_a) {
-            if (!past_end) {
-              if (even) mbar_expect_tx(&full[st], 2u * f.bytes);
-            } else {
-              if (even) mbar_arrive(&full[st]);
-              mbar_expect_tx(&past[st], f.bytes);
+            if (even) {
+              notes[st] = BlockNote{idesc, flags | (kb == kb0 ? NOTE_FIRST : 0u) | (kb == kb1 - 1 ? NOTE_LAST : 0u) |
+                                               (past_end ? NOTE_PAST : 0u)};
+              if (past_end || nothing) mbar_arrive(&full[st]);
+              else mbar_expect_tx(&full[st], 2u * f.bytes);
             }
+            if (past_end) mbar_expect_tx(&past[st], f.bytes);
           }
-          tma_load_3d_pair(to, f.map, bar, x, y, f.batch);
-          if (f.boxes > 1) tma_load_3d_pair(to + BOX_BYTES, f.map, bar, x + 64, y, f.batch);
+          if (!nothing) {
+            tma_load_3d_pair(to, f.map, bar, x, y, f.batch);
+            if (f.boxes > 1) tma_load_3d_pair(to + BOX_BYTES, f.map, bar, x + 64, y, f.batch);
+          }
         }
         __syncwarp();
         x += f.x_step;
@@ -295,53 +318,51 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     }
   } else if (warp == 1) {
     if (even) {
-      // ---------------- MMA issuer of the pair.  The next unit is decoded under this one's first MMAs.
+      // ---------------- MMA issuer of the pair: block after block as the notes say
       const uint64_t desc = smem_desc_sw128(0, 0, 1024);             // but for the address and the step between boxes
       const uint32_t a_ring = smem_u32(sA) >> 4, b_ring = smem_u32(sB) >> 4;
-      uint32_t k = 0, past_phase = 0, st = 0, ph = 0;
+      uint32_t past_phase = 0, st = 0, ph = 0, dacc = tmem, idesc = 0, a_step = 0, b_step = 0;
+      uint64_t a_desc = desc, b_desc = desc;
+      int k = 0;
       bool ok = true;
-      Unit u;
-      if (pair < units) decode_same(P, G, first_units, pair, u);
-      for (int at = pair; at < units && ok && !__any_sync(0xffffffffu, *abort_flag); at += pairs, ++k) {
-        const LinearJob& J = P.job[u.job];
-        const uint32_t buf = k & 1;
-        const uint32_t dacc = tmem + buf * ACC_COLS;
-        const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
-        const uint32_t a_step = (J.a_mn ? 2048u : 32u) >> 4, b_step = (J.b_mn ? 2048u : 32u) >> 4;
-        const uint64_t a_desc = desc | static_cast<uint64_t>((J.a_mn ? BOX_BYTES : 16) >> 4) << 16;
-        const uint64_t b_desc = desc | static_cast<uint64_t>((J.b_mn ? BOX_BYTES : 16) >> 4) << 16;
-        const int past_at = past_from(P, J, u), kb0 = u.kb0, kb1 = u.kb1;
-        if (k >= 2) {
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&tempty[buf], ((k >> 1) - 1) & 1, abort_flag));
+      while (k < mine) {
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&full[st], ph, abort_flag));
+        if (!ok) break;
+        const uint32_t flags = same(notes[st].flags);
+        if (flags & NOTE_FIRST) {
+          idesc = same(notes[st].idesc);
+          a_step = (flags & NOTE_A_MN ? 2048u : 32u) >> 4;
+          b_step = (flags & NOTE_B_MN ? 2048u : 32u) >> 4;
+          a_desc = desc | static_cast<uint64_t>((flags & NOTE_A_MN ? BOX_BYTES : 16) >> 4) << 16;
+          b_desc = desc | static_cast<uint64_t>((flags & NOTE_B_MN ? BOX_BYTES : 16) >> 4) << 16;
+          dacc = tmem + (k & 1) * ACC_COLS;
+          if (k >= 2) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&tempty[k & 1], ((k >> 1) - 1) & 1, abort_flag));
+            if (!ok) break;
+          }
+        }
+        if (flags & NOTE_PAST) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&cleared[st], (past_phase >> st) & 1u, abort_flag));
           if (!ok) break;
+          past_phase ^= 1u << st;
         }
         tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&full[st], ph, abort_flag));
-          if (!ok) break;
-          if (kb >= past_at) {
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&cleared[st], (past_phase >> st) & 1u, abort_flag));
-            if (!ok) break;
-            past_phase ^= 1u << st;
-          }
-          tc_fence_after();
-          const uint64_t a0 = a_desc + (a_ring + st * (TILE_BYTES >> 4)), b0 = b_desc + (b_ring + st * (TILE_BYTES >> 4));
-          if (elect_lane()) {
+        const uint64_t a0 = a_desc + (a_ring + st * (TILE_BYTES >> 4)), b0 = b_desc + (b_ring + st * (TILE_BYTES >> 4));
+        if (elect_lane()) {
+          if (!(flags & NOTE_NOTHING)) {
 #pragma unroll
             for (int kk = 0; kk < LINEAR_DEEP / 16; ++kk)
-              umma_bf16_pair(dacc, a0 + kk * a_step, b0 + kk * b_step, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-            umma_commit_pair_both(&empty[st]);   // the stage may be refilled in both CTAs
+              umma_bf16_pair(dacc, a0 + kk * a_step, b0 + kk * b_step, idesc, (flags & NOTE_FIRST) && kk == 0 ? 0u : 1u);
           }
-          __syncwarp();
-          if (++st == STAGES) {
-            st = 0;
-            ph ^= 1u;
-          }
-          if (kb == kb0 && at + pairs < units) decode_same(P, G, first_units, at + pairs, u);
+          umma_commit_pair_both(&empty[st]);   // the stage may be refilled in both CTAs
+          if (flags & NOTE_LAST) umma_commit_pair_both(&tfull[k & 1]);
         }
-        if (kb0 == kb1 && at + pairs < units) decode_same(P, G, first_units, at + pairs, u);
-        if (elect_lane()) umma_commit_pair_both(&tfull[buf]);
         __syncwarp();
+        if (flags & NOTE_LAST) ++k;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
       if (!ok) fail();
     }
@@ -350,12 +371,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     // ---------------- blocks that reach past a group: their rows from the group's end on become zero
     uint32_t it = 0, past_phase = 0;
     const uint32_t cleared_even = map_to_rank(&cleared[0], 0);
-    for (int at = pair; at < units && !*abort_flag; at += pairs) {
+    for (int i = 0; i < mine && !__any_sync(0xffffffffu, *abort_flag); ++i) {
       Unit u;
-      decode_unit(P, G, first_units, at, u);
+      decode_unit(P, G, first_units, deal(i), u);
       const LinearJob& J = P.job[u.job];
-      const int blocks = u.kb1 - u.kb0;
-      if (blocks > 0 && u.kb1 - 1 >= past_from(P, J, u)) {      // only a group's last block does
+      const int blocks = max(u.kb1 - u.kb0, 1);                  // (without blocks: a stage for the note)
+      if (u.kb1 > u.kb0 && u.kb1 - 1 >= past_from(P, J, u)) {      // only a group's last block does
         const int st = (it + blocks - 1) % STAGES;
         if (!mbar_wait_or_abort(&past[st], (past_phase >> st) & 1u, abort_flag)) {
           fail();
@@ -366,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         const int keep = u.k_end - u.k_begin - (u.kb1 - 1) * LINEAR_DEEP;
         for (int box = 0; box < 2 + (u.wide >> 7); ++box) {
           uint8_t* base = box < 2 ? sA + st * TILE_BYTES + box * BOX_BYTES : sB + st * TILE_BYTES + (box - 2) * BOX_BYTES;
-          for (int i = keep * 8 + lane; i < LINEAR_DEEP * 8; i += 32) reinterpret_cast<uint4*>(base)[i] = make_uint4(0, 0, 0, 0);
+          for (int j = keep * 8 + lane; j < LINEAR_DEEP * 8; j += 32) reinterpret_cast<uint4*>(base)[j] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -385,12 +406,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     w.bias = reinterpret_cast<float*>(sBias + ew * BIAS_BYTES);
     const uint32_t tempty_even = map_to_rank(&tempty[0], 0);
     side_work<T>(P, G, static_cast<long long>(blockIdx.x) * EPI_WARPS + ew, static_cast<long long>(gridDim.x) * EPI_WARPS, lane);
-    uint32_t k = 0;
-    for (int at = pair; at < units; at += pairs, ++k) {
+    for (int k = 0; k < mine; ++k) {
       Unit u;
-      decode_unit(P, G, first_units, at, u);
+      decode_unit(P, G, first_units, deal(k), u);
       const LinearJob& J = P.job[u.job];
-      const uint32_t buf = k & 1;
+      const int buf = k & 1;
       w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
       w.rows = min(32, u.m_end - w.row0);
       if constexpr (FORWARD) fetch_bias<T>(P, J, u, w, half);

@@ -115,6 +115,37 @@ __device__ __forceinline__ void decode_tile(const LinearJob& J, const Groups& G,
   }
 }
 
+// The units that a pair takes, in order: of the first job every `pairs`th; where those do not come out even, the pairs that have
+// one less take `extra` of the second job's each; then every `pairs`th of what is left.
+struct Deal {
+  int pair, pairs, first, units;   // first: the first job's units
+  int firsts, extras;              // that this pair takes
+  int rest, skipped;               // pairs with an extra share begin at `skipped`; the units from `rest` on are left
+  __device__ __forceinline__ Deal(int pair_, int pairs_, int first_, int units_, int extra) {
+    pair = pair_;
+    pairs = pairs_;
+    first = first_;
+    units = units_;
+    firsts = pair < first ? (first - pair + pairs - 1) / pairs : 0;
+    skipped = first % pairs;
+    const int others = pairs - skipped;
+    extra = skipped > 0 ? min(extra, (units - first) / others) : 0;
+    extras = pair >= skipped ? extra : 0;
+    rest = first + extra * others;
+  }
+  // The pair's unit number i; none from `units` on.
+  __device__ __forceinline__ int operator()(int i) const {
+    if (i < firsts) return pair + i * pairs;
+    i -= firsts;
+    if (i < extras) return first + (pair - skipped) + i * (pairs - skipped);
+    return rest + pair + (i - extras) * pairs;
+  }
+  __device__ __forceinline__ int count() const {
+    const int left = units - rest - pair;
+    return firsts + extras + (left > 0 ? (left + pairs - 1) / pairs : 0);
+  }
+};
+
 __device__ __forceinline__ void decode_unit(const LinearParams& P, const Groups& G, int first_units, int at, Unit& u) {
   u.job = at >= first_units ? 1 : 0;
   if (u.job) at -= first_units;

@@ -36,6 +36,7 @@ struct LinearJob {
 struct LinearParams {
   LinearJob job[2];
   int jobs;
+  int extra;               // units of the second job for pairs that have one of the first less than others
   int rows, groups;
   const int* ends;         // [groups] or null: one group of all rows
   int status_from;         // whether this launch reports bad ends

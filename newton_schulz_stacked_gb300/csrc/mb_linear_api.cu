@@ -97,42 +97,45 @@ struct Cut {
   size_t at;               // of the parts' sums
 };
 
-Cut cut_tiles(int64_t m_tiles, int64_t n, int64_t blocks) {
-  Cut c{};
-  // A tile of 128 columns takes about 0.6 of the time of one of 256: narrow tiles where they fill the pairs better.
-  const int64_t wide = m_tiles * parts_of(n, 256), narrow = m_tiles * parts_of(n, 128);
-  c.wide = n <= 128 || 10 * parts_of(wide, MAX_PAIRS) > 6 * parts_of(narrow, MAX_PAIRS) ? 128 : 256;
-  c.tiles = c.wide == 256 ? wide : narrow;
-  c.blocks = blocks;
-  c.splits = 1;
-  return c;
-}
+// Time in blocks of 256 x 256 x 64 (0.29 us): one of 128 columns takes 0.85 of it (measured: dW of 65536 rows 458 cycles
+// against 551), a tile's begin about one.
+double unit_time(const Cut& c) { return static_cast<double>(c.blocks) / c.splits * (c.wide == 256 ? 1.0 : 0.85) + 1; }
 
-// The time of the busiest pair, in blocks, when its units are dealt out in turn: `first` before `second`.  An epilogue that
-// nothing hides, and the sums of a part on their way to memory and back, count as some blocks.
-double busiest(const Cut& first, int splits, const Cut* second) {
-  const double a = static_cast<double>(first.blocks) / splits + 4 + (splits > 1 ? 10 : 0);
-  const double b = second ? static_cast<double>(second->blocks) + 4 : 0;
-  const int64_t n = first.tiles * splits, all = n + (second ? second->tiles : 0);
-  double most = 0;
-  for (int64_t p = 0; p < MAX_PAIRS; ++p) {
-    const int64_t mine_a = n > p ? parts_of(n - p, MAX_PAIRS) : 0;
-    const int64_t mine = all > p ? parts_of(all - p, MAX_PAIRS) : 0;
-    const double t = mine_a * a + (mine - mine_a) * b;
-    if (t > most) most = t;
+// The units of the second product that a pair takes for one of the first that others have more than it.
+int extra_units(const Cut& first, const Cut& second) { return static_cast<int>(unit_time(first) / unit_time(second) + 0.5); }
+
+// The time of the busiest pair, the last epilogue, and what the parts of a contraction cost: the join's launch, and 256 KB
+// of sums for each unit there and back.
+double busiest(const Cut& first, const Cut* second) {
+  const double a = unit_time(first), b = second ? unit_time(*second) : 0;
+  const int64_t n = first.tiles * first.splits, rounds = n / MAX_PAIRS, over = n % MAX_PAIRS;
+  double t;
+  if (!second) {
+    t = (rounds + (over > 0)) * a;
+  } else {
+    const int64_t extra = over > 0 ? extra_units(first, *second) : 0;
+    const int64_t rest = second->tiles - extra * (MAX_PAIRS - over);
+    const int64_t more = rest > 0 ? parts_of(rest, MAX_PAIRS) : 0;
+    const double with = (rounds + (over > 0)) * a + more * b, without = rounds * a + (extra + more) * b;
+    t = with > without ? with : without;
   }
-  return most + (splits > 1 ? 12 : 0);           // the join's launch
+  return t + 8 + (first.splits > 1 ? 10 + 0.27 * first.wide / 256 * static_cast<double>(n) : 0);
 }
 
-void cut_contraction(Cut& c, const Cut* second) {
-  double best = busiest(c, 1, second);
-  for (int s = 2; s <= MAX_SPLITS && c.blocks / s >= 8; ++s) {
-    const double t = busiest(c, s, second);
-    if (t < 0.97 * best) {
-      best = t;
-      c.splits = s;
+// The cut of tiles and contraction that takes the busiest pair least time, wide and whole where others gain little.
+Cut cut(int64_t m_tiles, int64_t n, int64_t blocks, const Cut* second) {
+  Cut best{};
+  double least = 0;
+  for (int wide = n <= 128 ? 128 : 256; wide >= 128; wide /= 2)
+    for (int s = 1; s <= MAX_SPLITS && (s == 1 || blocks / s >= 8); ++s) {
+      const Cut c{wide, s, m_tiles * parts_of(n, wide), blocks, 0};
+      const double t = busiest(c, second);
+      if (best.wide == 0 || t < 0.97 * least) {
+        best = c;
+        least = t;
+      }
     }
-  }
+  return best;
 }
 
 void reserve_parts(Cut& c, Workspace& ws) {
@@ -152,8 +155,7 @@ ForwardPlan plan_forward(const mb_linear_desc& d) {
   p.w = operand(d.weight, d.in, static_cast<int64_t>(d.groups) * d.out, d.in);
   if (p.x.copy) p.x.at = ws.take(p.x.rows * p.x.ld * 2);
   if (p.w.copy) p.w.at = ws.take(p.w.rows * p.w.ld * 2);
-  p.y = cut_tiles(parts_of(d.rows, LINEAR_TILE) + (d.ends ? d.groups : 0), d.out, parts_of(d.in, LINEAR_DEEP));
-  cut_contraction(p.y, nullptr);
+  p.y = cut(parts_of(d.rows, LINEAR_TILE) + (d.ends ? d.groups : 0), d.out, parts_of(d.in, LINEAR_DEEP), nullptr);
   reserve_parts(p.y, ws);
   p.end = ws.end;
   return p;
@@ -183,15 +185,16 @@ BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
   if (d.dweight) {
     p.x = operand(d.x, d.x_stride, d.rows, d.in);
     if (p.x.copy) p.x.at = ws.take(p.x.rows * p.x.ld * 2);
-    p.dw = cut_tiles(d.groups * parts_of(d.out, LINEAR_TILE), d.in, parts_of(parts_of(d.rows, d.groups), LINEAR_DEEP));
   }
   if (d.dx) {
     p.w = operand(d.weight, d.in, static_cast<int64_t>(d.groups) * d.out, d.in);
     if (p.w.copy) p.w.at = ws.take(p.w.rows * p.w.ld * 2);
-    p.dx = cut_tiles(parts_of(d.rows, LINEAR_TILE) + (d.ends ? d.groups : 0), d.in, parts_of(d.out, LINEAR_DEEP));
+    p.dx = cut(parts_of(d.rows, LINEAR_TILE) + (d.ends ? d.groups : 0), d.in, parts_of(d.out, LINEAR_DEEP), nullptr);
+    if (d.dweight) p.dx.splits = 1;              // dealt out after the other's units, which even them out
   }
-  if (d.dweight) cut_contraction(p.dw, d.dx ? &p.dx : nullptr);
-  else if (d.dx) cut_contraction(p.dx, nullptr);
+  if (d.dweight)
+    p.dw = cut(d.groups * parts_of(d.out, LINEAR_TILE), d.in, parts_of(parts_of(d.rows, d.groups), LINEAR_DEEP),
+               d.dx ? &p.dx : nullptr);
   if (d.dweight) reserve_parts(p.dw, ws);
   if (d.dx) reserve_parts(p.dx, ws);
   // slabs of rows: about four CTAs for an SM, 32 to 1024 rows
@@ -460,6 +463,7 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     j.bulk = j.splits == 1 && bulk_stores(d.dx, d.dx_stride, d.in, d.rows);
     if (j.bulk) MB_TRY(call.result_map(&j.d, d.dx, d.rows, d.in, 1, d.dx_stride));
   }
+  if (p.jobs == 2) p.extra = extra_units(plan.dw, plan.dx);
   MB_TRY(run_products(p, cuts, false, call));
   api_launched(MB_MARK_LINEAR_BACKWARD, call.launches, call.stream);
   return MB_OK;
