@@ -39,14 +39,14 @@ namespace mb {
 namespace {
 
 constexpr int BM = 128;
-constexpr int STAGES = 5;
+constexpr int STAGES = 6;
 constexpr int TILE_BYTES = BM * LINEAR_DEEP * 2;     // 16 KB: a CTA's rows of one operand's block
 constexpr int BOX_BYTES = 64 * LINEAR_DEEP * 2;      // 8 KB: one 64 x 64 box
 constexpr int EPI_WARPS = 8;
 constexpr int A_WARP = 0, FIX_WARP = 2 + EPI_WARPS, B_WARP = FIX_WARP + 1;
 constexpr int THREADS = 32 * (B_WARP + 1);
 constexpr int BIAS_BYTES = 4 * 32 * 4;               // per epilogue warp
-constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * (2 * CHUNK_BYTES + BIAS_BYTES) + GROUPS_BYTES + 1024 /* alignment */ +
+constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * (CHUNK_BYTES + BIAS_BYTES) + GROUPS_BYTES + 1024 /* alignment */ +
                      512 /* barriers */;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t ACC_COLS = 256, TMEM_COLS = 512;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * TILE_BYTES;
   uint8_t* sChunk = sB + STAGES * TILE_BYTES;
-  uint8_t* sBias = sChunk + EPI_WARPS * 2 * CHUNK_BYTES;
+  uint8_t* sBias = sChunk + EPI_WARPS * CHUNK_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(sBias + EPI_WARPS * BIAS_BYTES);   // [STAGES] (even) both CTAs' operands landed
   uint64_t* empty = full + STAGES;           // [STAGES] the pair's MMAs are done with the stage
   uint64_t* past = empty + STAGES;           // [STAGES] this CTA's part of a block that reaches past its group landed
@@ -401,8 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
     WarpPlace w;
     w.lane = lane;
-    w.buf = sChunk + ew * 2 * CHUNK_BYTES;
-    w.buf_z = w.buf + CHUNK_BYTES;
+    w.buf = sChunk + ew * CHUNK_BYTES;
     w.bias = reinterpret_cast<float*>(sBias + ew * BIAS_BYTES);
     const uint32_t tempty_even = map_to_rank(&tempty[0], 0);
     side_work<T>(P, G, static_cast<long long>(blockIdx.x) * EPI_WARPS + ew, static_cast<long long>(gridDim.x) * EPI_WARPS, lane);
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
 template <bool FORWARD, typename T>
 __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __grid_constant__ LinearParams P, int job) {
   __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
-  __shared__ alignas(16) uint8_t chunk[EPI_WARPS * 2 * CHUNK_BYTES];
+  __shared__ alignas(16) uint8_t chunk[EPI_WARPS * CHUNK_BYTES];
   __shared__ alignas(16) float bias[EPI_WARPS * 128];
   begin_after_previous();
   const LinearJob& J = P.job[job];
@@ -479,8 +478,7 @@ __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __gri
   const int quad = (ew + 2) & 3, half = ew >> 2;         // as warps 2..9 of the kernel above
   WarpPlace w;
   w.lane = lane;
-  w.buf = chunk + ew * 2 * CHUNK_BYTES;
-  w.buf_z = w.buf + CHUNK_BYTES;
+  w.buf = chunk + ew * CHUNK_BYTES;
   w.bias = bias + ew * 128;
   w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
   w.rows = min(32, u.m_end - w.row0);

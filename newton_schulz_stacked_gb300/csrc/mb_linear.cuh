@@ -292,32 +292,47 @@ __device__ __forceinline__ void add_row(const uint8_t* buf, float (&v)[32], int 
   }
 }
 
-// What an epilogue's warp holds: its rows of the tile, its chunk buffers, and the forward pass's bias of its columns.
+// What an epilogue's warp holds: its rows of the tile, its chunk buffer, and the forward pass's bias of its columns.
 struct WarpPlace {
   int row0;                // D's row of lane 0
   int rows;                // of the 32, how many belong to the group
   int lane;
-  uint8_t *buf, *buf_z;    // CHUNK_BYTES each
+  uint8_t* buf;            // CHUNK_BYTES
   float* bias;             // of the chunks that it takes, 32 each
 };
 
+// The chunk in the buffer to a result: whole by TMA where the layout allows it (BULK), else by row-wise stores.  The buffer
+// may be written again after `chunk_left`.
+template <bool BULK>
+__device__ __forceinline__ void send_chunk(const WarpPlace& w, bool bulk, const CUtensorMap* map, int batch, int access, void* to,
+                                           long long ld, int col0, int cols) {
+  if (BULK && bulk && w.rows >= 32) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (w.lane == 0) {
+      tma_store_3d(map, w.buf, col0, w.row0, batch);
+      bulk_commit();
+    }
+  } else {
+    __syncwarp();
+    store_chunk(access, w.buf, static_cast<uint16_t*>(to) + w.row0 * ld + col0, ld, w.rows, cols, w.lane);
+  }
+}
+template <bool BULK>
+__device__ __forceinline__ void chunk_left(const WarpPlace& w) {
+  if (BULK && w.lane == 0) bulk_wait_read_all();
+  __syncwarp();
+}
+
 // One chunk's sums to the results: columns col0 .. col0 + 31, `bias` those columns' (forward).
 //   z = v + bias;  y = act(z) + residual;  each rounded once.
-// Whole chunks leave by TMA where the results' layout allows it (BULK), the others by row-wise stores.
+// Both leave through one buffer: a second one would cost the products a stage of their ring, and with it 10 % of their rate.
 template <bool FORWARD, typename T, bool BULK>
 __device__ __forceinline__ void finish_chunk(const LinearParams& P, const LinearJob& J, const Unit& u, const WarpPlace& w,
                                              float (&v)[32], int col0, const float* bias) {
   const int cols = J.N - col0;
   if (w.rows <= 0 || cols <= 0) return;            // (the same for all lanes)
-  const bool z = FORWARD && P.z != nullptr, residual = FORWARD && P.residual != nullptr;
-  if constexpr (BULK) {
-    if (w.lane == 0) bulk_wait_read_all();         // the chunk before has left the buffers
-    __syncwarp();
-  }
   if constexpr (FORWARD) {
-    if (residual)
-      load_chunk(P.residual_access, w.buf, static_cast<const uint16_t*>(P.residual) + w.row0 * P.residual_ld + col0,
-                 P.residual_ld, w.rows, cols, w.lane);
     if (P.bias) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -328,33 +343,28 @@ __device__ __forceinline__ void finish_chunk(const LinearParams& P, const Linear
         v[4 * i + 3] += b.w;
       }
     }
-    if (z) put_row<T>(w.buf_z, v, w.lane);
+    if (P.z) {
+      chunk_left<BULK>(w);
+      put_row<T>(w.buf, v, w.lane);
+      send_chunk<BULK>(w, J.bulk, &P.z_map, 0, P.z_access, P.z, P.z_ld, col0, cols);
+    }
     with_activation(P.act, [&](auto act) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = activate<decltype(act)::value>(v[i]);
     });
-    if (residual) {
+  }
+  chunk_left<BULK>(w);
+  if constexpr (FORWARD) {
+    if (P.residual) {
+      load_chunk(P.residual_access, w.buf, static_cast<const uint16_t*>(P.residual) + w.row0 * P.residual_ld + col0,
+                 P.residual_ld, w.rows, cols, w.lane);
       __syncwarp();
       add_row<T>(w.buf, v, w.lane);                // (a lane reads and writes its own row)
     }
   }
   put_row<T>(w.buf, v, w.lane);
-  if (BULK && J.bulk && w.rows >= 32) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (w.lane == 0) {
-      tma_store_3d(&J.d, w.buf, col0, w.row0, u.group * J.over_rows);
-      if (z) tma_store_3d(&P.z_map, w.buf_z, col0, w.row0, 0);
-      bulk_commit();
-    }
-    return;
-  }
-  __syncwarp();
-  uint16_t* out = static_cast<uint16_t*>(J.out) + u.group * J.group_stride + w.row0 * J.ld + col0;
-  store_chunk(J.access, w.buf, out, J.ld, w.rows, cols, w.lane);
-  if (z)
-    store_chunk(P.z_access, w.buf_z, static_cast<uint16_t*>(P.z) + w.row0 * P.z_ld + col0, P.z_ld, w.rows, cols, w.lane);
-  __syncwarp();
+  send_chunk<BULK>(w, J.bulk, &J.d, u.group * J.over_rows, J.access, static_cast<uint16_t*>(J.out) + u.group * J.group_stride,
+                   J.ld, col0, cols);
 }
 
 // The bias of the warp's chunks of a unit (chunk i: columns n0 + 32 (half + 2 i)), zeros past the last column.
