@@ -69,7 +69,7 @@ struct LinearSlopeParams {
   const int* ends;
   float* parts;            // or null
   int slab;                // rows of a slab
-  int aligned;
+  int access;              // bytes that the rows allow to be read at a time: 16, 4 or 2
 };
 
 // Rows of 2-byte elements into rows that start at 16-byte boundaries.
@@ -80,6 +80,7 @@ struct LinearPackParams {
   long long dst_ld;
   long long rows;
   int cols;
+  int pairs;               // rows and columns come in 4-byte pairs
 };
 
 cudaError_t launch_linear(const LinearParams& p, int type, bool forward, int pairs_wanted, cudaStream_t s);

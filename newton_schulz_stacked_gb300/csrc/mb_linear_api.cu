@@ -222,7 +222,7 @@ struct Call {
     if (!o.copy) return MB_OK;
     o.base = ws + o.at;
     const LinearPackParams p{static_cast<const uint16_t*>(o.src), o.src_ld, reinterpret_cast<uint16_t*>(ws + o.at), o.ld,
-                             o.rows, static_cast<int>(o.cols)};
+                             o.rows, static_cast<int>(o.cols), access_of(o.src, o.src_ld, o.cols, o.rows) >= 4};
     const cudaError_t e = launch_linear_pack(p, sms, stream);
     if (e != cudaSuccess) return api_cuda_fail(e);
     ++launches;
@@ -413,8 +413,8 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     s.ends = d.ends;
     s.parts = d.dbias ? reinterpret_cast<float*>(call.ws + plan.db_parts) : nullptr;
     s.slab = plan.slab;
-    s.aligned = access_of(d.dy, d.dy_stride, d.out, d.rows) == 16 &&
-                (!plan.slope || access_of(d.z, d.z_stride, d.out, d.rows) == 16);
+    s.access = access_of(d.dy, d.dy_stride, d.out, d.rows);
+    if (plan.slope && access_of(d.z, d.z_stride, d.out, d.rows) < s.access) s.access = access_of(d.z, d.z_stride, d.out, d.rows);
     const cudaError_t e = launch_linear_slope(s, d.type, call.stream);
     if (e != cudaSuccess) return api_cuda_fail(e);
     ++call.launches;

@@ -8,58 +8,86 @@
 namespace mb {
 namespace {
 
-// A CTA takes 256 columns of a slab of rows, a warp every eighth row, a lane eight columns (neighbouring where the rows are
-// aligned, else every 32nd).  Bound by memory.  The sums are those of dz before it is rounded, one row of parts for every
-// piece of a slab that lies in one group: slab number + group number, which no two pieces share.
+// A CTA takes 256 columns of a slab of rows, a warp every eighth row, a lane eight columns: neighbouring ones where the rows
+// allow 16-byte accesses, else pairs or single ones 64 or 32 apart.  Bound by memory.  The sums are those of dz
+// before it is rounded, one row of parts for every piece of a slab that lies in one group: slab number + group number,
+// which no two pieces share.
 constexpr int SLOPE_COLS = 256, SLOPE_WARPS = 8;
 
-template <typename T, int ACT, bool ALIGNED>
+// The column of a lane's element j.
+template <int ACCESS>
+__device__ __forceinline__ int lane_col(int lane, int j) {
+  return ACCESS == 16 ? 8 * lane + j : ACCESS == 4 ? 64 * (j / 2) + 2 * lane + j % 2 : 32 * j + lane;
+}
+
+// Eight elements of a row, zeros past the last column.
+template <typename T, int ACCESS>
+__device__ __forceinline__ void load_lane(const T* row, int c0, int cols, int lane, float (&v)[8]) {
+  if constexpr (ACCESS == 16) {
+    Eight<T> e;
+    e.load(row + c0 + 8 * lane);
+    e.get(v);
+  } else if constexpr (ACCESS == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const int c = c0 + lane_col<4>(lane, j);
+      const float2 f = unpack2(c < cols ? *reinterpret_cast<const uint32_t*>(row + c) : 0u, T());
+      v[j] = f.x;
+      v[j + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + lane_col<2>(lane, j);
+      v[j] = c < cols ? to_float(row[c]) : 0.f;
+    }
+  }
+}
+
+template <typename T, int ACCESS>
+__device__ __forceinline__ void store_lane(T* row, int c0, int cols, int lane, const float (&v)[8]) {
+  if constexpr (ACCESS == 16) {
+    Eight<T> e;
+    e.set(v);
+    e.store(row + c0 + 8 * lane);
+  } else if constexpr (ACCESS == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const int c = c0 + lane_col<4>(lane, j);
+      if (c < cols) *reinterpret_cast<uint32_t*>(row + c) = pack2(v[j], v[j + 1], T());
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + lane_col<2>(lane, j);
+      if (c < cols) row[c] = from_float<T>(v[j]);
+    }
+  }
+}
+
+template <typename T, int ACT, int ACCESS>
 __device__ __forceinline__ void slope_rows(const LinearSlopeParams& p, int begin, int end, int c0, int warp, int lane,
                                            float (&sum)[8]) {
   const T* dy = static_cast<const T*>(p.dy);
   const T* z = static_cast<const T*>(p.z);
   T* dz = static_cast<T*>(p.dz);
-  const int first = ALIGNED ? c0 + 8 * lane : c0 + lane;
-  if (first >= p.cols) return;
+  if (c0 + lane_col<ACCESS>(lane, 0) >= p.cols) return;
 #pragma unroll 2
   for (int row = begin + warp; row < end; row += SLOPE_WARPS) {
-    const T* g = dy + row * p.dy_ld + first;
     float v[8], x[8];
-    if constexpr (ALIGNED) {
-      Eight<T> a, b;
-      a.load(g);
-      if (ACT != MB_ACT_NONE) {
-        b.load(z + row * p.z_ld + first);
-        b.get(x);
-      }
-      a.get(v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = first + 32 * j < p.cols ? to_float(g[32 * j]) : 0.f;
-        if (ACT != MB_ACT_NONE) x[j] = first + 32 * j < p.cols ? to_float(z[row * p.z_ld + first + 32 * j]) : 0.f;
-      }
-    }
+    load_lane<T, ACCESS>(dy + row * p.dy_ld, c0, p.cols, lane, v);
     if (ACT != MB_ACT_NONE) {
+      load_lane<T, ACCESS>(z + row * p.z_ld, c0, p.cols, lane, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= slope<ACT>(x[j]);
-      T* to = dz + row * p.dz_ld + first;
-      if constexpr (ALIGNED) {
-        Eight<T> a;
-        a.set(v);
-        a.store(to);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (first + 32 * j < p.cols) to[32 * j] = from_float<T>(v[j]);
-      }
+      store_lane<T, ACCESS>(dz + row * p.dz_ld, c0, p.cols, lane, v);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += v[j];
   }
 }
 
-template <typename T, bool ALIGNED>
+template <typename T, int ACCESS>
 __global__ void __launch_bounds__(32 * SLOPE_WARPS) linear_slope_kernel(const __grid_constant__ LinearSlopeParams p) {
   __shared__ float partial[SLOPE_WARPS][SLOPE_COLS];
   __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
@@ -85,12 +113,12 @@ __global__ void __launch_bounds__(32 * SLOPE_WARPS) linear_slope_kernel(const __
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] = 0.f;
     with_activation(p.z ? p.act : MB_ACT_NONE, [&](auto act) {
-      slope_rows<T, decltype(act)::value, ALIGNED>(p, row, stop, c0, warp, lane, sum);
+      slope_rows<T, decltype(act)::value, ACCESS>(p, row, stop, c0, warp, lane, sum);
     });
     row = stop;
     if (!p.parts) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) partial[warp][ALIGNED ? 8 * lane + j : 32 * j + lane] = sum[j];
+    for (int j = 0; j < 8; ++j) partial[warp][lane_col<ACCESS>(lane, j)] = sum[j];
     __syncthreads();
     const int col = threadIdx.x;
     if (c0 + col < p.cols) {
@@ -106,25 +134,33 @@ __global__ void __launch_bounds__(32 * SLOPE_WARPS) linear_slope_kernel(const __
 __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ LinearPackParams p) {
   begin_after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // a warp per row: single elements, read along the row
+  // a warp per row: pairs of elements, or single ones, read along the row
   for (long long row = static_cast<long long>(blockIdx.x) * 8 + warp; row < p.rows; row += static_cast<long long>(gridDim.x) * 8) {
     const uint16_t* from = p.src + row * p.src_ld;
     uint16_t* to = p.dst + row * p.dst_ld;
+    if (p.pairs) {
 #pragma unroll 4
-    for (int c = lane; c < p.cols; c += 32) to[c] = from[c];
+      for (int c = lane; c < p.cols / 2; c += 32) reinterpret_cast<uint32_t*>(to)[c] = reinterpret_cast<const uint32_t*>(from)[c];
+    } else {
+#pragma unroll 4
+      for (int c = lane; c < p.cols; c += 32) to[c] = from[c];
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream_t s) {
+template <typename T>
+cudaError_t launch_slope_type(const LinearSlopeParams& p, cudaStream_t s) {
   const dim3 grid((p.cols + SLOPE_COLS - 1) / SLOPE_COLS, (p.rows + p.slab - 1) / p.slab);
   const dim3 block(32 * SLOPE_WARPS);
-  if (type == MB_BF16)
-    return p.aligned ? launch_after(linear_slope_kernel<__nv_bfloat16, true>, grid, block, 0, s, p)
-                     : launch_after(linear_slope_kernel<__nv_bfloat16, false>, grid, block, 0, s, p);
-  return p.aligned ? launch_after(linear_slope_kernel<__half, true>, grid, block, 0, s, p)
-                   : launch_after(linear_slope_kernel<__half, false>, grid, block, 0, s, p);
+  if (p.access == 16) return launch_after(linear_slope_kernel<T, 16>, grid, block, 0, s, p);
+  if (p.access == 4) return launch_after(linear_slope_kernel<T, 4>, grid, block, 0, s, p);
+  return launch_after(linear_slope_kernel<T, 2>, grid, block, 0, s, p);
+}
+
+cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream_t s) {
+  return type == MB_BF16 ? launch_slope_type<__nv_bfloat16>(p, s) : launch_slope_type<__half>(p, s);
 }
 
 cudaError_t launch_linear_pack(const LinearPackParams& p, int sms, cudaStream_t s) {
