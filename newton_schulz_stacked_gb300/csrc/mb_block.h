@@ -15,9 +15,9 @@ int api_cuda_fail(cudaError_t e);    // keeps the message, returns MB_ERR_CUDA
 int api_device_sms(int* sms);        // checks the current device; its SM count
 int api_device_status(int** status); // checks the current device; its latched status word
 // A tensor map of `batch` matrices of rows x cols 2-byte elements, row stride ld (a multiple of 8) elements, in boxes of
-// box_rows x box_cols (64 in the 128-byte swizzle, 32 in the 64-byte one); after one of the two calls above.
+// box_rows x 64 in the 128-byte swizzle; after one of the two calls above.
 int api_encode_rows(CUtensorMap* map, const void* base, bool bf16, int64_t cols, int64_t rows, int64_t batch, int64_t ld,
-                    int box_rows, int box_cols);
+                    int box_rows);
 void api_launched(int label, int launches, cudaStream_t stream);   // counts launches and marks their end
 
 // ---------------------------------------------------------------- layer norm

@@ -45,10 +45,14 @@ constexpr int BOX_BYTES = 64 * LINEAR_DEEP * 2;      // 8 KB: one 64 x 64 box
 constexpr int EPI_WARPS = 8;
 constexpr int A_WARP = 0, FIX_WARP = 2 + EPI_WARPS, B_WARP = FIX_WARP + 1;
 constexpr int THREADS = 32 * (B_WARP + 1);
-constexpr int BIAS_BYTES = 4 * 32 * 4;               // per epilogue warp
-constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * (CHUNK_BYTES + BIAS_BYTES) + GROUPS_BYTES + 1024 /* alignment */ +
-                     512 /* barriers */;
+// What not every call needs takes the memory of the ring's last stages: the residual's buffers a whole one, the places of more
+// than FEW_GROUPS groups the A half of one.
+constexpr int FEW_GROUPS = 140;
+static_assert(EPI_WARPS * CHUNK_BYTES <= 2 * TILE_BYTES, "the residual's buffers fit a stage");
+constexpr int SMEM = 2 * STAGES * TILE_BYTES + EPI_WARPS * CHUNK_BYTES + 2 * (FEW_GROUPS + 1) * 4 + 1024 /* alignment */ +
+                     448 /* barriers, notes */;
 static_assert(SMEM <= 232448, "shared memory per CTA");
+static_assert(GROUPS_BYTES <= TILE_BYTES, "the groups' places fit a stage's");
 constexpr uint32_t ACC_COLS = 256, TMEM_COLS = 512;
 
 // Instruction descriptor, kind::f16, fp32 sums, M = 256 (a pair).
@@ -199,19 +203,22 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * TILE_BYTES;
   uint8_t* sChunk = sB + STAGES * TILE_BYTES;
-  uint8_t* sBias = sChunk + EPI_WARPS * CHUNK_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sBias + EPI_WARPS * BIAS_BYTES);   // [STAGES] (even) both CTAs' operands landed
+  const bool few = P.groups <= FEW_GROUPS;
+  const bool with_residual = FORWARD && P.residual_bulk;
+  const uint32_t stages = STAGES - (few ? 0 : 1) - (with_residual ? 1 : 0);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sChunk + EPI_WARPS * CHUNK_BYTES);   // [STAGES] (even) both CTAs' operands landed
   uint64_t* empty = full + STAGES;           // [STAGES] the pair's MMAs are done with the stage
   uint64_t* past = empty + STAGES;           // [STAGES] this CTA's part of a block that reaches past its group landed
   uint64_t* cleared = past + STAGES;         // [STAGES] (even) both CTAs have cleared it
   uint64_t* tfull = cleared + STAGES;        // [2] accumulator ready for the epilogue
   uint64_t* tempty = tfull + 2;              // [2] (even) both CTAs' epilogues drained the accumulator
-  BlockNote* notes = reinterpret_cast<BlockNote*>(tempty + 2);      // [STAGES]
+  uint64_t* landed = tempty + 2;             // [EPI_WARPS] the warp's chunk of the residual
+  BlockNote* notes = reinterpret_cast<BlockNote*>(landed + EPI_WARPS);      // [STAGES]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(notes + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Groups G;
-  G.row = reinterpret_cast<int*>(tmem_slot + 4);
-  G.tile = G.row + LINEAR_MAX_GROUPS + 1;
+  G.row = few ? reinterpret_cast<int*>(tmem_slot + 4) : reinterpret_cast<int*>(sA + stages * TILE_BYTES);
+  G.tile = G.row + P.groups + 1;
   G.n = P.groups;
 
   const int warp = same(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -229,6 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 2 * EPI_WARPS);
     }
+    for (int i = 0; i < EPI_WARPS; ++i) mbar_init(&landed[i], 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       const int kb0 = u.kb0, kb1 = max(u.kb1, kb0 + 1);        // a unit without blocks takes a stage for its note
       int x = f.x, y = f.y;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        if (it >= STAGES) {
+        if (it >= stages) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag));
           if (!ok) break;
         }
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         __syncwarp();
         x += f.x_step;
         y += f.y_step;
-        if (++st == STAGES) {
+        if (++st == stages) {
           st = 0;
           ph ^= 1u;
         }
@@ -310,8 +318,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     }
     if (!ok) fail();
     // this CTA stays until the multicast releases of every stage it filled have arrived
-    for (uint32_t i = it > STAGES ? it - STAGES : 0u; i < it; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[i % STAGES], (i / STAGES) & 1, abort_flag))) {
+    for (uint32_t i = it > stages ? it - stages : 0u; i < it; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[i % stages], (i / stages) & 1, abort_flag))) {
         fail();
         break;
       }
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         }
         __syncwarp();
         if (flags & NOTE_LAST) ++k;
-        if (++st == STAGES) {
+        if (++st == stages) {
           st = 0;
           ph ^= 1u;
         }
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       const LinearJob& J = P.job[u.job];
       const int blocks = max(u.kb1 - u.kb0, 1);                  // (without blocks: a stage for the note)
       if (u.kb1 > u.kb0 && u.kb1 - 1 >= past_from(P, J, u)) {      // only a group's last block does
-        const int st = (it + blocks - 1) % STAGES;
+        const int st = (it + blocks - 1) % stages;
         if (!mbar_wait_or_abort(&past[st], (past_phase >> st) & 1u, abort_flag)) {
           fail();
           break;
@@ -402,7 +410,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     WarpPlace w;
     w.lane = lane;
     w.buf = sChunk + ew * CHUNK_BYTES;
-    w.bias = reinterpret_cast<float*>(sBias + ew * BIAS_BYTES);
+    // (the last stage's two halves, four warps' buffers in each)
+    ResidualFeed res{with_residual ? (half ? sB : sA) + (STAGES - 1) * TILE_BYTES + (ew & 3) * CHUNK_BYTES : nullptr, &landed[ew], 0, 0};
     const uint32_t tempty_even = map_to_rank(&tempty[0], 0);
     side_work<T>(P, G, static_cast<long long>(blockIdx.x) * EPI_WARPS + ew, static_cast<long long>(gridDim.x) * EPI_WARPS, lane);
     for (int k = 0; k < mine; ++k) {
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       const int buf = k & 1;
       w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
       w.rows = min(32, u.m_end - w.row0);
-      if constexpr (FORWARD) fetch_bias<T>(P, J, u, w, half);
+      if constexpr (FORWARD) res.ask(P, J, w, u.n0 + CHUNK_COLS * half);
       if (!mbar_wait_or_abort(&tfull[buf], (k >> 1) & 1, abort_flag)) {
         fail();
         break;
@@ -420,29 +429,39 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       if (__any_sync(0xffffffffu, *abort_flag)) break;
       tc_fence_after();
       const uint32_t tacc = tmem + buf * ACC_COLS + (static_cast<uint32_t>(quad * 32) << 16);
-      const int chunks = u.wide / 32;
-      uint32_t r[32];
-      __syncwarp();
-      tmem_ld_32x32(tacc + 32 * half, r);
-      for (int c = half; c < chunks; c += 2) {
-        float v[32];
-        tmem_ld_ready(r);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = u.kb0 < u.kb1 ? __uint_as_float(r[i]) : 0.f;   // (else it holds another tile)
+      const int chunks = u.wide / CHUNK_COLS;
+      bool ok = true;
+      for (int c = half; c < chunks && ok; c += 2) {
+        uint32_t r[2][32];
         __syncwarp();
-        if (c + 2 < chunks) tmem_ld_32x32(tacc + 32 * (c + 2), r);     // under this chunk's work
+        tmem_ld_32x32(tacc + CHUNK_COLS * c, r[0]);
+        tmem_ld_32x32(tacc + CHUNK_COLS * c + 32, r[1]);
+        tmem_ld_ready(r[0]);
+        tmem_ld_ready(r[1]);
+        Row v;
+#pragma unroll
+        for (int i = 0; i < CHUNK_COLS / 2; ++i)             // (without blocks the accumulator holds another tile)
+          v.v[i] = u.kb0 < u.kb1 ? make_float2(__uint_as_float(r[i / 16][2 * i % 32]), __uint_as_float(r[i / 16][2 * i % 32 + 1]))
+                                 : make_float2(0.f, 0.f);
         if (J.splits > 1) {
           float4* part = part_of(J, u, u.split, rank, ew, c >> 1);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) part[32 * i + lane] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int i = 0; i < CHUNK_COLS / 4; ++i)
+            part[32 * i + lane] = make_float4(v.v[2 * i].x, v.v[2 * i].y, v.v[2 * i + 1].x, v.v[2 * i + 1].y);
         } else {
-          finish_chunk<FORWARD, T, true>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
+          ok = finish_chunk<FORWARD, T, true>(P, J, u, w, v, u.n0 + CHUNK_COLS * c, res, abort_flag);
         }
+      }
+      if (!ok) {
+        fail();
+        break;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(tempty_even + 8u * buf);    // the even CTA's MMA issuer may reuse the accumulator
     }
+    // copies in flight (a residual's only after an abort) end before the CTA does
+    if (res.asked != res.used) mbar_wait(res.landed, res.used & 1);
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
@@ -461,7 +480,6 @@ template <bool FORWARD, typename T>
 __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __grid_constant__ LinearParams P, int job) {
   __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
   __shared__ alignas(16) uint8_t chunk[EPI_WARPS * CHUNK_BYTES];
-  __shared__ alignas(16) float bias[EPI_WARPS * 128];
   begin_after_previous();
   const LinearJob& J = P.job[job];
   Groups G{groups, groups + LINEAR_MAX_GROUPS + 1, P.groups};
@@ -479,29 +497,26 @@ __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __gri
   WarpPlace w;
   w.lane = lane;
   w.buf = chunk + ew * CHUNK_BYTES;
-  w.bias = bias + ew * 128;
   w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
   w.rows = min(32, u.m_end - w.row0);
   if (w.rows <= 0) return;
-  if constexpr (FORWARD) fetch_bias<T>(P, J, u, w, half);
   const int c = half + 2 * blockIdx.y;
-  if (c >= u.wide / 32) return;
-  float v[32];
+  if (c >= u.wide / CHUNK_COLS) return;
+  ResidualFeed none{nullptr, nullptr, 0, 0};
+  Row v;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = 0.f;
+  for (int i = 0; i < CHUNK_COLS / 2; ++i) v.v[i] = make_float2(0.f, 0.f);
 #pragma unroll 2
   for (int s = 0; s < J.splits; ++s) {
     const float4* part = part_of(J, u, s, rank, ew, c >> 1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < CHUNK_COLS / 4; ++i) {
       const float4 q = part[32 * i + lane];
-      v[4 * i] += q.x;
-      v[4 * i + 1] += q.y;
-      v[4 * i + 2] += q.z;
-      v[4 * i + 3] += q.w;
+      v.v[2 * i] = __fadd2_rn(v.v[2 * i], make_float2(q.x, q.y));
+      v.v[2 * i + 1] = __fadd2_rn(v.v[2 * i + 1], make_float2(q.z, q.w));
     }
   }
-  finish_chunk<FORWARD, T, false>(P, J, u, w, v, u.n0 + 32 * c, w.bias + 32 * (c >> 1));
+  finish_chunk<FORWARD, T, false>(P, J, u, w, v, u.n0 + CHUNK_COLS * c, none, nullptr);
 }
 
 // Per-device set-up (the shared-memory limit, the number of pairs that can be resident) is done by the first call on each
@@ -540,7 +555,7 @@ cudaError_t launch_form(const LinearParams& p, int pairs_wanted, cudaStream_t s)
 template <bool FORWARD, typename T>
 cudaError_t launch_join_form(const LinearParams& p, int job, long long tiles, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), p.job[job].wide / 64);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), p.job[job].wide / 128);
   cfg.blockDim = dim3(32 * EPI_WARPS);
   cfg.stream = s;
   cudaLaunchAttribute a[1]{};

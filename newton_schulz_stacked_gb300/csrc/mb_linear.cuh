@@ -162,26 +162,40 @@ __device__ __forceinline__ void decode_unit(const LinearParams& P, const Groups&
 // ---------------------------------------------------------------- activations
 
 // exp2 and the reciprocal are the hardware's, within about 2^-22 of their values: a result is rounded to 16 bits.
-__device__ __forceinline__ float sigmoid(float x) {
+__device__ __forceinline__ float inverse_one_plus_exp2(float t) {
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
+__device__ __forceinline__ float sigmoid(float x) { return inverse_one_plus_exp2(x * -1.4426950408889634f); }
 constexpr float GELU_SCALE = 1.5957691216057308f;    // 2 sqrt(2 / pi): tanh(u) = 2 sigmoid(2 u) - 1
 constexpr float GELU_CUBE = 0.044715f;
 
 // (comparisons are written so that NaN stays NaN)
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
-  if (ACT == MB_ACT_RELU) return z < 0.f ? 0.f : z;
-  if (ACT == MB_ACT_RELU2) {
-    const float r = z < 0.f ? 0.f : z;
-    return r * r;
+  static_assert(ACT == MB_ACT_NONE || ACT == MB_ACT_RELU, "the others come in pairs");
+  return ACT == MB_ACT_RELU && z < 0.f ? 0.f : z;
+}
+
+// Two at a time: what the exponentials leave to do goes two to an instruction.
+template <int ACT>
+__device__ __forceinline__ float2 activate(float2 z) {
+  if constexpr (ACT == MB_ACT_GELU) {
+    // z s(z (a + b z^2)), the exponent's log2(e) in a and b
+    constexpr float A = -GELU_SCALE * 1.4426950408889634f, B = A * GELU_CUBE;
+    const float2 t = __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), make_float2(B, B), make_float2(A, A)));
+    return __fmul2_rn(z, make_float2(inverse_one_plus_exp2(t.x), inverse_one_plus_exp2(t.y)));
+  } else if constexpr (ACT == MB_ACT_SILU) {
+    const float2 t = __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    return __fmul2_rn(z, make_float2(inverse_one_plus_exp2(t.x), inverse_one_plus_exp2(t.y)));
+  } else if constexpr (ACT == MB_ACT_RELU2) {
+    const float2 t = make_float2(activate<MB_ACT_RELU>(z.x), activate<MB_ACT_RELU>(z.y));
+    return __fmul2_rn(t, t);
+  } else {
+    return make_float2(activate<ACT>(z.x), activate<ACT>(z.y));
   }
-  if (ACT == MB_ACT_SILU) return z * sigmoid(z);
-  if (ACT == MB_ACT_GELU) return z * sigmoid(GELU_SCALE * fmaf(GELU_CUBE * z * z, z, z));
-  return z;
 }
 
 template <int ACT>
@@ -211,98 +225,120 @@ __device__ __forceinline__ void with_activation(int act, F&& f) {
   }
 }
 
-// ---------------------------------------------------------------- chunks of 32 x 32
+// ---------------------------------------------------------------- chunks of 32 rows x 64 columns
 
-// A warp's chunk in shared memory: rows of 64 bytes whose 16-byte pieces are exchanged by row, so that lanes that each take
-// a row, and lanes that each take a piece of neighbouring rows, hit distinct banks.
-constexpr int CHUNK_BYTES = 32 * 64;
+// A warp's chunk in shared memory: rows of 128 bytes whose 16-byte pieces are exchanged by row (TMA's 128-byte swizzle), so
+// that lanes that each take a row, and lanes that each take a piece of neighbouring rows, hit distinct banks.  Whole lines
+// of memory: the TMA unit takes about two cycles for a row of a box whatever its length, and stores of 64-byte rows held
+// up the products' loads (65536x768->2816 with relu^2, z and a bias: 237 us in boxes of 32 columns).
+constexpr int CHUNK_COLS = 64;
+constexpr int CHUNK_BYTES = 32 * CHUNK_COLS * 2;
 __device__ __forceinline__ uint32_t chunk_at(int row, int piece) {
-  return static_cast<uint32_t>(row * 64 + 16 * (piece ^ ((row >> 1) & 3)));
+  return static_cast<uint32_t>(row * 128 + 16 * (piece ^ (row & 7)));
 }
 
-// Rows [0, rows) and columns [0, cols) of the chunk to memory, neighbouring lanes along rows.
+// The chunk's row-wise copies in accesses of ACCESS bytes, neighbouring lanes along rows: f(place in the buffer, place in memory)
+// for rows [0, rows) and columns [0, cols).
+template <int ACCESS, typename F>
+__device__ __forceinline__ void each_piece(uint16_t* at, long long ld, int rows, int cols, int lane, F&& f) {
+  constexpr int PIECES = CHUNK_COLS * 2 / ACCESS;              // of a row
+  constexpr int LANES = PIECES < 32 ? PIECES : 32, STEP = 32 / LANES;
+#pragma unroll
+  for (int part = 0; part < PIECES / LANES; ++part) {
+    const int piece = part * LANES + lane % LANES, col = piece * (ACCESS / 2);
+    const int row = lane / LANES;
+    uint16_t* to = at + row * ld + col;
+    const int some = col < cols ? rows : 0;
+#pragma unroll 8
+    for (int i = 0; i < 32 / STEP; ++i, to += STEP * ld)
+      if (i * STEP + row < some) f(chunk_at(i * STEP + row, piece * ACCESS / 16) + piece * ACCESS % 16, to);
+  }
+}
+template <int ACCESS>
+using AccessWord = std::conditional_t<ACCESS == 16, uint4, std::conditional_t<ACCESS == 4, uint32_t, uint16_t>>;
+
+// To memory, or from there (what lies outside is left as it is).
 template <int ACCESS>
 __device__ __forceinline__ void store_chunk(const uint8_t* buf, uint16_t* to, long long ld, int rows, int cols, int lane) {
-  constexpr int LANES = 64 / ACCESS, STEP = 32 / LANES;      // lanes of a row, rows at a time
-  const int piece = lane % LANES, col = piece * (ACCESS / 2);
-#pragma unroll
-  for (int i = 0; i < LANES; ++i) {
-    const int row = i * STEP + lane / LANES;
-    if (row < rows && col < cols) {
-      const uint8_t* from = buf + chunk_at(row, piece * ACCESS / 16) + piece * ACCESS % 16;
-      uint16_t* at = to + row * ld + col;
-      if constexpr (ACCESS == 16) *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(from);
-      else if constexpr (ACCESS == 4) *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(from);
-      else *at = *reinterpret_cast<const uint16_t*>(from);
-    }
-  }
+  each_piece<ACCESS>(to, ld, rows, cols, lane, [&](uint32_t at, uint16_t* p) {
+    *reinterpret_cast<AccessWord<ACCESS>*>(p) = *reinterpret_cast<const AccessWord<ACCESS>*>(buf + at);
+  });
 }
-__device__ __forceinline__ void store_chunk(int access, const uint8_t* buf, void* to, long long ld, int rows, int cols, int lane) {
-  uint16_t* at = static_cast<uint16_t*>(to);
-  if (access == 16) store_chunk<16>(buf, at, ld, rows, cols, lane);
-  else if (access == 4) store_chunk<4>(buf, at, ld, rows, cols, lane);
-  else store_chunk<2>(buf, at, ld, rows, cols, lane);
-}
-
-// The same from memory; what lies outside is left as it is.
 template <int ACCESS>
 __device__ __forceinline__ void load_chunk(uint8_t* buf, const uint16_t* from, long long ld, int rows, int cols, int lane) {
-  constexpr int LANES = 64 / ACCESS, STEP = 32 / LANES;
-  const int piece = lane % LANES, col = piece * (ACCESS / 2);
-#pragma unroll
-  for (int i = 0; i < LANES; ++i) {
-    const int row = i * STEP + lane / LANES;
-    if (row < rows && col < cols) {
-      uint8_t* to = buf + chunk_at(row, piece * ACCESS / 16) + piece * ACCESS % 16;
-      const uint16_t* at = from + row * ld + col;
-      if constexpr (ACCESS == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(at);
-      else if constexpr (ACCESS == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(at);
-      else *reinterpret_cast<uint16_t*>(to) = *at;
-    }
-  }
+  each_piece<ACCESS>(const_cast<uint16_t*>(from), ld, rows, cols, lane, [&](uint32_t at, const uint16_t* p) {
+    *reinterpret_cast<AccessWord<ACCESS>*>(buf + at) = *reinterpret_cast<const AccessWord<ACCESS>*>(p);
+  });
 }
-__device__ __forceinline__ void load_chunk(int access, uint8_t* buf, const void* from, long long ld, int rows, int cols, int lane) {
-  const uint16_t* at = static_cast<const uint16_t*>(from);
-  if (access == 16) load_chunk<16>(buf, at, ld, rows, cols, lane);
-  else if (access == 4) load_chunk<4>(buf, at, ld, rows, cols, lane);
-  else load_chunk<2>(buf, at, ld, rows, cols, lane);
+__device__ __forceinline__ void store_chunk(int access, const uint8_t* buf, uint16_t* to, long long ld, int rows, int cols, int lane) {
+  if (access == 16) store_chunk<16>(buf, to, ld, rows, cols, lane);
+  else if (access == 4) store_chunk<4>(buf, to, ld, rows, cols, lane);
+  else store_chunk<2>(buf, to, ld, rows, cols, lane);
 }
 
-// The lane's row of the chunk: rounded to T into it, or widened out of it.
+// A lane's row of a chunk: 64 sums, as pairs.
+struct Row {
+  float2 v[CHUNK_COLS / 2];
+};
+
+// Rounded to T into the buffer.
 template <typename T>
-__device__ __forceinline__ void put_row(uint8_t* buf, const float (&v)[32], int lane) {
+__device__ __forceinline__ void put_row(uint8_t* buf, const Row& r, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < CHUNK_COLS / 8; ++i)
     *reinterpret_cast<uint4*>(buf + chunk_at(lane, i)) =
-        make_uint4(pack2(v[8 * i], v[8 * i + 1], T()), pack2(v[8 * i + 2], v[8 * i + 3], T()),
-                   pack2(v[8 * i + 4], v[8 * i + 5], T()), pack2(v[8 * i + 6], v[8 * i + 7], T()));
+        make_uint4(pack2(r.v[4 * i].x, r.v[4 * i].y, T()), pack2(r.v[4 * i + 1].x, r.v[4 * i + 1].y, T()),
+                   pack2(r.v[4 * i + 2].x, r.v[4 * i + 2].y, T()), pack2(r.v[4 * i + 3].x, r.v[4 * i + 3].y, T()));
 }
+// Eight elements added to the pairs from 4 i on.
 template <typename T>
-__device__ __forceinline__ void add_row(const uint8_t* buf, float (&v)[32], int lane) {
+__device__ __forceinline__ void add_piece(Row& r, int i, uint4 q) {
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 q = *reinterpret_cast<const uint4*>(buf + chunk_at(lane, i));
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+  for (int j = 0; j < 4; ++j) r.v[4 * i + j] = __fadd2_rn(r.v[4 * i + j], unpack2(u[j], T()));
+}
+
+// bias[0 .. 63] added, of which `cols` exist: the same for all lanes, so 16-byte loads that one cache line answers.
+template <typename T, typename B>
+__device__ __forceinline__ void add_bias(Row& r, const B* bias, int cols) {
+  if (cols >= CHUNK_COLS && reinterpret_cast<uintptr_t>(bias) % 16 == 0) {
+    const uint4* q = reinterpret_cast<const uint4*>(bias);
+    if constexpr (sizeof(B) == 4) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2(u[j], T());
-      v[8 * i + 2 * j] += f.x;
-      v[8 * i + 2 * j + 1] += f.y;
+      for (int i = 0; i < CHUNK_COLS / 4; ++i) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(q) + i);
+        r.v[2 * i] = __fadd2_rn(r.v[2 * i], make_float2(f.x, f.y));
+        r.v[2 * i + 1] = __fadd2_rn(r.v[2 * i + 1], make_float2(f.z, f.w));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CHUNK_COLS / 8; ++i) add_piece<T>(r, i, __ldg(q + i));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CHUNK_COLS / 2; ++i) {
+      r.v[i].x += 2 * i < cols ? to_float(bias[2 * i]) : 0.f;
+      r.v[i].y += 2 * i + 1 < cols ? to_float(bias[2 * i + 1]) : 0.f;
     }
   }
 }
 
-// What an epilogue's warp holds: its rows of the tile, its chunk buffer, and the forward pass's bias of its columns.
+// What an epilogue's warp holds: its rows of the tile and its chunk buffer.
 struct WarpPlace {
   int row0;                // D's row of lane 0
   int rows;                // of the 32, how many belong to the group
   int lane;
   uint8_t* buf;            // CHUNK_BYTES
-  float* bias;             // of the chunks that it takes, 32 each
 };
 
-// The chunk in the buffer to a result: whole by TMA where the layout allows it (BULK), else by row-wise stores.  The buffer
-// may be written again after `chunk_left`.
+// What the buffer held has left it.
+template <bool BULK>
+__device__ __forceinline__ void chunk_left(const WarpPlace& w) {
+  if (BULK && w.lane == 0) bulk_wait_read_all();
+  __syncwarp();
+}
+
+// The chunk in the buffer to a result: whole by TMA where the layout allows it (BULK), else by row-wise stores.
 template <bool BULK>
 __device__ __forceinline__ void send_chunk(const WarpPlace& w, bool bulk, const CUtensorMap* map, int batch, int access, void* to,
                                            long long ld, int col0, int cols) {
@@ -318,76 +354,82 @@ __device__ __forceinline__ void send_chunk(const WarpPlace& w, bool bulk, const 
     store_chunk(access, w.buf, static_cast<uint16_t*>(to) + w.row0 * ld + col0, ld, w.rows, cols, w.lane);
   }
 }
-template <bool BULK>
-__device__ __forceinline__ void chunk_left(const WarpPlace& w) {
-  if (BULK && w.lane == 0) bulk_wait_read_all();
-  __syncwarp();
-}
 
-// One chunk's sums to the results: columns col0 .. col0 + 31, `bias` those columns' (forward).
+// The residual's chunks on their way by TMA into a buffer of the warp's own, a chunk ahead: their way from memory is longer
+// than a short product's tile (65536x768->2816: 590 us where it is waited for).  Rows that TMA cannot address are read into
+// the chunk's buffer when they are needed.
+struct ResidualFeed {
+  uint8_t* buf;            // CHUNK_BYTES, or null: not by TMA
+  uint64_t* landed;
+  uint32_t asked, used;
+  __device__ __forceinline__ void ask(const LinearParams& P, const LinearJob& J, const WarpPlace& w, int col0) {
+    if (!buf || w.rows <= 0 || col0 >= J.N) return;
+    ++asked;
+    if (w.lane != 0) return;
+    mbar_expect_tx(landed, CHUNK_BYTES);
+    tma_load_3d(buf, &P.residual_map, landed, col0, w.row0, 0);
+  }
+};
+
+// One chunk's sums to the results: columns col0 .. col0 + 63.
 //   z = v + bias;  y = act(z) + residual;  each rounded once.
 // Both leave through one buffer: a second one would cost the products a stage of their ring, and with it 10 % of their rate.
+// False if a wait for the residual ran out.
 template <bool FORWARD, typename T, bool BULK>
-__device__ __forceinline__ void finish_chunk(const LinearParams& P, const LinearJob& J, const Unit& u, const WarpPlace& w,
-                                             float (&v)[32], int col0, const float* bias) {
+__device__ __forceinline__ bool finish_chunk(const LinearParams& P, const LinearJob& J, const Unit& u, const WarpPlace& w, Row& r,
+                                             int col0, ResidualFeed& res, const volatile int* abort_flag) {
   const int cols = J.N - col0;
-  if (w.rows <= 0 || cols <= 0) return;            // (the same for all lanes)
+  if (w.rows <= 0 || cols <= 0) return true;       // (the same for all lanes)
   if constexpr (FORWARD) {
     if (P.bias) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 b = reinterpret_cast<const float4*>(bias)[i];
-        v[4 * i] += b.x;
-        v[4 * i + 1] += b.y;
-        v[4 * i + 2] += b.z;
-        v[4 * i + 3] += b.w;
-      }
+      const long long at = static_cast<long long>(u.group) * J.N + col0;
+      if (P.bias_f32) add_bias<T>(r, static_cast<const float*>(P.bias) + at, cols);
+      else add_bias<T>(r, static_cast<const T*>(P.bias) + at, cols);
     }
     if (P.z) {
       chunk_left<BULK>(w);
-      put_row<T>(w.buf, v, w.lane);
+      put_row<T>(w.buf, r, w.lane);
       send_chunk<BULK>(w, J.bulk, &P.z_map, 0, P.z_access, P.z, P.z_ld, col0, cols);
     }
     with_activation(P.act, [&](auto act) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate<decltype(act)::value>(v[i]);
+      for (int i = 0; i < CHUNK_COLS / 2; ++i) r.v[i] = activate<decltype(act)::value>(r.v[i]);
     });
+  }
+  if constexpr (FORWARD) {
+    if (BULK && res.buf) {
+      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(res.landed, res.used & 1, abort_flag))) return false;
+      ++res.used;
+#pragma unroll
+      for (int i = 0; i < CHUNK_COLS / 8; ++i)
+        add_piece<T>(r, i, *reinterpret_cast<const uint4*>(res.buf + chunk_at(w.lane, i)));
+      __syncwarp();                                // read: the next may land
+      if (col0 + 2 * CHUNK_COLS < u.n0 + u.wide) res.ask(P, J, w, col0 + 2 * CHUNK_COLS);
+    }
   }
   chunk_left<BULK>(w);
   if constexpr (FORWARD) {
-    if (P.residual) {
-      load_chunk(P.residual_access, w.buf, static_cast<const uint16_t*>(P.residual) + w.row0 * P.residual_ld + col0,
-                 P.residual_ld, w.rows, cols, w.lane);
+    if (P.residual && !(BULK && res.buf)) {
+      const uint16_t* from = static_cast<const uint16_t*>(P.residual) + w.row0 * P.residual_ld + col0;
+      if (P.residual_access == 16) load_chunk<16>(w.buf, from, P.residual_ld, w.rows, cols, w.lane);
+      else if (P.residual_access == 4) load_chunk<4>(w.buf, from, P.residual_ld, w.rows, cols, w.lane);
+      else load_chunk<2>(w.buf, from, P.residual_ld, w.rows, cols, w.lane);
       __syncwarp();
-      add_row<T>(w.buf, v, w.lane);                // (a lane reads and writes its own row)
+#pragma unroll
+      for (int i = 0; i < CHUNK_COLS / 8; ++i)     // (a lane reads and writes its own row)
+        add_piece<T>(r, i, *reinterpret_cast<const uint4*>(w.buf + chunk_at(w.lane, i)));
     }
   }
-  put_row<T>(w.buf, v, w.lane);
+  put_row<T>(w.buf, r, w.lane);
   send_chunk<BULK>(w, J.bulk, &J.d, u.group * J.over_rows, J.access, static_cast<uint16_t*>(J.out) + u.group * J.group_stride,
                    J.ld, col0, cols);
+  return true;
 }
 
-// The bias of the warp's chunks of a unit (chunk i: columns n0 + 32 (half + 2 i)), zeros past the last column.
-template <typename T>
-__device__ __forceinline__ void fetch_bias(const LinearParams& P, const LinearJob& J, const Unit& u, const WarpPlace& w, int half) {
-  if (!P.bias) return;
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int col = u.n0 + 32 * (half + 2 * i) + w.lane;
-    const long long at = static_cast<long long>(u.group) * J.N + col;
-    float b = 0.f;
-    if (col < J.N)
-      b = P.bias_f32 ? static_cast<const float*>(P.bias)[at] : to_float(static_cast<const T*>(P.bias)[at]);
-    w.bias[32 * i + w.lane] = b;
-  }
-  __syncwarp();
-}
-
-// Where the warp `warp` of CTA `rank` keeps the fp32 sums of one chunk of a unit: 8 float4 per lane, 32 lanes side by side.
+// Where the warp `warp` of CTA `rank` keeps the fp32 sums of one chunk of a unit: 16 float4 per lane, 32 lanes side by side.
 __device__ __forceinline__ float4* part_of(const LinearJob& J, const Unit& u, int split, uint32_t rank, int warp, int chunk) {
   const long long tile = split * J.part_tiles + u.tile;
-  return reinterpret_cast<float4*>(J.parts) + (((tile * 2 + rank) * 8 + warp) * (J.wide / 64) + chunk) * 8 * 32;
+  return reinterpret_cast<float4*>(J.parts) + (((tile * 2 + rank) * 8 + warp) * (J.wide / 128) + chunk) * 16 * 32;
 }
 
 }  // namespace mb

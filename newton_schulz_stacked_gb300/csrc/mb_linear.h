@@ -17,7 +17,7 @@ constexpr int LINEAR_DEEP = 64;          // of the contraction in one stage
 //   over a group's rows (dweight):  the contraction runs over them, D is the group's matrix.
 struct LinearJob {
   CUtensorMap a, b;
-  CUtensorMap d;           // the result in boxes of 32 x 32 (64-byte swizzle), where `bulk`
+  CUtensorMap d;           // the result in boxes of 32 rows x 64, where `bulk`
   int bulk;                // whole chunks are stored by TMA (of the forward pass: z too)
   int a_mn, b_mn;          // the operand's rows run along memory (boxes of 64 x 64), not the contraction
   int over_rows;
@@ -46,6 +46,8 @@ struct LinearParams {
   const void* residual;
   long long residual_ld;
   int residual_access;
+  int residual_bulk;       // its chunks come by TMA
+  CUtensorMap residual_map;
   void* z;
   long long z_ld;
   int z_access;

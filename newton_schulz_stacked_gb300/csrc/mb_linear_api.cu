@@ -229,15 +229,15 @@ struct Call {
     return MB_OK;
   }
   int map(CUtensorMap* m, const Operand& o, int64_t rows, int64_t batch, int box_rows) const {
-    return api_encode_rows(m, o.base, type == MB_BF16, o.cols, rows, batch, o.ld, box_rows, 64);
+    return api_encode_rows(m, o.base, type == MB_BF16, o.cols, rows, batch, o.ld, box_rows);
   }
   int result_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t batch, int64_t ld) const {
-    return api_encode_rows(m, p, type == MB_BF16, cols, rows, batch, rows > 1 ? ld : up(cols, 8), 32, 32);
+    return api_encode_rows(m, p, type == MB_BF16, cols, rows, batch, rows > 1 ? ld : up(cols, 8), 32);
   }
 };
 
-// Whole chunks of a result leave by TMA: rows at 16-byte boundaries.
-bool bulk_stores(const void* p, int64_t ld, int64_t cols, int64_t rows) {
+// Whether TMA can address chunks of a result or residual: rows at 16-byte boundaries.
+bool bulk_chunks(const void* p, int64_t ld, int64_t cols, int64_t rows) {
   return aligned(p, 16) && (rows <= 1 || (ld % 8 == 0 && ld >= cols));
 }
 
@@ -359,12 +359,14 @@ int mb_linear(const mb_linear_desc* desc, void* workspace, size_t workspace_byte
   set_cut(j, plan.y, call.ws);
   MB_TRY(call.map(&j.a, plan.x, d.rows, 1, 128));
   MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, j.wide / 2));
-  j.bulk = j.splits == 1 && bulk_stores(d.y, d.y_stride, d.out, d.rows) &&
-           (!d.z || bulk_stores(d.z, d.z_stride, d.out, d.rows));
+  j.bulk = j.splits == 1 && bulk_chunks(d.y, d.y_stride, d.out, d.rows) &&
+           (!d.z || bulk_chunks(d.z, d.z_stride, d.out, d.rows));
   if (j.bulk) {
     MB_TRY(call.result_map(&j.d, d.y, d.rows, d.out, 1, d.y_stride));
     if (d.z) MB_TRY(call.result_map(&p.z_map, d.z, d.rows, d.out, 1, d.z_stride));
   }
+  p.residual_bulk = d.residual && j.splits == 1 && bulk_chunks(d.residual, d.residual_stride, d.out, d.rows);
+  if (p.residual_bulk) MB_TRY(call.result_map(&p.residual_map, d.residual, d.rows, d.out, 1, d.residual_stride));
   const Cut* const cuts[2] = {&plan.y, nullptr};
   MB_TRY(run_products(p, cuts, true, call));
   api_launched(MB_MARK_LINEAR, call.launches, call.stream);
@@ -445,7 +447,7 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     set_cut(j, plan.dw, call.ws);
     MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 64));
     MB_TRY(call.map(&j.b, plan.x, d.rows, 1, 64));
-    j.bulk = j.splits == 1 && bulk_stores(d.dweight, d.in, d.in, 2);
+    j.bulk = j.splits == 1 && bulk_chunks(d.dweight, d.in, d.in, 2);
     if (j.bulk) MB_TRY(call.result_map(&j.d, d.dweight, d.out, d.in, d.groups, d.in));
   }
   if (d.dx) {
@@ -460,7 +462,7 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     set_cut(j, plan.dx, call.ws);
     MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 128));
     MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, 64));
-    j.bulk = j.splits == 1 && bulk_stores(d.dx, d.dx_stride, d.in, d.rows);
+    j.bulk = j.splits == 1 && bulk_chunks(d.dx, d.dx_stride, d.in, d.rows);
     if (j.bulk) MB_TRY(call.result_map(&j.d, d.dx, d.rows, d.in, 1, d.dx_stride));
   }
   if (p.jobs == 2) p.extra = extra_units(plan.dw, plan.dx);
