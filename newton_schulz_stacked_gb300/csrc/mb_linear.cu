@@ -421,7 +421,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       const int buf = k & 1;
       w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
       w.rows = min(32, u.m_end - w.row0);
-      if constexpr (FORWARD) res.ask(P, J, w, u.n0 + CHUNK_COLS * half);
+      float2 bias[2] = {};
+      if constexpr (FORWARD) {
+        res.ask(P, J, w, u.n0 + CHUNK_COLS * half);
+        bias[0] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * half, lane);
+        bias[1] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * (half + 2), lane);
+      }
       if (!mbar_wait_or_abort(&tfull[buf], (k >> 1) & 1, abort_flag)) {
         fail();
         break;
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
           for (int i = 0; i < CHUNK_COLS / 4; ++i)
             part[32 * i + lane] = make_float4(v.v[2 * i].x, v.v[2 * i].y, v.v[2 * i + 1].x, v.v[2 * i + 1].y);
         } else {
-          ok = finish_chunk<FORWARD, T, true>(P, J, u, w, v, u.n0 + CHUNK_COLS * c, res, abort_flag);
+          ok = finish_chunk<FORWARD, T, true>(P, J, u, w, v, u.n0 + CHUNK_COLS * c, c < 2 ? bias[0] : bias[1], res, abort_flag);
         }
       }
       if (!ok) {
@@ -502,6 +507,7 @@ __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __gri
   if (w.rows <= 0) return;
   const int c = half + 2 * blockIdx.y;
   if (c >= u.wide / CHUNK_COLS) return;
+  const float2 bias = FORWARD ? bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * c, lane) : make_float2(0.f, 0.f);
   ResidualFeed none{nullptr, nullptr, 0, 0};
   Row v;
 #pragma unroll
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __gri
       v.v[2 * i + 1] = __fadd2_rn(v.v[2 * i + 1], make_float2(q.z, q.w));
     }
   }
-  finish_chunk<FORWARD, T, false>(P, J, u, w, v, u.n0 + CHUNK_COLS * c, none, nullptr);
+  finish_chunk<FORWARD, T, false>(P, J, u, w, v, u.n0 + CHUNK_COLS * c, bias, none, nullptr);
 }
 
 // Per-device set-up (the shared-memory limit, the number of pairs that can be resident) is done by the first call on each

@@ -298,29 +298,29 @@ __device__ __forceinline__ void add_piece(Row& r, int i, uint4 q) {
   for (int j = 0; j < 4; ++j) r.v[4 * i + j] = __fadd2_rn(r.v[4 * i + j], unpack2(u[j], T()));
 }
 
-// bias[0 .. 63] added, of which `cols` exist: the same for all lanes, so 16-byte loads that one cache line answers.
-template <typename T, typename B>
-__device__ __forceinline__ void add_bias(Row& r, const B* bias, int cols) {
-  if (cols >= CHUNK_COLS && reinterpret_cast<uintptr_t>(bias) % 16 == 0) {
-    const uint4* q = reinterpret_cast<const uint4*>(bias);
-    if constexpr (sizeof(B) == 4) {
-#pragma unroll
-      for (int i = 0; i < CHUNK_COLS / 4; ++i) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(q) + i);
-        r.v[2 * i] = __fadd2_rn(r.v[2 * i], make_float2(f.x, f.y));
-        r.v[2 * i + 1] = __fadd2_rn(r.v[2 * i + 1], make_float2(f.z, f.w));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < CHUNK_COLS / 8; ++i) add_piece<T>(r, i, __ldg(q + i));
-    }
+// The bias of a chunk's columns, two to a lane, zeros past the last.  Asked for before the sums are there: with the ring in
+// shared memory next to nothing is left to cache it, and a chunk that waits for it takes 1700 cycles longer.
+template <typename T>
+__device__ __forceinline__ float2 bias_of(const LinearParams& P, const LinearJob& J, int group, int col0, int lane) {
+  const int col = col0 + 2 * lane;
+  const long long at = static_cast<long long>(group) * J.N + col;
+  float2 b = make_float2(0.f, 0.f);
+  if (!P.bias) return b;
+  if (P.bias_f32) {
+    const float* p = static_cast<const float*>(P.bias) + at;
+    if (col < J.N) b.x = p[0];
+    if (col + 1 < J.N) b.y = p[1];
   } else {
-#pragma unroll
-    for (int i = 0; i < CHUNK_COLS / 2; ++i) {
-      r.v[i].x += 2 * i < cols ? to_float(bias[2 * i]) : 0.f;
-      r.v[i].y += 2 * i + 1 < cols ? to_float(bias[2 * i + 1]) : 0.f;
-    }
+    const T* p = static_cast<const T*>(P.bias) + at;
+    if (col < J.N) b.x = to_float(p[0]);
+    if (col + 1 < J.N) b.y = to_float(p[1]);
   }
+  return b;
+}
+__device__ __forceinline__ void add_bias(Row& r, float2 bias) {
+#pragma unroll
+  for (int i = 0; i < CHUNK_COLS / 2; ++i)
+    r.v[i] = __fadd2_rn(r.v[i], make_float2(__shfl_sync(0xffffffffu, bias.x, i), __shfl_sync(0xffffffffu, bias.y, i)));
 }
 
 // What an epilogue's warp holds: its rows of the tile and its chunk buffer.
@@ -377,15 +377,11 @@ struct ResidualFeed {
 // False if a wait for the residual ran out.
 template <bool FORWARD, typename T, bool BULK>
 __device__ __forceinline__ bool finish_chunk(const LinearParams& P, const LinearJob& J, const Unit& u, const WarpPlace& w, Row& r,
-                                             int col0, ResidualFeed& res, const volatile int* abort_flag) {
+                                             int col0, float2 bias, ResidualFeed& res, const volatile int* abort_flag) {
   const int cols = J.N - col0;
   if (w.rows <= 0 || cols <= 0) return true;       // (the same for all lanes)
   if constexpr (FORWARD) {
-    if (P.bias) {
-      const long long at = static_cast<long long>(u.group) * J.N + col0;
-      if (P.bias_f32) add_bias<T>(r, static_cast<const float*>(P.bias) + at, cols);
-      else add_bias<T>(r, static_cast<const T*>(P.bias) + at, cols);
-    }
+    if (P.bias) add_bias(r, bias);
     if (P.z) {
       chunk_left<BULK>(w);
       put_row<T>(w.buf, r, w.lane);
