@@ -23,6 +23,10 @@
 //                   row-wise stores; before its first tile each takes a share of what else the call leaves to do: zeros in
 //                   rows of no group, dbias from the slabs' sums
 //   warp 10         clears the blocks that reach past a group
+// Where dz has to be formed first (dy act'(z), a pass over memory as long as half the products), the epilogue warps of the
+// backward pass do it in pieces while the MMAs run, in the order in which the products need the rows; the A operand's
+// producers wait for the slabs of rows that they load.  Pieces are claimed from a counter, so that a CTA that is not
+// resident yet holds none.
 // Producers and issuer run as whole warps, the same in all lanes, and elect a lane for each TMA copy, MMA or commit: those take
 // their operands from uniform registers, and values that one lane alone has worked out are moved there one by one.
 //
@@ -158,6 +162,12 @@ __device__ __forceinline__ Feed feed_of(const LinearParams& P, const Unit& u, bo
   return f;
 }
 
+__device__ __forceinline__ int claim_piece(unsigned* next, int lane) {
+  unsigned p = 0;
+  if (lane == 0) p = atomicAdd(next, 1u);
+  return static_cast<int>(__shfl_sync(0xffffffffu, p, 0));
+}
+
 // A share of the work beside the tiles, by the epilogue's warps: warp `me` of `all`.
 template <typename T>
 __device__ void side_work(const LinearParams& P, const Groups& G, long long me, long long all, int lane) {
@@ -275,6 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     uint8_t* const ring = for_a ? sA : sB;
     uint32_t st = 0, ph = 0, it = 0;
     bool ok = true;
+    Seen seen;
     for (int i = 0; i < mine && ok && !__any_sync(0xffffffffu, *abort_flag); ++i) {
       Unit u;
       decode_same(P, G, first_units, deal(i), u);
@@ -283,10 +294,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
       const uint32_t flags = (J.a_mn ? NOTE_A_MN : 0u) | (J.b_mn ? NOTE_B_MN : 0u) | (u.kb0 < u.kb1 ? 0u : NOTE_NOTHING);
       const int kb0 = u.kb0, kb1 = max(u.kb1, kb0 + 1);        // a unit without blocks takes a stage for its note
+      const bool await = !FORWARD && for_a && P.ahead.next && !(flags & NOTE_NOTHING);   // dz is still being made
+      if (await && !J.over_rows) {
+        const int row = u.m0 + static_cast<int>(rank) * BM;
+        ok = seen.rows(P.ahead, row, min(row + BM, u.m_end), lane, abort_flag);
+        if (!ok) break;
+      }
       int x = f.x, y = f.y;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         if (it >= stages) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag));
+          if (!ok) break;
+        }
+        if (await && J.over_rows) {
+          ok = seen.rows(P.ahead, y, min(y + LINEAR_DEEP, u.k_end), lane, abort_flag);
           if (!ok) break;
         }
         const bool nothing = (flags & NOTE_NOTHING) != 0, past_end = !nothing && kb >= f.past_from;
@@ -414,7 +435,19 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     ResidualFeed res{with_residual ? (half ? sB : sA) + (STAGES - 1) * TILE_BYTES + (ew & 3) * CHUNK_BYTES : nullptr, &landed[ew], 0, 0};
     const uint32_t tempty_even = map_to_rank(&tempty[0], 0);
     side_work<T>(P, G, static_cast<long long>(blockIdx.x) * EPI_WARPS + ew, static_cast<long long>(gridDim.x) * EPI_WARPS, lane);
-    for (int k = 0; k < mine; ++k) {
+    // the piece of dz that this warp has claimed (none from `pieces` on)
+    const int pieces = !FORWARD && P.ahead.next ? P.ahead.ways * P.ahead.per_way * P.ahead.column_groups : 0;
+    int piece = pieces > 0 ? claim_piece(P.ahead.next, lane) : 0;
+    for (int k = 0; k < mine || piece < pieces; ++k) {
+      // pieces while no sums are ready, each claimed under the work on the one before
+      while (piece < pieces &&
+             !(k < mine && __all_sync(0xffffffffu, mbar_test(&tfull[k & 1], (k >> 1) & 1))) &&
+             !__any_sync(0xffffffffu, *abort_flag)) {
+        const int now = piece;
+        piece = claim_piece(P.ahead.next, lane);
+        do_piece<T>(P.ahead, G, now, lane);
+      }
+      if (k >= mine) break;
       Unit u;
       decode_unit(P, G, first_units, deal(k), u);
       const LinearJob& J = P.job[u.job];

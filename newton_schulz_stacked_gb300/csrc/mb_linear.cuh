@@ -225,6 +225,118 @@ __device__ __forceinline__ void with_activation(int act, F&& f) {
   }
 }
 
+// ---------------------------------------------------------------- dz by pieces
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+// Orders this thread's generic accesses of global memory with asynchronous (TMA) ones.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// dz of rows [begin, end) of one group, columns col .. col + 7, eight rows on their way at a time; the sums of dz.
+template <typename T, int ACT, int ROWS>
+__device__ __forceinline__ void slope_rows_of(const T* dy, long long dy_ld, const T* z, long long z_ld, T* dz, long long dz_ld,
+                                              float (&sum)[8]) {
+  Eight<T> g[ROWS], x[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    g[i].load(dy + i * dy_ld);
+    x[i].load(z + i * z_ld);
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    float v[8], s[8];
+    g[i].get(v);
+    x[i].get(s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] *= slope<ACT>(s[j]);
+      sum[j] += v[j];
+    }
+    g[i].set(v);
+    g[i].store(dz + i * dz_ld);
+  }
+}
+template <typename T, int ACT>
+__device__ __forceinline__ void slope_piece(const LinearSlopeParams& p, int begin, int end, int col, float (&sum)[8]) {
+  constexpr int ROWS = 8;
+  const T* dy = static_cast<const T*>(p.dy) + begin * p.dy_ld + col;
+  const T* z = static_cast<const T*>(p.z) + begin * p.z_ld + col;
+  T* dz = static_cast<T*>(p.dz) + begin * p.dz_ld + col;
+  int left = end - begin;
+  for (; left >= ROWS; left -= ROWS, dy += ROWS * p.dy_ld, z += ROWS * p.z_ld, dz += ROWS * p.dz_ld)
+    slope_rows_of<T, ACT, ROWS>(dy, p.dy_ld, z, p.z_ld, dz, p.dz_ld, sum);
+  for (; left > 0; --left, dy += p.dy_ld, z += p.z_ld, dz += p.dz_ld)
+    slope_rows_of<T, ACT, 1>(dy, p.dy_ld, z, p.z_ld, dz, p.dz_ld, sum);
+}
+
+// Piece number `at` by one warp, and its report.
+template <typename T>
+__device__ __forceinline__ void do_piece(const LinearAhead& A, const Groups& G, int at, int lane) {
+  const LinearSlopeParams& p = A.slope;
+  const int turn = at / A.column_groups, column = at - turn * A.column_groups;
+  const int step = turn / A.ways, slab = (turn - step * A.ways) * A.per_way + step;
+  if (slab >= A.slabs) return;                     // (the last range may be shorter)
+  const int col = column * 256 + 8 * lane;
+  const int begin = slab * LINEAR_PIECE_ROWS, end = min(begin + LINEAR_PIECE_ROWS, G.row[G.n]);
+  int g = 0;
+  if (G.n > 1) {                                   // the first group whose rows end past the piece's begin
+    int hi = G.n;
+    while (g < hi) {
+      const int mid = (g + hi) >> 1;
+      if (G.row[mid + 1] > begin) hi = mid;
+      else g = mid + 1;
+    }
+  }
+  for (int row = begin; g < G.n && row < end; ++g) {
+    const int stop = min(end, G.row[g + 1]);
+    if (stop <= row) continue;
+    if (col < p.cols) {
+      float sum[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+      with_activation(p.act, [&](auto act) { slope_piece<T, decltype(act)::value>(p, row, stop, col, sum); });
+      if (p.parts) {
+        float4* to = reinterpret_cast<float4*>(p.parts + static_cast<long long>(slab + g) * p.cols + col);
+        to[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        to[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+      }
+    }
+    row = stop;
+  }
+  fence_async_global();
+  __syncwarp();
+  if (lane == 0) add_release(&A.done[slab], 1u);
+}
+
+// Which slabs of dz a producer has seen done: [begin, end).
+struct Seen {
+  int begin = 0, end = 0;
+  // Waits (bounded, as a whole warp) until the slabs of rows [from, to) are.
+  __device__ __forceinline__ bool rows(const LinearAhead& A, int from, int to, int lane, const volatile int* abort_flag) {
+    const int first = from / LINEAR_PIECE_ROWS, last = min((to - 1) / LINEAR_PIECE_ROWS, A.slabs - 1);
+    if (last < first || (first >= begin && last < end)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 0;; ++i) {
+      const int slab = first + lane;
+      const bool ok = slab < A.slabs && load_acquire(&A.done[slab]) >= static_cast<unsigned>(A.column_groups);
+      const unsigned missing = ~__ballot_sync(0xffffffffu, ok);
+      begin = first;
+      end = first + (missing ? __ffs(missing) - 1 : 32);
+      if (last < end) break;
+      __nanosleep(200);
+      if (__any_sync(0xffffffffu, *abort_flag || globaltimer_ns() - t0 > WAIT_LIMIT_NS)) return false;
+    }
+    fence_async_global();
+    return true;
+  }
+};
+
 // ---------------------------------------------------------------- chunks of 32 rows x 64 columns
 
 // A warp's chunk in shared memory: rows of 128 bytes whose 16-byte pieces are exchanged by row (TMA's 128-byte swizzle), so

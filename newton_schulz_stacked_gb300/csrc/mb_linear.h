@@ -33,6 +33,32 @@ struct LinearJob {
   long long part_tiles;    // tiles that it holds for each split
 };
 
+// dz = dy act'(z) and the sums of dz over slabs of rows.
+struct LinearSlopeParams {
+  const void* dy;
+  long long dy_ld;
+  const void* z;           // or null: dz = dy, not written
+  long long z_ld;
+  void* dz;                // [rows, dz_ld], 16-byte aligned rows
+  long long dz_ld;
+  int act, rows, cols, groups;
+  const int* ends;
+  float* parts;            // or null
+  int slab;                // rows of a slab
+  int access;              // bytes that the rows allow to be read at a time: 16, 4 or 2
+};
+
+// The same as pieces that the products' epilogue warps take while they have nothing to store (LINEAR_PIECE_ROWS rows x 256
+// columns, in the order in which the products need them).
+constexpr int LINEAR_PIECE_ROWS = 32;
+struct LinearAhead {
+  LinearSlopeParams slope;
+  unsigned* next;          // the next piece, zero at the launch; null: dz is there already
+  unsigned* done;          // [slabs of LINEAR_PIECE_ROWS rows] column groups that are done, zero at the launch
+  int slabs, column_groups;
+  int ways, per_way;       // the pieces go through `ways` ranges of `per_way` slabs in turn
+};
+
 struct LinearParams {
   LinearJob job[2];
   int jobs;
@@ -57,21 +83,15 @@ struct LinearParams {
   void* db;
   int db_f32, db_cols, slab;
   int* status;
+  LinearAhead ahead;       // backward
 };
 
-// dz = dy act'(z) and the sums of dz over slabs of rows.
-struct LinearSlopeParams {
-  const void* dy;
-  long long dy_ld;
-  const void* z;           // or null: dz = dy, not written
-  long long z_ld;
-  void* dz;                // [rows, dz_ld], 16-byte aligned rows
-  long long dz_ld;
-  int act, rows, cols, groups;
+// dbias from the sums over slabs of rows.
+struct LinearBiasParams {
+  const float* parts;      // [slabs + groups][cols]
+  void* db;
+  int f32, cols, slab, rows, groups;
   const int* ends;
-  float* parts;            // or null
-  int slab;                // rows of a slab
-  int access;              // bytes that the rows allow to be read at a time: 16, 4 or 2
 };
 
 // Rows of 2-byte elements into rows that start at 16-byte boundaries.
@@ -88,6 +108,7 @@ struct LinearPackParams {
 cudaError_t launch_linear(const LinearParams& p, int type, bool forward, int pairs_wanted, cudaStream_t s);
 cudaError_t launch_linear_join(const LinearParams& p, int job, int type, bool forward, long long tiles, cudaStream_t s);
 cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream_t s);
+cudaError_t launch_linear_bias(const LinearBiasParams& p, int type, cudaStream_t s);
 cudaError_t launch_linear_pack(const LinearPackParams& p, int sms, cudaStream_t s);
 
 }  // namespace mb

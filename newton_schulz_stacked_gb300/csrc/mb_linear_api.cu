@@ -19,6 +19,7 @@ namespace {
 constexpr int64_t MAX_ROWS = 1ll << 30, MAX_WIDTH = 1ll << 20;
 constexpr int64_t MAX_PAIRS = 76;        // what the cuts are planned for: the pairs of a GB300's 152 SMs
 constexpr int MAX_SPLITS = 16;
+constexpr int64_t AHEAD_ELEMENTS = 1ll << 22;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t parts_of(int64_t n, int64_t by) { return (n + by - 1) / by; }
@@ -163,6 +164,9 @@ ForwardPlan plan_forward(const mb_linear_desc& d) {
 
 struct BackwardPlan {
   bool slope;              // dz is formed (else it is dy)
+  bool ahead;              // by the products' launch
+  size_t counters;         // ahead: the next piece, and the column groups done of each slab
+  int64_t counter_bytes;
   Operand dz, x, w;
   Cut dx, dw;
   int slab;
@@ -197,6 +201,18 @@ BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
                d.dx ? &p.dx : nullptr);
   if (d.dweight) reserve_parts(p.dw, ws);
   if (d.dx) reserve_parts(p.dx, ws);
+  // Forming dz in a launch of its own pays where it is shorter than what its start under the products costs.
+  p.ahead = p.slope && products && d.rows * static_cast<int64_t>(d.out) >= AHEAD_ELEMENTS &&
+            access_of(d.dy, d.dy_stride, d.out, d.rows) == 16 && access_of(d.z, d.z_stride, d.out, d.rows) == 16;
+  if (p.ahead) {
+    p.slab = LINEAR_PIECE_ROWS;
+    p.slabs = parts_of(d.rows, p.slab);
+    p.counter_bytes = (1 + p.slabs) * 4;
+    p.counters = ws.take(p.counter_bytes);
+    if (d.dbias) p.db_parts = ws.take((p.slabs + d.groups) * d.out * 4);
+    p.end = ws.end;
+    return p;
+  }
   // slabs of rows: about four CTAs for an SM, 32 to 1024 rows
   const int64_t columns = parts_of(d.out, 256);
   int64_t slab = up(parts_of(d.rows * columns, 608), 32);
@@ -400,6 +416,7 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
   else if (d.dx || d.dweight) MB_TRY(call.lay_out(plan.dz));
   if (d.dweight) MB_TRY(call.lay_out(plan.x));
   if (d.dx) MB_TRY(call.lay_out(plan.w));
+  LinearParams p{};
   if (plan.slope || d.dbias) {
     LinearSlopeParams s{};
     s.dy = d.dy;
@@ -417,17 +434,30 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     s.slab = plan.slab;
     s.access = access_of(d.dy, d.dy_stride, d.out, d.rows);
     if (plan.slope && access_of(d.z, d.z_stride, d.out, d.rows) < s.access) s.access = access_of(d.z, d.z_stride, d.out, d.rows);
-    const cudaError_t e = launch_linear_slope(s, d.type, call.stream);
-    if (e != cudaSuccess) return api_cuda_fail(e);
-    ++call.launches;
+    if (plan.ahead) {
+      LinearAhead& a = p.ahead;
+      a.slope = s;
+      a.next = reinterpret_cast<unsigned*>(call.ws + plan.counters);
+      a.done = a.next + 1;
+      a.slabs = static_cast<int>(plan.slabs);
+      a.column_groups = static_cast<int>(parts_of(d.out, 256));
+      // the units of dW go through their parts of the rows side by side
+      a.ways = d.dweight && d.groups == 1 ? plan.dw.splits : 1;
+      a.per_way = static_cast<int>(parts_of(plan.slabs, a.ways));
+      const cudaError_t e = cudaMemsetAsync(a.next, 0, plan.counter_bytes, call.stream);
+      if (e != cudaSuccess) return api_cuda_fail(e);
+    } else {
+      const cudaError_t e = launch_linear_slope(s, d.type, call.stream);
+      if (e != cudaSuccess) return api_cuda_fail(e);
+      ++call.launches;
+    }
   }
-  LinearParams p{};
   p.rows = static_cast<int>(d.rows);
   p.groups = d.groups;
   p.ends = d.ends;
   p.status = call.status;
   p.status_from = 1;
-  p.db = d.dbias;
+  p.db = plan.ahead ? nullptr : d.dbias;
   p.db_parts = reinterpret_cast<const float*>(call.ws + plan.db_parts);
   p.db_f32 = d.bias_type == MB_F32;
   p.db_cols = d.out;
@@ -467,6 +497,13 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
   }
   if (p.jobs == 2) p.extra = extra_units(plan.dw, plan.dx);
   MB_TRY(run_products(p, cuts, false, call));
+  if (plan.ahead && d.dbias) {
+    const LinearBiasParams b{reinterpret_cast<const float*>(call.ws + plan.db_parts), d.dbias, d.bias_type == MB_F32, d.out,
+                             plan.slab, static_cast<int>(d.rows), d.groups, d.ends};
+    const cudaError_t e = launch_linear_bias(b, d.type, call.stream);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    ++call.launches;
+  }
   api_launched(MB_MARK_LINEAR_BACKWARD, call.launches, call.stream);
   return MB_OK;
 }

@@ -148,7 +148,39 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
   }
 }
 
-}  // namespace
+// dbias of 32 columns of one group: the sums over the slabs that hold its rows, a run of them to each warp, then the warps', in
+// order.
+constexpr int BIAS_WARPS = 16;
+template <typename T>
+__global__ void __launch_bounds__(32 * BIAS_WARPS) linear_bias_kernel(const __grid_constant__ LinearBiasParams p) {
+  __shared__ float partial[BIAS_WARPS][32];
+  __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
+  begin_after_previous();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Groups G{groups, groups + LINEAR_MAX_GROUPS + 1, p.groups};
+  if (warp == 0) fill_groups(G, p.ends, p.rows, lane);
+  __syncthreads();
+  const int g = blockIdx.y, col = blockIdx.x * 32 + lane;
+  const int begin = G.row[g], end = G.row[g + 1];
+  const int first = begin / p.slab, slabs = end > begin ? (end - 1) / p.slab - first + 1 : 0;
+  const int from = static_cast<int>(static_cast<long long>(slabs) * warp / BIAS_WARPS);
+  const int to = static_cast<int>(static_cast<long long>(slabs) * (warp + 1) / BIAS_WARPS);
+  float sum = 0.f;
+  if (col < p.cols) {
+    const float* at = p.parts + static_cast<long long>(first + g) * p.cols + col;
+#pragma unroll 8
+    for (int s = from; s < to; ++s) sum += at[static_cast<long long>(s) * p.cols];
+  }
+  partial[warp][lane] = sum;
+  __syncthreads();
+  if (warp > 0 || col >= p.cols) return;
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < BIAS_WARPS; ++i) sum += partial[i][lane];
+  const long long out = static_cast<long long>(g) * p.cols + col;
+  if (p.f32) static_cast<float*>(p.db)[out] = sum;
+  else static_cast<T*>(p.db)[out] = from_float<T>(sum);
+}
 
 template <typename T>
 cudaError_t launch_slope_type(const LinearSlopeParams& p, cudaStream_t s) {
@@ -157,6 +189,14 @@ cudaError_t launch_slope_type(const LinearSlopeParams& p, cudaStream_t s) {
   if (p.access == 16) return launch_after(linear_slope_kernel<T, 16>, grid, block, 0, s, p);
   if (p.access == 4) return launch_after(linear_slope_kernel<T, 4>, grid, block, 0, s, p);
   return launch_after(linear_slope_kernel<T, 2>, grid, block, 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_bias(const LinearBiasParams& p, int type, cudaStream_t s) {
+  const dim3 grid((p.cols + 31) / 32, p.groups), block(32 * BIAS_WARPS);
+  return type == MB_BF16 ? launch_after(linear_bias_kernel<__nv_bfloat16>, grid, block, 0, s, p)
+                         : launch_after(linear_bias_kernel<__half>, grid, block, 0, s, p);
 }
 
 cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream_t s) {

@@ -279,6 +279,30 @@ def test_long_contractions_are_cut(nss):
     _check_backward(nss, dy, x, w2, None, "none", ends)
 
 
+@pytest.mark.parametrize("ends", [None, [6001, 6001, 6100, 19990], [20000], [0, 3]])
+@pytest.mark.parametrize("act,dtype", [("relu2", "bf16"), ("gelu", "f16")])
+def test_large_backward_forms_dz_under_the_products(nss, ends, act, dtype):
+    """dz in pieces by the products' launch; the same bits each time, any of the results alone."""
+    g, t, rows, cols, out = _gen(27), TYPES[dtype], 20000, 264, 520
+    x, dy, z = _rows(rows, cols, t, g), _rows(rows, out, t, g), _rows(rows, out, t, g)
+    n = 1 if ends is None else len(ends)
+    w = (torch.randn(n, out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
+    w = w[0] if ends is None else w
+    for tensor in (x, dy, z):
+        if ends is not None:
+            tensor[ends[-1]:] = math.nan
+    first = _check_backward(nss, dy, x, w, z, act, ends)
+    dev = None if ends is None else torch.tensor(ends, dtype=torch.int32, device="cuda")
+    workspace = torch.full((1 << 27,), 0xFF, dtype=torch.uint8, device="cuda")          # NaN everywhere
+    again = nss.mb_linear_backward(dy, x, w, z, act, dev, bias=True, workspace=workspace)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    for wanted in range(1, 7):
+        which = {"input_grad": bool(wanted & 1), "weight_grad": bool(wanted & 2), "bias": bool(wanted & 4)}
+        got = _check_backward(nss, dy, x, w, z, act, ends, workspace=workspace, **which)
+        assert [r is not None for r in got] == list(which.values())
+    assert nss.mb_sync_status() == 0
+
+
 def test_nothing(nss):
     w, ends = torch.ones(2, 16, 8, device="cuda", dtype=torch.bfloat16), torch.zeros(2, device="cuda", dtype=torch.int32)
     x, dy = torch.ones(0, 8, device="cuda", dtype=torch.bfloat16), torch.ones(0, 16, device="cuda", dtype=torch.bfloat16)
