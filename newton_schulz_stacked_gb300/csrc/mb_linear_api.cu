@@ -19,7 +19,11 @@ namespace {
 constexpr int64_t MAX_ROWS = 1ll << 30, MAX_WIDTH = 1ll << 20;
 constexpr int64_t MAX_PAIRS = 76;        // what the cuts are planned for: the pairs of a GB300's 152 SMs
 constexpr int MAX_SPLITS = 16;
-constexpr int64_t AHEAD_ELEMENTS = 1ll << 22;
+// From so many elements on dz is formed under the products' MMAs, below by a launch before them.  Both, with dx, dW and db on
+// one GB300, in us: 32768x768->768 100 and 90, 8192x1024->4096 140 and 136, 32768x2048->2048 379 and 390, 65536x768->2816
+// 471 and 530, 131072x1024->2816 over 64 groups 1190 and 1278.  (The two products side by side on a share of the pairs
+// each, so that neither runs ahead of dz, took 486 and 1199.)
+constexpr int64_t AHEAD_ELEMENTS = 3ll << 24;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t parts_of(int64_t n, int64_t by) { return (n + by - 1) / by; }
@@ -201,7 +205,6 @@ BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
                d.dx ? &p.dx : nullptr);
   if (d.dweight) reserve_parts(p.dw, ws);
   if (d.dx) reserve_parts(p.dx, ws);
-  // Forming dz in a launch of its own pays where it is shorter than what its start under the products costs.
   p.ahead = p.slope && products && d.rows * static_cast<int64_t>(d.out) >= AHEAD_ELEMENTS &&
             access_of(d.dy, d.dy_stride, d.out, d.rows) == 16 && access_of(d.z, d.z_stride, d.out, d.rows) == 16;
   if (p.ahead) {

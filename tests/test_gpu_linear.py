@@ -283,7 +283,7 @@ def test_long_contractions_are_cut(nss):
 @pytest.mark.parametrize("act,dtype", [("relu2", "bf16"), ("gelu", "f16")])
 def test_large_backward_forms_dz_under_the_products(nss, ends, act, dtype):
     """dz in pieces by the products' launch; the same bits each time, any of the results alone."""
-    g, t, rows, cols, out = _gen(27), TYPES[dtype], 20000, 264, 520
+    g, t, rows, cols, out = _gen(27), TYPES[dtype], 20000, 72, 2528
     x, dy, z = _rows(rows, cols, t, g), _rows(rows, out, t, g), _rows(rows, out, t, g)
     n = 1 if ends is None else len(ends)
     w = (torch.randn(n, out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
