@@ -28,7 +28,9 @@ namespace mb {
 namespace {
 
 constexpr int BLOCK = 256;              // elements of a warp's turn, and of a scale
-constexpr int THREADS = 256, WARPS = THREADS / 32;
+// Small CTAs: 2 x 38633472 elements with 8-bit moments took 238 us in CTAs of 256 threads, 212 of 128, 186 of 64, 211 of 32 (24
+// warps per SM each: 80 registers), since a CTA's registers are free again only when its last warp is done.
+constexpr int THREADS = 64, WARPS = THREADS / 32, CTAS = 12;
 constexpr float TOP = 448.f;            // the largest e4m3 number
 constexpr float LEAST_SCALED = 0x1p-100f;   // a block whose largest magnitude is below this is held as zeros
 
@@ -117,11 +119,17 @@ __device__ __forceinline__ Raw load_eight(const void* p, long long at, int type)
 
 __device__ __forceinline__ void widen(const Raw& r, int type, float2 (&v)[4]) {
   const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  // (branches, the same for the warp: as a choice of values all three would be computed)
+  if (type == MB_BF16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = type == MB_F32    ? make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))
-           : type == MB_BF16 ? unpack2(u[i], __nv_bfloat16())
-                             : unpack2(u[i], __half());
+    for (int i = 0; i < 4; ++i) v[i] = unpack2(u[i], __nv_bfloat16());
+  } else if (type == MB_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = unpack2(u[i], __half());
+  }
 }
 
 __device__ __forceinline__ float load_one(const void* p, long long at, int type) {
@@ -144,9 +152,13 @@ __device__ __forceinline__ void store_eight(void* p, long long at, int type, con
     return;
   }
   uint32_t u[4];
+  if (type == MB_BF16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    u[i] = type == MB_BF16 ? pack2(v[i].x, v[i].y, __nv_bfloat16()) : pack2(v[i].x, v[i].y, __half());
+    for (int i = 0; i < 4; ++i) u[i] = pack2(v[i].x, v[i].y, __nv_bfloat16());
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = pack2(v[i].x, v[i].y, __half());
+  }
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
@@ -164,10 +176,15 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The largest magnitude of the warp's finite values.  The bits of non-negative floats are ordered as their values are, and
 // those of infinities and NaN are above: only a warp that has one of them looks at each.
+template <bool ROOT>
 __device__ __forceinline__ float block_size(const float2 (&v)[4], bool& all_finite) {
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) top = max(top, max(magnitude(v[j].x), magnitude(v[j].y)));
+  for (int j = 0; j < 4; ++j) {
+    // (a root has no sign but NaN's, which is above all the same)
+    if (ROOT) top = max(top, max(__float_as_uint(v[j].x), __float_as_uint(v[j].y)));
+    else top = max(top, max(magnitude(v[j].x), magnitude(v[j].y)));
+  }
   top = __reduce_max_sync(0xffffffffu, top);
   all_finite = top < 0x7F800000u;
   if (!all_finite) {
@@ -199,11 +216,11 @@ __device__ __forceinline__ float round_at_random(float q, uint32_t bits16) {
 template <bool ROOT>
 __device__ __forceinline__ float scale_block(const float2 (&v)[4], float2 (&q)[4], bool random, const uint32_t (&bits)[8]) {
   bool all_finite;
-  const float size = block_size(v, all_finite);
+  const float size = block_size<ROOT>(v, all_finite);
   const bool some = size >= LEAST_SCALED;
   const float inv = some ? __fmul_rn(__frcp_rn(size), TOP) : 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) q[j] = make_float2(__fmul_rn(v[j].x, inv), __fmul_rn(v[j].y, inv));
+  for (int j = 0; j < 4; ++j) q[j] = __fmul2_rn(v[j], both(inv));
   if (!all_finite) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -312,14 +329,13 @@ struct Loaded {
   }
   __device__ __forceinline__ void get(const AdamTensor& T, Lane& e, float z) const {
     widen(g, T.grad_type, e.g);
-    widen(p, T.param_type, e.w);
     if (T.mantissa) {
-      const uint32_t l[4] = {low.x, low.y, low.z, low.w};
+      const uint32_t l[4] = {low.x, low.y, low.z, low.w}, h[4] = {p.a.x, p.a.y, p.a.z, p.a.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        e.w[j].x = __uint_as_float(__float_as_uint(e.w[j].x) | (l[j] & 0xFFFFu));
-        e.w[j].y = __uint_as_float(__float_as_uint(e.w[j].y) | (l[j] >> 16));
-      }
+      for (int j = 0; j < 4; ++j)
+        e.w[j] = make_float2(__uint_as_float(__byte_perm(l[j], h[j], 0x5410)), __uint_as_float(__byte_perm(l[j], h[j], 0x7632)));
+    } else {
+      widen(p, T.param_type, e.w);
     }
     if constexpr (EIGHT) {
 #pragma unroll
@@ -423,12 +439,13 @@ __device__ __forceinline__ void step_single(const AdamTensor& T, const AdamScala
   }
 }
 
-// Blocks of 256 elements that a warp takes in turn, the next one's loads under this one's arithmetic.
-constexpr int TURNS = 4;
-constexpr int CHUNK = WARPS * TURNS * BLOCK;
+// Blocks of 256 elements that a warp takes in turn, the next one's loads under this one's arithmetic: 8-bit moments 186 us with
+// four or eight, 199 with two; fp32 288 with two, 292 with four, 296 with eight.
+template <bool EIGHT>
+constexpr int CHUNK = WARPS * (EIGHT ? 4 : 2) * BLOCK;
 
 template <int CAP, bool EIGHT>
-__global__ void __launch_bounds__(THREADS, 3) adamw_kernel(const __grid_constant__ AdamParams<CAP> p) {
+__global__ void __launch_bounds__(THREADS, CTAS) adamw_kernel(const __grid_constant__ AdamParams<CAP> p) {
   begin_after_previous();
   int i = 0, end = p.count;
   while (end - i > 1) {
@@ -445,8 +462,8 @@ __global__ void __launch_bounds__(THREADS, 3) adamw_kernel(const __grid_constant
     rate = each[1];
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long at = static_cast<long long>(blockIdx.x - T.first) * CHUNK + warp * BLOCK;
-  const long long stop = min(static_cast<long long>(blockIdx.x - T.first + 1) * CHUNK, T.n);
+  long long at = static_cast<long long>(blockIdx.x - T.first) * CHUNK<EIGHT> + warp * BLOCK;
+  const long long stop = min(static_cast<long long>(blockIdx.x - T.first + 1) * CHUNK<EIGHT>, T.n);
   if (T.aligned) {
     Loaded<EIGHT> next;
     if (at + BLOCK <= stop) next.load(T, at, lane);
@@ -590,7 +607,7 @@ cudaError_t launch_kind(const mb_adamw_tensor* list, int n, const AdamScalars& s
   for (int i = 0; i < n; ++i) {
     const mb_adamw_tensor& t = list[i];
     if (t.n == 0 || (t.state_type == MB_E4M3) != EIGHT) continue;
-    const long long need = (t.n + CHUNK - 1) / CHUNK;
+    const long long need = (t.n + CHUNK<EIGHT> - 1) / CHUNK<EIGHT>;
     if (p.count == CAP || blocks + need > (1ll << 30)) {
       const cudaError_t e = launch();
       if (e != cudaSuccess) return e;

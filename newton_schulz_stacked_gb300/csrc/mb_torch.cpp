@@ -707,6 +707,12 @@ struct AdamwList {
   Tensor first;
   c10::Device device = c10::Device(c10::kCPU);
 
+  // The memory of one element's tensors that have been looked at.
+  struct Range {
+    uintptr_t begin, end;
+  } range[7];
+  int ranges = 0;
+
   static std::string name(int field, Py_ssize_t at) { return std::string(NAMES[field]) + " of tensor " + std::to_string(at); }
 
   void* place(const Tensor& t, int field, Py_ssize_t at, int64_t n, ScalarType dtype, ScalarType also) {
@@ -717,7 +723,13 @@ struct AdamwList {
     if (t.device() != device) throw Refused{name(field, at) + " is on " + t.device().str() + ", expected " + device.str()};
     if (!t.is_contiguous()) throw Refused{name(field, at) + " must be contiguous"};
     if (field != 1) written.push_back(&t);
-    return t.data_ptr();
+    void* p = t.data_ptr();
+    const Range r{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + static_cast<size_t>(n) * t.element_size()};
+    for (int i = 0; i < ranges; ++i)       // (all but the gradient are written)
+      if (r.begin < range[i].end && range[i].begin < r.end)
+        throw Refused{"tensors that the call writes overlap: " + name(field, at)};
+    range[ranges++] = r;
+    return p;
   }
 
   void add(PyObject* const* f, Py_ssize_t at) {
@@ -734,7 +746,7 @@ struct AdamwList {
     d.param_type = type_of(param, NAMES[0]);
     d.grad_type = type_of(grad, NAMES[1]);
     const auto none = ScalarType::Undefined;
-    const size_t begin = written.size();
+    ranges = 0;
     d.param = place(param, 0, at, d.n, param.scalar_type(), none);
     if (grad.sizes() != param.sizes()) throw Refused{name(1, at) + " is " + str(grad) + ", its parameter " + str(param)};
     d.grad = place(grad, 1, at, d.n, grad.scalar_type(), none);
@@ -753,16 +765,6 @@ struct AdamwList {
       if (eight)
         (i == 0 ? d.avg_scale : d.sq_scale) =
             static_cast<float*>(place(*scale[i], 5 + i, at, (d.n + 255) / 256, ScalarType::Float, none));
-    }
-    // the element's own tensors one against another, the gradient among them
-    const auto apart = [](const Tensor& a, const Tensor& b) {
-      const auto p = reinterpret_cast<uintptr_t>(a.data_ptr()), q = reinterpret_cast<uintptr_t>(b.data_ptr());
-      return p + a.nbytes() <= q || q + b.nbytes() <= p;
-    };
-    for (size_t i = begin; i < written.size(); ++i) {
-      if (!apart(*written[i], grad)) throw Refused{"the gradient of tensor " + std::to_string(at) + " overlaps what the call writes"};
-      for (size_t j = begin; j < i; ++j)
-        if (!apart(*written[i], *written[j])) throw Refused{"tensors that the call writes overlap in tensor " + std::to_string(at)};
     }
     d.lr_mul = number(f[7]);
     d.wd_mul = number(f[8]);
