@@ -1,9 +1,11 @@
 """Trains one mixture-of-experts block over image patches with the Muon step.
 
 The block's matrices live in stacked banks (q/k/v/o, the experts' two products, the router's
-gate), which muon_multi_step updates in place; what stands between the products is this
-library's: layer norm, rotary positions over (height, width), expert routing with its balance
-loss, each through its gradient.  The products and the attention are torch's.
+gate), which muon_multi_step updates in place; the norms, which are in no bank, take an AdamW
+step.  The products with the banks (the experts' over their groups of tokens, with the activation;
+the output's onto its residual) and what stands between them are this library's: layer norm,
+rotary positions over (height, width), expert routing with its balance loss, each through its
+gradient.  The attention itself is torch's.
 
     python examples/moe_block_step.py [--steps 30]
 
@@ -36,19 +38,22 @@ def bank(shape, gen):
 def forward(x, banks, norms, positions, inv_freq):
     q_w, k_w, v_w, o_w = banks["attn"]["weight"]
     h = block.layer_norm(x, *norms[0])
-    q, k, v = ((h @ w.T).view(BATCH, TOKENS, HEADS, DIM) for w in (q_w, k_w, v_w))
+    q, k, v = (block.linear(h, w).view(BATCH, TOKENS, HEADS, DIM) for w in (q_w, k_w, v_w))
     q, k = block.rotary(q, k, positions, inv_freq, (DIM // 4, DIM // 4))
     scores = torch.einsum("bqhd,bkhd->bhqk", q, k).float() * DIM ** -0.5
     mix = torch.einsum("bhqk,bkhd->bqhd", scores.softmax(-1).to(x.dtype), v)
-    x = x + mix.reshape(BATCH, TOKENS, WIDTH) @ o_w.T
+    x = block.linear(mix.reshape(BATCH, TOKENS, WIDTH), o_w, residual=x)
 
     h = block.layer_norm(x, *norms[1]).view(-1, WIDTH)
-    routing = block.route(h @ banks["gate"]["weight"][0].T, TOP_K, normalize=True)
+    routing = block.route(block.linear(h, banks["gate"]["weight"][0]), TOP_K, normalize=True)
+    # the places sorted by expert (those without one last, where rows of no group are zero)
+    expert = routing.index.flatten()
+    place = expert.masked_fill(expert < 0, EXPERTS).argsort(stable=True)
+    token, ends = place // TOP_K, routing.counts.cumsum(0, dtype=torch.int32)
+    y = block.linear(h[token], banks["up"]["weight"], activation="relu2", ends=ends)
+    y = block.linear(y, banks["down"]["weight"], ends=ends)
     out = torch.zeros_like(h, dtype=torch.float32)
-    for e in range(EXPERTS):
-        token, place = torch.nonzero(routing.index == e, as_tuple=True)
-        y = torch.relu(h[token] @ banks["up"]["weight"][e].T).square() @ banks["down"]["weight"][e].T
-        out = out.index_add(0, token, y.float() * routing.gate[token, place, None])
+    out = out.index_add(0, token, y.float() * routing.gate.flatten()[place, None])
     return x + out.view_as(x).to(x.dtype), routing
 
 
@@ -65,6 +70,7 @@ def train(steps=30, lr=0.02, balance=0.01, seed=0):
     x = torch.randn((BATCH, TOKENS, WIDTH), generator=gen, device="cuda").bfloat16()
     mix = torch.randn((WIDTH, WIDTH), generator=gen, device="cuda") * WIDTH ** -0.5
     goal = x.float().view(BATCH, GRID, GRID, WIDTH).roll(1, dims=1).reshape(x.shape) @ mix
+    adam = [nss.adamw_state(p, wd_mul=0.0) for norm in norms for p in norm]
     workspace, losses = None, []
     for step in range(steps):
         y, routing = forward(x, banks, norms, positions, inv_freq)
@@ -74,11 +80,10 @@ def train(steps=30, lr=0.02, balance=0.01, seed=0):
             states = [nss.BankState(b["weight"].detach(), b["weight"].grad, b["momentum"], b["mantissa"])
                       for b in banks.values()]
             workspace = nss.muon_multi_step(states, lr, 0.01, 0.9, workspace=workspace)
-            for p in (p for norm in norms for p in norm):
-                p -= 0.1 * p.grad
+            leaves = [p for norm in norms for p in norm]
+            nss.adamw_multi_step([s._replace(grad=p.grad) for s, p in zip(adam, leaves)], 0.3 * lr, 0.01, step=step + 1)
+            for p in leaves + [b["weight"] for b in banks.values()]:
                 p.grad = None
-            for b in banks.values():
-                b["weight"].grad = None
         losses.append((task.item(), routing.loss.item()))
         if step % 5 == 0 or step == steps - 1:
             print(f"step {step:3d}  task {losses[-1][0]:.4f}  balance {losses[-1][1]:.4f}  counts {routing.counts.tolist()}")
