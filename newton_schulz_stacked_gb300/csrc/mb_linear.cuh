@@ -361,7 +361,7 @@ __device__ __forceinline__ void each_piece(uint16_t* at, long long ld, int rows,
     const int row = lane / LANES;
     uint16_t* to = at + row * ld + col;
     const int some = col < cols ? rows : 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int i = 0; i < 32 / STEP; ++i, to += STEP * ld)
       if (i * STEP + row < some) f(chunk_at(i * STEP + row, piece * ACCESS / 16) + piece * ACCESS % 16, to);
   }
