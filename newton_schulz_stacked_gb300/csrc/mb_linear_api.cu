@@ -255,10 +255,12 @@ struct Call {
   }
 };
 
-// Whether TMA can address chunks of a result or residual: rows at 16-byte boundaries.
-bool bulk_chunks(const void* p, int64_t ld, int64_t cols, int64_t rows) {
+// Whether TMA can read chunks of a matrix: rows at 16-byte boundaries.  To write them, rows have to end at such boundaries
+// too: past a row's end it leaves only whole 16-byte pieces alone.
+bool bulk_loads(const void* p, int64_t ld, int64_t cols, int64_t rows) {
   return aligned(p, 16) && (rows <= 1 || (ld % 8 == 0 && ld >= cols));
 }
+bool bulk_stores(const void* p, int64_t ld, int64_t cols, int64_t rows) { return cols % 8 == 0 && bulk_loads(p, ld, cols, rows); }
 
 void set_cut(LinearJob& j, const Cut& c, uint8_t* ws) {
   j.wide = c.wide;
@@ -378,13 +380,13 @@ int mb_linear(const mb_linear_desc* desc, void* workspace, size_t workspace_byte
   set_cut(j, plan.y, call.ws);
   MB_TRY(call.map(&j.a, plan.x, d.rows, 1, 128));
   MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, j.wide / 2));
-  j.bulk = j.splits == 1 && bulk_chunks(d.y, d.y_stride, d.out, d.rows) &&
-           (!d.z || bulk_chunks(d.z, d.z_stride, d.out, d.rows));
+  j.bulk = j.splits == 1 && bulk_stores(d.y, d.y_stride, d.out, d.rows) &&
+           (!d.z || bulk_stores(d.z, d.z_stride, d.out, d.rows));
   if (j.bulk) {
     MB_TRY(call.result_map(&j.d, d.y, d.rows, d.out, 1, d.y_stride));
     if (d.z) MB_TRY(call.result_map(&p.z_map, d.z, d.rows, d.out, 1, d.z_stride));
   }
-  p.residual_bulk = d.residual && j.splits == 1 && bulk_chunks(d.residual, d.residual_stride, d.out, d.rows);
+  p.residual_bulk = d.residual && j.splits == 1 && bulk_loads(d.residual, d.residual_stride, d.out, d.rows);
   if (p.residual_bulk) MB_TRY(call.result_map(&p.residual_map, d.residual, d.rows, d.out, 1, d.residual_stride));
   const Cut* const cuts[2] = {&plan.y, nullptr};
   MB_TRY(run_products(p, cuts, true, call));
@@ -480,7 +482,7 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     set_cut(j, plan.dw, call.ws);
     MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 64));
     MB_TRY(call.map(&j.b, plan.x, d.rows, 1, 64));
-    j.bulk = j.splits == 1 && bulk_chunks(d.dweight, d.in, d.in, 2);
+    j.bulk = j.splits == 1 && bulk_stores(d.dweight, d.in, d.in, 2);
     if (j.bulk) MB_TRY(call.result_map(&j.d, d.dweight, d.out, d.in, d.groups, d.in));
   }
   if (d.dx) {
@@ -495,7 +497,7 @@ int mb_linear_backward(const mb_linear_backward_desc* desc, void* workspace, siz
     set_cut(j, plan.dx, call.ws);
     MB_TRY(call.map(&j.a, plan.dz, d.rows, 1, 128));
     MB_TRY(call.map(&j.b, plan.w, d.out, d.groups, 64));
-    j.bulk = j.splits == 1 && bulk_chunks(d.dx, d.dx_stride, d.in, d.rows);
+    j.bulk = j.splits == 1 && bulk_stores(d.dx, d.dx_stride, d.in, d.rows);
     if (j.bulk) MB_TRY(call.result_map(&j.d, d.dx, d.rows, d.in, 1, d.dx_stride));
   }
   if (p.jobs == 2) p.extra = extra_units(plan.dw, plan.dx);

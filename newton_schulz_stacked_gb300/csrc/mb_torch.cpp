@@ -680,8 +680,10 @@ PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
     db = result(a[11], "dbias", s.param, type, device);
     d.dbias = dense(&db, "dbias", s.param, type, device);
   }
-  d.x = x.data_ptr();
-  d.x_stride = row_stride(x, "x");
+  if (d.dweight) {
+    d.x = x.data_ptr();
+    d.x_stride = row_stride(x, "x");
+  }
   d.weight = w.data_ptr();
   d.ends = s.ends;
   d.rows = s.rows;

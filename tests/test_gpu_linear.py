@@ -143,7 +143,8 @@ def test_forward_epilogues(nss, dtype, act, bias, residual):
 
 
 @pytest.mark.parametrize("cols,out,pad,shift", [(7, 5, 0, 0), (65, 67, 0, 0), (64, 64, 8, 0), (64, 64, 3, 0), (64, 64, 0, 1),
-                                                (64, 66, 2, 2), (129, 1, 0, 0), (1, 130, 0, 0), (1, 1, 0, 0)])
+                                                (64, 66, 2, 2), (129, 1, 0, 0), (1, 130, 0, 0), (1, 1, 0, 0), (61, 61, 3, 0),
+                                                (63, 191, 1, 8), (64, 333, 3, 0)])
 def test_forward_layouts(nss, cols, out, pad, shift):
     """Odd widths, rows and tensors off 16-byte boundaries, results in wider buffers (whose other columns stay)."""
     g, rows = _gen(5), 270
@@ -175,27 +176,30 @@ def test_forward_groups(nss, ends, out):
     assert not y[ends[-1]:].any() and not z[ends[-1]:].any()
 
 
-def test_many_groups(nss):
-    """The most groups that a call takes, most of them small, some empty."""
-    g, n, cols, out, t = _gen(9), 1024, 64, 64, torch.bfloat16
+@pytest.mark.parametrize("n", [140, 141, 1024])
+def test_many_groups(nss, n):
+    """Up to the most groups that a call takes, most of them small, some empty; with a residual."""
+    g, cols, out, t = _gen(n), 64, 64, torch.bfloat16
     sizes = torch.randint(0, 9, (n,), generator=g, device="cuda")
-    sizes[100], sizes[500] = 700, 0
+    sizes[100], sizes[50] = 700, 0
     ends = sizes.cumsum(0).tolist()
     x, w = _rows(ends[-1] + 5, cols, t, g), (torch.randn(n, out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
     dev = torch.tensor(ends, dtype=torch.int32, device="cuda")
-    y, _ = nss.mb_linear(x, w, ends=dev)
+    r = _rows(ends[-1] + 5, out, t, g)
+    y, _ = nss.mb_linear(x, w, residual=r, ends=dev)
     dy = _rows(ends[-1] + 5, out, t, g)
     dx, dw, _ = nss.mb_linear_backward(dy, x, w, ends=dev)
     which = torch.bucketize(torch.arange(ends[-1], device="cuda"), dev, right=True)
     X, D = x[:ends[-1]].double(), dy[:ends[-1]].double()
     W = w.double()[which]
-    _near(y[:ends[-1]], torch.einsum("ti,toi->to", X, W), _add(cols) * torch.einsum("ti,toi->to", X.abs(), W.abs()))
+    _near(y[:ends[-1]], torch.einsum("ti,toi->to", X, W) + r[:ends[-1]].double(),
+          _add(cols) * torch.einsum("ti,toi->to", X.abs(), W.abs()) + 2.0 ** -23 * r[:ends[-1]].double().abs())
     _near(dx[:ends[-1]], torch.einsum("to,toi->ti", D, W), _add(out) * torch.einsum("to,toi->ti", D.abs(), W.abs()))
     want, size = (torch.zeros(n, out, cols, dtype=torch.double, device="cuda") for _ in range(2))
     want.index_add_(0, which, D[:, :, None] * X[:, None, :])
     size.index_add_(0, which, (D[:, :, None] * X[:, None, :]).abs())
     _near(dw, want, _add(700) * size)
-    assert not y[ends[-1]:].any() and not dx[ends[-1]:].any() and not dw[500].any()
+    assert not y[ends[-1]:].any() and not dx[ends[-1]:].any() and not dw[50].any()
 
 
 @pytest.mark.parametrize("rows,cols,out", [(1, 8, 8), (7, 40, 24), (64, 64, 64), (128, 128, 256), (129, 72, 264), (1000, 200, 520),
@@ -224,7 +228,7 @@ def test_backward_activations(nss, dtype, act):
 
 
 @pytest.mark.parametrize("cols,out,pad,shift", [(7, 5, 0, 0), (65, 67, 0, 0), (64, 64, 8, 0), (64, 66, 3, 1), (129, 1, 0, 0),
-                                                (1, 130, 0, 0), (1, 1, 0, 0)])
+                                                (1, 130, 0, 0), (1, 1, 0, 0), (61, 61, 3, 0), (191, 63, 1, 8)])
 @pytest.mark.parametrize("act", ["none", "relu2"])
 def test_backward_layouts(nss, cols, out, pad, shift, act):
     g, rows, t = _gen(13), 270, torch.bfloat16
@@ -301,6 +305,53 @@ def test_large_backward_forms_dz_under_the_products(nss, ends, act, dtype):
         got = _check_backward(nss, dy, x, w, z, act, ends, workspace=workspace, **which)
         assert [r is not None for r in got] == list(which.values())
     assert nss.mb_sync_status() == 0
+
+
+def test_rows_of_any_shape(nss):
+    """More dimensions than two, rows all the same (a stride of 0), every second row."""
+    g, t = _gen(29), torch.bfloat16
+    w = _rows(96, 64, t, g, std=0.125)
+    x = _rows(24, 64, t, g)
+    flat, _ = nss.mb_linear(x, w)
+    y, _ = nss.mb_linear(x.view(2, 3, 4, 64), w)
+    assert y.shape == (2, 3, 4, 96) and torch.equal(y.view(24, 96), flat)
+    one, _ = nss.mb_linear(x[0], w)
+    assert one.shape == (96,) and torch.equal(one, flat[0])
+    y, _ = nss.mb_linear(x[:1].expand(300, 64), w)
+    assert torch.equal(y, flat[:1].expand(300, 96))
+    y, _ = nss.mb_linear(x[::2], w)
+    assert torch.equal(y, flat[::2])
+    dy = _rows(24, 96, t, g)
+    dx, dw, _ = nss.mb_linear_backward(dy, x, w)
+    dx2, dw2, _ = nss.mb_linear_backward(dy.view(4, 6, 96), x.view(4, 6, 64), w)
+    assert dx2.shape == (4, 6, 64) and torch.equal(dx2.view(24, 64), dx) and torch.equal(dw2, dw)
+    _, dw3, _ = nss.mb_linear_backward(dy[:1].expand(8, 96), x[:8], w, input_grad=False)
+    _near(dw3, dy[:1].expand(8, 96).double().T @ x[:8].double(), _add(8) * (dy[:1].expand(8, 96).double().abs().T @ x[:8].double().abs()))
+
+
+def test_host_threads(nss):
+    """Calls of two threads on streams of their own."""
+    import threading
+    g, t = _gen(31), torch.bfloat16
+    x, w, dy = _rows(512, 128, t, g), _rows(256, 128, t, g, std=0.09), _rows(512, 256, t, g)
+    want = (*nss.mb_linear(x, w, activation="gelu", keep=True), *nss.mb_linear_backward(dy, x, w))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(200):
+                got = (*nss.mb_linear(x, w, activation="gelu", keep=True), *nss.mb_linear_backward(dy, x, w))
+        stream.synchronize()
+        wrong.extend(1 for a, b in zip(got, want) if a is not b and not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
 
 
 def test_nothing(nss):
