@@ -478,9 +478,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         tmem_ld_ready(r[1]);
         Row v;
 #pragma unroll
-        for (int i = 0; i < CHUNK_COLS / 2; ++i)             // (without blocks the accumulator holds another tile)
-          v.v[i] = u.kb0 < u.kb1 ? make_float2(__uint_as_float(r[i / 16][2 * i % 32]), __uint_as_float(r[i / 16][2 * i % 32 + 1]))
-                                 : make_float2(0.f, 0.f);
+        for (int i = 0; i < CHUNK_COLS / 2; ++i)
+          v.v[i] = make_float2(__uint_as_float(r[i / 16][2 * i % 32]), __uint_as_float(r[i / 16][2 * i % 32 + 1]));
+        if (u.kb0 == u.kb1) {                                // without blocks the accumulator holds another tile
+#pragma unroll
+          for (int i = 0; i < CHUNK_COLS / 2; ++i) v.v[i] = make_float2(0.f, 0.f);
+        }
         if (J.splits > 1) {
           float4* part = part_of(J, u, u.split, rank, ew, c >> 1);
 #pragma unroll

@@ -172,11 +172,11 @@ __device__ __forceinline__ float sigmoid(float x) { return inverse_one_plus_exp2
 constexpr float GELU_SCALE = 1.5957691216057308f;    // 2 sqrt(2 / pi): tanh(u) = 2 sigmoid(2 u) - 1
 constexpr float GELU_CUBE = 0.044715f;
 
-// (comparisons are written so that NaN stays NaN)
-template <int ACT>
-__device__ __forceinline__ float activate(float z) {
-  static_assert(ACT == MB_ACT_NONE || ACT == MB_ACT_RELU, "the others come in pairs");
-  return ACT == MB_ACT_RELU && z < 0.f ? 0.f : z;
+// max(z, 0), NaN for NaN.
+__device__ __forceinline__ float relu(float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+  return r;
 }
 
 // Two at a time: what the exponentials leave to do goes two to an instruction.
@@ -191,10 +191,12 @@ __device__ __forceinline__ float2 activate(float2 z) {
     const float2 t = __fmul2_rn(z, make_float2(-1.4426950408889634f, -1.4426950408889634f));
     return __fmul2_rn(z, make_float2(inverse_one_plus_exp2(t.x), inverse_one_plus_exp2(t.y)));
   } else if constexpr (ACT == MB_ACT_RELU2) {
-    const float2 t = make_float2(activate<MB_ACT_RELU>(z.x), activate<MB_ACT_RELU>(z.y));
+    const float2 t = make_float2(relu(z.x), relu(z.y));
     return __fmul2_rn(t, t);
+  } else if constexpr (ACT == MB_ACT_RELU) {
+    return make_float2(relu(z.x), relu(z.y));
   } else {
-    return make_float2(activate<ACT>(z.x), activate<ACT>(z.y));
+    return z;
   }
 }
 
