@@ -112,6 +112,7 @@ __device__ __forceinline__ void decode_same(const LinearParams& P, const Groups&
   u.wide = same(u.wide);
   u.k_begin = same(u.k_begin);
   u.k_end = same(u.k_end);
+  u.blocks = same(u.blocks);
   u.kb0 = same(u.kb0);
   u.kb1 = same(u.kb1);
 }
@@ -130,7 +131,7 @@ enum : uint32_t {
   NOTE_B_MN = 32
 };
 
-// The first block of a unit that reaches into the next group's rows (the last block, or none: INT_MAX).
+// The block of a pass that reaches into the next group's rows (the last, or none: INT_MAX).
 __device__ __forceinline__ int past_from(const LinearParams& P, const LinearJob& J, const Unit& u) {
   const int whole = (u.k_end - u.k_begin) / LINEAR_DEEP;
   return J.over_rows && u.k_end < P.rows && whole * LINEAR_DEEP < u.k_end - u.k_begin ? whole : INT_MAX;
@@ -140,7 +141,8 @@ __device__ __forceinline__ int past_from(const LinearParams& P, const LinearJob&
 // for each block (as the compiler does behind a barrier's memory clobber) costs the producer more than the MMAs take.
 struct Feed {
   const CUtensorMap* map;
-  int x, y, x_step, y_step, batch, boxes;
+  int x, y, x_step, y_step, batch, boxes;   // x, y: of a pass's first block
+  int pass_cols;           // from one pass to the next
   uint32_t bytes;          // of both operands
   int past_from;
 };
@@ -149,12 +151,13 @@ __device__ __forceinline__ Feed feed_of(const LinearParams& P, const Unit& u, bo
   Feed f;
   f.map = for_a ? &J.a : &J.b;
   const int mn = for_a ? u.m0 + static_cast<int>(rank) * BM : u.n0 + static_cast<int>(rank) * (u.wide >> 1);
-  const int k = u.k_begin + u.kb0 * LINEAR_DEEP;
+  const int k = u.k_begin;
   const bool turned = for_a ? J.a_mn : J.b_mn;
   f.x = turned ? mn : k;
   f.y = turned ? k : mn;
   f.x_step = turned ? 0 : LINEAR_DEEP;
   f.y_step = turned ? LINEAR_DEEP : 0;
+  f.pass_cols = for_a ? J.pass_cols : 0;
   f.batch = for_a || J.over_rows ? 0 : u.group;
   f.boxes = !turned ? 1 : for_a ? 2 : u.wide >> 7;
   f.bytes = TILE_BYTES + (J.b_mn ? (u.wide >> 7) * BOX_BYTES : (J.wide >> 1) * LINEAR_DEEP * 2);
@@ -218,8 +221,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   const uint32_t stages = STAGES - (few ? 0 : 1) - (with_residual ? 1 : 0);
   uint64_t* full = reinterpret_cast<uint64_t*>(sChunk + EPI_WARPS * CHUNK_BYTES);   // [STAGES] (even) both CTAs' operands landed
   uint64_t* empty = full + STAGES;           // [STAGES] the pair's MMAs are done with the stage
-  uint64_t* past = empty + STAGES;           // [STAGES] this CTA's part of a block that reaches past its group landed
-  uint64_t* cleared = past + STAGES;         // [STAGES] (even) both CTAs have cleared it
+  uint64_t* past_bar = empty + STAGES;       // [STAGES] this CTA's part of a block that reaches past its group landed
+  uint64_t* cleared = past_bar + STAGES;         // [STAGES] (even) both CTAs have cleared it
   uint64_t* tfull = cleared + STAGES;        // [2] accumulator ready for the epilogue
   uint64_t* tempty = tfull + 2;              // [2] (even) both CTAs' epilogues drained the accumulator
   uint64_t* landed = tempty + 2;             // [EPI_WARPS] the warp's chunk of the residual
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&past[s], 1);
+      mbar_init(&past_bar[s], 1);
       mbar_init(&cleared[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   if (warp == A_WARP || warp == B_WARP) {
     // ---------------- TMA producer of one operand (both CTAs); the A operand's also announces the bytes of both
     const bool for_a = warp == A_WARP;
-    const uint32_t full_even = map_to_rank(&full[0], 0), past_own = map_to_rank(&past[0], rank);
+    const uint32_t full_even = map_to_rank(&full[0], 0), past_own = map_to_rank(&past_bar[0], rank);
     uint8_t* const ring = for_a ? sA : sB;
     uint32_t st = 0, ph = 0, it = 0;
     bool ok = true;
@@ -300,7 +303,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         ok = seen.rows(P.ahead, row, min(row + BM, u.m_end), lane, abort_flag);
         if (!ok) break;
       }
-      int x = f.x, y = f.y;
+      int at_block = kb0 < u.blocks ? kb0 : kb0 - u.blocks;                // of its pass
+      int x = f.x + at_block * f.x_step + (kb0 < u.blocks ? 0 : f.pass_cols), y = f.y + at_block * f.y_step;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         if (it >= stages) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag));
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
           ok = seen.rows(P.ahead, y, min(y + LINEAR_DEEP, u.k_end), lane, abort_flag);
           if (!ok) break;
         }
-        const bool nothing = (flags & NOTE_NOTHING) != 0, past_end = !nothing && kb >= f.past_from;
+        const bool nothing = (flags & NOTE_NOTHING) != 0, past_end = !nothing && at_block >= f.past_from;
         const uint32_t bar = (past_end ? past_own : full_even) + 8u * st;
         uint8_t* to = ring + st * TILE_BYTES;
         if (elect_lane()) {
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
               if (past_end || nothing) mbar_arrive(&full[st]);
               else mbar_expect_tx(&full[st], 2u * f.bytes);
             }
-            if (past_end) mbar_expect_tx(&past[st], f.bytes);
+            if (past_end) mbar_expect_tx(&past_bar[st], f.bytes);
           }
           if (!nothing) {
             tma_load_3d_pair(to, f.map, bar, x, y, f.batch);
@@ -331,6 +335,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         __syncwarp();
         x += f.x_step;
         y += f.y_step;
+        if (++at_block == u.blocks) {              // the next pass
+          at_block = 0;
+          x = f.x + f.pass_cols;
+          y = f.y;
+        }
         if (++st == stages) {
           st = 0;
           ph ^= 1u;
@@ -405,15 +414,17 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       decode_unit(P, G, first_units, deal(i), u);
       const LinearJob& J = P.job[u.job];
       const int blocks = max(u.kb1 - u.kb0, 1);                  // (without blocks: a stage for the note)
-      if (u.kb1 > u.kb0 && u.kb1 - 1 >= past_from(P, J, u)) {      // only a group's last block does
-        const int st = (it + blocks - 1) % stages;
-        if (!mbar_wait_or_abort(&past[st], (past_phase >> st) & 1u, abort_flag)) {
-          fail();
-          break;
-        }
+      const int past = past_from(P, J, u);
+      bool ok = true;
+      for (int pass = 0; pass < J.passes && past < u.blocks && ok; ++pass) {
+        const int kb = pass * u.blocks + past;
+        if (kb < u.kb0 || kb >= u.kb1) continue;
+        const int st = (it + kb - u.kb0) % stages;
+        ok = mbar_wait_or_abort(&past_bar[st], (past_phase >> st) & 1u, abort_flag);
+        if (!ok) break;
         past_phase ^= 1u << st;
         // a box's rows of 128 bytes are its rows of the contraction (the swizzle stays within a row)
-        const int keep = u.k_end - u.k_begin - (u.kb1 - 1) * LINEAR_DEEP;
+        const int keep = u.k_end - u.k_begin - past * LINEAR_DEEP;
         for (int box = 0; box < 2 + (u.wide >> 7); ++box) {
           uint8_t* base = box < 2 ? sA + st * TILE_BYTES + box * BOX_BYTES : sB + st * TILE_BYTES + (box - 2) * BOX_BYTES;
           for (int j = keep * 8 + lane; j < LINEAR_DEEP * 8; j += 32) reinterpret_cast<uint4*>(base)[j] = make_uint4(0, 0, 0, 0);
@@ -421,6 +432,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(cleared_even + 8u * static_cast<uint32_t>(st));
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        fail();
+        break;
       }
       it += blocks;
     }

@@ -25,6 +25,7 @@ struct LinearJob {
   int N, K;                // D's columns; the contraction (not over_rows)
   int wide;                // 128 or 256
   int m_tiles, n_tiles;    // m_tiles: over_rows only
+  int passes, pass_cols;   // 2: the A operand comes as two halves, the second pass_cols columns on, and the contraction runs twice
   int splits;              // parts of the contraction
   int access;              // bytes that D's rows allow to be stored at a time: 16, 4 or 2
   void* out;
@@ -41,6 +42,7 @@ struct LinearSlopeParams {
   long long z_ld;
   void* dz;                // [rows, dz_ld], 16-byte aligned rows
   long long dz_ld;
+  int low;                 // 0, or the columns to dz's low halves: what its rounding left; zeros up to there past the last, rows of 2 low
   int act, rows, cols, groups;
   const int* ends;
   float* parts;            // or null

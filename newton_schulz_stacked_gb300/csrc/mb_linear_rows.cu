@@ -71,16 +71,30 @@ __device__ __forceinline__ void slope_rows(const LinearSlopeParams& p, int begin
   const T* dy = static_cast<const T*>(p.dy);
   const T* z = static_cast<const T*>(p.z);
   T* dz = static_cast<T*>(p.dz);
-  if (c0 + lane_col<ACCESS>(lane, 0) >= p.cols) return;
+  const int first = c0 + lane_col<ACCESS>(lane, 0);
+  const int most = p.low ? p.low : p.cols;       // columns that are written: with low halves the gap before them too
+  if (first >= (ACT == MB_ACT_NONE ? p.cols : most)) return;
 #pragma unroll 2
   for (int row = begin + warp; row < end; row += SLOPE_WARPS) {
     float v[8], x[8];
-    load_lane<T, ACCESS>(dy + row * p.dy_ld, c0, p.cols, lane, v);
+    const bool some = ACCESS != 16 || first < p.cols;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x[j] = 0.f;
+    if (some) load_lane<T, ACCESS>(dy + row * p.dy_ld, c0, p.cols, lane, v);
     if (ACT != MB_ACT_NONE) {
-      load_lane<T, ACCESS>(z + row * p.z_ld, c0, p.cols, lane, x);
+      if (some) load_lane<T, ACCESS>(z + row * p.z_ld, c0, p.cols, lane, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= slope<ACT>(x[j]);
-      store_lane<T, ACCESS>(dz + row * p.dz_ld, c0, p.cols, lane, v);
+      T* to = dz + row * p.dz_ld;
+      store_lane<T, ACCESS>(to, c0, most, lane, v);
+      if (p.low) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float left = v[j] - to_float(from_float<T>(v[j]));
+          x[j] = isfinite(left) ? left : 0.f;      // (an infinite half: all of it)
+        }
+        store_lane<T, ACCESS>(to + p.low, c0, most, lane, x);
+      }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += v[j];

@@ -508,3 +508,49 @@ def test_refusals(nss):
     refused("workspace", dy, x, w, torch.ones_like(dy), "relu", workspace=torch.empty(8, device="cuda", dtype=torch.uint8),
             f=nss.mb_linear_backward)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,cols,out,pad", [(1, 1, 1, 0), (1, 8, 8, 0), (1, 2048, 4096, 0), (2, 1000, 2000, 0), (26, 512, 77, 3),
+                                               (31, 65, 1000, 0), (200, 72, 10, 0), (256, 8, 300, 8), (2, 2816, 768, 0)])
+@pytest.mark.parametrize("groups", [0, 4])
+def test_few_rows_keep_dz_in_two_halves(nss, dtype, rows, cols, out, pad, groups):
+    """With up to 2048 elements of x or y dz is not rounded to 16 bits: what its halves leave is u^2 of it (fp16: half of the least
+    subnormal at least), over twice the terms."""
+    g, t = _gen(rows + cols), TYPES[dtype]
+    shape = (groups, out, cols) if groups else (out, cols)
+    ends = [rows // 3, rows // 3, rows - rows // 5, rows - rows // 8] if groups else None
+    bounds, u = _bounds(ends, rows), HALF_STEP[t] ** 2
+    x, dy, z = _rows(rows, cols, t, g, pad), _rows(rows, out, t, g, pad), _rows(rows, out, t, g, pad)
+    w = (torch.randn(shape, generator=g, device="cuda") * cols ** -0.5).to(t)
+    if groups:
+        for tensor in (x, dy, z):
+            tensor[ends[-1]:] = math.nan
+    dev = None if ends is None else torch.tensor(ends, dtype=torch.int32, device="cuda")
+    workspace = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")          # NaN everywhere
+    tiny = 2.0 ** -25 if dtype == "f16" else 0
+    for act in ACTS[1:]:
+        dx, dw, db = nss.mb_linear_backward(dy, x, w, z, act, dev, bias=True, workspace=workspace)
+        _check_backward(nss, dy, x, w, z, act, ends)
+        for i, (a, e) in enumerate(bounds):
+            W, X, D = (w[i] if groups else w).double(), x[a:e].double(), dy[a:e].double() * _slope(z[a:e].double(), act)
+            off = (u + 2.0 ** -18) * D.abs() + tiny
+            _near(dx[a:e], D @ W, off @ W.abs() + _add(2 * out) * (D.abs() @ W.abs()))
+            _near(dw[i] if groups else dw, D.T @ X, off.T @ X.abs() + _add(2 * max(e - a, 1)) * (D.abs().T @ X.abs()))
+        assert not dx[bounds[-1][1]:].any()
+        for which in ({"input_grad": False}, {"weight_grad": False}):
+            one = nss.mb_linear_backward(dy, x, w, z, act, dev, workspace=workspace, **which)
+            for got, want in ((one[0], dx), (one[1], dw)):
+                assert got is None or torch.allclose(got.float(), want.float(), rtol=4 * HALF_STEP[t], atol=1e-3)
+    assert nss.mb_sync_status() == 0
+
+
+def test_dz_past_the_type_is_infinite(nss):
+    """fp16: a dz past 65504 makes its sums infinite, not NaN, with few rows (two halves) as with many."""
+    for rows in (2, 3000):
+        x, w = torch.ones(rows, 64, device="cuda", dtype=torch.float16), torch.ones(64, 64, device="cuda", dtype=torch.float16)
+        dy, z = torch.ones_like(x), torch.ones_like(x)
+        dy[1, 3] = z[1, 3] = 30000.0
+        dx, dw, _ = nss.mb_linear_backward(dy, x, w, z, "relu2")
+        assert (dx[1] == math.inf).all() and dx[0].eq(128).all()
+        assert (dw[3] == math.inf).all() and dw[:3].isfinite().all() and dw[4:].isfinite().all()
