@@ -190,18 +190,21 @@ __device__ void side_work(const LinearParams& P, const Groups& G, long long me, 
     }
   }
   if (P.db) {
-    // dbias of 32 columns of one group: its sums over the slabs that hold its rows, in order
-    const int across = (P.db_cols + 31) / 32;
+    // dbias of 8 columns of one group: its sums over the slabs that hold its rows, every fourth to a lane of each column (with 32
+    // columns to a warp the chain of loads took 8 us for 98 slabs)
+    const int across = (P.db_cols + 7) / 8;
     for (long long i = me; i < static_cast<long long>(G.n) * across; i += all) {
-      const int g = static_cast<int>(i / across), col = static_cast<int>(i % across) * 32 + lane;
-      if (col >= P.db_cols) continue;
+      const int g = static_cast<int>(i / across), col = static_cast<int>(i % across) * 8 + (lane & 7);
       float sum = 0.f;
       const int begin = G.row[g], end = G.row[g + 1];
-      if (end > begin) {
+      if (end > begin && col < P.db_cols) {
         const int last = (end - 1) / P.slab;
 #pragma unroll 8
-        for (int s = begin / P.slab; s <= last; ++s) sum += P.db_parts[static_cast<long long>(s + g) * P.db_cols + col];
+        for (int s = begin / P.slab + (lane >> 3); s <= last; s += 4) sum += P.db_parts[static_cast<long long>(s + g) * P.db_cols + col];
       }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (lane >= 8 || col >= P.db_cols) continue;
       const long long at = static_cast<long long>(g) * P.db_cols + col;
       if (P.db_f32) static_cast<float*>(P.db)[at] = sum;
       else static_cast<T*>(P.db)[at] = from_float<T>(sum);

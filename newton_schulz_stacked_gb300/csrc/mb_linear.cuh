@@ -129,6 +129,7 @@ struct Deal {
     pairs = pairs_;
     first = first_;
     units = units_;
+    if (units <= pairs) first = units;             // one each
     firsts = pair < first ? (first - pair + pairs - 1) / pairs : 0;
     skipped = first % pairs;
     const int others = pairs - skipped;

@@ -103,6 +103,7 @@ struct Workspace {
 struct Cut {
   int wide, splits;
   int64_t tiles, blocks;   // tiles (the most that there can be), blocks of the contraction (on average)
+  int64_t n;               // columns
   size_t at;               // of the parts' sums
 };
 
@@ -113,8 +114,10 @@ double unit_time(const Cut& c) { return static_cast<double>(c.blocks) / c.splits
 // The units of the second product that a pair takes for one of the first that others have more than it.
 int extra_units(const Cut& first, const Cut& second) { return static_cast<int>(unit_time(first) / unit_time(second) + 0.5); }
 
-// The time of the busiest pair, the last epilogue, and what the parts of a contraction cost: the join's launch, and 256 KB
-// of sums for each unit there and back.
+// What the parts of a contraction cost: the join's launch, and 256 KB of sums for each unit there and back.
+double join_time(const Cut& c) { return c.splits > 1 ? 10 + 0.27 * c.wide / 256 * static_cast<double>(c.tiles * c.splits) : 0; }
+
+// The time of the busiest pair and the last epilogue.
 double busiest(const Cut& first, const Cut* second) {
   const double a = unit_time(first), b = second ? unit_time(*second) : 0;
   const int64_t n = first.tiles * first.splits, rounds = n / MAX_PAIRS, over = n % MAX_PAIRS;
@@ -128,7 +131,7 @@ double busiest(const Cut& first, const Cut* second) {
     const double with = (rounds + (over > 0)) * a + more * b, without = rounds * a + (extra + more) * b;
     t = with > without ? with : without;
   }
-  return t + 8 + (first.splits > 1 ? 10 + 0.27 * first.wide / 256 * static_cast<double>(n) : 0);
+  return t + 8 + join_time(first);
 }
 
 // The cut of tiles and contraction that takes the busiest pair least time, wide and whole where others gain little.
@@ -137,7 +140,7 @@ Cut cut(int64_t m_tiles, int64_t n, int64_t blocks, const Cut* second) {
   double least = 0;
   for (int wide = n <= 128 ? 128 : 256; wide >= 128; wide /= 2)
     for (int s = 1; s <= MAX_SPLITS && (s == 1 || blocks / s >= 8); ++s) {
-      const Cut c{wide, s, m_tiles * parts_of(n, wide), blocks, 0};
+      const Cut c{wide, s, m_tiles * parts_of(n, wide), blocks, n, 0};
       const double t = busiest(c, second);
       if (best.wide == 0 || t < 0.97 * least) {
         best = c;
@@ -145,6 +148,32 @@ Cut cut(int64_t m_tiles, int64_t n, int64_t blocks, const Cut* second) {
       }
     }
   return best;
+}
+
+// Two products of few tiles, with a pair for every unit: both in parts where that is shorter.
+void cut_few(Cut& first, Cut& second) {
+  Cut a = first, b = second;
+  double least = 0;
+  bool any = false;
+  for (int ways = 0; ways < 4; ++ways)
+    for (int i = 1; i <= MAX_SPLITS && (i == 1 || first.blocks / i >= 4); ++i)
+      for (int j = 1; j <= MAX_SPLITS && (j == 1 || second.blocks / j >= 4); ++j) {
+        const int a_wide = ways & 1 ? 128 : 256, b_wide = ways & 2 ? 128 : 256;
+        const Cut f{a_wide, i, first.tiles / parts_of(first.n, first.wide) * parts_of(first.n, a_wide), first.blocks, first.n, 0};
+        const Cut s{b_wide, j, second.tiles / parts_of(second.n, second.wide) * parts_of(second.n, b_wide), second.blocks, second.n, 0};
+        if (f.tiles * i + s.tiles * j > MAX_PAIRS) continue;
+        const double t = std::max(unit_time(f), unit_time(s)) + 8 + join_time(f) + join_time(s);
+        if (!any || t < 0.97 * least) {
+          any = true;
+          least = t;
+          a = f;
+          b = s;
+        }
+      }
+  if (any && least < busiest(first, &second)) {
+    first = a;
+    second = b;
+  }
 }
 
 void reserve_parts(Cut& c, Workspace& ws) {
@@ -212,6 +241,7 @@ BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
   if (d.dweight)
     p.dw = cut(d.groups * parts_of(d.out, LINEAR_TILE), d.in, parts_of(parts_of(d.rows, d.groups), LINEAR_DEEP) * (p.low ? 2 : 1),
                d.dx ? &p.dx : nullptr);
+  if (d.dx && d.dweight) cut_few(p.dw, p.dx);
   if (d.dweight) reserve_parts(p.dw, ws);
   if (d.dx) reserve_parts(p.dx, ws);
   p.ahead = p.slope && products && d.rows * static_cast<int64_t>(d.out) >= AHEAD_ELEMENTS &&
@@ -225,10 +255,10 @@ BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
     p.end = ws.end;
     return p;
   }
-  // slabs of rows: about four CTAs for an SM, 32 to 1024 rows
+  // slabs of rows: about four CTAs for an SM, 8 (a row for each warp) to 1024 rows
   const int64_t columns = parts_of(d.out, 256);
-  int64_t slab = up(parts_of(d.rows * columns, 608), 32);
-  slab = slab < 32 ? 32 : slab > 1024 ? 1024 : slab;
+  int64_t slab = up(parts_of(d.rows * columns, 608), 8);
+  slab = slab < 8 ? 8 : slab > 1024 ? 1024 : slab;
   if (parts_of(d.rows, slab) > 65535) slab = up(parts_of(d.rows, 65535), 32);
   p.slab = static_cast<int>(slab);
   p.slabs = parts_of(d.rows, slab);

@@ -145,19 +145,31 @@ __global__ void __launch_bounds__(32 * SLOPE_WARPS) linear_slope_kernel(const __
   }
 }
 
+constexpr int PACK_COLS = 256;
 __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ LinearPackParams p) {
   begin_after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // a warp per row: pairs of elements, or single ones, read along the row
+  // a warp for 256 columns of a row: pairs of elements, or single ones, read along the row, all before the first is stored
+  const int c0 = blockIdx.y * PACK_COLS, cols = min(p.cols - c0, PACK_COLS);
   for (long long row = static_cast<long long>(blockIdx.x) * 8 + warp; row < p.rows; row += static_cast<long long>(gridDim.x) * 8) {
-    const uint16_t* from = p.src + row * p.src_ld;
-    uint16_t* to = p.dst + row * p.dst_ld;
+    const uint16_t* from = p.src + row * p.src_ld + c0;
+    uint16_t* to = p.dst + row * p.dst_ld + c0;
     if (p.pairs) {
-#pragma unroll 4
-      for (int c = lane; c < p.cols / 2; c += 32) reinterpret_cast<uint32_t*>(to)[c] = reinterpret_cast<const uint32_t*>(from)[c];
+      uint32_t v[PACK_COLS / 64];
+#pragma unroll
+      for (int i = 0; i < PACK_COLS / 64; ++i)
+        if (lane + 32 * i < cols / 2) v[i] = reinterpret_cast<const uint32_t*>(from)[lane + 32 * i];
+#pragma unroll
+      for (int i = 0; i < PACK_COLS / 64; ++i)
+        if (lane + 32 * i < cols / 2) reinterpret_cast<uint32_t*>(to)[lane + 32 * i] = v[i];
     } else {
-#pragma unroll 4
-      for (int c = lane; c < p.cols; c += 32) to[c] = from[c];
+      uint16_t v[PACK_COLS / 32];
+#pragma unroll
+      for (int i = 0; i < PACK_COLS / 32; ++i)
+        if (lane + 32 * i < cols) v[i] = from[lane + 32 * i];
+#pragma unroll
+      for (int i = 0; i < PACK_COLS / 32; ++i)
+        if (lane + 32 * i < cols) to[lane + 32 * i] = v[i];
     }
   }
 }
@@ -218,8 +230,9 @@ cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream
 }
 
 cudaError_t launch_linear_pack(const LinearPackParams& p, int sms, cudaStream_t s) {
-  const long long need = (p.rows + 7) / 8, most = 8ll * sms;
-  return launch_after(linear_pack_kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(256), 0, s, p);
+  const int pieces = (p.cols + PACK_COLS - 1) / PACK_COLS;
+  const long long need = (p.rows + 7) / 8, most = pieces < 8 ? 8ll * sms / pieces : sms;
+  return launch_after(linear_pack_kernel, dim3(static_cast<unsigned>(need < most ? need : most), pieces), dim3(256), 0, s, p);
 }
 
 }  // namespace mb
