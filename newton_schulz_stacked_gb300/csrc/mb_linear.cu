@@ -533,17 +533,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
   }
 }
 
-// The parts of a job's contraction added in order, then the epilogue: a CTA for one chunk of every epilogue warp of half a
-// pair's tile, so that a few tiles' parts are read by many CTAs.
+// The parts of a job's contraction added, then the epilogue: a CTA for one chunk of one epilogue warp, whose warps take every
+// fourth part each, and the first of them the others' sums in order.  The parts' loads are a chain of waits on the L2 that the
+// ways shorten (16 parts by one warp: 9 us).
+constexpr int JOIN_WAYS = 4;
 template <bool FORWARD, typename T>
-__global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __grid_constant__ LinearParams P, int job) {
+__global__ void __launch_bounds__(32 * JOIN_WAYS) linear_join_kernel(const __grid_constant__ LinearParams P, int job) {
   __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
-  __shared__ alignas(16) uint8_t chunk[EPI_WARPS * CHUNK_BYTES];
+  __shared__ alignas(16) uint8_t chunk[CHUNK_BYTES];
+  __shared__ float4 sums[JOIN_WAYS - 1][CHUNK_COLS / 4 * 32];
   begin_after_previous();
   const LinearJob& J = P.job[job];
   Groups G{groups, groups + LINEAR_MAX_GROUPS + 1, P.groups};
-  const int ew = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (ew == 0) fill_groups(G, P.ends, P.rows, lane);
+  const int way = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (way == 0) fill_groups(G, P.ends, P.rows, lane);
   __syncthreads();
   const int tile = blockIdx.x >> 1;
   const uint32_t rank = blockIdx.x & 1;
@@ -552,31 +555,40 @@ __global__ void __launch_bounds__(32 * EPI_WARPS) linear_join_kernel(const __gri
   u.job = job;
   u.split = 0;
   decode_tile(J, G, tile, u);
-  const int quad = (ew + 2) & 3, half = ew >> 2;         // as warps 2..9 of the kernel above
+  const int ew = blockIdx.y & (EPI_WARPS - 1), quad = (ew + 2) & 3, half = ew >> 2;         // as warps 2..9 of the kernel above
   WarpPlace w;
   w.lane = lane;
-  w.buf = chunk + ew * CHUNK_BYTES;
+  w.buf = chunk;
   w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
   w.rows = min(32, u.m_end - w.row0);
   if (w.rows <= 0) return;
-  const int c = half + 2 * blockIdx.y;
-  if (c >= u.wide / CHUNK_COLS) return;
-  const float2 bias = FORWARD ? bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * c, lane) : make_float2(0.f, 0.f);
+  const int c = half + 2 * (blockIdx.y / EPI_WARPS), col0 = u.n0 + CHUNK_COLS * c;
+  if (c >= u.wide / CHUNK_COLS || col0 >= J.N) return;
+  const float2 bias = FORWARD ? bias_of<T>(P, J, u.group, col0, lane) : make_float2(0.f, 0.f);
   ResidualFeed none{nullptr, nullptr, 0, 0};
   Row v;
-#pragma unroll
-  for (int i = 0; i < CHUNK_COLS / 2; ++i) v.v[i] = make_float2(0.f, 0.f);
-#pragma unroll 2
-  for (int s = 0; s < J.splits; ++s) {
-    const float4* part = part_of(J, u, s, rank, ew, c >> 1);
+  const auto add = [&](const float4* part) {
 #pragma unroll
     for (int i = 0; i < CHUNK_COLS / 4; ++i) {
       const float4 q = part[32 * i + lane];
       v.v[2 * i] = __fadd2_rn(v.v[2 * i], make_float2(q.x, q.y));
       v.v[2 * i + 1] = __fadd2_rn(v.v[2 * i + 1], make_float2(q.z, q.w));
     }
+  };
+#pragma unroll
+  for (int i = 0; i < CHUNK_COLS / 2; ++i) v.v[i] = make_float2(0.f, 0.f);
+#pragma unroll 2
+  for (int s = way; s < J.splits; s += JOIN_WAYS) add(part_of(J, u, s, rank, ew, c >> 1));
+  if (way > 0) {
+#pragma unroll
+    for (int i = 0; i < CHUNK_COLS / 4; ++i)
+      sums[way - 1][32 * i + lane] = make_float4(v.v[2 * i].x, v.v[2 * i].y, v.v[2 * i + 1].x, v.v[2 * i + 1].y);
   }
-  finish_chunk<FORWARD, T, false>(P, J, u, w, v, u.n0 + CHUNK_COLS * c, bias, none, nullptr);
+  __syncthreads();
+  if (way > 0) return;
+#pragma unroll 1
+  for (int i = 0; i < JOIN_WAYS - 1; ++i) add(sums[i]);
+  finish_chunk<FORWARD, T, false>(P, J, u, w, v, col0, bias, none, nullptr);
 }
 
 // Per-device set-up (the shared-memory limit, the number of pairs that can be resident) is done by the first call on each
@@ -615,8 +627,8 @@ cudaError_t launch_form(const LinearParams& p, int pairs_wanted, cudaStream_t s)
 template <bool FORWARD, typename T>
 cudaError_t launch_join_form(const LinearParams& p, int job, long long tiles, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), p.job[job].wide / 128);
-  cfg.blockDim = dim3(32 * EPI_WARPS);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), EPI_WARPS * (p.job[job].wide / 128));
+  cfg.blockDim = dim3(32 * JOIN_WAYS);
   cfg.stream = s;
   cudaLaunchAttribute a[1]{};
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
