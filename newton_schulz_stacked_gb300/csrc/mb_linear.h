@@ -107,6 +107,27 @@ struct LinearPackParams {
   int pairs;               // rows and columns come in 4-byte pairs
 };
 
+// The product over at most LINEAR_FEW_ROWS rows.
+constexpr int LINEAR_FEW_ROWS = 8;
+struct LinearFewParams {
+  const void* x;
+  long long x_ld;
+  const void* w;           // [groups, out, in]
+  const void* bias;        // [groups, out] or null
+  int bias_f32, act;
+  const void* residual;
+  long long residual_ld;
+  void* z;
+  long long z_ld;
+  void* y;
+  long long y_ld;
+  int rows, in, out, groups;
+  const int* ends;
+  int access;              // bytes that the rows of x and w allow to be read at a time
+  int* status;
+};
+cudaError_t launch_linear_few(const LinearFewParams& p, int type, cudaStream_t s);
+
 cudaError_t launch_linear(const LinearParams& p, int type, bool forward, int pairs_wanted, cudaStream_t s);
 cudaError_t launch_linear_join(const LinearParams& p, int job, int type, bool forward, long long tiles, cudaStream_t s);
 cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream_t s);

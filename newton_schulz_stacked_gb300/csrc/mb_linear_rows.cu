@@ -1,5 +1,5 @@
 // The passes over rows around the products of mb_linear: dz = dy act'(z) with its sums over slabs of rows, and rows copied to
-// 16-byte boundaries for operands that TMA cannot address.
+// 16-byte boundaries for operands that TMA cannot address; and the product over a few rows, which is a pass over W's.
 #include <type_traits>
 
 #include "mb_block.h"
@@ -208,6 +208,113 @@ __global__ void __launch_bounds__(32 * BIAS_WARPS) linear_bias_kernel(const __gr
   else static_cast<T*>(p.db)[out] = from_float<T>(sum);
 }
 
+// y of up to 8 rows: bound by reading W, which the tensor cores' tiles of 256 rows would only wait for.  A CTA takes four columns
+// of y (rows of W) of one group, its warps every eighth 256 elements of them, each lane eight for all rows of x in fp32;
+// the lanes' sums, then the warps', are added in order.  1x4096->4096 7.9 us, 1x4096->16384 23.5 (5.7 TB/s); with more rows the
+// conversions and sums bound it: 4x4096->4096 13.8, 8x4096->4096 21.0, where the tiles take 20.1.
+constexpr int FEW_WARPS = 8, FEW_COLS = 4;
+
+template <typename T, int ACCESS, int ROWS>
+__global__ void __launch_bounds__(32 * FEW_WARPS, ROWS == 1 ? 4 : 2) linear_few_kernel(const __grid_constant__ LinearFewParams p) {
+  __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
+  __shared__ float partial[FEW_WARPS][ROWS * FEW_COLS];
+  begin_after_previous();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col0 = blockIdx.x * FEW_COLS;
+  int g = 0, begin = 0, end = p.rows, last = p.rows;
+  if (p.ends) {
+    Groups G{groups, groups + LINEAR_MAX_GROUPS + 1, p.groups};
+    if (warp == 0 && fill_groups(G, p.ends, p.rows, lane) && blockIdx.x == 0 && blockIdx.y == 0 && lane == 0)
+      latch_status(p.status, DEV_BAD_SCALAR);
+    __syncthreads();
+    // the blockIdx.y'th group that has rows
+    last = G.row[G.n];
+    begin = end = last;
+    int before = static_cast<int>(blockIdx.y);
+    for (int g0 = 0; g0 < G.n; g0 += 32) {
+      const int at = g0 + lane;
+      const bool some = at < G.n && G.row[at + 1] > G.row[at];
+      const unsigned all = __ballot_sync(0xffffffffu, some);
+      const bool mine = some && __popc(all & ((1u << lane) - 1)) == before;
+      const unsigned found = __ballot_sync(0xffffffffu, mine);
+      if (found) {
+        g = g0 + __ffs(found) - 1;
+        begin = G.row[g];
+        end = G.row[g + 1];
+        break;
+      }
+      before -= __popc(all);
+    }
+  }
+  const T* x = static_cast<const T*>(p.x);
+  T* z = static_cast<T*>(p.z);
+  T* y = static_cast<T*>(p.y);
+  if (blockIdx.y == 0 && static_cast<int>(threadIdx.x) < (p.rows - last) * FEW_COLS) {
+    // zeros in the rows of no group
+    const long long row = last + threadIdx.x / FEW_COLS;
+    const int col = col0 + threadIdx.x % FEW_COLS;
+    if (col < p.out) {
+      y[row * p.y_ld + col] = from_float<T>(0.f);
+      if (z) z[row * p.z_ld + col] = from_float<T>(0.f);
+    }
+  }
+  const int n = end - begin;
+  if (n == 0) return;
+  const T* w = static_cast<const T*>(p.w) + (static_cast<long long>(g) * p.out + col0) * p.in;
+  float2 sum[FEW_COLS][ROWS];                    // of even and odd elements
+#pragma unroll
+  for (int c = 0; c < FEW_COLS; ++c)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) sum[c][r] = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int k = 256 * warp; k < p.in; k += 256 * FEW_WARPS) {
+    if (ACCESS == 16 && k + 8 * lane >= p.in) continue;
+    float a[FEW_COLS][8], b[8];
+#pragma unroll
+    for (int c = 0; c < FEW_COLS; ++c)           // (past the last column: that one again)
+      load_lane<T, ACCESS>(w + static_cast<long long>(min(c, p.out - 1 - col0)) * p.in, k, p.in, lane, a[c]);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {             // (and past the last row)
+      load_lane<T, ACCESS>(x + (begin + min(r, n - 1)) * p.x_ld, k, p.in, lane, b);
+#pragma unroll
+      for (int c = 0; c < FEW_COLS; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          sum[c][r] = __ffma2_rn(make_float2(a[c][j], a[c][j + 1]), make_float2(b[j], b[j + 1]), sum[c][r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int c = 0; c < FEW_COLS; ++c) {
+      float s = sum[c][r].x + sum[c][r].y;
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+      if (lane == 0) partial[warp][r * FEW_COLS + c] = s;
+    }
+  __syncthreads();
+  const int r = threadIdx.x / FEW_COLS, col = col0 + threadIdx.x % FEW_COLS;
+  if (r >= n || col >= p.out) return;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < FEW_WARPS; ++i) v += partial[i][threadIdx.x];
+  const long long row = begin + r, at = static_cast<long long>(g) * p.out + col;
+  if (p.bias) v += p.bias_f32 ? static_cast<const float*>(p.bias)[at] : to_float(static_cast<const T*>(p.bias)[at]);
+  if (z) z[row * p.z_ld + col] = from_float<T>(v);
+  with_activation(p.act, [&](auto act) { v = activate<decltype(act)::value>(make_float2(v, 0.f)).x; });
+  if (p.residual) v += to_float(static_cast<const T*>(p.residual)[row * p.residual_ld + col]);
+  y[row * p.y_ld + col] = from_float<T>(v);
+}
+
+template <typename T>
+cudaError_t launch_few_type(const LinearFewParams& p, cudaStream_t s) {
+  const dim3 grid((p.out + FEW_COLS - 1) / FEW_COLS, p.groups < p.rows ? p.groups : p.rows), block(32 * FEW_WARPS);
+  if (p.access != 16 && p.rows == 1) return launch_after(linear_few_kernel<T, 2, 1>, grid, block, 0, s, p);
+  if (p.access != 16) return launch_after(linear_few_kernel<T, 2, LINEAR_FEW_ROWS>, grid, block, 0, s, p);
+  if (p.rows == 1) return launch_after(linear_few_kernel<T, 16, 1>, grid, block, 0, s, p);
+  if (p.rows <= 4) return launch_after(linear_few_kernel<T, 16, 4>, grid, block, 0, s, p);
+  return launch_after(linear_few_kernel<T, 16, LINEAR_FEW_ROWS>, grid, block, 0, s, p);
+}
+
 template <typename T>
 cudaError_t launch_slope_type(const LinearSlopeParams& p, cudaStream_t s) {
   const dim3 grid((p.cols + SLOPE_COLS - 1) / SLOPE_COLS, (p.rows + p.slab - 1) / p.slab);
@@ -227,6 +334,10 @@ cudaError_t launch_linear_bias(const LinearBiasParams& p, int type, cudaStream_t
 
 cudaError_t launch_linear_slope(const LinearSlopeParams& p, int type, cudaStream_t s) {
   return type == MB_BF16 ? launch_slope_type<__nv_bfloat16>(p, s) : launch_slope_type<__half>(p, s);
+}
+
+cudaError_t launch_linear_few(const LinearFewParams& p, int type, cudaStream_t s) {
+  return type == MB_BF16 ? launch_few_type<__nv_bfloat16>(p, s) : launch_few_type<__half>(p, s);
 }
 
 cudaError_t launch_linear_pack(const LinearPackParams& p, int sms, cudaStream_t s) {

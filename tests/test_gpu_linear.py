@@ -554,3 +554,45 @@ def test_dz_past_the_type_is_infinite(nss):
         dx, dw, _ = nss.mb_linear_backward(dy, x, w, z, "relu2")
         assert (dx[1] == math.inf).all() and dx[0].eq(128).all()
         assert (dw[3] == math.inf).all() and dw[:3].isfinite().all() and dw[4:].isfinite().all()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("cols,out,pad,shift", [(1, 1, 0, 0), (8, 8, 0, 0), (768, 768, 0, 0), (4096, 1001, 0, 0), (2056, 130, 8, 0),
+                                                (257, 66, 0, 0), (64, 67, 3, 1), (5000, 3, 0, 8), (1000, 1, 0, 0)])
+def test_forward_few_rows(nss, rows, cols, out, pad, shift):
+    """Single tokens: a pass over W, the tests' other sizes and epilogues with up to 8 rows."""
+    for dtype, act in (("bf16", "gelu"), ("f16", "relu2")):
+        g, t = _gen(rows + cols), TYPES[dtype]
+        x, w = _rows(rows, cols, t, g, pad, shift), _rows(out, cols, t, g, 0, shift, std=cols ** -0.5)
+        r, b = _rows(rows, out, t, g, pad, shift), torch.randn(out, generator=g, device="cuda")
+        whole = [torch.full((rows * (out + pad) + shift,), 7.0, device="cuda", dtype=t) for _ in range(2)]
+        y, z = (f[shift:].view(rows, out + pad)[:, :out] for f in whole)
+        _check_forward(nss, x, w, b, r, act, None, y=y, z=z)
+        for f in whole:
+            assert (f[:shift] == 7).all() and (f[shift:].view(rows, out + pad)[:, out:] == 7).all()
+        want, _ = _check_forward(nss, x, w, b.to(t), r, act, None, keep=False)
+        y.copy_(r)
+        nss.mb_linear(x, w, b.to(t), y, act, y=y)                           # over the residual
+        assert torch.equal(y, want)
+        _check_forward(nss, x, w, None, None, "silu", None)
+
+
+@pytest.mark.parametrize("ends", [[0, 0, 0], [8], [3, 3, 7], [0, 1, 2, 3, 4, 5, 6, 7], [1] * 40 + [2] * 30 + [8], [0] * 1023 + [5]])
+@pytest.mark.parametrize("out", [200, 131])
+def test_forward_few_rows_of_groups(nss, ends, out):
+    g, rows, cols, t = _gen(33), 8, 72, torch.bfloat16
+    x, w = _rows(rows, cols, t, g), (torch.randn(len(ends), out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
+    x[ends[-1]:] = math.nan
+    b, r = torch.randn(len(ends), out, generator=g, device="cuda"), _rows(rows, out, t, g)
+    y, z = (torch.full((rows, out), 7.0, device="cuda", dtype=t) for _ in range(2))
+    _check_forward(nss, x, w, b, r, "silu", ends, y=y, z=z)
+    assert not y[ends[-1]:].any() and not z[ends[-1]:].any()
+    if len(ends) == 3:
+        from newton_schulz_stacked_gb300 import _binding as binding
+        assert nss.mb_sync_status() == 0
+        for bad, held in (([5, 2, 8], [5, 5, 8]), ([1, 2, 30], [1, 2, 8]), ([-5, 2, 6], [0, 2, 6])):
+            x = _rows(rows, cols, t, g)
+            y, _ = nss.mb_linear(x, w, ends=torch.tensor(bad, dtype=torch.int32, device="cuda"))
+            assert nss.mb_sync_status() == binding.MB_ERR_ARG
+            want, _ = nss.mb_linear(x, w, ends=torch.tensor(held, dtype=torch.int32, device="cuda"))
+            assert nss.mb_sync_status() == 0 and torch.equal(y, want)
