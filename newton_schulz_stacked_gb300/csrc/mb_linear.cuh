@@ -348,7 +348,7 @@ struct Seen {
 // A warp's chunk in shared memory: rows of 128 bytes whose 16-byte pieces are exchanged by row (TMA's 128-byte swizzle), so
 // that lanes that each take a row, and lanes that each take a piece of neighbouring rows, hit distinct banks.  Whole lines
 // of memory: the TMA unit takes about two cycles for a row of a box whatever its length, and stores of 64-byte rows held
-// up the products' loads (65536x768->2816 with relu^2, z and a bias: 237 us in boxes of 32 columns).
+// up the products' loads (65536x768->2816 with gelu, z and a bias: 284 us in boxes of 32 columns, 267 in these).
 constexpr int CHUNK_COLS = 64;
 constexpr int CHUNK_BYTES = 32 * CHUNK_COLS * 2;
 __device__ __forceinline__ uint32_t chunk_at(int row, int piece) {
@@ -474,7 +474,7 @@ __device__ __forceinline__ void send_chunk(const WarpPlace& w, bool bulk, const 
 }
 
 // The residual's chunks on their way by TMA into a buffer of the warp's own, a chunk ahead: their way from memory is longer
-// than a short product's tile (65536x768->2816: 590 us where it is waited for).  Rows that TMA cannot address are read into
+// than a short product's tile (65536x768->2816 with a residual: 593 us where it is waited for, 228 so).  Rows that TMA cannot address are read into
 // the chunk's buffer when they are needed.
 struct ResidualFeed {
   uint8_t* buf;            // CHUNK_BYTES, or null: not by TMA

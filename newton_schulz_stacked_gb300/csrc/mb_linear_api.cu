@@ -245,7 +245,7 @@ BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
   if (d.dx && d.dweight) cut_few(p.dw, p.dx);
   if (d.dweight) reserve_parts(p.dw, ws);
   if (d.dx) reserve_parts(p.dx, ws);
-  p.ahead = p.slope && products && d.rows * static_cast<int64_t>(d.out) >= AHEAD_ELEMENTS &&
+  p.ahead = p.slope && !p.low && products && d.rows * static_cast<int64_t>(d.out) >= AHEAD_ELEMENTS &&
             access_of(d.dy, d.dy_stride, d.out, d.rows) == 16 && access_of(d.z, d.z_stride, d.out, d.rows) == 16;
   if (p.ahead) {
     p.slab = LINEAR_PIECE_ROWS;

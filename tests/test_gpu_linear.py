@@ -596,3 +596,12 @@ def test_forward_few_rows_of_groups(nss, ends, out):
             assert nss.mb_sync_status() == binding.MB_ERR_ARG
             want, _ = nss.mb_linear(x, w, ends=torch.tensor(held, dtype=torch.int32, device="cuda"))
             assert nss.mb_sync_status() == 0 and torch.equal(y, want)
+
+
+def test_narrow_products_with_many_columns(nss):
+    """dz of more elements than are formed under the products, with sums so few that it comes in two halves."""
+    g, t, rows, cols, out = _gen(35), torch.bfloat16, 1024, 2, 50000
+    x, w = _rows(rows, cols, t, g), _rows(out, cols, t, g)
+    dy, z = _rows(rows, out, t, g), _rows(rows, out, t, g)
+    workspace = torch.full((1 << 29,), 0xFF, dtype=torch.uint8, device="cuda")
+    _check_backward(nss, dy, x, w, z, "silu", None, workspace=workspace)
