@@ -120,7 +120,8 @@ def mb_linear(x, weight, bias=None, residual=None, activation: str = "none", end
     are consecutive groups, group g ending before row ends[g], such as tokens sorted by expert with
     ends = counts.cumsum(0, dtype=torch.int32); rows from the last end on get zeros.  The ends stay on the device.
     activation: "none", "relu", "relu2" (its square), "silu" or "gelu" (the tanh form).  One row, and up to 8 with weights that
-    are not large, take a kernel of their own that reads the weights once (single tokens).
+    are not large, take a kernel of their own that reads the weights once (single tokens).  y may be the residual; no
+    other overlap of a result.
     """
     return (_native or load_binding()).mb_linear(x, weight, bias, residual, activation, ends, keep, y, z, workspace, stream)
 
@@ -131,7 +132,7 @@ def mb_linear_backward(dy, x, weight, z=None, activation: str = "none", ends=Non
     """Gradients of mb_linear: (dx, dweight, dbias), None for those that are not wanted (input_grad, weight_grad, bias).
 
     z is the forward call's (not needed without an activation).  dweight is laid out as the weight, the gradient of a bank as
-    muon_multi_step takes it; dbias comes in x's type unless a float32 one is passed.  The residual's gradient is dy.
+    muon_multi_step takes it; dbias comes in x's type unless a float32 one is passed.  The residual's gradient is dy.  No result may overlap an input.
     """
     return (_native or load_binding()).mb_linear_backward(dy, x, weight, z, activation, ends, input_grad, weight_grad, bias,
                                                           dx, dweight, dbias, workspace, stream)

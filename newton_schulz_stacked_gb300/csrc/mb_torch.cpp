@@ -589,6 +589,18 @@ c10::DimVector with(const c10::DimVector& lead, int64_t last) {
   return d;
 }
 
+// Results that begin where an input of the call, or another result, does.
+void apart(std::initializer_list<std::pair<const char*, const void*>> results,
+           std::initializer_list<std::pair<const char*, const void*>> inputs) {
+  for (auto r = results.begin(); r != results.end(); ++r) {
+    if (!r->second) continue;
+    for (const auto& i : inputs)
+      if (r->second == i.second) throw Refused{std::string(r->first) + " may not be written over " + i.first};
+    for (auto o = results.begin(); o != r; ++o)
+      if (r->second == o->second) throw Refused{std::string(r->first) + " may not be written over " + o->first};
+  }
+}
+
 // x, weight, bias, residual, activation, ends, keep, y, z, workspace, stream
 PyObject* linear(PyObject* const* a, Py_ssize_t n) {
   const Tensor &x = cuda_tensor(a[0], "x"), &w = tensor(a[1], "weight");
@@ -631,6 +643,8 @@ PyObject* linear(PyObject* const* a, Py_ssize_t n) {
   d.out = static_cast<int32_t>(s.out);
   d.groups = static_cast<int32_t>(s.groups);
   d.type = s.type;
+  apart({{"y", d.y}, {"z", d.z}}, {{"x", d.x}, {"weight", d.weight}, {"bias", d.bias}});
+  if (d.z) apart({{"z", d.z}}, {{"residual", d.residual}});
   size_t need = 0;
   checked("mb_linear_workspace_bytes", mb_linear_workspace_bytes(&d, &need));
   const Workspace ws(a[9], need, device);
@@ -691,6 +705,7 @@ PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
   d.out = static_cast<int32_t>(s.out);
   d.groups = static_cast<int32_t>(s.groups);
   d.type = s.type;
+  apart({{"dx", d.dx}, {"dweight", d.dweight}, {"dbias", d.dbias}}, {{"dy", d.dy}, {"x", x.data_ptr()}, {"weight", d.weight}, {"z", d.z}});
   size_t need = 0;
   checked("mb_linear_backward_workspace_bytes", mb_linear_backward_workspace_bytes(&d, &need));
   const Workspace ws(a[12], need, device);

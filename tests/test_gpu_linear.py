@@ -605,3 +605,18 @@ def test_narrow_products_with_many_columns(nss):
     dy, z = _rows(rows, out, t, g), _rows(rows, out, t, g)
     workspace = torch.full((1 << 29,), 0xFF, dtype=torch.uint8, device="cuda")
     _check_backward(nss, dy, x, w, z, "silu", None, workspace=workspace)
+
+
+def test_results_over_inputs_are_refused(nss):
+    t = torch.bfloat16
+    x, w = torch.ones(12, 64, device="cuda", dtype=t), torch.ones(64, 64, device="cuda", dtype=t)
+    z, dy = torch.ones_like(x), torch.ones_like(x)
+    for given in ({"y": x}, {"z": x}, {"y": z, "z": z}, {"residual": z, "z": z}, {"y": w[:12]}):
+        with pytest.raises(ValueError):
+            nss.mb_linear(x, w, activation="relu", **given)
+    for given in ({"dx": dy}, {"dx": x}, {"dx": z}, {"dweight": w}):
+        with pytest.raises(ValueError):
+            nss.mb_linear_backward(dy, x, w, z, "relu", **given)
+    both = torch.ones(12, 128, device="cuda", dtype=t)                      # side by side is no overlap
+    y, _ = nss.mb_linear(both[:, :64], w, y=both[:, 64:])
+    assert (both[:, 64:] == 64).all() and (both[:, :64] == 1).all()
