@@ -164,5 +164,8 @@ def _of_groups(dy, ends):
 
 
 def linear(x, weight, bias=None, residual=None, activation: str = "none", ends=None) -> torch.Tensor:
-    """mb_linear, differentiable in x, weight, bias and residual; over groups of rows where ends are given."""
+    """mb_linear, differentiable in x, weight, bias and residual; over groups of rows where ends are given.
+
+    A backward pass can be captured into a CUDA graph; as with torch's own functions not while another graph of the same
+    leaves, made on another stream, is alive (capture then ends with an error)."""
     return _Linear.apply(x, weight, bias, residual, activation, ends)
