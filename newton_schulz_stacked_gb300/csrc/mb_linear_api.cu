@@ -375,13 +375,15 @@ int few_access(const mb_linear_desc& d) {
   return std::min(access_of(d.x, d.x_stride, d.in, d.rows), access_of(d.weight, d.in, d.in, 2));
 }
 
-// A single row, or up to 8 with weights that are short enough to read without tensor cores (us, rows of W's width x its rows):
-// one row 4096x4096 7.9 against 20.0 by tiles, 768x768 1.9 against 9.2; eight rows 768x768 3.6 against 9.2, 768x2816 8.3
-// against 9.7, 4096x4096 21.0 against 20.0, 4096x16384 70 against 38.  Off 16-byte boundaries elements come one by one.
+// Whether a pass over W is shorter than tiles.  On one GB300, us, in a graph, W from memory, by rows against by tiles: one row
+// 768->768 1.9 and 9.2, 4096->4096 7.8 and 20; 16 rows 768->768 2.8 and 9.3, 4096->4096 10.0 and 20, 4096->16384 34 and 32; 32 rows
+// 4096->4096 19.6 and 20, 4096->16384 65 and 32; 64 rows 768->768 3.5 and 9.3, 768->2816 5.6 and 9.9, 4096->1024 10.0 and 14.3,
+// 4096->4096 30 and 20.  Off 16-byte boundaries elements come one by one: one row 4095->4095 10.5 and 32, eight 765->765 6.5 and 14.
 bool by_rows(const mb_linear_desc& d) {
   if (d.rows == 1) return true;
   const int64_t elements = static_cast<int64_t>(d.in) * d.out;
-  return d.rows <= LINEAR_FEW_ROWS && elements <= (few_access(d) != 16 ? 1 << 20 : d.rows <= 4 ? 1 << 24 : 1 << 22);
+  if (few_access(d) != 16) return d.rows <= LINEAR_FEW_ROWS && elements <= 1 << 20;
+  return d.rows <= 16 || (d.rows <= LINEAR_SOME_ROWS && elements <= (d.rows <= 32 ? 1 << 24 : 1 << 22));
 }
 
 int few_rows(const mb_linear_desc& d, cudaStream_t stream) {

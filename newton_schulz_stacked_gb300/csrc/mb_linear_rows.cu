@@ -208,11 +208,63 @@ __global__ void __launch_bounds__(32 * BIAS_WARPS) linear_bias_kernel(const __gr
   else static_cast<T*>(p.db)[out] = from_float<T>(sum);
 }
 
-// y of up to 8 rows: bound by reading W, which the tensor cores' tiles of 256 rows would only wait for.  A CTA takes four columns
-// of y (rows of W) of one group, its warps every eighth 256 elements of them, each lane eight for all rows of x in fp32;
-// the lanes' sums, then the warps', are added in order.  1x4096->4096 7.9 us, 1x4096->16384 23.5 (5.7 TB/s); with more rows the
-// conversions and sums bound it: 4x4096->4096 13.8, 8x4096->4096 21.0, where the tiles take 20.1.
+// y of one row (off 16-byte boundaries up to 8): bound by reading W, which the tensor cores' tiles of 256 rows would only wait
+// for.  A CTA takes four columns of y (rows of W) of one group, its warps every eighth 256 elements of them, each lane eight
+// for all rows of x in fp32; the lanes' sums, then the warps', are added in order.  1x4096->4096 7.8 us, 1x4096->16384 23.6
+// (5.7 TB/s); with more rows the conversions and sums would bound it (8x4096->4096 21.0).
 constexpr int FEW_WARPS = 8, FEW_COLS = 4;
+
+// The rows of the blockIdx.y'th group that has any, and zeros in the columns from col0 on of the rows of no group.
+struct FewRows {
+  int g, begin, end;
+};
+template <typename T>
+__device__ __forceinline__ FewRows few_rows(const LinearFewParams& p, int* groups, int col0, int cols) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  FewRows f{0, 0, p.rows};
+  if (!p.ends) return f;
+  Groups G{groups, groups + LINEAR_MAX_GROUPS + 1, p.groups};
+  if (warp == 0 && fill_groups(G, p.ends, p.rows, lane) && blockIdx.x == 0 && blockIdx.y == 0 && lane == 0)
+    latch_status(p.status, DEV_BAD_SCALAR);
+  __syncthreads();
+  const int last = G.row[G.n];
+  f.begin = f.end = last;
+  int before = static_cast<int>(blockIdx.y);
+  for (int g0 = 0; g0 < G.n; g0 += 32) {
+    const int at = g0 + lane;
+    const bool some = at < G.n && G.row[at + 1] > G.row[at];
+    const unsigned all = __ballot_sync(0xffffffffu, some);
+    const unsigned found = __ballot_sync(0xffffffffu, some && __popc(all & ((1u << lane) - 1)) == before);
+    if (found) {
+      f.g = g0 + __ffs(found) - 1;
+      f.begin = G.row[f.g];
+      f.end = G.row[f.g + 1];
+      break;
+    }
+    before -= __popc(all);
+  }
+  if (blockIdx.y == 0 && blockIdx.z == 0) {
+    for (int i = threadIdx.x; i < (p.rows - last) * cols; i += blockDim.x) {
+      const long long row = last + i / cols;
+      const int col = col0 + i % cols;
+      if (col >= p.out) continue;
+      static_cast<T*>(p.y)[row * p.y_ld + col] = from_float<T>(0.f);
+      if (p.z) static_cast<T*>(p.z)[row * p.z_ld + col] = from_float<T>(0.f);
+    }
+  }
+  return f;
+}
+
+// One sum on its way out.
+template <typename T>
+__device__ __forceinline__ void finish_one(const LinearFewParams& p, float v, int g, long long row, int col) {
+  const long long at = static_cast<long long>(g) * p.out + col;
+  if (p.bias) v += p.bias_f32 ? static_cast<const float*>(p.bias)[at] : to_float(static_cast<const T*>(p.bias)[at]);
+  if (p.z) static_cast<T*>(p.z)[row * p.z_ld + col] = from_float<T>(v);
+  with_activation(p.act, [&](auto act) { v = activate<decltype(act)::value>(make_float2(v, 0.f)).x; });
+  if (p.residual) v += to_float(static_cast<const T*>(p.residual)[row * p.residual_ld + col]);
+  static_cast<T*>(p.y)[row * p.y_ld + col] = from_float<T>(v);
+}
 
 template <typename T, int ACCESS, int ROWS>
 __global__ void __launch_bounds__(32 * FEW_WARPS, ROWS == 1 ? 4 : 2) linear_few_kernel(const __grid_constant__ LinearFewParams p) {
@@ -220,43 +272,9 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, ROWS == 1 ? 4 : 2) linear_few_
   __shared__ float partial[FEW_WARPS][ROWS * FEW_COLS];
   begin_after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col0 = blockIdx.x * FEW_COLS;
-  int g = 0, begin = 0, end = p.rows, last = p.rows;
-  if (p.ends) {
-    Groups G{groups, groups + LINEAR_MAX_GROUPS + 1, p.groups};
-    if (warp == 0 && fill_groups(G, p.ends, p.rows, lane) && blockIdx.x == 0 && blockIdx.y == 0 && lane == 0)
-      latch_status(p.status, DEV_BAD_SCALAR);
-    __syncthreads();
-    // the blockIdx.y'th group that has rows
-    last = G.row[G.n];
-    begin = end = last;
-    int before = static_cast<int>(blockIdx.y);
-    for (int g0 = 0; g0 < G.n; g0 += 32) {
-      const int at = g0 + lane;
-      const bool some = at < G.n && G.row[at + 1] > G.row[at];
-      const unsigned all = __ballot_sync(0xffffffffu, some);
-      const bool mine = some && __popc(all & ((1u << lane) - 1)) == before;
-      const unsigned found = __ballot_sync(0xffffffffu, mine);
-      if (found) {
-        g = g0 + __ffs(found) - 1;
-        begin = G.row[g];
-        end = G.row[g + 1];
-        break;
-      }
-      before -= __popc(all);
-    }
-  }
+  const FewRows f = few_rows<T>(p, groups, col0, FEW_COLS);
+  const int g = f.g, begin = f.begin, end = f.end;
   const T* x = static_cast<const T*>(p.x);
-  T* z = static_cast<T*>(p.z);
-  T* y = static_cast<T*>(p.y);
-  if (blockIdx.y == 0 && static_cast<int>(threadIdx.x) < (p.rows - last) * FEW_COLS) {
-    // zeros in the rows of no group
-    const long long row = last + threadIdx.x / FEW_COLS;
-    const int col = col0 + threadIdx.x % FEW_COLS;
-    if (col < p.out) {
-      y[row * p.y_ld + col] = from_float<T>(0.f);
-      if (z) z[row * p.z_ld + col] = from_float<T>(0.f);
-    }
-  }
   const int n = end - begin;
   if (n == 0) return;
   const T* w = static_cast<const T*>(p.w) + (static_cast<long long>(g) * p.out + col0) * p.in;
@@ -297,22 +315,97 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, ROWS == 1 ? 4 : 2) linear_few_
   float v = 0.f;
 #pragma unroll
   for (int i = 0; i < FEW_WARPS; ++i) v += partial[i][threadIdx.x];
-  const long long row = begin + r, at = static_cast<long long>(g) * p.out + col;
-  if (p.bias) v += p.bias_f32 ? static_cast<const float*>(p.bias)[at] : to_float(static_cast<const T*>(p.bias)[at]);
-  if (z) z[row * p.z_ld + col] = from_float<T>(v);
-  with_activation(p.act, [&](auto act) { v = activate<decltype(act)::value>(make_float2(v, 0.f)).x; });
-  if (p.residual) v += to_float(static_cast<const T*>(p.residual)[row * p.residual_ld + col]);
-  y[row * p.y_ld + col] = from_float<T>(v);
+  finish_one<T>(p, v, g, begin + r, col);
+}
+
+// y of up to 64 rows: bound by reading W as well, the products by warps' MMAs (16 x 8 x 16) whose operands come straight from
+// memory: a lane's 16 bytes of a row hold what two MMAs take of it, in an order of the contraction that is the same for x
+// and W.  A CTA takes 16 columns of y (rows of W) and 16 or 32 rows of one group, each of its warps 32 elements of the
+// contraction in turn, which are added in order.  A call is a chain of waits on memory: long contractions go to 16 warps
+// (16x4096->1024 8.3 us, by 8 warps 13.2), short ones of 32 rows to 8 (32x768->2816 4.9, by 16 6.1).
+constexpr int SOME_COLS = 16, SOME_LD = SOME_COLS + 2;
+
+template <typename T>
+__device__ __forceinline__ void warp_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename T, int TILES, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) linear_some_kernel(const __grid_constant__ LinearFewParams p) {
+  constexpr int AHEAD = TILES == 2 && WARPS == 16 ? 4 : 2;
+  __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
+  __shared__ float partial[WARPS][16 * TILES][SOME_LD];
+  begin_after_previous();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col0 = blockIdx.x * SOME_COLS;
+  FewRows f = few_rows<T>(p, groups, col0, SOME_COLS);
+  f.begin += static_cast<int>(blockIdx.z) * 16 * TILES;
+  const int n = min(f.end - f.begin, 16 * TILES), quad = lane >> 2, k0 = 8 * (lane & 3);
+  if (n <= 0) return;
+  const T* w[2];
+  const T* x[2 * TILES];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)                    // (past the last column, or row: that one again)
+    w[i] = static_cast<const T*>(p.w) + (static_cast<long long>(f.g) * p.out + min(col0 + 8 * i + quad, p.out - 1)) * p.in + k0;
+#pragma unroll
+  for (int i = 0; i < 2 * TILES; ++i)
+    x[i] = static_cast<const T*>(p.x) + (f.begin + min(8 * i + quad, n - 1)) * p.x_ld + k0;
+  float sum[TILES][2][4];
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[t][i / 4][i % 4] = 0.f;
+#pragma unroll AHEAD
+  for (int k = 32 * warp; k < p.in; k += 32 * WARPS) {
+    const bool some = k + k0 < p.in;
+    uint4 a[2 * TILES], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) b[i] = some ? *reinterpret_cast<const uint4*>(w[i] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * TILES; ++i) a[i] = some ? *reinterpret_cast<const uint4*>(x[i] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        warp_mma<T>(sum[t][i], a[2 * t].x, a[2 * t + 1].x, a[2 * t].y, a[2 * t + 1].y, b[i].x, b[i].y);
+        warp_mma<T>(sum[t][i], a[2 * t].z, a[2 * t + 1].z, a[2 * t].w, a[2 * t + 1].w, b[i].z, b[i].w);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 16 * t + quad, col = 8 * i + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(&partial[warp][row][col]) = make_float2(sum[t][i][0], sum[t][i][1]);
+      *reinterpret_cast<float2*>(&partial[warp][row + 8][col]) = make_float2(sum[t][i][2], sum[t][i][3]);
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * SOME_COLS; i += 32 * WARPS) {
+    const int row = i / SOME_COLS, col = i % SOME_COLS;
+    if (col0 + col >= p.out) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < WARPS; ++j) v += partial[j][row][col];
+    finish_one<T>(p, v, f.g, f.begin + row, col0 + col);
+  }
 }
 
 template <typename T>
 cudaError_t launch_few_type(const LinearFewParams& p, cudaStream_t s) {
-  const dim3 grid((p.out + FEW_COLS - 1) / FEW_COLS, p.groups < p.rows ? p.groups : p.rows), block(32 * FEW_WARPS);
+  const int groups = p.groups < p.rows ? p.groups : p.rows;
+  const dim3 grid((p.out + FEW_COLS - 1) / FEW_COLS, groups), wide((p.out + SOME_COLS - 1) / SOME_COLS, groups, (p.rows + 31) / 32), block(32 * FEW_WARPS);
   if (p.access != 16 && p.rows == 1) return launch_after(linear_few_kernel<T, 2, 1>, grid, block, 0, s, p);
   if (p.access != 16) return launch_after(linear_few_kernel<T, 2, LINEAR_FEW_ROWS>, grid, block, 0, s, p);
   if (p.rows == 1) return launch_after(linear_few_kernel<T, 16, 1>, grid, block, 0, s, p);
-  if (p.rows <= 4) return launch_after(linear_few_kernel<T, 16, 4>, grid, block, 0, s, p);
-  return launch_after(linear_few_kernel<T, 16, LINEAR_FEW_ROWS>, grid, block, 0, s, p);
+  if (p.rows <= 16) return launch_after(linear_some_kernel<T, 1, 16>, wide, dim3(512), 0, s, p);
+  if (p.in <= 1024) return launch_after(linear_some_kernel<T, 2, 8>, wide, dim3(256), 0, s, p);
+  return launch_after(linear_some_kernel<T, 2, 16>, wide, dim3(512), 0, s, p);
 }
 
 template <typename T>

@@ -620,3 +620,30 @@ def test_results_over_inputs_are_refused(nss):
     both = torch.ones(12, 128, device="cuda", dtype=t)                      # side by side is no overlap
     y, _ = nss.mb_linear(both[:, :64], w, y=both[:, 64:])
     assert (both[:, 64:] == 64).all() and (both[:, :64] == 1).all()
+
+
+@pytest.mark.parametrize("rows", [2, 7, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("cols,out,pad", [(8, 8, 0), (40, 1, 8), (264, 67, 0), (768, 768, 0), (1000, 130, 24), (4096, 333, 0)])
+def test_forward_some_rows(nss, rows, cols, out, pad):
+    """Up to 64 rows from 16-byte boundaries: the warps' products, and one row more."""
+    for dtype, act in (("bf16", "silu"), ("f16", "none")):
+        g, t = _gen(rows + cols), TYPES[dtype]
+        x, w = _rows(rows, cols, t, g, pad), _rows(out, cols, t, g, std=cols ** -0.5)
+        r, b = _rows(rows, out, t, g, 5), torch.randn(out, generator=g, device="cuda").to(t)
+        whole = torch.full((rows, out + 3), 7.0, device="cuda", dtype=t)
+        _check_forward(nss, x, w, b, r, act, None, y=whole[:, :out])
+        assert (whole[:, out:] == 7).all()
+        _check_forward(nss, x, w, None, None, "relu2", None, keep=False)
+
+
+@pytest.mark.parametrize("ends", [[0, 0, 0], [60], [3, 3, 50], [5, 20, 20, 41, 57, 64], [1] * 40 + [30] * 30 + [62],
+                                  list(range(1, 65)), [0] * 1023 + [64]])
+@pytest.mark.parametrize("out", [200, 131])
+def test_forward_some_rows_of_groups(nss, ends, out):
+    g, rows, cols, t = _gen(37), 64, 72, torch.bfloat16
+    x, w = _rows(rows, cols, t, g), (torch.randn(len(ends), out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
+    x[ends[-1]:] = math.nan
+    b, r = torch.randn(len(ends), out, generator=g, device="cuda"), _rows(rows, out, t, g)
+    y, z = (torch.full((rows, out), 7.0, device="cuda", dtype=t) for _ in range(2))
+    _check_forward(nss, x, w, b, r, "gelu", ends, y=y, z=z)
+    assert not y[ends[-1]:].any() and not z[ends[-1]:].any()
