@@ -1,5 +1,5 @@
 // The passes over rows around the products of mb_linear: dz = dy act'(z) with its sums over slabs of rows, and rows copied to
-// 16-byte boundaries for operands that TMA cannot address; and the product over a few rows, which is a pass over W's.
+// 16-byte boundaries for operands that TMA cannot address; and the product over a few rows, which is a pass over W.
 #include <type_traits>
 
 #include "mb_block.h"
