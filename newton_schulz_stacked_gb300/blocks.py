@@ -119,8 +119,8 @@ def mb_linear(x, weight, bias=None, residual=None, activation: str = "none", end
     [..., out].  With `ends`, int32 [groups], weight is a bank [groups, out, in] (and bias [groups, out]): the rows of x
     are consecutive groups, group g ending before row ends[g], such as tokens sorted by expert with
     ends = counts.cumsum(0, dtype=torch.int32); rows from the last end on get zeros.  The ends stay on the device.
-    activation: "none", "relu", "relu2" (its square), "silu" or "gelu" (the tanh form).  A few rows (single tokens, up to
-    64 with weights that are not large) take kernels of their own that read the weights once.  y may be the residual; no
+    activation: "none", "relu", "relu2" (its square), "silu" or "gelu" (the tanh form).  A few rows (single tokens, up
+    to 512 with small weights) take kernels of their own, without tiles.  y may be the residual; no
     other overlap of a result.
     """
     return (_native or load_binding()).mb_linear(x, weight, bias, residual, activation, ends, keep, y, z, workspace, stream)

@@ -107,8 +107,9 @@ struct LinearPackParams {
   int pairs;               // rows and columns come in 4-byte pairs
 };
 
-// The product over a few rows: at most LINEAR_SOME_ROWS where W's and x's rows start at 16-byte boundaries, else LINEAR_FEW_ROWS.
-constexpr int LINEAR_FEW_ROWS = 8, LINEAR_SOME_ROWS = 64;
+// The product over a few rows: at most LINEAR_SOME_ROWS (LINEAR_SOME_GROUPED over groups) where W's and x's rows start at 16-byte
+// boundaries, else LINEAR_FEW_ROWS.
+constexpr int LINEAR_FEW_ROWS = 8, LINEAR_SOME_ROWS = 512, LINEAR_SOME_GROUPED = 64;
 struct LinearFewParams {
   const void* x;
   long long x_ld;

@@ -376,14 +376,16 @@ int few_access(const mb_linear_desc& d) {
 }
 
 // Whether a pass over W is shorter than tiles.  On one GB300, us, in a graph, W from memory, by rows against by tiles: one row
-// 768->768 1.9 and 9.2, 4096->4096 7.8 and 20; 16 rows 768->768 2.8 and 9.3, 4096->4096 10.0 and 20, 4096->16384 34 and 32; 32 rows
-// 4096->4096 19.6 and 20, 4096->16384 65 and 32; 64 rows 768->768 3.5 and 9.3, 768->2816 5.6 and 9.9, 4096->1024 10.0 and 14.3,
-// 4096->4096 30 and 20.  Off 16-byte boundaries elements come one by one: one row 4095->4095 10.5 and 32, eight 765->765 6.5 and 14.
+// 768->768 1.9 and 9.2, 4096->4096 7.8 and 20; 16 rows 768->768 2.6 and 9.3, 4096->4096 10.0 and 20, 4096->16384 34 and 32; 64 rows
+// 768->768 3.5 and 9.3, 768->2816 5.6 and 9.9, 4096->1024 10.1 and 14.4, 4096->4096 30 and 20; 128 rows 768->2816 8.9 and 9.9; 256
+// rows 768->768 4.7 and 9.4, 1024->1024 8.4 and 10.5, 768->2816 14.7 and 9.9; 512 rows 768->768 7.9 and 9.4, 1024->1024 13.1 and
+// 10.6.  Over groups the grid has places for every group with all rows, so that it is kept to fewer.  Off 16-byte
+// boundaries elements come one by one: one row 4095->4095 10.5 and 32, eight 765->765 6.5 and 14.
 bool by_rows(const mb_linear_desc& d) {
   if (d.rows == 1) return true;
   const int64_t elements = static_cast<int64_t>(d.in) * d.out;
   if (few_access(d) != 16) return d.rows <= LINEAR_FEW_ROWS && elements <= 1 << 20;
-  return d.rows <= 16 || (d.rows <= LINEAR_SOME_ROWS && elements <= (d.rows <= 32 ? 1 << 24 : 1 << 22));
+  return d.rows <= 16 || (d.rows <= (d.groups > 1 ? LINEAR_SOME_GROUPED : LINEAR_SOME_ROWS) && d.rows * elements <= 1 << 28);
 }
 
 int few_rows(const mb_linear_desc& d, cudaStream_t stream) {

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, ROWS == 1 ? 4 : 2) linear_few_
   finish_one<T>(p, v, g, begin + r, col);
 }
 
-// y of up to 64 rows: bound by reading W as well, the products by warps' MMAs (16 x 8 x 16) whose operands come straight from
+// y of up to 512 rows: bound by reading W as well, the products by warps' MMAs (16 x 8 x 16) whose operands come straight from
 // memory: a lane's 16 bytes of a row hold what two MMAs take of it, in an order of the contraction that is the same for x
 // and W.  A CTA takes 16 columns of y (rows of W) and 16 or 32 rows of one group, each of its warps 32 elements of the
 // contraction in turn, which are added in order.  A call is a chain of waits on memory: long contractions go to 16 warps

@@ -122,7 +122,8 @@ def _check_backward(nss, dy, x, w, z, act, ends, bias=True, **given):
 
 
 @pytest.mark.parametrize("rows,cols,out", [(1, 8, 8), (1, 64, 64), (7, 40, 24), (64, 768, 768), (128, 64, 256), (129, 72, 264),
-                                           (255, 128, 128), (256, 256, 256), (257, 320, 520), (1000, 200, 1000), (3000, 64, 40)])
+                                           (255, 128, 128), (256, 256, 256), (257, 320, 520), (1000, 200, 1000), (3000, 64, 40), (511, 264, 40), (512, 64, 264),
+                                           (513, 64, 264), (520, 8, 8), (600, 768, 768), (769, 72, 264)])
 def test_forward_sizes(nss, rows, cols, out):
     g = _gen(rows + cols)
     x, w = _rows(rows, cols, torch.bfloat16, g), _rows(out, cols, torch.bfloat16, g, std=cols ** -0.5)
@@ -132,9 +133,10 @@ def test_forward_sizes(nss, rows, cols, out):
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("bias,residual", [(None, False), ("own", True), ("f32", False), (None, True)])
-def test_forward_epilogues(nss, dtype, act, bias, residual):
+@pytest.mark.parametrize("rows", [300, 600])
+def test_forward_epilogues(nss, dtype, act, bias, residual, rows):
     g, t = _gen(3), TYPES[dtype]
-    rows, cols, out = 300, 136, 392
+    cols, out = 136, 392
     x, w = _rows(rows, cols, t, g), _rows(out, cols, t, g, std=cols ** -0.5)
     b = None if bias is None else torch.randn(out, generator=g, device="cuda").to(t if bias == "own" else torch.float32)
     r = _rows(rows, out, t, g) if residual else None
@@ -145,9 +147,10 @@ def test_forward_epilogues(nss, dtype, act, bias, residual):
 @pytest.mark.parametrize("cols,out,pad,shift", [(7, 5, 0, 0), (65, 67, 0, 0), (64, 64, 8, 0), (64, 64, 3, 0), (64, 64, 0, 1),
                                                 (64, 66, 2, 2), (129, 1, 0, 0), (1, 130, 0, 0), (1, 1, 0, 0), (61, 61, 3, 0),
                                                 (63, 191, 1, 8), (64, 333, 3, 0)])
-def test_forward_layouts(nss, cols, out, pad, shift):
+@pytest.mark.parametrize("rows", [270, 530])
+def test_forward_layouts(nss, cols, out, pad, shift, rows):
     """Odd widths, rows and tensors off 16-byte boundaries, results in wider buffers (whose other columns stay)."""
-    g, rows = _gen(5), 270
+    g = _gen(5)
     t = torch.bfloat16
     x, w = _rows(rows, cols, t, g, pad, shift), _rows(out, cols, t, g, 0, shift, std=cols ** -0.5)
     r, b = _rows(rows, out, t, g, pad, shift), torch.randn(out, generator=g, device="cuda").to(t)
@@ -363,17 +366,18 @@ def test_nothing(nss):
     assert dx.shape == (0, 8) and not dw.any() and not db.any()
 
 
-def test_values_that_are_no_numbers(nss):
+@pytest.mark.parametrize("rows", [300, 600])
+def test_values_that_are_no_numbers(nss, rows):
     """A NaN or an infinity of a row stays in the row; through the activations as in torch."""
     g, t = _gen(19), torch.bfloat16
-    x, w = _rows(300, 64, t, g), _rows(128, 64, t, g, std=0.125)
+    x, w = _rows(rows, 64, t, g), _rows(128, 64, t, g, std=0.125)
     for act in ACTS:
         x[5, 3], x[6, 3], x[7, 3] = math.nan, math.inf, 1e30
         y, z = nss.mb_linear(x, w, activation=act, keep=True)
         want = _act(z.float(), act).to(t)
         assert torch.equal(y.isnan()[[5, 6]], want.isnan()[[5, 6]])
         assert z[5].isnan().all() and y[5].isnan().all()
-        keep = [i for i in range(300) if i not in (5, 6, 7)]
+        keep = [i for i in range(rows) if i not in (5, 6, 7)]
         assert y[keep].isfinite().all()
 
 
