@@ -29,6 +29,8 @@
 // resident yet holds none.
 // Producers and issuer run as whole warps, the same in all lanes, and elect a lane for each TMA copy, MMA or commit: those take
 // their operands from uniform registers, and values that one lane alone has worked out are moved there one by one.
+// Every bounded wait of a warp is decided by all of its lanes: each looks at a clock of its own, and a lane that gave up alone
+// would leave the others at the warp's next barrier.
 //
 // A long contraction over few tiles is cut into parts whose fp32 sums go to the workspace, and linear_join_kernel adds them.
 //
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         const int kb = pass * u.blocks + past;
         if (kb < u.kb0 || kb >= u.kb1) continue;
         const int st = (it + kb - u.kb0) % stages;
-        ok = mbar_wait_or_abort(&past_bar[st], (past_phase >> st) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&past_bar[st], (past_phase >> st) & 1u, abort_flag));
         if (!ok) break;
         past_phase ^= 1u << st;
         // a box's rows of 128 bytes are its rows of the contraction (the swizzle stays within a row)
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(cleared_even + 8u * static_cast<uint32_t>(st));
       }
-      if (!__all_sync(0xffffffffu, ok)) {
+      if (!ok) {
         fail();
         break;
       }
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         bias[0] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * half, lane);
         bias[1] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * (half + 2), lane);
       }
-      if (!mbar_wait_or_abort(&tfull[buf], (k >> 1) & 1, abort_flag)) {
+      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&tfull[buf], (k >> 1) & 1, abort_flag))) {
         fail();
         break;
       }

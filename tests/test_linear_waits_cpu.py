@@ -1,0 +1,25 @@
+"""The waits of the products' kernel as its source has them: what they guard against cannot be provoked without a wait that
+runs out or a race, so the text itself is held to its two rules."""
+import os
+import re
+
+import newton_schulz_stacked_gb300 as nss
+
+CSRC = os.path.join(os.path.dirname(nss.__file__), "csrc")
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_bounded_waits_are_decided_by_whole_warps():
+    """Lanes time a wait by clocks of their own: what one of them decides, all have to."""
+    found = 0
+    for name in ("mb_linear.cu", "mb_linear.cuh"):
+        text = _source(name)
+        for call in re.finditer(r"mbar_wait(?:_cluster)?_or_abort\(", text):
+            found += 1
+            before = text[:call.start()].rstrip()
+            assert re.search(r"__all_sync\(0xffffffffu,$", before), text[call.start() - 120:call.end() + 80]
+    assert found >= 8
