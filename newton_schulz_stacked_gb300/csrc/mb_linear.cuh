@@ -338,6 +338,8 @@ struct Seen {
       __nanosleep(200);
       if (__any_sync(0xffffffffu, *abort_flag || globaltimer_ns() - t0 > WAIT_LIMIT_NS)) return false;
     }
+    // each lane has acquired a slab of its own, and any one of them issues the loads of all: votes order no memory
+    __syncwarp();
     fence_async_global();
     return true;
   }

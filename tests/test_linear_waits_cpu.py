@@ -23,3 +23,12 @@ def test_bounded_waits_are_decided_by_whole_warps():
             before = text[:call.start()].rstrip()
             assert re.search(r"__all_sync\(0xffffffffu,$", before), text[call.start() - 120:call.end() + 80]
     assert found >= 8
+
+
+def test_slabs_of_dz_are_handed_over_through_a_barrier():
+    """A lane acquires its slab's counter, another lane issues the load: a warp barrier, then the fence between generic and
+    asynchronous accesses, stand between them."""
+    text = _source("mb_linear.cuh")
+    body = text[text.index("bool rows(const LinearAhead& A"):]
+    body = body[body.index("load_acquire"):body.index("return true;", body.index("load_acquire"))]
+    assert re.search(r"__syncwarp\(\);\s*fence_async_global\(\);\s*$", body), body
