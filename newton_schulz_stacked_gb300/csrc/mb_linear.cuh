@@ -214,7 +214,10 @@ __device__ __forceinline__ float slope(float z) {
   }
   if (ACT == MB_ACT_GELU) {
     const float p = sigmoid(GELU_SCALE * fmaf(GELU_CUBE * z * z, z, z));
-    return p * fmaf(GELU_SCALE * z * (1.f - p), fmaf(3.f * GELU_CUBE * z, z, 1.f), 1.f);
+    // past 16 p is 0 or 1 and the slope is p, which a product that overflows (z^3 from 10^13 on) would make NaN; an
+    // infinite z makes it (z 0)
+    const float c = fminf(fmaxf(z, -16.f), 16.f);
+    return p * fmaf(GELU_SCALE * c * (1.f - p), fmaf(3.f * GELU_CUBE * c, c, 1.f), fmaf(z, 0.f, 1.f));
   }
   return 1.f;
 }
