@@ -375,17 +375,56 @@ int few_access(const mb_linear_desc& d) {
   return std::min(access_of(d.x, d.x_stride, d.in, d.rows), access_of(d.weight, d.in, d.in, 2));
 }
 
-// Whether a pass over W is shorter than tiles.  On one GB300, us, in a graph, W from memory, by rows against by tiles: one row
-// 768->768 1.9 and 9.2, 4096->4096 7.8 and 20; 16 rows 768->768 2.6 and 9.3, 4096->4096 10.0 and 20, 4096->16384 34 and 32; 64 rows
-// 768->768 3.5 and 9.3, 768->2816 5.6 and 9.9, 4096->1024 10.1 and 14.4, 4096->4096 30 and 20; 128 rows 768->2816 8.9 and 9.9; 256
-// rows 768->768 4.7 and 9.4, 1024->1024 8.4 and 10.5, 768->2816 14.7 and 9.9; 512 rows 768->768 7.9 and 9.4, 1024->1024 13.1 and
-// 10.6.  Over groups the grid has places for every group with all rows, so that it is kept to fewer.  Off 16-byte
-// boundaries elements come one by one: one row 4095->4095 10.5 and 32, eight 765->765 6.5 and 14.
+// A kernel of mb_linear_rows.cu as its time goes: columns and rows of a CTA, how deep its warps reach in one step; then in ns what
+// a CTA costs an otherwise full GPU, the same per element of `in`, and a CTA that finds no rows; in us a step's wait and
+// the begin; and the rate at which W comes, in TB/s.
+struct RowsForm {
+  int cols, rows, deep;
+  double cta, per_in, idle, step, begin, rate;
+};
+
+// The time of a product by rows, in us: its CTAs' work or the chain of waits along the contraction, whichever is longer, and the
+// lesser of the two as far as it shows.
+double time_by_rows(const mb_linear_desc& d, bool wide) {
+  const RowsForm some16{16, 16, 512, 3.3, 0.0039, 1.8, 0.51, 1.8, 7.4}, short32{16, 32, 256, 3.0, 0.008, 0.9, 0.59, 1.6, 5.5},
+      long32{16, 32, 512, 14.0, 0.0077, 2.9, 0.58, 1.0, 3.9}, one{4, 1, 2048, 1.7, 0.0007, 1.0, 0.41, 1.3, 9.5},
+      one_single{4, 1, 2048, 1.8, 0.0005, 1.0, 0.5, 1.4, 4.0}, few_single{4, 8, 2048, 13.0, 0.0062, 1.0, 4.1, 0.8, 20.0};
+  const RowsForm& f = !wide ? (d.rows == 1 ? one_single : few_single)
+                            : d.rows == 1 ? one : d.rows <= 16 ? some16 : d.in <= 1024 ? short32 : long32;
+  const int64_t columns = parts_of(d.out, f.cols), slabs = parts_of(d.rows, f.rows);
+  const int64_t some = std::min<int64_t>(d.groups, d.rows);      // groups that can have rows
+  double ctas = columns * std::max(some, slabs) * (f.cta + f.per_in * d.in);
+  if (d.groups > 1) ctas += columns * some * slabs * f.idle * (1 + d.groups / 64.0);     // (each looks the groups through)
+  const double waits = f.step * parts_of(d.in, f.deep) + 2e-6 * d.in * d.out * some / f.rate;
+  return f.begin + std::sqrt(1e-6 * ctas * ctas + waits * waits);
+}
+
+// And by tiles, from the same cut as the call's: a tile of a short contraction takes as long as its results take to leave.
+double time_by_tiles(const mb_linear_desc& d, bool wide) {
+  const Cut c = plan_forward(d).y;
+  const int64_t some = std::min<int64_t>(d.groups, d.rows), tiles = std::max(some, parts_of(d.rows, LINEAR_TILE)) * parts_of(d.out, c.wide);
+  const Cut held{c.wide, c.splits, tiles, c.blocks, c.n, 0};
+  const double weights = 2e-6 * d.in * d.out * d.groups;         // MB
+  double t = 2.3 + 0.33 * (parts_of(tiles * c.splits, MAX_PAIRS) * std::max(unit_time(c), 7.6 * c.wide / 256) + 8 + join_time(held)) +
+             0.07 * weights * some / d.groups;
+  if (!wide) t += 2.5 + 0.57 * (weights + 2e-6 * d.rows * d.in); // laid out at 16-byte boundaries first
+  return t;
+}
+
+// Whether a few rows go by the kernels without tiles.  The two times above are fitted to 540 calls on one GB300 (in a graph, W from
+// memory; 1 to 512 rows, in and out 8 to 65536, 1 to 256 groups): within about 15 % each, and the choice by them costs 1 %
+// over the better side of each call.  Both sides of some, us, by rows and by tiles: one row 768->768 1.8 and 8.6, 4096->4096
+// 7.9 and 22, 8->65536 28 and 15; 16 rows 4096->4096 10.0 and 20, 65536->64 99 and 28; 64 rows 768->768 3.5 and 8.5,
+// 4096->1024 10.2 and 14.5, 64->32768 16 and 9.4, 65536->64 125 and 28; 256 rows 768->768 4.6 and 8.9, 64->8192 15 and 6.8; 512
+// rows 64->64 2.0 and 5.3, 768->768 8.0 and 9.0, 64->2816 11 and 6.6, 64->8192 29 and 7.3, 8->65536 208 and 37, 4096->128
+// 6.5 and 12.  Over groups: 64 rows of 8 256->1024 5.0 and 7.7, 1024->2816 24 and 19; of 64 1024->64 7.3 and 12, 1024->2816 170 and
+// 67.  Off 16-byte boundaries elements come one by one: one row 4095->4095 10 and 33; eight 765->765 6.9 and 12, 33->65535
+// 220 and 34.  No product by tiles takes less than 5.
 bool by_rows(const mb_linear_desc& d) {
-  if (d.rows == 1) return true;
-  const int64_t elements = static_cast<int64_t>(d.in) * d.out;
-  if (few_access(d) != 16) return d.rows <= LINEAR_FEW_ROWS && elements <= 1 << 20;
-  return d.rows <= 16 || (d.rows <= (d.groups > 1 ? LINEAR_SOME_GROUPED : LINEAR_SOME_ROWS) && d.rows * elements <= 1 << 28);
+  const bool wide = few_access(d) == 16;
+  if (d.rows > (!wide ? LINEAR_FEW_ROWS : d.groups > 1 ? LINEAR_SOME_GROUPED : LINEAR_SOME_ROWS)) return false;
+  const double t = time_by_rows(d, wide);
+  return t < 5 || t < time_by_tiles(d, wide);
 }
 
 int few_rows(const mb_linear_desc& d, cudaStream_t stream) {

@@ -318,10 +318,12 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, ROWS == 1 ? 4 : 2) linear_few_
   finish_one<T>(p, v, g, begin + r, col);
 }
 
-// y of up to 512 rows: bound by reading W as well, the products by warps' MMAs (16 x 8 x 16) whose operands come straight from
-// memory: a lane's 16 bytes of a row hold what two MMAs take of it, in an order of the contraction that is the same for x
-// and W.  A CTA takes 16 columns of y (rows of W) and 16 or 32 rows of one group, each of its warps 32 elements of the
-// contraction in turn, which are added in order.  A call is a chain of waits on memory: long contractions go to 16 warps
+// y of up to 512 rows, the products by warps' MMAs (16 x 8 x 16) whose operands come straight from memory.  With up to 32 rows
+// bound by reading W (16x4096->4096 10.0 us, 3.4 TB/s) and the chain of waits on it; with more, every 32 rows read W again
+// (from the L2) and every 16 columns x, and the number of CTAs is what counts (512x768->768 8.0 us, 768 CTAs).  A lane's
+// 16 bytes of a row hold what two MMAs take of it, in an order of the contraction that is the same for x and W.  A CTA
+// takes 16 columns of y (rows of W) and 16 or 32 rows of one group, each of its warps 32 elements of the contraction in turn,
+// which are added in order.  A call is a chain of waits on memory: long contractions go to 16 warps
 // (16x4096->1024 8.3 us, by 8 warps 13.2), short ones of 32 rows to 8 (32x768->2816 4.9, by 16 6.1).
 constexpr int SOME_COLS = 16, SOME_LD = SOME_COLS + 2;
 

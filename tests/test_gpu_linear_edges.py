@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_linear import ACTS, _add, _gen, _near, _rows, _slope, nss  # noqa: F401
+from test_gpu_linear import ACTS, _add, _check_forward, _gen, _near, _rows, _slope, nss  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,73 @@ def _wide_slope(z, act):
     far = z.abs() > 1e3
     near = _slope(torch.where(far, 1.0, z), act)
     return torch.where(far, 2 * z.clamp(min=0) if act == "relu2" else (z > 0).double(), near)
+
+
+def _time(call, n=20):
+    """us of a call among others: in a graph, the best of five replays."""
+    for _ in range(3):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    best = math.inf
+    for _ in range(6):
+        begin.record()
+        graph.replay()
+        end.record()
+        end.synchronize()
+        best = min(best, begin.elapsed_time(end) * 1e3 / n)
+    return best
+
+
+@pytest.mark.parametrize("cols,out,groups", [(8, 8192, 0), (8, 65536, 0), (64, 2816, 0), (64, 8192, 0), (64, 64, 0), (768, 768, 0),
+                                             (256, 16384, 0), (16384, 768, 0), (65536, 8, 0), (65536, 64, 0), (33, 20001, 0),
+                                             (64, 8192, 64), (1024, 2816, 8), (1024, 2816, 64), (1024, 64, 64), (2816, 1024, 256)])
+def test_fewer_rows_take_no_longer(nss, cols, out, groups):
+    """Whichever kernels a call's sizes choose, more rows must not be the cheaper call."""
+    g, t = _gen(43), torch.bfloat16
+    x = _rows(513, cols, t, g)
+    w = torch.randn(*((groups,) if groups else ()), out, cols, generator=g, device="cuda").to(t)
+
+    def time(rows):
+        ends = None
+        if groups:
+            ends = torch.tensor([rows * (i + 1) // groups for i in range(groups)], dtype=torch.int32, device="cuda")
+        y = torch.empty(rows, out, device="cuda", dtype=t)
+        workspace = torch.empty(1 << 28, device="cuda", dtype=torch.uint8)
+        return _time(lambda: nss.mb_linear(x[:rows], w, ends=ends, y=y, workspace=workspace))
+
+    most = time(513)
+    for rows in (1, 2, 8, 16, 17, 64, 128, 256, 512):
+        few = time(rows)
+        assert few <= 1.6 * most + 1, (rows, few, most)
+
+
+@pytest.mark.parametrize("rows,cols,out", [(1, 8, 65536), (1, 65536, 8), (2, 40, 20000), (2, 16384, 72), (5, 33, 9001), (8, 4095, 15),
+                                           (16, 32, 40008), (16, 20000, 16), (17, 2056, 1000), (64, 64, 33000), (65, 1024, 4096),
+                                           (250, 8, 8200), (256, 256, 1000), (256, 256, 4096), (512, 64, 264), (512, 64, 8192),
+                                           (512, 72, 1003), (512, 768, 768), (500, 4096, 130), (512, 4096, 1040)])
+def test_forward_on_both_sides_of_the_rule(nss, rows, cols, out):
+    """Few rows by the kernels without tiles and by tiles, narrow and wide, with everything around the product."""
+    for dtype, act in ((torch.bfloat16, "silu"), (torch.float16, "none")):
+        g = _gen(rows + cols)
+        x, w = _rows(rows, cols, dtype, g), _rows(out, cols, dtype, g, std=cols ** -0.5)
+        r, b = _rows(rows, out, dtype, g), torch.randn(out, generator=g, device="cuda")
+        _check_forward(nss, x, w, b, r, act, None)
+
+
+@pytest.mark.parametrize("rows,cols,out,groups", [(64, 1024, 520, 3), (65, 1024, 520, 3), (64, 64, 8192, 8), (63, 256, 1000, 20),
+                                                  (64, 768, 1001, 64), (16, 768, 1000, 9), (9, 64, 8192, 30), (64, 2056, 64, 64)])
+def test_groups_on_both_sides_of_the_rule(nss, rows, cols, out, groups):
+    g, t = _gen(rows + groups), torch.bfloat16
+    sizes = torch.rand(groups, generator=g, device="cuda").cumsum(0)
+    ends = (sizes / sizes[-1] * (rows - 2)).int().tolist()
+    x, w = _rows(rows, cols, t, g), (torch.randn(groups, out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
+    x[ends[-1]:] = math.nan
+    b, r = torch.randn(groups, out, generator=g, device="cuda"), _rows(rows, out, t, g)
+    y, z = (torch.full((rows, out), 7.0, device="cuda", dtype=t) for _ in range(2))
+    _check_forward(nss, x, w, b, r, "gelu", ends, y=y, z=z)
+    assert not y[ends[-1]:].any() and not z[ends[-1]:].any()
