@@ -108,3 +108,47 @@ def test_groups_on_both_sides_of_the_rule(nss, rows, cols, out, groups):
     y, z = (torch.full((rows, out), 7.0, device="cuda", dtype=t) for _ in range(2))
     _check_forward(nss, x, w, b, r, "gelu", ends, y=y, z=z)
     assert not y[ends[-1]:].any() and not z[ends[-1]:].any()
+
+
+@pytest.mark.parametrize("rows", [300, 1024])
+@pytest.mark.parametrize("cols,out", [(64, 96), (768, 2816)])
+def test_forward_rows_of_any_shape(nss, rows, cols, out):
+    """Rows that are all one (a stride of 0), folded leading dimensions, every second row: by tiles as well as without them.
+    Kernels may add in another order: the tolerance is that of the sums."""
+    g, t = _gen(47), torch.bfloat16
+    w, x = _rows(out, cols, t, g, std=cols ** -0.5), _rows(2 * rows, cols, t, g)
+    _check_forward(nss, x[:1].expand(rows, cols), w, None, None, "relu2", None)
+    _check_forward(nss, x[::2], w, None, None, "gelu", None)
+    flat, _ = nss.mb_linear(x[:rows], w)
+    y, _ = nss.mb_linear(x[:rows].view(2, rows // 4, 2, cols), w)
+    assert y.shape == (2, rows // 4, 2, out) and torch.equal(y.view(rows, out), flat)
+    one, _ = nss.mb_linear(x[0], w)
+    _near(one[None], x[:1].double() @ w.double().T, _add(cols) * (x[:1].double().abs() @ w.double().abs().T))
+
+
+@pytest.mark.parametrize("rows,cols,out", [(1024, 256, 512), (2000, 768, 768)])
+def test_threads_with_products_by_tiles(nss, rows, cols, out):
+    """Calls of three host threads on streams of their own, forward and backward, by tiles."""
+    import threading
+    g, t = _gen(53), torch.bfloat16
+    x, w, dy = _rows(rows, cols, t, g), _rows(out, cols, t, g, std=cols ** -0.5), _rows(rows, out, t, g)
+    y, z = nss.mb_linear(x, w, activation="gelu", keep=True)
+    want = (y, z, *nss.mb_linear_backward(dy, x, w, z, "gelu", bias=True))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(100):
+                y, z = nss.mb_linear(x, w, activation="gelu", keep=True)
+                got = (y, z, *nss.mb_linear_backward(dy, x, w, z, "gelu", bias=True))
+        stream.synchronize()
+        wrong.extend(1 for a, b in zip(got, want) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong and nss.mb_sync_status() == 0
