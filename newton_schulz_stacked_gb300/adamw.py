@@ -1,8 +1,9 @@
 """AdamW over the tensors that are in no bank: embeddings, heads, norms, biases.
 
 adamw_multi_step steps a whole list in one launch; include/muonbank.h gives the formulas and the 8-bit
-moments' format.  The tensors are the caller's and are updated in place; they must be contiguous and may not
-overlap.  What is laid out otherwise, or has another size, type or device, is refused with ValueError before
+moments' format.  The tensors are the caller's and are updated in place; they must be contiguous, and what a
+call writes may not overlap anything else of it (gradients, which are only read, may share memory with one
+another).  What is laid out otherwise, or has another size, type or device, is refused with ValueError before
 anything is stepped; what the library refuses raises MuonBankError.
 """
 from __future__ import annotations

@@ -724,11 +724,12 @@ struct AdamwList {
   Tensor first;
   c10::Device device = c10::Device(c10::kCPU);
 
-  // The memory of one element's tensors that have been looked at.
+  // The memory of every tensor of the list, field by field; an empty one has none.
   struct Range {
-    uintptr_t begin, end;
-  } range[7];
-  int ranges = 0;
+    uintptr_t begin = 0, end = 0;
+  };
+  std::vector<Range> memory;
+  bool present[7] = {};
 
   static std::string name(int field, Py_ssize_t at) { return std::string(NAMES[field]) + " of tensor " + std::to_string(at); }
 
@@ -741,11 +742,11 @@ struct AdamwList {
     if (!t.is_contiguous()) throw Refused{name(field, at) + " must be contiguous"};
     if (field != 1) written.push_back(&t);
     void* p = t.data_ptr();
-    const Range r{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + static_cast<size_t>(n) * t.element_size()};
-    for (int i = 0; i < ranges; ++i)       // (all but the gradient are written)
-      if (r.begin < range[i].end && range[i].begin < r.end)
-        throw Refused{"tensors that the call writes overlap: " + name(field, at)};
-    range[ranges++] = r;
+    if (n > 0) {
+      const auto at_byte = reinterpret_cast<uintptr_t>(p);
+      memory[field * (memory.size() / 7) + at] = {at_byte, at_byte + static_cast<size_t>(n) * t.element_size()};
+      present[field] = true;
+    }
     return p;
   }
 
@@ -763,7 +764,6 @@ struct AdamwList {
     d.param_type = type_of(param, NAMES[0]);
     d.grad_type = type_of(grad, NAMES[1]);
     const auto none = ScalarType::Undefined;
-    ranges = 0;
     d.param = place(param, 0, at, d.n, param.scalar_type(), none);
     if (grad.sizes() != param.sizes()) throw Refused{name(1, at) + " is " + str(grad) + ", its parameter " + str(param)};
     d.grad = place(grad, 1, at, d.n, grad.scalar_type(), none);
@@ -788,16 +788,93 @@ struct AdamwList {
     descs.push_back(d);
   }
 
-  // A tensor that is given twice would be stepped by two CTAs at once.
-  void check_params() const {
-    const auto size = [](const mb_adamw_tensor& d) { return static_cast<size_t>(d.n) * (d.param_type == MB_F32 ? 4 : 2); };
-    std::vector<std::pair<uintptr_t, uintptr_t>> at;
-    at.reserve(descs.size());
-    for (const auto& d : descs)
-      if (d.n > 0) at.emplace_back(reinterpret_cast<uintptr_t>(d.param), reinterpret_cast<uintptr_t>(d.param) + size(d));
-    if (!std::is_sorted(at.begin(), at.end())) std::sort(at.begin(), at.end());
-    for (size_t i = 1; i < at.size(); ++i)
-      if (at[i].first < at[i - 1].second) throw Refused{"parameters of the call overlap"};
+  static Range range_of(const void* p, size_t bytes) {
+    const auto begin = reinterpret_cast<uintptr_t>(p);
+    return p ? Range{begin, begin + bytes} : Range{};
+  }
+
+  // What the call reads or writes beside the list.
+  struct Beside {
+    const char* name;
+    Range range;
+    bool written;
+  };
+
+  // One field's memory over the list: from the first byte to the last, and whether the tensors ascend (or descend) apart.
+  struct Field {
+    const Range* at;
+    Range whole;
+    bool up = true, down = true;
+    explicit Field(const Range* at_, size_t n) : at(at_) {
+      Range last;
+      for (size_t i = 0; i < n; ++i) {
+        const Range& r = at[i];
+        if (r.end == 0) continue;
+        if (last.end > 0) {
+          up &= r.begin >= last.end;
+          down &= r.end <= last.begin;
+        }
+        last = r;
+        whole.begin = whole.end == 0 ? r.begin : std::min(whole.begin, r.begin);
+        whole.end = std::max(whole.end, r.end);
+      }
+    }
+    // Whether two fields, each in order, share a byte.
+    bool meets(const Field& o, size_t n) const {
+      for (size_t i = 0, j = 0; i < n && j < n;) {
+        const Range &a = at[up ? i : n - 1 - i], &b = o.at[o.up ? j : n - 1 - j];
+        if (a.end <= b.begin || a.end == 0) ++i;
+        else if (b.end <= a.begin) ++j;
+        else return true;
+      }
+      return false;
+    }
+  };
+
+  // Nothing that the call writes may be in two places of it: two CTAs would step it at once.  (What is only read may.)  Where each
+  // field's tensors are in the order of their memory, as allocated in turn or cut from one buffer, the fields are compared
+  // side by side; else all are sorted (50 tensors of four fields: 1 and 2 us).
+  void check_memory(std::initializer_list<Beside> beside) const {
+    const size_t n = descs.size();
+    std::optional<Field> fields[7];
+    bool apart = true;
+    const auto clear = [](const Range& a, const Range& b) { return a.begin >= b.end || b.begin >= a.end; };
+    for (int f = 0; f < 7 && apart; ++f) {
+      if (!present[f]) continue;
+      const Field& w = fields[f].emplace(&memory[f * n], n);
+      apart = w.up || w.down;
+      for (int g = 0; g < f && apart; ++g)
+        if (fields[g] && !clear(fields[g]->whole, w.whole)) apart = !fields[g]->meets(w, n);
+      for (const Beside& b : beside)
+        if (!clear(b.range, w.whole))
+          for (size_t i = 0; i < n && apart; ++i) apart = clear(b.range, w.at[i]);
+    }
+    for (auto b = beside.begin(); b != beside.end(); ++b)
+      for (auto o = beside.begin(); o != b; ++o) apart = apart && clear(b->range, o->range);
+    if (apart) return;
+    // by first byte: what is written begins behind all before it, what is read behind all that is written
+    std::vector<std::pair<uintptr_t, size_t>> order;
+    order.reserve(memory.size() + beside.size());
+    const auto range = [&](size_t i) { return i < memory.size() ? memory[i] : beside.begin()[i - memory.size()].range; };
+    for (size_t i = 0; i < memory.size() + beside.size(); ++i)
+      if (range(i).end > 0) order.emplace_back(range(i).begin, i);
+    std::sort(order.begin(), order.end());
+    size_t last = 0, last_written = 0;     // of those so far, the ones that end last, as places in `order`
+    uintptr_t end = 0, end_written = 0;
+    const auto title = [&](size_t k) {
+      const size_t i = order[k].second;
+      return i < memory.size() ? name(static_cast<int>(i / n), static_cast<Py_ssize_t>(i % n))
+                               : std::string(beside.begin()[i - memory.size()].name);
+    };
+    for (size_t k = 0; k < order.size(); ++k) {
+      const size_t i = order[k].second;
+      const bool writes = i < memory.size() ? i / n != 1 : beside.begin()[i - memory.size()].written;
+      if (order[k].first < (writes ? end : end_written))
+        throw Refused{"memory that the call writes overlaps: " + title(writes ? last : last_written) + " and " + title(k)};
+      const uintptr_t e = range(i).end;
+      if (e > end) end = e, last = k;
+      if (writes) end_written = e, last_written = k;
+    }
   }
 
   explicit AdamwList(PyObject* list) {
@@ -810,6 +887,7 @@ struct AdamwList {
       if (n > MB_ADAMW_MAX_TENSORS) checked("adamw_multi_step", MB_ERR_TOO_MANY);
       descs.reserve(n);
       written.reserve(5 * n);
+      memory.resize(7 * n);
       held.reserve(n + 1);
       for (Py_ssize_t i = 0; i < n; ++i) {
         PyObject* item = PySequence_Fast_GET_ITEM(seq, i);
@@ -819,7 +897,6 @@ struct AdamwList {
         for (int k = 0; k < 9; ++k) f[k] = PyTuple_GET_ITEM(item, k);
         add(f, i);
       }
-      check_params();
     } catch (...) {
       release();
       throw;
@@ -873,6 +950,7 @@ PyObject* adamw(PyObject* const* a, Py_ssize_t n) {
       static_cast<const float*>(dense(tensor_or_none(a[7], "grad_scale"), "grad_scale", {1}, ScalarType::Float, list.device));
   int stochastic = 0;
   const uint32_t seed = seed_of(a[8], &stochastic);
+  list.check_memory({{"grad_scale", AdamwList::range_of(scale, 4), false}});
   checked("adamw_multi_step", unlocked([&] {
             return adamw_multi_step(list.descs.data(), static_cast<int>(list.descs.size()), lr, wd, beta1, beta2, eps, step,
                                     scale, stochastic, seed, where.stream);
@@ -896,6 +974,9 @@ PyObject* adamw_dev(PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   checked("adamw_multi_step_dev_workspace_bytes", adamw_multi_step_dev_workspace_bytes(count, &need));
   const Workspace ws(a[4], need, list.device);
+  list.check_memory({{"grad_scale", AdamwList::range_of(scale, 4), false},
+                     {"scalars", AdamwList::range_of(scalars, 48), false},
+                     {"workspace", AdamwList::range_of(ws.ptr, need), true}});
   checked("adamw_multi_step_dev", unlocked([&] {
             return adamw_multi_step_dev(list.descs.data(), count, scalars, scale, stochastic, seed, ws.ptr, ws.bytes,
                                         where.stream);
