@@ -55,8 +55,8 @@ def adamw_multi_step(tensors: Sequence[AdamState], lr: float, wd: float, beta1: 
                      eps: float = 1e-8, step: int = 1, grad_scale=None, seed: Optional[int] = None, stream=None) -> None:
     """One AdamW step of every tensor of the list, in place.
 
-    step counts from 1.  grad_scale, a CUDA float32 tensor of one value, multiplies every gradient (a clipping
-    factor).  With a seed (0 to 2^32 - 1) 8-bit moments are rounded at random, the same way for the same seed, step
+    step counts from 1.  grad_scale, a CUDA float32 tensor of one value (a scalar, or of shape [1]), multiplies every
+    gradient (a clipping factor).  With a seed (0 to 2^32 - 1) 8-bit moments are rounded at random, the same way for the same seed, step
     and place in the list; without one, to the nearest.
     """
     (_k._native or _k.load_binding()).adamw_multi_step(tensors, lr, wd, beta1, beta2, eps, step, grad_scale, seed, stream)

@@ -939,6 +939,14 @@ uint32_t seed_of(PyObject* o, int* stochastic) {
   return static_cast<uint32_t>(v);
 }
 
+// A clipping factor: one fp32 value, as a scalar tensor (what a norm gives) or of one dimension.
+const float* factor(PyObject* o, c10::Device device) {
+  const Tensor* t = tensor_or_none(o, "grad_scale");
+  const int64_t one = 1;
+  const c10::IntArrayRef shape(&one, t && t->dim() == 0 ? 0 : 1);
+  return static_cast<const float*>(dense(t, "grad_scale", shape, ScalarType::Float, device));
+}
+
 // tensors, lr, wd, beta1, beta2, eps, step, grad_scale, seed, stream
 PyObject* adamw(PyObject* const* a, Py_ssize_t n) {
   const AdamwList list(a[0]);
@@ -946,8 +954,7 @@ PyObject* adamw(PyObject* const* a, Py_ssize_t n) {
   if (a[9] != Py_None) list.record(where.stream);
   const double lr = real(a[1]), wd = real(a[2]), beta1 = real(a[3]), beta2 = real(a[4]), eps = real(a[5]);
   const long long step = integer(a[6], "step");
-  const auto* scale =
-      static_cast<const float*>(dense(tensor_or_none(a[7], "grad_scale"), "grad_scale", {1}, ScalarType::Float, list.device));
+  const float* scale = factor(a[7], list.device);
   int stochastic = 0;
   const uint32_t seed = seed_of(a[8], &stochastic);
   list.check_memory({{"grad_scale", AdamwList::range_of(scale, 4), false}});
@@ -966,8 +973,7 @@ PyObject* adamw_dev(PyObject* const* a, Py_ssize_t n) {
   if (a[5] != Py_None) list.record(where.stream);
   const auto* scalars =
       static_cast<const double*>(dense(&tensor(a[1], "scalars"), "scalars", {6}, ScalarType::Double, list.device));
-  const auto* scale =
-      static_cast<const float*>(dense(tensor_or_none(a[2], "grad_scale"), "grad_scale", {1}, ScalarType::Float, list.device));
+  const float* scale = factor(a[2], list.device);
   int stochastic = 0;
   const uint32_t seed = seed_of(a[3], &stochastic);
   const int count = static_cast<int>(list.descs.size());

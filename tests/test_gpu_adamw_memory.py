@@ -98,3 +98,21 @@ def test_memory_in_any_order(nss):
                     nss.adamw_multi_step(listed, LR, WD, grad_scale=factor)
             with pytest.raises(ValueError, match="grad_scale"):
                 nss.adamw_multi_step(states, LR, WD, grad_scale=states[5].exp_avg[63:])
+
+
+def test_a_scalar_clipping_factor(nss):
+    """What a norm gives has no dimension: the same step as from one value in a row, by value and from the device."""
+    states = [_state(nss, 3000, bits=b) for b in (32, 32, 32)]
+    factor = torch.full((2, 2), 0.25, device="cuda").norm()               # 0.5
+    assert factor.dim() == 0
+    scalars = torch.tensor([LR, WD, 0.9, 0.95, 1e-8, 4], dtype=torch.float64, device="cuda")
+    want = _expect(states[0], 0, 4, 0.5)
+    nss.adamw_multi_step([states[0]], LR, WD, 0.9, 0.95, 1e-8, 4, grad_scale=factor)
+    nss.adamw_multi_step([states[1]], LR, WD, 0.9, 0.95, 1e-8, 4, grad_scale=factor.reshape(1))
+    nss.adamw_multi_step_dev([states[2]], scalars, grad_scale=factor)
+    for s in states:
+        _check(s, want)
+    for bad in (torch.ones(2, device="cuda"), torch.ones(1, 1, device="cuda"), torch.ones((), device="cuda", dtype=torch.float64),
+                torch.ones(())):
+        with pytest.raises(ValueError, match="grad_scale"):
+            nss.adamw_multi_step(states, LR, WD, grad_scale=bad)
