@@ -589,15 +589,49 @@ c10::DimVector with(const c10::DimVector& lead, int64_t last) {
   return d;
 }
 
-// Results that begin where an input of the call, or another result, does.
-void apart(std::initializer_list<std::pair<const char*, const void*>> results,
-           std::initializer_list<std::pair<const char*, const void*>> inputs) {
+// Where a tensor of a call lies: rows of `width` bytes, `step` bytes apart.
+struct Place {
+  const char* name;
+  const void* at;          // or null: there is none
+  int64_t rows, width, step;
+  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(at); }
+  uintptr_t end() const { return begin() + static_cast<uintptr_t>((rows - 1) * step + width); }
+};
+Place place_of(const char* name, const void* at, int64_t rows, int64_t cols, int64_t stride, int64_t size = 2) {
+  return {name, rows > 0 && cols > 0 ? at : nullptr, rows, cols * size, stride * size};
+}
+Place bytes_at(const char* name, const void* at, size_t bytes) {
+  return {name, bytes > 0 ? at : nullptr, 1, static_cast<int64_t>(bytes), static_cast<int64_t>(bytes)};
+}
+
+// Whether any byte of one is a byte of the other.  Views of one buffer side by side are apart.
+bool overlap(const Place& a, const Place& b) {
+  if (!a.at || !b.at || a.begin() >= b.end() || b.begin() >= a.end()) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const Place &few = a.rows <= b.rows ? a : b, &many = a.rows <= b.rows ? b : a;
+  if (a.step == b.step && a.step >= a.width && a.step >= b.width) {
+    // columns of rows of one width: a's begin at 0, b's at d, and wrap around
+    const int64_t apart = static_cast<int64_t>(b.begin()) - static_cast<int64_t>(a.begin());
+    const int64_t d = (apart % a.step + a.step) % a.step;
+    return d < a.width || d + b.width > a.step;
+  }
+  for (int64_t i = 0; i < few.rows; ++i) {       // each row of one: the rows of the other that end past its begin
+    const auto lo = static_cast<int64_t>(few.begin() + i * few.step), hi = lo + few.width, at = static_cast<int64_t>(many.begin());
+    int64_t first = 0;
+    if (many.step > 0 && lo >= at + many.width) first = (lo - at - many.width) / many.step + 1;
+    if (first < many.rows && at + first * many.step < hi && at + first * many.step + many.width > lo) return true;
+  }
+  return false;
+}
+
+// Results that share memory with an input of the call, or with another result.
+void apart(std::initializer_list<Place> results, std::initializer_list<Place> inputs) {
   for (auto r = results.begin(); r != results.end(); ++r) {
-    if (!r->second) continue;
+    if (!r->at) continue;
     for (const auto& i : inputs)
-      if (r->second == i.second) throw Refused{std::string(r->first) + " may not be written over " + i.first};
+      if (overlap(*r, i)) throw Refused{std::string(r->name) + " may not be written over " + i.name};
     for (auto o = results.begin(); o != r; ++o)
-      if (r->second == o->second) throw Refused{std::string(r->first) + " may not be written over " + o->first};
+      if (overlap(*r, *o)) throw Refused{std::string(r->name) + " may not be written over " + o->name};
   }
 }
 
@@ -643,11 +677,16 @@ PyObject* linear(PyObject* const* a, Py_ssize_t n) {
   d.out = static_cast<int32_t>(s.out);
   d.groups = static_cast<int32_t>(s.groups);
   d.type = s.type;
-  apart({{"y", d.y}, {"z", d.z}}, {{"x", d.x}, {"weight", d.weight}, {"bias", d.bias}});
-  if (d.z) apart({{"z", d.z}}, {{"residual", d.residual}});
   size_t need = 0;
   checked("mb_linear_workspace_bytes", mb_linear_workspace_bytes(&d, &need));
   const Workspace ws(a[9], need, device);
+  const Place residual_at = place_of("residual", d.residual, s.rows, s.out, d.residual_stride);
+  const Place z_at = place_of("z", d.z, s.rows, s.out, d.z_stride), scratch = bytes_at("workspace", ws.ptr, need);
+  const bool over = d.y == d.residual && (d.y_stride == d.residual_stride || s.rows <= 1);      // each element over its own
+  apart({place_of("y", d.y, s.rows, s.out, d.y_stride), z_at, scratch},
+        {place_of("x", d.x, s.rows, s.in, d.x_stride), bytes_at("weight", d.weight, w.nbytes()),
+         bytes_at("bias", d.bias, bias ? bias->nbytes() : 0), bytes_at("ends", d.ends, s.groups * 4), over ? Place{} : residual_at});
+  if (over) apart({z_at, scratch}, {residual_at});
   checked("mb_linear", unlocked([&] { return mb_linear(&d, ws.ptr, ws.bytes, where.stream); }));
   return tuple(give(a[7], y), give(a[8], z));
 }
@@ -705,10 +744,14 @@ PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
   d.out = static_cast<int32_t>(s.out);
   d.groups = static_cast<int32_t>(s.groups);
   d.type = s.type;
-  apart({{"dx", d.dx}, {"dweight", d.dweight}, {"dbias", d.dbias}}, {{"dy", d.dy}, {"x", x.data_ptr()}, {"weight", d.weight}, {"z", d.z}});
   size_t need = 0;
   checked("mb_linear_backward_workspace_bytes", mb_linear_backward_workspace_bytes(&d, &need));
   const Workspace ws(a[12], need, device);
+  apart({place_of("dx", d.dx, s.rows, s.in, d.dx_stride), bytes_at("dweight", d.dweight, dw.defined() ? dw.nbytes() : 0),
+         bytes_at("dbias", d.dbias, db.defined() ? db.nbytes() : 0), bytes_at("workspace", ws.ptr, need)},
+        {place_of("dy", d.dy, s.rows, s.out, d.dy_stride), place_of("x", x.data_ptr(), s.rows, s.in, row_stride(x, "x")),
+         bytes_at("weight", d.weight, w.nbytes()), place_of("z", d.z, s.rows, s.out, d.z_stride),
+         bytes_at("ends", d.ends, s.groups * 4)});
   checked("mb_linear_backward", unlocked([&] { return mb_linear_backward(&d, ws.ptr, ws.bytes, where.stream); }));
   return tuple(give(a[9], dx), give(a[10], dw), give(a[11], db));
 }

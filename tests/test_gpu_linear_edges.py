@@ -152,3 +152,58 @@ def test_threads_with_products_by_tiles(nss, rows, cols, out):
     for th in threads:
         th.join()
     assert not wrong and nss.mb_sync_status() == 0
+
+
+def test_results_that_share_memory_are_refused(nss):
+    """Any shared byte, not only a shared first one; views side by side are none."""
+    t = torch.bfloat16
+    g = _gen(59)
+    buf, w = _rows(40, 192, t, g), _rows(64, 64, t, g, std=0.125)
+    x, side, last = buf[:20, :64], buf[:20, 64:128], buf[:20, 128:]
+    ends = torch.tensor([20], dtype=torch.int32, device="cuda")
+
+    def refused(call, *args, **more):
+        before = buf.clone()
+        with pytest.raises(ValueError, match="may not be written over"):
+            call(*args, **more)
+        torch.cuda.synchronize()
+        assert torch.equal(buf, before)
+
+    flat = buf.view(-1)
+    shifted = lambda n: flat[n:n + 20 * 192].view(20, 192)[:, :64]                         # noqa: E731
+    for y in (buf[1:21, :64], buf[:20, 63:127], buf[:20, 1:65], shifted(160), flat[64:64 + 20 * 64].view(20, 64),
+              buf[19:39, 10:74]):
+        refused(nss.mb_linear, x, w, y=y)
+        refused(nss.mb_linear, x.clone(), w, y=x, z=y)
+        refused(nss.mb_linear, x.clone(), w, residual=x, z=y)
+    for y in (side, last, buf[20:, :64], flat[20 * 192:20 * 192 + 20 * 64].view(20, 64)):
+        want, _ = nss.mb_linear(x.clone(), w)
+        nss.mb_linear(x, w, y=y)
+        assert torch.equal(y, want)
+    # the residual: over itself, element by element, and no other way
+    refused(nss.mb_linear, x, w, residual=side, y=buf[1:21, 64:128])
+    refused(nss.mb_linear, x, w, residual=flat[64:64 + 20 * 64].view(20, 64), y=side)
+    refused(nss.mb_linear, x, w, residual=side[:1].expand(20, 64), y=side)
+    one = last[0:1].expand(20, 64)                                                         # one row for all
+    nss.mb_linear(x, w, residual=one, y=side)
+    want, _ = nss.mb_linear(x, w, residual=side.clone())
+    nss.mb_linear(x, w, residual=side, y=side)
+    assert torch.equal(side, want)
+    # weights, biases, ends, workspaces
+    refused(nss.mb_linear, x, w, y=w[10:30])
+    many = torch.zeros(20 * 64 + 64, device="cuda", dtype=t)
+    refused(nss.mb_linear, x, w, many[20 * 64 - 8:20 * 64 + 56], y=many[:20 * 64].view(20, 64))
+    refused(nss.mb_linear, x, w[None], ends=many[20:22].view(torch.int32), y=many[:20 * 64].view(20, 64))
+    odd = flat[1:1 + 20 * 64].view(20, 64)                                                 # copied: a workspace
+    refused(nss.mb_linear, odd, w, workspace=buf.view(torch.uint8))
+    dy = torch.ones(20, 64, device="cuda", dtype=t)
+    refused(nss.mb_linear_backward, dy, x, w, dx=buf[1:21, :64])
+    refused(nss.mb_linear_backward, x, dy, w, dx=buf[:20, 32:96])
+    refused(nss.mb_linear_backward, dy, x, w, dweight=flat[100:100 + 64 * 64].view(64, 64))
+    refused(nss.mb_linear_backward, dy, x, w, dbias=flat[50:114])
+    refused(nss.mb_linear_backward, dy, x, w, dx=side, dbias=flat[70:134])
+    refused(nss.mb_linear_backward, dy, x, w, torch.ones_like(dy), "relu", workspace=buf.view(torch.uint8))
+    want, _, _ = nss.mb_linear_backward(dy, x, w)
+    nss.mb_linear_backward(dy, x, w, dx=side, dbias=flat[20 * 192:20 * 192 + 64])
+    assert torch.equal(side, want)
+    assert nss.mb_sync_status() == 0
