@@ -130,17 +130,25 @@ def route(logits, top_k: int, valid=None, normalize: bool = False) -> Routing:
 
 
 class _Linear(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, bias, residual, activation, ends):
-        keep = activation != "none" and any(ctx.needs_input_grad[:3])
-        y, z = _k.mb_linear(x, weight, bias, residual, activation, ends, keep=keep)
-        ctx.save_for_backward(x, weight, z, ends)
-        ctx.activation = activation
-        ctx.bias_dtype = None if bias is None else bias.dtype
-        return y
+    """y and z.  z leaves as a result of its own, which nobody sees: saved as one, it ties a second derivative, which reaches x,
+    weight and bias through it, to the graph without their values."""
 
     @staticmethod
-    def backward(ctx, dy):
+    def forward(ctx, x, weight, bias, residual, activation, ends):
+        want = ctx.needs_input_grad
+        keep = activation != "none" and any(want[:3])
+        y, z = _k.mb_linear(x, weight, bias, residual, activation, ends, keep=keep)
+        # dweight alone reads x, dx alone the weight: what no wanted gradient reads is neither kept nor held to its values
+        ctx.save_for_backward(x if want[1] else None, weight if want[0] else None, z, ends)
+        ctx.activation = activation
+        ctx.bias = None if bias is None else (bias.shape, bias.dtype)
+        ctx.set_materialize_grads(False)
+        return y, z
+
+    @staticmethod
+    def backward(ctx, dy, _dz):
+        if dy is None:
+            return None, None, None, None, None, None
         x, weight, z, ends = ctx.saved_tensors
         want = ctx.needs_input_grad
         grads = (None, None, None)
@@ -148,7 +156,8 @@ class _Linear(torch.autograd.Function):
             def call(dy, x, weight, z, ends):
                 dbias = None
                 if want[2]:
-                    dbias = torch.empty(weight.shape[:-1], dtype=ctx.bias_dtype, device=weight.device)
+                    shape, dtype = ctx.bias
+                    dbias = torch.empty(shape, dtype=dtype, device=dy.device)
                 return _k.mb_linear_backward(dy, x, weight, z, ctx.activation, ends, input_grad=want[0], weight_grad=want[1],
                                              dbias=dbias)
             grads = _first_only("linear", call, dy.resolve_neg().contiguous(), x, weight, z, ends)
@@ -168,4 +177,4 @@ def linear(x, weight, bias=None, residual=None, activation: str = "none", ends=N
 
     A backward pass can be captured into a CUDA graph; as with torch's own functions not while another graph of the same
     leaves, made on another stream, is alive (capture then ends with an error)."""
-    return _Linear.apply(x, weight, bias, residual, activation, ends)
+    return _Linear.apply(x, weight, bias, residual, activation, ends)[0]

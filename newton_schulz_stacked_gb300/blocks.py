@@ -131,7 +131,8 @@ def mb_linear_backward(dy, x, weight, z=None, activation: str = "none", ends=Non
                        stream=None):
     """Gradients of mb_linear: (dx, dweight, dbias), None for those that are not wanted (input_grad, weight_grad, bias).
 
-    z is the forward call's (not needed without an activation).  dweight is laid out as the weight, the gradient of a bank as
+    z is the forward call's (not needed without an activation).  x is read for dweight only, weight for dx only: either may be
+    None where that gradient is not wanted.  dweight is laid out as the weight, the gradient of a bank as
     muon_multi_step takes it; dbias comes in x's type unless a float32 one is passed.  The residual's gradient is dy.  No result may overlap an input.
     """
     return (_native or load_binding()).mb_linear_backward(dy, x, weight, z, activation, ends, input_grad, weight_grad, bias,

@@ -556,30 +556,44 @@ struct LinearShape {
   c10::DimVector param;       // of a bias
 };
 
-LinearShape linear_shape(const Tensor& x, const Tensor& w, PyObject* ends) {
+// Of x and w; in a backward call one of them may be absent, and dy stands in for what it would say.
+LinearShape linear_shape(const Tensor* x, const Tensor* w, PyObject* ends, const Tensor* dy = nullptr) {
   LinearShape s{};
-  if (x.dim() < 1) throw Refused{"x must have at least one dimension"};
-  if (w.dim() != 2 && w.dim() != 3) throw Refused{"weight must be [out, in], or [groups, out, in] with ends"};
-  if (x.scalar_type() != ScalarType::BFloat16 && x.scalar_type() != ScalarType::Half)
-    throw Refused{std::string("x has dtype ") + c10::toString(x.scalar_type()) + ", expected bfloat16 or float16"};
-  s.type = type_of(x, "x");
-  const auto wn = w.sizes();
-  s.in = wn[w.dim() - 1];
-  s.out = wn[w.dim() - 2];
-  s.groups = w.dim() == 3 ? wn[0] : 1;
-  if (s.in == 0 || s.out == 0 || s.groups == 0) throw Refused{"weight has no elements"};
-  if (s.in > 1 << 20 || s.out > 1 << 20 || s.groups > 1024) checked("mb_linear", MB_ERR_SHAPE);
-  if (x.sizes().back() != s.in)
-    throw Refused{"x is " + str(x) + ", its last dimension must be the weight's " + std::to_string(s.in)};
-  dense(&w, "weight", wn, x.scalar_type(), x.device());
-  s.rows = x.numel() / s.in;
-  if (s.rows > 1ll << 30) checked("mb_linear", MB_ERR_SHAPE);
-  s.lead.assign(x.sizes().begin(), x.sizes().end() - 1);
+  const Tensor& rows = x ? *x : *dy;
+  const char* const rows_name = x ? "x" : "dy";
+  if (rows.dim() < 1) throw Refused{std::string(rows_name) + " must have at least one dimension"};
+  if (w && w->dim() != 2 && w->dim() != 3) throw Refused{"weight must be [out, in], or [groups, out, in] with ends"};
+  if (rows.scalar_type() != ScalarType::BFloat16 && rows.scalar_type() != ScalarType::Half)
+    throw Refused{std::string(rows_name) + " has dtype " + c10::toString(rows.scalar_type()) + ", expected bfloat16 or float16"};
+  s.type = type_of(rows, rows_name);
   const Tensor* e = tensor_or_none(ends, "ends");
-  if ((e != nullptr) != (w.dim() == 3))
+  if (w) {
+    const auto wn = w->sizes();
+    s.in = wn[w->dim() - 1];
+    s.out = wn[w->dim() - 2];
+    s.groups = w->dim() == 3 ? wn[0] : 1;
+    if (s.in == 0 || s.out == 0 || s.groups == 0) throw Refused{"weight has no elements"};
+    s.param.assign(wn.begin(), wn.end() - 1);
+  } else {
+    if (dy->dim() < 1) throw Refused{"dy must have at least one dimension"};
+    s.in = x ? x->sizes().back() : 1;
+    s.out = dy->sizes().back();
+    s.groups = e ? e->numel() : 1;
+    if (s.in == 0 || s.out == 0 || s.groups == 0) throw Refused{"the weight would have no elements"};
+    if (e) s.param.push_back(s.groups);
+    s.param.push_back(s.out);
+  }
+  if (s.in > 1 << 20 || s.out > 1 << 20 || s.groups > 1024) checked("mb_linear", MB_ERR_SHAPE);
+  const int64_t last = x ? s.in : s.out;
+  if (rows.sizes().back() != last)
+    throw Refused{std::string(rows_name) + " is " + str(rows) + ", its last dimension must be the weight's " + std::to_string(last)};
+  if (w) dense(w, "weight", w->sizes(), rows.scalar_type(), rows.device());
+  s.rows = rows.numel() / last;
+  if (s.rows > 1ll << 30) checked("mb_linear", MB_ERR_SHAPE);
+  s.lead.assign(rows.sizes().begin(), rows.sizes().end() - 1);
+  if (w && (e != nullptr) != (w->dim() == 3))
     throw Refused{e ? "ends needs a weight of [groups, out, in]" : "a weight of [groups, out, in] needs ends"};
-  if (e) s.ends = static_cast<const int32_t*>(dense(e, "ends", {s.groups}, ScalarType::Int, x.device()));
-  s.param.assign(wn.begin(), wn.end() - 1);
+  if (e) s.ends = static_cast<const int32_t*>(dense(e, "ends", {s.groups}, ScalarType::Int, rows.device()));
   return s;
 }
 
@@ -641,7 +655,7 @@ PyObject* linear(PyObject* const* a, Py_ssize_t n) {
   const auto device = x.device();
   const auto dtype = x.scalar_type();
   Where where(x, a[10], a, n);
-  const LinearShape s = linear_shape(x, w, a[5]);
+  const LinearShape s = linear_shape(&x, &w, a[5]);
   const auto shape = with(s.lead, s.out);
   mb_linear_desc d{};
   d.activation = activation_of(a[4]);
@@ -694,12 +708,18 @@ PyObject* linear(PyObject* const* a, Py_ssize_t n) {
 // dy, x, weight, z, activation, ends, input_grad, weight_grad, bias (whether its gradient is wanted), dx, dweight, dbias,
 // workspace, stream
 PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
-  const Tensor &x = cuda_tensor(a[1], "x"), &w = tensor(a[2], "weight"), &dy = tensor(a[0], "dy");
-  const auto device = x.device();
-  const auto dtype = x.scalar_type();
-  Where where(x, a[13], a, n);
-  const LinearShape s = linear_shape(x, w, a[5]);
+  const Tensor& dy = cuda_tensor(a[0], "dy");
+  const Tensor *x = tensor_or_none(a[1], "x"), *w = tensor_or_none(a[2], "weight");
+  const auto device = dy.device();
+  const auto dtype = dy.scalar_type();
+  Where where(dy, a[13], a, n);
+  const bool want_dx = a[9] != Py_None || truth(a[6]), want_dw = a[10] != Py_None || truth(a[7]);
+  if (want_dx && !w) throw Refused{"the gradient of x needs the weight"};
+  if (want_dw && !x) throw Refused{"the gradient of the weight needs x"};
+  const LinearShape s = linear_shape(x, w, a[5], &dy);
   const auto shape = with(s.lead, s.out);
+  if (x && (x->device() != device || x->scalar_type() != dtype))
+    throw Refused{"x is " + str(*x) + ", dy " + str(dy) + ": expected one type and device"};
   mb_linear_backward_desc d{};
   d.activation = activation_of(a[4]);
   like(dy, "dy", shape, dtype, device);
@@ -713,14 +733,17 @@ PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
     d.z_stride = row_stride(*z, "z");
   }
   Tensor dx, dw, db;
-  if (a[9] != Py_None || truth(a[6])) {
-    dx = result(a[9], "dx", x.sizes(), dtype, device);
+  if (want_dx) {
+    dx = result(a[9], "dx", with(s.lead, s.in), dtype, device);
     d.dx = dx.data_ptr();
     d.dx_stride = row_stride(dx, "dx");
   }
-  if (a[10] != Py_None || truth(a[7])) {
-    dw = result(a[10], "dweight", w.sizes(), dtype, device);
-    d.dweight = dense(&dw, "dweight", w.sizes(), dtype, device);
+  if (want_dw) {
+    const auto matrices = with(s.param, s.in);
+    dw = result(a[10], "dweight", matrices, dtype, device);
+    d.dweight = dense(&dw, "dweight", matrices, dtype, device);
+    d.x = x->data_ptr();
+    d.x_stride = row_stride(*x, "x");
   }
   d.bias_type = s.type;
   if (a[11] != Py_None || truth(a[8])) {
@@ -733,11 +756,7 @@ PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
     db = result(a[11], "dbias", s.param, type, device);
     d.dbias = dense(&db, "dbias", s.param, type, device);
   }
-  if (d.dweight) {
-    d.x = x.data_ptr();
-    d.x_stride = row_stride(x, "x");
-  }
-  d.weight = w.data_ptr();
+  if (want_dx) d.weight = w->data_ptr();
   d.ends = s.ends;
   d.rows = s.rows;
   d.in = static_cast<int32_t>(s.in);
@@ -749,8 +768,8 @@ PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
   const Workspace ws(a[12], need, device);
   apart({place_of("dx", d.dx, s.rows, s.in, d.dx_stride), bytes_at("dweight", d.dweight, dw.defined() ? dw.nbytes() : 0),
          bytes_at("dbias", d.dbias, db.defined() ? db.nbytes() : 0), bytes_at("workspace", ws.ptr, need)},
-        {place_of("dy", d.dy, s.rows, s.out, d.dy_stride), place_of("x", x.data_ptr(), s.rows, s.in, row_stride(x, "x")),
-         bytes_at("weight", d.weight, w.nbytes()), place_of("z", d.z, s.rows, s.out, d.z_stride),
+        {place_of("dy", d.dy, s.rows, s.out, d.dy_stride), place_of("x", d.x, s.rows, s.in, d.x_stride),
+         bytes_at("weight", d.weight, want_dx ? w->nbytes() : 0), place_of("z", d.z, s.rows, s.out, d.z_stride),
          bytes_at("ends", d.ends, s.groups * 4)});
   checked("mb_linear_backward", unlocked([&] { return mb_linear_backward(&d, ws.ptr, ws.bytes, where.stream); }));
   return tuple(give(a[9], dx), give(a[10], dw), give(a[11], db));
