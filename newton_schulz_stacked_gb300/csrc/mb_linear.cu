@@ -4,7 +4,8 @@
 // Pairs of CTAs compute tiles of 256 rows x 256 (or 128) columns with M = 256 tcgen05 MMAs (cta_group::2): CTA r of a
 // pair holds rows 128 r .. of the A operand and half of the B operand's, staged by TMA with 128-byte swizzle in 64-deep
 // blocks, and receives its 128 rows x all columns of the fp32 sums in TMEM (two accumulators, so that one tile's epilogue
-// runs under the next one's MMAs).  An operand whose contraction runs along memory is staged K-major, one box a block;
+// runs under the next one's MMAs).  Where dz comes in two halves (LOW) each has an accumulator of its own, and the epilogue adds
+// them.  An operand whose contraction runs along memory is staged K-major, one box a block;
 // the others (W in dx, both in dW) as boxes of 64 x 64 in MN-major layout.
 //
 // The units are dealt to the pairs in turn (Deal); the roles find them themselves from the groups' first rows and tiles, which
@@ -117,7 +118,6 @@ __device__ __forceinline__ void decode_same(const LinearParams& P, const Groups&
   u.wide = same(u.wide);
   u.k_begin = same(u.k_begin);
   u.k_end = same(u.k_end);
-  u.blocks = same(u.blocks);
   u.kb0 = same(u.kb0);
   u.kb1 = same(u.kb1);
 }
@@ -133,7 +133,8 @@ enum : uint32_t {
   NOTE_NOTHING = 4,        // a unit without blocks: no MMAs
   NOTE_PAST = 8,           // reaches past its group: wait until it is cleared
   NOTE_A_MN = 16,
-  NOTE_B_MN = 32
+  NOTE_B_MN = 32,
+  NOTE_SECOND = 64         // the second pass begins: other sums, anew
 };
 
 // The block of a pass that reaches into the next group's rows (the last, or none: INT_MAX).
@@ -217,8 +218,10 @@ __device__ void side_work(const LinearParams& P, const Groups& G, long long me, 
   }
 }
 
-template <bool FORWARD, typename T>
+template <bool FORWARD, typename T, bool LOW>
 __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constant__ LinearParams P) {
+  constexpr int PASSES = LOW ? 2 : 1;
+  constexpr int TURNS = LOW ? 1 : 2;           // tiles whose sums TMEM holds
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -304,16 +307,17 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       const LinearJob& J = P.job[u.job];
       const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
       const uint32_t flags = (J.a_mn ? NOTE_A_MN : 0u) | (J.b_mn ? NOTE_B_MN : 0u) | (u.kb0 < u.kb1 ? 0u : NOTE_NOTHING);
-      const int kb0 = u.kb0, kb1 = max(u.kb1, kb0 + 1);        // a unit without blocks takes a stage for its note
-      const bool await = !FORWARD && for_a && P.ahead.next && !(flags & NOTE_NOTHING);   // dz is still being made
+      // (a unit without blocks takes a stage for its note)
+      const int blocks = max((u.kb1 - u.kb0) * PASSES, 1);
+      const bool await = !FORWARD && !LOW && for_a && P.ahead.next && !(flags & NOTE_NOTHING);   // dz is still being made
       if (await && !J.over_rows) {
         const int row = u.m0 + static_cast<int>(rank) * BM;
         ok = seen.rows(P.ahead, row, min(row + BM, u.m_end), lane, abort_flag);
         if (!ok) break;
       }
-      int at_block = kb0 < u.blocks ? kb0 : kb0 - u.blocks;                // of its pass
-      int x = f.x + at_block * f.x_step + (kb0 < u.blocks ? 0 : f.pass_cols), y = f.y + at_block * f.y_step;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      int at_block = u.kb0;                        // of its pass
+      int x = f.x + at_block * f.x_step, y = f.y + at_block * f.y_step;
+      for (int left = blocks; left > 0; --left, ++it) {
         if (it >= stages) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag));
           if (!ok) break;
@@ -328,8 +332,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         if (elect_lane()) {
           if (for_a) {
             if (even) {
-              notes[st] = BlockNote{idesc, flags | (kb == kb0 ? NOTE_FIRST : 0u) | (kb == kb1 - 1 ? NOTE_LAST : 0u) |
-                                               (past_end ? NOTE_PAST : 0u)};
+              notes[st] = BlockNote{idesc, flags | (left == blocks ? NOTE_FIRST : LOW && at_block == u.kb0 ? NOTE_SECOND : 0u) |
+                                               (left == 1 ? NOTE_LAST : 0u) | (past_end ? NOTE_PAST : 0u)};
               if (past_end || nothing) mbar_arrive(&full[st]);
               else mbar_expect_tx(&full[st], 2u * f.bytes);
             }
@@ -343,10 +347,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         __syncwarp();
         x += f.x_step;
         y += f.y_step;
-        if (++at_block == u.blocks) {              // the next pass
-          at_block = 0;
-          x = f.x + f.pass_cols;
-          y = f.y;
+        ++at_block;
+        if (LOW && at_block == u.kb1) {            // the next pass
+          at_block = u.kb0;
+          x = f.x + at_block * f.x_step + f.pass_cols;
+          y = f.y + at_block * f.y_step;
         }
         if (++st == stages) {
           st = 0;
@@ -381,11 +386,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
           b_step = (flags & NOTE_B_MN ? 2048u : 32u) >> 4;
           a_desc = desc | static_cast<uint64_t>((flags & NOTE_A_MN ? BOX_BYTES : 16) >> 4) << 16;
           b_desc = desc | static_cast<uint64_t>((flags & NOTE_B_MN ? BOX_BYTES : 16) >> 4) << 16;
-          dacc = tmem + (k & 1) * ACC_COLS;
-          if (k >= 2) {
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&tempty[k & 1], ((k >> 1) - 1) & 1, abort_flag));
+          dacc = tmem + k % TURNS * ACC_COLS;
+          if (k >= TURNS) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&tempty[k % TURNS], (k / TURNS - 1) & 1, abort_flag));
             if (!ok) break;
           }
+        } else if (LOW && (flags & NOTE_SECOND)) {
+          dacc += ACC_COLS;
         }
         if (flags & NOTE_PAST) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&cleared[st], (past_phase >> st) & 1u, abort_flag));
@@ -398,10 +405,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
           if (!(flags & NOTE_NOTHING)) {
 #pragma unroll
             for (int kk = 0; kk < LINEAR_DEEP / 16; ++kk)
-              umma_bf16_pair(dacc, a0 + kk * a_step, b0 + kk * b_step, idesc, (flags & NOTE_FIRST) && kk == 0 ? 0u : 1u);
+              umma_bf16_pair(dacc, a0 + kk * a_step, b0 + kk * b_step, idesc,
+                             (flags & (LOW ? NOTE_FIRST | NOTE_SECOND : NOTE_FIRST)) && kk == 0 ? 0u : 1u);
           }
           umma_commit_pair_both(&empty[st]);   // the stage may be refilled in both CTAs
-          if (flags & NOTE_LAST) umma_commit_pair_both(&tfull[k & 1]);
+          if (flags & NOTE_LAST) umma_commit_pair_both(&tfull[k % TURNS]);
         }
         __syncwarp();
         if (flags & NOTE_LAST) ++k;
@@ -421,13 +429,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       Unit u;
       decode_unit(P, G, first_units, deal(i), u);
       const LinearJob& J = P.job[u.job];
-      const int blocks = max(u.kb1 - u.kb0, 1);                  // (without blocks: a stage for the note)
+      const int part = u.kb1 - u.kb0, blocks = max(part * PASSES, 1);     // (without blocks: a stage for the note)
       const int past = past_from(P, J, u);
       bool ok = true;
-      for (int pass = 0; pass < J.passes && past < u.blocks && ok; ++pass) {
-        const int kb = pass * u.blocks + past;
-        if (kb < u.kb0 || kb >= u.kb1) continue;
-        const int st = (it + kb - u.kb0) % stages;
+      for (int pass = 0; pass < PASSES && past >= u.kb0 && past < u.kb1; ++pass) {
+        const int st = (it + pass * part + past - u.kb0) % stages;
         ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&past_bar[st], (past_phase >> st) & 1u, abort_flag));
         if (!ok) break;
         past_phase ^= 1u << st;
@@ -459,12 +465,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
     const uint32_t tempty_even = map_to_rank(&tempty[0], 0);
     side_work<T>(P, G, static_cast<long long>(blockIdx.x) * EPI_WARPS + ew, static_cast<long long>(gridDim.x) * EPI_WARPS, lane);
     // the piece of dz that this warp has claimed (none from `pieces` on)
-    const int pieces = !FORWARD && P.ahead.next ? P.ahead.ways * P.ahead.per_way * P.ahead.column_groups : 0;
+    const int pieces = !FORWARD && !LOW && P.ahead.next ? P.ahead.ways * P.ahead.per_way * P.ahead.column_groups : 0;
     int piece = pieces > 0 ? claim_piece(P.ahead.next, lane) : 0;
     for (int k = 0; k < mine || piece < pieces; ++k) {
       // pieces while no sums are ready, each claimed under the work on the one before
       while (piece < pieces &&
-             !(k < mine && __all_sync(0xffffffffu, mbar_test(&tfull[k & 1], (k >> 1) & 1))) &&
+             !(k < mine && __all_sync(0xffffffffu, mbar_test(&tfull[k % TURNS], (k / TURNS) & 1))) &&
              !__any_sync(0xffffffffu, *abort_flag)) {
         const int now = piece;
         piece = claim_piece(P.ahead.next, lane);
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       Unit u;
       decode_unit(P, G, first_units, deal(k), u);
       const LinearJob& J = P.job[u.job];
-      const int buf = k & 1;
+      const int buf = k % TURNS;
       w.row0 = u.m0 + static_cast<int>(rank) * BM + quad * 32;
       w.rows = min(32, u.m_end - w.row0);
       float2 bias[2] = {};
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         bias[0] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * half, lane);
         bias[1] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * (half + 2), lane);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&tfull[buf], (k >> 1) & 1, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&tfull[buf], (k / TURNS) & 1, abort_flag))) {
         fail();
         break;
       }
@@ -506,6 +512,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         if (u.kb0 == u.kb1) {                                // without blocks the accumulator holds another tile
 #pragma unroll
           for (int i = 0; i < CHUNK_COLS / 2; ++i) v.v[i] = make_float2(0.f, 0.f);
+        } else if (LOW) {
+          // what dz's rounding left, but where the sums without it are no numbers: zero times infinity is none
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+            tmem_ld_32x32(tacc + ACC_COLS + CHUNK_COLS * c + 32 * h, r[0]);
+            tmem_ld_ready(r[0]);
+#pragma unroll
+            for (int i = 0; i < CHUNK_COLS / 4; ++i) {
+              float2& s = v.v[CHUNK_COLS / 4 * h + i];
+              s.x = isfinite(s.x) ? s.x + __uint_as_float(r[0][2 * i]) : s.x;
+              s.y = isfinite(s.y) ? s.y + __uint_as_float(r[0][2 * i + 1]) : s.y;
+            }
+          }
         }
         if (J.splits > 1) {
           float4* part = part_of(J, u, u.split, rank, ew, c >> 1);
@@ -598,7 +618,7 @@ __global__ void __launch_bounds__(32 * JOIN_WAYS) linear_join_kernel(const __gri
 
 // Per-device set-up (the shared-memory limit, the number of pairs that can be resident) is done by the first call on each
 // device; concurrent first calls do the same idempotent work.
-template <bool FORWARD, typename T>
+template <bool FORWARD, typename T, bool LOW>
 cudaError_t launch_form(const LinearParams& p, int pairs_wanted, cudaStream_t s) {
   static std::atomic<int> resident[64];
   int dev = 0;
@@ -607,7 +627,7 @@ cudaError_t launch_form(const LinearParams& p, int pairs_wanted, cudaStream_t s)
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int most = resident[dev].load(std::memory_order_acquire);
   if (most == 0) {
-    e = cudaFuncSetAttribute(linear_kernel<FORWARD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    e = cudaFuncSetAttribute(linear_kernel<FORWARD, T, LOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
@@ -620,13 +640,13 @@ cudaError_t launch_form(const LinearParams& p, int pairs_wanted, cudaStream_t s)
     cfg.dynamicSmemBytes = SMEM;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&most, linear_kernel<FORWARD, T>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&most, linear_kernel<FORWARD, T, LOW>, &cfg);
     if (e != cudaSuccess) return e;
     if (most <= 0) return cudaErrorInvalidConfiguration;
     resident[dev].store(most, std::memory_order_release);
   }
   const int pairs = pairs_wanted < most ? pairs_wanted : most;
-  return launch_after(linear_kernel<FORWARD, T>, dim3(2 * pairs), dim3(THREADS), SMEM, s, p, 2);
+  return launch_after(linear_kernel<FORWARD, T, LOW>, dim3(2 * pairs), dim3(THREADS), SMEM, s, p, 2);
 }
 
 template <bool FORWARD, typename T>
@@ -646,9 +666,14 @@ cudaError_t launch_join_form(const LinearParams& p, int job, long long tiles, cu
 }  // namespace
 
 cudaError_t launch_linear(const LinearParams& p, int type, bool forward, int pairs_wanted, cudaStream_t s) {
+  const bool low = p.jobs > 0 && p.job[0].passes > 1;      // (both jobs contract dz)
   if (type == MB_BF16)
-    return forward ? launch_form<true, __nv_bfloat16>(p, pairs_wanted, s) : launch_form<false, __nv_bfloat16>(p, pairs_wanted, s);
-  return forward ? launch_form<true, __half>(p, pairs_wanted, s) : launch_form<false, __half>(p, pairs_wanted, s);
+    return forward ? launch_form<true, __nv_bfloat16, false>(p, pairs_wanted, s)
+           : low   ? launch_form<false, __nv_bfloat16, true>(p, pairs_wanted, s)
+                   : launch_form<false, __nv_bfloat16, false>(p, pairs_wanted, s);
+  return forward ? launch_form<true, __half, false>(p, pairs_wanted, s)
+         : low   ? launch_form<false, __half, true>(p, pairs_wanted, s)
+                 : launch_form<false, __half, false>(p, pairs_wanted, s);
 }
 
 cudaError_t launch_linear_join(const LinearParams& p, int job, int type, bool forward, long long tiles, cudaStream_t s) {

@@ -68,8 +68,7 @@ struct Unit {
   int m0, m_end;           // D's rows: the tile's first, and where the group's (or matrix's) end
   int n0, wide;            // D's columns
   int k_begin, k_end;      // over_rows: the group's rows
-  int blocks;              // of 64 of the contraction, once
-  int kb0, kb1;            // the unit's part of them, counted through the passes
+  int kb0, kb1;            // the unit's blocks of 64 of the contraction (the same in each pass)
 };
 
 // (the host refuses what 31 bits cannot number: a division of 64 bits takes a role longer than a block's MMAs)
@@ -108,8 +107,6 @@ __device__ __forceinline__ void decode_tile(const LinearJob& J, const Groups& G,
   // the last columns' tile is as narrow as its operand's layout allows
   const int left = J.N - u.n0, step = J.b_mn ? 128 : 64;
   u.wide = min(J.wide, (left + step - 1) & -step);
-  u.blocks = blocks;
-  blocks *= J.passes;
   u.kb0 = 0;
   u.kb1 = blocks;
   if (J.splits > 1) {                            // (blocks < 2^25, splits < 2^5)

@@ -25,7 +25,7 @@ struct LinearJob {
   int N, K;                // D's columns; the contraction (not over_rows)
   int wide;                // 128 or 256
   int m_tiles, n_tiles;    // m_tiles: over_rows only
-  int passes, pass_cols;   // 2: the A operand comes as two halves, the second pass_cols columns on, and the contraction runs twice
+  int passes, pass_cols;   // 2: the A operand comes as two halves, the second pass_cols columns on: each has sums of its own
   int splits;              // parts of the contraction
   int access;              // bytes that D's rows allow to be stored at a time: 16, 4 or 2
   void* out;

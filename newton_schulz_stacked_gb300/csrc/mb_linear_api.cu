@@ -219,8 +219,7 @@ BackwardPlan plan_backward(const mb_linear_backward_desc& d) {
   const bool products = d.dx || d.dweight;
   p.slope = d.activation != MB_ACT_NONE;
   if (p.slope) {
-    // The products take dz rounded to 16 bits, half a step in every term; the smallest calls take it in two halves.  (An infinite
-    // weight or x then meets a half of 0: NaN where the sum would be infinite.)
+    // The products take dz rounded to 16 bits, half a step in every term; the smallest calls take it in two halves.
     p.low = d.rows * (d.in < d.out ? d.in : d.out) <= TWO_HALVES ? static_cast<int>(up(d.out, LINEAR_DEEP)) : 0;
     const int64_t width = p.low ? p.low + d.out : d.out;
     p.dz = Operand{nullptr, p.low ? 2 * p.low : up(width, 8), false, 0, d.rows, width, nullptr, 0};

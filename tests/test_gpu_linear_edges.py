@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_linear import ACTS, _add, _check_forward, _gen, _near, _rows, _slope, nss  # noqa: F401
+from test_gpu_linear import ACTS, TYPES, _add, _bounds, _check_forward, _gen, _near, _rows, _slope, nss  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -207,3 +207,27 @@ def test_results_that_share_memory_are_refused(nss):
     nss.mb_linear_backward(dy, x, w, dx=side, dbias=flat[20 * 192:20 * 192 + 64])
     assert torch.equal(side, want)
     assert nss.mb_sync_status() == 0
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+@pytest.mark.parametrize("rows,cols,out,groups", [(1, 64, 64, 0), (2, 1000, 72, 0), (30, 65, 130, 0), (1, 8, 20000, 0), (2, 20008, 3, 0),
+                                                  (24, 64, 96, 3), (300, 64, 96, 0), (600, 136, 200, 3)])
+def test_infinite_operands_of_the_gradient(nss, dtype, act, rows, cols, out, groups):
+    """An infinity in x or in a weight makes its sums infinite, and NaN only where the formula has it, with dz in two halves (the
+    smallest calls) as in one."""
+    g, t = _gen(rows + cols), TYPES[dtype]
+    n = max(groups, 1)
+    x, dy, z = _rows(rows, cols, t, g), _rows(rows, out, t, g), _rows(rows, out, t, g).abs_().add_(0.5)
+    w = (torch.randn(n, out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
+    dy[0, ::2] = 1.0                             # some of dz fit 16 bits as they are: nothing is left of them
+    z[0, ::2] = 2.0
+    x[0, 1], x[rows // 2, cols - 1], w[0, 1, 0], w[0, out // 2, cols // 2] = math.inf, -math.inf, math.inf, -math.inf
+    ends = [rows // 3, rows // 3, rows - 1] if groups else None
+    dev = torch.tensor(ends, dtype=torch.int32, device="cuda") if groups else None
+    dx, dw, _ = nss.mb_linear_backward(dy, x, w if groups else w[0], z, act, dev)
+    for i, (a, e) in enumerate(_bounds(ends, rows)):
+        D, X, W = dy[a:e].double() * _slope(z[a:e].double(), act), x[a:e].double(), w[i].double()
+        for got, want in ((dx[a:e], D @ W), (dw[i] if groups else dw, D.T @ X)):
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+            assert torch.equal(got[got.isinf()].double(), want[want.isinf()])
