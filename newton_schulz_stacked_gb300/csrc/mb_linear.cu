@@ -130,7 +130,7 @@ struct BlockNote {
 enum : uint32_t {
   NOTE_FIRST = 1,          // of its unit: the accumulator starts anew
   NOTE_LAST = 2,
-  NOTE_NOTHING = 4,        // a unit without blocks: no MMAs
+  NOTE_NOTHING = 4,        // a unit without blocks, one of zeros in their place: no MMAs
   NOTE_PAST = 8,           // reaches past its group: wait until it is cleared
   NOTE_A_MN = 16,
   NOTE_B_MN = 32,
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       const LinearJob& J = P.job[u.job];
       const uint32_t idesc = instruction<T>(u.wide, J.a_mn, J.b_mn);
       const uint32_t flags = (J.a_mn ? NOTE_A_MN : 0u) | (J.b_mn ? NOTE_B_MN : 0u) | (u.kb0 < u.kb1 ? 0u : NOTE_NOTHING);
-      // (a unit without blocks takes a stage for its note)
+      // (a unit without blocks has one for its note)
       const int blocks = max((u.kb1 - u.kb0) * PASSES, 1);
       const bool await = !FORWARD && !LOW && for_a && P.ahead.next && !(flags & NOTE_NOTHING);   // dz is still being made
       if (await && !J.over_rows) {
@@ -317,6 +317,9 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       }
       int at_block = u.kb0;                        // of its pass
       int x = f.x + at_block * f.x_step, y = f.y + at_block * f.y_step;
+      // A unit without blocks (of dW) loads one from behind the rows, zeros that cost no traffic: each block has all four
+      // producers' copies in it, so that the stages' phases cannot pass one of them that is late by two turns of the ring.
+      if (flags & NOTE_NOTHING) y = P.rows;
       for (int left = blocks; left > 0; --left, ++it) {
         if (it >= stages) {
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_or_abort(&empty[st], ph ^ 1u, abort_flag));
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
           ok = seen.rows(P.ahead, y, min(y + LINEAR_DEEP, u.k_end), lane, abort_flag);
           if (!ok) break;
         }
-        const bool nothing = (flags & NOTE_NOTHING) != 0, past_end = !nothing && at_block >= f.past_from;
+        const bool past_end = !(flags & NOTE_NOTHING) && at_block >= f.past_from;
         const uint32_t bar = (past_end ? past_own : full_even) + 8u * st;
         uint8_t* to = ring + st * TILE_BYTES;
         if (elect_lane()) {
@@ -334,15 +337,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
             if (even) {
               notes[st] = BlockNote{idesc, flags | (left == blocks ? NOTE_FIRST : LOW && at_block == u.kb0 ? NOTE_SECOND : 0u) |
                                                (left == 1 ? NOTE_LAST : 0u) | (past_end ? NOTE_PAST : 0u)};
-              if (past_end || nothing) mbar_arrive(&full[st]);
+              if (past_end) mbar_arrive(&full[st]);
               else mbar_expect_tx(&full[st], 2u * f.bytes);
             }
             if (past_end) mbar_expect_tx(&past_bar[st], f.bytes);
           }
-          if (!nothing) {
-            tma_load_3d_pair(to, f.map, bar, x, y, f.batch);
-            if (f.boxes > 1) tma_load_3d_pair(to + BOX_BYTES, f.map, bar, x + 64, y, f.batch);
-          }
+          tma_load_3d_pair(to, f.map, bar, x, y, f.batch);
+          if (f.boxes > 1) tma_load_3d_pair(to + BOX_BYTES, f.map, bar, x + 64, y, f.batch);
         }
         __syncwarp();
         x += f.x_step;

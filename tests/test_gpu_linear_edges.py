@@ -231,3 +231,33 @@ def test_infinite_operands_of_the_gradient(nss, dtype, act, rows, cols, out, gro
         for got, want in ((dx[a:e], D @ W), (dw[i] if groups else dw, D.T @ X)):
             assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
             assert torch.equal(got[got.isinf()].double(), want[want.isinf()])
+
+
+@pytest.mark.parametrize("used", [[1023], [0], [500, 501], []])
+@pytest.mark.parametrize("cols,out", [(8, 8), (200, 520)])
+def test_runs_of_groups_without_rows(nss, used, cols, out):
+    """Most of 1024 experts without a token, so that a pair has many units without blocks in a row: the same result each time."""
+    g, t, rows = _gen(67), torch.bfloat16, 700
+    sizes = torch.zeros(1024, dtype=torch.int64)
+    for i in used:
+        sizes[i] = rows // len(used)
+    ends = sizes.cumsum(0).tolist()
+    x, dy = _rows(rows, cols, t, g), _rows(rows, out, t, g)
+    w = (torch.randn(1024, out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
+    dev = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    dx, dw, db = nss.mb_linear_backward(dy, x, w, ends=dev, bias=True)
+    for i in range(1024):
+        if i not in used:
+            continue
+        a = ends[i] - int(sizes[i])
+        X, D = x[a:ends[i]].double(), dy[a:ends[i]].double()
+        _near(dw[i], D.T @ X, _add(rows) * (D.abs().T @ X.abs()))
+        _near(dx[a:ends[i]], D @ w[i].double(), _add(out) * (D.abs() @ w[i].double().abs()))
+    rest = torch.ones(1024, dtype=torch.bool)
+    rest[used] = False
+    for turn in range(30):
+        given = torch.full_like(dw, 7.0)
+        dx2, dw2, db2 = nss.mb_linear_backward(dy, x, w, ends=dev, bias=True, dweight=given)
+        assert torch.equal(dx2, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+        assert not dw2[rest.cuda()].any()
+    assert nss.mb_sync_status() == 0

@@ -32,3 +32,22 @@ def test_slabs_of_dz_are_handed_over_through_a_barrier():
     body = text[text.index("bool rows(const LinearAhead& A"):]
     body = body[body.index("load_acquire"):body.index("return true;", body.index("load_acquire"))]
     assert re.search(r"__syncwarp\(\);\s*fence_async_global\(\);\s*$", body), body
+
+
+def test_every_block_has_all_producers_in_it():
+    """A stage is released by what was loaded into it.  A block that some producer had no part in could be released, and the
+    stage with it, twice before that producer looks: it would wait for a phase that has passed."""
+    text = _source("mb_linear.cu")
+    loop = text[text.index("for (int left = blocks; left > 0;"):]
+    loop = loop[:loop.index("__syncwarp();")]
+    loads = loop[loop.index("if (elect_lane())"):]
+    depth, guards = 0, []
+    for line in loads.splitlines():
+        if "tma_load_3d_pair(to, f.map" in line:
+            break
+        guards = guards[:depth]
+        if line.rstrip().endswith("{"):
+            guards.append(line.strip())
+        depth += line.count("{") - line.count("}")
+    assert guards[:depth] == ["if (elect_lane()) {"], guards[:depth]
+    assert re.search(r"if \(past_end\) mbar_arrive\(&full\[st\]\);\s*else mbar_expect_tx\(&full\[st\]", loop)
