@@ -122,6 +122,12 @@ __device__ __forceinline__ void decode_same(const LinearParams& P, const Groups&
   u.kb1 = same(u.kb1);
 }
 
+// How long a unit's sums may take: a block 0.3 us, and where 2^28 rows are one group's its 2^22 blocks 1.15 s.
+constexpr uint64_t BLOCK_LIMIT_NS = 4000;
+__device__ __forceinline__ uint64_t unit_limit_ns(const Unit& u) {
+  return WAIT_LIMIT_NS + static_cast<uint64_t>(u.kb1 - u.kb0) * BLOCK_LIMIT_NS;
+}
+
 // What the MMA issuer has to know of a block, written by the A operand's producer of the even CTA: it need not decode units
 // itself, which took it longer (750 cycles) than a block's MMAs.
 struct BlockNote {
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
       bool ok = true;
       for (int pass = 0; pass < PASSES && past >= u.kb0 && past < u.kb1; ++pass) {
         const int st = (it + pass * part + past - u.kb0) % stages;
-        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&past_bar[st], (past_phase >> st) & 1u, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&past_bar[st], (past_phase >> st) & 1u, abort_flag, unit_limit_ns(u)));
         if (!ok) break;
         past_phase ^= 1u << st;
         // a box's rows of 128 bytes are its rows of the contraction (the swizzle stays within a row)
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_kernel(const __grid_constan
         bias[0] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * half, lane);
         bias[1] = bias_of<T>(P, J, u.group, u.n0 + CHUNK_COLS * (half + 2), lane);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&tfull[buf], (k / TURNS) & 1, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&tfull[buf], (k / TURNS) & 1, abort_flag, unit_limit_ns(u)))) {
         fail();
         break;
       }

@@ -261,3 +261,19 @@ def test_runs_of_groups_without_rows(nss, used, cols, out):
         assert torch.equal(dx2, dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
         assert not dw2[rest.cuda()].any()
     assert nss.mb_sync_status() == 0
+
+
+def test_very_many_rows_in_one_group(nss):
+    """2^29 rows, all of them one expert's of 1024: two contractions of 1.15 s, longer than a wait may take that does not count its
+    blocks."""
+    rows, t = 1 << 29, torch.bfloat16
+    x, dy = (torch.zeros(rows, 8, device="cuda", dtype=t) for _ in range(2))
+    dy += 1
+    at = torch.tensor([0, 1, rows // 2 - 1, rows // 2, rows - 1], device="cuda")
+    x[at] = torch.tensor([1.0, 2.0, 4.0, 8.0, 16.0], device="cuda", dtype=t)[:, None]
+    ends = torch.full((1024,), rows, dtype=torch.int32, device="cuda")
+    ends[:700] = 0
+    w = torch.zeros(1024, 8, 8, device="cuda", dtype=t)
+    _, dw, _ = nss.mb_linear_backward(dy, x, w, ends=ends, input_grad=False)
+    assert nss.mb_sync_status() == 0
+    assert (dw[700] == 31).all() and not dw[:700].any() and not dw[701:].any()
