@@ -343,7 +343,9 @@ template <typename T, int TILES, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) linear_some_kernel(const __grid_constant__ LinearFewParams p) {
   constexpr int AHEAD = TILES == 2 && WARPS == 16 ? 4 : 2;
   __shared__ int groups[2 * (LINEAR_MAX_GROUPS + 1)];
-  __shared__ float partial[WARPS][16 * TILES][SOME_LD];
+  // (written in pairs)
+  static_assert(SOME_LD % 2 == 0, "a row of sums begins at a pair");
+  __shared__ alignas(16) float partial[WARPS][16 * TILES][SOME_LD];
   begin_after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col0 = blockIdx.x * SOME_COLS;
   FewRows f = few_rows<T>(p, groups, col0, SOME_COLS);
