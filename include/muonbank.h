@@ -371,7 +371,8 @@ int mb_router_backward(const float* dloss, const float* dgate, const void* logit
  * and nothing of them is in dW and db.  A group without rows has zero dW and db.
  *
  * Operands are bf16 or fp16, sums fp32, each result rounded once; dz is rounded to the operands' type before the
- * products (the tensor cores take no wider operand), but not for db.  Where rows * min(in, out) <= 2048 what the
+ * products (the tensor cores take no wider operand), but not for db; in fp16 a dz below 2^-14 is held in steps of 2^-24, so that
+ * gradients of such sizes lose bits that their sums could hold (scale the loss, as elsewhere in fp16).  Where rows * min(in, out) <= 2048 what the
  * rounding left goes through the products too, and is left out of a sum that is not finite without it.  Activations take the hardware's exponential and reciprocal, each within about 2^-22.  The order of a
  * sum follows from the call's sizes and alignments, so that results repeat bit for bit, but a row's result can differ in
  * its last bits between calls of different row counts.  The conventions are the block operators'; operands whose rows

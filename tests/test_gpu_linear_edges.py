@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_linear import ACTS, TYPES, _add, _bounds, _check_forward, _gen, _near, _rows, _slope, nss  # noqa: F401
+from test_gpu_linear import ACTS, TYPES, _add, _bounds, _check_backward, _check_forward, _gen, _near, _rows, _slope, nss  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -277,3 +277,23 @@ def test_very_many_rows_in_one_group(nss):
     _, dw, _ = nss.mb_linear_backward(dy, x, w, ends=ends, input_grad=False)
     assert nss.mb_sync_status() == 0
     assert (dw[700] == 31).all() and not dw[:700].any() and not dw[701:].any()
+
+
+def test_what_small_fp16_gradients_lose(nss):
+    """fp16 holds dz below 2^-14 in steps of 2^-24: gradients of 1e-6 keep the bound that counts half a step per term, which is some
+    percent of dW here; the same gradients 2^12 larger, as a scaled loss makes them, keep fp16's own half step."""
+    g, t, rows, cols, out = _gen(71), torch.float16, 4096, 64, 72
+    x, w, z = _rows(rows, cols, t, g), _rows(out, cols, t, g, std=cols ** -0.5), _rows(rows, out, t, g)
+    dy = torch.randn(rows, out, generator=g, device="cuda")
+    off = {}
+    for size in (1e-6, 1e-6 * 2 ** 12):
+        d = (size * dy).to(t)
+        _, dw, db = _check_backward(nss, d, x, w, z, "silu", None)
+        want = (d.double() * _slope(z.double(), "silu")).T @ x.double()
+        off[size] = ((dw.double() - want).norm() / want.norm()).item()
+        # dbias takes dz as it is
+        _near(db, (d.double() * _slope(z.double(), "silu")).sum(0), (_add(rows) + 2.0 ** -18) * d.double().abs().sum(0) * 1.1)
+    # an even error within half a step has a deviation of 2^-24 / sqrt(12) a term, beside dz of 1e-6 * 0.61 (silu' of a normal)
+    expected = 2.0 ** -24 / math.sqrt(12) / (1e-6 * 0.61)
+    assert 0.5 * expected <= off[1e-6] <= 1.5 * expected
+    assert off[1e-6 * 2 ** 12] <= 2.0 ** -11
