@@ -297,3 +297,47 @@ def test_what_small_fp16_gradients_lose(nss):
     expected = 2.0 ** -24 / math.sqrt(12) / (1e-6 * 0.61)
     assert 0.5 * expected <= off[1e-6] <= 1.5 * expected
     assert off[1e-6 * 2 ** 12] <= 2.0 ** -11
+
+
+@pytest.mark.parametrize("ends", [None, [6001, 6001, 6100, 19990]])
+def test_large_backward_in_graphs_and_at_once(nss, ends):
+    """dz formed under the products: two graphs replayed in turn with new inputs, and two calls at once on streams of their own,
+    give the bits of a call alone."""
+    g, t, rows, cols, out = _gen(73), torch.bfloat16, 20000, 136, 2528
+    x, dy, z = _rows(rows, cols, t, g), _rows(rows, out, t, g), _rows(rows, out, t, g)
+    n = 1 if ends is None else len(ends)
+    w = (torch.randn(n, out, cols, generator=g, device="cuda") * cols ** -0.5).to(t)
+    w = w[0] if ends is None else w
+    dev = None if ends is None else torch.tensor(ends, dtype=torch.int32, device="cuda")
+    call = lambda: nss.mb_linear_backward(dy, x, w, z, "silu", dev, bias=True)               # noqa: E731
+    first = call()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call())
+        graphs.append(graph)
+    for turn in range(3):
+        if turn:
+            dy.mul_(-0.5)
+            z.neg_()
+            torch.cuda.synchronize()
+        want = call()
+        assert turn or all(torch.equal(a, b) for a, b in zip(first, want))
+        for graph, got in zip(graphs, outs):
+            for o in got:
+                o.fill_(7.0)
+            graph.replay()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append([call() for _ in range(3)])
+    torch.cuda.synchronize()
+    for calls in got:
+        for o in calls:
+            assert all(torch.equal(a, b) for a, b in zip(o, want))
+    assert nss.mb_sync_status() == 0
