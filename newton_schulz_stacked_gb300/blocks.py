@@ -119,9 +119,9 @@ def mb_linear(x, weight, bias=None, residual=None, activation: str = "none", end
     [..., out].  With `ends`, int32 [groups], weight is a bank [groups, out, in] (and bias [groups, out]): the rows of x
     are consecutive groups, group g ending before row ends[g], such as tokens sorted by expert with
     ends = counts.cumsum(0, dtype=torch.int32); rows from the last end on get zeros.  The ends stay on the device.
-    activation: "none", "relu", "relu2" (its square), "silu" or "gelu" (the tanh form).  A few rows (single tokens, up
-    to 512 with small weights) take kernels of their own, without tiles.  y may be the residual; no
-    other overlap of a result.
+    activation: "none", "relu", "relu2" (its square), "silu" or "gelu" (the tanh form).  A few rows (single tokens, up to
+    512) take kernels of their own, without tiles, where those are the shorter way.  y may be the residual, with its
+    strides; a result that shares memory with anything else of the call is refused.
     """
     return (_native or load_binding()).mb_linear(x, weight, bias, residual, activation, ends, keep, y, z, workspace, stream)
 
@@ -133,7 +133,8 @@ def mb_linear_backward(dy, x, weight, z=None, activation: str = "none", ends=Non
 
     z is the forward call's (not needed without an activation).  x is read for dweight only, weight for dx only: either may be
     None where that gradient is not wanted.  dweight is laid out as the weight, the gradient of a bank as
-    muon_multi_step takes it; dbias comes in x's type unless a float32 one is passed.  The residual's gradient is dy.  No result may overlap an input.
+    muon_multi_step takes it; dbias comes in x's type unless a float32 one is passed.  The residual's gradient is dy.  A result
+    that shares memory with anything else of the call is refused.
     """
     return (_native or load_binding()).mb_linear_backward(dy, x, weight, z, activation, ends, input_grad, weight_grad, bias,
                                                           dx, dweight, dbias, workspace, stream)

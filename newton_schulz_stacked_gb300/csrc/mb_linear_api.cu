@@ -22,7 +22,8 @@ constexpr int64_t MAX_PAIRS = 76;        // what the cuts are planned for: the p
 constexpr int MAX_SPLITS = 16;
 // Up to so many elements (of x or y) dz's rounding is kept in a second half.  Over random cases of 1 to 64 rows and widths of 64
 // to 2048 the gradients' errors with one half were 1.4 times those of rounding the exact sums, and more than 1.5 times in 3 %,
-// none of them above 1610 elements.  The second pass takes 1x768->768 from 11 to 15 us, which wider calls are spared.
+// none of them above 1610 elements.  The second pass takes 1x768->768 from 10.5 to 12.6 us and 1x2048->2048 from 18 to 28 (in a
+// graph), which wider calls are spared.
 constexpr int64_t TWO_HALVES = 1 << 11;
 // From so many elements on dz is formed under the products' MMAs, below by a launch before them.  Both, with dx, dW and db on
 // one GB300, in us: 32768x768->768 100 and 90, 8192x1024->4096 140 and 136, 32768x2048->2048 379 and 390, 65536x768->2816
