@@ -134,9 +134,9 @@ class _Linear(torch.autograd.Function):
     weight and bias through it, to the graph without their values."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, activation, ends):
-        want = ctx.needs_input_grad
-        keep = activation != "none" and any(want[:3])
+    def forward(ctx, x, weight, bias, residual, activation, ends, recorded):
+        want = ctx.needs_input_grad                # (whether or not the call is recorded)
+        keep = recorded and activation != "none" and any(want[:3])
         y, z = _k.mb_linear(x, weight, bias, residual, activation, ends, keep=keep)
         # dweight alone reads x, dx alone the weight: what no wanted gradient reads is neither kept nor held to its values
         ctx.save_for_backward(x if want[1] else None, weight if want[0] else None, z, ends)
@@ -148,7 +148,7 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, _dz):
         if dy is None:
-            return None, None, None, None, None, None
+            return None, None, None, None, None, None, None
         x, weight, z, ends = ctx.saved_tensors
         want = ctx.needs_input_grad
         grads = (None, None, None)
@@ -161,7 +161,7 @@ class _Linear(torch.autograd.Function):
                 return _k.mb_linear_backward(dy, x, weight, z, ctx.activation, ends, input_grad=want[0], weight_grad=want[1],
                                              dbias=dbias)
             grads = _first_only("linear", call, dy.resolve_neg().contiguous(), x, weight, z, ends)
-        return (*grads, _of_groups(dy, ends) if want[3] else None, None, None)
+        return (*grads, _of_groups(dy, ends) if want[3] else None, None, None, None)
 
 
 def _of_groups(dy, ends):
@@ -177,4 +177,4 @@ def linear(x, weight, bias=None, residual=None, activation: str = "none", ends=N
 
     A backward pass can be captured into a CUDA graph; as with torch's own functions not while another graph of the same
     leaves, made on another stream, is alive (capture then ends with an error)."""
-    return _Linear.apply(x, weight, bias, residual, activation, ends)[0]
+    return _Linear.apply(x, weight, bias, residual, activation, ends, torch.is_grad_enabled())[0]

@@ -103,3 +103,25 @@ def test_backward_calls_without_what_they_do_not_read(nss):
         if groups:
             with pytest.raises(ValueError, match="ends"):
                 nss.mb_linear_backward(dy, x, None, z, "silu", ends.long(), input_grad=False)
+
+
+def test_z_is_formed_for_a_backward_pass_only(nss, monkeypatch):
+    """Parameters that require gradients, evaluated without recording: no second result is written."""
+    from newton_schulz_stacked_gb300 import autograd
+    x, w, b, r, _, ends = _leaves(3, "silu")
+    w.requires_grad_()
+    kept, call = [], autograd._k.mb_linear
+
+    def seen(*args, keep, **more):
+        kept.append(keep)
+        return call(*args, keep=keep, **more)
+
+    monkeypatch.setattr(autograd._k, "mb_linear", seen)
+    want = autograd.linear(x, w, b, r, "silu", ends)
+    with torch.no_grad():
+        assert torch.equal(autograd.linear(x, w, b, r, "silu", ends), want)
+    with torch.inference_mode():
+        assert torch.equal(autograd.linear(x, w, b, r, "silu", ends), want)
+    autograd.linear(x, w, b, r, "none", ends)
+    autograd.linear(x, w.detach(), b, r, "silu", ends)
+    assert kept == [True, False, False, False, False]
