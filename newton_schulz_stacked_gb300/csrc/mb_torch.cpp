@@ -612,7 +612,7 @@ struct Place {
   uintptr_t end() const { return begin() + static_cast<uintptr_t>((rows - 1) * step + width); }
 };
 Place place_of(const char* name, const void* at, int64_t rows, int64_t cols, int64_t stride, int64_t size = 2) {
-  return {name, rows > 0 && cols > 0 ? at : nullptr, rows, cols * size, stride * size};
+  return {name, rows > 0 && cols > 0 ? at : nullptr, stride == 0 ? 1 : rows, cols * size, stride * size};   // (one row for all)
 }
 Place bytes_at(const char* name, const void* at, size_t bytes) {
   return {name, bytes > 0 ? at : nullptr, 1, static_cast<int64_t>(bytes), static_cast<int64_t>(bytes)};
